@@ -67,6 +67,9 @@ typedef enum {
 #define NBX_DEV_BAD_PAGE 0x2   /* a block-table entry inside a sequence is -1 or >= num_pages: tile skipped */
 #define NBX_DEV_BAD_LEN 0x4    /* seq_lens[b] < 0, > max_seq_len or > max_pages * page_tokens: sequence read as empty */
 #define NBX_DEV_TIMEOUT 0x8    /* a bounded wait inside a kernel gave up: the output is incomplete */
+#define NBX_DEV_BAD_SCALE 0x10 /* a block's scale is not a number in [2^-48, 2^48]: its positions are skipped */
+#define NBX_DEV_BAD_ROW 0x20   /* a fork names a row outside the table, or a destination a second time: skipped */
+#define NBX_DEV_NO_PAGE 0x40   /* a fork found no free page for its partial page: its row is left empty */
 
 /* Positions per staged tile: every page must hold a whole number of tiles, so no
  * tile straddles two pages (paged_decode_attention's "ZERO FALLBACK" check). */
@@ -267,6 +270,121 @@ NBX_API int nbx_paged_decode_attn_fixed_shift(const void* q, int q_dtype, int ba
  * and gate = floor((C + 125) / 2). Host-only. NBX_ERR_VALUE for n_keys < 1 or v_max_bound < 1.
  */
 NBX_API int nbx_decode_fixed_shift_gate(int n_keys, double v_max_bound, int* c_out, int* gate_out);
+
+/* ------------------------------------------------------------------------------------------------
+ * The block-scaled cache: E4M3 pools with one fp32 scale per block of tokens and KV head.
+ *
+ *   k_pool, v_pool      [num_pages, h_kv, page_tokens, d] E4M3 codes
+ *   k_scales, v_scales  [num_pages, h_kv, page_tokens / scale_tokens] fp32, each in [2^-48, 2^48]:
+ *                       position j of a page stands for code * scale[j / scale_tokens]
+ *   scale_tokens        16, 32, 64 or 128, dividing page_tokens (NBX_ERR_PAGE_ALIGN otherwise)
+ * These calls and the score modifications and page calls below are additions of this library; the
+ * pages it was written from have no counterpart.
+ */
+
+/*
+ * nbx_paged_kv_append_block_scaled -- write new positions into a block-scaled cache.
+ *
+ * Sequence b's new tokens are rows tok_start[b] .. tok_start[b + 1] - 1 of new_k / new_v; they go to
+ * positions lens[b], lens[b] + 1, ... through the block table. For every block of scale_tokens
+ * positions that gets new tokens, per KV head, K and V apart:
+ *   need = the smallest power of two in [2^-48, 2^48] with max |x| <= 448 * need over the finite values
+ *          of the block's new tokens;
+ *   S    = need when the block's first position is new, else max(the block's scale, need);
+ *   new codes are e4m3(x / S) (nearest even, saturating at +-448; NaN stays NaN); if S grew, the codes
+ *   of the positions held before become e4m3(code * old S / S), which is exact but for results under 2^-6.
+ * Positions past the new ones are left as they are. lens is not advanced. Appending the same tokens
+ * again at the same lens gives the same cache.
+ *
+ *   new_k, new_v [device] [n_tok, h_kv, d], new_dtype NBX_F32 or NBX_BF16
+ *   block_table  [device] int32 [batch, max_pages];  lens [device] int32 [batch]
+ *   tok_start    [device] int32 [batch + 1], ascending, tok_start[batch] <= n_tok
+ * A sequence whose tok_start or lens make no sense, or a block past max_pages, is skipped with
+ * NBX_DEV_BAD_LEN, a page outside the pool with NBX_DEV_BAD_PAGE; a held block whose scale is not in
+ * [2^-48, 2^48] gets need and NBX_DEV_BAD_SCALE. No two sequences may append to one page.
+ * Requirements: d in {64, 128, 256}; buffers 16-byte aligned. n_tok == 0 or batch == 0 returns NBX_OK
+ * without a launch.
+ */
+NBX_API int nbx_paged_kv_append_block_scaled(const void* new_k, const void* new_v, int new_dtype, int n_tok, int h_kv,
+                                             int d, void* k_pool, void* v_pool, float* k_scales, float* v_scales,
+                                             int scale_tokens, int num_pages, int page_tokens,
+                                             const int32_t* block_table, int max_pages, int batch,
+                                             const int32_t* lens, const int32_t* tok_start, int32_t* status,
+                                             void* stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * Pages. A page is in use while an entry of the block table names it, within its row's length or past
+ * it (a page reserved for growth). There are no reference counts: filling a row with -1 frees the pages
+ * that no other row names. Rows may share pages.
+ */
+
+/*
+ * nbx_paged_kv_copy_pages -- copy the held positions of pages to other pages.
+ *
+ * moves [device] int32 [max_moves, 3]: {source page, destination page, positions}, the first *n_moves
+ * of them used ([device] int32; clamped to [0, max_moves]): positions 0 .. positions - 1 of every KV
+ * head of both pools, and with k_scales / v_scales (an E4M3 pool; otherwise NULL) the scales of the
+ * blocks that hold them. The moves of a fork or a compaction of one layer's table are applied to the
+ * other layers' pools with this call.
+ * No page may be a destination twice, or a destination and a source. A page outside the pool is skipped
+ * with NBX_DEV_BAD_PAGE, a count outside [0, page_tokens] with NBX_DEV_BAD_LEN.
+ * Requirements: d a multiple of 16 and <= 1024; a page of all heads under 2 GB; pools 16-byte aligned.
+ */
+NBX_API int nbx_paged_kv_copy_pages(const int32_t* moves, const int32_t* n_moves, int max_moves, void* k_pool,
+                                    void* v_pool, int pool_dtype, int num_pages, int h_kv, int page_tokens, int d,
+                                    float* k_scales, float* v_scales, int scale_tokens, int32_t* status,
+                                    void* stream);
+
+/*
+ * nbx_paged_kv_fork -- rows of the block table become copies of other rows.
+ *
+ * For i = 0 .. n_fork - 1, row fork_dst[i] becomes row fork_src[i] as it was before the call, in length
+ * and content. Full pages are shared; a last page that is partly filled is copied to the lowest free
+ * page, in order of i, so that both can go on appending. Where the source row is itself a destination
+ * (a beam that is replaced), its first reader takes the partial page over without a copy. The rest of
+ * the destination row is -1; what it held before is free, unless another row names it.
+ *
+ *   block_table  [device] int32 [batch, max_pages], updated;  seq_lens [device] int32 [batch], updated
+ *   fork_src, fork_dst [device] int32 [n_fork]; destinations distinct
+ *   k_pool, v_pool and the arguments after them as for nbx_paged_kv_copy_pages; both NULL (the sizes
+ *                num_pages and page_tokens still count): the table only, nothing is copied
+ *   moves        [device] int32 [n_fork, 3], written: the copies {source, fresh page, positions} in
+ *                order of i, then -1;  n_moves [device] int32, written
+ *   workspace    [device] nbx_paged_kv_fork_workspace_bytes(batch, max_pages, n_fork, num_pages) bytes,
+ *                256-byte aligned
+ * A row outside the table, or a destination named a second time, sets NBX_DEV_BAD_ROW and that fork is
+ * skipped; a source length outside its bounds sets NBX_DEV_BAD_LEN and a missing free page
+ * NBX_DEV_NO_PAGE, and the destination is left empty (length 0, all -1). n_fork == 0 or batch == 0
+ * returns NBX_OK without a launch.
+ */
+NBX_API size_t nbx_paged_kv_fork_workspace_bytes(int batch, int max_pages, int n_fork, int num_pages);
+NBX_API int nbx_paged_kv_fork(int32_t* block_table, int max_pages, int32_t* seq_lens, int batch,
+                              const int32_t* fork_src, const int32_t* fork_dst, int n_fork, void* k_pool, void* v_pool,
+                              int pool_dtype, int num_pages, int h_kv, int page_tokens, int d, float* k_scales,
+                              float* v_scales, int scale_tokens, int32_t* moves, int32_t* n_moves, void* workspace,
+                              size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * nbx_paged_kv_compact -- move the pages in use to the lowest ids.
+ *
+ * With n_live pages in use, the k-th page in use at an id >= n_live (ascending) moves to the k-th free
+ * id < n_live; new_block_table is the table with the new ids. Ids from n_live on are then free, and the
+ * pool can be cut there. The held positions of a page are copied (the most that any row holds of it).
+ *
+ *   block_table  [device] int32 [batch, max_pages];  new_block_table the same shape, may be block_table
+ *   moves        [device] int32 [max_moves, 3], written as by nbx_paged_kv_fork; max_moves >= num_pages / 2
+ *   counts       [device] int32 [2], written: {moves, pages in use}
+ *   workspace    [device] nbx_paged_kv_compact_workspace_bytes(num_pages) bytes, 256-byte aligned
+ *   pools        as for nbx_paged_kv_fork (both NULL: nothing is copied)
+ * Entries that name no page of the pool are kept (NBX_DEV_BAD_PAGE if >= num_pages). num_pages <= 2^30.
+ * batch == 0 returns NBX_OK without a launch.
+ */
+NBX_API size_t nbx_paged_kv_compact_workspace_bytes(int num_pages);
+NBX_API int nbx_paged_kv_compact(const int32_t* block_table, int32_t* new_block_table, int max_pages,
+                                 const int32_t* seq_lens, int batch, void* k_pool, void* v_pool, int pool_dtype,
+                                 int num_pages, int h_kv, int page_tokens, int d, float* k_scales, float* v_scales,
+                                 int scale_tokens, int32_t* moves, int max_moves, int32_t* counts, void* workspace,
+                                 size_t workspace_bytes, int32_t* status, void* stream);
 
 /* Bytes of device scratch that libnbx keeps for nbx_paged_decode_attn_noalloc (32 MiB). */
 #define NBX_NOALLOC_SCRATCH_BYTES (32u * 1024u * 1024u)

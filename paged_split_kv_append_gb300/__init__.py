@@ -25,12 +25,15 @@ __all__ = [
     "nbx_paged_kv_append", "nbx_paged_decode_workspace_bytes", "nbx_paged_decode_attn",
     "nbx_paged_decode_merge", "nbx_set_decode_grid_limit", "nbx_set_decode_wait_test", "nbx_status_string",
     "nbx_paged_decode_bounds", "nbx_paged_decode_attn_fixed_shift", "nbx_decode_fixed_shift_gate",
+    "nbx_paged_kv_append_block_scaled", "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork",
+    "nbx_paged_kv_fork_workspace_bytes", "nbx_paged_kv_compact", "nbx_paged_kv_compact_workspace_bytes",
     "dtype_code",
-    "DEV_BAD_SLOT", "DEV_BAD_PAGE", "DEV_BAD_LEN", "DEV_TIMEOUT",
+    "DEV_BAD_SLOT", "DEV_BAD_PAGE", "DEV_BAD_LEN", "DEV_TIMEOUT", "DEV_BAD_SCALE", "DEV_BAD_ROW", "DEV_NO_PAGE",
 ]
 
 NBX_F32, NBX_BF16, NBX_E4M3 = 0, 1, 2
 DEV_BAD_SLOT, DEV_BAD_PAGE, DEV_BAD_LEN, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_SCALE, DEV_BAD_ROW, DEV_NO_PAGE = 0x10, 0x20, 0x40
 PARTIAL_SIMT, PARTIAL_TCGEN05, PARTIAL_TCGEN05_FP8 = 0, 1, 2
 
 _lib = None
@@ -89,6 +92,21 @@ def _declare(l):
     l.nbx_paged_decode_attn_fixed_shift.restype = i32
     l.nbx_decode_fixed_shift_gate.argtypes = [i32, ctypes.c_double, ctypes.POINTER(i32), ctypes.POINTER(i32)]
     l.nbx_decode_fixed_shift_gate.restype = i32
+    l.nbx_paged_kv_append_block_scaled.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, i32, i32, vp, i32,
+                                                   i32, vp, vp, vp, vp]
+    l.nbx_paged_kv_append_block_scaled.restype = i32
+    l.nbx_paged_kv_copy_pages.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp]
+    l.nbx_paged_kv_copy_pages.restype = i32
+    l.nbx_paged_kv_fork_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    l.nbx_paged_kv_fork_workspace_bytes.restype = sz
+    l.nbx_paged_kv_fork.argtypes = [vp, i32, vp, i32, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp,
+                                    vp, sz, vp, vp]
+    l.nbx_paged_kv_fork.restype = i32
+    l.nbx_paged_kv_compact_workspace_bytes.argtypes = [i32]
+    l.nbx_paged_kv_compact_workspace_bytes.restype = sz
+    l.nbx_paged_kv_compact.argtypes = [vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp,
+                                       vp, sz, vp, vp]
+    l.nbx_paged_kv_compact.restype = i32
     l.nbx_status_string.argtypes = [i32]
     l.nbx_status_string.restype = ctypes.c_char_p
     l.nbx_abi_version.argtypes = []
@@ -388,3 +406,183 @@ def nbx_decode_fixed_shift_gate(n_keys: int, v_max_bound: float = 256.0):
     st = lib().nbx_decode_fixed_shift_gate(int(n_keys), float(v_max_bound), ctypes.byref(c), ctypes.byref(g))
     _check("nbx_decode_fixed_shift_gate", st)
     return c.value, g.value
+
+
+# ---------------------------------------------------------------- the block-scaled cache and the pages
+# These calls check that every tensor sits on one device, and run there whatever the current device is.
+class _Device:
+    """The device of a call's tensors, made current for the call; the stream defaults to its current one."""
+
+    def __init__(self, **tensors):
+        self.dev = None
+        for n, t in tensors.items():
+            if t is None:
+                continue
+            _cuda_contig(n, t)
+            if self.dev is None:
+                self.dev = t.device
+            elif t.device != self.dev:
+                raise ValueError(f"{n} is on {t.device}, not on {self.dev}")
+        self.back = None
+
+    def stream(self, stream) -> ctypes.c_void_p:
+        return _stream(torch.cuda.current_stream(self.dev) if stream is None else stream)
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.dev)
+        return self
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _int32(shape_ok: bool = True, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{n} must be int32")
+    if not shape_ok:
+        raise ValueError("shapes do not fit: " + ", ".join(f"{n} {list(t.shape)}" for n, t in tensors.items()
+                                                           if t is not None))
+
+
+def _pools(k_pool, v_pool, k_scales, v_scales):
+    """(num_pages, h_kv, page_tokens, d, positions per scale or 0) of a layer's pools."""
+    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype:
+        raise ValueError("k_pool and v_pool [num_pages, h_kv, page_tokens, d] must match")
+    num_pages, h_kv, page_tokens, d = k_pool.shape
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales come together")
+    if k_scales is None:
+        return num_pages, h_kv, page_tokens, d, 0
+    if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32 or k_scales.shape != v_scales.shape or \
+            k_scales.dim() != 3 or tuple(k_scales.shape[:2]) != (num_pages, h_kv) or k_scales.shape[2] < 1 or \
+            page_tokens % k_scales.shape[2] != 0:
+        raise ValueError(f"k_scales {list(k_scales.shape)} and v_scales {list(v_scales.shape)} must be fp32 "
+                         f"[num_pages, h_kv, page_tokens / scale_tokens] for the pool {list(k_pool.shape)}")
+    if dtype_code(k_pool) != NBX_E4M3:
+        raise ValueError("only e4m3 pools have scales")
+    return num_pages, h_kv, page_tokens, d, page_tokens // k_scales.shape[2]
+
+
+def nbx_paged_kv_append_block_scaled(new_k: torch.Tensor, new_v: torch.Tensor, k_pool: torch.Tensor,
+                                     v_pool: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                     block_table: torch.Tensor, lens: torch.Tensor, tok_start: torch.Tensor,
+                                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """new_k / new_v [n_tok, h_kv, d] (fp32 or bf16): rows tok_start[b] .. tok_start[b + 1] - 1 are sequence
+    b's tokens at positions lens[b] and up, quantised into the e4m3 pools and scales [num_pages, h_kv,
+    page_tokens / scale_tokens]. lens [batch] and tok_start [batch + 1] int32; lens is not advanced."""
+    dv = _Device(new_k=new_k, new_v=new_v, k_pool=k_pool, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales,
+                 block_table=block_table, lens=lens, tok_start=tok_start, status=status)
+    if new_k.dim() != 3 or new_k.shape != new_v.shape or new_k.dtype != new_v.dtype:
+        raise ValueError("new_k and new_v [n_tok, h_kv, d] must match")
+    num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
+    n_tok = new_k.shape[0]
+    if tuple(new_k.shape[1:]) != (h_kv, d):
+        raise ValueError(f"new {list(new_k.shape)} does not fit the pool {list(k_pool.shape)}")
+    batch = lens.numel()
+    _int32(block_table.dim() == 2 and block_table.shape[0] == batch and tok_start.numel() == batch + 1,
+           block_table=block_table, lens=lens, tok_start=tok_start, status=status)
+    with dv:
+        st = lib().nbx_paged_kv_append_block_scaled(
+            _ptr(new_k), _ptr(new_v), dtype_code(new_k), n_tok, h_kv, d, _ptr(k_pool), _ptr(v_pool), _ptr(k_scales),
+            _ptr(v_scales), block, num_pages, page_tokens, _ptr(block_table), block_table.shape[1], batch, _ptr(lens),
+            _ptr(tok_start), _ptr(status), dv.stream(stream))
+    _check("nbx_paged_kv_append_block_scaled", st)
+
+
+def nbx_paged_kv_copy_pages(moves: torch.Tensor, n_moves: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                            k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+                            status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The first n_moves[0] of moves [max_moves, 3] int32 {source page, destination page, positions}, on one
+    layer's pools and, for a block-scaled cache, scales."""
+    dv = _Device(moves=moves, n_moves=n_moves, k_pool=k_pool, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales,
+                 status=status)
+    num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
+    _int32(moves.dim() == 2 and moves.shape[1] == 3 and n_moves.numel() >= 1, moves=moves, n_moves=n_moves,
+           status=status)
+    with dv:
+        st = lib().nbx_paged_kv_copy_pages(_ptr(moves), _ptr(n_moves), moves.shape[0], _ptr(k_pool), _ptr(v_pool),
+                                           dtype_code(k_pool), num_pages, h_kv, page_tokens, d, _ptr(k_scales),
+                                           _ptr(v_scales), block, _ptr(status), dv.stream(stream))
+    _check("nbx_paged_kv_copy_pages", st)
+
+
+def nbx_paged_kv_fork_workspace_bytes(batch: int, max_pages: int, n_fork: int, num_pages: int) -> int:
+    return int(lib().nbx_paged_kv_fork_workspace_bytes(batch, max_pages, n_fork, num_pages))
+
+
+def nbx_paged_kv_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, fork_src: torch.Tensor,
+                      fork_dst: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                      k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None,
+                      moves: Optional[torch.Tensor] = None, n_moves: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Rows fork_dst[i] of block_table [batch, max_pages] and seq_lens [batch] become rows fork_src[i] as they
+    were (all int32): full pages shared, the last partial page copied to a free one. Returns (moves [n_fork, 3],
+    n_moves [1]): the copies made, for nbx_paged_kv_copy_pages on the other layers' pools."""
+    dv = _Device(block_table=block_table, seq_lens=seq_lens, fork_src=fork_src, fork_dst=fork_dst, k_pool=k_pool,
+                 v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, moves=moves, n_moves=n_moves,
+                 workspace=workspace, status=status)
+    num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
+    n = fork_src.numel()
+    if moves is None:
+        moves = torch.full((n, 3), -1, dtype=torch.int32, device=dv.dev)
+    if n_moves is None:
+        n_moves = torch.zeros(1, dtype=torch.int32, device=dv.dev)
+    _int32(block_table.dim() == 2 and block_table.shape[0] == seq_lens.numel() and fork_dst.numel() == n and
+           tuple(moves.shape) == (n, 3) and n_moves.numel() >= 1, block_table=block_table, seq_lens=seq_lens,
+           fork_src=fork_src, fork_dst=fork_dst, moves=moves, n_moves=n_moves, status=status)
+    batch, max_pages = block_table.shape
+    if workspace is None:
+        workspace = torch.empty(max(nbx_paged_kv_fork_workspace_bytes(batch, max_pages, n, num_pages), 256),
+                                dtype=torch.uint8, device=dv.dev)
+    with dv:
+        st = lib().nbx_paged_kv_fork(_ptr(block_table), max_pages, _ptr(seq_lens), batch, _ptr(fork_src),
+                                     _ptr(fork_dst), n, _ptr(k_pool), _ptr(v_pool), dtype_code(k_pool), num_pages,
+                                     h_kv, page_tokens, d, _ptr(k_scales), _ptr(v_scales), block, _ptr(moves),
+                                     _ptr(n_moves), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                     _ptr(status), dv.stream(stream))
+    _check("nbx_paged_kv_fork", st)
+    return moves, n_moves
+
+
+def nbx_paged_kv_compact_workspace_bytes(num_pages: int) -> int:
+    return int(lib().nbx_paged_kv_compact_workspace_bytes(num_pages))
+
+
+def nbx_paged_kv_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, k_pool: torch.Tensor,
+                         v_pool: torch.Tensor, k_scales: Optional[torch.Tensor] = None,
+                         v_scales: Optional[torch.Tensor] = None, new_block_table: Optional[torch.Tensor] = None,
+                         moves: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """The pages in use moved to the lowest ids. Returns (new_block_table, moves [num_pages // 2, 3], counts [2] =
+    {moves, pages in use}); new_block_table may be block_table itself. The moves are for
+    nbx_paged_kv_copy_pages on the other layers' pools."""
+    dv = _Device(block_table=block_table, seq_lens=seq_lens, k_pool=k_pool, v_pool=v_pool, k_scales=k_scales,
+                 v_scales=v_scales, new_block_table=new_block_table, moves=moves, counts=counts, workspace=workspace,
+                 status=status)
+    num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
+    if new_block_table is None:
+        new_block_table = torch.empty_like(block_table)
+    if moves is None:
+        moves = torch.full((max(1, num_pages // 2), 3), -1, dtype=torch.int32, device=dv.dev)
+    if counts is None:
+        counts = torch.zeros(2, dtype=torch.int32, device=dv.dev)
+    _int32(block_table.dim() == 2 and block_table.shape[0] == seq_lens.numel() and
+           new_block_table.shape == block_table.shape and moves.dim() == 2 and moves.shape[1] == 3 and
+           counts.numel() >= 2, block_table=block_table, seq_lens=seq_lens, new_block_table=new_block_table,
+           moves=moves, counts=counts, status=status)
+    if workspace is None:
+        workspace = torch.empty(max(nbx_paged_kv_compact_workspace_bytes(num_pages), 256), dtype=torch.uint8,
+                                device=dv.dev)
+    with dv:
+        st = lib().nbx_paged_kv_compact(_ptr(block_table), _ptr(new_block_table), block_table.shape[1],
+                                        _ptr(seq_lens), block_table.shape[0], _ptr(k_pool), _ptr(v_pool),
+                                        dtype_code(k_pool), num_pages, h_kv, page_tokens, d, _ptr(k_scales),
+                                        _ptr(v_scales), block, _ptr(moves), moves.shape[0], _ptr(counts),
+                                        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
+                                        dv.stream(stream))
+    _check("nbx_paged_kv_compact", st)
+    return new_block_table, moves, counts

@@ -24,7 +24,6 @@ constexpr unsigned long long kMaxProducerDelayNs = 50000000ull;     // 50 ms
 std::atomic<unsigned long long> g_wait_limit_ns{kDefaultWaitLimitNs};
 std::atomic<unsigned long long> g_producer_delay_ns{0};
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool finite(float x) { return std::isfinite(x); }
 }  // namespace
 

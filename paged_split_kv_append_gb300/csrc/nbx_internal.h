@@ -21,6 +21,81 @@ struct DeviceInfo {
 // Facts of the current device, queried once per device.
 const DeviceInfo& device_info();
 
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// ---------------------------------------------------------------- block-scaled pools
+// Scales of an E4M3 pool's blocks lie in [2^-48, 2^48]. With every ratio of two scales inside 2^96, the
+// weights p * v_scale of one row's softmax keep their order in fp32 with 2^30 to spare.
+constexpr int kMaxScaleLog2 = 48;
+constexpr float kMaxScale = 281474976710656.f;   // 2^48
+constexpr float kMinScale = 1.f / 281474976710656.f;
+
+// Positions a scale covers: 16, 32, 64 or 128, and a page holds a whole number of such blocks.
+inline bool scale_tokens_ok(int t, int page_tokens) {
+  return (t == 16 || t == 32 || t == 64 || t == 128) && page_tokens % t == 0;
+}
+
+struct AppendBlockParams {
+  const void* new_k;
+  const void* new_v;
+  void* k_pool;
+  void* v_pool;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* block_table;
+  const int32_t* lens;
+  const int32_t* tok_start;
+  int32_t* status;
+  int n_tok, h_kv, d, num_pages, page_tokens, max_pages, batch, scale_tokens;
+  int64_t n_flat;   // flat block indices: n_tok / T + 2 batch
+};
+
+// ---------------------------------------------------------------- pages
+struct CopyPagesParams {
+  void* k_pool;
+  void* v_pool;
+  float* k_scales;
+  float* v_scales;
+  const int32_t* moves;
+  const int32_t* n_moves;
+  int32_t* status;
+  int max_moves, num_pages, h_kv, page_tokens;
+  int row_bytes;      // bytes of one position of one KV head
+  int scale_tokens;
+  int chunks;         // 4 KB pieces of one KV head's page
+};
+
+enum { kForkNone = 0, kForkShare = 1, kForkCopy = 2, kForkEmpty = 3 };
+
+struct ForkParams {
+  int32_t* block_table;
+  int32_t* seq_lens;
+  const int32_t* fork_src;
+  const int32_t* fork_dst;
+  int32_t* moves;
+  int32_t* n_moves;
+  int32_t* status;
+  uint32_t* bitmap;     // [num_pages] bits: pages in use
+  int4* row_info;       // [batch] {fork that overwrites the row, first fork that reads it, length, -}; n_fork: none
+  int4* outcome;        // [n_fork] {kFork..., rank among the copies, length, fresh page}
+  int32_t* fresh;       // [n_fork] free pages in ascending order
+  int32_t* row_keep;    // [batch, max_pages] rows that are both read and overwritten, as they were
+  int max_pages, batch, n_fork, num_pages, page_tokens;
+};
+
+struct CompactParams {
+  const int32_t* block_table;
+  int32_t* new_block_table;
+  const int32_t* seq_lens;
+  int32_t* moves;
+  int32_t* counts;
+  int32_t* status;
+  int32_t* fill;        // [num_pages] 1 + positions held, 0 for a free page
+  int32_t* chunk_live;  // [n_chunks] pages in use per chunk
+  int32_t* rank;        // [num_pages] move number of a page that moves
+  int batch, max_pages, num_pages, page_tokens, max_moves, n_chunks;
+};
+
 struct AppendParams {
   const void* new_k;
   const void* new_v;
