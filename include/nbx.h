@@ -312,6 +312,50 @@ NBX_API int nbx_paged_kv_append_block_scaled(const void* new_k, const void* new_
                                              const int32_t* lens, const int32_t* tok_start, int32_t* status,
                                              void* stream);
 
+/*
+ * nbx_paged_decode_attn_block_scaled -- split-KV decode attention over a block-scaled cache.
+ * nbx_paged_decode_attn_modified     -- nbx_paged_decode_attn with the score modifications below.
+ *
+ * For sequence b of n = seq_lens[b] positions, query row r at position p = n - rows + r and query head h,
+ * with key j standing for its value (code * block scale, or element * k_scale / v_scale):
+ *   the visible keys are j in [begin, end), cut to [0, n): begin = key_begin[b, r] (0 if NULL),
+ *     end = key_end[b, r] (p + 1 if NULL);
+ *   z_j = scale * (q . k_j);  with softcap > 0: z_j = softcap * tanh(z_j / softcap);
+ *     with slopes: z_j -= slopes[h] * |p - j|;
+ *   out = sum_j e^(z_j - max z) v_j / sum_j e^(z_j - max z), 0 for a row that sees no key.
+ * A document mask is key_begin = the start of the row's document, a prefix mask key_end =
+ * max(p + 1, prefix length), a window key_begin = p + 1 - window. Keys that no row of a work unit sees are
+ * not read: their pages may be gone from the table (-1).
+ *
+ *   softcap      finite, >= 0 (0: none)
+ *   slopes       [device] fp32 [h_q] or NULL
+ *   key_begin, key_end  [device] int32 [batch, rows] or NULL each
+ *   out          [device] [batch, rows, h_q, d] in out_dtype: NBX_F32, or NBX_BF16 (rounded once)
+ *   workspace    [device] nbx_paged_decode_modified_workspace_bytes(...) bytes, 256-byte aligned
+ *   k_scales, v_scales, scale_tokens  as for nbx_paged_kv_append_block_scaled; scales need not be powers of
+ *                two here. A block that is read whose scale is not in [2^-48, 2^48] sets NBX_DEV_BAD_SCALE and
+ *                its positions are skipped.
+ *   every other argument, rule and status bit as for nbx_paged_decode_attn; results likewise do not depend
+ *   on page ids or on the order the work runs in.
+ */
+NBX_API size_t nbx_paged_decode_modified_workspace_bytes(int batch, int rows, int h_q, int h_kv, int d,
+                                                         int max_seq_len);
+NBX_API int nbx_paged_decode_attn_block_scaled(const void* q, int q_dtype, int batch, int rows, int h_q, int d,
+                                               const void* k_pool, const void* v_pool, const float* k_scales,
+                                               const float* v_scales, int scale_tokens, int num_pages, int h_kv,
+                                               int page_tokens, const int32_t* block_table, int max_pages,
+                                               const int32_t* seq_lens, int max_seq_len, float scale, float softcap,
+                                               const float* slopes, const int32_t* key_begin, const int32_t* key_end,
+                                               void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                                               int32_t* status, void* stream);
+NBX_API int nbx_paged_decode_attn_modified(const void* q, int q_dtype, int batch, int rows, int h_q, int d,
+                                           const void* k_pool, const void* v_pool, int pool_dtype, int num_pages,
+                                           int h_kv, int page_tokens, const int32_t* block_table, int max_pages,
+                                           const int32_t* seq_lens, int max_seq_len, float scale, float k_scale,
+                                           float v_scale, float softcap, const float* slopes,
+                                           const int32_t* key_begin, const int32_t* key_end, void* out, int out_dtype,
+                                           void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
 /* ------------------------------------------------------------------------------------------------
  * Pages. A page is in use while an entry of the block table names it, within its row's length or past
  * it (a page reserved for growth). There are no reference counts: filling a row with -1 frees the pages

@@ -25,7 +25,8 @@ __all__ = [
     "nbx_paged_kv_append", "nbx_paged_decode_workspace_bytes", "nbx_paged_decode_attn",
     "nbx_paged_decode_merge", "nbx_set_decode_grid_limit", "nbx_set_decode_wait_test", "nbx_status_string",
     "nbx_paged_decode_bounds", "nbx_paged_decode_attn_fixed_shift", "nbx_decode_fixed_shift_gate",
-    "nbx_paged_kv_append_block_scaled", "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork",
+    "nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
+    "nbx_paged_decode_modified_workspace_bytes", "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork",
     "nbx_paged_kv_fork_workspace_bytes", "nbx_paged_kv_compact", "nbx_paged_kv_compact_workspace_bytes",
     "dtype_code",
     "DEV_BAD_SLOT", "DEV_BAD_PAGE", "DEV_BAD_LEN", "DEV_TIMEOUT", "DEV_BAD_SCALE", "DEV_BAD_ROW", "DEV_NO_PAGE",
@@ -95,6 +96,14 @@ def _declare(l):
     l.nbx_paged_kv_append_block_scaled.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, i32, i32, vp, i32,
                                                    i32, vp, vp, vp, vp]
     l.nbx_paged_kv_append_block_scaled.restype = i32
+    l.nbx_paged_decode_modified_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    l.nbx_paged_decode_modified_workspace_bytes.restype = sz
+    l.nbx_paged_decode_attn_block_scaled.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp,
+                                                     i32, vp, i32, f32, f32, vp, vp, vp, vp, i32, vp, sz, vp, vp]
+    l.nbx_paged_decode_attn_block_scaled.restype = i32
+    l.nbx_paged_decode_attn_modified.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp,
+                                                 i32, f32, f32, f32, f32, vp, vp, vp, vp, i32, vp, sz, vp, vp]
+    l.nbx_paged_decode_attn_modified.restype = i32
     l.nbx_paged_kv_copy_pages.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp]
     l.nbx_paged_kv_copy_pages.restype = i32
     l.nbx_paged_kv_fork_workspace_bytes.argtypes = [i32, i32, i32, i32]
@@ -491,6 +500,89 @@ def nbx_paged_kv_append_block_scaled(new_k: torch.Tensor, new_v: torch.Tensor, k
             _ptr(v_scales), block, num_pages, page_tokens, _ptr(block_table), block_table.shape[1], batch, _ptr(lens),
             _ptr(tok_start), _ptr(status), dv.stream(stream))
     _check("nbx_paged_kv_append_block_scaled", st)
+
+
+def nbx_paged_decode_modified_workspace_bytes(batch: int, rows: int, h_q: int, h_kv: int, d: int,
+                                              max_seq_len: int) -> int:
+    return int(lib().nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len))
+
+
+def _modified_call(dv, q, k_pool, block_table, seq_lens, max_seq_len, slopes, key_begin, key_end, out, out_dtype,
+                   workspace, status):
+    """The shapes and types the two modified decodes share: (out, workspace, workspace bytes)."""
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, rows, h_q, d]")
+    batch, rows, h_q, d = q.shape
+    _int32(block_table.dim() == 2 and block_table.shape[0] == batch and seq_lens.numel() == batch and
+           all(k is None or tuple(k.shape) == (batch, rows) for k in (key_begin, key_end)), block_table=block_table,
+           seq_lens=seq_lens, key_begin=key_begin, key_end=key_end, status=status)
+    if k_pool.shape[3] != d:
+        raise ValueError(f"q {list(q.shape)} does not fit the pool {list(k_pool.shape)}")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != h_q):
+        raise ValueError("slopes must be fp32 [h_q]")
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or torch.float32, device=dv.dev)
+    elif out.shape != q.shape or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be {list(q.shape)}" + (f" {out_dtype}" if out_dtype else ""))
+    if workspace is None:
+        need = nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, k_pool.shape[1], d, max_seq_len)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dv.dev)
+    return out, workspace, workspace.numel() * workspace.element_size()
+
+
+def nbx_paged_decode_attn_block_scaled(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                                       k_scales: torch.Tensor, v_scales: torch.Tensor, block_table: torch.Tensor,
+                                       seq_lens: torch.Tensor, max_seq_len: int, scale: float, softcap: float = 0.0,
+                                       slopes: Optional[torch.Tensor] = None, key_begin: Optional[torch.Tensor] = None,
+                                       key_end: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                       out_dtype: Optional[torch.dtype] = None,
+                                       workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                                       stream=None) -> torch.Tensor:
+    """q [batch, rows, h_q, d] (fp32 or bf16) over a block-scaled cache (e4m3 pools, scales [num_pages, h_kv,
+    page_tokens / scale_tokens] fp32) -> out [batch, rows, h_q, d], fp32 or bf16 (out's dtype, or out_dtype).
+    The score modifications are those of nbx_paged_decode_attn_modified."""
+    dv = _Device(q=q, k_pool=k_pool, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, block_table=block_table,
+                 seq_lens=seq_lens, slopes=slopes, key_begin=key_begin, key_end=key_end, out=out, workspace=workspace,
+                 status=status)
+    num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
+    out, workspace, ws_bytes = _modified_call(dv, q, k_pool, block_table, seq_lens, max_seq_len, slopes, key_begin,
+                                              key_end, out, out_dtype, workspace, status)
+    batch, rows, h_q, _ = q.shape
+    with dv:
+        st = lib().nbx_paged_decode_attn_block_scaled(
+            _ptr(q), dtype_code(q), batch, rows, h_q, d, _ptr(k_pool), _ptr(v_pool), _ptr(k_scales), _ptr(v_scales), block,
+            num_pages, h_kv, page_tokens, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), int(max_seq_len),
+            float(scale), float(softcap), _ptr(slopes), _ptr(key_begin), _ptr(key_end), _ptr(out), dtype_code(out),
+            _ptr(workspace), ws_bytes, _ptr(status), dv.stream(stream))
+    _check("nbx_paged_decode_attn_block_scaled", st)
+    return out
+
+
+def nbx_paged_decode_attn_modified(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                                   block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, scale: float,
+                                   k_scale: float = 1.0, v_scale: float = 1.0, softcap: float = 0.0,
+                                   slopes: Optional[torch.Tensor] = None, key_begin: Optional[torch.Tensor] = None,
+                                   key_end: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                   out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None,
+                                   status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """nbx_paged_decode_attn with score modifications: a cap (softcap * tanh(z / softcap)), a bias by distance
+    (-slopes[h] * |p - j|, slopes [h_q] fp32) and per-row key ranges (key_begin / key_end [batch, rows] int32, by
+    default 0 and p + 1: document, prefix and window masks). out [batch, rows, h_q, d] is fp32 or bf16 (out's dtype,
+    or out_dtype)."""
+    dv = _Device(q=q, k_pool=k_pool, v_pool=v_pool, block_table=block_table, seq_lens=seq_lens, slopes=slopes,
+                 key_begin=key_begin, key_end=key_end, out=out, workspace=workspace, status=status)
+    num_pages, h_kv, page_tokens, d, _ = _pools(k_pool, v_pool, None, None)
+    out, workspace, ws_bytes = _modified_call(dv, q, k_pool, block_table, seq_lens, max_seq_len, slopes, key_begin,
+                                              key_end, out, out_dtype, workspace, status)
+    batch, rows, h_q, _ = q.shape
+    with dv:
+        st = lib().nbx_paged_decode_attn_modified(
+            _ptr(q), dtype_code(q), batch, rows, h_q, d, _ptr(k_pool), _ptr(v_pool), dtype_code(k_pool), num_pages, h_kv,
+            page_tokens, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), int(max_seq_len), float(scale),
+            float(k_scale), float(v_scale), float(softcap), _ptr(slopes), _ptr(key_begin), _ptr(key_end), _ptr(out),
+            dtype_code(out), _ptr(workspace), ws_bytes, _ptr(status), dv.stream(stream))
+    _check("nbx_paged_decode_attn_modified", st)
+    return out
 
 
 def nbx_paged_kv_copy_pages(moves: torch.Tensor, n_moves: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,

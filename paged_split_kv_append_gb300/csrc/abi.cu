@@ -150,6 +150,19 @@ NBX_API size_t nbx_paged_decode_workspace_bytes_for(int q_dtype, int pool_dtype,
   return w.total;
 }
 
+// What a modified or block-scaled decode adds to a plain one.
+struct ModArgs {
+  bool block_scaled;
+  const float* k_scales;
+  const float* v_scales;
+  int scale_tokens;
+  float softcap;
+  const float* slopes;
+  const int32_t* key_begin;
+  const int32_t* key_end;
+  int out_dtype;
+};
+
 // The decode call behind every decode entry point. `identity` reads the pools as one page per
 // sequence through an identity block table the plan kernel writes into the workspace; `lens_out`
 // and `len_add` make it a decode step's (attend with seq_lens + len_add, write that length back).
@@ -159,7 +172,7 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
                        float scale, float k_scale, float v_scale, float* out, void* workspace,
                        size_t workspace_bytes, int32_t* status, cudaStream_t stream, bool identity,
                        int32_t* lens_out, int len_add, const float* fs_q_norm = nullptr,
-                       const float* fs_kv_max = nullptr) {
+                       const float* fs_kv_max = nullptr, const ModArgs* mod = nullptr) {
   if (!decode_shape_ok(batch, rows, h_q, h_kv, d, max_seq_len)) return NBX_ERR_SHAPE;
   if (num_pages < 1 || page_tokens < 1 || max_pages < 1) return NBX_ERR_SHAPE;
   if (static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_pages) * page_tokens) return NBX_ERR_SHAPE;
@@ -168,13 +181,20 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
   if (pool_dtype != NBX_F32 && pool_dtype != NBX_BF16 && pool_dtype != NBX_E4M3) return NBX_ERR_DTYPE;
   if (!finite(scale) || !finite(k_scale) || !finite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f))
     return NBX_ERR_VALUE;
+  if (mod) {
+    if (mod->out_dtype != NBX_F32 && mod->out_dtype != NBX_BF16) return NBX_ERR_DTYPE;
+    if (mod->block_scaled && !scale_tokens_ok(mod->scale_tokens, page_tokens)) return NBX_ERR_PAGE_ALIGN;
+    if (!(mod->softcap >= 0.f) || !finite(mod->softcap)) return NBX_ERR_VALUE;
+    if (mod->softcap > 0.f && !finite(1.f / (mod->softcap * kLog2eHost))) return NBX_ERR_VALUE;
+  }
   if (batch == 0) return NBX_OK;
   if (!q || !k_pool || !v_pool || (!identity && !block_table) || !seq_lens || !out || !workspace) return NBX_ERR_NULL;
+  if (mod && mod->block_scaled && (!mod->k_scales || !mod->v_scales)) return NBX_ERR_NULL;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return NBX_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return NBX_ERR_ALIGN;
   WorkspaceLayout w;
   if (!workspace_layout(batch, rows, h_q, h_kv, d, max_seq_len, &w)) return NBX_ERR_SHAPE;
-  if (workspace_bytes < w.total) return NBX_ERR_WORKSPACE;
+  if (workspace_bytes < (mod ? w.total_mod : w.total)) return NBX_ERR_WORKSPACE;
 
   char* ws = static_cast<char*>(workspace);
   DecodeParams p = {};
@@ -218,7 +238,23 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
     const double part_bytes = static_cast<double>(batch) * rows * h_q * w.max_splits * d * 4.0;
     p.keep_frac = static_cast<float>(part_bytes <= 67108864.0 ? 1.0 : 67108864.0 / part_bytes);
   }
-  const cudaError_t e = decode_dispatch(p, q_dtype, pool_dtype, g_grid_limit.load(), stream);
+  int x = 0;
+  if (mod) {
+    const bool scored = mod->softcap > 0.f || mod->slopes || mod->key_begin || mod->key_end;
+    p.out_bf16 = mod->out_dtype == NBX_BF16;
+    p.cap_log2 = mod->softcap * kLog2eHost;
+    p.cap_inv = mod->softcap > 0.f ? 1.f / p.cap_log2 : 0.f;
+    p.slopes = mod->slopes;
+    p.key_begin = mod->key_begin;
+    p.key_end = mod->key_end;
+    p.k_scales = mod->k_scales;
+    p.v_scales = mod->v_scales;
+    p.scale_tokens = mod->scale_tokens;
+    p.ranges = reinterpret_cast<int2*>(ws + w.ranges);
+    // an fp32 output without a modification is the plain decode's
+    x = mod->block_scaled ? kBlockScaled | (scored ? kScoreMod : 0) : (scored || p.out_bf16 ? kScoreMod : 0);
+  }
+  const cudaError_t e = decode_dispatch(p, q_dtype, pool_dtype, x, g_grid_limit.load(), stream);
   return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
 }
 
@@ -231,6 +267,43 @@ NBX_API int nbx_paged_decode_attn(const void* q, int q_dtype, int batch, int row
   return decode_call(q, q_dtype, batch, rows, h_q, d, k_pool, v_pool, pool_dtype, num_pages, h_kv, page_tokens,
                      block_table, max_pages, seq_lens, max_seq_len, scale, k_scale, v_scale, out, workspace,
                      workspace_bytes, status, static_cast<cudaStream_t>(stream), false, nullptr, 0);
+}
+
+NBX_API size_t nbx_paged_decode_modified_workspace_bytes(int batch, int rows, int h_q, int h_kv, int d,
+                                                         int max_seq_len) {
+  if (!decode_shape_ok(batch, rows, h_q, h_kv, d, max_seq_len)) return 0;
+  WorkspaceLayout w;
+  if (!workspace_layout(batch, rows, h_q, h_kv, d, max_seq_len, &w)) return 0;
+  return w.total_mod;
+}
+
+NBX_API int nbx_paged_decode_attn_modified(const void* q, int q_dtype, int batch, int rows, int h_q, int d,
+                                           const void* k_pool, const void* v_pool, int pool_dtype, int num_pages,
+                                           int h_kv, int page_tokens, const int32_t* block_table, int max_pages,
+                                           const int32_t* seq_lens, int max_seq_len, float scale, float k_scale,
+                                           float v_scale, float softcap, const float* slopes,
+                                           const int32_t* key_begin, const int32_t* key_end, void* out, int out_dtype,
+                                           void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+  const ModArgs mod = {false, nullptr, nullptr, 0, softcap, slopes, key_begin, key_end, out_dtype};
+  return decode_call(q, q_dtype, batch, rows, h_q, d, k_pool, v_pool, pool_dtype, num_pages, h_kv, page_tokens,
+                     block_table, max_pages, seq_lens, max_seq_len, scale, k_scale, v_scale, static_cast<float*>(out),
+                     workspace, workspace_bytes, status, static_cast<cudaStream_t>(stream), false, nullptr, 0, nullptr,
+                     nullptr, &mod);
+}
+
+NBX_API int nbx_paged_decode_attn_block_scaled(const void* q, int q_dtype, int batch, int rows, int h_q, int d,
+                                               const void* k_pool, const void* v_pool, const float* k_scales,
+                                               const float* v_scales, int scale_tokens, int num_pages, int h_kv,
+                                               int page_tokens, const int32_t* block_table, int max_pages,
+                                               const int32_t* seq_lens, int max_seq_len, float scale, float softcap,
+                                               const float* slopes, const int32_t* key_begin, const int32_t* key_end,
+                                               void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                                               int32_t* status, void* stream) {
+  const ModArgs mod = {true, k_scales, v_scales, scale_tokens, softcap, slopes, key_begin, key_end, out_dtype};
+  return decode_call(q, q_dtype, batch, rows, h_q, d, k_pool, v_pool, NBX_E4M3, num_pages, h_kv, page_tokens,
+                     block_table, max_pages, seq_lens, max_seq_len, scale, 1.f, 1.f, static_cast<float*>(out), workspace,
+                     workspace_bytes, status, static_cast<cudaStream_t>(stream), false, nullptr, 0, nullptr, nullptr,
+                     &mod);
 }
 
 NBX_API int nbx_paged_decode_attn_fixed_shift(const void* q, int q_dtype, int batch, int rows, int h_q, int d,

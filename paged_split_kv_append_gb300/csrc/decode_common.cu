@@ -1,5 +1,6 @@
 // The split plan kernel, the standalone merge kernel, the workspace layout and the
 // decode launch sequence (plan, then the persistent partial kernel).
+#include <climits>
 #include <cuda_fp16.h>
 
 #include "decode_kernels.cuh"
@@ -51,6 +52,9 @@ bool workspace_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq
   w->acc_part = off;
   off += up(prow * static_cast<size_t>(d) * 4);
   w->total = off;
+  w->ranges = off;
+  const size_t m_tiles = (static_cast<size_t>(rows) * (h_q / h_kv) + kMmaRowsPerTile - 1) / kMmaRowsPerTile;
+  w->total_mod = off + up(static_cast<size_t>(batch) * m_tiles * sizeof(int2));
   w->max_splits = static_cast<int>(S);
   w->row_blocks = static_cast<int>(rb);
   return true;
@@ -72,7 +76,10 @@ __device__ __forceinline__ void plan_finish(const DecodeParams& p) {
 // keep their own order and take a slower serial path.
 // TC: a tensor-core window, whose splits are sized by the call's total work (DecodeParams::tc_units);
 // otherwise splits of kSimtSplitPositions. Two instantiations keep each rule's code free of the other.
-template <bool TC>
+// X: a modified decode. With key ranges a sequence's splits cut only the positions from the first key that
+// some row sees (down to a split boundary's alignment) to the last one, and a tensor-core window gets the
+// range of every M tile; the ranges come from the caller's kernels, so that plan waits before it reads.
+template <bool TC, bool X>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   extern __shared__ int plan_sm[];   // plan_smem_bytes(batch)
   int* const s_len = plan_sm;
@@ -88,7 +95,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   const int B = p.batch;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_tokens;
   const bool small = B <= kSortMax;
+  if constexpr (X) pdl_wait();
   pdl_launch_dependents();   // the partial kernel may start its prologue now; it waits for this grid
+  const bool ranges = X && (p.key_begin != nullptr || p.key_end != nullptr);
+  // splits start on whole pages, or on 256-position boundaries when a page is longer (a
+  // contiguous cache read as one page per sequence): tile starts either way
+  const int align = p.page_tokens <= NBX_SPLIT_POSITIONS ? p.page_tokens : NBX_SPLIT_POSITIONS;
   __shared__ long long s_total;
   if (tid == 0) {
     s_empty = 0;
@@ -97,13 +109,60 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     p.header[1] = 0;
   }
   __syncthreads();
+  if constexpr (X) {
+    if (ranges) {   // a warp per (sequence, M tile), or per sequence: the keys its rows see between them
+      for (int64_t it = warp; it < static_cast<int64_t>(B) * p.range_tiles; it += kPlanThreads / 32) {
+        const int b = static_cast<int>(it / p.range_tiles);
+        const int mt = static_cast<int>(it - static_cast<int64_t>(b) * p.range_tiles);
+        const int L = p.seq_lens[b];
+        const bool fit = L >= 0 && L <= p.max_seq_len && static_cast<int64_t>(L) <= cap;
+        const int r0 = TC ? mt * kMmaRowsPerTile / p.group : 0;
+        const int r1 = TC ? min(p.rows, ((mt + 1) * kMmaRowsPerTile + p.group - 1) / p.group) : p.rows;
+        int lo = INT_MAX, hi = 0;
+        for (int r = r0 + lane; r < r1; r += 32) {
+          const KeyRange kr = key_range(p, b, r, fit ? L : 0);
+          if (kr.hi > kr.lo) {
+            lo = min(lo, kr.lo);
+            hi = max(hi, kr.hi);
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        }
+        if (lane == 0) p.ranges[it] = hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
+      }
+      __syncthreads();   // orders the ranges' global writes before this CTA's reads
+    }
+  }
+  // the positions of sequence b that are read: its length, or its rows' range from an aligned start
+  auto reach = [&](int b, int L) -> int2 {
+    if (!ranges) return make_int2(0, L);
+    int lo = INT_MAX, hi = 0;
+    for (int mt = 0; mt < p.range_tiles; ++mt) {
+      const int2 r = p.ranges[static_cast<int64_t>(b) * p.range_tiles + mt];
+      if (r.y > r.x) {
+        lo = min(lo, r.x);
+        hi = max(hi, r.y);
+      }
+    }
+    return hi > 0 ? make_int2(lo / align * align, min(hi, L)) : make_int2(0, 0);
+  };
   // a tensor-core window sizes its splits by the whole call's work: the sum of the lengths
   long long len_sum = 0;
   if constexpr (TC) {
     long long part = 0;
     for (int b = tid; b < B; b += kPlanThreads) {
       const int L = p.seq_lens[b] + p.len_add;
-      if (L > 0 && L <= p.max_seq_len && static_cast<int64_t>(L) <= cap) part += L;
+      if (L > 0 && L <= p.max_seq_len && static_cast<int64_t>(L) <= cap) {
+        if constexpr (X) {
+          const int2 w = reach(b, L);
+          part += w.y - w.x;
+        } else {
+          part += L;
+        }
+      }
     }
     for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == 0 && part) atomicAdd(reinterpret_cast<unsigned long long*>(&s_total), static_cast<unsigned long long>(part));
@@ -116,6 +175,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     if (L < 0 || L > p.max_seq_len || static_cast<int64_t>(L) > cap) {
       raise_status(p.status, NBX_DEV_BAD_LEN);
       L = 0;
+    }
+    const int len = L;
+    int first = 0;   // X: L becomes the positions read, from `first` on
+    if constexpr (X) {
+      const int2 w = reach(b, L);
+      first = w.x;
+      L = w.y - w.x;
     }
     int S;
     if (TC && len_sum > 0) {
@@ -131,17 +197,14 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
       S = S > NBX_MAX_SPLITS ? NBX_MAX_SPLITS : S;
     }
     int seg = (L + S - 1) / S;
-    // splits start on whole pages, or on 256-position boundaries when a page is longer (a
-    // contiguous cache read as one page per sequence): tile starts either way
-    const int align = p.page_tokens <= NBX_SPLIT_POSITIONS ? p.page_tokens : NBX_SPLIT_POSITIONS;
     seg = ((seg + align - 1) / align) * align;
     const int n = L > 0 ? (L + seg - 1) / seg : 0;
     // kept in L2 for the merge, which reads the split counts after the K/V stream
-    st_global_hint(reinterpret_cast<int4*>(p.plan + b), make_int4(L, seg, n, 0), l2_evict_last_policy());
+    st_global_hint(reinterpret_cast<int4*>(p.plan + b), make_int4(X ? len : L, seg, n, first), l2_evict_last_policy());
     if (n == 0) s_empty = 1;
     else if (small) atomicAdd(&s_nb, 1);
     if (small) {
-      s_len[b] = L;
+      s_len[b] = X ? first + L : L;
       s_seg[b] = seg;
       s_n[b] = n;
     }
@@ -149,7 +212,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   __syncthreads();
   // a sequence with no position to read gets no work unit: its rows are written here (0)
   if (s_empty) {
-    const int64_t row_vec4 = static_cast<int64_t>(p.rows) * p.h_q * p.d / 4;
+    // 16-byte pieces of a sequence's output (d is a multiple of 64)
+    const int64_t row_vec4 = static_cast<int64_t>(p.rows) * p.h_q * p.d / (X && p.out_bf16 ? 8 : 4);
     for (int b = 0; b < B; ++b) {
       if ((small ? s_n[b] : p.plan[b].n_splits) != 0) continue;
       float4* o = reinterpret_cast<float4*>(p.out) + b * row_vec4;
@@ -166,8 +230,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
           Entry e;
           e.b = b;
           e.s = s;
-          e.start = s * sp.seg;
-          e.end = min((s + 1) * sp.seg, sp.len);
+          e.start = sp.first + s * sp.seg;
+          e.end = min(sp.first + (s + 1) * sp.seg, X ? reach(b, sp.len).y : sp.len);
           e.len = sp.len;
           e.n_splits = sp.n_splits;
           e.pad0 = e.pad1 = 0;
@@ -243,9 +307,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     Entry en;
     en.b = b;
     en.s = s;
-    en.start = s * s_seg[b];
-    en.end = min((s + 1) * s_seg[b], s_len[b]);
-    en.len = s_len[b];
+    if constexpr (X) {   // the list of splits starts at the first position read and ends at the last
+      const SeqPlan sp = p.plan[b];
+      en.start = sp.first + s * s_seg[b];
+      en.end = min(sp.first + (s + 1) * s_seg[b], s_len[b]);
+      en.len = sp.len;
+    } else {
+      en.start = s * s_seg[b];
+      en.end = min((s + 1) * s_seg[b], s_len[b]);
+      en.len = s_len[b];
+    }
     en.n_splits = s_n[b];
     en.pad0 = en.pad1 = 0;
     p.entries[e] = en;
@@ -311,7 +382,8 @@ constexpr int kDecodeMergeThreads = 32;   // one warp per CTA
 // float4 of the output, with every split's accumulator load in flight and the sum in ascending
 // split order.
 // F16: the partials are f16 acc / l (DecodeParams::part_f16); a split then weighs 2^(m - M) * l.
-template <bool F16>
+// X: a modified decode, whose output may be bf16.
+template <bool F16, bool X>
 __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(DecodeParams p) {
   const int lane = threadIdx.x;
   const int RG = p.rows * p.group;
@@ -405,9 +477,15 @@ __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(Decod
         }
       }
     }
-    if (j < d4)
-      reinterpret_cast<float4*>(p.out + orow * p.d)[j] =
-          dead ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(A.x * sc, A.y * sc, A.z * sc, A.w * sc);
+    const float4 o = dead ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(A.x * sc, A.y * sc, A.z * sc, A.w * sc);
+    if (X && p.out_bf16) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
+      if (j < d4)
+        reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * p.d)[j] =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    } else if (j < d4) {
+      reinterpret_cast<float4*>(p.out + orow * p.d)[j] = o;
+    }
   }
 }
 
@@ -514,33 +592,50 @@ cudaError_t bounds_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
   return cudaGetLastError();
 }
 
-cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, int grid_limit,
+template <bool X>
+cudaError_t launch_plan(const DecodeParams& p, cudaStream_t stream) {
+  const size_t smem = plan_smem_bytes(p.batch);
+  return p.tc_units > 0 ? launch_pdl(plan_kernel<true, X>, 1u, kPlanThreads, smem, stream, p)
+                        : launch_pdl(plan_kernel<false, X>, 1u, kPlanThreads, smem, stream, p);
+}
+
+template <bool X>
+cudaError_t launch_merge(const DecodeParams& p, unsigned grid, cudaStream_t stream) {
+  return p.part_f16 ? launch_pdl(decode_merge_kernel<true, X>, grid, kDecodeMergeThreads, 0, stream, p)
+                    : launch_pdl(decode_merge_kernel<false, X>, grid, kDecodeMergeThreads, 0, stream, p);
+}
+
+cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, int x, int grid_limit,
                             cudaStream_t stream) {
   DecodeParams q = p;
-  const bool mma = mma_path_applies(p, q_dtype, pool_dtype);
+  const bool mma = x == 0 && mma_path_applies(p, q_dtype, pool_dtype);
   q.part_f16 = mma && pool_dtype == NBX_E4M3 ? 1 : 0;   // fp8 pools on tensor cores: f16 partials
+  q.range_tiles = 1;
   if (mma) {
     // a tensor-core window: splits sized for one wave of work units over the GPU's SMs (the grid
     // limit does not enter, so the partition, and the result, is the same at any grid size)
     q.tc_units = device_info().sm_count;
     q.tc_pairs = p.h_kv * ((p.rows * p.group + kMmaRowsPerTile - 1) / kMmaRowsPerTile);
   }
-  const size_t plan_smem = plan_smem_bytes(q.batch);
-  cudaError_t e = q.tc_units > 0 ? launch_pdl(plan_kernel<true>, 1u, kPlanThreads, plan_smem, stream, q)
-                                 : launch_pdl(plan_kernel<false>, 1u, kPlanThreads, plan_smem, stream, q);
+  cudaError_t e = x ? launch_plan<true>(q, stream) : launch_plan<false>(q, stream);
   if (e != cudaSuccess) return e;
   if (mma) e = decode_dispatch_mma(q, pool_dtype, grid_limit, stream);
-  else if (pool_dtype == NBX_F32) e = decode_dispatch_F32(q, q_dtype, grid_limit, stream);
-  else if (pool_dtype == NBX_BF16) e = decode_dispatch_BF16(q, q_dtype, grid_limit, stream);
-  else e = decode_dispatch_E4M3(q, q_dtype, grid_limit, stream);
+  else if (x & kBlockScaled)
+    e = x & kScoreMod ? decode_dispatch_E4M3_block_mod(q, q_dtype, grid_limit, stream)
+                      : decode_dispatch_E4M3_block(q, q_dtype, grid_limit, stream);
+  else if (pool_dtype == NBX_F32)
+    e = x ? decode_dispatch_F32_mod(q, q_dtype, grid_limit, stream) : decode_dispatch_F32(q, q_dtype, grid_limit, stream);
+  else if (pool_dtype == NBX_BF16)
+    e = x ? decode_dispatch_BF16_mod(q, q_dtype, grid_limit, stream) : decode_dispatch_BF16(q, q_dtype, grid_limit, stream);
+  else
+    e = x ? decode_dispatch_E4M3_mod(q, q_dtype, grid_limit, stream) : decode_dispatch_E4M3(q, q_dtype, grid_limit, stream);
   if (e != cudaSuccess) return e;
   if (q.max_splits <= 1) return cudaSuccess;   // every sequence has one split: the partials are the output
   const int64_t items = static_cast<int64_t>(q.batch) * q.h_kv * q.row_blocks * kQB * ((q.d / 4 + 31) / 32);
   int64_t grid = static_cast<int64_t>(device_info().sm_count) * 24;
   if (grid > items) grid = items;
-  if (q.part_f16)
-    return launch_pdl(decode_merge_kernel<true>, static_cast<unsigned>(grid), kDecodeMergeThreads, 0, stream, q);
-  return launch_pdl(decode_merge_kernel<false>, static_cast<unsigned>(grid), kDecodeMergeThreads, 0, stream, q);
+  const unsigned g = static_cast<unsigned>(grid);
+  return x ? launch_merge<true>(q, g, stream) : launch_merge<false>(q, g, stream);
 }
 
 }  // namespace nbx

@@ -1,0 +1,6 @@
+// Instantiations of the split-KV partial kernel for E4M3 pools, with score modifications (query fp32 / bf16, head dim 64 / 128 / 256).
+#include "decode_kernels.cuh"
+
+namespace nbx {
+NBX_DECODE_FOR_POOL(E4M3_mod, E4M3, kScoreMod)
+}  // namespace nbx

@@ -42,6 +42,9 @@
 //    flight land and returns.
 #pragma once
 
+#include <climits>
+#include <type_traits>
+
 #include "nbx_device.cuh"
 #include "nbx_internal.h"
 
@@ -56,8 +59,18 @@ struct UnitMeta {
   int64_t orow[kQB];   // output row (b * rows + r) * h_q + h * group + g
 };
 
-template <class PT, class QT, int D>
+// The same for a decode with score modifications (kScoreMod).
+struct UnitMetaMod : UnitMeta {
+  int32_t lo[kQB];      // first key each vector sees (pos above: the last)
+  int32_t at[kQB];      // its position p, from which distances count
+  float slope[kQB];     // bias per position of distance, log2 units
+  int32_t all_lo, all_hi;   // keys that every vector of the unit sees: [all_lo, all_hi]
+};
+
+template <class PT, class QT, int D, int X = 0>
 struct DecodeCfg {
+  using Meta = std::conditional_t<(X & kScoreMod) != 0, UnitMetaMod, UnitMeta>;
+  static constexpr bool kBlk = (X & kBlockScaled) != 0;
   static constexpr int kLPT = D / 16;                  // lanes per position in the score layout
   static constexpr int kTPG = kLPT >= 8 ? 2 : 1;       // positions each lane group scores per pass
   static constexpr int kTG = 32 / kLPT;                // lane groups per warp
@@ -81,7 +94,7 @@ struct DecodeCfg {
   // copies: the copy engine's fixed cost per bulk request would cap the stream below HBM speed
   static constexpr bool kWarpCopy = kTileBytes <= 4096;
   static constexpr int kFixed = 2 * kQBytes + (kRedInStage ? 0 : 2 * kRedFloats * 4) + kPBufBytes +
-                                2 * (int)sizeof(UnitMeta) + 2048;
+                                2 * (int)sizeof(Meta) + (kBlk ? 8 * 16 : 0) + 2048;
   // resident CTAs per SM: 3 (2 at head dim 256, where the registers allow no more), fewer when
   // shared memory cannot hold two stages for each of them
   static constexpr int kBlocksBySmem = kSmemPerSm / (kFixed + 2 * kStageBytes + 1024);
@@ -93,14 +106,16 @@ struct DecodeCfg {
   static_assert(kWarpTok % kPassTok == 0, "a warp's share of a stage holds whole passes");
   static_assert(!kRedInStage || kWarpTok * D * PT::kBytes >= 2 * kQB * 4, "a warp's V rows hold its m and l");
   static_assert(kLPT >= 4 && kLPT <= 16, "head dim 64..256");
+  static_assert(!kBlk || (PT::kCode == NBX_E4M3 && kWarpCopy), "block scales ride with the lanes' copies of E4M3 tiles");
 };
 
+template <class C>
 struct SmemLayout {
   char* stages;
   char* qbuf;        // [2][kQBytes]
   float* red;        // [2][warps][kQB*D acc | kQB m | kQB l], or null when it lives in a stage
   f32x2* pbuf;       // [warps][kPassTok][kQB] (p, p) pairs
-  UnitMeta* meta;    // [2]
+  typename C::Meta* meta;    // [2]
   int* stage_ok;     // [stages] bit h: tile h of the stage was copied
   int* flags;        // [0] abort, [2] tiles issued
   uint64_t* full;    // [stages]
@@ -108,6 +123,7 @@ struct SmemLayout {
   uint64_t* qfull;   // [2]
   uint64_t* qempty;  // [2]
   uint64_t* cbar;    // consumer-warp barrier
+  float* scales;     // [stages][4] block scales of a stage: K of its two tiles, then V (kBlockScaled)
 };
 
 template <class C>
@@ -115,10 +131,11 @@ struct Carver {
   static constexpr int r(int b) { return ((b + 127) / 128) * 128; }
   static constexpr int bytes() {
     return r(C::kStages * C::kStageBytes) + r(2 * C::kQBytes) + r(C::kRedInStage ? 0 : 2 * C::kRedFloats * 4) + r(C::kPBufBytes) +
-           r(2 * (int)sizeof(UnitMeta)) + r(C::kStages * 4) + r(16) + 2 * r(C::kStages * 8) + 2 * r(16) + r(8);
+           r(2 * (int)sizeof(typename C::Meta)) + r(C::kStages * 4) + r(16) + 2 * r(C::kStages * 8) + 2 * r(16) + r(8) +
+           (C::kBlk ? r(C::kStages * 16) : 0);
   }
-  __device__ static SmemLayout carve(char* base) {
-    SmemLayout s;
+  __device__ static SmemLayout<C> carve(char* base) {
+    SmemLayout<C> s;
     char* p = base;
     auto take = [&](int b) {
       char* q = p;
@@ -129,7 +146,7 @@ struct Carver {
     s.qbuf = take(2 * C::kQBytes);
     s.red = C::kRedInStage ? nullptr : reinterpret_cast<float*>(take(2 * C::kRedFloats * 4));
     s.pbuf = reinterpret_cast<f32x2*>(take(C::kPBufBytes));
-    s.meta = reinterpret_cast<UnitMeta*>(take(2 * sizeof(UnitMeta)));
+    s.meta = reinterpret_cast<typename C::Meta*>(take(2 * sizeof(typename C::Meta)));
     s.stage_ok = reinterpret_cast<int*>(take(C::kStages * 4));
     s.flags = reinterpret_cast<int*>(take(16));
     s.full = reinterpret_cast<uint64_t*>(take(C::kStages * 8));
@@ -137,6 +154,7 @@ struct Carver {
     s.qfull = reinterpret_cast<uint64_t*>(take(16));
     s.qempty = reinterpret_cast<uint64_t*>(take(16));
     s.cbar = reinterpret_cast<uint64_t*>(take(8));
+    s.scales = C::kBlk ? reinterpret_cast<float*>(take(C::kStages * 16)) : nullptr;
     return s;
   }
 };
@@ -225,10 +243,21 @@ __device__ __forceinline__ void pv_step_masked(uint32_t pb, uint32_t va, f32x2 (
 }
 
 // ------------------------------------------------------------------------------------ partial
-template <class PT, class QT, int D>
-__global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBlocks)
+// X: what the call adds to the plain decode (kScoreMod, kBlockScaled bits). The additions, per score:
+//  * block scales: s_j is multiplied by its K block's scale, and the weight that enters P*V by its V
+//    block's (l keeps the weight itself). The producer's lanes 0-3 copy a stage's four scales with its
+//    tiles, 16 bytes beside 2 to 8 KB. A block whose scale is not in [2^-48, 2^48] counts as a missing tile.
+//  * cap: z = cap tanh(s / cap), one tanhf per lane and pass (each lane holds one score), in the shadow of
+//    the 64 to 256 packed FMAs of the pass. The hardware's tanh.approx is off by 2^-11, too much for a
+//    logit of tens.
+//  * distance: z -= slope |p - j|.
+//  * key ranges: the producer cuts the unit to the keys its vectors see (whole 16-position tiles), the
+//    consumers mask the rest. A page that no row sees is not read, so it may be gone from the table.
+template <class PT, class QT, int D, int X = 0>
+__global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D, X>::kMinBlocks)
     decode_partial_kernel(DecodeParams p) {
-  using C = DecodeCfg<PT, QT, D>;
+  using C = DecodeCfg<PT, QT, D, X>;
+  constexpr bool kMod = (X & kScoreMod) != 0;
   constexpr int NS = C::kStages;
   constexpr int LPT = C::kLPT;
   constexpr int TPG = C::kTPG;
@@ -238,7 +267,7 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
   constexpr int NW = kConsumerWarps;
 
   extern __shared__ __align__(1024) char smem_raw[];
-  SmemLayout sm = Carver<C>::carve(smem_raw);
+  SmemLayout<C> sm = Carver<C>::carve(smem_raw);
   volatile int* abort_flag = sm.flags;
 
   const int warp = threadIdx.x >> 5;
@@ -297,16 +326,50 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
       const int rem = u - e_idx * unit_span;
       const int h = p.row_blocks == 1 ? rem : rem / p.row_blocks;
       const int rb = rem - h * p.row_blocks;
-      const Entry en = p.entries[e_idx];   // carries its sequence's length and split count
+      Entry en = p.entries[e_idx];   // carries its sequence's length and split count
       int u_next = 0;
       if (lane == 0) u_next = atomicAdd(&p.header[1], 1);
+      int v_lo[kQB], v_hi[kQB], v_at[kQB];   // kMod: range, position and bias of the unit's vectors
+      float v_slope[kQB];
+      int all_lo = 0, all_hi = 0;
+      bool nothing = false;   // no vector of the unit sees a key of the split: one stage without a tile
+      if constexpr (kMod) {   // lane l reads vector l & 3's
+        const int v = rb * kQB + (lane & (kQB - 1));
+        const bool vq = v < RG;
+        const int r = vq ? v / p.group : 0;
+        const KeyRange kr = vq ? key_range(p, en.b, r, en.len) : KeyRange{0, 0};
+        const float slope = vq && p.slopes ? p.slopes[h * p.group + (v - r * p.group)] * kLog2e : 0.f;
+#pragma unroll
+        for (int i = 0; i < kQB; ++i) {
+          v_lo[i] = __shfl_sync(0xffffffffu, kr.lo, i);
+          v_hi[i] = __shfl_sync(0xffffffffu, kr.hi, i);
+          v_at[i] = __shfl_sync(0xffffffffu, en.len - p.rows + r, i);
+          v_slope[i] = __shfl_sync(0xffffffffu, slope, i);
+        }
+        // the keys some vector sees, and the keys every vector sees, over lanes 0-3 (alike in every four)
+        int lo = kr.hi > kr.lo ? kr.lo : INT_MAX, hi = kr.hi;
+        all_lo = vq ? kr.lo : 0;
+        all_hi = vq ? kr.hi : INT_MAX;
+#pragma unroll
+        for (int o = 1; o < kQB; o <<= 1) {
+          lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+          hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+          all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
+          all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
+        }
+        lo = max(en.start, lo & ~(kTileN - 1));
+        hi = min(en.end, hi);
+        nothing = hi <= lo;
+        en.start = nothing ? en.start : lo;
+        en.end = nothing ? en.start : hi;
+      }
       if (lane == 0) {
-        UnitMeta mt;
+        typename C::Meta mt;
         mt.b = en.b;
         mt.s = en.s;
         mt.h = h;
         mt.start = en.start;
-        mt.end = en.end;
+        mt.end = kMod && nothing ? en.end + 1 : en.end;
         mt.n_splits = en.n_splits;
         const int q0 = rb * kQB;
         const int nvalid = min(kQB, RG - q0);
@@ -325,6 +388,17 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
             ++r;
           }
         }
+        if constexpr (kMod) {
+          mt.all_lo = all_lo;
+          mt.all_hi = all_hi - 1;
+#pragma unroll
+          for (int i = 0; i < kQB; ++i) {
+            mt.lo[i] = v_lo[i];
+            mt.pos[i] = v_hi[i] - 1;
+            mt.at[i] = v_at[i];
+            mt.slope[i] = v_slope[i];
+          }
+        }
         sm.meta[slot] = mt;
         mbar_arrive_expect_tx(&sm.qfull[slot], static_cast<uint32_t>(nvalid * D * QT::kBytes));
         for (int i = 0; i < nvalid; ++i)
@@ -339,7 +413,7 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
       int my_page = (pc + lane <= last_page) ? bt_row[pc + lane] : -1;
       // page index and position in the page of the next tile, advanced tile by tile (no division)
       int t_pi = pc, t_po = en.start - pc * P;
-      for (int n0 = en.start; n0 < en.end; n0 += C::kStageTok) {
+      for (int n0 = en.start; n0 < en.end || (kMod && nothing && n0 == en.start); n0 += C::kStageTok) {
         int pages[2], pofs[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -413,6 +487,13 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
               cp_async16(dst + hf * C::kTileBytes + c * 16, ks + c * 16);
               cp_async16(dst + C::kHalfBytes + hf * C::kTileBytes + c * 16, vs + c * 16);
             }
+            if constexpr (C::kBlk) {   // lanes 0 and 1: the tile's K and V scale
+              if (lane < 2) {
+                const int64_t blk = (static_cast<int64_t>(pages[hf]) * p.h_kv + h) * (P / p.scale_tokens) +
+                                    pofs[hf] / p.scale_tokens;
+                cp_async4(smem_u32(sm.scales + stage * 4 + lane * 2 + hf), (lane ? p.v_scales : p.k_scales) + blk);
+              }
+            }
           }
           cp_async_arrive_noinc(&sm.full[stage]);
         }
@@ -466,7 +547,7 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
       break;
     }
     // the unit's metadata stays in its shared slot until this unit's epilogue is done
-    const UnitMeta* mtp = &sm.meta[slot];
+    const typename C::Meta* mtp = &sm.meta[slot];
     const int u_b = mtp->b;
     if (u_b < 0) break;
     const int u_start = mtp->start, u_end = mtp->end, u_nvec = mtp->nvec;
@@ -490,6 +571,13 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
       }
     }
     const int pos_sel = mtp->pos[vsel];   // last visible key of vector vsel
+    int lo_sel = 0, at_sel = 0;           // kMod: its first visible key, its position, its bias per position
+    float slope_sel = 0.f;
+    if constexpr (kMod) {
+      lo_sel = mtp->lo[vsel];
+      at_sel = mtp->at[vsel];
+      slope_sel = mtp->slope[vsel];
+    }
 
     float m_run = -INFINITY;
     float l_run = 0.f;
@@ -507,12 +595,28 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
         ok = false;
         break;
       }
-      const int okbits = sm.stage_ok[stage];
+      int okbits = sm.stage_ok[stage];
+      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};   // kBlk: scales of the stage's two tiles
+      if constexpr (C::kBlk) {
+        const uint4 w = lds128(smem_u32(sm.scales + stage * 4));
+        ks[0] = __uint_as_float(w.x), ks[1] = __uint_as_float(w.y);
+        vs[0] = __uint_as_float(w.z), vs[1] = __uint_as_float(w.w);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const bool fit = ks[hf] >= kMinScale && ks[hf] <= kMaxScale && vs[hf] >= kMinScale && vs[hf] <= kMaxScale;
+          if (((okbits >> hf) & 1) && !fit) {
+            okbits &= ~(1 << hf);
+            if (lane == 0) raise_status(p.status, NBX_DEV_BAD_SCALE);
+          }
+        }
+      }
       if (okbits) {
         const int n0 = u_start + t * C::kStageTok;
         // every position of the stage copied, inside the split, and seen by every vector of the unit
         // (vector 0 has the unit's smallest causal limit)
-        const bool full_stage = (okbits == 3) && (n0 + C::kStageTok <= u_end) && (n0 + C::kStageTok - 1 <= mtp->pos[0]);
+        bool full_stage = (okbits == 3) && (n0 + C::kStageTok <= u_end);
+        if constexpr (kMod) full_stage = full_stage && n0 >= mtp->all_lo && n0 + C::kStageTok - 1 <= mtp->all_hi;
+        else full_stage = full_stage && (n0 + C::kStageTok - 1 <= mtp->pos[0]);
         const uint32_t st_base = stages_base + stage * C::kStageBytes;
 #pragma unroll 1
         for (int pass = 0; pass < C::kWarpPasses; ++pass) {
@@ -567,7 +671,13 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
           }
           const int rs = pbase + tg * TPG + tsel;   // this lane's position inside the stage
           const int n = n0 + rs;
-          const bool valid = ((okbits >> (rs / kTileN)) & 1) && (n < u_end) && (n <= pos_sel);
+          bool valid = ((okbits >> (rs / kTileN)) & 1) && (n < u_end) && (n <= pos_sel);
+          if constexpr (C::kBlk) mine *= rs < kTileN ? ks[0] : ks[1];
+          if constexpr (kMod) {
+            valid = valid && n >= lo_sel;
+            if (p.cap_log2 > 0.f) mine = p.cap_log2 * tanhf(mine * p.cap_inv);
+            mine = fmaf(-slope_sel, static_cast<float>(abs(at_sel - n)), mine);
+          }
           const float s = valid ? mine : -INFINITY;
           // ---- online softmax, lazy rescale; the max runs over the lanes holding the same vector
           // (NaN-propagating max: a NaN score makes the running max NaN, so it reaches the output)
@@ -594,7 +704,8 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
           }
           const float pw = valid ? fast_exp2(s - m_run) : 0.f;
           l_run += pw;
-          if (p_writer) sts64(p_store, pack2(pw, pw));
+          const float pv = C::kBlk ? pw * (rs < kTileN ? vs[0] : vs[1]) : pw;
+          if (p_writer) sts64(p_store, pack2(pv, pv));
           __syncwarp();
           // ---- acc_i += p_i,n * v_n over this pass's positions (no per-position test in full stages)
           if (full_stage) {
@@ -607,8 +718,11 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
             for (int pt = 0; pt < C::kPassTok; ++pt) {
               const int n = n0 + pbase + pt;
               if (((okbits >> ((pbase + pt) / kTileN)) & 1) && n < u_end) {
-                const int mask = (n <= mtp->pos[0] ? 1 : 0) | (n <= mtp->pos[1] ? 2 : 0) | (n <= mtp->pos[2] ? 4 : 0) |
-                                 (n <= mtp->pos[3] ? 8 : 0);
+                int mask = (n <= mtp->pos[0] ? 1 : 0) | (n <= mtp->pos[1] ? 2 : 0) | (n <= mtp->pos[2] ? 4 : 0) |
+                           (n <= mtp->pos[3] ? 8 : 0);
+                if constexpr (kMod)
+                  mask &= (n >= mtp->lo[0] ? 1 : 0) | (n >= mtp->lo[1] ? 2 : 0) | (n >= mtp->lo[2] ? 4 : 0) |
+                          (n >= mtp->lo[3] ? 8 : 0);
                 pv_step_masked<PT, VPL>(pb_addr + pt * kQB * 8, st_base + v_lane_off + (pbase + pt) * D * PT::kBytes,
                                         acc2, mask);
               }
@@ -706,7 +820,9 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
       if (r_row[x] < 0) continue;
       const int dd = (ct + x * NW * 32) % D;
       if (!multi) {
-        p.out[r_row[x] * D + dd] = (r_m[x] == -INFINITY) ? 0.f : r_a[x] * (p.v_scale / r_l[x]);
+        const float o = (r_m[x] == -INFINITY) ? 0.f : r_a[x] * (p.v_scale / r_l[x]);
+        if (X != 0 && p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[r_row[x] * D + dd] = __float2bfloat16_rn(o);
+        else p.out[r_row[x] * D + dd] = o;
       } else {
         // the partial stays in L2 for the merge
         const uint64_t keep = l2_keep_policy(p.keep_frac);
@@ -735,15 +851,15 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D>::kMinBloc
 }
 
 // ------------------------------------------------------------------------------------ launch
-template <class PT, class QT, int D>
+template <class PT, class QT, int D, int X = 0>
 cudaError_t launch_decode(const DecodeParams& p, int grid_limit, cudaStream_t stream) {
-  using C = DecodeCfg<PT, QT, D>;
+  using C = DecodeCfg<PT, QT, D, X>;
   constexpr int smem = Carver<C>::bytes();
   static_assert(smem <= C::kSmemPerCta, "shared memory per CTA");
   const DeviceInfo& di = device_info();
   static int configured_for = -1;
   if (configured_for != di.device) {
-    cudaError_t e = cudaFuncSetAttribute(decode_partial_kernel<PT, QT, D>,
+    cudaError_t e = cudaFuncSetAttribute(decode_partial_kernel<PT, QT, D, X>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     configured_for = di.device;
@@ -753,23 +869,34 @@ cudaError_t launch_decode(const DecodeParams& p, int grid_limit, cudaStream_t st
   if (grid_limit > 0 && grid > grid_limit) grid = grid_limit;
   if (grid > upper) grid = upper;
   if (grid < 1) grid = 1;
-  return launch_pdl(decode_partial_kernel<PT, QT, D>, static_cast<unsigned>(grid), kDecodeThreads, smem, stream, p);
+  return launch_pdl(decode_partial_kernel<PT, QT, D, X>, static_cast<unsigned>(grid), kDecodeThreads, smem, stream, p);
 }
 
-#define NBX_DECODE_FOR_POOL(PT)                                                                                   \
-  cudaError_t decode_dispatch_##PT(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream) {     \
-    if (q_dtype == NBX_F32) {                                                                                      \
-      if (p.d == 64) return launch_decode<PT, F32, 64>(p, grid_limit, stream);                                     \
-      if (p.d == 128) return launch_decode<PT, F32, 128>(p, grid_limit, stream);                                   \
-      return launch_decode<PT, F32, 256>(p, grid_limit, stream);                                                   \
-    }                                                                                                              \
-    if (p.d == 64) return launch_decode<PT, BF16, 64>(p, grid_limit, stream);                                      \
-    if (p.d == 128) return launch_decode<PT, BF16, 128>(p, grid_limit, stream);                                    \
-    return launch_decode<PT, BF16, 256>(p, grid_limit, stream);                                                    \
+template <class PT, int X>
+cudaError_t decode_dispatch_pool(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream) {
+  if (q_dtype == NBX_F32) {
+    if (p.d == 64) return launch_decode<PT, F32, 64, X>(p, grid_limit, stream);
+    if (p.d == 128) return launch_decode<PT, F32, 128, X>(p, grid_limit, stream);
+    return launch_decode<PT, F32, 256, X>(p, grid_limit, stream);
+  }
+  if (p.d == 64) return launch_decode<PT, BF16, 64, X>(p, grid_limit, stream);
+  if (p.d == 128) return launch_decode<PT, BF16, 128, X>(p, grid_limit, stream);
+  return launch_decode<PT, BF16, 256, X>(p, grid_limit, stream);
+}
+
+// One definition per translation unit, so that the instantiations compile in parallel.
+#define NBX_DECODE_FOR_POOL(NAME, PT, X)                                                                        \
+  cudaError_t decode_dispatch_##NAME(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream) { \
+    return decode_dispatch_pool<PT, X>(p, q_dtype, grid_limit, stream);                                         \
   }
 
 cudaError_t decode_dispatch_F32(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
 cudaError_t decode_dispatch_BF16(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
 cudaError_t decode_dispatch_E4M3(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
+cudaError_t decode_dispatch_F32_mod(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
+cudaError_t decode_dispatch_BF16_mod(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
+cudaError_t decode_dispatch_E4M3_mod(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
+cudaError_t decode_dispatch_E4M3_block(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
+cudaError_t decode_dispatch_E4M3_block_mod(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
 
 }  // namespace nbx

@@ -125,7 +125,7 @@ struct SeqPlan {
   int32_t len;       // positions read (0 if the length was out of bounds)
   int32_t seg;       // positions per split (a whole number of pages)
   int32_t n_splits;  // non-empty splits: ceil(len / seg)
-  int32_t pad;
+  int32_t first;     // first position of the first split (0 but with key ranges)
 };
 
 // One (sequence, split) of the work list; a work unit is (entry, KV head, row block). The
@@ -146,6 +146,8 @@ struct WorkspaceLayout {
   size_t l_part;    // f32[batch * rows * h_q * max_splits]
   size_t acc_part;  // f32[batch * rows * h_q * max_splits * d]
   size_t total;
+  size_t ranges;    // int2[batch * M tiles of 128 vectors], after `total`: modified decodes only
+  size_t total_mod;
   int max_splits;
   int row_blocks;
 };
@@ -205,12 +207,45 @@ struct DecodeParams {
   // len / 64)]
   int tc_units;
   int tc_pairs;
+  // ---- read only by the kernels of the modified and block-scaled decodes (kScoreMod, kBlockScaled)
+  int out_bf16;            // the output is bf16, rounded once from the fp32 result
+  float cap_log2;          // softcap * log2(e), and its reciprocal; 0: no cap
+  float cap_inv;
+  const float* slopes;     // [h_q] bias per position of distance, or null
+  const int32_t* key_begin;   // [batch, rows] first visible key and one past the last, or null (0, p + 1)
+  const int32_t* key_end;
+  const float* k_scales;   // [num_pages, h_kv, page_tokens / scale_tokens]
+  const float* v_scales;
+  int scale_tokens;
+  int2* ranges;            // [batch, range_tiles] keys the rows of a sequence's M tile see (SIMT: of the sequence)
+  int range_tiles;
 };
+
+// What a decode adds to the plain one, as a template argument of its kernels: score modifications (a cap,
+// a bias by distance, per-row key ranges), pools with a scale per block. Plain calls run instantiations
+// without any of it.
+constexpr int kScoreMod = 1;
+constexpr int kBlockScaled = 2;
+
+// The visible keys of query row r of a sequence of len positions: [lo, hi), empty as lo = hi = 0.
+struct KeyRange {
+  int lo, hi;
+};
+#ifdef __CUDACC__
+__device__ __forceinline__ KeyRange key_range(const DecodeParams& p, int b, int r, int len) {
+  const int64_t i = static_cast<int64_t>(b) * p.rows + r;
+  const int lo = p.key_begin ? max(0, p.key_begin[i]) : 0;
+  const int hi = min(len, p.key_end ? p.key_end[i] : len - p.rows + r + 1);
+  return hi > lo ? KeyRange{lo, hi} : KeyRange{0, 0};
+}
+#endif
 
 cudaError_t bounds_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, float* q_norm, float* kv_max,
                             cudaStream_t stream);
 
-cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, int grid_limit, cudaStream_t stream);
+// x: 0, or kScoreMod and kBlockScaled bits of a modified decode
+cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, int x, int grid_limit,
+                            cudaStream_t stream);
 
 // The tensor-core partial kernel: used when the query vectors of one KV head fill an MMA tile
 // (rows x group >= 64), q is bf16, the pools bf16 (kind::f16) or E4M3 (kind::f8f6f4 on the codes),

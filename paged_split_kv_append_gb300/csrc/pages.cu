@@ -239,10 +239,10 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
   if (tid == 0) *p.n_moves = n_copy;
 }
 
-// Step 3, one warp per fork: the destination's row and length.
+// Step 3, one warp per fork: the destination's row and length. (It lets no dependent start early: the
+// plan of a decode launched next reads the lengths before it waits for the grid ahead of it.)
 __global__ void __launch_bounds__(256) fork_rows_kernel(ForkParams p) {
   pdl_wait();
-  pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int warp = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
   const int n_warps = static_cast<int>((gridDim.x * blockDim.x) >> 5);

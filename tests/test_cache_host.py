@@ -80,6 +80,40 @@ def test_compact_refusals(lib, want, kw):
     assert call(lib.nbx_paged_kv_compact, COMPACT, **kw) == want
 
 
+SIZES = dict(q=FAKE, q_dtype=1, batch=2, rows=1, h_q=8, d=128, k_pool=FAKE, v_pool=FAKE)
+TAIL = dict(softcap=0.0, slopes=NULL, kb=NULL, ke=NULL, out=FAKE, out_dtype=0, ws=FAKE, ws_bytes=1 << 30, status=NULL,
+            stream=NULL)
+MODIFIED = dict(**SIZES, pool_dtype=1, num_pages=100, h_kv=2, page_tokens=32, bt=FAKE, max_pages=10, lens=FAKE,
+                max_seq_len=160, scale=0.1, k_scale=1.0, v_scale=1.0, **TAIL)
+BLOCK = dict(**SIZES, ks=FAKE, vs=FAKE, block=16, num_pages=100, h_kv=2, page_tokens=32, bt=FAKE, max_pages=10, lens=FAKE,
+             max_seq_len=160, scale=0.1, **TAIL)
+BAD_DECODE = [(0, dict(batch=0)), (-1, dict(q=NULL)), (-1, dict(out=NULL)), (-1, dict(bt=NULL)), (-1, dict(ws=NULL)),
+              (-2, dict(h_q=9)), (-2, dict(d=96)), (-2, dict(rows=0)), (-2, dict(max_seq_len=321)), (-3, dict(q_dtype=2)),
+              (-3, dict(out_dtype=2)), (-4, dict(page_tokens=40, max_seq_len=100)), (-5, dict(ws_bytes=1000)),
+              (-7, dict(out=FAKE_ODD)), (-7, dict(q=FAKE_ODD)), (-7, dict(ws=ctypes.c_void_p(0x10010))),
+              (-8, dict(scale=float("nan"))), (-8, dict(softcap=-1.0)), (-8, dict(softcap=float("inf"))),
+              (-8, dict(softcap=float("nan"))), (-8, dict(softcap=1e-40))]
+
+
+@pytest.mark.parametrize("want,kw", BAD_DECODE + [(-3, dict(pool_dtype=7)), (-8, dict(v_scale=0.0))])
+def test_modified_decode_refusals(lib, want, kw):
+    assert call(lib.nbx_paged_decode_attn_modified, MODIFIED, **kw) == want
+
+
+@pytest.mark.parametrize("want,kw", BAD_DECODE + [(-1, dict(ks=NULL)), (-4, dict(block=0)), (-4, dict(block=24)),
+                                                  (-4, dict(block=64))])
+def test_block_scaled_decode_refusals(lib, want, kw):
+    assert call(lib.nbx_paged_decode_attn_block_scaled, BLOCK, **kw) == want
+
+
+def test_modified_decode_workspace(lib):
+    f = lib.nbx_paged_decode_modified_workspace_bytes
+    assert f(2, 1, 8, 3, 128, 100) == 0
+    n = f(2, 1, 8, 2, 128, 160)
+    assert n >= lib.nbx_paged_decode_workspace_bytes(2, 1, 8, 2, 128, 160)
+    assert call(lib.nbx_paged_decode_attn_modified, MODIFIED, ws_bytes=n - 1) == -5
+
+
 def test_page_workspaces(lib):
     assert lib.nbx_paged_kv_fork_workspace_bytes(-1, 4, 2, 8) == 0
     assert lib.nbx_paged_kv_fork_workspace_bytes(5, 4, 2, 0) == 0

@@ -1,0 +1,362 @@
+"""The block-scaled decode and the score modifications against their definition in 64 bits (oracle.cache).
+
+Tolerances, from the arithmetic. A weight's relative error is that of its score plus that of 2^x (2^-22).
+A score is a sum of d products rounded at most 16 times on its way (8 fused pairs a lane, the pair, a tree
+of four, the scale, the block's scale), so it is off by 2^-20 Z, Z = scale |q| |k| a bound on the scores; a
+cap or a bias adds less. Sums of weights and of weighted values are fp32, at most 512 terms in a row and 64
+splits, hence 2^-14.8 in the worst case. The output is a weighted mean of the values, off by twice the
+weights' error times the largest value: max|v| (2^-19 Z + 2^-14). On tensor cores a bf16 window holds P to
+2^-17 (two bf16 terms), and an E4M3 window P to 2^-9 (two E4M3 terms, with the floors of small weights
+within 2^-8 of the sum) and q to 2^-9 of its largest element at worst. A bf16 output adds half a step: 2^-8.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.cache as oc
+import oracle.formats as of
+import paged_split_kv_append_gb300 as nbx
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+OUT = {"f32": torch.float32, "bf16": torch.bfloat16}
+EDGE_LENS = (0, 1, 15, 16, 17, 100, 255, 256, 257, 513, 1100)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    nbx.build()
+    nbx.nbx_set_decode_grid_limit(0)
+    yield
+    nbx.nbx_set_decode_grid_limit(0)
+
+
+class Case:
+    """One decode on both sides. pool: f32, bf16, e4m3 (one scale), block (a scale per T positions)."""
+
+    def __init__(self, pool, q_type, rows, h_q, h_kv, d, P, lens, T=0, seed=0, magnitude=1.0, two=True):
+        g = np.random.default_rng(seed)
+        self.pool, self.T, self.P, self.d, self.rows, self.h_q = pool, T, P, d, rows, h_q
+        self.lens = np.asarray(lens, dtype=np.int32)
+        B = len(lens)
+        need = [-(-int(n) // P) for n in lens]
+        self.num_pages = sum(need) + 2
+        self.width = max(1, max(need)) + 1
+        ids = g.permutation(self.num_pages).astype(np.int32)
+        self.table = np.full((B, self.width), -1, dtype=np.int32)
+        at = 0
+        for b, k in enumerate(need):
+            self.table[b, :k] = ids[at:at + k]
+            at += k
+        self.scale = 1.0 / math.sqrt(d)
+        shape = (self.num_pages, h_kv, P, d)
+        self.kw, self.scales, self.codes = {}, [None, None], []
+        for w in range(2):
+            x = (g.standard_normal(shape) * np.exp(0.5 * g.standard_normal(shape[:3] + (1,)))).astype(np.float32)
+            x *= magnitude
+            if pool == "block":
+                s = np.exp2(g.integers(-9, -5, shape[:2] + (P // T,))).astype(np.float32) * np.float32(magnitude)
+                if not two:
+                    s *= g.uniform(0.6, 1.0, s.shape).astype(np.float32)
+                self.scales[w] = s
+                x = x / np.repeat(s, T, axis=2)[..., None]
+            elif pool == "e4m3":
+                self.kw["kv"[w] + "_scale"] = float(np.float32(np.abs(x).max() / 448))
+                x = x / self.kw["kv"[w] + "_scale"]
+            self.codes.append(of.encode(x, "e4m3" if pool == "block" else pool))
+        kind = "e4m3" if pool == "block" else pool
+        self.values = [oc.pool_values(c, kind, self.kw.get("kv"[w] + "_scale", 1.0), self.scales[w])
+                       for w, c in enumerate(self.codes)]
+        # what no sequence holds is NaN on the device
+        nan = {"f32": np.float32("nan"), "bf16": np.uint16(0x7FC0), "e4m3": np.uint8(0x7F)}[kind]
+        held = np.zeros(shape[:1] + shape[2:3], dtype=bool)
+        for b in range(B):
+            for j in range(int(lens[b])):
+                held[self.table[b, j // P], j % P] = True
+        self.dev = []
+        for c in self.codes:
+            c = c.copy()
+            c[np.broadcast_to(~held[:, None, :, None], c.shape)] = nan
+            t = torch.from_numpy(c.view(np.int16) if kind == "bf16" else c).to(DEV)
+            self.dev.append(t.view(torch.bfloat16) if kind == "bf16" else t)
+        q = torch.from_numpy(g.standard_normal((B, rows, h_q, d)).astype(np.float32))
+        self.q = q.to(torch.bfloat16 if q_type == "bf16" else torch.float32)
+
+    def call(self, out_type="f32", softcap=0.0, slopes=None, key_begin=None, key_end=None, table=None, **kw):
+        i32 = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(DEV)  # noqa: E731
+        args = dict(softcap=softcap, slopes=None if slopes is None else torch.tensor(slopes, device=DEV),
+                    key_begin=i32(key_begin), key_end=i32(key_end), out_dtype=OUT[out_type], **kw)
+        most = max(1, int(self.lens.max()))
+        t, n = i32(self.table if table is None else table), i32(self.lens)
+        if self.pool == "block":
+            s = [torch.from_numpy(x).to(DEV) if isinstance(x, np.ndarray) else x for x in self.scales]
+            return nbx.nbx_paged_decode_attn_block_scaled(self.q.to(DEV), *self.dev, *s, t, n, most, self.scale, **args)
+        return nbx.nbx_paged_decode_attn_modified(self.q.to(DEV), *self.dev, t, n, most, self.scale, **self.kw, **args)
+
+    def tolerance(self, out_type, weight=0.0):
+        z = self.scale * float(np.linalg.norm(self.q.float().numpy(), axis=-1).max()) * \
+            float(np.linalg.norm(self.values[0], axis=-1).max())
+        v = float(np.abs(self.values[1]).max())
+        return v * (2.0 ** -19 * z + 2.0 ** -14 + 2 * weight + (2.0 ** -8 if out_type == "bf16" else 0.0))
+
+    def check(self, out_type="f32", weight=0.0, **mod):
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = self.call(out_type, status=status, **mod)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        ref = oc.attention(self.q.float().numpy(), *self.values, self.table, self.lens, self.scale, **mod)
+        got = out.double().cpu().numpy()
+        assert np.all(np.isfinite(got))
+        err = float(np.abs(got - ref).max())
+        tol = self.tolerance(out_type, weight)
+        assert err <= tol, f"error {err:.3e}, tolerance {tol:.3e}"
+        empty = np.all(ref == 0, axis=-1)
+        assert np.all(got[empty] == 0)
+        return out
+
+
+def slopes_for(h):
+    return [2.0 ** (-8.0 * (i + 1) / h) for i in range(h)]
+
+
+def ranges(kind, lens, rows, seed=0):
+    """(key_begin, key_end) [B, rows]."""
+    n = np.asarray(lens, dtype=np.int64)[:, None]
+    p = n - rows + np.arange(rows)[None, :]
+    if kind == "documents":
+        return np.maximum(p, 0) // 100 * 100, p + 1
+    if kind == "prefix":
+        return None, np.maximum(p + 1, 70)
+    if kind == "window":
+        return np.maximum(0, p + 1 - 37), None
+    g = np.random.default_rng(seed)
+    lo = g.integers(-5, np.maximum(n, 1) + 5, p.shape)        # anything: empty rows, ends before starts, outside
+    return lo, lo + g.integers(-20, 400, p.shape)
+
+
+SIMT = [("f32", "f32", 1, 4, 2, 64, 16, 0), ("bf16", "bf16", 1, 32, 8, 128, 16, 0), ("bf16", "f32", 3, 12, 4, 256, 64, 0),
+        ("e4m3", "bf16", 1, 8, 8, 128, 32, 0), ("e4m3", "f32", 5, 6, 2, 64, 16, 0), ("block", "bf16", 1, 32, 8, 128, 16, 16),
+        ("block", "f32", 2, 6, 1, 256, 64, 32), ("block", "bf16", 7, 8, 2, 64, 128, 128), ("f32", "bf16", 4, 5, 1, 128, 512, 0),
+        ("block", "bf16", 1, 7, 1, 128, 48, 16)]
+MODS = [dict(), dict(softcap=2.0), dict(slopes=True), dict(mask="documents"), dict(mask="prefix"), dict(mask="window"),
+        dict(mask="random", softcap=5.0, slopes=True)]
+
+
+def made(mod, lens, rows, h_q):
+    m = {k: v for k, v in mod.items() if k == "softcap"}
+    if "slopes" in mod:
+        m["slopes"] = np.float32(slopes_for(h_q)).tolist()
+    if "mask" in mod:
+        m["key_begin"], m["key_end"] = ranges(mod["mask"], lens, rows)
+    return m
+
+
+@pytest.mark.parametrize("mod", MODS, ids=lambda m: "-".join(str(v) for v in m.values()) or "plain")
+@pytest.mark.parametrize("pool,q_type,rows,h_q,h_kv,d,P,T", SIMT)
+def test_single_rows_and_short_windows(pool, q_type, rows, h_q, h_kv, d, P, T, mod):
+    c = Case(pool, q_type, rows, h_q, h_kv, d, P, EDGE_LENS, T, seed=1, two=(rows == 1))
+    for out_type in ("f32", "bf16"):
+        c.check(out_type, **made(mod, EDGE_LENS, rows, h_q))
+
+
+def test_a_cap_on_large_scores():
+    # scores up to a hundred times the cap, and far under it
+    for magnitude in (100.0, 1e-3):
+        c = Case("bf16", "f32", 1, 8, 2, 128, 16, (1, 40, 700), seed=2, magnitude=magnitude)
+        out = c.call(softcap=30.0)
+        ref = oc.attention(c.q.numpy(), *c.values, c.table, c.lens, c.scale, softcap=30.0)
+        # capped scores are off by at most 30 * 2^-22 (tanhf) and what is left of the score's own error there,
+        # s 2^-20 tanh'(s / 30) <= 30 * 2^-20
+        tol = float(np.abs(c.values[1]).max()) * (2 * 30 * 2.0 ** -19 + 2.0 ** -14)
+        assert np.abs(out.double().cpu().numpy() - ref).max() <= tol
+
+
+def test_slopes_of_any_sign_and_size():
+    c = Case("bf16", "bf16", 2, 8, 2, 128, 16, (3, 600, 1500), seed=3)
+    for s in (0.0, -0.01, 1e4, 1e-8):
+        c.check(slopes=[s] * 8)
+    c.check(slopes=[1e30] * 8)          # all weight on the row's own position
+
+
+def test_pages_no_row_sees_may_be_gone():
+    # a window of 37 keys: the pages before it are -1, as a serving loop frees them; and out of the pool
+    for pool, T in (("bf16", 0), ("block", 16)):
+        c = Case(pool, "bf16", 3, 8, 2, 128, 16, (600, 1300, 40), T, seed=4)
+        lo, _ = ranges("window", c.lens, 3)
+        whole = c.call(key_begin=lo)
+        t = c.table.copy()
+        for b in range(3):
+            t[b, : int(lo[b].min()) // 16] = -1 if b else 10 ** 6
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = c.call(key_begin=lo, table=t, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0 and torch.equal(out, whole)
+
+
+def test_nan_and_infinity_outside_the_ranges_stay_outside():
+    for pool in ("f32", "bf16"):
+        c = Case(pool, "f32", 4, 4, 1, 64, 16, (300,), seed=5)
+        lo, hi = np.array([[50, 60, 70, 0]]), np.array([[100, 61, 200, 0]])
+        ref = oc.attention(c.q.numpy(), *c.values, c.table, c.lens, c.scale, key_begin=lo, key_end=hi)
+        for j, bad in ((49, "nan"), (200, "inf"), (10, "-inf"), (299, "nan")):
+            for w in range(2):
+                c.dev[w][c.table[0, j // 16], :, j % 16] = float(bad)
+        out = c.call(key_begin=lo, key_end=hi).double().cpu().numpy()
+        assert np.abs(out - ref).max() <= c.tolerance("f32")
+        # a NaN that is seen reaches the rows that see it, and no other
+        c.dev[0][c.table[0, 60 // 16], :, 60 % 16] = float("nan")
+        out = c.call(key_begin=lo, key_end=hi).cpu().numpy()
+        assert np.all(np.isnan(out[0, :2])) and np.all(np.isfinite(out[0, 2:]))
+
+
+def test_without_modifications_it_is_the_plain_decode():
+    c = Case("bf16", "bf16", 1, 32, 8, 128, 16, (5, 900, 2000), seed=6)
+    i32 = lambda a: torch.from_numpy(a).to(DEV)   # noqa: E731
+    plain = nbx.nbx_paged_decode_attn(c.q.to(DEV), *c.dev, i32(c.table), i32(c.lens), 2000, c.scale)
+    assert torch.equal(plain, c.call())
+    # a range that hides nothing, slopes of 0: the same sums in the same order
+    assert torch.equal(plain, c.call(slopes=[0.0] * 32))
+    assert torch.equal(plain.to(torch.bfloat16), c.call("bf16"))
+
+
+def test_block_scales_of_one_are_the_plain_decode():
+    c = Case("block", "bf16", 1, 32, 8, 128, 16, (5, 900, 2000), 16, seed=7)
+    c.scales = [np.ones_like(s) for s in c.scales]
+    i32 = lambda a: torch.from_numpy(a).to(DEV)   # noqa: E731
+    plain = nbx.nbx_paged_decode_attn(c.q.to(DEV), *c.dev, i32(c.table), i32(c.lens), 2000, c.scale)
+    assert torch.equal(plain, c.call())
+
+
+def test_scales_at_the_ends_of_their_range():
+    # a block of tiny values beside a block of large ones: the weights of both count
+    c = Case("block", "f32", 1, 4, 1, 128, 16, (64, 33), 16, seed=8)
+    g = np.random.default_rng(8)
+    c.scales[1] = np.where(g.random(c.scales[1].shape) < 0.5, np.float32(2.0 ** -48), np.float32(2.0 ** 48))
+    c.values[1] = oc.pool_values(c.codes[1], "e4m3", scales=c.scales[1])
+    out = c.call().double().cpu().numpy()
+    ref = oc.attention(c.q.numpy(), *c.values, c.table, c.lens, c.scale)
+    assert np.abs(out - ref).max() <= c.tolerance("f32")
+
+
+@pytest.mark.parametrize("bad", [0.0, -1.0, float("nan"), float("inf"), 2.0 ** -49, 2.0 ** 49])
+def test_a_bad_scale_sets_its_bit_and_its_block_is_skipped(bad):
+    c = Case("block", "bf16", 1, 8, 2, 128, 32, (200, 90), 16, seed=9)
+    page = int(c.table[0, 2])
+    for w in range(2):
+        c.scales[w] = torch.from_numpy(c.scales[w]).to(DEV)
+        good = c.scales[w].clone()
+        c.scales[w][page, 1, 1] = bad
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = c.call(status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == nbx.DEV_BAD_SCALE
+        c.scales[w] = good
+        # positions 80..95 of KV head 1 of sequence 0 are as if they were not there
+        keep = [j for j in range(200) if not 80 <= j < 96]
+        K, V = (x[c.table[0, :7].astype(int), 1].reshape(-1, 128)[keep] for x in c.values)
+        s = c.scale * (c.q[0, 0, 4:].double().numpy() @ K.T)
+        e = np.exp(s - s.max(-1, keepdims=True))
+        ref = e @ V / e.sum(-1, keepdims=True)
+        assert np.abs(out[0, 0, 4:].double().cpu().numpy() - ref).max() <= c.tolerance("f32")
+        assert torch.equal(out[1], c.call()[1])
+
+
+def test_bad_pages_and_lengths_are_reported():
+    c = Case("block", "bf16", 1, 8, 2, 128, 16, (200, 90), 16, seed=10)
+    t = c.table.copy()
+    t[0, 3] = -1
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = c.call(table=t, status=status, slopes=[0.1] * 8)
+    torch.cuda.synchronize()
+    assert int(status.item()) == nbx.DEV_BAD_PAGE and bool(torch.isfinite(out).all())
+    n = c.lens.copy()
+    c.lens = np.array([-1, 90], dtype=np.int32)
+    status.zero_()
+    out = c.call(status=status, key_begin=np.zeros((2, 1)))
+    torch.cuda.synchronize()
+    assert int(status.item()) == nbx.DEV_BAD_LEN and bool((out[0] == 0).all())
+    c.lens = n
+
+
+@pytest.mark.parametrize("pool,T", [("bf16", 0), ("block", 16)])
+def test_grid_size_and_page_ids_do_not_change_bits(pool, T):
+    c = Case(pool, "bf16", 2, 16, 4, 128, 16, (900, 3, 2000, 0, 700), T, seed=11)
+    mod = made(dict(mask="documents", softcap=3.0, slopes=True), c.lens, 2, 16)
+    ref = c.call(**mod)
+    for limit in (1, 7, 100):
+        nbx.nbx_set_decode_grid_limit(limit)
+        out = c.call(**mod)
+        nbx.nbx_set_decode_grid_limit(0)
+        assert torch.equal(out, ref)
+    perm = np.random.default_rng(12).permutation(c.num_pages)
+    inv = torch.from_numpy(np.argsort(perm)).to(DEV)
+    c.dev = [t[inv] for t in c.dev]
+    if T:
+        c.scales = [s[np.argsort(perm)] for s in c.scales]
+    t = np.where(c.table >= 0, perm[np.maximum(c.table, 0)], c.table)
+    assert torch.equal(c.call(table=t, **mod), ref)
+
+
+def test_more_sequences_than_the_plan_sorts():
+    B = 2100
+    lens = np.random.default_rng(13).integers(0, 40, B)
+    c = Case("block", "bf16", 1, 2, 1, 64, 16, lens, 16, seed=13)
+    c.check(**made(dict(mask="window", softcap=3.0), lens, 1, 2))
+
+
+def test_two_streams_and_a_replayed_graph():
+    c = Case("block", "bf16", 1, 8, 2, 128, 16, (900, 3, 2000), 16, seed=14)
+    i32 = lambda a: torch.from_numpy(a).to(DEV)   # noqa: E731
+    need = nbx.nbx_paged_decode_modified_workspace_bytes(3, 1, 8, 2, 128, 2000)
+    ws = [torch.empty(need, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    outs = [torch.zeros(c.q.shape, device=DEV) for _ in range(2)]
+    s = [torch.from_numpy(x).to(DEV) for x in c.scales]
+    q, t, n = c.q.to(DEV), i32(c.table), i32(c.lens)
+    run = lambda i, q: nbx.nbx_paged_decode_attn_block_scaled(q, *c.dev, *s, t, n, 2000, c.scale, softcap=4.0 + i,  # noqa: E731
+                                                             out=outs[i], workspace=ws[i])
+    ref = [run(i, q).clone() for i in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):         # both at once
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                run(i, q)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+    q2 = q.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(0, q2)
+    q2.copy_(torch.randn_like(q2.float()).to(q2.dtype))
+    g.replay()
+    torch.cuda.synchronize()
+    got = outs[0].clone()
+    assert torch.equal(got, run(0, q2))
+
+
+def test_refusals_of_the_bindings():
+    c = Case("block", "bf16", 1, 8, 2, 128, 32, (200, 90), 16, seed=15)
+    with pytest.raises(ValueError):
+        c.call(key_begin=np.zeros((2, 2)))
+    with pytest.raises(ValueError):
+        c.call(slopes=[0.1] * 7)
+    with pytest.raises(ValueError):
+        c.call(out=torch.empty((2, 1, 8, 64), device=DEV))
+    with pytest.raises(nbx.NbxError):
+        c.call(softcap=-1.0)
+    with pytest.raises(nbx.NbxError):
+        c.call(workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
+    with pytest.raises(TypeError):
+        nbx.nbx_paged_decode_attn_block_scaled(c.q.to(DEV), *c.dev, *[torch.from_numpy(x).to(DEV) for x in c.scales],
+                                               torch.from_numpy(c.table).to(DEV), torch.from_numpy(c.lens).to(DEV), 200,
+                                               c.scale, out_dtype=torch.float16)
+    half = [s[:, :, :1].copy() for s in c.scales]
+    c.scales = [half[0], c.scales[1]]
+    with pytest.raises(ValueError):
+        c.call()
