@@ -45,6 +45,7 @@ KERNEL_SOURCES = ("paged_split_kv_append_gb300/csrc/decode_kernels.cuh",
                   "paged_split_kv_append_gb300/csrc/nbx_device.cuh",
                   "paged_split_kv_append_gb300/csrc/nbx_tcgen05.cuh",
                   "paged_split_kv_append_gb300/csrc/decode_common.cu",
+                  "paged_split_kv_append_gb300/csrc/decode_mma.cuh",
                   "paged_split_kv_append_gb300/csrc/decode_mma.cu")
 
 

@@ -340,6 +340,15 @@ NBX_API int nbx_paged_kv_append_block_scaled(const void* new_k, const void* new_
  */
 NBX_API size_t nbx_paged_decode_modified_workspace_bytes(int batch, int rows, int h_q, int h_kv, int d,
                                                          int max_seq_len);
+
+/*
+ * nbx_paged_decode_modified_partial_kernel -- which split-partial kernel these two calls run (block-scaled
+ * pools: pool_dtype NBX_E4M3). Host-only. As nbx_paged_decode_partial_kernel, but an fp8 window with an fp32
+ * output runs NBX_PARTIAL_SIMT: on tensor cores an fp8 window's weights are held to 2^-9, which suits a bf16
+ * output. A bf16 window's are held to 2^-17.
+ */
+NBX_API int nbx_paged_decode_modified_partial_kernel(int q_dtype, int pool_dtype, int out_dtype, int rows, int h_q,
+                                                     int h_kv, int d, int num_pages, int page_tokens);
 NBX_API int nbx_paged_decode_attn_block_scaled(const void* q, int q_dtype, int batch, int rows, int h_q, int d,
                                                const void* k_pool, const void* v_pool, const float* k_scales,
                                                const float* v_scales, int scale_tokens, int num_pages, int h_kv,

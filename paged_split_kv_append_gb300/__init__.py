@@ -26,7 +26,7 @@ __all__ = [
     "nbx_paged_decode_merge", "nbx_set_decode_grid_limit", "nbx_set_decode_wait_test", "nbx_status_string",
     "nbx_paged_decode_bounds", "nbx_paged_decode_attn_fixed_shift", "nbx_decode_fixed_shift_gate",
     "nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
-    "nbx_paged_decode_modified_workspace_bytes", "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork",
+    "nbx_paged_decode_modified_workspace_bytes", "nbx_paged_decode_modified_partial_kernel", "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork",
     "nbx_paged_kv_fork_workspace_bytes", "nbx_paged_kv_compact", "nbx_paged_kv_compact_workspace_bytes",
     "dtype_code",
     "DEV_BAD_SLOT", "DEV_BAD_PAGE", "DEV_BAD_LEN", "DEV_TIMEOUT", "DEV_BAD_SCALE", "DEV_BAD_ROW", "DEV_NO_PAGE",
@@ -98,6 +98,8 @@ def _declare(l):
     l.nbx_paged_kv_append_block_scaled.restype = i32
     l.nbx_paged_decode_modified_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     l.nbx_paged_decode_modified_workspace_bytes.restype = sz
+    l.nbx_paged_decode_modified_partial_kernel.argtypes = [i32] * 9
+    l.nbx_paged_decode_modified_partial_kernel.restype = i32
     l.nbx_paged_decode_attn_block_scaled.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp,
                                                      i32, vp, i32, f32, f32, vp, vp, vp, vp, i32, vp, sz, vp, vp]
     l.nbx_paged_decode_attn_block_scaled.restype = i32
@@ -505,6 +507,15 @@ def nbx_paged_kv_append_block_scaled(new_k: torch.Tensor, new_v: torch.Tensor, k
 def nbx_paged_decode_modified_workspace_bytes(batch: int, rows: int, h_q: int, h_kv: int, d: int,
                                               max_seq_len: int) -> int:
     return int(lib().nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len))
+
+
+def nbx_paged_decode_modified_partial_kernel(q_dtype: int, pool_dtype: int, out_dtype: int, rows: int, h_q: int,
+                                             h_kv: int, d: int, num_pages: int, page_tokens: int) -> int:
+    """The split-partial kernel a modified or block-scaled decode with these sizes runs (PARTIAL_...)."""
+    k = lib().nbx_paged_decode_modified_partial_kernel(q_dtype, pool_dtype, out_dtype, rows, h_q, h_kv, d, num_pages,
+                                                       page_tokens)
+    _check("nbx_paged_decode_modified_partial_kernel", k if k < 0 else 0)
+    return k
 
 
 def _modified_call(dv, q, k_pool, block_table, seq_lens, max_seq_len, slopes, key_begin, key_end, out, out_dtype,

@@ -132,6 +132,14 @@ NBX_API int nbx_paged_decode_partial_kernel(int q_dtype, int pool_dtype, int row
   return pool_dtype == NBX_E4M3 ? NBX_PARTIAL_TCGEN05_FP8 : NBX_PARTIAL_TCGEN05;
 }
 
+NBX_API int nbx_paged_decode_modified_partial_kernel(int q_dtype, int pool_dtype, int out_dtype, int rows, int h_q,
+                                                     int h_kv, int d, int num_pages, int page_tokens) {
+  const int k = nbx_paged_decode_partial_kernel(q_dtype, pool_dtype, rows, h_q, h_kv, d, num_pages, page_tokens);
+  if (k < 0) return k;
+  if (out_dtype != NBX_F32 && out_dtype != NBX_BF16) return NBX_ERR_DTYPE;
+  return k == NBX_PARTIAL_TCGEN05_FP8 && out_dtype == NBX_F32 ? NBX_PARTIAL_SIMT : k;
+}
+
 NBX_API size_t nbx_paged_decode_workspace_bytes(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len) {
   if (!decode_shape_ok(batch, rows, h_q, h_kv, d, max_seq_len)) return 0;
   WorkspaceLayout w;

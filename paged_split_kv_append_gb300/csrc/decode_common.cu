@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     s_nb = 0;
     if constexpr (TC) s_total = 0;
     p.header[1] = 0;
+    if constexpr (X) p.header[2] = 0;   // set when a partial is to be recomputed
   }
   __syncthreads();
   if constexpr (X) {
@@ -372,6 +373,83 @@ cudaError_t merge_dispatch(const MergeParams& p, cudaStream_t stream) {
 // ------------------------------------------------------------------------------------ decode merge
 constexpr int kDecodeMergeThreads = 32;   // one warp per CTA
 
+// One query vector's partial over keys [start, end) of a bf16-query window, key by key: m, l (the same in
+// every lane) and this lane's float4 j of acc (zeros past d). Only rows that a tensor-core window marked
+// come here: a value row holds a NaN or an infinity, or O overflowed.
+struct RowPartial {
+  float m, l;
+  float4 acc;
+};
+__device__ __noinline__ RowPartial recompute_partial(const DecodeParams& p, int b, int h, int r, int g, int start, int end,
+                                                     int len, int j) {
+  const int lane = threadIdx.x & 31;
+  const int64_t orow = (static_cast<int64_t>(b) * p.rows + r) * p.h_q + static_cast<int64_t>(h) * p.group + g;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + orow * p.d;
+  const KeyRange kr = key_range(p, b, r, len);
+  const float slope = p.slopes ? p.slopes[h * p.group + g] * kLog2e : 0.f;
+  const int at = len - p.rows + r;
+  RowPartial o = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int n = max(start, kr.lo); n < min(end, kr.hi); ++n) {
+    const int page = p.block_table[static_cast<int64_t>(b) * p.max_pages + n / p.page_tokens];
+    if (page < 0 || page >= p.num_pages) continue;
+    const int in_page = n % p.page_tokens;
+    const int64_t head = static_cast<int64_t>(page) * p.h_kv + h;
+    float ks = 1.f, vs = 1.f;
+    if (p.k_scales) {
+      const int64_t blk = head * (p.page_tokens / p.scale_tokens) + in_page / p.scale_tokens;
+      ks = p.k_scales[blk];
+      vs = p.v_scales[blk];
+      if (!(ks >= kMinScale && ks <= kMaxScale && vs >= kMinScale && vs <= kMaxScale)) continue;
+    }
+    const int64_t row = (head * p.page_tokens + in_page) * p.d;
+    float s = 0.f;
+    for (int e = 2 * lane; e < p.d; e += 64) {
+      const float2 qq = load_pair<BF16>(q + e);
+      const float2 kk = p.pool_e4m3 ? load_pair<E4M3>(static_cast<const char*>(p.k_pool) + row + e)
+                                    : load_pair<BF16>(static_cast<const char*>(p.k_pool) + (row + e) * 2);
+      s = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, s));
+    }
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
+    float z = s * p.qk_scale_log2 * ks;
+    if (p.cap_log2 > 0.f) z = p.cap_log2 * tanhf(z * p.cap_inv);
+    z = fmaf(-slope, static_cast<float>(abs(at - n)), z);
+    const float m = max_nan(o.m, z);
+    if (m == -INFINITY) continue;
+    const float f = fast_exp2(o.m - m), w = fast_exp2(z - m);
+    const float wv = w * vs;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < p.d / 4) {
+      float2 lo, hi;
+      if (p.pool_e4m3) {
+        lo = load_pair<E4M3>(static_cast<const char*>(p.v_pool) + row + 4 * j);
+        hi = load_pair<E4M3>(static_cast<const char*>(p.v_pool) + row + 4 * j + 2);
+      } else {
+        lo = load_pair<BF16>(static_cast<const char*>(p.v_pool) + (row + 4 * j) * 2);
+        hi = load_pair<BF16>(static_cast<const char*>(p.v_pool) + (row + 4 * j + 2) * 2);
+      }
+      v = make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+    o.acc = make_float4(fmaf(o.acc.x, f, wv * v.x), fmaf(o.acc.y, f, wv * v.y), fmaf(o.acc.z, f, wv * v.z),
+                        fmaf(o.acc.w, f, wv * v.w));
+    o.l = fmaf(o.l, f, w);
+    o.m = m;
+  }
+  return o;
+}
+
+// Four output values (columns 4 j .. 4 j + 3 of row orow); a modified decode's output may be bf16.
+template <bool X>
+__device__ __forceinline__ void store_out4(const DecodeParams& p, int64_t orow, int j, float4 o) {
+  if (X && p.out_bf16) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
+    reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * p.d)[j] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  } else {
+    reinterpret_cast<float4*>(p.out + orow * p.d)[j] = o;
+  }
+}
+
 // Merges the split partials of every query vector of a (sequence, KV head) with more than one
 // split: M = max_s m_s, w_s = 2^(m_s - M) (m in log2 units; splits with m = -inf skipped),
 // out = v_scale * sum_s w_s acc_s / sum_s w_s l_s, s ascending. One-split sequences were written
@@ -382,7 +460,8 @@ constexpr int kDecodeMergeThreads = 32;   // one warp per CTA
 // float4 of the output, with every split's accumulator load in flight and the sum in ascending
 // split order.
 // F16: the partials are f16 acc / l (DecodeParams::part_f16); a split then weighs 2^(m - M) * l.
-// X: a modified decode, whose output may be bf16.
+// X: a modified decode, whose output may be bf16, and whose windows on tensor cores mark partials to be
+// recomputed (header[2] says that there are any): such rows take the slow path above, splits ascending too.
 template <bool F16, bool X>
 __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(DecodeParams p) {
   const int lane = threadIdx.x;
@@ -398,6 +477,7 @@ __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(Decod
   if (blockIdx.x < n_items)
     s_first = __ldcg(&p.plan[blockIdx.x / (static_cast<int64_t>(per_seq) * kQB * n_col)].n_splits);
   pdl_wait();   // every partial of the decode is written and visible from here on
+  const bool redo_any = X && p.header[2] != 0;
   for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
     const int64_t vi = it / n_col;
     const int j = static_cast<int>(it - vi * n_col) * 32 + lane;   // this lane's float4 column
@@ -410,12 +490,53 @@ __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(Decod
     const int qi = rb * kQB + i;
     if (qi >= RG) continue;
     const int S = it == blockIdx.x ? s_first : p.plan[b].n_splits;
-    if (S <= 1) continue;
+    if (S <= 1 && !redo_any) continue;
     const int r = qi / p.group;
     const int g = qi - r * p.group;
     const int64_t orow = (static_cast<int64_t>(b) * p.rows + r) * p.h_q + static_cast<int64_t>(h) * p.group + g;
     const float* m = p.m_part + orow * p.max_splits;
     const float* l = p.l_part + orow * p.max_splits;
+    if (X && redo_any) {
+      bool redo = false;
+      for (int sp = lane; sp < S; sp += 32) redo = redo || __float_as_uint(m[sp]) == kRedoBits;
+      if (__any_sync(0xffffffffu, redo)) {
+        const SeqPlan plan = p.plan[b];
+        RowPartial t = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int sp = 0; sp < S; ++sp) {
+          RowPartial o;
+          if (__float_as_uint(m[sp]) == kRedoBits) {
+            const int start = plan.first + sp * plan.seg;
+            o = recompute_partial(p, b, h, r, g, start, start + plan.seg, plan.len, j);
+          } else {
+            o.m = m[sp];
+            o.l = l[sp];
+            o.acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float* a = p.acc_part + (orow * p.max_splits + sp) * p.d;
+            if (j < d4) {
+              if constexpr (F16) {
+                const uint2 hv = reinterpret_cast<const uint2*>(a)[j];
+                const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&hv.x));
+                const float2 hi = __half22float2(*reinterpret_cast<const __half2*>(&hv.y));
+                o.acc = make_float4(lo.x * o.l, lo.y * o.l, hi.x * o.l, hi.y * o.l);
+              } else {
+                o.acc = reinterpret_cast<const float4*>(a)[j];
+              }
+            }
+          }
+          if (o.m == -INFINITY) continue;
+          const float M2 = max_nan(t.m, o.m);
+          const float f = fast_exp2(t.m - M2), w = fast_exp2(o.m - M2);
+          t.acc = make_float4(fmaf(t.acc.x, f, w * o.acc.x), fmaf(t.acc.y, f, w * o.acc.y),
+                              fmaf(t.acc.z, f, w * o.acc.z), fmaf(t.acc.w, f, w * o.acc.w));
+          t.l = fmaf(t.l, f, w * o.l);
+          t.m = M2;
+        }
+        const float tc = t.m == -INFINITY ? 0.f : p.v_scale / t.l;
+        if (j < d4) store_out4<X>(p, orow, j, make_float4(t.acc.x * tc, t.acc.y * tc, t.acc.z * tc, t.acc.w * tc));
+        continue;
+      }
+      if (S <= 1) continue;
+    }
     const float4* acc = reinterpret_cast<const float4*>(p.acc_part + orow * p.max_splits * p.d);
     // f16 partials: the d halves at the start of each split's d-float slot, 4 per lane (8 bytes)
     const uint2* acc_h = reinterpret_cast<const uint2*>(p.acc_part + orow * p.max_splits * p.d);
@@ -477,15 +598,9 @@ __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(Decod
         }
       }
     }
-    const float4 o = dead ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(A.x * sc, A.y * sc, A.z * sc, A.w * sc);
-    if (X && p.out_bf16) {
-      const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
-      if (j < d4)
-        reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * p.d)[j] =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-    } else if (j < d4) {
-      reinterpret_cast<float4*>(p.out + orow * p.d)[j] = o;
-    }
+    if (j < d4)
+      store_out4<X>(p, orow, j,
+                    dead ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(A.x * sc, A.y * sc, A.z * sc, A.w * sc));
   }
 }
 
@@ -608,18 +723,23 @@ cudaError_t launch_merge(const DecodeParams& p, unsigned grid, cudaStream_t stre
 cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, int x, int grid_limit,
                             cudaStream_t stream) {
   DecodeParams q = p;
-  const bool mma = x == 0 && mma_path_applies(p, q_dtype, pool_dtype);
-  q.part_f16 = mma && pool_dtype == NBX_E4M3 ? 1 : 0;   // fp8 pools on tensor cores: f16 partials
+  const bool mma = x ? mma_path_applies_modified(p, q_dtype, pool_dtype) : mma_path_applies(p, q_dtype, pool_dtype);
+  // fp8 pools on tensor cores: f16 partials (block scales may take acc / l out of f16's range)
+  q.part_f16 = mma && pool_dtype == NBX_E4M3 && !(x & kBlockScaled) ? 1 : 0;
+  q.pool_e4m3 = pool_dtype == NBX_E4M3;
   q.range_tiles = 1;
   if (mma) {
     // a tensor-core window: splits sized for one wave of work units over the GPU's SMs (the grid
     // limit does not enter, so the partition, and the result, is the same at any grid size)
     q.tc_units = device_info().sm_count;
-    q.tc_pairs = p.h_kv * ((p.rows * p.group + kMmaRowsPerTile - 1) / kMmaRowsPerTile);
+    q.range_tiles = (p.rows * p.group + kMmaRowsPerTile - 1) / kMmaRowsPerTile;
+    q.tc_pairs = p.h_kv * q.range_tiles;
   }
   cudaError_t e = x ? launch_plan<true>(q, stream) : launch_plan<false>(q, stream);
   if (e != cudaSuccess) return e;
-  if (mma) e = decode_dispatch_mma(q, pool_dtype, grid_limit, stream);
+  if (mma && (x & kBlockScaled)) e = decode_dispatch_mma_block(q, (x & kScoreMod) != 0, grid_limit, stream);
+  else if (mma)
+    e = x ? decode_dispatch_mma_mod(q, pool_dtype, grid_limit, stream) : decode_dispatch_mma(q, pool_dtype, grid_limit, stream);
   else if (x & kBlockScaled)
     e = x & kScoreMod ? decode_dispatch_E4M3_block_mod(q, q_dtype, grid_limit, stream)
                       : decode_dispatch_E4M3_block(q, q_dtype, grid_limit, stream);
@@ -630,7 +750,8 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
   else
     e = x ? decode_dispatch_E4M3_mod(q, q_dtype, grid_limit, stream) : decode_dispatch_E4M3(q, q_dtype, grid_limit, stream);
   if (e != cudaSuccess) return e;
-  if (q.max_splits <= 1) return cudaSuccess;   // every sequence has one split: the partials are the output
+  // every sequence has one split: the partials are the output (but for rows a modified window marked)
+  if (q.max_splits <= 1 && !(x && mma)) return cudaSuccess;
   const int64_t items = static_cast<int64_t>(q.batch) * q.h_kv * q.row_blocks * kQB * ((q.d / 4 + 31) / 32);
   int64_t grid = static_cast<int64_t>(device_info().sm_count) * 24;
   if (grid > items) grid = items;

@@ -184,6 +184,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// 1 / x with the hardware approximation (relative error 2^-23; 1 / inf = 0)
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ---------------------------------------------------------------- status word
 __device__ __forceinline__ void raise_status(int32_t* status, int32_t bits) {
   if (status != nullptr) atomicOr(status, bits);

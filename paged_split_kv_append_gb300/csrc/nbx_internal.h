@@ -219,6 +219,7 @@ struct DecodeParams {
   int scale_tokens;
   int2* ranges;            // [batch, range_tiles] keys the rows of a sequence's M tile see (SIMT: of the sequence)
   int range_tiles;
+  int pool_e4m3;           // the pools are E4M3 (else bf16): what a recomputed partial of a window reads
 };
 
 // What a decode adds to the plain one, as a template argument of its kernels: score modifications (a cap,
@@ -253,6 +254,12 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
 bool mma_path_applies(const DecodeParams& p, int q_dtype, int pool_dtype);
 constexpr int kMmaRowsPerTile = 128;   // query vectors of one M tile of the tensor-core kernel
 cudaError_t decode_dispatch_mma(const DecodeParams& p, int pool_dtype, int grid_limit, cudaStream_t stream);
+// The same for modified decodes. An E4M3 window holds P to 2^-9, which only a bf16 output may take.
+bool mma_path_applies_modified(const DecodeParams& p, int q_dtype, int pool_dtype);
+cudaError_t decode_dispatch_mma_mod(const DecodeParams& p, int pool_dtype, int grid_limit, cudaStream_t stream);
+cudaError_t decode_dispatch_mma_block(const DecodeParams& p, bool mod, int grid_limit, cudaStream_t stream);
+// m of a partial that the merge has to recompute: a NaN no computation gives
+constexpr uint32_t kRedoBits = 0x7fffbad0u;
 
 // Launch with programmatic dependent launch: the grid may start while the previous kernel in the
 // stream finishes; the kernel orders itself after it with griddepcontrol.wait.

@@ -152,12 +152,10 @@ __global__ void __launch_bounds__(256) fork_mark_kernel(ForkParams p) {
 // and the list of moves.
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
   __shared__ int s_scan[33];
-  __shared__ int s_need, s_free;
+  __shared__ int s_free;
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x;
-  if (tid == 0) s_need = 0;
-  __syncthreads();
   // ---- forks that need a fresh page, ranked in order
   int base = 0;
   for (int i0 = 0; i0 < p.n_fork; i0 += kPlanThreads) {

@@ -7,7 +7,8 @@ cap or a bias adds less. Sums of weights and of weighted values are fp32, at mos
 splits, hence 2^-14.8 in the worst case. The output is a weighted mean of the values, off by twice the
 weights' error times the largest value: max|v| (2^-19 Z + 2^-14). On tensor cores a bf16 window holds P to
 2^-17 (two bf16 terms), and an E4M3 window P to 2^-9 (two E4M3 terms, with the floors of small weights
-within 2^-8 of the sum) and q to 2^-9 of its largest element at worst. A bf16 output adds half a step: 2^-8.
+within 2^-8 of the sum) and each element of q to 2^-16 of the vector's largest, so a score to
+2^-16 sqrt(d) Z. A bf16 output adds half a step: 2^-8.
 """
 
 import math
@@ -100,6 +101,8 @@ class Case:
         z = self.scale * float(np.linalg.norm(self.q.float().numpy(), axis=-1).max()) * \
             float(np.linalg.norm(self.values[0], axis=-1).max())
         v = float(np.abs(self.values[1]).max())
+        if weight > 2.0 ** -10:
+            weight += 2.0 ** -16 * math.sqrt(self.d) * z
         return v * (2.0 ** -19 * z + 2.0 ** -14 + 2 * weight + (2.0 ** -8 if out_type == "bf16" else 0.0))
 
     def check(self, out_type="f32", weight=0.0, **mod):
@@ -279,6 +282,140 @@ def test_bad_pages_and_lengths_are_reported():
     torch.cuda.synchronize()
     assert int(status.item()) == nbx.DEV_BAD_LEN and bool((out[0] == 0).all())
     c.lens = n
+
+
+# ------------------------------------------------------------------------------------------------ tensor cores
+# rows x group of 64 and more, bf16 q, d 128 or 256, pages of whole 64-position tiles
+TENSOR = [("bf16", 16, 24, 4, 256, 64, 0), ("bf16", 8, 32, 4, 128, 128, 0), ("bf16", 70, 12, 4, 128, 64, 0),
+          ("e4m3", 16, 24, 4, 256, 64, 0), ("e4m3", 33, 8, 2, 128, 192, 0), ("block", 16, 24, 4, 256, 64, 64),
+          ("block", 8, 32, 4, 128, 64, 16), ("block", 40, 4, 1, 128, 128, 128), ("block", 130, 2, 2, 256, 128, 32),
+          ("bf16", 128, 2, 1, 128, 512, 0)]
+WINDOW_LENS = (0, 1, 17, 63, 64, 65, 129, 300, 513, 1100)
+P_WEIGHT = {"bf16": 2.0 ** -17, "e4m3": 2.0 ** -9 + 2.0 ** -8, "block": 2.0 ** -9 + 2.0 ** -8}
+
+
+def on_tensor_cores(c, out_type):
+    kind = nbx.NBX_BF16 if c.pool == "bf16" else nbx.NBX_E4M3
+    h_kv = c.dev[0].shape[1]
+    return nbx.nbx_paged_decode_modified_partial_kernel(nbx.dtype_code(c.q), kind, nbx.NBX_BF16 if out_type == "bf16" else
+                                                        nbx.NBX_F32, c.rows, c.h_q, h_kv, c.d, c.num_pages,
+                                                        c.P) != nbx.PARTIAL_SIMT
+
+
+@pytest.mark.parametrize("mod", MODS, ids=lambda m: "-".join(str(v) for v in m.values()) or "plain")
+@pytest.mark.parametrize("pool,rows,h_q,h_kv,d,P,T", TENSOR)
+def test_windows_on_tensor_cores(pool, rows, h_q, h_kv, d, P, T, mod):
+    c = Case(pool, "bf16", rows, h_q, h_kv, d, P, WINDOW_LENS, T, seed=20, two=(rows != 8))
+    assert on_tensor_cores(c, "bf16")
+    c.check("bf16", weight=P_WEIGHT[pool], **made(mod, WINDOW_LENS, rows, h_q))
+    if pool == "bf16":
+        c.check("f32", weight=P_WEIGHT[pool], **made(mod, WINDOW_LENS, rows, h_q))
+    else:
+        assert not on_tensor_cores(c, "f32")
+
+
+def test_fp8_windows_with_an_fp32_output_keep_fp32_weights():
+    c = Case("block", "bf16", 16, 24, 4, 256, 64, (5, 400), 32, seed=21)
+    c.check("f32", softcap=5.0)
+
+
+@pytest.mark.parametrize("pool,T", [("bf16", 0), ("e4m3", 0), ("block", 16)])
+def test_one_cta_runs_every_unit_of_a_masked_window(pool, T):
+    # units of one tile, of many, and of none that any row sees, one after another on one CTA
+    c = Case(pool, "bf16", 64, 8, 2, 128, 64, (2000, 70, 900, 0, 64), T, seed=22)
+    mod = made(dict(mask="random", softcap=4.0, slopes=True), c.lens, 64, 8)
+    ref = c.call("bf16", **mod)
+    for limit in (1, 3):
+        nbx.nbx_set_decode_grid_limit(limit)
+        out = c.call("bf16", **mod)
+        nbx.nbx_set_decode_grid_limit(0)
+        assert torch.equal(out, ref)
+    c.check("bf16", weight=P_WEIGHT[pool], **mod)
+
+
+def test_windows_with_gone_pages():
+    for pool, T in (("bf16", 0), ("block", 64)):
+        c = Case(pool, "bf16", 16, 16, 2, 128, 64, (1600, 2300, 40), T, seed=23)
+        lo, _ = ranges("window", c.lens, 16)
+        whole = c.call("bf16", key_begin=lo)
+        t = c.table.copy()
+        for b in range(3):
+            t[b, : int(lo[b].min()) // 64] = -1
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = c.call("bf16", key_begin=lo, table=t, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0 and torch.equal(out, whole)
+
+
+@pytest.mark.parametrize("lens", [(300,), (3000,)])       # one split, and several
+@pytest.mark.parametrize("pool,T", [("bf16", 0), ("e4m3", 0), ("block", 16)])
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(pool, T, lens):
+    n, rows = lens[0], 64
+    c = Case(pool, "bf16", rows, 4, 1, 128, 64, lens, T, seed=24)
+    lo = np.zeros((1, rows), dtype=np.int64)
+    lo[0, 32:] = 100                              # rows 32.. do not see position 50
+    lo[0, 60] = n                                 # row 60 sees nothing
+    ref = oc.attention(c.q.float().numpy(), *c.values, c.table, c.lens, c.scale, key_begin=lo, softcap=3.0)
+    at = (c.table[0, 0], slice(None), 50)
+    for w in range(2):
+        c.dev[w][at] = 0x7F if pool != "bf16" else float("nan")
+    last = (c.table[0, (n - 1) // 64], slice(None), (n - 1) % 64)    # seen by the last row alone
+    if pool == "bf16":
+        c.dev[1][last] = float("inf")
+    out = c.call("bf16", key_begin=lo, softcap=3.0).double().cpu().numpy()
+    assert np.all(np.isnan(out[0, :32]))
+    stop = rows - 1 if pool == "bf16" else rows
+    assert np.abs(out[0, 32:stop] - ref[0, 32:stop]).max() <= c.tolerance("bf16", P_WEIGHT[pool])
+    assert np.all(out[0, 60] == 0)
+    if pool == "bf16":
+        assert np.all(np.isposinf(out[0, -1]))
+
+
+def test_scales_far_apart_in_a_window():
+    # a sink: a block of nearly zero values that takes most of the weight beside blocks of ordinary ones
+    for small in (2.0 ** -20, 2.0 ** -48):
+        c = Case("block", "bf16", 64, 4, 1, 128, 64, (700,), 16, seed=25)
+        first = (int(c.table[0, 0]), 0, 0)
+        c.scales[1] = c.scales[1].copy()
+        c.scales[1][first] = small
+        c.values[1] = oc.pool_values(c.codes[1], "e4m3", scales=c.scales[1])
+        k = c.values[0][first[0], 0, :16]
+        c.q = (c.q + 3.0 * torch.from_numpy(k.mean(0)).float()).to(torch.bfloat16)
+        c.check("bf16", weight=P_WEIGHT["block"])
+        c.check("bf16", weight=P_WEIGHT["block"], slopes=[0.01] * 4)
+
+
+def test_a_bad_scale_in_a_window():
+    c = Case("block", "bf16", 64, 4, 1, 128, 64, (700,), 16, seed=26)
+    page = int(c.table[0, 3])
+    s = c.scales[1].copy()
+    s[page, 0, 2] = float("nan")
+    c.scales[1] = s
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = c.call("bf16", status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == nbx.DEV_BAD_SCALE
+    keep = [j for j in range(700) if not 3 * 64 + 32 <= j < 3 * 64 + 48]
+    vals = [x[c.table[0, :11].astype(int), 0].reshape(-1, 128) for x in c.values]
+    for r in (0, 33, 63):
+        seen = [j for j in keep if j <= 700 - 64 + r]
+        z = c.scale * (c.q[0, r].double().numpy() @ vals[0][seen].T)
+        e = np.exp(z - z.max(-1, keepdims=True))
+        ref = e @ vals[1][seen] / e.sum(-1, keepdims=True)
+        c.values[1] = np.nan_to_num(c.values[1])
+        assert np.abs(out[0, r].double().cpu().numpy() - ref).max() <= c.tolerance("bf16", P_WEIGHT["block"])
+
+
+def test_a_wait_that_runs_out_in_a_modified_window_returns_with_its_bit():
+    for pool, T in (("bf16", 0), ("block", 64)):
+        c = Case(pool, "bf16", 16, 24, 4, 256, 64, (1500, 900), T, seed=27)
+        nbx.nbx_set_decode_wait_test(200_000, 20_000_000)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        c.call("bf16", status=status, softcap=4.0)
+        torch.cuda.synchronize()
+        nbx.nbx_set_decode_wait_test(0, 0)
+        assert int(status.item()) & nbx.DEV_TIMEOUT
+        c.check("bf16", weight=P_WEIGHT[pool], softcap=4.0)
 
 
 @pytest.mark.parametrize("pool,T", [("bf16", 0), ("block", 16)])
