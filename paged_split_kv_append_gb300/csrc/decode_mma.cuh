@@ -57,7 +57,11 @@
 //  * Every wait is bounded. On timeout the kernel records NBX_DEV_TIMEOUT, waits (bounded) for
 //    its copies and MMAs in flight, releases its TMEM and returns.
 //
-// Modified decodes (X: kScoreMod and kBlockScaled bits) add, in the softmax warps:
+// Modified decodes (X: kScoreMod and kBlockScaled bits) have a softmax role of their own
+// (softmax_modified): eight warps instead of four. With one warp on each scheduler the plain role is a
+// chain of latencies that already sets the pace of a tile; 64 more multiplications a thread took a 16-row
+// window from 121 to 146 us, and a cap to 211. Two warps share 32 rows, 32 columns of S each, and swap
+// their half maxima through shared memory (bounded waits, like every other). They add:
 //  * block scales: with c_k the scale of a K block folded into the score's own factor, and log2 of a V
 //    block's scale added to the exponent, P' = 2^(z + log2 v_scale - m) enters the product as any weight
 //    does, and the row's sum takes each 16-column part of P' divided by its V scale. So P' keeps its terms'
@@ -89,6 +93,7 @@ constexpr int kMmaM = 128;       // TMEM lanes / rows of an M tile
 static_assert(kMmaM == kMmaRowsPerTile, "the plan's M tiles");
 constexpr int kMmaN = 64;        // positions per K/V tile
 constexpr int kMmaThreads = 256;
+constexpr int kMmaThreadsMod = 384;   // a modified decode: four more softmax warps
 constexpr int kSoftmaxThreads = 128;
 constexpr float kMmaTau = 8.0f;  // lazy-rescale threshold, log2 units
 constexpr int kChunk = 32;       // output columns per epilogue step
@@ -100,7 +105,7 @@ constexpr int kAtomBytes = kMmaN * 128;   // one 128-byte-wide swizzle column of
 // the gathered weight stays <= 2^40
 constexpr float kF8Hi = 8.75f, kF8Mid = 5.f, kF8MaxWeight = 1099511627776.f;
 
-template <int D, bool F8>
+template <int D, bool F8, int X = 0>
 struct MmaCfg {
   static constexpr int kHalves = F8 ? 1 : D / 128;         // ring slots per K (or V) tile
   static constexpr int kKSlots = D <= 128 ? 5 : 4;         // K ring
@@ -110,13 +115,14 @@ struct MmaCfg {
   static constexpr int kKOff = kQBytes;
   static constexpr int kVOff = kKOff + kKSlots * kSlotBytes;
   static constexpr int kBarOff = kVOff + kVSlots * kSlotBytes;
-  static constexpr int kSmem = kBarOff + 512 + 1024;   // barriers + slack for 1024-byte alignment
+  static constexpr int kXBytes = X ? 2 * 8 * 32 * 8 : 0;        // what the softmax warps of a row exchange
+  static constexpr int kSmem = kBarOff + 512 + kXBytes + 1024;   // barriers + slack for 1024-byte alignment
   // TMEM columns: S/P buffers [0, 192), O [192, 192 + D)
   static constexpr uint32_t kOCol = kSBufs * kMmaN;
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kOCol + D <= kTmemCols, "TMEM");
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert((2 * (kKSlots + kVSlots) + 3 * kSBufs + 7) * 8 <= 512, "barrier area");
+  static_assert((2 * (kKSlots + kVSlots) + 3 * kSBufs + 11) * 8 <= 512, "barrier area");
   // one PV MMA spans both V halves of a tile: their slots must be adjacent (even ordinals)
   static_assert(kHalves == 1 || (kVSlots % kHalves) == 0, "V ring length");
 };
@@ -330,8 +336,9 @@ __device__ __forceinline__ void p_terms4(const float* pv, uint32_t& wh, uint32_t
 // Q tile's 128-byte-swizzled K-major atoms: Q_hi atoms first, then Q_lo. Rows past the last vector
 // are zero; a vector holding NaN or infinity gets NaN codes. Returns 2^-e, which the row's scores
 // take back.
-template <int D>
-__device__ __forceinline__ float q_to_e4m3_terms(const DecodeParams& p, const MmaUnit& mu, int row, char* q_s) {
+// kParts threads share a row: thread `part` of them writes its share of the columns.
+template <int D, int kParts = 1>
+__device__ __forceinline__ float q_to_e4m3_terms(const DecodeParams& p, const MmaUnit& mu, int row, char* q_s, int part = 0) {
   const int G = p.group;
   const int vq = mu.mt * kMmaM + row;
   const bool ok = vq < p.rows * G;
@@ -362,7 +369,7 @@ __device__ __forceinline__ float q_to_e4m3_terms(const DecodeParams& p, const Mm
   char* row_hi = q_s + row * 128;
   char* row_lo = q_s + (D / 128) * (kMmaM * 128) + row * 128;
 #pragma unroll 2
-  for (int c = 0; c < D / 16; ++c) {   // 16 elements: one 16-byte chunk of each term
+  for (int c = part * (D / 16 / kParts); c < (part + 1) * (D / 16 / kParts); ++c) {   // 16 elements: one 16-byte chunk of each term
     uint4 ph = make_uint4(0u, 0u, 0u, 0u), pl = ph;
     if (ok) {
       const uint4 v0 = __ldg(src + 2 * c), v1 = __ldg(src + 2 * c + 1);
@@ -385,20 +392,20 @@ __device__ __forceinline__ float q_to_e4m3_terms(const DecodeParams& p, const Mm
   return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
-// The scales of a tile's four 16-position parts: K's, V's, log2 and reciprocal of V's. A block whose scale is
-// not in [2^-48, 2^48] counts as missing (bit k of `bad`).
+constexpr int kHalf = kMmaN / 2;   // columns of S of one softmax thread of a modified decode
+constexpr int kParts = kHalf / 16;  // 16-position parts of them, each of one block of scales
+
+// The scales of a thread's parts of a tile.
 struct TileScales {
-  float k[4], v[4];
+  float k[kParts], v[kParts];
   __device__ __forceinline__ void load(const DecodeParams& p, const MmaUnit& mu, int n0, int page) {
-    if (page < 0 || page >= p.num_pages || mu.nothing) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) k[i] = v[i] = 1.f;
-      return;
-    }
+    for (int i = 0; i < kParts; ++i) k[i] = v[i] = 1.f;
+    if (page < 0 || page >= p.num_pages || mu.nothing) return;
     const int64_t base = (static_cast<int64_t>(page) * p.h_kv + mu.h) * (p.page_tokens / p.scale_tokens);
     const int in_page = n0 % p.page_tokens;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kParts; ++i) {
       const int64_t at = base + (in_page + 16 * i) / p.scale_tokens;
       k[i] = p.k_scales[at];
       v[i] = p.v_scales[at];
@@ -406,12 +413,12 @@ struct TileScales {
   }
 };
 
-// tanh of the scores of a tile, cap * tanh(s * c_k / cap) in log2 units: sr[j] in, z out. c: factor of each
-// 16-column part from a raw score to s / cap.
-__device__ __forceinline__ void cap_scores(uint32_t (&sr)[kMmaN], const float (&c)[4], float cap) {
+// Capped scores in log2 units, cap * tanh(s * c / cap): sr[j] raw in, z out. c: each part's factor from a raw
+// score to s / cap.
+__device__ __forceinline__ void cap_scores(uint32_t (&sr)[kHalf], const float (&c)[kParts], float cap) {
   float ax = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < kParts; ++k) {
     float m[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) m[i] = fabsf(__uint_as_float(sr[16 * k + i]));
@@ -427,7 +434,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[kMmaN], const float (&
                 a5 = pack2(-0.0076394579373300076f, -0.0076394579373300076f),
                 a6 = pack2(0.0017277069855481386f, 0.0017277069855481386f), one = pack2(1.f, 1.f), cap2 = pack2(cap, cap);
 #pragma unroll
-    for (int j = 0; j < kMmaN; j += 2) {
+    for (int j = 0; j < kHalf; j += 2) {
       const f32x2 ck = pack2(c[j >> 4], c[j >> 4]);
       const f32x2 x = mul2(pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), ck);
       const f32x2 u = mul2(x, x);
@@ -443,11 +450,397 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[kMmaN], const float (&
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kMmaN; ++j) {
+    for (int j = 0; j < kHalf; ++j) {
       const float e = fast_exp2(__uint_as_float(sr[j]) * (c[j >> 4] * (2.f * kLog2e)));   // e^2x
       sr[j] = __float_as_uint(fmaf(-2.f * cap, fast_rcp(1.f + e), cap));
     }
   }
+}
+
+// The softmax role of a modified decode (warps 0-3 and 8-11): thread = one query vector (TMEM lane) and half
+// of its tile's columns. The two threads of a row hold the same m, the same weight gathered and the same
+// budget of floors, from the same exchanged numbers, so they take every decision alike; each keeps the sum of
+// its own half and half of O's columns. Returns false if a wait ran out.
+template <int D, bool F8, int X>
+__device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_s, uint64_t* s_full, uint64_t* p_full,
+                                                 uint64_t* sp_free, uint64_t* q_full, uint64_t* o_free, uint64_t* xbar,
+                                                 float2* xbuf, uint32_t tmem, int m_tiles, int n_units,
+                                                 volatile int* abort_flag, uint64_t wlim) {
+  using C = MmaCfg<D, F8, X>;
+  constexpr bool kMod = (X & kScoreMod) != 0;
+  constexpr bool kBlk = (X & kBlockScaled) != 0;
+  constexpr int HI = C::kHalves;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = warp >> 3, quarter = warp & 3;
+  const int row = quarter * 32 + lane;
+  const int G = p.group, RG = p.rows * G;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const uint64_t keep = l2_keep_policy(p.keep_frac);   // the split partials stay in L2 for the merge
+  uint32_t xphase = 0;
+  // Swaps two numbers with the other warp of these rows. Everything each warp did before is visible to the
+  // other after it, its TMEM loads included, so the columns they read may be written over.
+  auto swap = [&](float2 mine, float2& other) -> bool {
+    float2* buf = xbuf + (xphase & 1u) * 256;
+    buf[(half * 4 + quarter) * 32 + lane] = mine;
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&xbar[quarter]);
+    const bool r = warp_wait(&xbar[quarter], xphase & 1u, abort_flag, wlim);
+    ++xphase;
+    if (!r) return false;
+    tc_fence_after();
+    other = buf[((half ^ 1) * 4 + quarter) * 32 + lane];
+    return true;
+  };
+  uint32_t gb = 0, gp = 0;     // S/P buffer of the tile (ordinal % 3) and its phase count (ordinal / 3)
+  TileIter<kMod> it;
+  it.begin(p, m_tiles, n_units, HI);
+  int pg_cur = it.done ? 0 : chunk_pages(p, it.mu, 0, lane), pg_nxt = 0;   // lane l: page of tile 32c + l
+  float q_inv = 1.f;   // fp8 pools: 2^-e of this thread's query vector in the unit's Q terms
+  if constexpr (F8) {
+    if (!it.done) {
+      q_inv = q_to_e4m3_terms<D, 2>(p, it.mu, row, q_s, half);
+      fence_proxy_async();   // the terms are read by the tensor pipe (async proxy)
+      mbar_arrive(q_full);
+    }
+  }
+  const bool shaped = kMod && (p.cap_log2 > 0.f || p.slopes != nullptr);   // scores are more than scaled
+  while (!it.done) {
+    const MmaUnit mu = it.mu;
+    const int vq = mu.mt * kMmaM + row;            // this thread's query vector of the KV head
+    const bool row_ok = vq < RG;
+    const int r = row_ok ? vq / G : 0;             // its query row
+    const int gq = row_ok ? vq - r * G : 0;        // its query head within the KV head's group
+    const int at = mu.len - p.rows + r;            // its position
+    int first_key = 0, last_key = at;              // the keys it sees
+    float slope = 0.f;
+    if constexpr (kMod) {
+      const KeyRange kr = row_ok ? key_range(p, mu.b, r, mu.len) : KeyRange{0, 0};
+      first_key = kr.lo;
+      last_key = kr.hi - 1;
+      if (row_ok && p.slopes) slope = p.slopes[mu.h * G + gq] * kLog2e;
+    }
+    last_key = row_ok ? min(mu.end - 1, last_key) : -1;
+    const float c = F8 ? p.qk_scale_log2 * q_inv : p.qk_scale_log2;   // 2^-e: exact
+    float m_run = -INFINITY;
+    float l_run = 0.f;     // the sum of P over this thread's columns
+    // fp8: the sum of P' (of P, without block scales) over the row and the bound on its terms' floor errors,
+    // both through the last tile but for its sums, which follow with the next exchange
+    float w_run = 0.f, w_half = 0.f, e_run = 0.f;
+    TileScales ts_next;
+    if constexpr (kBlk) ts_next.load(p, mu, mu.start + half * kHalf, __shfl_sync(0xffffffffu, pg_cur, 0));
+    uint32_t pb = 0, pp = 0;   // buffer and phase count of the previous tile
+    for (int t = 0; t < mu.tiles; ++t) {
+      const int n0 = mu.start + t * kMmaN + half * kHalf;   // position of this thread's first column
+      if ((t & 31) == 0 && t + 32 < mu.tiles) pg_nxt = chunk_pages(p, mu, (t >> 5) + 1, lane);
+      const int page = __shfl_sync(0xffffffffu, pg_cur, t & 31);
+      if ((t & 31) == 31) pg_cur = pg_nxt;
+      const bool tile_ok = page >= 0 && page < p.num_pages && !mu.nothing;
+      float ck[kParts], lv[kParts], iv[kParts];   // factor of a raw score; log2 and reciprocal of the V scale
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        ck[k] = c;
+        lv[k] = 0.f;
+        iv[k] = 1.f;
+      }
+      uint32_t bad_blocks = 0;
+      if constexpr (kBlk) {
+        const TileScales ts = ts_next;
+        const int next = __shfl_sync(0xffffffffu, pg_cur, (t + 1) & 31);
+        if (t + 1 < mu.tiles) ts_next.load(p, mu, n0 + kMmaN, next);
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) {
+          const bool fit = ts.k[k] >= kMinScale && ts.k[k] <= kMaxScale && ts.v[k] >= kMinScale && ts.v[k] <= kMaxScale;
+          // a block that no row sees does not count, whatever its scale
+          if (!fit && n0 + 16 * k < mu.end && n0 + 16 * k + 16 > mu.lo && lane == 0 && quarter == 0)
+            raise_status(p.status, NBX_DEV_BAD_SCALE);
+          if (!fit) bad_blocks |= 1u << k;
+          if (fit) {
+            ck[k] *= ts.k[k];
+            lv[k] = __log2f(ts.v[k]);
+            iv[k] = __frcp_rn(ts.v[k]);
+          }
+        }
+      }
+      const uint32_t sbuf = gb * kMmaN;
+      if (!warp_wait(&s_full[gb], gp & 1u, abort_flag, wlim)) return false;
+      tc_fence_after();
+      uint32_t sr[kHalf];
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) tmem_ld16(lane_base + sbuf + half * kHalf + k * 16, sr + k * 16);
+      tmem_wait_ld();
+      // ---- the scores: raw, with factors ck, or, capped or biased, z in log2 units with factors 1
+      if constexpr (kMod) {
+        if (shaped) {
+          if (p.cap_log2 > 0.f) {
+            float cx[kParts];
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) cx[k] = ck[k] * p.cap_inv;
+            cap_scores(sr, cx, p.cap_log2);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) ck[k] = 1.f;
+          }
+          if (p.slopes != nullptr) {
+            const float far = static_cast<float>(n0 - at);   // minus the distance of the first column
+            if (__all_sync(0xffffffffu, far + static_cast<float>(kHalf) <= 0.f)) {   // every key is at or before its row
+              const float b0 = slope * far;
+#pragma unroll
+              for (int j = 0; j < kHalf; ++j)
+                sr[j] = __float_as_uint(fmaf(__uint_as_float(sr[j]), ck[j >> 4], fmaf(slope, static_cast<float>(j), b0)));
+            } else {
+#pragma unroll
+              for (int j = 0; j < kHalf; ++j)
+                sr[j] = __float_as_uint(fmaf(-slope, fabsf(far + static_cast<float>(j)), __uint_as_float(sr[j]) * ck[j >> 4]));
+            }
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) ck[k] = 1.f;
+          }
+        }
+      }
+      // ---- mask (causal or key range, split end, missing page, block without a scale), row max of
+      // z + log2 v_scale; the factors are positive and NaN propagates through the max
+      const int lim = tile_ok ? last_key - n0 : -1, low = kMod ? first_key - n0 : 0;   // visible columns [low, lim]
+      if (!__all_sync(0xffffffffu, lim >= kHalf - 1 && low <= 0 && bad_blocks == 0)) {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j)
+          sr[j] = j <= lim && j >= low && !((bad_blocks >> (j >> 4)) & 1u) ? sr[j] : 0xff800000u;   // -inf
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        float m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = __uint_as_float(sr[16 * k + i]);
+#pragma unroll
+        for (int i = 4; i < 16; ++i) m[i & 3] = max_nan(m[i & 3], __uint_as_float(sr[16 * k + i]));
+        mx = max_nan(mx, fmaf(max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3])), ck[k], lv[k]));
+      }
+      float2 other;
+      if (!swap(make_float2(mx, w_half), other)) return false;
+      mx = max_nan(mx, other.x);
+      if constexpr (F8) w_run += w_half + other.y;   // the weight through the last tile
+      // a NaN running max stays NaN (a later tile the row cannot see, max -inf, must not replace it)
+      const bool grow = !(mx <= m_run + (F8 ? kF8Hi : kMmaTau)) && m_run == m_run;
+      float m_new = grow ? (F8 ? mx - kF8Mid : mx) : m_run;
+      float f = grow ? fast_exp2(m_run - m_new) : 1.f;
+      const float nm = (m_new == -INFINITY) ? 0.f : -m_new;   // all scores -inf: p = 0
+      float part[kParts][2];   // two chains a part
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) part[k][0] = part[k][1] = 0.f;
+      if constexpr (F8) {
+        float pv[kHalf];
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+          pv[j] = fast_exp2(fmaf(__uint_as_float(sr[j]), ck[j >> 4], nm + lv[j >> 4]));
+          part[j >> 4][j & 1] += pv[j];
+        }
+        // The budget of the E4M3 terms' floors, as the plain role keeps it (each weight below 2^-1 is off by at
+        // most 2^-9, in all at most 2^-8 of the weight gathered). The first test takes what both threads of
+        // the row know, the tile's largest weight for its sum, and only a row that fails it has its sums and
+        // its counts of small weights exchanged and looked at.
+        const int vis_all = tile_ok ? max(0, min(kMmaN - 1, last_key - (n0 - half * kHalf)) -
+                                               max(0, kMod ? first_key - (n0 - half * kHalf) : 0) + 1)
+                                    : 0;
+        float e_tile = 0.001953125f * static_cast<float>(vis_all);
+        const bool tight = mx > -INFINITY && e_run * f + e_tile > 0.00390625f * (w_run * f + fast_exp2(mx - m_new));
+        if (__any_sync(0xffffffffu, tight)) {
+          uint32_t n = 0;   // weights below 2^-1, zeros among them
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j) n += (__float_as_uint(pv[j]) - 0x3F000000u) >> 31;
+          float w_t = 0.f;
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) w_t += part[k][0] + part[k][1];
+          if (!swap(make_float2(w_t, static_cast<float>(n)), other)) return false;
+          const float budget = 0.00390625f * (w_run * f + (w_t + other.x));
+          if (tight) {
+            const int small = static_cast<int>(n) + static_cast<int>(other.y) - (kMmaN - vis_all);
+            e_tile = 0.001953125f * static_cast<float>(max(0, small));
+            const float fd = fast_exp2(m_new - (mx - kF8Mid));
+            if (e_run * f + e_tile > budget && fd > 1.f && w_run * f * fd <= kF8MaxWeight) {
+              m_new = mx - kF8Mid;
+              f *= fd;
+#pragma unroll
+              for (int j = 0; j < kHalf; ++j) pv[j] *= fd;
+#pragma unroll
+              for (int k = 0; k < kParts; ++k) {
+                part[k][0] *= fd;
+                part[k][1] *= fd;
+              }
+              e_tile = 0.001953125f * static_cast<float>(vis_all);   // <= 2^-8 * 2^kF8Mid
+            }
+          }
+        }
+        e_run = e_run * f + e_tile;
+        // E4M3 terms (split4), four codes a column: P_hi over S columns [0, 16), P_lo over [16, 32)
+        uint32_t wh[kHalf / 4], wl[kHalf / 4];
+#pragma unroll
+        for (int i = 0; i < kHalf / 4; ++i) p_terms4(pv + 4 * i, wh[i], wl[i]);
+        tmem_st8(lane_base + sbuf + half * (kHalf / 4), wh);
+        tmem_st8(lane_base + sbuf + kMmaN / 4 + half * (kHalf / 4), wl);
+      } else {
+        // bf16 terms: P_hi = p with the low 16 bits cleared (exact), P_lo = p - P_hi rounded: 2^-17 p, without
+        // the bias of a truncation; hi over S columns [0, 32), lo over [32, 64)
+        uint32_t wh[kHalf / 2], wl[kHalf / 2];
+#pragma unroll
+        for (int i = 0; i < kHalf / 2; ++i) {
+          const int j = 2 * i;
+          const float p0 = fast_exp2(fmaf(__uint_as_float(sr[j]), ck[j >> 4], nm));
+          const float p1 = fast_exp2(fmaf(__uint_as_float(sr[j + 1]), ck[j >> 4], nm));
+          part[j >> 4][0] += p0;
+          part[j >> 4][1] += p1;
+          const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+          wh[i] = __byte_perm(u0, u1, 0x7632);
+          const __nv_bfloat162 lr = __floats2bfloat162_rn(p0 - __uint_as_float(u0 & 0xffff0000u),
+                                                          p1 - __uint_as_float(u1 & 0xffff0000u));
+          wl[i] = *reinterpret_cast<const uint32_t*>(&lr);
+        }
+        tmem_st16(lane_base + sbuf + half * (kHalf / 2), wh);
+        tmem_st16(lane_base + sbuf + kMmaN / 2 + half * (kHalf / 2), wl);
+      }
+      // ---- the sums: of P' (what the product gathers) and of P (the softmax's denominator)
+      float l_t = 0.f;
+      w_half = 0.f;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        const float s = part[k][0] + part[k][1];
+        w_half += s;
+        l_t += kBlk ? s * iv[k] : s;
+      }
+      if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+        // O holds the PVs of the unit's earlier tiles: wait for the last, then rescale this thread's half
+        if (!warp_wait(&sp_free[pb], pp & 1u, abort_flag, wlim)) return false;
+        tc_fence_after();
+#pragma unroll 1
+        for (int cc = 0; cc < D / 128; ++cc) {
+          const uint32_t col = lane_base + C::kOCol + half * (D / 2) + cc * 64;
+          uint32_t ov[64];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld16(col + q * 16, ov + q * 16);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 64; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_st16(col + q * 16, ov + q * 16);
+        }
+      }
+      m_run = m_new;
+      l_run = l_run * f + l_t;
+      if constexpr (F8) w_run *= f;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&p_full[gb]);
+      pb = gb;
+      pp = gp;
+      if (++gb == kSBufs) {
+        gb = 0;
+        ++gp;
+      }
+    }
+    float2 other;
+    if (!swap(make_float2(l_run, 0.f), other)) return false;
+    l_run += other.x;
+    float q_inv_next = 1.f;
+    if constexpr (F8) {
+      // the next unit's Q terms: every QK^T of this unit has completed (its last S was read)
+      if (it.has_next) {
+        q_inv_next = q_to_e4m3_terms<D, 2>(p, it.next_mu(), row, q_s, half);
+        fence_proxy_async();
+        mbar_arrive(q_full);
+      }
+    }
+    // ---- the unit's last PV is done: O is complete
+    if (!warp_wait(&sp_free[pb], pp & 1u, abort_flag, wlim)) return false;
+    it.next_unit(p);
+    q_inv = q_inv_next;
+    if (!it.done) pg_cur = chunk_pages(p, it.mu, 0, lane);
+    // ---- epilogue: this thread's half of its row of O, 32 columns at a time, straight from registers
+    tc_fence_after();
+    const bool single = mu.n_splits <= 1;
+    const bool empty = m_run == -INFINITY;   // 0, whatever the product of its zero weights gave
+    const float sc = single ? p.v_scale / l_run : 1.f;
+    const bool half_part = F8 && p.part_f16 && !single;   // f16 partials: acc / l
+    const float il = empty ? 0.f : 1.f / l_run;
+    const int64_t orow = (static_cast<int64_t>(mu.b) * p.rows + r) * p.h_q + static_cast<int64_t>(mu.h) * G + gq;
+    const int64_t slot = orow * p.max_splits + mu.s;
+    bool finite_row = true;
+#pragma unroll 1
+    for (int ch = 0; ch < D / 2 / kChunk; ++ch) {
+      const int col = half * (D / 2) + ch * kChunk;
+      uint32_t ov[kChunk];
+      tmem_ld16(lane_base + C::kOCol + col, ov);
+      tmem_ld16(lane_base + C::kOCol + col + 16, ov + 16);
+      tmem_wait_ld();
+      if (ch == D / 2 / kChunk - 1) {   // O is free for the next unit's first PV
+        tc_fence_before();
+        mbar_arrive(o_free);
+      }
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) big = max_nan(big, fabsf(__uint_as_float(ov[i])));
+      finite_row = finite_row && big <= 3.402823466e38f;
+      if (!row_ok) continue;
+      if (empty) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) ov[i] = 0u;
+      }
+      if (half_part) {
+        // 32 halves: two 32-byte stores into the first half of the split's slot
+        float* dst = p.acc_part + slot * D + col / 2;
+#pragma unroll
+        for (int c16 = 0; c16 < kChunk / 16; ++c16) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const __half2 h = __floats2half2_rn(__uint_as_float(ov[16 * c16 + 2 * e]) * il,
+                                                __uint_as_float(ov[16 * c16 + 2 * e + 1]) * il);
+            v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+          }
+          st_global_v8_hint(dst + c16 * 8, v, keep);
+        }
+      } else if (!single) {
+        float* dst = p.acc_part + slot * D + col;
+#pragma unroll
+        for (int c8 = 0; c8 < kChunk / 8; ++c8) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[8 * c8 + e]);
+          st_global_v8_hint(dst + c8 * 8, v, keep);
+        }
+      } else if (p.out_bf16) {   // the output, 16 bytes a store (it is aligned to no more), rounded once
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * D + col);
+        const float scale = empty ? 0.f : sc;
+#pragma unroll
+        for (int c8 = 0; c8 < kChunk / 8; ++c8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(ov[8 * c8 + 2 * e]) * scale,
+                                                            __uint_as_float(ov[8 * c8 + 2 * e + 1]) * scale);
+            w[e] = *reinterpret_cast<const uint32_t*>(&b2);
+          }
+          dst[c8] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.out + orow * D + col);
+        const float scale = empty ? 0.f : sc;
+#pragma unroll
+        for (int c4 = 0; c4 < kChunk / 4; ++c4)
+          dst[c4] = make_float4(__uint_as_float(ov[4 * c4]) * scale, __uint_as_float(ov[4 * c4 + 1]) * scale,
+                                __uint_as_float(ov[4 * c4 + 2]) * scale, __uint_as_float(ov[4 * c4 + 3]) * scale);
+      }
+    }
+    // ---- m and l; m also says whether the row is to be recomputed (a NaN m is a NaN that the row sees)
+    if (!swap(make_float2(finite_row ? 0.f : 1.f, 0.f), other)) return false;
+    if (half == 0) {
+      const bool redo = row_ok && (!finite_row || other.x != 0.f) && m_run == m_run && !empty;
+      if (__any_sync(0xffffffffu, redo) && lane == 0) p.header[2] = 1;
+      if (row_ok) {
+        st_global_hint(p.m_part + slot, redo ? __uint_as_float(kRedoBits) : m_run, keep);
+        st_global_hint(p.l_part + slot, l_run, keep);
+      }
+    }
+  }
+  return true;
 }
 
 // F8: the pools hold E4M3 codes, read as they are by kind::f8f6f4 MMAs (Q and P as two E4M3 terms
@@ -456,12 +849,12 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[kMmaN], const float (&
 // start after DecodeParams::producer_delay_ns.
 // X: a modified decode (see above).
 template <int D, bool F8, bool TW, int X = 0>
-__global__ void __launch_bounds__(kMmaThreads, 1)
+__global__ void __launch_bounds__(X ? kMmaThreadsMod : kMmaThreads, 1)
     decode_partial_mma_kernel(DecodeParams p, const __grid_constant__ MmaMaps maps) {
-  using C = MmaCfg<D, F8>;
+  using C = MmaCfg<D, F8, X>;
   constexpr bool kMod = (X & kScoreMod) != 0;
-  constexpr bool kBlk = (X & kBlockScaled) != 0;
-  static_assert(!kBlk || F8, "block scales belong to E4M3 pools");
+  static_assert((X & kBlockScaled) == 0 || F8, "block scales belong to E4M3 pools");
+  constexpr int kRowThreads = X ? 2 * kSoftmaxThreads : kSoftmaxThreads;   // softmax threads
   constexpr int NK = C::kKSlots;
   constexpr int NV = C::kVSlots;
   constexpr int HI = C::kHalves;
@@ -476,16 +869,18 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   uint64_t* vfull = kempty + NK;       // [NV]  the V slot's half landed
   uint64_t* vempty = vfull + NV;       // [NV]  the V slot's half consumed (its PV done)
   uint64_t* s_full = vempty + NV;      // [3]   S of the buffer's tile in TMEM
-  uint64_t* p_full = s_full + kSBufs;  // [3]   P of the buffer's tile in TMEM (128 arrivals)
+  uint64_t* p_full = s_full + kSBufs;  // [3]   P of the buffer's tile in TMEM (every softmax thread arrives)
   uint64_t* sp_free = p_full + kSBufs; // [3]   PV of the buffer's tile done: buffer reusable, O
                                        //       holds every PV up to that tile
   uint64_t* q_full = sp_free + kSBufs; //       the unit's Q tile landed (the QK warp's lanes 1-31)
   uint64_t* q_empty = q_full + 1;      //       every QK^T of the unit done
-  uint64_t* o_free = q_full + 2;       //       O read out by the epilogue (128 arrivals)
+  uint64_t* o_free = q_full + 2;       //       O read out by the epilogue (every softmax thread arrives)
   uint64_t* done_bar = q_full + 3;     //       every PV of the CTA done
   uint64_t* done_qk = q_full + 4;      //       every QK^T of the CTA done
   volatile int* abort_flag = reinterpret_cast<int*>(q_full + 5);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(q_full + 6);
+  uint64_t* xbar = q_full + 7;         // [4]   X: exchanges between the two softmax warps of 32 rows
+  float2* xbuf = reinterpret_cast<float2*>(smem + C::kBarOff + 512);   // [2][8][32], X only
   // Phase discipline: a thread waits on phase j of a barrier only once it knows phase j - 1 has
   // completed and while phase j + 1 cannot have (a parity wait cannot tell them apart). Each
   // issuer consumes its ring slots in order, so it tests a slot's half only after the half a ring
@@ -508,14 +903,16 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], kSoftmaxThreads);
+      mbar_init(&p_full[i], kRowThreads);
       mbar_init(&sp_free[i], 1);
     }
     // the E4M3 terms of the 128 softmax threads, a tensor box (one arrival with the byte count), or
     // the cp.async completions of lanes 1-31
-    mbar_init(q_full, F8 ? kSoftmaxThreads : (whole_row_tile_rows(p.rows, p.group) > 0 ? 1 : 31));
+    mbar_init(q_full, F8 ? kRowThreads : (whole_row_tile_rows(p.rows, p.group) > 0 ? 1 : 31));
     mbar_init(q_empty, 1);
-    mbar_init(o_free, kSoftmaxThreads);
+    mbar_init(o_free, kRowThreads);
+    if constexpr (X != 0)
+      for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 2);
     mbar_init(done_bar, 1);
     mbar_init(done_qk, 1);
     *abort_flag = 0;
@@ -773,419 +1170,294 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     }
     __syncwarp();
   } else {
-    // ======================================================== softmax warps (row = threadIdx.x)
-    const int row = threadIdx.x;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    // the split partials stay in L2 for the merge
-    const uint64_t keep = l2_keep_policy(p.keep_frac);
-    bool ok = true;
-    uint32_t g = 0;              // tile ordinal
-    uint32_t gb = 0, gp = 0;     // S/P buffer (g % 3) and its phase count (g / 3)
-    TileIter<kMod> it;
-    it.begin(p, m_tiles, n_units, HI);
-    int pg_cur = it.done ? 0 : chunk_pages(p, it.mu, 0, lane), pg_nxt = 0;   // lane l: page of tile 32c + l
-    float q_inv = 1.f;   // fp8 pools: 2^-e of this thread's query vector in the unit's Q terms
-    if constexpr (F8) {
-      if (!it.done) {
-        q_inv = q_to_e4m3_terms<D>(p, it.mu, row, q_s);
-        fence_proxy_async();   // the terms are read by the tensor pipe (async proxy)
-        mbar_arrive(q_full);
+    if constexpr (X == 0) {
+      // ======================================================== softmax warps (row = threadIdx.x)
+      const int row = threadIdx.x;
+      const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+      // the split partials stay in L2 for the merge
+      const uint64_t keep = l2_keep_policy(p.keep_frac);
+      bool ok = true;
+      uint32_t g = 0;              // tile ordinal
+      uint32_t gb = 0, gp = 0;     // S/P buffer (g % 3) and its phase count (g / 3)
+      TileIter<false> it;
+      it.begin(p, m_tiles, n_units, HI);
+      int pg_cur = it.done ? 0 : chunk_pages(p, it.mu, 0, lane), pg_nxt = 0;   // lane l: page of tile 32c + l
+      float q_inv = 1.f;   // fp8 pools: 2^-e of this thread's query vector in the unit's Q terms
+      if constexpr (F8) {
+        if (!it.done) {
+          q_inv = q_to_e4m3_terms<D>(p, it.mu, row, q_s);
+          fence_proxy_async();   // the terms are read by the tensor pipe (async proxy)
+          mbar_arrive(q_full);
+        }
       }
-    }
-    while (!it.done && ok) {
-      const MmaUnit mu = it.mu;
-      const int vq = mu.mt * kMmaM + row;            // this thread's query vector of the KV head
-      const bool row_ok = vq < RG;
-      const int r = row_ok ? vq / G : 0;             // its query row
-      const int gq = row_ok ? vq - r * G : 0;        // its query head within the KV head's group
-      int pos = mu.len - p.rows + r;   // last position this row sees
-      const int at = pos;              // kMod: the row's position, its first visible key, its bias per position
-      int lo_key = 0;
-      float slope = 0.f;
-      if constexpr (kMod) {
-        const KeyRange kr = row_ok ? key_range(p, mu.b, r, mu.len) : KeyRange{0, 0};
-        lo_key = kr.lo;
-        pos = kr.hi - 1;
-        if (row_ok && p.slopes) slope = p.slopes[mu.h * G + gq] * kLog2e;
-      }
-      // Fixed shift (maxdiffusion PR #477, "fixed-m"), when the caller passes score bounds: a row
-      // whose bound U >= |z| (log2 units, Cauchy-Schwarz: |q| max|k| scale log2 e) passes the gate
-      // floor((C + 125) / 2), C = 127 - ceil(log2 n) - ceil(log2 256) for the split's n keys, with
-      // every |v| <= 256, takes its weights as 2^(z - m) with m = ceil(U) - C fixed before the split is
-      // read: no running max, no rescale, and no term overflows or falls below 2^-125. Other rows keep
-      // the online max. P in E4M3 (an fp8 pool) cannot hold 2^C: that path is never fixed.
-      bool fixed = false;
-      float m_fix = 0.f;
-      if (!F8 && X == 0 && p.fs_kv_max != nullptr && row_ok) {
-        const int64_t orow = (static_cast<int64_t>(mu.b) * p.rows + r) * p.h_q + static_cast<int64_t>(mu.h) * G + gq;
-        const float2 kv = *reinterpret_cast<const float2*>(p.fs_kv_max + 2 * (static_cast<int64_t>(mu.b) * p.h_kv + mu.h));
-        const float U = p.fs_q_norm[orow] * kv.x * p.fs_scale_log2;
-        const int n_keys = max(mu.end - mu.start, 1);
-        const int Cn = 127 - (32 - __clz(n_keys - 1)) - 8;   // ceil(log2 n), ceil(log2 256) = 8
-        fixed = U <= static_cast<float>((Cn + 125) / 2) && kv.y <= 256.f;   // false for NaN bounds
-        m_fix = ceilf(U) - static_cast<float>(Cn);
-      }
-      float m_run = fixed ? m_fix : -INFINITY, l_run = 0.f;
-      float e_run = 0.f;   // fp8 pools: bound on the terms' absolute floor errors so far (same scale as l)
-      float w_run = 0.f;   // kBlk: the weight gathered as the product has it, sum of P' (l_run: of P)
-      TileScales ts, ts_next;
-      if constexpr (kBlk) ts_next.load(p, mu, mu.start, __shfl_sync(0xffffffffu, pg_cur, 0));
-      uint32_t pb = 0, pp = 0;   // buffer and phase count of the previous tile (g - 1)
-      for (int t = 0; t < mu.tiles; ++t) {
-        const int n0 = mu.start + t * kMmaN;
-        if ((t & 31) == 0 && t + 32 < mu.tiles) pg_nxt = chunk_pages(p, mu, (t >> 5) + 1, lane);
-        const int page = __shfl_sync(0xffffffffu, pg_cur, t & 31);
-        if ((t & 31) == 31) pg_cur = pg_nxt;
-        const bool tile_ok = page >= 0 && page < p.num_pages && !mu.nothing;
-        float ck[4] = {1.f, 1.f, 1.f, 1.f}, lv[4] = {0.f, 0.f, 0.f, 0.f}, iv[4] = {1.f, 1.f, 1.f, 1.f};
-        uint32_t bad_blocks = 0;
-        if constexpr (kBlk) {
-          ts = ts_next;
-          const int next = __shfl_sync(0xffffffffu, pg_cur, (t + 1) & 31);
-          if (t + 1 < mu.tiles) ts_next.load(p, mu, n0 + kMmaN, next);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const bool fit = ts.k[k] >= kMinScale && ts.k[k] <= kMaxScale && ts.v[k] >= kMinScale && ts.v[k] <= kMaxScale;
-            // a block that no row sees does not count, whatever its scale
-            if (!fit && n0 + 16 * k < mu.end && n0 + 16 * k + 16 > mu.lo && lane == 0 && warp == 0) raise_status(p.status, NBX_DEV_BAD_SCALE);
-            if (!fit) bad_blocks |= 1u << k;
-            ck[k] = fit ? ts.k[k] : 1.f;
-            lv[k] = fit ? __log2f(ts.v[k]) : 0.f;
-            iv[k] = fit ? __frcp_rn(ts.v[k]) : 1.f;
-          }
+      while (!it.done && ok) {
+        const MmaUnit mu = it.mu;
+        const int vq = mu.mt * kMmaM + row;            // this thread's query vector of the KV head
+        const bool row_ok = vq < RG;
+        const int r = row_ok ? vq / G : 0;             // its query row
+        const int gq = row_ok ? vq - r * G : 0;        // its query head within the KV head's group
+        const int pos = mu.len - p.rows + r;   // last position this row sees
+        // Fixed shift (maxdiffusion PR #477, "fixed-m"), when the caller passes score bounds: a row
+        // whose bound U >= |z| (log2 units, Cauchy-Schwarz: |q| max|k| scale log2 e) passes the gate
+        // floor((C + 125) / 2), C = 127 - ceil(log2 n) - ceil(log2 256) for the split's n keys, with
+        // every |v| <= 256, takes its weights as 2^(z - m) with m = ceil(U) - C fixed before the split is
+        // read: no running max, no rescale, and no term overflows or falls below 2^-125. Other rows keep
+        // the online max. P in E4M3 (an fp8 pool) cannot hold 2^C: that path is never fixed.
+        bool fixed = false;
+        float m_fix = 0.f;
+        if (!F8 && p.fs_kv_max != nullptr && row_ok) {
+          const int64_t orow = (static_cast<int64_t>(mu.b) * p.rows + r) * p.h_q + static_cast<int64_t>(mu.h) * G + gq;
+          const float2 kv = *reinterpret_cast<const float2*>(p.fs_kv_max + 2 * (static_cast<int64_t>(mu.b) * p.h_kv + mu.h));
+          const float U = p.fs_q_norm[orow] * kv.x * p.fs_scale_log2;
+          const int n_keys = max(mu.end - mu.start, 1);
+          const int Cn = 127 - (32 - __clz(n_keys - 1)) - 8;   // ceil(log2 n), ceil(log2 256) = 8
+          fixed = U <= static_cast<float>((Cn + 125) / 2) && kv.y <= 256.f;   // false for NaN bounds
+          m_fix = ceilf(U) - static_cast<float>(Cn);
         }
-        const uint32_t sbuf = tmem + gb * kMmaN;
-        if (!warp_wait(&s_full[gb], gp & 1u, abort_flag, wlim)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        uint32_t sr[kMmaN];
-#pragma unroll
-        for (int c = 0; c < kMmaN / 16; ++c) tmem_ld16(lane_base + (sbuf - tmem) + c * 16, sr + c * 16);
-        tmem_wait_ld();
-        const int lim = (row_ok && tile_ok) ? min(mu.end - 1, pos) - n0 : -1;   // last visible column
-        const float c = F8 ? p.qk_scale_log2 * q_inv : p.qk_scale_log2;   // 2^-e: exact
-        float mx = -INFINITY;
-        int masked;   // columns the row does not see
-        if constexpr (X == 0) {
-          masked = lim >= kMmaN - 1 ? 0 : kMmaN - 1 - lim;
-          // ---- mask, row max of the raw scores (the scale is positive, so it is the max of the
-          // scaled ones; NaN propagates through the max), 8 independent chains
-          if (!__all_sync(0xffffffffu, lim >= kMmaN - 1)) {
-#pragma unroll
-            for (int j = 0; j < kMmaN; ++j) sr[j] = j <= lim ? sr[j] : 0xff800000u;   // -inf
-          }
-          if (!fixed) {
-            float mxa[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mxa[i] = __uint_as_float(sr[i]);
-#pragma unroll
-            for (int j = 8; j < kMmaN; ++j) mxa[j & 7] = max_nan(mxa[j & 7], __uint_as_float(sr[j]));
-#pragma unroll
-            for (int w = 4; w > 0; w >>= 1)
-#pragma unroll
-              for (int i = 0; i < w; ++i) mxa[i] = max_nan(mxa[i], mxa[i + w]);
-            mx = mxa[0] * c;
-          }
-        } else {
-          // ---- the modified scores in log2 units (block scales alone stay folded into the factors ck)
-          const int low = kMod ? max(0, lo_key - n0) : 0;   // first visible column
-          masked = kMmaN - max(0, min(kMmaN - 1, lim) - low + 1);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) ck[k] *= c;
-          if constexpr (kMod) {
-            if (p.cap_log2 > 0.f) {
-              const float cx[4] = {ck[0] * p.cap_inv, ck[1] * p.cap_inv, ck[2] * p.cap_inv, ck[3] * p.cap_inv};
-              cap_scores(sr, cx, p.cap_log2);
-            } else {
-#pragma unroll
-              for (int j = 0; j < kMmaN; ++j) sr[j] = __float_as_uint(__uint_as_float(sr[j]) * ck[j >> 4]);
-            }
-            if (p.slopes != nullptr) {
-              const float far = static_cast<float>(n0 - at);
-#pragma unroll
-              for (int j = 0; j < kMmaN; ++j)
-                sr[j] = __float_as_uint(fmaf(-slope, fabsf(far + static_cast<float>(j)), __uint_as_float(sr[j])));
-            }
-          }
-          if (!__all_sync(0xffffffffu, lim >= kMmaN - 1 && low == 0 && bad_blocks == 0)) {
-#pragma unroll
-            for (int j = 0; j < kMmaN; ++j)
-              sr[j] = j <= lim && j >= low && !((bad_blocks >> (j >> 4)) & 1u) ? sr[j] : 0xff800000u;   // -inf
-          }
-          // ---- the row max of z + log2 of the V scale, by 16-column parts
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float m[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = __uint_as_float(sr[16 * k + i]);
-#pragma unroll
-            for (int i = 4; i < 16; ++i) m[i & 3] = max_nan(m[i & 3], __uint_as_float(sr[16 * k + i]));
-            const float mk = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
-            mx = max_nan(mx, kMod ? mk + lv[k] : fmaf(mk, ck[k], lv[k]));
-          }
-        }
-        // a NaN running max stays NaN (a later tile the row cannot see, max -inf, must not replace it)
-        const bool grow = !fixed && !(mx <= m_run + (F8 ? kF8Hi : kMmaTau)) && m_run == m_run;
-        float m_new = grow ? (F8 ? mx - kF8Mid : mx) : m_run;
-        float f = grow ? fast_exp2(m_run - m_new) : 1.f;
-        float ls[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ls[i] = 0.f;
-        float pv[F8 ? kMmaN : 1];   // fp8 pools: the tile's weights, kept until m is settled
-        float e_tile = 0.f;
-        if constexpr (F8) {
-          const float nm0 = (m_new == -INFINITY) ? 0.f : -m_new;
-#pragma unroll
-          for (int j = 0; j < kMmaN; ++j) {
-            if constexpr (X == 0) pv[j] = fast_exp2(fmaf(__uint_as_float(sr[j]), c, nm0));
-            else if constexpr (kMod) pv[j] = fast_exp2(__uint_as_float(sr[j]) + (nm0 + lv[j >> 4]));
-            else pv[j] = fast_exp2(fmaf(__uint_as_float(sr[j]), ck[j >> 4], nm0 + lv[j >> 4]));
-            ls[kBlk ? (j >> 4) * 2 + (j & 1) : j & 7] += pv[j];   // kBlk: two chains for each 16-column part
-          }
-          // The terms hold each p to 2^-9 p, plus an absolute floor of 2^-9 when p < 2^-1 (E4M3
-          // holds nothing below 2^-9). The floors are kept within 2^-8 of the weight gathered,
-          // l: e_run bounds their sum. A tile adds at most 2^-9 per visible position; only when
-          // that could pass the budget are its weights below 2^-1 counted (branch-free: the sign
-          // of bits(p) - bits(1/2), less the masked columns, exact zeros), and if they still pass
-          // it, m moves down to put the tile's largest weight at 2^kF8Mid = 32, which leaves the
-          // tile's floors (at most 64 * 2^-9) within 2^-8 of its weight and the budget kept -- unless
-          // the weight gathered would pass 2^40 (f = inf included), when the tile adds less than
-          // 2^-25 of the total.
-          e_tile = 0.001953125f * static_cast<float>(kMmaN - masked);
-          float w_t = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w_t += ls[i];
-          const float gathered = kBlk ? w_run : l_run;
-          const float budget = 0.00390625f * (gathered * f + w_t);
-          if (e_run * f + e_tile > budget && mx > -INFINITY) {
-            uint32_t n = 0;
-#pragma unroll
-            for (int j = 0; j < kMmaN; ++j) n += (__float_as_uint(pv[j]) - 0x3F000000u) >> 31;
-            e_tile = 0.001953125f * static_cast<float>(static_cast<int>(n) - masked);
-            const float fd = fast_exp2(m_new - (mx - kF8Mid));
-            if (e_run * f + e_tile > budget && fd > 1.f && gathered * f * fd <= kF8MaxWeight) {
-              m_new = mx - kF8Mid;
-              f *= fd;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) ls[i] *= fd;
-#pragma unroll
-              for (int j = 0; j < kMmaN; ++j) pv[j] *= fd;
-              e_tile = 0.001953125f * static_cast<float>(kMmaN - masked);   // <= 2^-8 * 2^kF8Mid
-            }
-          }
-        }
-        const float nm = (m_new == -INFINITY) ? 0.f : -m_new;   // all scores -inf: p = 0
-        // ---- p = 2^(s c - m) as two terms written over the S columns they came from (before any
-        // rescale of O: the product of the previous tile may still run meanwhile)
-        if constexpr (F8) {
-          // E4M3 terms (split4), four codes a column: P_hi over S columns [0, 16), P_lo over [16, 32)
-          uint32_t wh[16], wl[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) p_terms4(pv + 4 * i, wh[i], wl[i]);
-          tmem_st16(lane_base + (sbuf - tmem), wh);
-          tmem_st16(lane_base + (sbuf - tmem) + kMmaN / 4, wl);
-        } else {
-          // bf16 terms: P_hi = p with the low 16 bits cleared, P_lo = (p - P_hi) likewise, both exact
-          // bf16 values, p - P_hi - P_lo < 2^-14 p; pairs packed with a byte permute (upper halves),
-          // hi over S columns [0, 32), lo over [32, 64)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t wh[16], wl[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int j = half * 32 + 2 * i;
-              const float p0 = fast_exp2(kMod ? __uint_as_float(sr[j]) + nm : fmaf(__uint_as_float(sr[j]), c, nm));
-              const float p1 = fast_exp2(kMod ? __uint_as_float(sr[j + 1]) + nm : fmaf(__uint_as_float(sr[j + 1]), c, nm));
-              ls[j & 7] += p0;
-              ls[(j + 1) & 7] += p1;
-              const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-              wh[i] = __byte_perm(u0, u1, 0x7632);
-              const float l0 = p0 - __uint_as_float(u0 & 0xffff0000u);
-              const float l1 = p1 - __uint_as_float(u1 & 0xffff0000u);
-              if constexpr (X == 0) {
-                wl[i] = __byte_perm(__float_as_uint(l0), __float_as_uint(l1), 0x7632);
-              } else {   // rounded: 2^-17 p, and no bias (truncation always takes away)
-                const __nv_bfloat162 lr = __floats2bfloat162_rn(l0, l1);
-                wl[i] = *reinterpret_cast<const uint32_t*>(&lr);
-              }
-            }
-            tmem_st16(lane_base + (sbuf - tmem) + half * 16, wh);
-            tmem_st16(lane_base + (sbuf - tmem) + kMmaN / 2 + half * 16, wl);
-          }
-        }
-        if constexpr (kBlk) {
-          float parts = 0.f;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float part = ls[2 * k] + ls[2 * k + 1];
-            parts += part;
-            ls[2 * k] = part * iv[k];   // back to the sum of P
-          }
-          w_run = w_run * f + parts;
-          ls[0] = (ls[0] + ls[2]) + (ls[4] + ls[6]);
-        } else {
-#pragma unroll
-          for (int w = 4; w > 0; w >>= 1)
-#pragma unroll
-            for (int i = 0; i < w; ++i) ls[i] += ls[i + w];
-        }
-        if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-          // O holds the PVs of tiles g-t .. g-1: wait for the last, then rescale it in TMEM, 64
-          // columns a round with the loads in flight together
-          if (!warp_wait(&sp_free[pb], pp & 1u, abort_flag, wlim)) {
+        float m_run = fixed ? m_fix : -INFINITY, l_run = 0.f;
+        float e_run = 0.f;   // fp8 pools: bound on the terms' absolute floor errors so far (same scale as l)
+        uint32_t pb = 0, pp = 0;   // buffer and phase count of the previous tile (g - 1)
+        for (int t = 0; t < mu.tiles; ++t) {
+          const int n0 = mu.start + t * kMmaN;
+          if ((t & 31) == 0 && t + 32 < mu.tiles) pg_nxt = chunk_pages(p, mu, (t >> 5) + 1, lane);
+          const int page = __shfl_sync(0xffffffffu, pg_cur, t & 31);
+          if ((t & 31) == 31) pg_cur = pg_nxt;
+          const bool tile_ok = page >= 0 && page < p.num_pages;
+          const uint32_t sbuf = tmem + gb * kMmaN;
+          if (!warp_wait(&s_full[gb], gp & 1u, abort_flag, wlim)) {
             ok = false;
             break;
           }
           tc_fence_after();
-#pragma unroll 1
-          for (int cc = 0; cc < D / 64; ++cc) {
-            uint32_t ov[64];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld16(lane_base + C::kOCol + cc * 64 + q * 16, ov + q * 16);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 64; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_st16(lane_base + C::kOCol + cc * 64 + q * 16, ov + q * 16);
+          uint32_t sr[kMmaN];
+  #pragma unroll
+          for (int c = 0; c < kMmaN / 16; ++c) tmem_ld16(lane_base + (sbuf - tmem) + c * 16, sr + c * 16);
+          tmem_wait_ld();
+          // ---- mask, row max of the raw scores (the scale is positive, so it is the max of the
+          // scaled ones; NaN propagates through the max), 8 independent chains
+          const int lim = (row_ok && tile_ok) ? min(mu.end - 1, pos) - n0 : -1;   // last visible column
+          if (!__all_sync(0xffffffffu, lim >= kMmaN - 1)) {
+  #pragma unroll
+            for (int j = 0; j < kMmaN; ++j) sr[j] = j <= lim ? sr[j] : 0xff800000u;   // -inf
           }
-        }
-        m_run = m_new;
-        l_run = l_run * f + ls[0];
-        if constexpr (F8) e_run = e_run * f + e_tile;
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[gb]);
-        pb = gb;
-        pp = gp;
-        ++g;
-        if (++gb == kSBufs) {
-          gb = 0;
-          ++gp;
-        }
-      }
-      if (!ok) break;
-      if (fixed && l_run == 0.f) m_run = -INFINITY;   // no visible key: an empty partial, as online
-      float q_inv_next = 1.f;
-      if constexpr (F8) {
-        // the next unit's Q terms: every QK^T of this unit has completed (its last S was read)
-        if (it.has_next) {
-          q_inv_next = q_to_e4m3_terms<D>(p, it.next_mu(), row, q_s);
-          fence_proxy_async();
-          mbar_arrive(q_full);
-        }
-      }
-      // ---- the unit's last PV is done: O is complete
-      if (!warp_wait(&sp_free[pb], pp & 1u, abort_flag, wlim)) {
-        ok = false;
-        break;
-      }
-      it.next_unit(p);
-      q_inv = q_inv_next;
-      if (!it.done) pg_cur = chunk_pages(p, it.mu, 0, lane);
-      // ---- epilogue: O from TMEM. Each thread stores its own row, 32 columns at a time, straight
-      // from registers with 32-byte stores: every store fills whole 32-byte sectors, and nothing
-      // waits on the copy engine, which is busy with the K/V stream.
-      tc_fence_after();
-      const bool single = mu.n_splits <= 1;
-      const float sc = single ? ((m_run == -INFINITY) ? 0.f : p.v_scale / l_run) : 1.f;
-      // f16 partials (fp8 pools): acc / l, which stays within the E4M3 codes' range
-      const bool half_part = F8 && p.part_f16 && !single;
-      const float il = (m_run == -INFINITY) ? 0.f : 1.f / l_run;
-      float* dst = nullptr;
-      if (row_ok) {
-        const int64_t orow = (static_cast<int64_t>(mu.b) * p.rows + r) * p.h_q + static_cast<int64_t>(mu.h) * G + gq;
-        dst = single ? p.out + orow * D : p.acc_part + (orow * p.max_splits + mu.s) * D;
-        if (X == 0 && !single) {
-          st_global_hint(p.m_part + orow * p.max_splits + mu.s, m_run, keep);
-          st_global_hint(p.l_part + orow * p.max_splits + mu.s, l_run, keep);
-        }
-      }
-      bool finite_row = true;   // X: every value of this row of O is finite
-#pragma unroll 1
-      for (int ch = 0; ch < D / kChunk; ++ch) {
-        uint32_t ov[kChunk];
-        tmem_ld16(lane_base + C::kOCol + ch * kChunk, ov);
-        tmem_ld16(lane_base + C::kOCol + ch * kChunk + 16, ov + 16);
-        tmem_wait_ld();
-        if (ch == D / kChunk - 1) {   // O is free for the next unit's first PV
-          tc_fence_before();
-          mbar_arrive(o_free);
-        }
-        if constexpr (X != 0) {
-          float big = 0.f;   // NaN-propagating
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) big = max_nan(big, fabsf(__uint_as_float(ov[i])));
-          finite_row = finite_row && big <= 3.402823466e38f;
-        }
-        if (X != 0 && dst != nullptr && single) {
-          // the output, 16 bytes a store (it may be aligned to no more), rounded once if it is bf16
-          // (a row that sees no key is 0 whatever the product of its zero weights gave)
-          if (m_run == -INFINITY) {
-#pragma unroll
-            for (int i = 0; i < kChunk; ++i) ov[i] = 0u;
+          const float c = F8 ? p.qk_scale_log2 * q_inv : p.qk_scale_log2;   // 2^-e: exact
+          float mx = -INFINITY;
+          if (!fixed) {
+            float mxa[8];
+  #pragma unroll
+            for (int i = 0; i < 8; ++i) mxa[i] = __uint_as_float(sr[i]);
+  #pragma unroll
+            for (int j = 8; j < kMmaN; ++j) mxa[j & 7] = max_nan(mxa[j & 7], __uint_as_float(sr[j]));
+  #pragma unroll
+            for (int w = 4; w > 0; w >>= 1)
+  #pragma unroll
+              for (int i = 0; i < w; ++i) mxa[i] = max_nan(mxa[i], mxa[i + w]);
+            mx = mxa[0] * c;
           }
-          if (p.out_bf16) {
-            uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + (dst - p.out) + ch * kChunk);
-#pragma unroll
-            for (int c8 = 0; c8 < kChunk / 8; ++c8) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(ov[8 * c8 + 2 * e]) * sc,
-                                                                __uint_as_float(ov[8 * c8 + 2 * e + 1]) * sc);
-                w[e] = *reinterpret_cast<const uint32_t*>(&b2);
+          // a NaN running max stays NaN (a later tile the row cannot see, max -inf, must not replace it)
+          const bool grow = !fixed && !(mx <= m_run + (F8 ? kF8Hi : kMmaTau)) && m_run == m_run;
+          float m_new = grow ? (F8 ? mx - kF8Mid : mx) : m_run;
+          float f = grow ? fast_exp2(m_run - m_new) : 1.f;
+          float ls[8];
+  #pragma unroll
+          for (int i = 0; i < 8; ++i) ls[i] = 0.f;
+          float pv[F8 ? kMmaN : 1];   // fp8 pools: the tile's weights, kept until m is settled
+          float e_tile = 0.f;
+          if constexpr (F8) {
+            const float nm0 = (m_new == -INFINITY) ? 0.f : -m_new;
+  #pragma unroll
+            for (int j = 0; j < kMmaN; ++j) {
+              pv[j] = fast_exp2(fmaf(__uint_as_float(sr[j]), c, nm0));
+              ls[j & 7] += pv[j];
+            }
+            // The terms hold each p to 2^-9 p, plus an absolute floor of 2^-9 when p < 2^-1 (E4M3
+            // holds nothing below 2^-9). The floors are kept within 2^-8 of the weight gathered,
+            // l: e_run bounds their sum. A tile adds at most 2^-9 per visible position; only when
+            // that could pass the budget are its weights below 2^-1 counted (branch-free: the sign
+            // of bits(p) - bits(1/2), less the masked columns, exact zeros), and if they still pass
+            // it, m moves down to put the tile's largest weight at 2^kF8Mid = 32, which leaves the
+            // tile's floors (at most 64 * 2^-9) within 2^-8 of its weight and the budget kept -- unless
+            // the weight gathered would pass 2^40 (f = inf included), when the tile adds less than
+            // 2^-25 of the total.
+            const int masked = lim >= kMmaN - 1 ? 0 : kMmaN - 1 - lim;
+            e_tile = 0.001953125f * static_cast<float>(kMmaN - masked);
+            float w_t = 0.f;
+  #pragma unroll
+            for (int i = 0; i < 8; ++i) w_t += ls[i];
+            const float budget = 0.00390625f * (l_run * f + w_t);
+            if (e_run * f + e_tile > budget && mx > -INFINITY) {
+              uint32_t n = 0;
+  #pragma unroll
+              for (int j = 0; j < kMmaN; ++j) n += (__float_as_uint(pv[j]) - 0x3F000000u) >> 31;
+              e_tile = 0.001953125f * static_cast<float>(static_cast<int>(n) - masked);
+              const float fd = fast_exp2(m_new - (mx - kF8Mid));
+              if (e_run * f + e_tile > budget && fd > 1.f && l_run * f * fd <= kF8MaxWeight) {
+                m_new = mx - kF8Mid;
+                f *= fd;
+  #pragma unroll
+                for (int i = 0; i < 8; ++i) ls[i] *= fd;
+  #pragma unroll
+                for (int j = 0; j < kMmaN; ++j) pv[j] *= fd;
+                e_tile = 0.001953125f * static_cast<float>(kMmaN - masked);   // <= 2^-8 * 2^kF8Mid
               }
-              o[c8] = make_uint4(w[0], w[1], w[2], w[3]);
             }
+          }
+          const float nm = (m_new == -INFINITY) ? 0.f : -m_new;   // all scores -inf: p = 0
+          // ---- p = 2^(s c - m) as two terms written over the S columns they came from (before any
+          // rescale of O: the product of the previous tile may still run meanwhile)
+          if constexpr (F8) {
+            // E4M3 terms (split4), four codes a column: P_hi over S columns [0, 16), P_lo over [16, 32)
+            uint32_t wh[16], wl[16];
+  #pragma unroll
+            for (int i = 0; i < 16; ++i) p_terms4(pv + 4 * i, wh[i], wl[i]);
+            tmem_st16(lane_base + (sbuf - tmem), wh);
+            tmem_st16(lane_base + (sbuf - tmem) + kMmaN / 4, wl);
           } else {
-            float4* o = reinterpret_cast<float4*>(dst + ch * kChunk);
-#pragma unroll
-            for (int c4 = 0; c4 < kChunk / 4; ++c4)
-              o[c4] = make_float4(__uint_as_float(ov[4 * c4]) * sc, __uint_as_float(ov[4 * c4 + 1]) * sc,
-                                  __uint_as_float(ov[4 * c4 + 2]) * sc, __uint_as_float(ov[4 * c4 + 3]) * sc);
-          }
-        } else if (dst != nullptr && half_part) {
-          // 32 halves: two 32-byte stores into the first half of the split's slot
-#pragma unroll
-          for (int c16 = 0; c16 < kChunk / 16; ++c16) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const __half2 h = __floats2half2_rn(__uint_as_float(ov[16 * c16 + 2 * e]) * il,
-                                                  __uint_as_float(ov[16 * c16 + 2 * e + 1]) * il);
-              v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+            // bf16 terms: P_hi = p with the low 16 bits cleared, P_lo = (p - P_hi) likewise, both exact
+            // bf16 values, p - P_hi - P_lo < 2^-14 p; pairs packed with a byte permute (upper halves),
+            // hi over S columns [0, 32), lo over [32, 64)
+  #pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t wh[16], wl[16];
+  #pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int j = half * 32 + 2 * i;
+                const float p0 = fast_exp2(fmaf(__uint_as_float(sr[j]), c, nm));
+                const float p1 = fast_exp2(fmaf(__uint_as_float(sr[j + 1]), c, nm));
+                ls[j & 7] += p0;
+                ls[(j + 1) & 7] += p1;
+                const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+                wh[i] = __byte_perm(u0, u1, 0x7632);
+                const float l0 = p0 - __uint_as_float(u0 & 0xffff0000u);
+                const float l1 = p1 - __uint_as_float(u1 & 0xffff0000u);
+                wl[i] = __byte_perm(__float_as_uint(l0), __float_as_uint(l1), 0x7632);
+              }
+              tmem_st16(lane_base + (sbuf - tmem) + half * 16, wh);
+              tmem_st16(lane_base + (sbuf - tmem) + kMmaN / 2 + half * 16, wl);
             }
-            st_global_v8_hint(dst + (ch * kChunk) / 2 + c16 * 8, v, keep);   // kept in L2 for the merge
           }
-        } else if (dst != nullptr) {
-#pragma unroll
-          for (int c8 = 0; c8 < kChunk / 8; ++c8) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[8 * c8 + e]) * sc;
-            if (single) st_global_v8(dst + ch * kChunk + c8 * 8, v);
-            else st_global_v8_hint(dst + ch * kChunk + c8 * 8, v, keep);   // kept in L2 for the merge
+  #pragma unroll
+          for (int w = 4; w > 0; w >>= 1)
+  #pragma unroll
+            for (int i = 0; i < w; ++i) ls[i] += ls[i + w];
+          if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            // O holds the PVs of tiles g-t .. g-1: wait for the last, then rescale it in TMEM, 64
+            // columns a round with the loads in flight together
+            if (!warp_wait(&sp_free[pb], pp & 1u, abort_flag, wlim)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+  #pragma unroll 1
+            for (int cc = 0; cc < D / 64; ++cc) {
+              uint32_t ov[64];
+  #pragma unroll
+              for (int q = 0; q < 4; ++q) tmem_ld16(lane_base + C::kOCol + cc * 64 + q * 16, ov + q * 16);
+              tmem_wait_ld();
+  #pragma unroll
+              for (int i = 0; i < 64; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+  #pragma unroll
+              for (int q = 0; q < 4; ++q) tmem_st16(lane_base + C::kOCol + cc * 64 + q * 16, ov + q * 16);
+            }
+          }
+          m_run = m_new;
+          l_run = l_run * f + ls[0];
+          if constexpr (F8) e_run = e_run * f + e_tile;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&p_full[gb]);
+          pb = gb;
+          pp = gp;
+          ++g;
+          if (++gb == kSBufs) {
+            gb = 0;
+            ++gp;
           }
         }
-      }
-      if constexpr (X != 0) {
-        // m and l come last: m says whether the row is to be recomputed (a NaN m is a NaN that the row sees)
-        const bool redo = !finite_row && m_run == m_run && m_run != -INFINITY;
-        if (__any_sync(0xffffffffu, redo && dst != nullptr) && lane == 0) p.header[2] = 1;
-        if (dst != nullptr) {
+        if (!ok) break;
+        if (fixed && l_run == 0.f) m_run = -INFINITY;   // no visible key: an empty partial, as online
+        float q_inv_next = 1.f;
+        if constexpr (F8) {
+          // the next unit's Q terms: every QK^T of this unit has completed (its last S was read)
+          if (it.has_next) {
+            q_inv_next = q_to_e4m3_terms<D>(p, it.next_mu(), row, q_s);
+            fence_proxy_async();
+            mbar_arrive(q_full);
+          }
+        }
+        // ---- the unit's last PV is done: O is complete
+        if (!warp_wait(&sp_free[pb], pp & 1u, abort_flag, wlim)) {
+          ok = false;
+          break;
+        }
+        it.next_unit(p);
+        q_inv = q_inv_next;
+        if (!it.done) pg_cur = chunk_pages(p, it.mu, 0, lane);
+        // ---- epilogue: O from TMEM. Each thread stores its own row, 32 columns at a time, straight
+        // from registers with 32-byte stores: every store fills whole 32-byte sectors, and nothing
+        // waits on the copy engine, which is busy with the K/V stream.
+        tc_fence_after();
+        const bool single = mu.n_splits <= 1;
+        const float sc = single ? ((m_run == -INFINITY) ? 0.f : p.v_scale / l_run) : 1.f;
+        // f16 partials (fp8 pools): acc / l, which stays within the E4M3 codes' range
+        const bool half_part = F8 && p.part_f16 && !single;
+        const float il = (m_run == -INFINITY) ? 0.f : 1.f / l_run;
+        float* dst = nullptr;
+        if (row_ok) {
           const int64_t orow = (static_cast<int64_t>(mu.b) * p.rows + r) * p.h_q + static_cast<int64_t>(mu.h) * G + gq;
-          const int64_t slot = orow * p.max_splits + mu.s;
-          st_global_hint(p.m_part + slot, redo ? __uint_as_float(kRedoBits) : m_run, keep);
-          st_global_hint(p.l_part + slot, l_run, keep);
+          dst = single ? p.out + orow * D : p.acc_part + (orow * p.max_splits + mu.s) * D;
+          if (!single) {
+            st_global_hint(p.m_part + orow * p.max_splits + mu.s, m_run, keep);
+            st_global_hint(p.l_part + orow * p.max_splits + mu.s, l_run, keep);
+          }
         }
+  #pragma unroll 1
+        for (int ch = 0; ch < D / kChunk; ++ch) {
+          uint32_t ov[kChunk];
+          tmem_ld16(lane_base + C::kOCol + ch * kChunk, ov);
+          tmem_ld16(lane_base + C::kOCol + ch * kChunk + 16, ov + 16);
+          tmem_wait_ld();
+          if (ch == D / kChunk - 1) {   // O is free for the next unit's first PV
+            tc_fence_before();
+            mbar_arrive(o_free);
+          }
+          if (dst != nullptr && half_part) {
+            // 32 halves: two 32-byte stores into the first half of the split's slot
+  #pragma unroll
+            for (int c16 = 0; c16 < kChunk / 16; ++c16) {
+              float v[8];
+  #pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const __half2 h = __floats2half2_rn(__uint_as_float(ov[16 * c16 + 2 * e]) * il,
+                                                    __uint_as_float(ov[16 * c16 + 2 * e + 1]) * il);
+                v[e] = __uint_as_float(*reinterpret_cast<const uint32_t*>(&h));
+              }
+              st_global_v8_hint(dst + (ch * kChunk) / 2 + c16 * 8, v, keep);   // kept in L2 for the merge
+            }
+          } else if (dst != nullptr) {
+  #pragma unroll
+            for (int c8 = 0; c8 < kChunk / 8; ++c8) {
+              float v[8];
+  #pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[8 * c8 + e]) * sc;
+              if (single) st_global_v8(dst + ch * kChunk + c8 * 8, v);
+              else st_global_v8_hint(dst + ch * kChunk + c8 * 8, v, keep);   // kept in L2 for the merge
+            }
+          }
+        }
+        if (!ok) break;
       }
-      if (!ok) break;
-    }
-    if (!ok) {
-      *abort_flag = 1;
-      if (threadIdx.x == 0) raise_status(p.status, NBX_DEV_TIMEOUT);
+      if (!ok) {
+        *abort_flag = 1;
+        if (threadIdx.x == 0) raise_status(p.status, NBX_DEV_TIMEOUT);
+      }
+    } else {
+      // ====================================================== softmax warps of a modified decode
+      if (!softmax_modified<D, F8, X>(p, q_s, s_full, p_full, sp_free, q_full, o_free, xbar, xbuf, tmem, m_tiles, n_units,
+                                      abort_flag, wlim)) {
+        *abort_flag = 1;
+        if (threadIdx.x == 0 || threadIdx.x == 256) raise_status(p.status, NBX_DEV_TIMEOUT);
+      }
     }
   }
 
@@ -1275,7 +1547,7 @@ const MmaMaps* cached_maps(const DecodeParams& p, bool f8, int device) {
 
 template <int D, bool F8, int X = 0>
 cudaError_t launch_mma(const DecodeParams& p, int grid_limit, cudaStream_t stream) {
-  using C = MmaCfg<D, F8>;
+  using C = MmaCfg<D, F8, X>;
   static std::atomic<uint64_t> configured{0};   // devices whose shared-memory limit is raised
   const DeviceInfo& di = device_info();
   const MmaMaps* maps = cached_maps(p, F8, di.device);
@@ -1297,9 +1569,9 @@ cudaError_t launch_mma(const DecodeParams& p, int grid_limit, cudaStream_t strea
   if (grid > upper) grid = upper;
   if (grid < 1) grid = 1;
   if (p.wait_limit_ns != kWaitLimitNs || p.producer_delay_ns != 0)   // a test of the timeout path
-    return launch_pdl(decode_partial_mma_kernel<D, F8, true, X>, static_cast<unsigned>(grid), kMmaThreads, C::kSmem,
+    return launch_pdl(decode_partial_mma_kernel<D, F8, true, X>, static_cast<unsigned>(grid), X ? kMmaThreadsMod : kMmaThreads, C::kSmem,
                       stream, p, *maps);
-  return launch_pdl(decode_partial_mma_kernel<D, F8, false, X>, static_cast<unsigned>(grid), kMmaThreads, C::kSmem,
+  return launch_pdl(decode_partial_mma_kernel<D, F8, false, X>, static_cast<unsigned>(grid), X ? kMmaThreadsMod : kMmaThreads, C::kSmem,
                     stream, p, *maps);
 }
 
