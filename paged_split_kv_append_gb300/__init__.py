@@ -421,61 +421,78 @@ def nbx_decode_fixed_shift_gate(n_keys: int, v_max_bound: float = 256.0):
 
 # ---------------------------------------------------------------- the block-scaled cache and the pages
 # These calls check that every tensor sits on one device, and run there whatever the current device is.
-class _Device:
-    """The device of a call's tensors, made current for the call; the stream defaults to its current one."""
-
-    def __init__(self, **tensors):
-        self.dev = None
-        for n, t in tensors.items():
-            if t is None:
-                continue
-            _cuda_contig(n, t)
-            if self.dev is None:
-                self.dev = t.device
-            elif t.device != self.dev:
-                raise ValueError(f"{n} is on {t.device}, not on {self.dev}")
-        self.back = None
-
-    def stream(self, stream) -> ctypes.c_void_p:
-        return _stream(torch.cuda.current_stream(self.dev) if stream is None else stream)
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.dev)
-        return self
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+# Their GPU work can be as short as a few microseconds, so the checks keep to a few cheap tensor methods,
+# pointers are passed as plain integers and the stream is looked up as a raw handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _int32(shape_ok: bool = True, **tensors):
-    for n, t in tensors.items():
-        if t is not None and t.dtype != torch.int32:
-            raise ValueError(f"{n} must be int32")
-    if not shape_ok:
-        raise ValueError("shapes do not fit: " + ", ".join(f"{n} {list(t.shape)}" for n, t in tensors.items()
-                                                           if t is not None))
+def _one_device(names: str, *tensors) -> int:
+    """The index of the CUDA device that all the given tensors (None skipped) sit on; contiguous all."""
+    dev = -2
+    for i, t in enumerate(tensors):
+        if t is None:
+            continue
+        d = t.get_device()
+        if d != dev or not t.is_contiguous():
+            name = names.split()[i]
+            if d < 0:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if dev >= 0:
+                raise ValueError(f"{name} is on cuda:{d}, not on cuda:{dev}")
+            dev = d
+    return dev
+
+
+def _int32(names: str, *tensors):
+    for i, t in enumerate(tensors):
+        if t is not None and t.dtype is not torch.int32:
+            raise ValueError(f"{names.split()[i]} must be int32")
+
+
+def _misfit(names: str, *tensors):
+    raise ValueError("shapes do not fit: " + ", ".join(f"{n} {list(t.shape)}" for n, t in zip(names.split(), tensors)
+                                                       if t is not None))
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(func: str, dev: int, stream, *args):
+    """Calls the entry point on device `dev` and the given (or its current) stream, the last argument."""
+    st = _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
+    f = getattr(_lib or lib(), func)
+    if torch.cuda.current_device() == dev:
+        code = f(*args, st)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, st)
+    if code:
+        raise NbxError(func, code)
 
 
 def _pools(k_pool, v_pool, k_scales, v_scales):
     """(num_pages, h_kv, page_tokens, d, positions per scale or 0) of a layer's pools."""
-    if k_pool.dim() != 4 or k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype:
+    shape = k_pool.shape
+    if len(shape) != 4 or shape != v_pool.shape or k_pool.dtype != v_pool.dtype:
         raise ValueError("k_pool and v_pool [num_pages, h_kv, page_tokens, d] must match")
-    num_pages, h_kv, page_tokens, d = k_pool.shape
-    if (k_scales is None) != (v_scales is None):
-        raise ValueError("k_scales and v_scales come together")
-    if k_scales is None:
+    num_pages, h_kv, page_tokens, d = shape
+    if k_scales is None and v_scales is None:
         return num_pages, h_kv, page_tokens, d, 0
-    if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32 or k_scales.shape != v_scales.shape or \
-            k_scales.dim() != 3 or tuple(k_scales.shape[:2]) != (num_pages, h_kv) or k_scales.shape[2] < 1 or \
-            page_tokens % k_scales.shape[2] != 0:
-        raise ValueError(f"k_scales {list(k_scales.shape)} and v_scales {list(v_scales.shape)} must be fp32 "
-                         f"[num_pages, h_kv, page_tokens / scale_tokens] for the pool {list(k_pool.shape)}")
+    if k_scales is None or v_scales is None:
+        raise ValueError("k_scales and v_scales come together")
+    blocks = k_scales.shape
+    if k_scales.dtype is not torch.float32 or v_scales.dtype is not torch.float32 or blocks != v_scales.shape or \
+            len(blocks) != 3 or blocks[0] != num_pages or blocks[1] != h_kv or blocks[2] < 1 or \
+            page_tokens % blocks[2] != 0:
+        raise ValueError(f"k_scales {list(blocks)} and v_scales {list(v_scales.shape)} must be fp32 "
+                         f"[num_pages, h_kv, page_tokens / scale_tokens] for the pool {list(shape)}")
     if dtype_code(k_pool) != NBX_E4M3:
         raise ValueError("only e4m3 pools have scales")
-    return num_pages, h_kv, page_tokens, d, page_tokens // k_scales.shape[2]
+    return num_pages, h_kv, page_tokens, d, page_tokens // blocks[2]
 
 
 def nbx_paged_kv_append_block_scaled(new_k: torch.Tensor, new_v: torch.Tensor, k_pool: torch.Tensor,
@@ -485,23 +502,17 @@ def nbx_paged_kv_append_block_scaled(new_k: torch.Tensor, new_v: torch.Tensor, k
     """new_k / new_v [n_tok, h_kv, d] (fp32 or bf16): rows tok_start[b] .. tok_start[b + 1] - 1 are sequence
     b's tokens at positions lens[b] and up, quantised into the e4m3 pools and scales [num_pages, h_kv,
     page_tokens / scale_tokens]. lens [batch] and tok_start [batch + 1] int32; lens is not advanced."""
-    dv = _Device(new_k=new_k, new_v=new_v, k_pool=k_pool, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales,
-                 block_table=block_table, lens=lens, tok_start=tok_start, status=status)
-    if new_k.dim() != 3 or new_k.shape != new_v.shape or new_k.dtype != new_v.dtype:
-        raise ValueError("new_k and new_v [n_tok, h_kv, d] must match")
+    dev = _one_device("new_k new_v k_pool v_pool k_scales v_scales block_table lens tok_start status", new_k, new_v,
+                      k_pool, v_pool, k_scales, v_scales, block_table, lens, tok_start, status)
+    _int32("block_table lens tok_start status", block_table, lens, tok_start, status)
     num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
-    n_tok = new_k.shape[0]
-    if tuple(new_k.shape[1:]) != (h_kv, d):
-        raise ValueError(f"new {list(new_k.shape)} does not fit the pool {list(k_pool.shape)}")
-    batch = lens.numel()
-    _int32(block_table.dim() == 2 and block_table.shape[0] == batch and tok_start.numel() == batch + 1,
-           block_table=block_table, lens=lens, tok_start=tok_start, status=status)
-    with dv:
-        st = lib().nbx_paged_kv_append_block_scaled(
-            _ptr(new_k), _ptr(new_v), dtype_code(new_k), n_tok, h_kv, d, _ptr(k_pool), _ptr(v_pool), _ptr(k_scales),
-            _ptr(v_scales), block, num_pages, page_tokens, _ptr(block_table), block_table.shape[1], batch, _ptr(lens),
-            _ptr(tok_start), _ptr(status), dv.stream(stream))
-    _check("nbx_paged_kv_append_block_scaled", st)
+    new, table, batch = new_k.shape, block_table.shape, lens.numel()
+    if new != new_v.shape or new_k.dtype != new_v.dtype or len(new) != 3 or new[1] != h_kv or new[2] != d or \
+            len(table) != 2 or table[0] != batch or tok_start.numel() != batch + 1:
+        _misfit("new_k new_v k_pool block_table lens tok_start", new_k, new_v, k_pool, block_table, lens, tok_start)
+    _run("nbx_paged_kv_append_block_scaled", dev, stream, new_k.data_ptr(), new_v.data_ptr(), dtype_code(new_k), new[0],
+         h_kv, d, k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block, num_pages,
+         page_tokens, block_table.data_ptr(), table[1], batch, lens.data_ptr(), tok_start.data_ptr(), _p(status))
 
 
 def nbx_paged_decode_modified_workspace_bytes(batch: int, rows: int, h_q: int, h_kv: int, d: int,
@@ -518,27 +529,26 @@ def nbx_paged_decode_modified_partial_kernel(q_dtype: int, pool_dtype: int, out_
     return k
 
 
-def _modified_call(dv, q, k_pool, block_table, seq_lens, max_seq_len, slopes, key_begin, key_end, out, out_dtype,
-                   workspace, status):
-    """The shapes and types the two modified decodes share: (out, workspace, workspace bytes)."""
-    if q.dim() != 4:
-        raise ValueError("q must be [batch, rows, h_q, d]")
-    batch, rows, h_q, d = q.shape
-    _int32(block_table.dim() == 2 and block_table.shape[0] == batch and seq_lens.numel() == batch and
-           all(k is None or tuple(k.shape) == (batch, rows) for k in (key_begin, key_end)), block_table=block_table,
-           seq_lens=seq_lens, key_begin=key_begin, key_end=key_end, status=status)
-    if k_pool.shape[3] != d:
-        raise ValueError(f"q {list(q.shape)} does not fit the pool {list(k_pool.shape)}")
-    if slopes is not None and (slopes.dtype != torch.float32 or slopes.numel() != h_q):
-        raise ValueError("slopes must be fp32 [h_q]")
+def _modified_shapes(q, d, block_table, seq_lens, slopes, key_begin, key_end, out, out_dtype, status):
+    """The checks the two modified decodes share: (batch, rows, h_q, max_pages, out)."""
+    shape, table = q.shape, block_table.shape
+    _int32("block_table seq_lens key_begin key_end status", block_table, seq_lens, key_begin, key_end, status)
+    if len(shape) != 4 or shape[3] != d or len(table) != 2 or table[0] != shape[0] or seq_lens.numel() != shape[0] or \
+            (key_begin is not None and key_begin.shape != shape[:2]) or \
+            (key_end is not None and key_end.shape != shape[:2]) or \
+            (slopes is not None and slopes.numel() != shape[2]):
+        _misfit("q block_table seq_lens slopes key_begin key_end", q, block_table, seq_lens, slopes, key_begin, key_end)
+    if slopes is not None and slopes.dtype is not torch.float32:
+        raise ValueError("slopes must be fp32")
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or torch.float32, device=dv.dev)
-    elif out.shape != q.shape or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out must be {list(q.shape)}" + (f" {out_dtype}" if out_dtype else ""))
-    if workspace is None:
-        need = nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, k_pool.shape[1], d, max_seq_len)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dv.dev)
-    return out, workspace, workspace.numel() * workspace.element_size()
+        out = torch.empty(shape, dtype=out_dtype or torch.float32, device=q.device)
+    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be {list(shape)}" + (f" {out_dtype}" if out_dtype else ""))
+    return shape[0], shape[1], shape[2], table[1], out
+
+
+def _workspace(need, q):
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
 
 
 def nbx_paged_decode_attn_block_scaled(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -552,20 +562,19 @@ def nbx_paged_decode_attn_block_scaled(q: torch.Tensor, k_pool: torch.Tensor, v_
     """q [batch, rows, h_q, d] (fp32 or bf16) over a block-scaled cache (e4m3 pools, scales [num_pages, h_kv,
     page_tokens / scale_tokens] fp32) -> out [batch, rows, h_q, d], fp32 or bf16 (out's dtype, or out_dtype).
     The score modifications are those of nbx_paged_decode_attn_modified."""
-    dv = _Device(q=q, k_pool=k_pool, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, block_table=block_table,
-                 seq_lens=seq_lens, slopes=slopes, key_begin=key_begin, key_end=key_end, out=out, workspace=workspace,
-                 status=status)
+    dev = _one_device("q k_pool v_pool k_scales v_scales block_table seq_lens slopes key_begin key_end out workspace status",
+                      q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, slopes, key_begin, key_end, out,
+                      workspace, status)
     num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
-    out, workspace, ws_bytes = _modified_call(dv, q, k_pool, block_table, seq_lens, max_seq_len, slopes, key_begin,
-                                              key_end, out, out_dtype, workspace, status)
-    batch, rows, h_q, _ = q.shape
-    with dv:
-        st = lib().nbx_paged_decode_attn_block_scaled(
-            _ptr(q), dtype_code(q), batch, rows, h_q, d, _ptr(k_pool), _ptr(v_pool), _ptr(k_scales), _ptr(v_scales), block,
-            num_pages, h_kv, page_tokens, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), int(max_seq_len),
-            float(scale), float(softcap), _ptr(slopes), _ptr(key_begin), _ptr(key_end), _ptr(out), dtype_code(out),
-            _ptr(workspace), ws_bytes, _ptr(status), dv.stream(stream))
-    _check("nbx_paged_decode_attn_block_scaled", st)
+    batch, rows, h_q, max_pages, out = _modified_shapes(q, d, block_table, seq_lens, slopes, key_begin, key_end, out,
+                                                        out_dtype, status)
+    if workspace is None:
+        workspace = _workspace(nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len), q)
+    _run("nbx_paged_decode_attn_block_scaled", dev, stream, q.data_ptr(), dtype_code(q), batch, rows, h_q, d,
+         k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block, num_pages, h_kv,
+         page_tokens, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), int(max_seq_len), float(scale), float(softcap), _p(slopes),
+         _p(key_begin), _p(key_end), out.data_ptr(), dtype_code(out), workspace.data_ptr(), workspace.nbytes,
+         _p(status))
     return out
 
 
@@ -580,19 +589,17 @@ def nbx_paged_decode_attn_modified(q: torch.Tensor, k_pool: torch.Tensor, v_pool
     (-slopes[h] * |p - j|, slopes [h_q] fp32) and per-row key ranges (key_begin / key_end [batch, rows] int32, by
     default 0 and p + 1: document, prefix and window masks). out [batch, rows, h_q, d] is fp32 or bf16 (out's dtype,
     or out_dtype)."""
-    dv = _Device(q=q, k_pool=k_pool, v_pool=v_pool, block_table=block_table, seq_lens=seq_lens, slopes=slopes,
-                 key_begin=key_begin, key_end=key_end, out=out, workspace=workspace, status=status)
+    dev = _one_device("q k_pool v_pool block_table seq_lens slopes key_begin key_end out workspace status", q, k_pool,
+                      v_pool, block_table, seq_lens, slopes, key_begin, key_end, out, workspace, status)
     num_pages, h_kv, page_tokens, d, _ = _pools(k_pool, v_pool, None, None)
-    out, workspace, ws_bytes = _modified_call(dv, q, k_pool, block_table, seq_lens, max_seq_len, slopes, key_begin,
-                                              key_end, out, out_dtype, workspace, status)
-    batch, rows, h_q, _ = q.shape
-    with dv:
-        st = lib().nbx_paged_decode_attn_modified(
-            _ptr(q), dtype_code(q), batch, rows, h_q, d, _ptr(k_pool), _ptr(v_pool), dtype_code(k_pool), num_pages, h_kv,
-            page_tokens, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), int(max_seq_len), float(scale),
-            float(k_scale), float(v_scale), float(softcap), _ptr(slopes), _ptr(key_begin), _ptr(key_end), _ptr(out),
-            dtype_code(out), _ptr(workspace), ws_bytes, _ptr(status), dv.stream(stream))
-    _check("nbx_paged_decode_attn_modified", st)
+    batch, rows, h_q, max_pages, out = _modified_shapes(q, d, block_table, seq_lens, slopes, key_begin, key_end, out,
+                                                        out_dtype, status)
+    if workspace is None:
+        workspace = _workspace(nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len), q)
+    _run("nbx_paged_decode_attn_modified", dev, stream, q.data_ptr(), dtype_code(q), batch, rows, h_q, d,
+         k_pool.data_ptr(), v_pool.data_ptr(), dtype_code(k_pool), num_pages, h_kv, page_tokens, block_table.data_ptr(),
+         max_pages, seq_lens.data_ptr(), int(max_seq_len), float(scale), float(k_scale), float(v_scale), float(softcap),
+         _p(slopes), _p(key_begin), _p(key_end), out.data_ptr(), dtype_code(out), workspace.data_ptr(), workspace.nbytes, _p(status))
     return out
 
 
@@ -601,16 +608,15 @@ def nbx_paged_kv_copy_pages(moves: torch.Tensor, n_moves: torch.Tensor, k_pool: 
                             status: Optional[torch.Tensor] = None, stream=None) -> None:
     """The first n_moves[0] of moves [max_moves, 3] int32 {source page, destination page, positions}, on one
     layer's pools and, for a block-scaled cache, scales."""
-    dv = _Device(moves=moves, n_moves=n_moves, k_pool=k_pool, v_pool=v_pool, k_scales=k_scales, v_scales=v_scales,
-                 status=status)
+    dev = _one_device("moves n_moves k_pool v_pool k_scales v_scales status", moves, n_moves, k_pool, v_pool, k_scales,
+                      v_scales, status)
     num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
-    _int32(moves.dim() == 2 and moves.shape[1] == 3 and n_moves.numel() >= 1, moves=moves, n_moves=n_moves,
-           status=status)
-    with dv:
-        st = lib().nbx_paged_kv_copy_pages(_ptr(moves), _ptr(n_moves), moves.shape[0], _ptr(k_pool), _ptr(v_pool),
-                                           dtype_code(k_pool), num_pages, h_kv, page_tokens, d, _ptr(k_scales),
-                                           _ptr(v_scales), block, _ptr(status), dv.stream(stream))
-    _check("nbx_paged_kv_copy_pages", st)
+    _int32("moves n_moves status", moves, n_moves, status)
+    if moves.dim() != 2 or moves.shape[1] != 3 or n_moves.numel() < 1:
+        _misfit("moves n_moves", moves, n_moves)
+    _run("nbx_paged_kv_copy_pages", dev, stream, moves.data_ptr(), n_moves.data_ptr(), moves.shape[0], k_pool.data_ptr(),
+         v_pool.data_ptr(), dtype_code(k_pool), num_pages, h_kv, page_tokens, d, _p(k_scales), _p(v_scales), block,
+         _p(status))
 
 
 def nbx_paged_kv_fork_workspace_bytes(batch: int, max_pages: int, n_fork: int, num_pages: int) -> int:
@@ -625,29 +631,27 @@ def nbx_paged_kv_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, fork_sr
     """Rows fork_dst[i] of block_table [batch, max_pages] and seq_lens [batch] become rows fork_src[i] as they
     were (all int32): full pages shared, the last partial page copied to a free one. Returns (moves [n_fork, 3],
     n_moves [1]): the copies made, for nbx_paged_kv_copy_pages on the other layers' pools."""
-    dv = _Device(block_table=block_table, seq_lens=seq_lens, fork_src=fork_src, fork_dst=fork_dst, k_pool=k_pool,
-                 v_pool=v_pool, k_scales=k_scales, v_scales=v_scales, moves=moves, n_moves=n_moves,
-                 workspace=workspace, status=status)
+    dev = _one_device("block_table seq_lens fork_src fork_dst k_pool v_pool k_scales v_scales moves n_moves workspace status",
+                      block_table, seq_lens, fork_src, fork_dst, k_pool, v_pool, k_scales, v_scales, moves, n_moves,
+                      workspace, status)
+    _int32("block_table seq_lens fork_src fork_dst moves n_moves status", block_table, seq_lens, fork_src, fork_dst, moves,
+           n_moves, status)
     num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
-    n = fork_src.numel()
+    n, table = fork_src.numel(), block_table.shape
     if moves is None:
-        moves = torch.full((n, 3), -1, dtype=torch.int32, device=dv.dev)
+        moves = torch.full((n, 3), -1, dtype=torch.int32, device=block_table.device)
     if n_moves is None:
-        n_moves = torch.zeros(1, dtype=torch.int32, device=dv.dev)
-    _int32(block_table.dim() == 2 and block_table.shape[0] == seq_lens.numel() and fork_dst.numel() == n and
-           tuple(moves.shape) == (n, 3) and n_moves.numel() >= 1, block_table=block_table, seq_lens=seq_lens,
-           fork_src=fork_src, fork_dst=fork_dst, moves=moves, n_moves=n_moves, status=status)
-    batch, max_pages = block_table.shape
+        n_moves = torch.zeros(1, dtype=torch.int32, device=block_table.device)
+    if len(table) != 2 or seq_lens.numel() != table[0] or fork_dst.numel() != n or moves.shape != (n, 3) or \
+            n_moves.numel() < 1:
+        _misfit("block_table seq_lens fork_src fork_dst moves n_moves", block_table, seq_lens, fork_src, fork_dst, moves,
+                n_moves)
     if workspace is None:
-        workspace = torch.empty(max(nbx_paged_kv_fork_workspace_bytes(batch, max_pages, n, num_pages), 256),
-                                dtype=torch.uint8, device=dv.dev)
-    with dv:
-        st = lib().nbx_paged_kv_fork(_ptr(block_table), max_pages, _ptr(seq_lens), batch, _ptr(fork_src),
-                                     _ptr(fork_dst), n, _ptr(k_pool), _ptr(v_pool), dtype_code(k_pool), num_pages,
-                                     h_kv, page_tokens, d, _ptr(k_scales), _ptr(v_scales), block, _ptr(moves),
-                                     _ptr(n_moves), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                     _ptr(status), dv.stream(stream))
-    _check("nbx_paged_kv_fork", st)
+        workspace = _workspace(nbx_paged_kv_fork_workspace_bytes(table[0], table[1], n, num_pages), block_table)
+    _run("nbx_paged_kv_fork", dev, stream, block_table.data_ptr(), table[1], seq_lens.data_ptr(), table[0],
+         fork_src.data_ptr(), fork_dst.data_ptr(), n, k_pool.data_ptr(), v_pool.data_ptr(), dtype_code(k_pool), num_pages,
+         h_kv, page_tokens, d, _p(k_scales), _p(v_scales), block, moves.data_ptr(), n_moves.data_ptr(),
+         workspace.data_ptr(), workspace.nbytes, _p(status))
     return moves, n_moves
 
 
@@ -663,29 +667,26 @@ def nbx_paged_kv_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, k_po
     """The pages in use moved to the lowest ids. Returns (new_block_table, moves [num_pages // 2, 3], counts [2] =
     {moves, pages in use}); new_block_table may be block_table itself. The moves are for
     nbx_paged_kv_copy_pages on the other layers' pools."""
-    dv = _Device(block_table=block_table, seq_lens=seq_lens, k_pool=k_pool, v_pool=v_pool, k_scales=k_scales,
-                 v_scales=v_scales, new_block_table=new_block_table, moves=moves, counts=counts, workspace=workspace,
-                 status=status)
+    dev = _one_device("block_table seq_lens k_pool v_pool k_scales v_scales new_block_table moves counts workspace status",
+                      block_table, seq_lens, k_pool, v_pool, k_scales, v_scales, new_block_table, moves, counts, workspace,
+                      status)
+    _int32("block_table seq_lens new_block_table moves counts status", block_table, seq_lens, new_block_table, moves, counts,
+           status)
     num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
+    table = block_table.shape
     if new_block_table is None:
         new_block_table = torch.empty_like(block_table)
     if moves is None:
-        moves = torch.full((max(1, num_pages // 2), 3), -1, dtype=torch.int32, device=dv.dev)
+        moves = torch.full((max(1, num_pages // 2), 3), -1, dtype=torch.int32, device=block_table.device)
     if counts is None:
-        counts = torch.zeros(2, dtype=torch.int32, device=dv.dev)
-    _int32(block_table.dim() == 2 and block_table.shape[0] == seq_lens.numel() and
-           new_block_table.shape == block_table.shape and moves.dim() == 2 and moves.shape[1] == 3 and
-           counts.numel() >= 2, block_table=block_table, seq_lens=seq_lens, new_block_table=new_block_table,
-           moves=moves, counts=counts, status=status)
+        counts = torch.zeros(2, dtype=torch.int32, device=block_table.device)
+    if len(table) != 2 or seq_lens.numel() != table[0] or new_block_table.shape != table or moves.dim() != 2 or \
+            moves.shape[1] != 3 or counts.numel() < 2:
+        _misfit("block_table seq_lens new_block_table moves counts", block_table, seq_lens, new_block_table, moves, counts)
     if workspace is None:
-        workspace = torch.empty(max(nbx_paged_kv_compact_workspace_bytes(num_pages), 256), dtype=torch.uint8,
-                                device=dv.dev)
-    with dv:
-        st = lib().nbx_paged_kv_compact(_ptr(block_table), _ptr(new_block_table), block_table.shape[1],
-                                        _ptr(seq_lens), block_table.shape[0], _ptr(k_pool), _ptr(v_pool),
-                                        dtype_code(k_pool), num_pages, h_kv, page_tokens, d, _ptr(k_scales),
-                                        _ptr(v_scales), block, _ptr(moves), moves.shape[0], _ptr(counts),
-                                        _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
-                                        dv.stream(stream))
-    _check("nbx_paged_kv_compact", st)
+        workspace = _workspace(nbx_paged_kv_compact_workspace_bytes(num_pages), block_table)
+    _run("nbx_paged_kv_compact", dev, stream, block_table.data_ptr(), new_block_table.data_ptr(), table[1],
+         seq_lens.data_ptr(), table[0], k_pool.data_ptr(), v_pool.data_ptr(), dtype_code(k_pool), num_pages, h_kv,
+         page_tokens, d, _p(k_scales), _p(v_scales), block, moves.data_ptr(), moves.shape[0], counts.data_ptr(),
+         workspace.data_ptr(), workspace.nbytes, _p(status))
     return new_block_table, moves, counts
