@@ -81,6 +81,7 @@ struct ForkParams {
   int32_t* fresh;       // [n_fork] free pages in ascending order
   int32_t* row_keep;    // [batch, max_pages] rows that are both read and overwritten, as they were
   int max_pages, batch, n_fork, num_pages, page_tokens;
+  bool copies;          // the moves are copied by the kernel launched next
 };
 
 struct CompactParams {

@@ -9,6 +9,8 @@
 // The copies bound these calls: 2 bytes of traffic a byte moved. A warp moves 4 KB of one (page, KV head,
 // K or V) at a time, every lane with eight 16-byte loads in flight, so small pages and partly filled ones
 // spread over the SMs as whole ones do; only the positions a page holds are copied.
+#include <atomic>
+
 #include "nbx_device.cuh"
 #include "nbx_internal.h"
 
@@ -19,6 +21,12 @@ constexpr int kChunk = 4096;          // bytes a warp copies at a time
 constexpr int kCopyThreads = 256;
 constexpr int kPlanThreads = 1024;    // single-CTA steps
 constexpr int kScanPages = 2048;      // pages per CTA of the compaction's scan
+// Up to these sizes one CTA does all the bookkeeping of a call: it reads 64 Ki table entries in about 8 us,
+// where the launches of the steps of their own cost about 10 (and each costs the host 2 us).
+constexpr int64_t kSmallTable = 65536;        // entries of the block table
+constexpr int kForkSmallPages = 262144;       // pages: a bitmap of 32 KB
+constexpr int64_t kForkSmallWork = 1 << 20;   // rows x forks compared
+constexpr int kCompactSmallPages = 24576;     // pages: fill counts of 96 KB
 
 int64_t up256(int64_t x) { return (x + 255) & ~static_cast<int64_t>(255); }
 
@@ -110,16 +118,16 @@ __device__ __forceinline__ int block_scan(int v, int* s, int* total) {
 }
 
 // ------------------------------------------------------------------------------------ fork
+// Three steps, each over a group of threads (`id` of `n`): the whole grid of a kernel of its own for a large
+// table, or the one CTA that does all three in turn for a small one (a launch less saves more than the SMs
+// would: 64 forks in 72 rows of 250 pages took 14.5 us on the GPU as memset and four launches).
+//
 // Step 1, one warp per row: which fork overwrites the row (the first in order that names it), which
 // fork is the first to read it, and, for a row whose pages stay (not overwritten, or read), its pages
 // marked in the bitmap. A row that is both read and overwritten is kept aside, as are the lengths, so
 // that step 3 writes rows in any order.
-__global__ void __launch_bounds__(256) fork_mark_kernel(ForkParams p) {
-  pdl_wait();
-  pdl_launch_dependents();
+__device__ __forceinline__ void fork_mark(const ForkParams& p, uint32_t* bitmap, int warp, int n_warps) {
   const int lane = threadIdx.x & 31;
-  const int warp = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
-  const int n_warps = static_cast<int>((gridDim.x * blockDim.x) >> 5);
   for (int row = warp; row < p.batch; row += n_warps) {
     int writer = p.n_fork, reader = p.n_fork;
     for (int i = lane; i < p.n_fork; i += 32) {
@@ -133,16 +141,15 @@ __global__ void __launch_bounds__(256) fork_mark_kernel(ForkParams p) {
       reader = min(reader, __shfl_xor_sync(0xffffffffu, reader, o));
     }
     const bool over = writer < p.n_fork, read = reader < p.n_fork;
-    if (lane == 0) {
-      p.row_info[row] = make_int4(writer, reader, p.seq_lens[row], 0);
-    }
+    if (lane == 0) p.row_info[row] = make_int4(writer, reader, p.seq_lens[row], 0);
     if (over && !read) continue;
     const int32_t* const bt = p.block_table + static_cast<int64_t>(row) * p.max_pages;
     int32_t* const keep = p.row_keep + static_cast<int64_t>(row) * p.max_pages;
+#pragma unroll 4
     for (int j = lane; j < p.max_pages; j += 32) {
       const int pg = bt[j];
       if (over) keep[j] = pg;
-      if (pg >= 0 && pg < p.num_pages) atomicOr(p.bitmap + (pg >> 5), 1u << (pg & 31));
+      if (pg >= 0 && pg < p.num_pages) atomicOr(bitmap + (pg >> 5), 1u << (pg & 31));
       else if (pg >= p.num_pages) raise_status(p.status, NBX_DEV_BAD_PAGE);
     }
   }
@@ -150,11 +157,8 @@ __global__ void __launch_bounds__(256) fork_mark_kernel(ForkParams p) {
 
 // Step 2, one CTA: every fork's outcome, the fresh pages (the lowest free ids, in order of the forks)
 // and the list of moves.
-__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
+__device__ __forceinline__ void fork_plan(const ForkParams& p, const uint32_t* bitmap) {
   __shared__ int s_scan[33];
-  __shared__ int s_free;
-  pdl_wait();
-  pdl_launch_dependents();
   const int tid = threadIdx.x;
   // ---- forks that need a fresh page, ranked in order
   int base = 0;
@@ -202,7 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
     const int w = w0 + tid;
     uint32_t free_bits = 0;
     if (w < words) {
-      free_bits = ~__ldcg(p.bitmap + w);
+      free_bits = ~bitmap[w];
       if (w == words - 1 && (p.num_pages & 31)) free_bits &= (1u << (p.num_pages & 31)) - 1u;
     }
     int total;
@@ -213,9 +217,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
       free_bits &= free_bits - 1;
     }
   }
-  if (tid == 0) s_free = min(found, n_need);
-  __syncthreads();   // also orders the writes of fresh and outcome before the reads below (same CTA)
-  const int n_copy = s_free;
+  const int n_copy = min(found, n_need);   // the same in every thread
+  __syncthreads();   // orders the writes of fresh and outcome before the reads below (same CTA)
   for (int i = tid; i < p.n_fork; i += kPlanThreads) {
     int4 o = p.outcome[i];
     if (o.x != kForkCopy) continue;
@@ -233,17 +236,14 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
     }
     p.outcome[i] = o;
   }
-  for (int i = 3 * n_copy + tid; i < 3 * p.n_fork; i += kPlanThreads) p.moves[i] = -1;
+  for (int64_t i = 3 * static_cast<int64_t>(n_copy) + tid; i < 3 * static_cast<int64_t>(p.n_fork); i += kPlanThreads)
+    p.moves[i] = -1;
   if (tid == 0) *p.n_moves = n_copy;
 }
 
-// Step 3, one warp per fork: the destination's row and length. (It lets no dependent start early: the
-// plan of a decode launched next reads the lengths before it waits for the grid ahead of it.)
-__global__ void __launch_bounds__(256) fork_rows_kernel(ForkParams p) {
-  pdl_wait();
+// Step 3, one warp per fork: the destination's row and length.
+__device__ __forceinline__ void fork_rows(const ForkParams& p, int warp, int n_warps) {
   const int lane = threadIdx.x & 31;
-  const int warp = static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
-  const int n_warps = static_cast<int>((gridDim.x * blockDim.x) >> 5);
   for (int i = warp; i < p.n_fork; i += n_warps) {
     const int4 o = p.outcome[i];
     if (o.x == kForkNone) continue;
@@ -253,13 +253,61 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(ForkParams p) {
     int32_t* const to = p.block_table + static_cast<int64_t>(d) * p.max_pages;
     const int len = o.x == kForkEmpty ? 0 : o.z;
     const int pages = (len + p.page_tokens - 1) / p.page_tokens;   // len <= max_pages * page_tokens
+#pragma unroll 4
     for (int j = lane; j < p.max_pages; j += 32)
       to[j] = j >= pages ? -1 : (o.x == kForkCopy && j == pages - 1 ? o.w : from[j]);
     if (lane == 0) p.seq_lens[d] = len;
   }
 }
 
+// A kernel that writes the lengths lets its dependents start early only if they are the copies of the same
+// call: the plan of a decode reads the lengths before it waits for the grid ahead of it.
+__global__ void __launch_bounds__(256) fork_mark_kernel(ForkParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  fork_mark(p, p.bitmap, static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5),
+            static_cast<int>((gridDim.x * blockDim.x) >> 5));
+}
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  fork_plan(p, p.bitmap);
+}
+__global__ void __launch_bounds__(256) fork_rows_kernel(ForkParams p) {
+  pdl_wait();
+  if (p.copies) pdl_launch_dependents();
+  fork_rows(p, static_cast<int>((blockIdx.x * blockDim.x + threadIdx.x) >> 5),
+            static_cast<int>((gridDim.x * blockDim.x) >> 5));
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(ForkParams p) {
+  __shared__ uint32_t bitmap[kForkSmallPages / 32];
+  for (int w = threadIdx.x; w < (p.num_pages + 31) / 32; w += kPlanThreads) bitmap[w] = 0u;
+  pdl_wait();
+  if (p.copies) pdl_launch_dependents();
+  __syncthreads();
+  fork_mark(p, bitmap, threadIdx.x >> 5, kPlanThreads / 32);
+  __syncthreads();   // the bitmap, and row_info and row_keep in global memory (same CTA)
+  fork_plan(p, bitmap);
+  __syncthreads();   // outcome
+  fork_rows(p, threadIdx.x >> 5, kPlanThreads / 32);
+}
+
 // ------------------------------------------------------------------------------------ compaction
+// Positions row `row` holds of its page number j, or -1 if the entry names no page of the pool.
+__device__ __forceinline__ int compact_fill(const CompactParams& p, int row, int j, int pg) {
+  if (pg < 0) return -1;
+  if (pg >= p.num_pages) {
+    raise_status(p.status, NBX_DEV_BAD_PAGE);
+    return -1;
+  }
+  const int64_t len = p.seq_lens[row];
+  if (j == 0 && (len < 0 || len > static_cast<int64_t>(p.max_pages) * p.page_tokens))
+    raise_status(p.status, NBX_DEV_BAD_LEN);
+  const int64_t left = len - static_cast<int64_t>(j) * p.page_tokens;
+  return left <= 0 ? 0 : (left >= p.page_tokens ? p.page_tokens : static_cast<int>(left));
+}
+
 // fill[page] = 1 + the most positions a row holds of the page, 0 for a free page.
 __global__ void __launch_bounds__(256) compact_mark_kernel(CompactParams p) {
   pdl_wait();
@@ -273,17 +321,8 @@ __global__ void __launch_bounds__(256) compact_mark_kernel(CompactParams p) {
     const int j = static_cast<int>(it - static_cast<int64_t>(row) * per_row) * 32 + lane;
     if (j >= p.max_pages) continue;
     const int pg = p.block_table[static_cast<int64_t>(row) * p.max_pages + j];
-    if (pg < 0) continue;
-    if (pg >= p.num_pages) {
-      raise_status(p.status, NBX_DEV_BAD_PAGE);
-      continue;
-    }
-    const int64_t len = p.seq_lens[row];
-    if (j == 0 && (len < 0 || len > static_cast<int64_t>(p.max_pages) * p.page_tokens))
-      raise_status(p.status, NBX_DEV_BAD_LEN);
-    const int64_t left = len - static_cast<int64_t>(j) * p.page_tokens;
-    const int cnt = left <= 0 ? 0 : (left >= p.page_tokens ? p.page_tokens : static_cast<int>(left));
-    atomicMax(p.fill + pg, 1 + cnt);
+    const int cnt = compact_fill(p, row, j, pg);
+    if (cnt >= 0) atomicMax(p.fill + pg, 1 + cnt);
   }
 }
 
@@ -359,6 +398,62 @@ __global__ void __launch_bounds__(256) compact_rank_kernel(CompactParams p) {
   if (blockIdx.x == 0 && tid == 0) {
     p.counts[0] = n_moves;
     p.counts[1] = n_live;
+  }
+}
+
+// All of it in one CTA, for a small table and pool: fill lives in shared memory, and holds -1 - (new id) for
+// the pages that move once their moves are known.
+__global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(CompactParams p) {
+  extern __shared__ int fill[];   // [num_pages]
+  __shared__ int s_scan[33];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < p.num_pages; i += kPlanThreads) fill[i] = 0;
+  pdl_wait();
+  pdl_launch_dependents();   // (this kernel writes no lengths)
+  __syncthreads();
+  const int n = p.batch * p.max_pages;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int row = i / p.max_pages;
+    const int cnt = compact_fill(p, row, i - row * p.max_pages, p.block_table[i]);
+    if (cnt >= 0) atomicMax(fill + p.block_table[i], 1 + cnt);
+  }
+  __syncthreads();
+  // each thread takes a run of pages; ranks as in compact_rank_kernel
+  const int per = (p.num_pages + kPlanThreads - 1) / kPlanThreads;
+  const int lo = min(p.num_pages, tid * per), hi = min(p.num_pages, lo + per);
+  int mine = 0;
+  for (int i = lo; i < hi; ++i) mine += fill[i] != 0;
+  int n_live, below;
+  int live = block_scan(mine, s_scan, &n_live);
+  int low = 0;
+  for (int i = lo; i < min(hi, n_live); ++i) low += fill[i] != 0;
+  block_scan(low, s_scan, &below);
+  for (int pg = lo; pg < hi; ++pg) {
+    const int f = fill[pg];
+    if (f != 0) {
+      if (pg >= n_live) {
+        p.moves[3 * (live - below)] = pg;
+        p.moves[3 * (live - below) + 2] = f - 1;
+      }
+      ++live;
+    } else if (pg < n_live) {
+      p.moves[3 * (pg - live) + 1] = pg;
+    }
+  }
+  const int n_moves = n_live - below;
+  for (int i = 3 * n_moves + tid; i < 3 * p.max_moves; i += kPlanThreads) p.moves[i] = -1;
+  if (tid == 0) {
+    p.counts[0] = n_moves;
+    p.counts[1] = n_live;
+  }
+  __syncthreads();   // the moves (same CTA)
+  for (int k = tid; k < n_moves; k += kPlanThreads) fill[p.moves[3 * k]] = -1 - p.moves[3 * k + 1];
+  __syncthreads();
+#pragma unroll 4
+  for (int i = tid; i < n; i += kPlanThreads) {
+    const int pg = p.block_table[i];
+    p.new_block_table[i] = pg >= n_live && pg < p.num_pages ? -1 - fill[pg] : pg;
   }
 }
 
@@ -464,6 +559,16 @@ CompactLayout compact_layout(int64_t num_pages) {
   w.total = off;
   return w;
 }
+// Raises compact_small_kernel's shared-memory limit, once per device.
+cudaError_t compact_small_smem() {
+  static std::atomic<uint64_t> configured{0};
+  const uint64_t bit = 1ull << (device_info().device & 63);
+  if (configured.load() & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(compact_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCompactSmallPages * 4);
+  if (e == cudaSuccess) configured.fetch_or(bit);
+  return e;
+}
 bool table_ok(int batch, int max_pages) {
   return batch >= 0 && max_pages >= 1 && static_cast<int64_t>(batch) * max_pages <= 0x7fffffffll;
 }
@@ -530,7 +635,15 @@ NBX_API int nbx_paged_kv_fork(int32_t* block_table, int max_pages, int32_t* seq_
   p.n_fork = n_fork;
   p.num_pages = num_pages;
   p.page_tokens = page_tokens;
-  cudaError_t e = cudaMemsetAsync(p.bitmap, 0, static_cast<size_t>(w.row_info - w.bitmap), st);
+  p.copies = copies;
+  cudaError_t e;
+  if (static_cast<int64_t>(batch) * max_pages <= kSmallTable && num_pages <= kForkSmallPages &&
+      static_cast<int64_t>(batch) * n_fork <= kForkSmallWork) {
+    e = launch_pdl(fork_small_kernel, 1u, kPlanThreads, 0, st, p);
+    if (e == cudaSuccess && copies) e = launch_copy(copy_params(a, moves, n_moves, n_fork, status), st);
+    return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
+  }
+  e = cudaMemsetAsync(p.bitmap, 0, static_cast<size_t>(w.row_info - w.bitmap), st);
   if (e == cudaSuccess) e = launch_pdl(fork_mark_kernel, grid_for(static_cast<int64_t>(batch) * 32, 256), 256u, 0, st, p);
   if (e == cudaSuccess) e = launch_pdl(fork_plan_kernel, 1u, kPlanThreads, 0, st, p);
   if (e == cudaSuccess) e = launch_pdl(fork_rows_kernel, grid_for(static_cast<int64_t>(n_fork) * 32, 256), 256u, 0, st, p);
@@ -580,7 +693,16 @@ NBX_API int nbx_paged_kv_compact(const int32_t* block_table, int32_t* new_block_
   p.n_chunks = w.n_chunks;
   const unsigned chunks = static_cast<unsigned>(w.n_chunks);
   const int64_t entries = static_cast<int64_t>(batch) * max_pages;
-  cudaError_t e = cudaMemsetAsync(p.fill, 0, static_cast<size_t>(num_pages) * 4, st);
+  cudaError_t e;
+  if (entries <= kSmallTable && num_pages <= kCompactSmallPages) {
+    e = compact_small_smem();
+    if (e == cudaSuccess)
+      e = launch_pdl(compact_small_kernel, 1u, kPlanThreads, static_cast<size_t>(num_pages) * 4, st, p);
+    if (e == cudaSuccess && copies && max_moves > 0)
+      e = launch_copy(copy_params(a, moves, counts, max_moves, status), st);
+    return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
+  }
+  e = cudaMemsetAsync(p.fill, 0, static_cast<size_t>(num_pages) * 4, st);
   if (e == cudaSuccess)
     e = launch_pdl(compact_mark_kernel, grid_for(static_cast<int64_t>(batch) * ((max_pages + 31) / 32) * 32, 256), 256u, 0,
                    st, p);

@@ -191,7 +191,7 @@ def test_compact(kind, h, P, d, T, in_place):
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(x, ref))
 
 
-@pytest.mark.parametrize("num_pages", [1, 2, 2047, 2048, 2049, 10000])
+@pytest.mark.parametrize("num_pages", [1, 2, 2047, 2048, 2049, 10000, 24576, 24577, 30000, 70000])
 def test_compact_over_the_scan_chunks(num_pages):
     g = np.random.default_rng(num_pages)
     for share in (0.0, 0.5, 1.0):
@@ -207,6 +207,55 @@ def test_compact_over_the_scan_chunks(num_pages):
         assert counts.tolist() == [len(want_m), live]
         assert np.array_equal(new.cpu().numpy(), want_t)
         assert all(torch.equal(a, b) for a, b in zip(x, ref))
+
+
+def test_compact_a_long_table_of_a_small_pool():
+    # more entries than the one-CTA form takes, most of them empty
+    g = np.random.default_rng(22)
+    table = np.full((900, 80), -1, dtype=np.int32)
+    lens = g.integers(0, 80 * 16, 900)
+    for i, p in enumerate(g.permutation(3000)[:1500]):
+        table[i % 900, i // 900] = p
+    x = pools(3000, 1, 16, 16, "bf16", 23)
+    want_t, want_m, live = oc.compact(table, lens, 16, 3000)
+    ref = moved(x, want_m)
+    new, moves, counts = nbx.nbx_paged_kv_compact(dev(table), dev(lens), *x)
+    torch.cuda.synchronize()
+    assert counts.tolist() == [len(want_m), live] and np.array_equal(new.cpu().numpy(), want_t)
+    assert all(torch.equal(a, b) for a, b in zip(x, ref))
+
+
+def test_fork_then_decode_reads_the_new_lengths():
+    # the decode's plan starts while the fork may still run: it has to see the lengths the fork writes, with
+    # copies behind them and without (a table-only fork), on both forms of the bookkeeping
+    for B in (8, 1200):
+        P, d = 16, 64
+        lens = [33] * (B // 2) + [0] * (B // 2)
+        table, n = table_for(lens, P, 60, 24, spread=2.0)
+        k, v = pools(n, 1, P, d, "bf16", 24)
+        q = torch.randn((B, 1, 2, d), device=DEV).to(torch.bfloat16)
+        q[B // 2:] = q[: B // 2]
+        src, dst = dev(np.arange(B // 2)), dev(np.arange(B // 2) + B // 2)
+        ws = torch.empty(nbx.nbx_paged_kv_fork_workspace_bytes(B, 60, B // 2, n), dtype=torch.uint8, device=DEV)
+        need = nbx.nbx_paged_decode_workspace_bytes(B, 1, 2, 1, d, 64)
+        dws = torch.empty(need, dtype=torch.uint8, device=DEV)
+        moves = torch.empty((B // 2, 3), dtype=torch.int32, device=DEV)
+        count = torch.empty(1, dtype=torch.int32, device=DEV)
+        for _ in range(5):
+            t, ln = dev(table), dev(lens)
+            torch.cuda.synchronize()
+            nbx.nbx_paged_kv_fork(t, ln, src, dst, k, v, moves=moves, n_moves=count, workspace=ws)
+            out = nbx.nbx_paged_decode_attn(q, k, v, t, ln, 64, 0.125, workspace=dws)
+            torch.cuda.synchronize()
+            assert torch.equal(out[: B // 2], out[B // 2:])
+            t, ln = dev(table), dev(lens)
+            args = [t.data_ptr(), 60, ln.data_ptr(), B, src.data_ptr(), dst.data_ptr(), B // 2, None, None, 1, n, 1, P, d,
+                    None, None, 0, moves.data_ptr(), count.data_ptr(), ws.data_ptr(), ws.numel(), None]
+            torch.cuda.synchronize()
+            assert nbx.lib().nbx_paged_kv_fork(*args, torch.cuda.current_stream().cuda_stream) == 0
+            shared = nbx.nbx_paged_decode_attn(q, k, v, t, ln, 32, 0.125, workspace=dws)   # full pages alone: len > 32 is
+            torch.cuda.synchronize()                                                       # out of bounds, read as empty
+            assert ln.tolist() == [33] * B and bool((shared == 0).all())
 
 
 def test_compact_keeps_entries_outside_the_pool():
