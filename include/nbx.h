@@ -343,9 +343,10 @@ NBX_API size_t nbx_paged_decode_modified_workspace_bytes(int batch, int rows, in
 
 /*
  * nbx_paged_decode_modified_partial_kernel -- which split-partial kernel these two calls run (block-scaled
- * pools: pool_dtype NBX_E4M3). Host-only. As nbx_paged_decode_partial_kernel, but an fp8 window with an fp32
- * output runs NBX_PARTIAL_SIMT: on tensor cores an fp8 window's weights are held to 2^-9, which suits a bf16
- * output. A bf16 window's are held to 2^-17.
+ * pools: pool_dtype NBX_E4M3). Host-only. A window that nbx_paged_decode_partial_kernel gives to the tensor
+ * cores runs there, but an fp8 one only with a bf16 output (its weights are held to 2^-9, a bf16 window's to
+ * 2^-17). Other E4M3 pools, and bf16 pools under bf16 queries, run NBX_PARTIAL_WARP, the rest
+ * NBX_PARTIAL_SIMT; both are as exact as fp32 sums.
  */
 NBX_API int nbx_paged_decode_modified_partial_kernel(int q_dtype, int pool_dtype, int out_dtype, int rows, int h_q,
                                                      int h_kv, int d, int num_pages, int page_tokens);
@@ -468,8 +469,9 @@ NBX_API int nbx_paged_decode_attn_noalloc(const void* q, int q_dtype, int batch,
 typedef enum {
     NBX_PARTIAL_SIMT = 0,            /* CUDA cores: work units of 4 query vectors, any supported shape */
     NBX_PARTIAL_TCGEN05 = 1,         /* tensor cores (tcgen05.mma): work units of 128 query vectors */
-    NBX_PARTIAL_TCGEN05_FP8 = 2      /* fp8 (E4M3) pool: the tensor-core kernel on the codes as stored
+    NBX_PARTIAL_TCGEN05_FP8 = 2,     /* fp8 (E4M3) pool: the tensor-core kernel on the codes as stored
                                         (tcgen05.mma kind::f8f6f4), Q and P as two E4M3 terms each */
+    NBX_PARTIAL_WARP = 3             /* modified decodes: work units of 8 query vectors, one warp each, on mma.sync */
 } nbx_partial_kernel;
 
 /*

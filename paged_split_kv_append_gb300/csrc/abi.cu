@@ -137,7 +137,8 @@ NBX_API int nbx_paged_decode_modified_partial_kernel(int q_dtype, int pool_dtype
   const int k = nbx_paged_decode_partial_kernel(q_dtype, pool_dtype, rows, h_q, h_kv, d, num_pages, page_tokens);
   if (k < 0) return k;
   if (out_dtype != NBX_F32 && out_dtype != NBX_BF16) return NBX_ERR_DTYPE;
-  return k == NBX_PARTIAL_TCGEN05_FP8 && out_dtype == NBX_F32 ? NBX_PARTIAL_SIMT : k;
+  if (k == NBX_PARTIAL_TCGEN05 || (k == NBX_PARTIAL_TCGEN05_FP8 && out_dtype == NBX_BF16)) return k;
+  return warp_path_applies(q_dtype, pool_dtype) ? NBX_PARTIAL_WARP : NBX_PARTIAL_SIMT;
 }
 
 NBX_API size_t nbx_paged_decode_workspace_bytes(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len) {
@@ -201,8 +202,8 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return NBX_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return NBX_ERR_ALIGN;
   WorkspaceLayout w;
-  if (!workspace_layout(batch, rows, h_q, h_kv, d, max_seq_len, &w)) return NBX_ERR_SHAPE;
-  if (workspace_bytes < (mod ? w.total_mod : w.total)) return NBX_ERR_WORKSPACE;
+  if (!workspace_layout(batch, rows, h_q, h_kv, d, max_seq_len, &w, mod != nullptr)) return NBX_ERR_SHAPE;
+  if (workspace_bytes < w.total) return NBX_ERR_WORKSPACE;
 
   char* ws = static_cast<char*>(workspace);
   DecodeParams p = {};
@@ -281,8 +282,8 @@ NBX_API size_t nbx_paged_decode_modified_workspace_bytes(int batch, int rows, in
                                                          int max_seq_len) {
   if (!decode_shape_ok(batch, rows, h_q, h_kv, d, max_seq_len)) return 0;
   WorkspaceLayout w;
-  if (!workspace_layout(batch, rows, h_q, h_kv, d, max_seq_len, &w)) return 0;
-  return w.total_mod;
+  if (!workspace_layout(batch, rows, h_q, h_kv, d, max_seq_len, &w, true)) return 0;
+  return w.total;
 }
 
 NBX_API int nbx_paged_decode_attn_modified(const void* q, int q_dtype, int batch, int rows, int h_q, int d,

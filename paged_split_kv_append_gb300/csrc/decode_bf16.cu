@@ -2,5 +2,5 @@
 #include "decode_kernels.cuh"
 
 namespace nbx {
-NBX_DECODE_FOR_POOL(BF16, BF16, 0)
+NBX_DECODE_FOR_POOL(BF16)
 }  // namespace nbx

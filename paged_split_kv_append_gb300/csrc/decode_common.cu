@@ -30,9 +30,11 @@ int splits_for(int length) {
   return s < 1 ? 1 : (s > NBX_MAX_SPLITS ? NBX_MAX_SPLITS : s);
 }
 
-bool workspace_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len, WorkspaceLayout* w) {
+bool workspace_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len, WorkspaceLayout* w,
+                      bool modified) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  const size_t S = static_cast<size_t>(splits_for(max_seq_len));
+  // 64-position splits of the modified decodes: a quarter of the pages' 256
+  const size_t S = static_cast<size_t>(splits_for(modified && max_seq_len < (1 << 28) ? 4 * max_seq_len : max_seq_len));
   const size_t rb = (static_cast<size_t>(rows) * (h_q / h_kv) + kQB - 1) / kQB;
   const size_t prow = static_cast<size_t>(batch) * rows * h_q * S;   // partial rows
   if (prow > (static_cast<size_t>(1) << 40) / static_cast<size_t>(d)) return false;
@@ -51,10 +53,10 @@ bool workspace_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq
   off += up(prow * 4);
   w->acc_part = off;
   off += up(prow * static_cast<size_t>(d) * 4);
-  w->total = off;
   w->ranges = off;
   const size_t m_tiles = (static_cast<size_t>(rows) * (h_q / h_kv) + kMmaRowsPerTile - 1) / kMmaRowsPerTile;
-  w->total_mod = off + up(static_cast<size_t>(batch) * m_tiles * sizeof(int2));
+  if (modified) off += up(static_cast<size_t>(batch) * m_tiles * sizeof(int2));
+  w->total = off;
   w->max_splits = static_cast<int>(S);
   w->row_blocks = static_cast<int>(rb);
   return true;
@@ -76,6 +78,7 @@ __device__ __forceinline__ void plan_finish(const DecodeParams& p) {
 // keep their own order and take a slower serial path.
 // TC: a tensor-core window, whose splits are sized by the call's total work (DecodeParams::tc_units);
 // otherwise splits of kSimtSplitPositions. Two instantiations keep each rule's code free of the other.
+// (TC is also the rule of a modified decode's one-warp kernel.)
 // X: a modified decode. With key ranges a sequence's splits cut only the positions from the first key that
 // some row sees (down to a split boundary's alignment) to the last one, and a tensor-core window gets the
 // range of every M tile; the ranges come from the caller's kernels, so that plan waits before it reads.
@@ -117,8 +120,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
         const int mt = static_cast<int>(it - static_cast<int64_t>(b) * p.range_tiles);
         const int L = p.seq_lens[b];
         const bool fit = L >= 0 && L <= p.max_seq_len && static_cast<int64_t>(L) <= cap;
-        const int r0 = TC ? mt * kMmaRowsPerTile / p.group : 0;
-        const int r1 = TC ? min(p.rows, ((mt + 1) * kMmaRowsPerTile + p.group - 1) / p.group) : p.rows;
+        const int r0 = mt * kMmaRowsPerTile / p.group;
+        const int r1 = p.range_tiles == 1 ? p.rows : min(p.rows, ((mt + 1) * kMmaRowsPerTile + p.group - 1) / p.group);
         int lo = INT_MAX, hi = 0;
         for (int r = r0 + lane; r < r1; r += 32) {
           const KeyRange kr = key_range(p, b, r, fit ? L : 0);
@@ -735,20 +738,24 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
     q.range_tiles = (p.rows * p.group + kMmaRowsPerTile - 1) / kMmaRowsPerTile;
     q.tc_pairs = p.h_kv * q.range_tiles;
   }
+  const bool warps = x && !mma && warp_path_applies(q_dtype, pool_dtype);
+  if (warps) {   // one unit a resident warp over the GPU
+    q.tc_units = device_info().sm_count * warp_path_warps(q_dtype, pool_dtype, p.d);
+    q.tc_pairs = p.h_kv * ((p.rows * p.group + kWarpUnitVectors - 1) / kWarpUnitVectors);
+  }
   cudaError_t e = x ? launch_plan<true>(q, stream) : launch_plan<false>(q, stream);
   if (e != cudaSuccess) return e;
   if (mma && (x & kBlockScaled)) e = decode_dispatch_mma_block(q, (x & kScoreMod) != 0, grid_limit, stream);
   else if (mma)
     e = x ? decode_dispatch_mma_mod(q, pool_dtype, grid_limit, stream) : decode_dispatch_mma(q, pool_dtype, grid_limit, stream);
-  else if (x & kBlockScaled)
-    e = x & kScoreMod ? decode_dispatch_E4M3_block_mod(q, q_dtype, grid_limit, stream)
-                      : decode_dispatch_E4M3_block(q, q_dtype, grid_limit, stream);
-  else if (pool_dtype == NBX_F32)
-    e = x ? decode_dispatch_F32_mod(q, q_dtype, grid_limit, stream) : decode_dispatch_F32(q, q_dtype, grid_limit, stream);
-  else if (pool_dtype == NBX_BF16)
-    e = x ? decode_dispatch_BF16_mod(q, q_dtype, grid_limit, stream) : decode_dispatch_BF16(q, q_dtype, grid_limit, stream);
-  else
-    e = x ? decode_dispatch_E4M3_mod(q, q_dtype, grid_limit, stream) : decode_dispatch_E4M3(q, q_dtype, grid_limit, stream);
+  else if (warps && (x & kBlockScaled)) e = decode_dispatch_warp_block(q, q_dtype, (x & kScoreMod) != 0, grid_limit, stream);
+  else if (warps)
+    e = pool_dtype == NBX_E4M3 ? decode_dispatch_warp_e4m3(q, q_dtype, grid_limit, stream)
+                               : decode_dispatch_warp_bf16(q, grid_limit, stream);
+  else if (x) e = decode_dispatch_simt_mod(q, q_dtype, pool_dtype, grid_limit, stream);
+  else if (pool_dtype == NBX_F32) e = decode_dispatch_F32(q, q_dtype, grid_limit, stream);
+  else if (pool_dtype == NBX_BF16) e = decode_dispatch_BF16(q, q_dtype, grid_limit, stream);
+  else e = decode_dispatch_E4M3(q, q_dtype, grid_limit, stream);
   if (e != cudaSuccess) return e;
   // every sequence has one split: the partials are the output (but for rows a modified window marked)
   if (q.max_splits <= 1 && !(x && mma)) return cudaSuccess;

@@ -2,5 +2,5 @@
 #include "decode_kernels.cuh"
 
 namespace nbx {
-NBX_DECODE_FOR_POOL(E4M3, E4M3, 0)
+NBX_DECODE_FOR_POOL(E4M3)
 }  // namespace nbx

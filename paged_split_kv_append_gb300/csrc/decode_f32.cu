@@ -2,5 +2,5 @@
 #include "decode_kernels.cuh"
 
 namespace nbx {
-NBX_DECODE_FOR_POOL(F32, F32, 0)
+NBX_DECODE_FOR_POOL(F32)
 }  // namespace nbx

@@ -70,7 +70,6 @@ struct UnitMetaMod : UnitMeta {
 template <class PT, class QT, int D, int X = 0>
 struct DecodeCfg {
   using Meta = std::conditional_t<(X & kScoreMod) != 0, UnitMetaMod, UnitMeta>;
-  static constexpr bool kBlk = (X & kBlockScaled) != 0;
   static constexpr int kLPT = D / 16;                  // lanes per position in the score layout
   static constexpr int kTPG = kLPT >= 8 ? 2 : 1;       // positions each lane group scores per pass
   static constexpr int kTG = 32 / kLPT;                // lane groups per warp
@@ -94,7 +93,7 @@ struct DecodeCfg {
   // copies: the copy engine's fixed cost per bulk request would cap the stream below HBM speed
   static constexpr bool kWarpCopy = kTileBytes <= 4096;
   static constexpr int kFixed = 2 * kQBytes + (kRedInStage ? 0 : 2 * kRedFloats * 4) + kPBufBytes +
-                                2 * (int)sizeof(Meta) + (kBlk ? 8 * 16 : 0) + 2048;
+                                2 * (int)sizeof(Meta) + 2048;
   // resident CTAs per SM: 3 (2 at head dim 256, where the registers allow no more), fewer when
   // shared memory cannot hold two stages for each of them
   static constexpr int kBlocksBySmem = kSmemPerSm / (kFixed + 2 * kStageBytes + 1024);
@@ -106,7 +105,6 @@ struct DecodeCfg {
   static_assert(kWarpTok % kPassTok == 0, "a warp's share of a stage holds whole passes");
   static_assert(!kRedInStage || kWarpTok * D * PT::kBytes >= 2 * kQB * 4, "a warp's V rows hold its m and l");
   static_assert(kLPT >= 4 && kLPT <= 16, "head dim 64..256");
-  static_assert(!kBlk || (PT::kCode == NBX_E4M3 && kWarpCopy), "block scales ride with the lanes' copies of E4M3 tiles");
 };
 
 template <class C>
@@ -123,7 +121,6 @@ struct SmemLayout {
   uint64_t* qfull;   // [2]
   uint64_t* qempty;  // [2]
   uint64_t* cbar;    // consumer-warp barrier
-  float* scales;     // [stages][4] block scales of a stage: K of its two tiles, then V (kBlockScaled)
 };
 
 template <class C>
@@ -131,8 +128,7 @@ struct Carver {
   static constexpr int r(int b) { return ((b + 127) / 128) * 128; }
   static constexpr int bytes() {
     return r(C::kStages * C::kStageBytes) + r(2 * C::kQBytes) + r(C::kRedInStage ? 0 : 2 * C::kRedFloats * 4) + r(C::kPBufBytes) +
-           r(2 * (int)sizeof(typename C::Meta)) + r(C::kStages * 4) + r(16) + 2 * r(C::kStages * 8) + 2 * r(16) + r(8) +
-           (C::kBlk ? r(C::kStages * 16) : 0);
+           r(2 * (int)sizeof(typename C::Meta)) + r(C::kStages * 4) + r(16) + 2 * r(C::kStages * 8) + 2 * r(16) + r(8);
   }
   __device__ static SmemLayout<C> carve(char* base) {
     SmemLayout<C> s;
@@ -154,7 +150,6 @@ struct Carver {
     s.qfull = reinterpret_cast<uint64_t*>(take(16));
     s.qempty = reinterpret_cast<uint64_t*>(take(16));
     s.cbar = reinterpret_cast<uint64_t*>(take(8));
-    s.scales = C::kBlk ? reinterpret_cast<float*>(take(C::kStages * 16)) : nullptr;
     return s;
   }
 };
@@ -243,10 +238,8 @@ __device__ __forceinline__ void pv_step_masked(uint32_t pb, uint32_t va, f32x2 (
 }
 
 // ------------------------------------------------------------------------------------ partial
-// X: what the call adds to the plain decode (kScoreMod, kBlockScaled bits). The additions, per score:
-//  * block scales: s_j is multiplied by its K block's scale, and the weight that enters P*V by its V
-//    block's (l keeps the weight itself). The producer's lanes 0-3 copy a stage's four scales with its
-//    tiles, 16 bytes beside 2 to 8 KB. A block whose scale is not in [2^-48, 2^48] counts as a missing tile.
+// X: what the call adds to the plain decode (0 or kScoreMod; block-scaled pools have kernels of their own).
+// The additions, per score:
 //  * cap: z = cap tanh(s / cap), one tanhf per lane and pass (each lane holds one score), in the shadow of
 //    the 64 to 256 packed FMAs of the pass. The hardware's tanh.approx is off by 2^-11, too much for a
 //    logit of tens.
@@ -487,13 +480,6 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D, X>::kMinB
               cp_async16(dst + hf * C::kTileBytes + c * 16, ks + c * 16);
               cp_async16(dst + C::kHalfBytes + hf * C::kTileBytes + c * 16, vs + c * 16);
             }
-            if constexpr (C::kBlk) {   // lanes 0 and 1: the tile's K and V scale
-              if (lane < 2) {
-                const int64_t blk = (static_cast<int64_t>(pages[hf]) * p.h_kv + h) * (P / p.scale_tokens) +
-                                    pofs[hf] / p.scale_tokens;
-                cp_async4(smem_u32(sm.scales + stage * 4 + lane * 2 + hf), (lane ? p.v_scales : p.k_scales) + blk);
-              }
-            }
           }
           cp_async_arrive_noinc(&sm.full[stage]);
         }
@@ -595,21 +581,7 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D, X>::kMinB
         ok = false;
         break;
       }
-      int okbits = sm.stage_ok[stage];
-      float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};   // kBlk: scales of the stage's two tiles
-      if constexpr (C::kBlk) {
-        const uint4 w = lds128(smem_u32(sm.scales + stage * 4));
-        ks[0] = __uint_as_float(w.x), ks[1] = __uint_as_float(w.y);
-        vs[0] = __uint_as_float(w.z), vs[1] = __uint_as_float(w.w);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const bool fit = ks[hf] >= kMinScale && ks[hf] <= kMaxScale && vs[hf] >= kMinScale && vs[hf] <= kMaxScale;
-          if (((okbits >> hf) & 1) && !fit) {
-            okbits &= ~(1 << hf);
-            if (lane == 0) raise_status(p.status, NBX_DEV_BAD_SCALE);
-          }
-        }
-      }
+      const int okbits = sm.stage_ok[stage];
       if (okbits) {
         const int n0 = u_start + t * C::kStageTok;
         // every position of the stage copied, inside the split, and seen by every vector of the unit
@@ -672,7 +644,6 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D, X>::kMinB
           const int rs = pbase + tg * TPG + tsel;   // this lane's position inside the stage
           const int n = n0 + rs;
           bool valid = ((okbits >> (rs / kTileN)) & 1) && (n < u_end) && (n <= pos_sel);
-          if constexpr (C::kBlk) mine *= rs < kTileN ? ks[0] : ks[1];
           if constexpr (kMod) {
             valid = valid && n >= lo_sel;
             if (p.cap_log2 > 0.f) mine = p.cap_log2 * tanhf(mine * p.cap_inv);
@@ -704,8 +675,7 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeCfg<PT, QT, D, X>::kMinB
           }
           const float pw = valid ? fast_exp2(s - m_run) : 0.f;
           l_run += pw;
-          const float pv = C::kBlk ? pw * (rs < kTileN ? vs[0] : vs[1]) : pw;
-          if (p_writer) sts64(p_store, pack2(pv, pv));
+          if (p_writer) sts64(p_store, pack2(pw, pw));
           __syncwarp();
           // ---- acc_i += p_i,n * v_n over this pass's positions (no per-position test in full stages)
           if (full_stage) {
@@ -872,31 +842,25 @@ cudaError_t launch_decode(const DecodeParams& p, int grid_limit, cudaStream_t st
   return launch_pdl(decode_partial_kernel<PT, QT, D, X>, static_cast<unsigned>(grid), kDecodeThreads, smem, stream, p);
 }
 
-template <class PT, int X>
-cudaError_t decode_dispatch_pool(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream) {
-  if (q_dtype == NBX_F32) {
-    if (p.d == 64) return launch_decode<PT, F32, 64, X>(p, grid_limit, stream);
-    if (p.d == 128) return launch_decode<PT, F32, 128, X>(p, grid_limit, stream);
-    return launch_decode<PT, F32, 256, X>(p, grid_limit, stream);
-  }
-  if (p.d == 64) return launch_decode<PT, BF16, 64, X>(p, grid_limit, stream);
-  if (p.d == 128) return launch_decode<PT, BF16, 128, X>(p, grid_limit, stream);
-  return launch_decode<PT, BF16, 256, X>(p, grid_limit, stream);
+template <class PT, class QT, int X>
+cudaError_t decode_dispatch_d(const DecodeParams& p, int grid_limit, cudaStream_t stream) {
+  if (p.d == 64) return launch_decode<PT, QT, 64, X>(p, grid_limit, stream);
+  if (p.d == 128) return launch_decode<PT, QT, 128, X>(p, grid_limit, stream);
+  return launch_decode<PT, QT, 256, X>(p, grid_limit, stream);
 }
 
 // One definition per translation unit, so that the instantiations compile in parallel.
-#define NBX_DECODE_FOR_POOL(NAME, PT, X)                                                                        \
-  cudaError_t decode_dispatch_##NAME(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream) { \
-    return decode_dispatch_pool<PT, X>(p, q_dtype, grid_limit, stream);                                         \
+#define NBX_DECODE_FOR_POOL(PT)                                                                               \
+  cudaError_t decode_dispatch_##PT(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream) { \
+    return q_dtype == NBX_F32 ? decode_dispatch_d<PT, F32, 0>(p, grid_limit, stream)                          \
+                              : decode_dispatch_d<PT, BF16, 0>(p, grid_limit, stream);                        \
   }
 
 cudaError_t decode_dispatch_F32(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
 cudaError_t decode_dispatch_BF16(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
 cudaError_t decode_dispatch_E4M3(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
-cudaError_t decode_dispatch_F32_mod(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
-cudaError_t decode_dispatch_BF16_mod(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
-cudaError_t decode_dispatch_E4M3_mod(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
-cudaError_t decode_dispatch_E4M3_block(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
-cudaError_t decode_dispatch_E4M3_block_mod(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
+// modified decodes that no kernel on the tensor cores takes: fp32 pools, and bf16 pools under fp32 queries
+cudaError_t decode_dispatch_simt_mod(const DecodeParams& p, int q_dtype, int pool_dtype, int grid_limit,
+                                     cudaStream_t stream);
 
 }  // namespace nbx

@@ -146,15 +146,16 @@ struct WorkspaceLayout {
   size_t m_part;    // f32[batch * rows * h_q * max_splits]   (log2 units)
   size_t l_part;    // f32[batch * rows * h_q * max_splits]
   size_t acc_part;  // f32[batch * rows * h_q * max_splits * d]
+  size_t ranges;    // int2[batch * M tiles of 128 vectors]: modified decodes only
   size_t total;
-  size_t ranges;    // int2[batch * M tiles of 128 vectors], after `total`: modified decodes only
-  size_t total_mod;
   int max_splits;
   int row_blocks;
 };
 
-// Returns false if the sizes overflow.
-bool workspace_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len, WorkspaceLayout* out);
+// Returns false if the sizes overflow. modified: for the modified decodes, whose splits may be as short as 64
+// positions (the kernels on the tensor cores size them by the whole call's work).
+bool workspace_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len, WorkspaceLayout* out,
+                      bool modified = false);
 
 int splits_for(int length);
 
@@ -202,7 +203,7 @@ struct DecodeParams {
   // <= 448, the v scale is applied by the merge), so f16 neither overflows nor loses more than
   // 2^-11 relative; each (row, split) slot holds d halves in the first half of its d floats
   int part_f16;
-  // split plan for a tensor-core window (0: the pages' rule, ceil(len / 256) splits of at most 64):
+  // split plan for a tensor-core window or the one-warp kernel (0: the pages' rule, ceil(len / 256) splits of at most 64):
   // about tc_units work units in all, each of the tc_pairs (KV head, M tile) pairs of a sequence
   // taking floor(tc_units * len / (tc_pairs * sum of lens)) splits, clamped to [1, min(max_splits,
   // len / 64)]
@@ -259,6 +260,21 @@ cudaError_t decode_dispatch_mma(const DecodeParams& p, int pool_dtype, int grid_
 bool mma_path_applies_modified(const DecodeParams& p, int q_dtype, int pool_dtype);
 cudaError_t decode_dispatch_mma_mod(const DecodeParams& p, int pool_dtype, int grid_limit, cudaStream_t stream);
 cudaError_t decode_dispatch_mma_block(const DecodeParams& p, bool mod, int grid_limit, cudaStream_t stream);
+// The one-warp partial kernel of modified decodes with few query vectors: E4M3 pools, bf16 pools under bf16
+// queries. Its work units cover kWarpUnitVectors query vectors of a KV head; warps resident on an SM for the
+// sizes of a call (what its splits are sized by).
+constexpr int kWarpUnitVectors = 8;
+inline bool warp_path_applies(int q_dtype, int pool_dtype) {
+  return pool_dtype == NBX_E4M3 || (pool_dtype == NBX_BF16 && q_dtype == NBX_BF16);
+}
+constexpr int warp_path_warps(int q_dtype, int pool_dtype, int d) {
+  if (pool_dtype == NBX_BF16) return d == 64 ? 16 : (d == 128 ? 12 : 6);
+  if (d == 256) return 8;
+  return q_dtype == NBX_F32 && d == 128 ? 12 : 16;
+}
+cudaError_t decode_dispatch_warp_bf16(const DecodeParams& p, int grid_limit, cudaStream_t stream);
+cudaError_t decode_dispatch_warp_e4m3(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
+cudaError_t decode_dispatch_warp_block(const DecodeParams& p, int q_dtype, bool mod, int grid_limit, cudaStream_t stream);
 // m of a partial that the merge has to recompute: a NaN no computation gives
 constexpr uint32_t kRedoBits = 0x7fffbad0u;
 

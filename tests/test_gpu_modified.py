@@ -184,6 +184,57 @@ def test_slopes_of_any_sign_and_size():
     c.check(slopes=[1e30] * 8)          # all weight on the row's own position
 
 
+def test_many_vectors_of_a_pool_without_tensor_core_windows():
+    # windows of 64 and more vectors that the window kernel does not take: pages of 16, d 64, fp32 queries
+    for pool, q_type, rows, h_q, h_kv, d, P, T in (("block", "bf16", 40, 8, 2, 128, 16, 16), ("e4m3", "f32", 70, 4, 1, 256, 64, 0),
+                                                   ("bf16", "bf16", 130, 3, 1, 64, 64, 0), ("bf16", "f32", 33, 4, 2, 128, 64, 0)):
+        c = Case(pool, q_type, rows, h_q, h_kv, d, P, (3, 200, 777), T, seed=16)
+        for mod in (MODS[0], MODS[3], MODS[6]):
+            c.check("f32", **made(mod, c.lens, rows, h_q))
+
+
+def test_a_nan_value_seen_by_some_vectors_of_a_tile():
+    # the key-by-key path of a tile: a NaN (and, in bf16, an infinity) that two of three rows see
+    for pool, T in (("e4m3", 0), ("block", 16), ("bf16", 0)):
+        for d in (64, 128, 256):
+            c = Case(pool, "bf16", 3, 4, 2, d, 16, (100,), T, seed=17)
+            lo = np.array([[0, 20, 40]])
+            ref = oc.attention(c.q.float().numpy(), *c.values, c.table, c.lens, c.scale, key_begin=lo)
+            c.dev[1][c.table[0, 1], :, 9, 5] = 0x7F if pool != "bf16" else float("nan")      # position 25
+            if pool == "bf16":
+                c.dev[1][c.table[0, 0], :, 3, 6] = float("-inf")                             # position 3
+            out = c.call(key_begin=lo).double().cpu().numpy()
+            assert np.all(np.isnan(out[0, :2, :, 5])) and np.all(np.isfinite(out[0, 2]))
+            if pool == "bf16":
+                assert np.all(np.isneginf(out[0, 0, :, 6])) and np.all(np.isfinite(out[0, 1, :, 6]))
+            keep = np.ones(d, dtype=bool)
+            keep[5:7] = False
+            assert np.abs(out[0][:, :, keep] - ref[0][:, :, keep]).max() <= c.tolerance("f32")
+
+
+def test_queries_of_any_size():
+    # the E4M3 kernels scale a query vector by a power of two: tiny, huge, zero, with elements far apart
+    for q_type in ("bf16", "f32"):
+        c = Case("block", q_type, 1, 8, 2, 128, 16, (200, 90), 16, seed=18)
+        q = c.q.float()
+        q[0, 0, 0] = 0.0
+        q[0, 0, 1] *= 1e-30
+        q[0, 0, 2] *= 1e-3
+        q[0, 0, 3, 5] = 300.0
+        q[1, 0, 4] *= torch.logspace(-12, 0, 128)
+        q[1, 0, 5] = float("nan")
+        q[1, 0, 6, 7] = float("inf")
+        c.q = q.to(c.q.dtype)
+        out = c.call().double().cpu().numpy()
+        with np.errstate(invalid="ignore"):
+            ref = oc.attention(c.q.float().numpy(), *c.values, c.table, c.lens, c.scale)
+        assert np.all(np.isnan(out[1, 0, 5])) and np.all(np.isnan(out[1, 0, 6]) | np.isfinite(out[1, 0, 6]))
+        c.q[1, 0, 5:7] = 0.0
+        c.q[0, 0, 3] = 0.0          # (its scores are large: left out of the tolerance's bound)
+        out[1, 0, 5:7] = ref[1, 0, 5:7] = out[0, 0, 3] = ref[0, 0, 3] = 0.0
+        assert np.abs(out - ref).max() <= c.tolerance("f32")
+
+
 def test_pages_no_row_sees_may_be_gone():
     # a window of 37 keys: the pages before it are -1, as a serving loop frees them; and out of the pool
     for pool, T in (("bf16", 0), ("block", 16)):
@@ -220,17 +271,19 @@ def test_without_modifications_it_is_the_plain_decode():
     i32 = lambda a: torch.from_numpy(a).to(DEV)   # noqa: E731
     plain = nbx.nbx_paged_decode_attn(c.q.to(DEV), *c.dev, i32(c.table), i32(c.lens), 2000, c.scale)
     assert torch.equal(plain, c.call())
-    # a range that hides nothing, slopes of 0: the same sums in the same order
-    assert torch.equal(plain, c.call(slopes=[0.0] * 32))
-    assert torch.equal(plain.to(torch.bfloat16), c.call("bf16"))
+    # slopes of 0 and a cap far above the scores: other kernels, the same numbers
+    for other in (c.call(slopes=[0.0] * 32), c.call(softcap=1e6), c.call("bf16")):
+        err = float((plain.double() - other.double()).abs().max())
+        assert err <= c.tolerance("bf16" if other.dtype == torch.bfloat16 else "f32") + c.tolerance("f32")
 
 
 def test_block_scales_of_one_are_the_plain_decode():
     c = Case("block", "bf16", 1, 32, 8, 128, 16, (5, 900, 2000), 16, seed=7)
     c.scales = [np.ones_like(s) for s in c.scales]
+    c.values = [oc.pool_values(x, "e4m3", scales=s) for x, s in zip(c.codes, c.scales)]
     i32 = lambda a: torch.from_numpy(a).to(DEV)   # noqa: E731
     plain = nbx.nbx_paged_decode_attn(c.q.to(DEV), *c.dev, i32(c.table), i32(c.lens), 2000, c.scale)
-    assert torch.equal(plain, c.call())
+    assert float((plain - c.call()).abs().max()) <= 2 * c.tolerance("f32")
 
 
 def test_scales_at_the_ends_of_their_range():
@@ -299,7 +352,7 @@ def on_tensor_cores(c, out_type):
     h_kv = c.dev[0].shape[1]
     return nbx.nbx_paged_decode_modified_partial_kernel(nbx.dtype_code(c.q), kind, nbx.NBX_BF16 if out_type == "bf16" else
                                                         nbx.NBX_F32, c.rows, c.h_q, h_kv, c.d, c.num_pages,
-                                                        c.P) != nbx.PARTIAL_SIMT
+                                                        c.P) in (nbx.PARTIAL_TCGEN05, nbx.PARTIAL_TCGEN05_FP8)
 
 
 @pytest.mark.parametrize("mod", MODS, ids=lambda m: "-".join(str(v) for v in m.values()) or "plain")
