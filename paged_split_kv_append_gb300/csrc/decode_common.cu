@@ -192,7 +192,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
       // about tc_units units in all, shared in proportion to the lengths (the grid's one wave); a
       // split keeps at least 64 positions (the tensor-core tile), and a sequence has at most the
       // workspace's partial slots (max_splits, the pages' rule at the longest length)
-      const long long want = static_cast<long long>(p.tc_units) * L / (static_cast<long long>(p.tc_pairs) * len_sum);
+      long long num = static_cast<long long>(p.tc_units) * L;
+      const long long den = static_cast<long long>(p.tc_pairs) * len_sum;
+      // units taken from a counter may pass one wave by a few, but must not be long: their splits round up
+      if (X && p.tc_round_up) num += den - 1;
+      const long long want = num / den;
       const int cap_s = min(p.max_splits, max(1, L / 64));
       S = static_cast<int>(want < 1 ? 1 : (want > cap_s ? cap_s : want));
     } else {
@@ -399,7 +403,7 @@ __device__ __noinline__ RowPartial recompute_partial(const DecodeParams& p, int 
     const int64_t head = static_cast<int64_t>(page) * p.h_kv + h;
     float ks = 1.f, vs = 1.f;
     if (p.k_scales) {
-      const int64_t blk = head * (p.page_tokens / p.scale_tokens) + in_page / p.scale_tokens;
+      const int64_t blk = head * (p.page_tokens >> p.scale_shift) + (in_page >> p.scale_shift);
       ks = p.k_scales[blk];
       vs = p.v_scales[blk];
       if (!(ks >= kMinScale && ks <= kMaxScale && vs >= kMinScale && vs <= kMaxScale)) continue;
@@ -740,8 +744,12 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
   }
   const bool warps = x && !mma && warp_path_applies(q_dtype, pool_dtype);
   if (warps) {   // one unit a resident warp over the GPU
-    q.tc_units = device_info().sm_count * warp_path_warps(q_dtype, pool_dtype, p.d);
+    // (splits round up, by half a split a sequence on average: taken off the aim)
+    const int units = device_info().sm_count * warp_path_warps(q_dtype, pool_dtype, p.d);
     q.tc_pairs = p.h_kv * ((p.rows * p.group + kWarpUnitVectors - 1) / kWarpUnitVectors);
+    const int64_t extra = static_cast<int64_t>(q.tc_pairs) * p.batch / 2;
+    q.tc_units = extra < units / 2 ? units - static_cast<int>(extra) : units / 2;
+    q.tc_round_up = 1;
   }
   cudaError_t e = x ? launch_plan<true>(q, stream) : launch_plan<false>(q, stream);
   if (e != cudaSuccess) return e;

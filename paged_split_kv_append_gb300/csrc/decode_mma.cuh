@@ -398,15 +398,15 @@ constexpr int kParts = kHalf / 16;  // 16-position parts of them, each of one bl
 // The scales of a thread's parts of a tile.
 struct TileScales {
   float k[kParts], v[kParts];
-  __device__ __forceinline__ void load(const DecodeParams& p, const MmaUnit& mu, int n0, int page) {
+  // in_page: the first column's position in its page
+  __device__ __forceinline__ void load(const DecodeParams& p, const MmaUnit& mu, int in_page, int page) {
 #pragma unroll
     for (int i = 0; i < kParts; ++i) k[i] = v[i] = 1.f;
     if (page < 0 || page >= p.num_pages || mu.nothing) return;
-    const int64_t base = (static_cast<int64_t>(page) * p.h_kv + mu.h) * (p.page_tokens / p.scale_tokens);
-    const int in_page = n0 % p.page_tokens;
+    const int64_t base = (static_cast<int64_t>(page) * p.h_kv + mu.h) * (p.page_tokens >> p.scale_shift);
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
-      const int64_t at = base + (in_page + 16 * i) / p.scale_tokens;
+      const int64_t at = base + ((in_page + 16 * i) >> p.scale_shift);
       k[i] = p.k_scales[at];
       v[i] = p.v_scales[at];
     }
@@ -528,7 +528,11 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
     // both through the last tile but for its sums, which follow with the next exchange
     float w_run = 0.f, w_half = 0.f, e_run = 0.f;
     TileScales ts_next;
-    if constexpr (kBlk) ts_next.load(p, mu, mu.start + half * kHalf, __shfl_sync(0xffffffffu, pg_cur, 0));
+    int in_page = 0;   // kBlk: position in its page of the next tile's first column, stepped without a division
+    if constexpr (kBlk) {
+      in_page = mu.start % p.page_tokens + half * kHalf;
+      ts_next.load(p, mu, in_page, __shfl_sync(0xffffffffu, pg_cur, 0));
+    }
     uint32_t pb = 0, pp = 0;   // buffer and phase count of the previous tile
     for (int t = 0; t < mu.tiles; ++t) {
       const int n0 = mu.start + t * kMmaN + half * kHalf;   // position of this thread's first column
@@ -547,7 +551,9 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       if constexpr (kBlk) {
         const TileScales ts = ts_next;
         const int next = __shfl_sync(0xffffffffu, pg_cur, (t + 1) & 31);
-        if (t + 1 < mu.tiles) ts_next.load(p, mu, n0 + kMmaN, next);
+        in_page += kMmaN;
+        if (in_page >= p.page_tokens) in_page = half * kHalf;
+        if (t + 1 < mu.tiles) ts_next.load(p, mu, in_page, next);
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
           const bool fit = ts.k[k] >= kMinScale && ts.k[k] <= kMaxScale && ts.v[k] >= kMinScale && ts.v[k] <= kMaxScale;

@@ -9,15 +9,20 @@
 //
 //  * Work unit = (split entry, KV head, 8 query vectors), taken by one warp from the list's counter. Warps
 //    share nothing: no barriers, no waits but for their own copies. Splits are sized for one unit a resident
-//    warp over the GPU (at least 64 positions each, at most 64 a sequence).
+//    warp over the GPU (at least 64 positions each, at most 64 a sequence), rounded up: rounded down, some
+//    sequences' units were twice the mean (ragged bf16: 246 against 220 us).
+//  * What bounds it: of the 62 us of that kernel the copies alone take 55 (5.4 TB/s, with the first tiles'
+//    chain of loads and the tail; 44 us at the copy rate), the arithmetic alone 47.
 //  * Each warp streams its unit's 16-position tiles into a ring of its own in shared memory with 16-byte
 //    cp.async copies (a tile of one KV head is one contiguous block of the pool), 16-byte chunks swizzled by
 //    row so that both products read them without bank conflicts.
-//  * S = Q K^T: M = the 8 vectors (rows 0-7; rows 8-15 hold the second term of fp32 queries, else zeros), N = 8
-//    keys, K = d. Lane (g, t) = (lane / 4, lane % 4) holds vector g's scores of keys 2t, 2t + 1 of each 8: the
-//    layout that the second product wants of P as its B operand.
-//  * O^T += V^T P^T: M = 16 of d, N = the 8 vectors, K = 16 keys. V's rows are keys, so two keys' values of one
-//    dimension are paired with byte permutes.
+//  * S^T = K Q^T: M = 16 keys, N = the 8 vectors, K = d. Lane (g, t) = (lane / 4, lane % 4) holds the scores of
+//    keys g and g + 8 for vectors 2t and 2t + 1, whose part of O it accumulates too. (Queries as the A operand,
+//    padded to 16 rows, gave P in place for the second product, but twice the MMAs and a register of zeros
+//    for every two of queries: 80 against 74 us a call for the 285 MB. The first product run a tile ahead of
+//    the second, to fill its latencies: no difference.)
+//  * O^T += V^T P^T: M = 16 of d, N = the 8 vectors, K = 16 keys. P is transposed on the way with movmatrix. V's
+//    rows are keys, so two keys' values of one dimension are paired with byte permutes.
 //  * Formats. E4M3: codes convert to f16 exactly; bf16 queries times a power of two are f16 exactly but for
 //    elements under 2^-29 of the vector's largest, fp32 ones are two f16 terms (22 bits); P is two f16 terms,
 //    2^-22, with the running max kept so that the largest weight lies in [2^7, 2^15]. bf16: the operands as
@@ -93,10 +98,11 @@ __device__ __forceinline__ void mma_pool(float (&c)[4], uint32_t a0, uint32_t a1
   if constexpr (kE4) mma_f16(c, a0, a1, a2, a3, b0, b1);
   else mma_bf16(c, a0, a1, a2, a3, b0, b1);
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t pair16) {
-  uint32_t h2;
-  asm("{ .reg .b16 t; cvt.u16.u32 t, %1; cvt.rn.f16x2.e4m3x2 %0, t; }" : "=r"(h2) : "r"(pair16));
-  return h2;
+// Four E4M3 codes to two f16 pairs, exactly (the low two codes in lo).
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 __device__ __forceinline__ uint32_t h2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -106,6 +112,13 @@ __device__ __forceinline__ float2 h2_floats(uint32_t w) { return __half22float2(
 __device__ __forceinline__ uint32_t b2_bits(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit elements, lane (g, t) holding row g's columns 2t and 2t + 1.
+__device__ __forceinline__ uint32_t transposed8x8(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
+  return r;
 }
 
 // Two weights as terms of the product's operand type: x = sum of the terms to 2^-22 (f16) or 2^-24 (bf16).
@@ -161,6 +174,14 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_u32(smem_raw) + warp * (C::kDepth * C::kStage);
+  // Offsets within a tile, fixed for the kernel: a lane's chunk of the copies (and the same with the swizzle of
+  // rows 4 further on), of its key rows g and 8 + g, and of its value rows 2t, 2t + 8 and 2t + 1, 2t + 9.
+  // Chunks c + 4 of a row lie at the offset of c with bit 6 flipped, chunks c + 8 128 bytes further on.
+  const int c_row = lane / C::kChunks;   // 0 with 32 chunks a row
+  const uint32_t c_off = c_row * C::kRow + swizzled<C::kChunks>(c_row, lane % C::kChunks) * 16;
+  const uint32_t k_off = g * C::kRow + swizzled<C::kChunks>(g, t) * 16;
+  const uint32_t v_off0 = 2 * t * C::kRow + (C::kChunks >= 8 ? swizzled<C::kChunks>(2 * t, g) * 16 : g * 8);
+  const uint32_t v_off1 = (2 * t + 1) * C::kRow + (C::kChunks >= 8 ? swizzled<C::kChunks>(2 * t + 1, g) * 16 : g * 8);
   pdl_wait();              // the plan kernel's work list and the append's positions are visible from here on
   pdl_launch_dependents(); // the merge kernel may be scheduled as CTAs of this grid retire
   const int RG = p.rows * p.group;
@@ -176,18 +197,31 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
     const int rem = u % span;
     const int h = rem / blocks, v0 = (rem - h * blocks) * kWarpVecs;
     const Entry en = p.entries[u / span];
-    // ---- vector g of the unit: its row, the keys it sees, its bias
-    const bool vq = v0 + g < RG;
-    const int r = vq ? (v0 + g) / p.group : 0, gq = vq ? v0 + g - r * p.group : 0;
-    const int at = en.len - p.rows + r;
-    KeyRange kr = {0, 0};
-    if (vq) kr = kMod ? key_range(p, en.b, r, en.len) : (at >= 0 ? KeyRange{0, at + 1} : KeyRange{0, 0});
-    const float slope = kMod && vq && p.slopes ? p.slopes[h * p.group + gq] * kLog2e : 0.f;
-    // the keys that some vector sees, cut to whole tiles of the split, and those that every vector sees
-    int lo = kr.hi > kr.lo ? kr.lo : INT_MAX, hi = kr.hi;
-    int all_lo = vq ? kr.lo : 0, all_hi = vq ? kr.hi : INT_MAX;
+    // ---- vectors 2t and 2t + 1 of the unit: their rows, the keys they see, their biases
+    int at[2], seen_lo[2], seen_hi[2];
+    float slope[2];
+    int lo = INT_MAX, hi = 0, all_lo = 0, all_hi = INT_MAX;
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
+    for (int y = 0; y < 2; ++y) {
+      const int v = v0 + 2 * t + y;
+      const bool vq = v < RG;
+      const int r = vq ? v / p.group : 0;
+      at[y] = en.len - p.rows + r;
+      KeyRange kr = {0, 0};
+      if (vq) kr = kMod ? key_range(p, en.b, r, en.len) : (at[y] >= 0 ? KeyRange{0, at[y] + 1} : KeyRange{0, 0});
+      slope[y] = kMod && vq && p.slopes ? p.slopes[h * p.group + (v - r * p.group)] * kLog2e : 0.f;
+      seen_lo[y] = kr.lo;
+      seen_hi[y] = kr.hi;
+      if (kr.hi > kr.lo) lo = min(lo, kr.lo);
+      hi = max(hi, kr.hi);
+      if (vq) {
+        all_lo = max(all_lo, kr.lo);
+        all_hi = min(all_hi, kr.hi);
+      }
+    }
+    // the keys that some vector sees, cut to whole tiles of the split, and those that every vector sees
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
       lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
       hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
       all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
@@ -204,8 +238,10 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
     int pages_next = pc + 32 + lane <= last_page ? bt[pc + 32 + lane] : -1;
     int i_pi = pc, i_po = start - pc * P;  // page index and position in it of the next tile to copy
     uint32_t ok_bits = 0;                  // bit s: stage s holds a tile
+    int fill = 0;                          // the stage that the next copy fills
     auto issue = [&](int i) {
-      const int slot = i % C::kDepth;
+      const int slot = fill;
+      fill = fill + 1 == C::kDepth ? 0 : fill + 1;
       if (i < tiles) {
         if (i_pi >= pc + 32) {
           pc += 32;
@@ -218,19 +254,23 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
         if (ok) {
           const int64_t head = static_cast<int64_t>(page) * p.h_kv + h;
           const int64_t off = (head * P + i_po) * C::kRow;
-          const char* const ks = static_cast<const char*>(p.k_pool) + off;
-          const char* const vs = static_cast<const char*>(p.v_pool) + off;
+          const char* const ks = static_cast<const char*>(p.k_pool) + off + lane * 16;
+          const char* const vs = static_cast<const char*>(p.v_pool) + off + lane * 16;
           const uint32_t dst = ring + slot * C::kStage;
 #pragma unroll
-          for (int c = lane; c < C::kTile / 16; c += 32) {
-            const int row = c / C::kChunks;
-            const uint32_t to = dst + row * C::kRow + swizzled<C::kChunks>(row, c % C::kChunks) * 16;
-            cp_async16(to, ks + c * 16);
-            cp_async16(to + C::kTile, vs + c * 16);
+          for (int j = 0; j < C::kTile / 512; ++j) {
+            // chunk 32 j + lane: row c_row + 32 j / kChunks
+            uint32_t to;
+            if constexpr (C::kChunks == 32) to = j * C::kRow + swizzled<32>(j, lane) * 16;
+            else if constexpr (C::kChunks == 16) to = 2 * j * C::kRow + (c_off ^ ((2 * j) & 6) * 16);
+            else if constexpr (C::kChunks == 8) to = 4 * j * C::kRow + (c_off ^ ((4 * j) & 4) * 16);
+            else to = 8 * j * C::kRow + c_off;
+            cp_async16(dst + to, ks + j * 512);
+            cp_async16(dst + to + C::kTile, vs + j * 512);
           }
           if (kBlk && lane < 2)
             cp_async4(dst + 2 * C::kTile + lane * 4,
-                      (lane ? p.v_scales : p.k_scales) + head * (P / p.scale_tokens) + i_po / p.scale_tokens);
+                      (lane ? p.v_scales : p.k_scales) + head * (P >> p.scale_shift) + (i_po >> p.scale_shift));
         } else if (lane == 0) {
           raise_status(p.status, NBX_DEV_BAD_PAGE);
         }
@@ -245,10 +285,13 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
 #pragma unroll 1
     for (int i = 0; i < C::kDepth - 1; ++i) issue(i);
 
-    // ---- the unit's queries as the A operand: lane (g, t) holds vector g's elements of its key chunks
+    // ---- the unit's queries as the B operand: lane (g, t) holds vector g's elements of the chunks that it reads
+    // of the keys
     uint32_t qh[C::kQFrags][2], ql[C::kTwo ? C::kQFrags : 1][2];
-    float fac = p.qk_scale_log2;   // from a product to log2 units
+    float fac[2] = {p.qk_scale_log2, p.qk_scale_log2};   // vectors 2t, 2t + 1: from a product to log2 units
     {
+      const bool vq = v0 + g < RG;
+      const int r = vq ? (v0 + g) / p.group : 0, gq = vq ? v0 + g - r * p.group : 0;
       constexpr int kElems = kE4 ? 16 : 8;   // elements of a 16-byte chunk
       const int64_t orow = (static_cast<int64_t>(en.b) * p.rows + r) * p.h_q + static_cast<int64_t>(h) * p.group + gq;
       const char* const q = static_cast<const char*>(p.q) + orow * D * QT::kBytes;
@@ -275,7 +318,9 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
         if (amax > 0.f && amax <= 3.402823466e38f)
           e2 = min(120, max(-120, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)));
         const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-        fac *= __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+        fac[0] *= __shfl_sync(0xffffffffu, down, 8 * t);
+        fac[1] *= __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
         for (int i = 0; i < C::kKLoads; ++i) {
 #pragma unroll
@@ -294,19 +339,20 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
       }
     }
 
-    float m_run = -INFINITY, l_run = 0.f;   // vector g: the exponent's reference, and this lane's part of the sum
-    float acc[C::kMTiles][4];               // vectors 2t, 2t + 1: D / 8 dimensions each (see the epilogue)
+    // vectors 2t, 2t + 1: the exponent's reference, this lane's part of the sum, D / 8 dimensions of O
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    float acc[C::kMTiles][4];
 #pragma unroll
     for (int i = 0; i < C::kMTiles; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 
+    int slot = 0;   // the stage of tile i
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
+    for (int i = 0; i < tiles; ++i, slot = slot + 1 == C::kDepth ? 0 : slot + 1) {
       issue(i + C::kDepth - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(C::kDepth - 1) : "memory");
       __syncwarp();   // every lane's copies of tile i have landed
-      const int slot = i % C::kDepth;
       const uint32_t kb = ring + slot * C::kStage, vb = kb + C::kTile;
       bool ok = (ok_bits >> slot) & 1u;
       float ks = 1.f, lv = 0.f, iv = 1.f;
@@ -323,36 +369,30 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
       }
       if (ok) {
         const int n0 = start + i * kTileN;
-        // ---- scores of vector g: keys n0 + 2t, + 1 (z[0], z[1]) and n0 + 8 + 2t, + 1 (z[2], z[3])
-        float z[4];
+        // ---- scores: z[0], z[1] of key n0 + g, z[2], z[3] of key n0 + 8 + g, for vectors 2t and 2t + 1
+        float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int row = nt * 8 + g;
-          float s[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < C::kKLoads; ++c) {
+          const uint32_t a = kb + (k_off ^ ((c & 1) * 64)) + (c >> 1) * 128;   // chunk t + 4 c of row g
+          const uint4 x = lds128(a), y = lds128(a + 8 * C::kRow);
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int c = 0; c < C::kKLoads; ++c) {
-            const uint4 kv = lds128(kb + row * C::kRow + swizzled<C::kChunks>(row, t + 4 * c) * 16);
-            const uint32_t w[4] = {kv.x, kv.y, kv.z, kv.w};
-#pragma unroll
-            for (int j = 0; j < C::kMmaPerChunk; ++j) {
-              uint32_t b0, b1;
-              if constexpr (kE4) {
-                b0 = e4m3x2_to_h2(w[j] & 0xffffu);
-                b1 = e4m3x2_to_h2(w[j] >> 16);
-              } else {
-                b0 = w[2 * j];
-                b1 = w[2 * j + 1];
-              }
-              const int f = c * C::kMmaPerChunk + j;
-              mma_pool<kE4>(s, qh[f][0], C::kTwo ? ql[C::kTwo ? f : 0][0] : 0u, qh[f][1], C::kTwo ? ql[C::kTwo ? f : 0][1] : 0u,
-                            b0, b1);
+          for (int j = 0; j < C::kMmaPerChunk; ++j) {
+            uint32_t a0, a1, a2, a3;
+            if constexpr (kE4) {
+              e4m3x4_to_h2(xw[j], a0, a2);
+              e4m3x4_to_h2(yw[j], a1, a3);
+            } else {
+              a0 = xw[2 * j], a2 = xw[2 * j + 1];
+              a1 = yw[2 * j], a3 = yw[2 * j + 1];
             }
+            const int f = c * C::kMmaPerChunk + j;
+            mma_pool<kE4>(z, a0, a1, a2, a3, qh[f][0], qh[f][1]);
+            if constexpr (C::kTwo) mma_pool<kE4>(z, a0, a1, a2, a3, ql[f][0], ql[f][1]);
           }
-          z[2 * nt] = C::kTwo ? s[0] + s[2] : s[0];
-          z[2 * nt + 1] = C::kTwo ? s[1] + s[3] : s[1];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] *= kBlk ? fac * ks : fac;
+        for (int e = 0; e < 4; ++e) z[e] *= kBlk ? fac[e & 1] * ks : fac[e & 1];
         if constexpr (kMod) {
           if (p.cap_log2 > 0.f) {
             const float x[4] = {z[0] * p.cap_inv, z[1] * p.cap_inv, z[2] * p.cap_inv, z[3] * p.cap_inv};
@@ -368,49 +408,62 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
           if (p.slopes != nullptr) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              z[e] = fmaf(-slope, static_cast<float>(abs(at - (n0 + (e >> 1) * 8 + 2 * t + (e & 1)))), z[e]);
+              z[e] = fmaf(-slope[e & 1], static_cast<float>(abs(at[e & 1] - (n0 + (e >> 1) * 8 + g))), z[e]);
           }
         }
         const bool full = n0 >= all_lo && n0 + kTileN <= all_hi && n0 + kTileN <= end;
-        uint32_t sees = 15u;   // bit e: the vector sees the key of z[e]
+        uint32_t sees = 15u;   // bit e: z[e]'s vector sees its key
         if (!full) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int n = n0 + (e >> 1) * 8 + 2 * t + (e & 1);
-            if (n < kr.lo || n >= kr.hi || n >= end) {
+            const int n = n0 + (e >> 1) * 8 + g;
+            if (n < seen_lo[e & 1] || n >= seen_hi[e & 1] || n >= end) {
               z[e] = -INFINITY;
               sees &= ~(1u << e);
             }
           }
         }
         // ---- the reference moves when a weight would pass 2^15; a NaN one stays NaN
-        float mx = max_nan(max_nan(z[0], z[1]), max_nan(z[2], z[3])) + lv;
-        if (__any_sync(0xffffffffu, !(mx <= m_run + kWarpHi) && m_run == m_run)) {
-          mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const bool move = !(mx <= m_run + kWarpHi) && m_run == m_run;
-          const float m_new = move ? mx - kWarpMid : m_run;
-          const float f = move ? fast_exp2(m_run - m_new) : 1.f;
-          m_run = m_new;
-          l_run *= f;
-          const float f0 = __shfl_sync(0xffffffffu, f, 8 * t), f1 = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+        float mx[2] = {max_nan(z[0], z[2]) + lv, max_nan(z[1], z[3]) + lv};
+        const bool past = (!(mx[0] <= m_run[0] + kWarpHi) && m_run[0] == m_run[0]) ||
+                          (!(mx[1] <= m_run[1] + kWarpHi) && m_run[1] == m_run[1]);
+        if (__any_sync(0xffffffffu, past)) {
+          float f[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx[y] = max_nan(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], o));
+            const bool move = !(mx[y] <= m_run[y] + kWarpHi) && m_run[y] == m_run[y];
+            const float m_new = move ? mx[y] - kWarpMid : m_run[y];
+            f[y] = move ? fast_exp2(m_run[y] - m_new) : 1.f;
+            m_run[y] = m_new;
+            l_run[y] *= f[y];
+          }
 #pragma unroll
           for (int j = 0; j < C::kMTiles; ++j) {
-            acc[j][0] *= f0;
-            acc[j][1] *= f1;
-            acc[j][2] *= f0;
-            acc[j][3] *= f1;
+            acc[j][0] *= f[0];
+            acc[j][1] *= f[1];
+            acc[j][2] *= f[0];
+            acc[j][3] *= f[1];
           }
         }
-        const float off = m_run == -INFINITY ? 0.f : lv - m_run;   // nothing seen yet: every z is -inf
         float pw[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pw[e] = fast_exp2(z[e] + off);
-        const float sum = (pw[0] + pw[1]) + (pw[2] + pw[3]);
-        l_run += kBlk ? sum * iv : sum;
-        uint32_t p0[3], p1[3];   // the B operand: keys 2t, 2t + 1, and 8 + 2t, 9 + 2t
+        for (int e = 0; e < 4; ++e) {   // nothing seen yet: every z is -inf
+          const float off = m_run[e & 1] == -INFINITY ? 0.f : lv - m_run[e & 1];
+          pw[e] = fast_exp2(z[e] + off);
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) l_run[y] += kBlk ? (pw[y] + pw[2 + y]) * iv : pw[y] + pw[2 + y];
+        // the B operand of the second product: vector g's weights of keys 2t, 2t + 1, and of 8 + 2t, 9 + 2t
+        uint32_t p0[3], p1[3];
         split_terms<kE4>(pw[0], pw[1], p0);
         split_terms<kE4>(pw[2], pw[3], p1);
+#pragma unroll
+        for (int x = 0; x < kTerms; ++x) {
+          p0[x] = transposed8x8(p0[x]);
+          p1[x] = transposed8x8(p1[x]);
+        }
         // ---- O^T += V^T P^T: lane (g, t) reads its 16-byte chunks of keys 2t, 2t + 1, 2t + 8, 2t + 9
         constexpr int kVLoads = C::kChunks >= 8 ? C::kChunks / 8 : 1;
         constexpr int kWords = C::kChunks >= 8 ? 4 : 2;   // 32-bit words of a load (rows of 64 bytes: 8 bytes a lane)
@@ -422,8 +475,7 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
           for (int c = 0; c < kVLoads; ++c)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int row = 2 * t + (e & 1) + (e >> 1) * 8;
-              const uint32_t a = vb + row * C::kRow + (kWords == 4 ? swizzled<C::kChunks>(row, g + 8 * c) * 16 : g * 8);
+              const uint32_t a = vb + ((e & 1) ? v_off1 : v_off0) + (e >> 1) * 8 * C::kRow + c * 128;   // chunk g + 8 c
               if constexpr (kWords == 4) {
                 bad = bad || not_finite<kE4>(lds128(a));
               } else {
@@ -439,12 +491,12 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
             uint32_t w[4][kWords];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int row = 2 * t + (e & 1) + (e >> 1) * 8;
+              const uint32_t a = vb + ((e & 1) ? v_off1 : v_off0) + (e >> 1) * 8 * C::kRow + c * 128;
               if constexpr (kWords == 4) {
-                const uint4 x = lds128(vb + row * C::kRow + swizzled<C::kChunks>(row, g + 8 * c) * 16);
+                const uint4 x = lds128(a);
                 w[e][0] = x.x, w[e][1] = x.y, w[e][2] = x.z, w[e][3] = x.w;
               } else {
-                const uint2 x = lds64(vb + row * C::kRow + g * 8);
+                const uint2 x = lds64(a);
                 w[e][0] = x.x, w[e][1] = x.y;
               }
             }
@@ -455,8 +507,9 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
                 for (int y = 0; y < 2; ++y) {
                   const uint32_t sel = y ? 0x7362u : 0x5140u;
                   const uint32_t ab = __byte_perm(w[0][k], w[1][k], sel), cd = __byte_perm(w[2][k], w[3][k], sel);
-                  const uint32_t a0 = e4m3x2_to_h2(ab & 0xffffu), a1 = e4m3x2_to_h2(ab >> 16);
-                  const uint32_t a2 = e4m3x2_to_h2(cd & 0xffffu), a3 = e4m3x2_to_h2(cd >> 16);
+                  uint32_t a0, a1, a2, a3;
+                  e4m3x4_to_h2(ab, a0, a1);
+                  e4m3x4_to_h2(cd, a2, a3);
                   float(&o)[4] = acc[(c * kWords + k) * 2 + y];
 #pragma unroll
                   for (int x = 0; x < kTerms; ++x) mma_f16(o, a0, a1, a2, a3, p0[x], p1[x]);
@@ -474,11 +527,11 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
           // key by key: a vector's accumulators take only the keys it sees
 #pragma unroll 1
           for (int k = 0; k < kTileN; ++k) {
-            const int e = (k & 1) + (k >> 3) * 2, tk = (k & 7) >> 1;   // which of its lane's four, which lane
-            const float pe = e == 0 ? pw[0] : (e == 1 ? pw[1] : (e == 2 ? pw[2] : pw[3]));
-            const uint32_t se = (sees >> e) & 1u;
-            const float pa = __shfl_sync(0xffffffffu, pe, 8 * t + tk), pb = __shfl_sync(0xffffffffu, pe, 8 * t + 4 + tk);
-            const uint32_t sa = __shfl_sync(0xffffffffu, se, 8 * t + tk), sb = __shfl_sync(0xffffffffu, se, 8 * t + 4 + tk);
+            const int from = (k & 7) * 4 + t;   // the lane with key k's weights for vectors 2t, 2t + 1
+            const float pa = __shfl_sync(0xffffffffu, k < 8 ? pw[0] : pw[2], from);
+            const float pb = __shfl_sync(0xffffffffu, k < 8 ? pw[1] : pw[3], from);
+            const uint32_t both = __shfl_sync(0xffffffffu, k < 8 ? sees : sees >> 2, from);
+            const bool sa = both & 1u, sb = both & 2u;
 #pragma unroll
             for (int j = 0; j < C::kMTiles; ++j) {
               // M tile j of this lane: elements 2 (j % per), + 1 of its chunk j / per
@@ -507,25 +560,24 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
     __syncwarp();
 
     // ---- the partial: lane (g, t) holds of vectors 2t and 2t + 1 the dimensions of its chunks
-    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
-    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
     const bool multi = en.n_splits > 1;
     const uint64_t keep = l2_keep_policy(p.keep_frac);   // the partials stay in L2 for the merge
-    if (multi && vq && t == 0) {
-      const int64_t slot = ((static_cast<int64_t>(en.b) * p.rows + r) * p.h_q + static_cast<int64_t>(h) * p.group + gq) *
-                               p.max_splits + en.s;
-      st_global_hint(p.m_part + slot, m_run, keep);
-      st_global_hint(p.l_part + slot, l_run, keep);
-    }
 #pragma unroll
     for (int y = 0; y < 2; ++y) {
+      float lw = l_run[y];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+      const float mv = m_run[y];
       const int v = v0 + 2 * t + y;
-      const float mv = __shfl_sync(0xffffffffu, m_run, 8 * t + 4 * y), lw = __shfl_sync(0xffffffffu, l_run, 8 * t + 4 * y);
       if (v >= RG) continue;
       const int rv = v / p.group;
       const int64_t orow = (static_cast<int64_t>(en.b) * p.rows + rv) * p.h_q + static_cast<int64_t>(h) * p.group +
                            (v - rv * p.group);
       const float sc = multi ? 1.f : (mv == -INFINITY ? 0.f : p.v_scale / lw);
+      if (multi && g == 0) {
+        st_global_hint(p.m_part + orow * p.max_splits + en.s, mv, keep);
+        st_global_hint(p.l_part + orow * p.max_splits + en.s, lw, keep);
+      }
       constexpr int kVLoads = C::kChunks >= 8 ? C::kChunks / 8 : 1;
       constexpr int kPer = C::kMTiles / kVLoads;   // M tiles of a chunk: 2 kPer consecutive dimensions
 #pragma unroll

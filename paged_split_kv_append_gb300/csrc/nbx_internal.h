@@ -209,6 +209,7 @@ struct DecodeParams {
   // len / 64)]
   int tc_units;
   int tc_pairs;
+  int tc_round_up;   // splits rounded up instead of down (units taken from the counter by single warps)
   // ---- read only by the kernels of the modified and block-scaled decodes (kScoreMod, kBlockScaled)
   int out_bf16;            // the output is bf16, rounded once from the fp32 result
   float cap_log2;          // softcap * log2(e), and its reciprocal; 0: no cap
@@ -218,7 +219,7 @@ struct DecodeParams {
   const int32_t* key_end;
   const float* k_scales;   // [num_pages, h_kv, page_tokens / scale_tokens]
   const float* v_scales;
-  int scale_tokens;
+  int scale_shift;         // log2 of the positions per scale
   int2* ranges;            // [batch, range_tiles] keys the rows of a sequence's M tile see (SIMT: of the sequence)
   int range_tiles;
   int pool_e4m3;           // the pools are E4M3 (else bf16): what a recomputed partial of a window reads
