@@ -745,7 +745,7 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
   const bool warps = x && !mma && warp_path_applies(q_dtype, pool_dtype);
   if (warps) {   // one unit a resident warp over the GPU
     // (splits round up, by half a split a sequence on average: taken off the aim)
-    const int units = device_info().sm_count * warp_path_warps(q_dtype, pool_dtype, p.d);
+    const int units = device_info().sm_count * warp_path_warps(pool_dtype, p.d);
     q.tc_pairs = p.h_kv * ((p.rows * p.group + kWarpUnitVectors - 1) / kWarpUnitVectors);
     const int64_t extra = static_cast<int64_t>(q.tc_pairs) * p.batch / 2;
     q.tc_units = extra < units / 2 ? units - static_cast<int>(extra) : units / 2;

@@ -57,8 +57,9 @@ struct WarpCfg {
   static constexpr int kQFrags = kKLoads * kMmaPerChunk;    // k16 steps of S
   static constexpr int kMTiles = D / 16;
   static constexpr int kWarpsCta = kStage <= 9000 ? 4 : 2;
-  // registers allow 16 warps an SM up to d = 128 (accumulators and query terms), 8 at 256
-  static constexpr int kRegWarps = D <= 128 ? (kTwo && D == 128 ? 12 : 16) : 8;
+  // warps an SM by their registers (accumulators and query terms): at d = 128, 16 of 128 registers spill and
+  // took 80 us where 12 of 168, a stage deeper, take 74
+  static constexpr int kRegWarps = D == 64 ? 16 : (D == 128 ? 12 : 8);
   static constexpr int kSmemAll = 220 * 1024;
   static constexpr int kDepthAt = kSmemAll / (kRegWarps * kStage);
   static constexpr int kDepth = kDepthAt > 6 ? 6 : (kDepthAt < 2 ? 2 : kDepthAt);   // stages of a warp's ring
@@ -66,7 +67,7 @@ struct WarpCfg {
   static constexpr int kCtas = (kRegWarps < kWarpsBySmem ? kRegWarps : kWarpsBySmem) / kWarpsCta;
   static constexpr int kSmem = kWarpsCta * kDepth * kStage;
   static_assert(kCtas >= 1 && kSmem <= 227 * 1024, "shared memory");
-  static_assert(kCtas * kWarpsCta == warp_path_warps(QT::kCode, PT::kCode, D), "the plan's warps an SM");
+  static_assert(kCtas * kWarpsCta == warp_path_warps(PT::kCode, D), "the plan's warps an SM");
 };
 
 // Physical 16-byte chunk of chunk c of a tile's row: rows 2j and 2j + 1 differ in bit 2, the even rows among
@@ -138,6 +139,19 @@ __device__ __forceinline__ void split_terms(float a, float b, uint32_t (&w)[3]) 
     h = bf16x2_to_float2(w[1]);
     w[2] = b2_bits(a - h.x, b - h.y);
   }
+}
+
+// acc += V^T P^T of one M tile and 16 keys: the terms' products from zero, the smallest first, and one rounded
+// addition. The MMA's own accumulation truncates: over the tiles of a 2048-position split that took 2e-6 off
+// the result, more than all other errors together.
+template <bool kE4>
+__device__ __forceinline__ void add_tile(float (&acc)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         const uint32_t (&p0)[3], const uint32_t (&p1)[3]) {
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int x = kE4 ? 1 : 2; x >= 0; --x) mma_pool<kE4>(o, a0, a1, a2, a3, p0[x], p1[x]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] += o[i];
 }
 
 // A 16-byte chunk of V that holds a NaN (E4M3) or a value that is not finite (bf16).
@@ -510,16 +524,12 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
                   uint32_t a0, a1, a2, a3;
                   e4m3x4_to_h2(ab, a0, a1);
                   e4m3x4_to_h2(cd, a2, a3);
-                  float(&o)[4] = acc[(c * kWords + k) * 2 + y];
-#pragma unroll
-                  for (int x = 0; x < kTerms; ++x) mma_f16(o, a0, a1, a2, a3, p0[x], p1[x]);
+                  add_tile<kE4>(acc[(c * kWords + k) * 2 + y], a0, a1, a2, a3, p0, p1);
                 }
               } else {               // two dimensions: one M tile
                 const uint32_t a0 = __byte_perm(w[0][k], w[1][k], 0x5410), a1 = __byte_perm(w[0][k], w[1][k], 0x7632);
                 const uint32_t a2 = __byte_perm(w[2][k], w[3][k], 0x5410), a3 = __byte_perm(w[2][k], w[3][k], 0x7632);
-                float(&o)[4] = acc[c * kWords + k];
-#pragma unroll
-                for (int x = 0; x < kTerms; ++x) mma_bf16(o, a0, a1, a2, a3, p0[x], p1[x]);
+                add_tile<kE4>(acc[c * kWords + k], a0, a1, a2, a3, p0, p1);
               }
             }
           }

@@ -268,10 +268,8 @@ constexpr int kWarpUnitVectors = 8;
 inline bool warp_path_applies(int q_dtype, int pool_dtype) {
   return pool_dtype == NBX_E4M3 || (pool_dtype == NBX_BF16 && q_dtype == NBX_BF16);
 }
-constexpr int warp_path_warps(int q_dtype, int pool_dtype, int d) {
-  if (pool_dtype == NBX_BF16) return d == 64 ? 16 : (d == 128 ? 12 : 6);
-  if (d == 256) return 8;
-  return q_dtype == NBX_F32 && d == 128 ? 12 : 16;
+constexpr int warp_path_warps(int pool_dtype, int d) {
+  return d == 64 ? 16 : (d == 128 ? 12 : (pool_dtype == NBX_E4M3 ? 8 : 6));
 }
 cudaError_t decode_dispatch_warp_bf16(const DecodeParams& p, int grid_limit, cudaStream_t stream);
 cudaError_t decode_dispatch_warp_e4m3(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
