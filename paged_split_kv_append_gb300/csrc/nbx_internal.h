@@ -47,6 +47,7 @@ struct AppendBlockParams {
   const int32_t* tok_start;
   int32_t* status;
   int n_tok, h_kv, d, num_pages, page_tokens, max_pages, batch, scale_tokens;
+  int scale_shift;  // log2 of scale_tokens
   int64_t n_flat;   // flat block indices: n_tok / T + 2 batch
 };
 
