@@ -26,7 +26,7 @@ constexpr int kScanPages = 2048;      // pages per CTA of the compaction's scan
 constexpr int64_t kSmallTable = 65536;        // entries of the block table
 constexpr int kForkSmallPages = 262144;       // pages: a bitmap of 32 KB
 constexpr int64_t kForkSmallWork = 1 << 20;   // rows x forks compared
-constexpr int kCompactSmallPages = 24576;     // pages: fill counts of 96 KB
+constexpr int kCompactSmallPages = 24576;     // pages: fill counts and destinations of 144 KB
 
 int64_t up256(int64_t x) { return (x + 255) & ~static_cast<int64_t>(255); }
 
@@ -401,12 +401,13 @@ __global__ void __launch_bounds__(256) compact_rank_kernel(CompactParams p) {
   }
 }
 
-// All of it in one CTA, for a small table and pool: fill lives in shared memory, and holds -1 - (new id) for
-// the pages that move once their moves are known.
+// All of it in one CTA, for a small table and pool: fill and the destinations live in shared memory, a page
+// that moves holds -1 - (number of its move) once it is ranked.
 __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(CompactParams p) {
-  extern __shared__ int fill[];   // [num_pages]
+  extern __shared__ int fill[];   // [num_pages], then the destinations [num_pages / 2]
   __shared__ int s_scan[33];
-  const int tid = threadIdx.x;
+  int* const dst = fill + p.num_pages;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < p.num_pages; i += kPlanThreads) fill[i] = 0;
   pdl_wait();
   pdl_launch_dependents();   // (this kernel writes no lengths)
@@ -414,32 +415,38 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(CompactPara
   const int n = p.batch * p.max_pages;
 #pragma unroll 4
   for (int i = tid; i < n; i += kPlanThreads) {
-    const int row = i / p.max_pages;
-    const int cnt = compact_fill(p, row, i - row * p.max_pages, p.block_table[i]);
-    if (cnt >= 0) atomicMax(fill + p.block_table[i], 1 + cnt);
+    const int row = i / p.max_pages, pg = p.block_table[i];
+    const int cnt = compact_fill(p, row, i - row * p.max_pages, pg);
+    if (cnt >= 0) atomicMax(fill + pg, 1 + cnt);
   }
   __syncthreads();
-  // each thread takes a run of pages; ranks as in compact_rank_kernel
-  const int per = (p.num_pages + kPlanThreads - 1) / kPlanThreads;
-  const int lo = min(p.num_pages, tid * per), hi = min(p.num_pages, lo + per);
+  // each warp takes a run of pages, 32 at a time; ranks as in compact_rank_kernel
+  const int per = (p.num_pages + kPlanThreads - 1) / kPlanThreads * 32;
+  const int lo = min(p.num_pages, warp * per), hi = min(p.num_pages, lo + per);
   int mine = 0;
-  for (int i = lo; i < hi; ++i) mine += fill[i] != 0;
+  for (int i = lo + lane; i < hi; i += 32) mine += fill[i] != 0;
   int n_live, below;
   int live = block_scan(mine, s_scan, &n_live);
+  live = __shfl_sync(0xffffffffu, live, 0);   // pages in use before the warp's run
   int low = 0;
-  for (int i = lo; i < min(hi, n_live); ++i) low += fill[i] != 0;
+  for (int i = lo + lane; i < min(hi, n_live); i += 32) low += fill[i] != 0;
   block_scan(low, s_scan, &below);
-  for (int pg = lo; pg < hi; ++pg) {
-    const int f = fill[pg];
-    if (f != 0) {
-      if (pg >= n_live) {
-        p.moves[3 * (live - below)] = pg;
-        p.moves[3 * (live - below) + 2] = f - 1;
+  for (int i0 = lo; i0 < hi; i0 += 32) {
+    const int pg = i0 + lane;
+    const int f = pg < hi ? fill[pg] : 0;
+    const uint32_t used = __ballot_sync(0xffffffffu, f != 0);
+    const int before = live + __popc(used & ((1u << lane) - 1u));
+    if (pg < hi) {
+      if (f != 0 && pg >= n_live) {
+        p.moves[3 * (before - below)] = pg;
+        p.moves[3 * (before - below) + 2] = f - 1;
+        fill[pg] = -1 - (before - below);
+      } else if (f == 0 && pg < n_live) {
+        p.moves[3 * (pg - before) + 1] = pg;
+        dst[pg - before] = pg;
       }
-      ++live;
-    } else if (pg < n_live) {
-      p.moves[3 * (pg - live) + 1] = pg;
     }
+    live += __popc(used);
   }
   const int n_moves = n_live - below;
   for (int i = 3 * n_moves + tid; i < 3 * p.max_moves; i += kPlanThreads) p.moves[i] = -1;
@@ -447,13 +454,11 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(CompactPara
     p.counts[0] = n_moves;
     p.counts[1] = n_live;
   }
-  __syncthreads();   // the moves (same CTA)
-  for (int k = tid; k < n_moves; k += kPlanThreads) fill[p.moves[3 * k]] = -1 - p.moves[3 * k + 1];
   __syncthreads();
 #pragma unroll 4
   for (int i = tid; i < n; i += kPlanThreads) {
     const int pg = p.block_table[i];
-    p.new_block_table[i] = pg >= n_live && pg < p.num_pages ? -1 - fill[pg] : pg;
+    p.new_block_table[i] = pg >= n_live && pg < p.num_pages ? dst[-1 - fill[pg]] : pg;
   }
 }
 
@@ -565,7 +570,7 @@ cudaError_t compact_small_smem() {
   const uint64_t bit = 1ull << (device_info().device & 63);
   if (configured.load() & bit) return cudaSuccess;
   const cudaError_t e =
-      cudaFuncSetAttribute(compact_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCompactSmallPages * 4);
+      cudaFuncSetAttribute(compact_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCompactSmallPages * 6);
   if (e == cudaSuccess) configured.fetch_or(bit);
   return e;
 }
@@ -697,7 +702,7 @@ NBX_API int nbx_paged_kv_compact(const int32_t* block_table, int32_t* new_block_
   if (entries <= kSmallTable && num_pages <= kCompactSmallPages) {
     e = compact_small_smem();
     if (e == cudaSuccess)
-      e = launch_pdl(compact_small_kernel, 1u, kPlanThreads, static_cast<size_t>(num_pages) * 4, st, p);
+      e = launch_pdl(compact_small_kernel, 1u, kPlanThreads, (static_cast<size_t>(num_pages) + num_pages / 2) * 4, st, p);
     if (e == cudaSuccess && copies && max_moves > 0)
       e = launch_copy(copy_params(a, moves, counts, max_moves, status), st);
     return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
