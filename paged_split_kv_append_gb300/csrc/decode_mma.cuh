@@ -67,8 +67,8 @@
 //    does, and the row's sum takes each 16-column part of P' divided by its V scale. So P' keeps its terms'
 //    precision relative to what a position adds to the output, whatever the scales, for a few operations
 //    per 16 positions. The scales of a tile are loaded one tile ahead.
-//  * a cap: z = cap tanh(s / cap). A tile whose scores all lie within 0.75 cap takes an odd polynomial (degree
-//    13, minimax-fitted, relative error 1.2e-8; 9 operations, packed in pairs); others 1 - 2 / (1 + e^2x), whose
+//  * a cap: z = cap tanh(s / cap). A tile whose scores all lie within 0.6 cap takes an odd polynomial (degree
+//    9, minimax-fitted, relative error 8e-8; 6 operations, packed in pairs); others 1 - 2 / (1 + e^2x), whose
 //    two special-function results per score would make the cap, not the stream, the bound of every tile.
 //  * a bias by distance (one FMA) and key ranges: a unit reads only the 64-position tiles between the
 //    first and the last key that some row of its M tile sees; the plan kernel wrote these ranges.
@@ -427,24 +427,33 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[kHalf], const float (&
     ax = fmaxf(ax, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c[k]);
   }
   // (a NaN is passed over by fmaxf, and stays a NaN in either branch; an infinity takes the second)
-  if (__all_sync(0xffffffffu, ax <= 0.75f)) {
-    // tanh(x) = x p(x^2), |x| <= 0.75: least maximum error, fitted in 64 bits
-    const f32x2 a1 = pack2(-0.3333330750465393f, -0.3333330750465393f), a2 = pack2(0.13332609832286835f, 0.13332609832286835f),
-                a3 = pack2(-0.05388793721795082f, -0.05388793721795082f), a4 = pack2(0.021438755095005035f, 0.021438755095005035f),
-                a5 = pack2(-0.0076394579373300076f, -0.0076394579373300076f),
-                a6 = pack2(0.0017277069855481386f, 0.0017277069855481386f), one = pack2(1.f, 1.f), cap2 = pack2(cap, cap);
+  if (__all_sync(0xffffffffu, ax <= 0.6f)) {
+    // cap tanh(c s) = s q(s^2), |c s| <= 0.6: the polynomial of least maximum error for tanh(x) / x in x^2 (fitted
+    // in 64 bits, relative error 8e-8), its coefficients scaled by cap and the powers of c
+    f32x2 q[kParts][5];
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+      const float u = c[k] * c[k];
+      float w = cap * c[k];
+      const float a[5] = {0.9999999403953552f, -0.3333234488964081f, 0.13310648500919342f, -0.052122555673122406f,
+                          0.015504649840295315f};
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const float x = a[i] * w;
+        q[k][i] = pack2(x, x);
+        w *= u;
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kHalf; j += 2) {
-      const f32x2 ck = pack2(c[j >> 4], c[j >> 4]);
-      const f32x2 x = mul2(pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), ck);
+      const f32x2 (&a)[5] = q[j >> 4];
+      const f32x2 x = pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
       const f32x2 u = mul2(x, x);
-      f32x2 t = fma2(u, a6, a5);
-      t = fma2(u, t, a4);
-      t = fma2(u, t, a3);
-      t = fma2(u, t, a2);
-      t = fma2(u, t, a1);
-      t = fma2(u, t, one);
-      const float2 z = unpack2(mul2(mul2(x, cap2), t));
+      f32x2 t = fma2(u, a[4], a[3]);
+      t = fma2(u, t, a[2]);
+      t = fma2(u, t, a[1]);
+      t = fma2(u, t, a[0]);
+      const float2 z = unpack2(mul2(x, t));
       sr[j] = __float_as_uint(z.x);
       sr[j + 1] = __float_as_uint(z.y);
     }
