@@ -61,7 +61,9 @@
 // (softmax_modified): eight warps instead of four. With one warp on each scheduler the plain role is a
 // chain of latencies that already sets the pace of a tile; 64 more multiplications a thread took a 16-row
 // window from 121 to 146 us, and a cap to 211. Two warps share 32 rows, 32 columns of S each, and swap
-// their half maxima through shared memory (bounded waits, like every other). They add:
+// their half maxima through shared memory (bounded waits, like every other). P_lo of an fp8 window is E5M2 there (A and
+// B of kind::f8f6f4 may differ): each weight is held to 2^-8 down to 2^-6, and no floor but 2^-14 needs a budget.
+// They add:
 //  * block scales: with c_k the scale of a K block folded into the score's own factor, and log2 of a V
 //    block's scale added to the exponent, P' = 2^(z + log2 v_scale - m) enters the product as any weight
 //    does, and the row's sum takes each 16-column part of P' divided by its V scale. So P' keeps its terms'
@@ -104,6 +106,9 @@ constexpr int kAtomBytes = kMmaN * 128;   // one 128-byte-wide swizzle column of
 // tile's max passes m + kF8Hi (p <= 2^8.75 = 430, below 448, the largest E4M3), down only while
 // the gathered weight stays <= 2^40
 constexpr float kF8Hi = 8.75f, kF8Mid = 5.f, kF8MaxWeight = 1099511627776.f;
+// the modified role, whose P_lo is E5M2: m sits kModMid below a tile's max after a move (further down than the
+// plain role's, records of a row's scores pass 8.75 less often; the floors, 2^-14 a weight at most, allow it)
+constexpr float kModMid = 6.f, kModFloor = 6.103515625e-05f;
 
 template <int D, bool F8, int X = 0>
 struct MmaCfg {
@@ -313,6 +318,13 @@ __device__ __forceinline__ uint32_t e4m3x2_rn(float a, float b) {
   return r;
 }
 
+// The same to E5M2.
+__device__ __forceinline__ uint32_t e5m2x2_rn(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
 // x = hi + lo exactly, hi = x rounded to nearest with 4 significant bits (Veltkamp's splitting with
 // the factor 2^20 + 1 on 24-bit significands; no operation may be fused or reordered, hence the _rn
 // intrinsics). x of an E4M3 term: |x| <= 2^8, far from overflow.
@@ -336,9 +348,8 @@ __device__ __forceinline__ void p_terms4(const float* pv, uint32_t& wh, uint32_t
 // Q tile's 128-byte-swizzled K-major atoms: Q_hi atoms first, then Q_lo. Rows past the last vector
 // are zero; a vector holding NaN or infinity gets NaN codes. Returns 2^-e, which the row's scores
 // take back.
-// kParts threads share a row: thread `part` of them writes its share of the columns.
-template <int D, int kParts = 1>
-__device__ __forceinline__ float q_to_e4m3_terms(const DecodeParams& p, const MmaUnit& mu, int row, char* q_s, int part = 0) {
+template <int D>
+__device__ __forceinline__ float q_to_e4m3_terms(const DecodeParams& p, const MmaUnit& mu, int row, char* q_s) {
   const int G = p.group;
   const int vq = mu.mt * kMmaM + row;
   const bool ok = vq < p.rows * G;
@@ -369,7 +380,7 @@ __device__ __forceinline__ float q_to_e4m3_terms(const DecodeParams& p, const Mm
   char* row_hi = q_s + row * 128;
   char* row_lo = q_s + (D / 128) * (kMmaM * 128) + row * 128;
 #pragma unroll 2
-  for (int c = part * (D / 16 / kParts); c < (part + 1) * (D / 16 / kParts); ++c) {   // 16 elements: one 16-byte chunk of each term
+  for (int c = 0; c < D / 16; ++c) {   // 16 elements: one 16-byte chunk of each term
     uint4 ph = make_uint4(0u, 0u, 0u, 0u), pl = ph;
     if (ok) {
       const uint4 v0 = __ldg(src + 2 * c), v1 = __ldg(src + 2 * c + 1);
@@ -400,21 +411,35 @@ struct TileScales {
   float k[kParts], v[kParts];
   // in_page: the first column's position in its page
   __device__ __forceinline__ void load(const DecodeParams& p, const MmaUnit& mu, int in_page, int page) {
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) k[i] = v[i] = 1.f;
+    k[0] = v[0] = k[1] = v[1] = 1.f;
     if (page < 0 || page >= p.num_pages || mu.nothing) return;
-    const int64_t base = (static_cast<int64_t>(page) * p.h_kv + mu.h) * (p.page_tokens >> p.scale_shift);
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) {
-      const int64_t at = base + ((in_page + 16 * i) >> p.scale_shift);
-      k[i] = p.k_scales[at];
-      v[i] = p.v_scales[at];
-    }
+    const int64_t at = (static_cast<int64_t>(page) * p.h_kv + mu.h) * (p.page_tokens >> p.scale_shift) +
+                       (in_page >> p.scale_shift);
+    k[0] = p.k_scales[at];
+    v[0] = p.v_scales[at];
+    // 32 columns from a multiple of 32 on lie in one block, or, with 16 positions a scale, in two
+    const int next = p.scale_shift == 4 ? 1 : 0;
+    k[1] = p.k_scales[at + next];
+    v[1] = p.v_scales[at + next];
   }
 };
+static_assert(kParts == 2, "TileScales");
+
+// log2 and 1 / x with the hardware's approximations (to 2^-22 and 2^-23)
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// a scale in [2^-48, 2^48], by its bits (a negative number, an infinity or a NaN is none)
+__device__ __forceinline__ bool scale_fits(float s) {
+  return __float_as_uint(s) - __float_as_uint(kMinScale) <= __float_as_uint(kMaxScale) - __float_as_uint(kMinScale);
+}
 
 // Capped scores in log2 units, cap * tanh(s * c / cap): sr[j] raw in, z out. c: each part's factor from a raw
 // score to s / cap.
+// kOne: the parts' factors are one.
+template <bool kOne>
 __device__ __forceinline__ void cap_scores(uint32_t (&sr)[kHalf], const float (&c)[kParts], float cap) {
   float ax = 0.f;
 #pragma unroll
@@ -428,31 +453,27 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[kHalf], const float (&
   }
   // (a NaN is passed over by fmaxf, and stays a NaN in either branch; an infinity takes the second)
   if (__all_sync(0xffffffffu, ax <= 0.6f)) {
-    // cap tanh(c s) = s q(s^2), |c s| <= 0.6: the polynomial of least maximum error for tanh(x) / x in x^2 (fitted
-    // in 64 bits, relative error 8e-8), its coefficients scaled by cap and the powers of c
-    f32x2 q[kParts][5];
+    // cap tanh(x) = x q(x^2), |x| <= 0.6: the polynomial of least maximum error for tanh(x) / x in x^2, fitted in 64
+    // bits, relative error 8e-8. With one factor for all columns it goes into the coefficients, q in s itself.
+    const float u1 = kOne ? c[0] * c[0] : 1.f;
+    float w = kOne ? cap * c[0] : cap;
+    const float a[5] = {0.9999999403953552f, -0.3333234488964081f, 0.13310648500919342f, -0.052122555673122406f,
+                        0.015504649840295315f};
+    f32x2 q[5];
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) {
-      const float u = c[k] * c[k];
-      float w = cap * c[k];
-      const float a[5] = {0.9999999403953552f, -0.3333234488964081f, 0.13310648500919342f, -0.052122555673122406f,
-                          0.015504649840295315f};
-#pragma unroll
-      for (int i = 0; i < 5; ++i) {
-        const float x = a[i] * w;
-        q[k][i] = pack2(x, x);
-        w *= u;
-      }
+    for (int i = 0; i < 5; ++i) {
+      q[i] = pack2(a[i] * w, a[i] * w);
+      w *= u1;
     }
 #pragma unroll
     for (int j = 0; j < kHalf; j += 2) {
-      const f32x2 (&a)[5] = q[j >> 4];
-      const f32x2 x = pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
+      f32x2 x = pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
+      if constexpr (!kOne) x = mul2(x, pack2(c[j >> 4], c[j >> 4]));
       const f32x2 u = mul2(x, x);
-      f32x2 t = fma2(u, a[4], a[3]);
-      t = fma2(u, t, a[2]);
-      t = fma2(u, t, a[1]);
-      t = fma2(u, t, a[0]);
+      f32x2 t = fma2(u, q[4], q[3]);
+      t = fma2(u, t, q[2]);
+      t = fma2(u, t, q[1]);
+      t = fma2(u, t, q[0]);
       const float2 z = unpack2(mul2(x, t));
       sr[j] = __float_as_uint(z.x);
       sr[j + 1] = __float_as_uint(z.y);
@@ -464,6 +485,62 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[kHalf], const float (&
       sr[j] = __float_as_uint(fmaf(-2.f * cap, fast_rcp(1.f + e), cap));
     }
   }
+}
+
+// The same terms by two threads a row, each of half of the vector. (Held in registers between its two passes it
+// spilled: 187 against 181 us for the 128-row chunk.) `swap` gives the other half's largest element. Returns 2^-e, or a negative number if a
+// wait ran out.
+template <int D, class Swap>
+__device__ __forceinline__ float q_to_e4m3_terms_half(const DecodeParams& p, const MmaUnit& mu, int row, int half, char* q_s,
+                                                      Swap& swap) {
+  const int G = p.group;
+  const int vq = mu.mt * kMmaM + row;
+  const bool ok = vq < p.rows * G;
+  const int r = ok ? vq / G : 0, gq = ok ? vq - r * G : 0;
+  const uint4* src = reinterpret_cast<const uint4*>(
+      static_cast<const char*>(p.q) +
+      (((static_cast<int64_t>(mu.b) * p.rows + r) * p.h_q) + static_cast<int64_t>(mu.h) * G + gq) * (D * 2) + half * D);
+  float amax = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < D / 16; ++c) {
+    const uint4 v = ok ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = bf16x2_to_float2(w[i]);
+      amax = max_nan(amax, max_nan(fabsf(f.x), fabsf(f.y)));
+    }
+  }
+  float2 other;
+  if (!swap(make_float2(amax, 0.f), other)) return -1.f;
+  amax = max_nan(amax, other.x);
+  const bool bad = !(amax <= 3.402823466e38f);   // NaN or infinity in the vector
+  int e = 0;
+  if (!bad && amax > 0.f) {
+    const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu) - 127;   // floor(log2 amax), normal amax
+    e = min(120, max(-120, 7 - ex));
+  }
+  const float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);   // 2^e
+  char* row_hi = q_s + row * 128;
+  char* row_lo = q_s + (D / 128) * (kMmaM * 128) + row * 128;
+#pragma unroll 2
+  for (int c = 0; c < D / 32; ++c) {   // 16 elements: one 16-byte chunk of each term
+    const uint4 v0 = ok ? __ldg(src + 2 * c) : make_uint4(0u, 0u, 0u, 0u), v1 = ok ? __ldg(src + 2 * c + 1) : make_uint4(0u, 0u, 0u, 0u);
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = bf16x2_to_float2(w[2 * i]), b = bf16x2_to_float2(w[2 * i + 1]);
+      const float x[4] = {__fmul_rn(a.x, sc), __fmul_rn(a.y, sc), __fmul_rn(b.x, sc), __fmul_rn(b.y, sc)};
+      p_terms4(x, hw[i], lw[i]);
+    }
+    const int cc = half * (D / 32) + c, a = cc >> 3;   // 128-byte atom and its 16-byte chunk
+    const int off = a * (kMmaM * 128) + (((cc & 7) ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(row_hi + off) =
+        bad ? make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu) : make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    *reinterpret_cast<uint4*>(row_lo + off) = bad ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(lw[0], lw[1], lw[2], lw[3]);
+  }
+  return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 }
 
 // The softmax role of a modified decode (warps 0-3 and 8-11): thread = one query vector (TMEM lane) and half
@@ -508,7 +585,8 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
   float q_inv = 1.f;   // fp8 pools: 2^-e of this thread's query vector in the unit's Q terms
   if constexpr (F8) {
     if (!it.done) {
-      q_inv = q_to_e4m3_terms<D, 2>(p, it.mu, row, q_s, half);
+      q_inv = q_to_e4m3_terms_half<D>(p, it.mu, row, half, q_s, swap);
+      if (__any_sync(0xffffffffu, q_inv < 0.f)) return false;
       fence_proxy_async();   // the terms are read by the tensor pipe (async proxy)
       mbar_arrive(q_full);
     }
@@ -565,15 +643,21 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
         if (t + 1 < mu.tiles) ts_next.load(p, mu, in_page, next);
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
-          const bool fit = ts.k[k] >= kMinScale && ts.k[k] <= kMaxScale && ts.v[k] >= kMinScale && ts.v[k] <= kMaxScale;
-          // a block that no row sees does not count, whatever its scale
-          if (!fit && n0 + 16 * k < mu.end && n0 + 16 * k + 16 > mu.lo && lane == 0 && quarter == 0)
-            raise_status(p.status, NBX_DEV_BAD_SCALE);
+          const bool fit = scale_fits(ts.k[k]) && scale_fits(ts.v[k]);
+          ck[k] *= ts.k[k];
+          lv[k] = fast_log2(ts.v[k]);
+          iv[k] = fast_rcp(ts.v[k]);
           if (!fit) bad_blocks |= 1u << k;
-          if (fit) {
-            ck[k] *= ts.k[k];
-            lv[k] = __log2f(ts.v[k]);
-            iv[k] = __frcp_rn(ts.v[k]);
+        }
+        if (bad_blocks) {   // every thread of the warp alike
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) {
+            if (!((bad_blocks >> k) & 1u)) continue;
+            ck[k] = iv[k] = 1.f;
+            lv[k] = 0.f;
+            // a block that no row sees does not count, whatever its scale
+            if (n0 + 16 * k < mu.end && n0 + 16 * k + 16 > mu.lo && lane == 0 && quarter == 0)
+              raise_status(p.status, NBX_DEV_BAD_SCALE);
           }
         }
       }
@@ -591,7 +675,7 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
             float cx[kParts];
 #pragma unroll
             for (int k = 0; k < kParts; ++k) cx[k] = ck[k] * p.cap_inv;
-            cap_scores(sr, cx, p.cap_log2);
+            cap_scores<!kBlk>(sr, cx, p.cap_log2);
 #pragma unroll
             for (int k = 0; k < kParts; ++k) ck[k] = 1.f;
           }
@@ -636,7 +720,7 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       if constexpr (F8) w_run += w_half + other.y;   // the weight through the last tile
       // a NaN running max stays NaN (a later tile the row cannot see, max -inf, must not replace it)
       const bool grow = !(mx <= m_run + (F8 ? kF8Hi : kMmaTau)) && m_run == m_run;
-      float m_new = grow ? (F8 ? mx - kF8Mid : mx) : m_run;
+      float m_new = grow ? (F8 ? mx - kModMid : mx) : m_run;
       float f = grow ? fast_exp2(m_run - m_new) : 1.f;
       const float nm = (m_new == -INFINITY) ? 0.f : -m_new;   // all scores -inf: p = 0
       float part[kParts][2];   // two chains a part
@@ -649,30 +733,33 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
           pv[j] = fast_exp2(fmaf(__uint_as_float(sr[j]), ck[j >> 4], nm + lv[j >> 4]));
           part[j >> 4][j & 1] += pv[j];
         }
-        // The budget of the E4M3 terms' floors, as the plain role keeps it (each weight below 2^-1 is off by at
-        // most 2^-9, in all at most 2^-8 of the weight gathered). The first test takes what both threads of
-        // the row know, the tile's largest weight for its sum, and only a row that fails it has its sums and
-        // its counts of small weights exchanged and looked at.
+        // P_lo in E5M2 leaves a weight of 2^-6 and more off by at most 2^-8 of itself, a smaller one by at most
+        // 2^-14 and 2^-4 of itself. Those floors are kept within 2^-8 of the weight gathered. The first test takes
+        // what both threads of the row know: the tile's largest weight, of which no floor is more than 2^-4, and
+        // for the tile's sum. Only a row that fails it has its floors summed and exchanged, and if they do not
+        // fit, m moves down to the tile (at the start of a row's keys, if at all).
+        // (With P_lo in E4M3, as the plain role has it, the floors are 2^-9 and such rows the rule wherever some
+        // scores stand far above the rest: m moved, and O was rescaled behind its last PV, in 91 % of the tiles
+        // of a chunk with keys of uneven size, 181 us; now in a third of them.)
         const int vis_all = tile_ok ? max(0, min(kMmaN - 1, last_key - (n0 - half * kHalf)) -
                                                max(0, kMod ? first_key - (n0 - half * kHalf) : 0) + 1)
                                     : 0;
-        float e_tile = 0.001953125f * static_cast<float>(vis_all);
-        const bool tight = mx > -INFINITY && e_run * f + e_tile > 0.00390625f * (w_run * f + fast_exp2(mx - m_new));
+        const float top = mx > -INFINITY ? fast_exp2(mx - m_new) : 0.f;   // (NaN: passes no comparison below)
+        float e_tile = static_cast<float>(vis_all) * fminf(kModFloor, 0.0625f * top);
+        const bool tight = e_run * f + e_tile > 0.00390625f * (w_run * f + top);
         if (__any_sync(0xffffffffu, tight)) {
-          uint32_t n = 0;   // weights below 2^-1, zeros among them
+          float floors = 0.f, w_t = 0.f;
 #pragma unroll
-          for (int j = 0; j < kHalf; ++j) n += (__float_as_uint(pv[j]) - 0x3F000000u) >> 31;
-          float w_t = 0.f;
+          for (int j = 0; j < kHalf; ++j) floors += pv[j] < 0.015625f ? fminf(0.0625f * pv[j], kModFloor) : 0.f;
 #pragma unroll
           for (int k = 0; k < kParts; ++k) w_t += part[k][0] + part[k][1];
-          if (!swap(make_float2(w_t, static_cast<float>(n)), other)) return false;
+          if (!swap(make_float2(w_t, floors), other)) return false;
           const float budget = 0.00390625f * (w_run * f + (w_t + other.x));
           if (tight) {
-            const int small = static_cast<int>(n) + static_cast<int>(other.y) - (kMmaN - vis_all);
-            e_tile = 0.001953125f * static_cast<float>(max(0, small));
-            const float fd = fast_exp2(m_new - (mx - kF8Mid));
+            e_tile = floors + other.y;
+            const float fd = fast_exp2(m_new - (mx - kModMid));
             if (e_run * f + e_tile > budget && fd > 1.f && w_run * f * fd <= kF8MaxWeight) {
-              m_new = mx - kF8Mid;
+              m_new = mx - kModMid;
               f *= fd;
 #pragma unroll
               for (int j = 0; j < kHalf; ++j) pv[j] *= fd;
@@ -681,15 +768,21 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
                 part[k][0] *= fd;
                 part[k][1] *= fd;
               }
-              e_tile = 0.001953125f * static_cast<float>(vis_all);   // <= 2^-8 * 2^kF8Mid
+              e_tile = static_cast<float>(vis_all) * kModFloor;   // <= 2^-8 * 2^kModMid
             }
           }
         }
         e_run = e_run * f + e_tile;
-        // E4M3 terms (split4), four codes a column: P_hi over S columns [0, 16), P_lo over [16, 32)
+        // P_hi in E4M3 and what it leaves in E5M2, four codes a column: over S columns [0, 16) and [16, 32)
         uint32_t wh[kHalf / 4], wl[kHalf / 4];
 #pragma unroll
-        for (int i = 0; i < kHalf / 4; ++i) p_terms4(pv + 4 * i, wh[i], wl[i]);
+        for (int i = 0; i < kHalf / 4; ++i) {
+          const float* x = pv + 4 * i;
+          const uint32_t h01 = e4m3x2_rn(x[0], x[1]), h23 = e4m3x2_rn(x[2], x[3]);
+          const float2 a = e4m3x2_to_float2(h01), b = e4m3x2_to_float2(h23);
+          wh[i] = h01 | (h23 << 16);
+          wl[i] = e5m2x2_rn(x[0] - a.x, x[1] - a.y) | (e5m2x2_rn(x[2] - b.x, x[3] - b.y) << 16);
+        }
         tmem_st8(lane_base + sbuf + half * (kHalf / 4), wh);
         tmem_st8(lane_base + sbuf + kMmaN / 4 + half * (kHalf / 4), wl);
       } else {
@@ -758,7 +851,8 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
     if constexpr (F8) {
       // the next unit's Q terms: every QK^T of this unit has completed (its last S was read)
       if (it.has_next) {
-        q_inv_next = q_to_e4m3_terms<D, 2>(p, it.next_mu(), row, q_s, half);
+        q_inv_next = q_to_e4m3_terms_half<D>(p, it.next_mu(), row, half, q_s, swap);
+        if (__any_sync(0xffffffffu, q_inv_next < 0.f)) return false;
         fence_proxy_async();
         mbar_arrive(q_full);
       }
@@ -1127,6 +1221,7 @@ __global__ void __launch_bounds__(X ? kMmaThreadsMod : kMmaThreads, 1)
       // ring slots (even ring ordinals, an even ring length), so their four 64-column atoms are
       // 8 KB apart throughout
       constexpr uint32_t kIdescO = mma_idesc(kMmaM, D, true, F8);   // bf16, or E4M3 (format 0)
+      constexpr uint32_t kIdescLo = F8 && X ? kIdescO | kIdescAE5M2 : kIdescO;   // a modified role's P_lo is E5M2
       constexpr int kStep = F8 ? 32 : 16;                           // positions of one MMA's K
       TileIter<kMod> it;
       it.begin(p, m_tiles, n_units, HI);
@@ -1162,7 +1257,7 @@ __global__ void __launch_bounds__(X ? kMmaThreadsMod : kMmaThreads, 1)
               const uint32_t acol = pcol + part * (F8 ? kMmaN / 4 : kMmaN / 2) + kk * 8;
               const uint64_t bd = smem_desc(vb + kk * (kStep * 128), kAtomBytes, 1024);
               const bool acc = !(it.t == 0 && part == 0 && kk == 0);
-              if constexpr (F8) tc_mma_ts_f8(tmem + C::kOCol, acol, bd, kIdescO, acc);
+              if constexpr (F8) tc_mma_ts_f8(tmem + C::kOCol, acol, bd, part ? kIdescLo : kIdescO, acc);
               else tc_mma_ts(tmem + C::kOCol, acol, bd, kIdescO, acc);
             }
           }

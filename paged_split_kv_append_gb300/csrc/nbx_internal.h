@@ -258,7 +258,7 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
 bool mma_path_applies(const DecodeParams& p, int q_dtype, int pool_dtype);
 constexpr int kMmaRowsPerTile = 128;   // query vectors of one M tile of the tensor-core kernel
 cudaError_t decode_dispatch_mma(const DecodeParams& p, int pool_dtype, int grid_limit, cudaStream_t stream);
-// The same for modified decodes. An E4M3 window holds P to 2^-9, which only a bf16 output may take.
+// The same for modified decodes. An E4M3 window holds P to 2^-8, which only a bf16 output may take.
 bool mma_path_applies_modified(const DecodeParams& p, int q_dtype, int pool_dtype);
 cudaError_t decode_dispatch_mma_mod(const DecodeParams& p, int pool_dtype, int grid_limit, cudaStream_t stream);
 cudaError_t decode_dispatch_mma_block(const DecodeParams& p, bool mod, int grid_limit, cudaStream_t stream);

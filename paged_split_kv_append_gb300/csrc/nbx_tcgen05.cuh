@@ -147,6 +147,8 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
 // and 10-12 = 1) or both f16 (0), A K-major or MN-major (bit 15), B K-major or MN-major (bit 16),
 // N >> 3 in bits 17-22, M >> 4 in bits 24-28. With kind::f8f6f4 the same formats field 0 means
 // E4M3 for both operands.
+// kind::f8f6f4 takes A and B of different 8-bit formats: this makes A's (bits 7-9) E5M2 (1) instead of E4M3 (0).
+constexpr uint32_t kIdescAE5M2 = 1u << 7;
 __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool b_mn_major, bool f16 = false,
                                                  bool a_mn_major = false) {
   const uint32_t fmt = f16 ? 0u : 1u;

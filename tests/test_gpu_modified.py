@@ -6,8 +6,8 @@ of four, the scale, the block's scale), so it is off by 2^-20 Z, Z = scale |q| |
 cap or a bias adds less. Sums of weights and of weighted values are fp32, at most 512 terms in a row and 64
 splits, hence 2^-14.8 in the worst case. The output is a weighted mean of the values, off by twice the
 weights' error times the largest value: max|v| (2^-19 Z + 2^-14). On tensor cores a bf16 window holds P to
-2^-17 (two bf16 terms), and an E4M3 window P to 2^-9 (two E4M3 terms, with the floors of small weights
-within 2^-8 of the sum) and each element of q to 2^-16 of the vector's largest, so a score to
+2^-17 (two bf16 terms), and an E4M3 window P to 2^-8 (an E4M3 term and an E5M2 one: a rounding to four bits
+leaves 2^-4, its rounding to three 2^-4 of that; with the floors of small weights within 2^-8 of the sum) and each element of q to 2^-16 of the vector's largest, so a score to
 2^-16 sqrt(d) Z. A bf16 output adds half a step: 2^-8.
 """
 
@@ -344,7 +344,7 @@ TENSOR = [("bf16", 16, 24, 4, 256, 64, 0), ("bf16", 8, 32, 4, 128, 128, 0), ("bf
           ("block", 8, 32, 4, 128, 64, 16), ("block", 40, 4, 1, 128, 128, 128), ("block", 130, 2, 2, 256, 128, 32),
           ("bf16", 128, 2, 1, 128, 512, 0)]
 WINDOW_LENS = (0, 1, 17, 63, 64, 65, 129, 300, 513, 1100)
-P_WEIGHT = {"bf16": 2.0 ** -17, "e4m3": 2.0 ** -9 + 2.0 ** -8, "block": 2.0 ** -9 + 2.0 ** -8}
+P_WEIGHT = {"bf16": 2.0 ** -17, "e4m3": 2.0 ** -7, "block": 2.0 ** -7}
 
 
 def on_tensor_cores(c, out_type):
