@@ -406,24 +406,17 @@ __device__ __forceinline__ float q_to_e4m3_terms(const DecodeParams& p, const Mm
 constexpr int kHalf = kMmaN / 2;   // columns of S of one softmax thread of a modified decode
 constexpr int kParts = kHalf / 16;  // 16-position parts of them, each of one block of scales
 
-// The scales of a thread's parts of a tile.
-struct TileScales {
-  float k[kParts], v[kParts];
-  // in_page: the first column's position in its page
-  __device__ __forceinline__ void load(const DecodeParams& p, const MmaUnit& mu, int in_page, int page) {
-    k[0] = v[0] = k[1] = v[1] = 1.f;
-    if (page < 0 || page >= p.num_pages || mu.nothing) return;
-    const int64_t at = (static_cast<int64_t>(page) * p.h_kv + mu.h) * (p.page_tokens >> p.scale_shift) +
-                       (in_page >> p.scale_shift);
-    k[0] = p.k_scales[at];
-    v[0] = p.v_scales[at];
-    // 32 columns from a multiple of 32 on lie in one block, or, with 16 positions a scale, in two
-    const int next = p.scale_shift == 4 ? 1 : 0;
-    k[1] = p.k_scales[at + next];
-    v[1] = p.v_scales[at + next];
-  }
-};
-static_assert(kParts == 2, "TileScales");
+// The scales of a warp's half of a tile: lane l < 4 holds K's (l < 2) or V's scale of part l & 1. (Every thread with
+// all four, and the numbers it needs of them, took 300 cycles more a tile.) in_page: the half's position in its
+// page; its 32 columns, from a multiple of 32 on, lie in one block, or, with 16 positions a scale, in two.
+__device__ __forceinline__ float tile_scale(const DecodeParams& p, const MmaUnit& mu, int in_page, int page) {
+  const int lane = threadIdx.x & 31;
+  if (lane >= 2 * kParts || page < 0 || page >= p.num_pages || mu.nothing) return 1.f;
+  const int64_t at = (static_cast<int64_t>(page) * p.h_kv + mu.h) * (p.page_tokens >> p.scale_shift) +
+                     ((in_page + 16 * (lane & 1)) >> p.scale_shift);
+  return (lane < kParts ? p.k_scales : p.v_scales)[at];
+}
+static_assert(kParts == 2, "tile_scale");
 
 // log2 and 1 / x with the hardware's approximations (to 2^-22 and 2^-23)
 __device__ __forceinline__ float fast_log2(float x) {
@@ -614,11 +607,11 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
     // fp8: the sum of P' (of P, without block scales) over the row and the bound on its terms' floor errors,
     // both through the last tile but for its sums, which follow with the next exchange
     float w_run = 0.f, w_half = 0.f, e_run = 0.f;
-    TileScales ts_next;
+    float ts_next = 1.f;
     int in_page = 0;   // kBlk: position in its page of the next tile's first column, stepped without a division
     if constexpr (kBlk) {
       in_page = mu.start % p.page_tokens + half * kHalf;
-      ts_next.load(p, mu, in_page, __shfl_sync(0xffffffffu, pg_cur, 0));
+      ts_next = tile_scale(p, mu, in_page, __shfl_sync(0xffffffffu, pg_cur, 0));
     }
     uint32_t pb = 0, pp = 0;   // buffer and phase count of the previous tile
     for (int t = 0; t < mu.tiles; ++t) {
@@ -636,18 +629,19 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       }
       uint32_t bad_blocks = 0;
       if constexpr (kBlk) {
-        const TileScales ts = ts_next;
+        const float ts = ts_next;
         const int next = __shfl_sync(0xffffffffu, pg_cur, (t + 1) & 31);
         in_page += kMmaN;
         if (in_page >= p.page_tokens) in_page = half * kHalf;
-        if (t + 1 < mu.tiles) ts_next.load(p, mu, in_page, next);
+        if (t + 1 < mu.tiles) ts_next = tile_scale(p, mu, in_page, next);
+        const float lg = fast_log2(ts), rc = fast_rcp(ts);
+        const uint32_t unfit = __ballot_sync(0xffffffffu, !scale_fits(ts));
+        bad_blocks = (unfit | (unfit >> kParts)) & 3u;
 #pragma unroll
         for (int k = 0; k < kParts; ++k) {
-          const bool fit = scale_fits(ts.k[k]) && scale_fits(ts.v[k]);
-          ck[k] *= ts.k[k];
-          lv[k] = fast_log2(ts.v[k]);
-          iv[k] = fast_rcp(ts.v[k]);
-          if (!fit) bad_blocks |= 1u << k;
+          ck[k] *= __shfl_sync(0xffffffffu, ts, k);
+          lv[k] = __shfl_sync(0xffffffffu, lg, kParts + k);
+          iv[k] = __shfl_sync(0xffffffffu, rc, kParts + k);
         }
         if (bad_blocks) {   // every thread of the warp alike
 #pragma unroll
