@@ -5,7 +5,12 @@ and V pools, the block table and lengths, the step's queries and new tokens, the
 decode workspace, the output and the status word. ``step()`` is one pass of the hot
 path through the C ABI: ``nbx_paged_kv_append`` writes the step's new positions into
 the pools, then ``nbx_paged_decode_attn`` computes attention for every query row.
-Nothing here computes: torch provides memory and streams only.
+
+With ``scale_tokens`` the pools are a block-scaled cache (E4M3 codes, a scale per block of tokens and
+head), appended to by ``nbx_paged_kv_append_block_scaled`` and read by
+``nbx_paged_decode_attn_block_scaled``; with score modifications (``set_modifications``) a decode is
+``nbx_paged_decode_attn_modified``. ``fork`` and ``compact`` manage the rows and pages of the block table
+in place. Nothing here computes: torch provides memory and streams only.
 """
 
 from __future__ import annotations
@@ -14,8 +19,11 @@ from typing import Optional
 
 import torch
 
-from . import (NBX_BF16, NBX_E4M3, NBX_F32, nbx_paged_decode_attn, nbx_paged_decode_workspace_bytes_for,
-               nbx_paged_kv_append)
+from . import (NBX_BF16, NBX_E4M3, NBX_F32, nbx_paged_decode_attn, nbx_paged_decode_attn_block_scaled,
+               nbx_paged_decode_attn_modified, nbx_paged_decode_modified_workspace_bytes,
+               nbx_paged_decode_workspace_bytes_for, nbx_paged_kv_append, nbx_paged_kv_append_block_scaled,
+               nbx_paged_kv_compact, nbx_paged_kv_compact_workspace_bytes, nbx_paged_kv_fork,
+               nbx_paged_kv_fork_workspace_bytes)
 
 POOL_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.uint8}
 
@@ -32,7 +40,11 @@ def new_pool(num_pages: int, h_kv: int, page_tokens: int, d: int, dtype: str, de
 
 class PagedDecodeSession:
     def __init__(self, *, num_pages: int, h_kv: int, page_tokens: int, d: int, pool_dtype: str, batch: int,
-                 rows: int, h_q: int, max_seq_len: int, device, fill_nan: bool = True, q_dtype: str = "bf16"):
+                 rows: int, h_q: int, max_seq_len: int, device, fill_nan: bool = True, q_dtype: str = "bf16",
+                 scale_tokens: int = 0, modified: bool = False, out_dtype: torch.dtype = torch.float32):
+        """scale_tokens: positions per scale of a block-scaled cache (pool_dtype "e4m3"), 0 for one scale per
+        pool. modified: size the workspace for score modifications. out_dtype: fp32, or bf16 for a session that is
+        block-scaled or modified."""
         self.device = torch.device(device)
         self.num_pages, self.h_kv, self.page_tokens, self.d = num_pages, h_kv, page_tokens, d
         self.pool_dtype = pool_dtype
@@ -40,16 +52,31 @@ class PagedDecodeSession:
         self.k_pool = new_pool(num_pages, h_kv, page_tokens, d, pool_dtype, self.device, fill_nan)
         self.v_pool = new_pool(num_pages, h_kv, page_tokens, d, pool_dtype, self.device, fill_nan)
         codes = {"f32": NBX_F32, "bf16": NBX_BF16, "e4m3": NBX_E4M3}
+        if scale_tokens and (pool_dtype != "e4m3" or page_tokens % scale_tokens):
+            raise ValueError("scales belong to e4m3 pools, and a page holds a whole number of their blocks")
+        self.k_scales = self.v_scales = None
+        if scale_tokens:
+            shape = (num_pages, h_kv, page_tokens // scale_tokens)
+            self.k_scales = torch.ones(shape, dtype=torch.float32, device=self.device)
+            self.v_scales = torch.ones_like(self.k_scales)
+        self.modified = modified or scale_tokens > 0
+        if out_dtype != torch.float32 and not self.modified:
+            raise ValueError("a plain decode's output is fp32")
         ws = nbx_paged_decode_workspace_bytes_for(codes[q_dtype], codes[pool_dtype], batch, rows, h_q, h_kv, d,
                                                   max_seq_len, page_tokens)
+        if self.modified:
+            ws = nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len)
         if ws == 0 and batch > 0:
             raise ValueError("invalid decode sizes")
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
-        self.out = torch.empty((batch, rows, h_q, d), dtype=torch.float32, device=self.device)
+        self.out = torch.empty((batch, rows, h_q, d), dtype=out_dtype, device=self.device)
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.q = self.block_table = self.seq_lens = None
         self.new_k = self.new_v = self.new_slots = None
+        self.held = self.tok_start = None
         self.scale, self.k_scale, self.v_scale = 1.0, 1.0, 1.0
+        self.modifications = {}
+        self._page_workspace = None
 
     # ---------------------------------------------------------------- state
     def append(self, new_k: torch.Tensor, new_v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
@@ -86,15 +113,70 @@ class PagedDecodeSession:
         self.new_slots = None if new_slots is None else dev(new_slots, torch.int32)
         self.scale, self.k_scale, self.v_scale = float(scale), float(k_scale), float(v_scale)
 
+    def append_block_scaled(self, new_k: torch.Tensor, new_v: torch.Tensor, held: torch.Tensor,
+                            tok_start: torch.Tensor, stream=None) -> None:
+        """Rows tok_start[b] .. tok_start[b + 1] - 1 to positions held[b] and up of sequence b (a block-scaled
+        cache)."""
+        nbx_paged_kv_append_block_scaled(new_k, new_v, self.k_pool, self.v_pool, self.k_scales, self.v_scales,
+                                         self.block_table, held, tok_start, status=self.status, stream=stream)
+
+    def set_new_tokens(self, new_k: torch.Tensor, new_v: torch.Tensor, held, tok_start) -> None:
+        """The tokens a step of a block-scaled session appends; host arrays are copied to the device once."""
+        def dev(x):
+            return torch.as_tensor(x).to(torch.int32).to(self.device).contiguous()
+        self.new_k, self.new_v = new_k.to(self.device).contiguous(), new_v.to(self.device).contiguous()
+        self.held, self.tok_start = dev(held), dev(tok_start)
+
+    def set_modifications(self, softcap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                          key_begin: Optional[torch.Tensor] = None, key_end: Optional[torch.Tensor] = None) -> None:
+        """The score modifications of the decodes from here on (device tensors)."""
+        if not self.modified:
+            raise ValueError("the session was not made for score modifications")
+        self.modifications = dict(softcap=softcap, slopes=slopes, key_begin=key_begin, key_end=key_end)
+
+    # ---------------------------------------------------------------- rows and pages
+    def _page_scratch(self) -> torch.Tensor:
+        """The workspace of forks (of up to a row each) and compactions, kept."""
+        need = max(nbx_paged_kv_fork_workspace_bytes(*self.block_table.shape, self.batch, self.num_pages),
+                   nbx_paged_kv_compact_workspace_bytes(self.num_pages))
+        if self._page_workspace is None or self._page_workspace.numel() < need:
+            self._page_workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        return self._page_workspace
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
+        """Rows dst of the block table and the lengths become rows src as they were (int32 device tensors). Returns
+        (moves, n_moves)."""
+        return nbx_paged_kv_fork(self.block_table, self.seq_lens, src, dst, self.k_pool, self.v_pool, self.k_scales,
+                                 self.v_scales, workspace=self._page_scratch(), status=self.status, stream=stream)
+
+    def compact(self, stream=None):
+        """The pages in use move to the lowest ids, in the block table too. Returns (moves, {moves, pages in use})."""
+        return nbx_paged_kv_compact(self.block_table, self.seq_lens, self.k_pool, self.v_pool, self.k_scales,
+                                    self.v_scales, new_block_table=self.block_table, workspace=self._page_scratch(),
+                                    status=self.status, stream=stream)[1:]
+
     # ---------------------------------------------------------------- the step
     def decode(self, stream=None) -> torch.Tensor:
+        if self.k_scales is not None:
+            return nbx_paged_decode_attn_block_scaled(self.q, self.k_pool, self.v_pool, self.k_scales, self.v_scales,
+                                                      self.block_table, self.seq_lens, self.max_seq_len, self.scale,
+                                                      out=self.out, workspace=self.workspace, status=self.status,
+                                                      stream=stream, **self.modifications)
+        if self.modified:
+            return nbx_paged_decode_attn_modified(self.q, self.k_pool, self.v_pool, self.block_table, self.seq_lens,
+                                                  self.max_seq_len, self.scale, self.k_scale, self.v_scale,
+                                                  out=self.out, workspace=self.workspace, status=self.status,
+                                                  stream=stream, **self.modifications)
         return nbx_paged_decode_attn(self.q, self.k_pool, self.v_pool, self.block_table, self.seq_lens,
                                      self.max_seq_len, self.scale, self.k_scale, self.v_scale, out=self.out,
                                      workspace=self.workspace, status=self.status, stream=stream)
 
     def step(self, stream=None) -> torch.Tensor:
         """Append the step's new positions, then decode: one pass of the hot path."""
-        if self.new_k is not None and self.new_k.shape[0] > 0:
+        if self.k_scales is not None:
+            if self.new_k is not None:
+                self.append_block_scaled(self.new_k, self.new_v, self.held, self.tok_start, stream=stream)
+        elif self.new_k is not None and self.new_k.shape[0] > 0:
             self.append(self.new_k, self.new_v, self.new_slots, stream=stream)
         return self.decode(stream=stream)
 

@@ -209,3 +209,17 @@ def test_attention_definition_on_two_keys():
     w = np.exp(-5.0)
     assert abs(out[0, 1, 0, 0] - (w * 1 + 3) / (w + 1)) < 1e-12
     assert of.E4M3_MAX == 448.0
+
+
+# ------------------------------------------------------------------------- the session
+def test_session_refusals():
+    from paged_split_kv_append_gb300.session import PagedDecodeSession
+    sizes = dict(num_pages=2, h_kv=1, page_tokens=32, d=64, batch=1, rows=1, h_q=1, max_seq_len=32, device="cpu")
+    for bad in (dict(pool_dtype="bf16", scale_tokens=16), dict(pool_dtype="e4m3", scale_tokens=64),
+                dict(pool_dtype="bf16", out_dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            PagedDecodeSession(**sizes, **bad)
+    with pytest.raises(ValueError):
+        PagedDecodeSession(**sizes, pool_dtype="bf16").set_modifications(softcap=1.0)
+    s = PagedDecodeSession(**sizes, pool_dtype="e4m3", scale_tokens=16)
+    assert s.k_scales.shape == s.v_scales.shape == (2, 1, 2) and s.modified
