@@ -260,6 +260,7 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
     p.v_scales = mod->v_scales;
     while (mod->block_scaled && (1 << p.scale_shift) < mod->scale_tokens) ++p.scale_shift;
     p.ranges = reinterpret_cast<int2*>(ws + w.ranges);
+    p.order = reinterpret_cast<int32_t*>(ws + w.order);
     // an fp32 output without a modification is the plain decode's
     x = mod->block_scaled ? kBlockScaled | (scored ? kScoreMod : 0) : (scored || p.out_bf16 ? kScoreMod : 0);
   }

@@ -56,6 +56,8 @@ bool workspace_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq
   w->ranges = off;
   const size_t m_tiles = (static_cast<size_t>(rows) * (h_q / h_kv) + kMmaRowsPerTile - 1) / kMmaRowsPerTile;
   if (modified) off += up(static_cast<size_t>(batch) * m_tiles * sizeof(int2));
+  w->order = off;
+  if (modified) off += up(kOrderMax * 4);
   w->total = off;
   w->max_splits = static_cast<int>(S);
   w->row_blocks = static_cast<int>(rb);
@@ -110,7 +112,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     s_nb = 0;
     if constexpr (TC) s_total = 0;
     p.header[1] = 0;
-    if constexpr (X) p.header[2] = 0;   // set when a partial is to be recomputed
+    if constexpr (X) {
+      p.header[2] = 0;   // set when a partial is to be recomputed
+      p.header[3] = 0;   // set when the work is ordered
+    }
   }
   __syncthreads();
   if constexpr (X) {
@@ -330,6 +335,39 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     p.entries[e] = en;
   }
   if (tid == 0) p.header[0] = total;
+  // A window whose rows see their own keys: its M tiles differ in length, and a CTA takes one or two units of
+  // them. Most keys first, dealt to the CTAs there and back, the longest CTA of 512 rows of documents of up to
+  // 1500 positions (256 units) reads 31 tiles where it read 39.
+  if constexpr (TC && X) {
+    __shared__ int4 s_cost[kOrderMax / 4];
+    int* const cost = reinterpret_cast<int*>(s_cost);
+    const int64_t all = static_cast<int64_t>(total) * p.range_tiles;
+    if (ranges && !p.tc_round_up && all <= kOrderMax && all * p.h_kv > p.tc_units) {
+      const int items = static_cast<int>(all);
+      __syncthreads();   // orders the entries' global writes before this CTA's reads
+      for (int i = tid; i < (items + 3) / 4 * 4; i += kPlanThreads) {
+        int c = -1;
+        if (i < items) {
+          const Entry en = p.entries[i / p.range_tiles];
+          const int2 r = p.ranges[static_cast<int64_t>(en.b) * p.range_tiles + i % p.range_tiles];
+          c = max(0, min(en.end, r.y) - max(en.start, r.x));
+        }
+        cost[i] = c;
+      }
+      __syncthreads();
+      if (tid < items) {
+        const int c = cost[tid];
+        int rank = 0;
+        for (int i = 0; i < items; i += 4) {   // stable: ties keep their order
+          const int4 o = s_cost[i / 4];
+          rank += (o.x > c || (o.x == c && i < tid)) + (o.y > c || (o.y == c && i + 1 < tid)) +
+                  (o.z > c || (o.z == c && i + 2 < tid)) + (o.w > c || (o.w == c && i + 3 < tid));
+        }
+        p.order[rank] = tid;
+      }
+      if (tid == 0) p.header[3] = items;
+    }
+  }
   plan_finish(p);
 }
 

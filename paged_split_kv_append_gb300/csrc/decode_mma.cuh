@@ -197,7 +197,8 @@ __device__ __forceinline__ MmaUnit unit_from(const Entry& en, int2 seen, int u, 
   return m;
 }
 
-// Walks this CTA's tiles in order: units blockIdx.x, blockIdx.x + gridDim.x, ..., tiles of each.
+// Walks this CTA's tiles in order: units blockIdx.x, blockIdx.x + gridDim.x, ..., tiles of each; where the
+// plan ordered the work (kRanges), places of that order, every other round of the CTAs backwards.
 // Ring ordinals: tile tt of the current unit fills slots kbase + tt * hh .. + hh - 1 of the K ring
 // (and the same ordinals of the V ring). The next unit's work-list entry is loaded one unit ahead.
 template <bool kRanges>
@@ -214,6 +215,17 @@ struct TileIter {
   MmaUnit mu;
   Entry nx;
   int2 nseen;        // kRanges: the next unit's visible keys
+  int nu;            // kRanges: the next unit
+  bool ordered;
+  // the unit of round r, n_units or above if there is none
+  __device__ __forceinline__ int unit_of(const DecodeParams& p, uint32_t r) const {
+    const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    if (!ordered) return static_cast<int>(r) * g + c;
+    const int place = static_cast<int>(r) * g + ((r & 1) ? g - 1 - c : c);
+    if (place >= n_units) return n_units;
+    const int item = p.order[place / p.h_kv];
+    return item / m_tiles * span + place % p.h_kv * m_tiles + item % m_tiles;
+  }
   __device__ __forceinline__ int2 seen_by(const DecodeParams& p, const Entry& en, int unit) const {
     if constexpr (kRanges) {
       if (p.key_begin == nullptr && p.key_end == nullptr) return make_int2(0, en.len);
@@ -222,7 +234,8 @@ struct TileIter {
     return make_int2(0, 0);
   }
   __device__ __forceinline__ void prefetch(const DecodeParams& p) {
-    const int u2 = u + static_cast<int>(gridDim.x);
+    int u2 = u + static_cast<int>(gridDim.x);
+    if constexpr (kRanges) nu = u2 = unit_of(p, k + 1);
     has_next = u2 < n_units;
     if (has_next) {
       nx = p.entries[u2 / span];
@@ -240,6 +253,10 @@ struct TileIter {
     x = 0;
     kbase = 0;
     has_next = false;
+    if constexpr (kRanges) {
+      ordered = p.header[3] > 0;
+      u = unit_of(p, 0);
+    }
     done = u >= n_units;
     if (!done) {
       const Entry en = p.entries[u / span];
@@ -249,13 +266,14 @@ struct TileIter {
   }
   __device__ __forceinline__ uint32_t item(int tt) const { return kbase + tt * hh; }
   __device__ __forceinline__ MmaUnit next_mu() const {
-    return unit_from<kRanges>(nx, nseen, u + static_cast<int>(gridDim.x), span, m_tiles);
+    return unit_from<kRanges>(nx, nseen, kRanges ? nu : u + static_cast<int>(gridDim.x), span, m_tiles);
   }
   __device__ __forceinline__ void next_unit(const DecodeParams& p) {
     kbase += mu.tiles * hh;
     t = 0;
     ++k;
-    u += gridDim.x;
+    if constexpr (kRanges) u = nu;
+    else u += gridDim.x;
     done = u >= n_units;
     if (!done) {
       mu = unit_from<kRanges>(nx, nseen, u, span, m_tiles);

@@ -148,6 +148,7 @@ struct WorkspaceLayout {
   size_t l_part;    // f32[batch * rows * h_q * max_splits]
   size_t acc_part;  // f32[batch * rows * h_q * max_splits * d]
   size_t ranges;    // int2[batch * M tiles of 128 vectors]: modified decodes only
+  size_t order;     // int32[kOrderMax]: modified decodes only
   size_t total;
   int max_splits;
   int row_blocks;
@@ -223,6 +224,7 @@ struct DecodeParams {
   int scale_shift;         // log2 of the positions per scale
   int2* ranges;            // [batch, range_tiles] keys the rows of a sequence's M tile see (SIMT: of the sequence)
   int range_tiles;
+  int32_t* order;          // header[3] > 0: that many (entry, M tile) = entry * range_tiles + tile, most keys first
   int pool_e4m3;           // the pools are E4M3 (else bf16): what a recomputed partial of a window reads
 };
 
@@ -257,6 +259,7 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
 // d is 128 or 256 and pages hold a multiple of 64 positions.
 bool mma_path_applies(const DecodeParams& p, int q_dtype, int pool_dtype);
 constexpr int kMmaRowsPerTile = 128;   // query vectors of one M tile of the tensor-core kernel
+constexpr int kOrderMax = 1024;        // (entry, M tile) pairs that the plan kernel sorts by their keys
 cudaError_t decode_dispatch_mma(const DecodeParams& p, int pool_dtype, int grid_limit, cudaStream_t stream);
 // The same for modified decodes. An E4M3 window holds P to 2^-8, which only a bf16 output may take.
 bool mma_path_applies_modified(const DecodeParams& p, int q_dtype, int pool_dtype);
