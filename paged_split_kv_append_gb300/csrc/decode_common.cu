@@ -107,14 +107,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   // contiguous cache read as one page per sequence): tile starts either way
   const int align = p.page_tokens <= NBX_SPLIT_POSITIONS ? p.page_tokens : NBX_SPLIT_POSITIONS;
   __shared__ long long s_total;
+  __shared__ int s_multi;
+  // X: the ranges of a small call, and its entries' {b, start, end}, where the steps below read them again
+  __shared__ int2 s_range[X && TC ? kOrderMax : 1];
+  __shared__ int4 s_entry[X && TC ? kOrderMax : 1];
+  const bool kept = X && TC && static_cast<int64_t>(B) * p.range_tiles <= kOrderMax;
   if (tid == 0) {
     s_empty = 0;
     s_nb = 0;
     if constexpr (TC) s_total = 0;
     p.header[1] = 0;
     if constexpr (X) {
-      p.header[2] = 0;   // set when a partial is to be recomputed
-      p.header[3] = 0;   // set when the work is ordered
+      p.header[3] = 0;
+      s_multi = B > kSortMax;
     }
   }
   __syncthreads();
@@ -140,7 +145,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
           lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
           hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
-        if (lane == 0) p.ranges[it] = hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
+        const int2 r = hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
+        if (lane == 0) {
+          p.ranges[it] = r;
+          if (kept) s_range[it] = r;
+        }
       }
       __syncthreads();   // orders the ranges' global writes before this CTA's reads
     }
@@ -150,7 +159,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     if (!ranges) return make_int2(0, L);
     int lo = INT_MAX, hi = 0;
     for (int mt = 0; mt < p.range_tiles; ++mt) {
-      const int2 r = p.ranges[static_cast<int64_t>(b) * p.range_tiles + mt];
+      const int64_t i = static_cast<int64_t>(b) * p.range_tiles + mt;
+      const int2 r = kept ? s_range[i] : p.ranges[i];
       if (r.y > r.x) {
         lo = min(lo, r.x);
         hi = max(hi, r.y);
@@ -214,6 +224,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     const int n = L > 0 ? (L + seg - 1) / seg : 0;
     // kept in L2 for the merge, which reads the split counts after the K/V stream
     st_global_hint(reinterpret_cast<int4*>(p.plan + b), make_int4(X ? len : L, seg, n, first), l2_evict_last_policy());
+    if constexpr (X) {
+      if (n > 1) s_multi = 1;
+    }
     if (n == 0) s_empty = 1;
     else if (small) atomicAdd(&s_nb, 1);
     if (small) {
@@ -223,6 +236,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     }
   }
   __syncthreads();
+  if constexpr (X) {
+    if (tid == 0) p.header[2] = s_multi ? kMergeSplits : 0;
+  }
   // a sequence with no position to read gets no work unit: its rows are written here (0)
   if (s_empty) {
     // 16-byte pieces of a sequence's output (d is a multiple of 64)
@@ -333,6 +349,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     en.n_splits = s_n[b];
     en.pad0 = en.pad1 = 0;
     p.entries[e] = en;
+    if constexpr (X && TC) {
+      if (e < kOrderMax) s_entry[e] = make_int4(en.b, en.start, en.end, 0);
+    }
   }
   if (tid == 0) p.header[0] = total;
   // A window whose rows see their own keys: its M tiles differ in length, and a CTA takes one or two units of
@@ -342,15 +361,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     __shared__ int4 s_cost[kOrderMax / 4];
     int* const cost = reinterpret_cast<int*>(s_cost);
     const int64_t all = static_cast<int64_t>(total) * p.range_tiles;
-    if (ranges && !p.tc_round_up && all <= kOrderMax && all * p.h_kv > p.tc_units) {
+    if (ranges && kept && !p.tc_round_up && all <= kOrderMax && all * p.h_kv > p.tc_units) {
       const int items = static_cast<int>(all);
-      __syncthreads();   // orders the entries' global writes before this CTA's reads
+      __syncthreads();
       for (int i = tid; i < (items + 3) / 4 * 4; i += kPlanThreads) {
         int c = -1;
         if (i < items) {
-          const Entry en = p.entries[i / p.range_tiles];
-          const int2 r = p.ranges[static_cast<int64_t>(en.b) * p.range_tiles + i % p.range_tiles];
-          c = max(0, min(en.end, r.y) - max(en.start, r.x));
+          const int4 en = s_entry[i / p.range_tiles];
+          const int2 r = s_range[en.x * p.range_tiles + i % p.range_tiles];
+          c = max(0, min(en.z, r.y) - max(en.y, r.x));
         }
         cost[i] = c;
       }
@@ -522,7 +541,9 @@ __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(Decod
   if (blockIdx.x < n_items)
     s_first = __ldcg(&p.plan[blockIdx.x / (static_cast<int64_t>(per_seq) * kQB * n_col)].n_splits);
   pdl_wait();   // every partial of the decode is written and visible from here on
-  const bool redo_any = X && p.header[2] != 0;
+  const int todo = X ? p.header[2] : kMergeSplits;
+  if (X && todo == 0) return;   // the partial kernel wrote every row
+  const bool redo_any = X && (todo & kMergeRedo) != 0;
   for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
     const int64_t vi = it / n_col;
     const int j = static_cast<int>(it - vi * n_col) * 32 + lane;   // this lane's float4 column

@@ -954,7 +954,7 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
     if (!swap(make_float2(finite_row ? 0.f : 1.f, 0.f), other)) return false;
     if (half == 0) {
       const bool redo = row_ok && (!finite_row || other.x != 0.f) && m_run == m_run && !empty;
-      if (__any_sync(0xffffffffu, redo) && lane == 0) p.header[2] = 1;
+      if (__any_sync(0xffffffffu, redo) && lane == 0) p.header[2] = kMergeSplits | kMergeRedo;
       if (row_ok) {
         st_global_hint(p.m_part + slot, redo ? __uint_as_float(kRedoBits) : m_run, keep);
         st_global_hint(p.l_part + slot, l_run, keep);

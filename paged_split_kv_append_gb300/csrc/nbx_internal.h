@@ -140,7 +140,10 @@ static_assert(sizeof(Entry) == 32, "Entry is one 32-byte load");
 
 // Byte offsets of the workspace sections (each 256-byte aligned).
 struct WorkspaceLayout {
-  size_t header;    // int32[64]: [0] entries in the list, [1] work counter
+  // int32[64]: [0] entries in the list, [1] work counter; modified decodes: [2] what the merge has to do,
+  // kMergeSplits if some sequence has more than one split and kMergeRedo if a partial is to be recomputed,
+  // [3] (entry, M tile) pairs in `order` (0: none)
+  size_t header;
   size_t ident_bt;  // int32[batch]: the identity block table of a contiguous cache (row b = page b)
   size_t plan;      // SeqPlan[batch]
   size_t entries;   // Entry[batch * max_splits]
@@ -259,7 +262,7 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
 // d is 128 or 256 and pages hold a multiple of 64 positions.
 bool mma_path_applies(const DecodeParams& p, int q_dtype, int pool_dtype);
 constexpr int kMmaRowsPerTile = 128;   // query vectors of one M tile of the tensor-core kernel
-constexpr int kOrderMax = 1024;        // (entry, M tile) pairs that the plan kernel sorts by their keys
+constexpr int kOrderMax = 512;         // (entry, M tile) pairs that the plan kernel sorts by their keys
 cudaError_t decode_dispatch_mma(const DecodeParams& p, int pool_dtype, int grid_limit, cudaStream_t stream);
 // The same for modified decodes. An E4M3 window holds P to 2^-8, which only a bf16 output may take.
 bool mma_path_applies_modified(const DecodeParams& p, int q_dtype, int pool_dtype);
@@ -278,6 +281,7 @@ constexpr int warp_path_warps(int pool_dtype, int d) {
 cudaError_t decode_dispatch_warp_bf16(const DecodeParams& p, int grid_limit, cudaStream_t stream);
 cudaError_t decode_dispatch_warp_e4m3(const DecodeParams& p, int q_dtype, int grid_limit, cudaStream_t stream);
 cudaError_t decode_dispatch_warp_block(const DecodeParams& p, int q_dtype, bool mod, int grid_limit, cudaStream_t stream);
+constexpr int kMergeSplits = 1, kMergeRedo = 2;   // header[2]
 // m of a partial that the merge has to recompute: a NaN no computation gives
 constexpr uint32_t kRedoBits = 0x7fffbad0u;
 
