@@ -436,6 +436,11 @@ __device__ __forceinline__ float tile_scale(const DecodeParams& p, const MmaUnit
 }
 static_assert(kParts == 2, "tile_scale");
 
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // log2 and 1 / x with the hardware's approximations (to 2^-22 and 2^-23)
 __device__ __forceinline__ float fast_log2(float x) {
   float y;
@@ -566,6 +571,7 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
   using C = MmaCfg<D, F8, X>;
   constexpr bool kMod = (X & kScoreMod) != 0;
   constexpr bool kBlk = (X & kBlockScaled) != 0;
+  constexpr bool kCap = (X & kCapped) != 0, kSlope = (X & kSloped) != 0;
   constexpr int HI = C::kHalves;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = warp >> 3, quarter = warp & 3;
@@ -602,7 +608,6 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       mbar_arrive(q_full);
     }
   }
-  const bool shaped = kMod && (p.cap_log2 > 0.f || p.slopes != nullptr);   // scores are more than scaled
   while (!it.done) {
     const MmaUnit mu = it.mu;
     const int vq = mu.mt * kMmaM + row;            // this thread's query vector of the KV head
@@ -616,7 +621,7 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       const KeyRange kr = row_ok ? key_range(p, mu.b, r, mu.len) : KeyRange{0, 0};
       first_key = kr.lo;
       last_key = kr.hi - 1;
-      if (row_ok && p.slopes) slope = p.slopes[mu.h * G + gq] * kLog2e;
+      if (kSlope && row_ok && p.slopes) slope = p.slopes[mu.h * G + gq] * kLog2e;
     }
     last_key = row_ok ? min(mu.end - 1, last_key) : -1;
     const float c = F8 ? p.qk_scale_log2 * q_inv : p.qk_scale_log2;   // 2^-e: exact
@@ -681,31 +686,36 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       for (int k = 0; k < kParts; ++k) tmem_ld16(lane_base + sbuf + half * kHalf + k * 16, sr + k * 16);
       tmem_wait_ld();
       // ---- the scores: raw, with factors ck, or, capped or biased, z in log2 units with factors 1
-      if constexpr (kMod) {
-        if (shaped) {
-          if (p.cap_log2 > 0.f) {
-            float cx[kParts];
+      if constexpr (kCap) {
+        if (p.cap_log2 > 0.f) {   // (true but in a test of the waits; as a branch it is scheduled better, 125 against 143 us)
+          float cx[kParts];
 #pragma unroll
-            for (int k = 0; k < kParts; ++k) cx[k] = ck[k] * p.cap_inv;
-            cap_scores<!kBlk>(sr, cx, p.cap_log2);
+          for (int k = 0; k < kParts; ++k) cx[k] = ck[k] * p.cap_inv;
+          cap_scores<!kBlk>(sr, cx, p.cap_log2);
 #pragma unroll
-            for (int k = 0; k < kParts; ++k) ck[k] = 1.f;
-          }
-          if (p.slopes != nullptr) {
-            const float far = static_cast<float>(n0 - at);   // minus the distance of the first column
-            if (__all_sync(0xffffffffu, far + static_cast<float>(kHalf) <= 0.f)) {   // every key is at or before its row
-              const float b0 = slope * far;
+          for (int k = 0; k < kParts; ++k) ck[k] = 1.f;
+        }
+      }
+      if constexpr (kSlope) {
+        if (p.slopes != nullptr) {
+          const float far = static_cast<float>(n0 - at);   // minus the distance of the first column
+          if (__all_sync(0xffffffffu, far + static_cast<float>(kHalf) <= 0.f)) {   // every key is at or before its row
+            const float b0 = slope * far;
 #pragma unroll
-              for (int j = 0; j < kHalf; ++j)
-                sr[j] = __float_as_uint(fmaf(__uint_as_float(sr[j]), ck[j >> 4], fmaf(slope, static_cast<float>(j), b0)));
-            } else {
-#pragma unroll
-              for (int j = 0; j < kHalf; ++j)
-                sr[j] = __float_as_uint(fmaf(-slope, fabsf(far + static_cast<float>(j)), __uint_as_float(sr[j]) * ck[j >> 4]));
+            for (int j = 0; j < kHalf; j += 2) {
+              const f32x2 bias = fma2(pack2(slope, slope), pack2(static_cast<float>(j), static_cast<float>(j + 1)), pack2(b0, b0));
+              const float2 z = unpack2(fma2(pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])),
+                                            pack2(ck[j >> 4], ck[j >> 4]), bias));
+              sr[j] = __float_as_uint(z.x);
+              sr[j + 1] = __float_as_uint(z.y);
             }
+          } else {
 #pragma unroll
-            for (int k = 0; k < kParts; ++k) ck[k] = 1.f;
+            for (int j = 0; j < kHalf; ++j)
+              sr[j] = __float_as_uint(fmaf(-slope, fabsf(far + static_cast<float>(j)), __uint_as_float(sr[j]) * ck[j >> 4]));
           }
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) ck[k] = 1.f;
         }
       }
       // ---- mask (causal or key range, split end, missing page, block without a scale), row max of
@@ -723,8 +733,9 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
 #pragma unroll
         for (int i = 0; i < 4; ++i) m[i] = __uint_as_float(sr[16 * k + i]);
 #pragma unroll
-        for (int i = 4; i < 16; ++i) m[i & 3] = max_nan(m[i & 3], __uint_as_float(sr[16 * k + i]));
-        mx = max_nan(mx, fmaf(max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3])), ck[k], lv[k]));
+        for (int i = 4; i < 16; i += 2)
+          m[(i >> 1) & 3] = max3_nan(m[(i >> 1) & 3], __uint_as_float(sr[16 * k + i]), __uint_as_float(sr[16 * k + i + 1]));
+        mx = max_nan(mx, fmaf(max_nan(max3_nan(m[0], m[1], m[2]), m[3]), ck[k], lv[k]));
       }
       float2 other;
       if (!swap(make_float2(mx, w_half), other)) return false;
@@ -735,15 +746,20 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       float m_new = grow ? (F8 ? mx - kModMid : mx) : m_run;
       float f = grow ? fast_exp2(m_run - m_new) : 1.f;
       const float nm = (m_new == -INFINITY) ? 0.f : -m_new;   // all scores -inf: p = 0
-      float part[kParts][2];   // two chains a part
+      f32x2 sums[kParts];   // two chains a part
 #pragma unroll
-      for (int k = 0; k < kParts; ++k) part[k][0] = part[k][1] = 0.f;
+      for (int k = 0; k < kParts; ++k) sums[k] = pack2(0.f, 0.f);
+      const f32x2 minus1 = pack2(-1.f, -1.f);
       if constexpr (F8) {
         float pv[kHalf];
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-          pv[j] = fast_exp2(fmaf(__uint_as_float(sr[j]), ck[j >> 4], nm + lv[j >> 4]));
-          part[j >> 4][j & 1] += pv[j];
+        for (int j = 0; j < kHalf; j += 2) {
+          const float b = nm + lv[j >> 4];
+          const float2 z = unpack2(fma2(pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])),
+                                        pack2(ck[j >> 4], ck[j >> 4]), pack2(b, b)));
+          pv[j] = fast_exp2(z.x);
+          pv[j + 1] = fast_exp2(z.y);
+          sums[j >> 4] = add2(sums[j >> 4], pack2(pv[j], pv[j + 1]));
         }
         // P_lo in E5M2 leaves a weight of 2^-6 and more off by at most 2^-8 of itself, a smaller one by at most
         // 2^-14 and 2^-4 of itself. Those floors are kept within 2^-8 of the weight gathered. The first test takes
@@ -764,7 +780,10 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
 #pragma unroll
           for (int j = 0; j < kHalf; ++j) floors += pv[j] < 0.015625f ? fminf(0.0625f * pv[j], kModFloor) : 0.f;
 #pragma unroll
-          for (int k = 0; k < kParts; ++k) w_t += part[k][0] + part[k][1];
+          for (int k = 0; k < kParts; ++k) {
+            const float2 s = unpack2(sums[k]);
+            w_t += s.x + s.y;
+          }
           if (!swap(make_float2(w_t, floors), other)) return false;
           const float budget = 0.00390625f * (w_run * f + (w_t + other.x));
           if (tight) {
@@ -776,10 +795,7 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
 #pragma unroll
               for (int j = 0; j < kHalf; ++j) pv[j] *= fd;
 #pragma unroll
-              for (int k = 0; k < kParts; ++k) {
-                part[k][0] *= fd;
-                part[k][1] *= fd;
-              }
+              for (int k = 0; k < kParts; ++k) sums[k] = mul2(sums[k], pack2(fd, fd));
               e_tile = static_cast<float>(vis_all) * kModFloor;   // <= 2^-8 * 2^kModMid
             }
           }
@@ -793,7 +809,9 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
           const uint32_t h01 = e4m3x2_rn(x[0], x[1]), h23 = e4m3x2_rn(x[2], x[3]);
           const float2 a = e4m3x2_to_float2(h01), b = e4m3x2_to_float2(h23);
           wh[i] = h01 | (h23 << 16);
-          wl[i] = e5m2x2_rn(x[0] - a.x, x[1] - a.y) | (e5m2x2_rn(x[2] - b.x, x[3] - b.y) << 16);
+          const float2 la = unpack2(fma2(pack2(a.x, a.y), minus1, pack2(x[0], x[1])));
+          const float2 lb = unpack2(fma2(pack2(b.x, b.y), minus1, pack2(x[2], x[3])));
+          wl[i] = e5m2x2_rn(la.x, la.y) | (e5m2x2_rn(lb.x, lb.y) << 16);
         }
         tmem_st8(lane_base + sbuf + half * (kHalf / 4), wh);
         tmem_st8(lane_base + sbuf + kMmaN / 4 + half * (kHalf / 4), wl);
@@ -804,14 +822,16 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
 #pragma unroll
         for (int i = 0; i < kHalf / 2; ++i) {
           const int j = 2 * i;
-          const float p0 = fast_exp2(fmaf(__uint_as_float(sr[j]), ck[j >> 4], nm));
-          const float p1 = fast_exp2(fmaf(__uint_as_float(sr[j + 1]), ck[j >> 4], nm));
-          part[j >> 4][0] += p0;
-          part[j >> 4][1] += p1;
+          const float2 z = unpack2(fma2(pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])),
+                                        pack2(ck[j >> 4], ck[j >> 4]), pack2(nm, nm)));
+          const float p0 = fast_exp2(z.x), p1 = fast_exp2(z.y);
+          const f32x2 pp2 = pack2(p0, p1);
+          sums[j >> 4] = add2(sums[j >> 4], pp2);
           const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
           wh[i] = __byte_perm(u0, u1, 0x7632);
-          const __nv_bfloat162 lr = __floats2bfloat162_rn(p0 - __uint_as_float(u0 & 0xffff0000u),
-                                                          p1 - __uint_as_float(u1 & 0xffff0000u));
+          const float2 lo = unpack2(fma2(pack2(__uint_as_float(u0 & 0xffff0000u), __uint_as_float(u1 & 0xffff0000u)),
+                                         minus1, pp2));
+          const __nv_bfloat162 lr = __floats2bfloat162_rn(lo.x, lo.y);
           wl[i] = *reinterpret_cast<const uint32_t*>(&lr);
         }
         tmem_st16(lane_base + sbuf + half * (kHalf / 2), wh);
@@ -822,7 +842,8 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       w_half = 0.f;
 #pragma unroll
       for (int k = 0; k < kParts; ++k) {
-        const float s = part[k][0] + part[k][1];
+        const float2 s2 = unpack2(sums[k]);
+        const float s = s2.x + s2.y;
         w_half += s;
         l_t += kBlk ? s * iv[k] : s;
       }
@@ -838,7 +859,11 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
           for (int q = 0; q < 4; ++q) tmem_ld16(col + q * 16, ov + q * 16);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 64; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f);
+          for (int i = 0; i < 64; i += 2) {
+            const float2 o2 = unpack2(mul2(pack2(__uint_as_float(ov[i]), __uint_as_float(ov[i + 1])), pack2(f, f)));
+            ov[i] = __float_as_uint(o2.x);
+            ov[i + 1] = __float_as_uint(o2.y);
+          }
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_st16(col + q * 16, ov + q * 16);
         }
@@ -1667,6 +1692,11 @@ const MmaMaps* cached_maps(const DecodeParams& p, bool f8, int device) {
   return &maps[slot];
 }
 
+// A test of the timeout path; among the kernels of modified decodes the one with everything in it takes them.
+bool waits_tested(const DecodeParams& p) { return p.wait_limit_ns != kWaitLimitNs || p.producer_delay_ns != 0; }
+constexpr int kMmaAll = kScoreMod | kCapped | kSloped;
+constexpr bool mma_tests_waits(int x) { return x == 0 || (x & kMmaAll) == kMmaAll; }
+
 template <int D, bool F8, int X = 0>
 cudaError_t launch_mma(const DecodeParams& p, int grid_limit, cudaStream_t stream) {
   using C = MmaCfg<D, F8, X>;
@@ -1678,9 +1708,10 @@ cudaError_t launch_mma(const DecodeParams& p, int grid_limit, cudaStream_t strea
   if ((configured.load() & bit) == 0) {
     cudaError_t e = cudaFuncSetAttribute(decode_partial_mma_kernel<D, F8, false, X>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(decode_partial_mma_kernel<D, F8, true, X>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               C::kSmem);
+    if constexpr (mma_tests_waits(X))
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(decode_partial_mma_kernel<D, F8, true, X>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::kSmem);
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
@@ -1690,11 +1721,27 @@ cudaError_t launch_mma(const DecodeParams& p, int grid_limit, cudaStream_t strea
   if (grid_limit > 0 && grid > grid_limit) grid = grid_limit;
   if (grid > upper) grid = upper;
   if (grid < 1) grid = 1;
-  if (p.wait_limit_ns != kWaitLimitNs || p.producer_delay_ns != 0)   // a test of the timeout path
-    return launch_pdl(decode_partial_mma_kernel<D, F8, true, X>, static_cast<unsigned>(grid), X ? kMmaThreadsMod : kMmaThreads, C::kSmem,
-                      stream, p, *maps);
-  return launch_pdl(decode_partial_mma_kernel<D, F8, false, X>, static_cast<unsigned>(grid), X ? kMmaThreadsMod : kMmaThreads, C::kSmem,
-                    stream, p, *maps);
+  constexpr unsigned threads = X ? kMmaThreadsMod : kMmaThreads;
+  if constexpr (mma_tests_waits(X))
+    if (waits_tested(p))
+      return launch_pdl(decode_partial_mma_kernel<D, F8, true, X>, static_cast<unsigned>(grid), threads, C::kSmem, stream, p,
+                        *maps);
+  return launch_pdl(decode_partial_mma_kernel<D, F8, false, X>, static_cast<unsigned>(grid), threads, C::kSmem, stream, p,
+                    *maps);
+}
+
+// A modified decode, by the kernel without the score modifications that it does not ask for: capped 16-row windows
+// at 32768 positions take 125 us, and 136 with the code of a bias compiled in but not taken.
+template <int D, bool F8, int X>
+cudaError_t launch_mma_mod(const DecodeParams& p, int grid_limit, cudaStream_t stream) {
+  if (waits_tested(p)) return launch_mma<D, F8, X | kMmaAll>(p, grid_limit, stream);
+  if constexpr ((X & kScoreMod) != 0) {
+    if (p.slopes != nullptr)
+      return p.cap_log2 > 0.f ? launch_mma<D, F8, X | kMmaAll>(p, grid_limit, stream)
+                              : launch_mma<D, F8, X | kSloped>(p, grid_limit, stream);
+    if (p.cap_log2 > 0.f) return launch_mma<D, F8, X | kCapped>(p, grid_limit, stream);
+  }
+  return launch_mma<D, F8, X>(p, grid_limit, stream);
 }
 
 }  // namespace

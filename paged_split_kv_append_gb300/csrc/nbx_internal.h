@@ -236,6 +236,9 @@ struct DecodeParams {
 // without any of it.
 constexpr int kScoreMod = 1;
 constexpr int kBlockScaled = 2;
+// Of the tensor-core kernel's score modifications, beside the key ranges of kScoreMod: a cap, a bias by distance.
+constexpr int kCapped = 4;
+constexpr int kSloped = 8;
 
 // The visible keys of query row r of a sequence of len positions: [lo, hi), empty as lo = hi = 0.
 struct KeyRange {
