@@ -327,7 +327,7 @@ NBX_API int nbx_paged_kv_append_block_scaled(const void* new_k, const void* new_
  * max(p + 1, prefix length), a window key_begin = p + 1 - window. Keys that no row of a work unit sees are
  * not read: their pages may be gone from the table (-1).
  *
- *   softcap      finite, >= 0 (0: none)
+ *   softcap      0 (none), or such that softcap * log2 e and its reciprocal are finite floats
  *   slopes       [device] fp32 [h_q] or NULL
  *   key_begin, key_end  [device] int32 [batch, rows] or NULL each
  *   out          [device] [batch, rows, h_q, d] in out_dtype: NBX_F32, or NBX_BF16 (rounded once)

@@ -26,7 +26,8 @@ __all__ = [
     "nbx_paged_decode_merge", "nbx_set_decode_grid_limit", "nbx_set_decode_wait_test", "nbx_status_string",
     "nbx_paged_decode_bounds", "nbx_paged_decode_attn_fixed_shift", "nbx_decode_fixed_shift_gate",
     "nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
-    "nbx_paged_decode_modified_workspace_bytes", "nbx_paged_decode_modified_partial_kernel", "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork",
+    "nbx_paged_decode_modified_workspace_bytes", "nbx_paged_decode_modified_partial_kernel",
+    "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork",
     "nbx_paged_kv_fork_workspace_bytes", "nbx_paged_kv_compact", "nbx_paged_kv_compact_workspace_bytes",
     "dtype_code",
     "DEV_BAD_SLOT", "DEV_BAD_PAGE", "DEV_BAD_LEN", "DEV_TIMEOUT", "DEV_BAD_SCALE", "DEV_BAD_ROW", "DEV_NO_PAGE",
@@ -100,8 +101,8 @@ def _declare(l):
     l.nbx_paged_decode_modified_workspace_bytes.restype = sz
     l.nbx_paged_decode_modified_partial_kernel.argtypes = [i32] * 9
     l.nbx_paged_decode_modified_partial_kernel.restype = i32
-    l.nbx_paged_decode_attn_block_scaled.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, vp,
-                                                     i32, vp, i32, f32, f32, vp, vp, vp, vp, i32, vp, sz, vp, vp]
+    l.nbx_paged_decode_attn_block_scaled.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32,
+                                                     vp, i32, vp, i32, f32, f32, vp, vp, vp, vp, i32, vp, sz, vp, vp]
     l.nbx_paged_decode_attn_block_scaled.restype = i32
     l.nbx_paged_decode_attn_modified.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp,
                                                  i32, f32, f32, f32, f32, vp, vp, vp, vp, i32, vp, sz, vp, vp]
@@ -461,6 +462,17 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An uninitialised tensor on `like`'s device for a call on `stream`. The allocator learns of a stream that is
+    not the current one, so that the memory is not handed out again while the call still runs there."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        handle = int(getattr(stream, "cuda_stream", stream))
+        if handle != _raw_stream(t.get_device()):
+            t.record_stream(torch.cuda.ExternalStream(handle, device=t.device))
+    return t
+
+
 def _run(func: str, dev: int, stream, *args):
     """Calls the entry point on device `dev` and the given (or its current) stream, the last argument."""
     st = _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
@@ -529,7 +541,7 @@ def nbx_paged_decode_modified_partial_kernel(q_dtype: int, pool_dtype: int, out_
     return k
 
 
-def _modified_shapes(q, d, block_table, seq_lens, slopes, key_begin, key_end, out, out_dtype, status):
+def _modified_shapes(q, d, block_table, seq_lens, slopes, key_begin, key_end, out, out_dtype, status, stream):
     """The checks the two modified decodes share: (batch, rows, h_q, max_pages, out)."""
     shape, table = q.shape, block_table.shape
     _int32("block_table seq_lens key_begin key_end status", block_table, seq_lens, key_begin, key_end, status)
@@ -541,14 +553,14 @@ def _modified_shapes(q, d, block_table, seq_lens, slopes, key_begin, key_end, ou
     if slopes is not None and slopes.dtype is not torch.float32:
         raise ValueError("slopes must be fp32")
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or torch.float32, device=q.device)
+        out = _new(shape, out_dtype or torch.float32, q, stream)
     elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError(f"out must be {list(shape)}" + (f" {out_dtype}" if out_dtype else ""))
     return shape[0], shape[1], shape[2], table[1], out
 
 
-def _workspace(need, q):
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+def _workspace(need, like, stream):
+    return _new(max(need, 256), torch.uint8, like, stream)
 
 
 def nbx_paged_decode_attn_block_scaled(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
@@ -562,19 +574,20 @@ def nbx_paged_decode_attn_block_scaled(q: torch.Tensor, k_pool: torch.Tensor, v_
     """q [batch, rows, h_q, d] (fp32 or bf16) over a block-scaled cache (e4m3 pools, scales [num_pages, h_kv,
     page_tokens / scale_tokens] fp32) -> out [batch, rows, h_q, d], fp32 or bf16 (out's dtype, or out_dtype).
     The score modifications are those of nbx_paged_decode_attn_modified."""
-    dev = _one_device("q k_pool v_pool k_scales v_scales block_table seq_lens slopes key_begin key_end out workspace status",
-                      q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, slopes, key_begin, key_end, out,
-                      workspace, status)
+    dev = _one_device("q k_pool v_pool k_scales v_scales block_table seq_lens slopes key_begin key_end out workspace "
+                      "status", q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, slopes, key_begin,
+                      key_end, out, workspace, status)
     num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
     batch, rows, h_q, max_pages, out = _modified_shapes(q, d, block_table, seq_lens, slopes, key_begin, key_end, out,
-                                                        out_dtype, status)
+                                                        out_dtype, status, stream)
     if workspace is None:
-        workspace = _workspace(nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len), q)
+        workspace = _workspace(nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len), q,
+                               stream)
     _run("nbx_paged_decode_attn_block_scaled", dev, stream, q.data_ptr(), dtype_code(q), batch, rows, h_q, d,
          k_pool.data_ptr(), v_pool.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block, num_pages, h_kv,
-         page_tokens, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), int(max_seq_len), float(scale), float(softcap), _p(slopes),
-         _p(key_begin), _p(key_end), out.data_ptr(), dtype_code(out), workspace.data_ptr(), workspace.nbytes,
-         _p(status))
+         page_tokens, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), int(max_seq_len), float(scale),
+         float(softcap), _p(slopes), _p(key_begin), _p(key_end), out.data_ptr(), dtype_code(out),
+         workspace.data_ptr(), workspace.nbytes, _p(status))
     return out
 
 
@@ -593,13 +606,15 @@ def nbx_paged_decode_attn_modified(q: torch.Tensor, k_pool: torch.Tensor, v_pool
                       v_pool, block_table, seq_lens, slopes, key_begin, key_end, out, workspace, status)
     num_pages, h_kv, page_tokens, d, _ = _pools(k_pool, v_pool, None, None)
     batch, rows, h_q, max_pages, out = _modified_shapes(q, d, block_table, seq_lens, slopes, key_begin, key_end, out,
-                                                        out_dtype, status)
+                                                        out_dtype, status, stream)
     if workspace is None:
-        workspace = _workspace(nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len), q)
+        workspace = _workspace(nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len), q,
+                               stream)
     _run("nbx_paged_decode_attn_modified", dev, stream, q.data_ptr(), dtype_code(q), batch, rows, h_q, d,
          k_pool.data_ptr(), v_pool.data_ptr(), dtype_code(k_pool), num_pages, h_kv, page_tokens, block_table.data_ptr(),
          max_pages, seq_lens.data_ptr(), int(max_seq_len), float(scale), float(k_scale), float(v_scale), float(softcap),
-         _p(slopes), _p(key_begin), _p(key_end), out.data_ptr(), dtype_code(out), workspace.data_ptr(), workspace.nbytes, _p(status))
+         _p(slopes), _p(key_begin), _p(key_end), out.data_ptr(), dtype_code(out), workspace.data_ptr(),
+         workspace.nbytes, _p(status))
     return out
 
 
@@ -614,9 +629,9 @@ def nbx_paged_kv_copy_pages(moves: torch.Tensor, n_moves: torch.Tensor, k_pool: 
     _int32("moves n_moves status", moves, n_moves, status)
     if moves.dim() != 2 or moves.shape[1] != 3 or n_moves.numel() < 1:
         _misfit("moves n_moves", moves, n_moves)
-    _run("nbx_paged_kv_copy_pages", dev, stream, moves.data_ptr(), n_moves.data_ptr(), moves.shape[0], k_pool.data_ptr(),
-         v_pool.data_ptr(), dtype_code(k_pool), num_pages, h_kv, page_tokens, d, _p(k_scales), _p(v_scales), block,
-         _p(status))
+    _run("nbx_paged_kv_copy_pages", dev, stream, moves.data_ptr(), n_moves.data_ptr(), moves.shape[0],
+         k_pool.data_ptr(), v_pool.data_ptr(), dtype_code(k_pool), num_pages, h_kv, page_tokens, d, _p(k_scales),
+         _p(v_scales), block, _p(status))
 
 
 def nbx_paged_kv_fork_workspace_bytes(batch: int, max_pages: int, n_fork: int, num_pages: int) -> int:
@@ -631,26 +646,31 @@ def nbx_paged_kv_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, fork_sr
     """Rows fork_dst[i] of block_table [batch, max_pages] and seq_lens [batch] become rows fork_src[i] as they
     were (all int32): full pages shared, the last partial page copied to a free one. Returns (moves [n_fork, 3],
     n_moves [1]): the copies made, for nbx_paged_kv_copy_pages on the other layers' pools."""
-    dev = _one_device("block_table seq_lens fork_src fork_dst k_pool v_pool k_scales v_scales moves n_moves workspace status",
-                      block_table, seq_lens, fork_src, fork_dst, k_pool, v_pool, k_scales, v_scales, moves, n_moves,
-                      workspace, status)
-    _int32("block_table seq_lens fork_src fork_dst moves n_moves status", block_table, seq_lens, fork_src, fork_dst, moves,
-           n_moves, status)
+    dev = _one_device("block_table seq_lens fork_src fork_dst k_pool v_pool k_scales v_scales moves n_moves workspace "
+                      "status", block_table, seq_lens, fork_src, fork_dst, k_pool, v_pool, k_scales, v_scales, moves,
+                      n_moves, workspace, status)
+    _int32("block_table seq_lens fork_src fork_dst moves n_moves status", block_table, seq_lens, fork_src, fork_dst,
+           moves, n_moves, status)
     num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
     n, table = fork_src.numel(), block_table.shape
+    # (the call writes all of both; one without a fork or a row writes nothing)
     if moves is None:
-        moves = torch.full((n, 3), -1, dtype=torch.int32, device=block_table.device)
+        moves = _new((n, 3), torch.int32, block_table, stream)
+        if len(table) == 2 and table[0] == 0:
+            moves.fill_(-1)
     if n_moves is None:
-        n_moves = torch.zeros(1, dtype=torch.int32, device=block_table.device)
+        n_moves = _new(1, torch.int32, block_table, stream)
+        if n == 0 or (len(table) == 2 and table[0] == 0):
+            n_moves.zero_()
     if len(table) != 2 or seq_lens.numel() != table[0] or fork_dst.numel() != n or moves.shape != (n, 3) or \
             n_moves.numel() < 1:
-        _misfit("block_table seq_lens fork_src fork_dst moves n_moves", block_table, seq_lens, fork_src, fork_dst, moves,
-                n_moves)
+        _misfit("block_table seq_lens fork_src fork_dst moves n_moves", block_table, seq_lens, fork_src, fork_dst,
+                moves, n_moves)
     if workspace is None:
-        workspace = _workspace(nbx_paged_kv_fork_workspace_bytes(table[0], table[1], n, num_pages), block_table)
+        workspace = _workspace(nbx_paged_kv_fork_workspace_bytes(table[0], table[1], n, num_pages), block_table, stream)
     _run("nbx_paged_kv_fork", dev, stream, block_table.data_ptr(), table[1], seq_lens.data_ptr(), table[0],
-         fork_src.data_ptr(), fork_dst.data_ptr(), n, k_pool.data_ptr(), v_pool.data_ptr(), dtype_code(k_pool), num_pages,
-         h_kv, page_tokens, d, _p(k_scales), _p(v_scales), block, moves.data_ptr(), n_moves.data_ptr(),
+         fork_src.data_ptr(), fork_dst.data_ptr(), n, k_pool.data_ptr(), v_pool.data_ptr(), dtype_code(k_pool),
+         num_pages, h_kv, page_tokens, d, _p(k_scales), _p(v_scales), block, moves.data_ptr(), n_moves.data_ptr(),
          workspace.data_ptr(), workspace.nbytes, _p(status))
     return moves, n_moves
 
@@ -667,24 +687,30 @@ def nbx_paged_kv_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, k_po
     """The pages in use moved to the lowest ids. Returns (new_block_table, moves [num_pages // 2, 3], counts [2] =
     {moves, pages in use}); new_block_table may be block_table itself. The moves are for
     nbx_paged_kv_copy_pages on the other layers' pools."""
-    dev = _one_device("block_table seq_lens k_pool v_pool k_scales v_scales new_block_table moves counts workspace status",
-                      block_table, seq_lens, k_pool, v_pool, k_scales, v_scales, new_block_table, moves, counts, workspace,
-                      status)
-    _int32("block_table seq_lens new_block_table moves counts status", block_table, seq_lens, new_block_table, moves, counts,
-           status)
+    dev = _one_device("block_table seq_lens k_pool v_pool k_scales v_scales new_block_table moves counts workspace "
+                      "status", block_table, seq_lens, k_pool, v_pool, k_scales, v_scales, new_block_table, moves,
+                      counts, workspace, status)
+    _int32("block_table seq_lens new_block_table moves counts status", block_table, seq_lens, new_block_table, moves,
+           counts, status)
     num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
     table = block_table.shape
     if new_block_table is None:
-        new_block_table = torch.empty_like(block_table)
+        new_block_table = _new(table, torch.int32, block_table, stream)
+    empty = len(table) == 2 and table[0] == 0   # (such a call writes nothing, any other all of moves and counts)
     if moves is None:
-        moves = torch.full((max(1, num_pages // 2), 3), -1, dtype=torch.int32, device=block_table.device)
+        moves = _new((max(1, num_pages // 2), 3), torch.int32, block_table, stream)
+        if empty:
+            moves.fill_(-1)
     if counts is None:
-        counts = torch.zeros(2, dtype=torch.int32, device=block_table.device)
+        counts = _new(2, torch.int32, block_table, stream)
+        if empty:
+            counts.zero_()
     if len(table) != 2 or seq_lens.numel() != table[0] or new_block_table.shape != table or moves.dim() != 2 or \
             moves.shape[1] != 3 or counts.numel() < 2:
-        _misfit("block_table seq_lens new_block_table moves counts", block_table, seq_lens, new_block_table, moves, counts)
+        _misfit("block_table seq_lens new_block_table moves counts", block_table, seq_lens, new_block_table, moves,
+                counts)
     if workspace is None:
-        workspace = _workspace(nbx_paged_kv_compact_workspace_bytes(num_pages), block_table)
+        workspace = _workspace(nbx_paged_kv_compact_workspace_bytes(num_pages), block_table, stream)
     _run("nbx_paged_kv_compact", dev, stream, block_table.data_ptr(), new_block_table.data_ptr(), table[1],
          seq_lens.data_ptr(), table[0], k_pool.data_ptr(), v_pool.data_ptr(), dtype_code(k_pool), num_pages, h_kv,
          page_tokens, d, _p(k_scales), _p(v_scales), block, moves.data_ptr(), moves.shape[0], counts.data_ptr(),

@@ -194,7 +194,8 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
     if (mod->out_dtype != NBX_F32 && mod->out_dtype != NBX_BF16) return NBX_ERR_DTYPE;
     if (mod->block_scaled && !scale_tokens_ok(mod->scale_tokens, page_tokens)) return NBX_ERR_PAGE_ALIGN;
     if (!(mod->softcap >= 0.f) || !finite(mod->softcap)) return NBX_ERR_VALUE;
-    if (mod->softcap > 0.f && !finite(1.f / (mod->softcap * kLog2eHost))) return NBX_ERR_VALUE;
+    const float cap = mod->softcap * kLog2eHost;   // the kernels take it and its reciprocal
+    if (mod->softcap > 0.f && (!finite(cap) || !finite(1.f / cap))) return NBX_ERR_VALUE;
   }
   if (batch == 0) return NBX_OK;
   if (!q || !k_pool || !v_pool || (!identity && !block_table) || !seq_lens || !out || !workspace) return NBX_ERR_NULL;

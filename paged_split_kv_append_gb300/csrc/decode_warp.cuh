@@ -42,12 +42,14 @@ namespace nbx {
 namespace {
 
 constexpr int kWarpVecs = kWarpUnitVectors;   // 8
-constexpr float kWarpMid = 7.f, kWarpHi = 15.f;   // log2 of the largest weight after a move of m, and at most
 
 template <class PT, class QT, int D, int X>
 struct WarpCfg {
   static constexpr bool kE4 = PT::kCode == NBX_E4M3;
   static constexpr bool kTwo = QT::kCode == NBX_F32;        // queries as two terms
+  // log2 of the largest weight after a move of m, and at most: high in f16's range under E4M3 values, low under
+  // bf16 ones, whose own range is fp32's
+  static constexpr float kMid = kE4 ? 7.f : 0.f, kHi = kE4 ? 15.f : 8.f;
   static constexpr int kRow = D * PT::kBytes;               // bytes of a position
   static constexpr int kTile = kTileN * kRow;               // bytes of 16 positions of K (or V)
   static constexpr int kStage = 2 * kTile + ((X & kBlockScaled) ? 16 : 0);
@@ -439,16 +441,16 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
         }
         // ---- the reference moves when a weight would pass 2^15; a NaN one stays NaN
         float mx[2] = {max_nan(z[0], z[2]) + lv, max_nan(z[1], z[3]) + lv};
-        const bool past = (!(mx[0] <= m_run[0] + kWarpHi) && m_run[0] == m_run[0]) ||
-                          (!(mx[1] <= m_run[1] + kWarpHi) && m_run[1] == m_run[1]);
+        const bool past = (!(mx[0] <= m_run[0] + C::kHi) && m_run[0] == m_run[0]) ||
+                          (!(mx[1] <= m_run[1] + C::kHi) && m_run[1] == m_run[1]);
         if (__any_sync(0xffffffffu, past)) {
           float f[2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx[y] = max_nan(mx[y], __shfl_xor_sync(0xffffffffu, mx[y], o));
-            const bool move = !(mx[y] <= m_run[y] + kWarpHi) && m_run[y] == m_run[y];
-            const float m_new = move ? mx[y] - kWarpMid : m_run[y];
+            const bool move = !(mx[y] <= m_run[y] + C::kHi) && m_run[y] == m_run[y];
+            const float m_new = move ? mx[y] - C::kMid : m_run[y];
             f[y] = move ? fast_exp2(m_run[y] - m_new) : 1.f;
             m_run[y] = m_new;
             l_run[y] *= f[y];

@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_small_kernel(CompactPara
     live += __popc(used);
   }
   const int n_moves = n_live - below;
-  for (int i = 3 * n_moves + tid; i < 3 * p.max_moves; i += kPlanThreads) p.moves[i] = -1;
+  for (int64_t i = 3 * n_moves + tid; i < 3 * static_cast<int64_t>(p.max_moves); i += kPlanThreads) p.moves[i] = -1;
   if (tid == 0) {
     p.counts[0] = n_moves;
     p.counts[1] = n_live;

@@ -211,6 +211,12 @@ def test_attention_definition_on_two_keys():
     assert of.E4M3_MAX == 448.0
 
 
+def test_a_cap_past_the_range_is_refused(lib):
+    # 3e38 is finite, 3e38 log2 e is not; without the refusal scores became infinity times zero
+    for f, args in ((lib.nbx_paged_decode_attn_modified, MODIFIED), (lib.nbx_paged_decode_attn_block_scaled, BLOCK)):
+        assert call(f, args, softcap=3e38) == -8
+
+
 # ------------------------------------------------------------------------- the session
 def test_session_refusals():
     from paged_split_kv_append_gb300.session import PagedDecodeSession

@@ -550,3 +550,32 @@ def test_refusals_of_the_bindings():
     c.scales = [half[0], c.scales[1]]
     with pytest.raises(ValueError):
         c.call()
+
+
+def test_large_bf16_values_stay_finite():
+    # values of 1e36 under weights held up to 2^8 of their row's largest: no sum leaves fp32's range
+    c = Case("bf16", "bf16", 1, 8, 2, 128, 16, (300, 33), 0, seed=77)
+    v = c.dev[1].float().nan_to_num(0.0).clamp(-1.0, 1.0) * 1e36
+    c.dev[1] = v.to(torch.bfloat16)
+    c.values = [c.values[0], c.dev[1].double().cpu().numpy() * c.kw.get("v_scale", 1.0)]
+    c.check(softcap=3.0)
+
+
+@pytest.mark.parametrize("pool,rows,h_q,h_kv,batch,longest", [
+    ("bf16", 128, 16, 4, 10, 700),       # 160 units, dealt out by their keys
+    ("block", 128, 16, 4, 10, 700),
+    ("bf16", 32, 16, 1, 131, 150),       # more M tiles than the plan sorts
+])
+def test_windows_of_many_units_over_key_ranges(pool, rows, h_q, h_kv, batch, longest):
+    """More work units than SMs, of uneven length: each is done once, on a full grid and on 7 CTAs."""
+    lens = np.random.default_rng(5).integers(rows, longest, batch)
+    lens[3] = 0
+    c = Case(pool, "bf16", rows, h_q, h_kv, 128, 64, lens, 64 if pool == "block" else 0, seed=88)
+    for mask in ("documents", "random"):
+        mod = made(dict(mask=mask), c.lens, rows, h_q)
+        out = c.check("bf16", P_WEIGHT[pool], **mod)
+        nbx.nbx_set_decode_grid_limit(7)
+        try:
+            assert torch.equal(c.call("bf16", **mod), out)
+        finally:
+            nbx.nbx_set_decode_grid_limit(0)

@@ -311,3 +311,34 @@ def test_fork_and_compact_captured_and_replayed():
             for j in range(int(l1[b])):
                 pg = int(t2[b, j // P])
                 assert all(torch.equal(a[pg, :, j % P], r[pg, :, j % P]) for a, r in zip(x, ref))
+
+
+def test_calls_on_another_stream_own_what_they_allocate():
+    """Moves and counts that a call allocates for a stream that is not the current one, which is busy."""
+    P, width = 16, 5
+    lens, src, dst = [20, 33, 47, 0, 0, 0], [0, 1, 1], [3, 4, 5]
+    table, n = table_for(lens, P, width, 19, spread=3.0)
+    x = pools(n, 2, P, 64, "bf16", 19)
+    t, ln, s, e = dev(table), dev(lens), dev(src), dev(dst)
+    t1, l1, mv1 = oc.fork(table, np.array(lens), src, dst, P, n)
+    t2, mv2, live = oc.compact(t1, l1, P, n)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)   # ten milliseconds or so of the current stream
+    m1, c1 = nbx.nbx_paged_kv_fork(t, ln, s, e, *x, stream=side)
+    new, m2, c2 = nbx.nbx_paged_kv_compact(t, ln, *x, stream=side)
+    torch.cuda.synchronize()
+    assert c1.tolist() == [len(mv1)] and [tuple(m) for m in m1[:len(mv1)].tolist()] == mv1
+    assert c2.tolist() == [len(mv2), live] and [tuple(m) for m in m2[:len(mv2)].tolist()] == mv2
+    assert np.array_equal(t.cpu().numpy(), t1) and np.array_equal(new.cpu().numpy(), t2)
+
+
+def test_calls_without_rows_or_forks_return_no_moves():
+    x = pools(8, 1, 16, 16, "f32", 18)
+    none = dev(np.zeros(0))
+    m, c = nbx.nbx_paged_kv_fork(dev([[1, 2]]), dev([20]), none, none, *x)
+    assert c.tolist() == [0] and m.shape == (0, 3)
+    m, c = nbx.nbx_paged_kv_fork(dev(np.zeros((0, 2))), none, dev([0]), dev([1]), *x)
+    assert c.tolist() == [0] and m.tolist() == [[-1, -1, -1]]
+    new, m, c = nbx.nbx_paged_kv_compact(dev(np.zeros((0, 2))), none, *x)
+    assert c.tolist() == [0, 0] and m.tolist() == [[-1, -1, -1]] * 4 and new.shape == (0, 2)
