@@ -523,10 +523,11 @@ __device__ __forceinline__ void store_out4(const DecodeParams& p, int64_t orow, 
 // reductions, a fixed order), the weights reach every lane by shuffles, and each lane owns one
 // float4 of the output, with every split's accumulator load in flight and the sum in ascending
 // split order.
+// N: the splits whose accumulators are loaded at once.
 // F16: the partials are f16 acc / l (DecodeParams::part_f16); a split then weighs 2^(m - M) * l.
 // X: a modified decode, whose output may be bf16, and whose windows on tensor cores mark partials to be
 // recomputed (header[2] says that there are any): such rows take the slow path above, splits ascending too.
-template <bool F16, bool X>
+template <bool F16, bool X, int N>
 __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(DecodeParams p) {
   const int lane = threadIdx.x;
   const int RG = p.rows * p.group;
@@ -606,9 +607,9 @@ __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(Decod
     const float4* acc = reinterpret_cast<const float4*>(p.acc_part + orow * p.max_splits * p.d);
     // f16 partials: the d halves at the start of each split's d-float slot, 4 per lane (8 bytes)
     const uint2* acc_h = reinterpret_cast<const uint2*>(p.acc_part + orow * p.max_splits * p.d);
-    auto load_batch = [&](int j, int s0, float4 (&a)[32]) {
+    auto load_batch = [&](int j, int s0, float4 (&a)[N]) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < N; ++k) {
         const bool in = j < d4 && s0 + k < S;
         if constexpr (F16) {
           const uint2 hv = in ? acc_h[static_cast<int64_t>(s0 + k) * (2 * d4) + j] : make_uint2(0u, 0u);
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(Decod
         }
       }
     };
-    float4 a[32];
+    float4 a[N];
     load_batch(j, 0, a);   // in flight together with the m / l loads
     float mv[2], lv[2];
     bool live[2];
@@ -649,13 +650,13 @@ __global__ void __launch_bounds__(kDecodeMergeThreads) decode_merge_kernel(Decod
     const float sc = p.v_scale / L;
     // every lane runs every step (the shuffles need the whole warp); lanes past the row store nothing
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < S; s0 += 32) {
+    for (int s0 = 0; s0 < S; s0 += N) {
       if (s0 > 0) load_batch(j, s0, a);
-      const float wsrc = s0 == 0 ? wv[0] : wv[1];
+      const float wsrc = s0 < 32 ? wv[0] : wv[1];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
+      for (int k = 0; k < N; ++k) {
         if (s0 + k >= S) break;
-        const float w = __shfl_sync(0xffffffffu, wsrc, k);
+        const float w = __shfl_sync(0xffffffffu, wsrc, (s0 + k) & 31);
         if (w != -1.f) {
           A.x += w * a[k].x;
           A.y += w * a[k].y;
@@ -780,10 +781,10 @@ cudaError_t launch_plan(const DecodeParams& p, cudaStream_t stream) {
                         : launch_pdl(plan_kernel<false, X>, 1u, kPlanThreads, smem, stream, p);
 }
 
-template <bool X>
+template <bool X, int N>
 cudaError_t launch_merge(const DecodeParams& p, unsigned grid, cudaStream_t stream) {
-  return p.part_f16 ? launch_pdl(decode_merge_kernel<true, X>, grid, kDecodeMergeThreads, 0, stream, p)
-                    : launch_pdl(decode_merge_kernel<false, X>, grid, kDecodeMergeThreads, 0, stream, p);
+  return p.part_f16 ? launch_pdl(decode_merge_kernel<true, X, N>, grid, kDecodeMergeThreads, 0, stream, p)
+                    : launch_pdl(decode_merge_kernel<false, X, N>, grid, kDecodeMergeThreads, 0, stream, p);
 }
 
 cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, int x, int grid_limit,
@@ -830,7 +831,10 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
   int64_t grid = static_cast<int64_t>(device_info().sm_count) * 24;
   if (grid > items) grid = items;
   const unsigned g = static_cast<unsigned>(grid);
-  return x ? launch_merge<true>(q, g, stream) : launch_merge<false>(q, g, stream);
+  // A window has many rows of few splits: fewer loads of a row in flight, more warps (128 rows of 24 heads of 256 in
+  // 6 splits: 2 of 11 us less). A single row has few rows and up to 64 splits.
+  if (x && mma) return launch_merge<true, 8>(q, g, stream);
+  return x ? launch_merge<true, 32>(q, g, stream) : launch_merge<false, 32>(q, g, stream);
 }
 
 }  // namespace nbx
