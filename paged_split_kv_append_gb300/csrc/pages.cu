@@ -21,12 +21,14 @@ constexpr int kChunk = 4096;          // bytes a warp copies at a time
 constexpr int kCopyThreads = 256;
 constexpr int kPlanThreads = 1024;    // single-CTA steps
 constexpr int kScanPages = 2048;      // pages per CTA of the compaction's scan
-// Up to these sizes one CTA does all the bookkeeping of a call: it reads 64 Ki table entries in about 8 us,
-// where the launches of the steps of their own cost about 10 (and each costs the host 2 us).
+// Up to these sizes one CTA does all the bookkeeping of a call, where the launches of the steps of their own cost
+// about 10 us on the GPU (and each costs the host 2). A fork of half of 64 rows of 250 pages: 7.5 us against 16.6, of
+// 250 rows of 250: 13 against 16, of 1000 rows of 10 (a warp takes a row at a time): 30 against 17. A compaction of 128
+// pages: 4.3 against 12.5, of 20000: 18 against 15.
 constexpr int64_t kSmallTable = 65536;        // entries of the block table
+constexpr int kForkSmallRows = 256;           // rows, and forks
 constexpr int kForkSmallPages = 262144;       // pages: a bitmap of 32 KB
-constexpr int64_t kForkSmallWork = 1 << 20;   // rows x forks compared
-constexpr int kCompactSmallPages = 24576;     // pages: fill counts and destinations of 144 KB
+constexpr int kCompactSmallPages = 12288;     // pages: fill counts and destinations of 72 KB
 
 int64_t up256(int64_t x) { return (x + 255) & ~static_cast<int64_t>(255); }
 
@@ -118,9 +120,9 @@ __device__ __forceinline__ int block_scan(int v, int* s, int* total) {
 }
 
 // ------------------------------------------------------------------------------------ fork
-// Three steps, each over a group of threads (`id` of `n`): the whole grid of a kernel of its own for a large
-// table, or the one CTA that does all three in turn for a small one (a launch less saves more than the SMs
-// would: 64 forks in 72 rows of 250 pages took 14.5 us on the GPU as memset and four launches).
+// Three steps, each a kernel of its own for a large table; for a small one a single CTA does all three in turn (a
+// launch less saves more than the SMs would: 64 forks in 72 rows of 250 pages took 14.5 us on the GPU as memset and
+// four launches).
 //
 // Step 1, one warp per row: which fork overwrites the row (the first in order that names it), which
 // fork is the first to read it, and, for a row whose pages stay (not overwritten, or read), its pages
@@ -280,17 +282,94 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(ForkParams p) {
             static_cast<int>((gridDim.x * blockDim.x) >> 5));
 }
 
+int fork_small_bytes(int batch, int n_fork, int num_pages) {   // of shared memory
+  return batch * 16 + n_fork * (16 + 4 + 4 + 4) + (num_pages + 31) / 32 * 4;
+}
+
+// The three steps in one CTA, what they hand on in shared memory (in global memory: 10.4 against 8.0 us for 64 forks in
+// 72 rows of 250 pages, the copies in it).
 __global__ void __launch_bounds__(kPlanThreads) fork_small_kernel(ForkParams p) {
-  __shared__ uint32_t bitmap[kForkSmallPages / 32];
-  for (int w = threadIdx.x; w < (p.num_pages + 31) / 32; w += kPlanThreads) bitmap[w] = 0u;
+  extern __shared__ int4 fork_sm[];
+  int4* const info = fork_sm;
+  ForkParams q = p;
+  q.row_info = info;
+  q.outcome = info + p.batch;
+  q.fresh = reinterpret_cast<int32_t*>(q.outcome + p.n_fork);
+  int32_t* const src = q.fresh + p.n_fork;
+  int32_t* const dst = src + p.n_fork;
+  uint32_t* const bitmap = reinterpret_cast<uint32_t*>(dst + p.n_fork);
+  q.fork_src = src;
+  q.fork_dst = dst;
+  const int tid = threadIdx.x;
+  for (int w = tid; w < (p.num_pages + 31) / 32; w += kPlanThreads) bitmap[w] = 0u;
   pdl_wait();
   if (p.copies) pdl_launch_dependents();
+  for (int r = tid; r < p.batch; r += kPlanThreads) info[r] = make_int4(p.n_fork, p.n_fork, p.seq_lens[r], 0);
+  for (int i = tid; i < p.n_fork; i += kPlanThreads) {
+    src[i] = p.fork_src[i];
+    dst[i] = p.fork_dst[i];
+  }
   __syncthreads();
-  fork_mark(p, bitmap, threadIdx.x >> 5, kPlanThreads / 32);
-  __syncthreads();   // the bitmap, and row_info and row_keep in global memory (same CTA)
-  fork_plan(p, bitmap);
-  __syncthreads();   // outcome
-  fork_rows(p, threadIdx.x >> 5, kPlanThreads / 32);
+  for (int i = tid; i < p.n_fork; i += kPlanThreads) {
+    const int s = src[i], d = dst[i];
+    if (s < 0 || s >= p.batch || d < 0 || d >= p.batch) continue;
+    atomicMin(&info[d].x, i);   // the fork that overwrites the row, and the first that reads it
+    atomicMin(&info[s].y, i);
+  }
+  __syncthreads();
+  // a warp a row (the table taken as one run of entries: 10 to 14 us), kBatch loads of a lane in flight before the
+  // stores, which may be to the same memory for all the compiler knows
+  constexpr int kBatch = 8;
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int row = warp; row < p.batch; row += kPlanThreads / 32) {
+    const int4 ri = info[row];
+    const bool over = ri.x < p.n_fork;
+    if (over && ri.y >= p.n_fork) continue;
+    const int32_t* const bt = p.block_table + row * p.max_pages;
+    for (int j0 = lane; j0 < p.max_pages; j0 += kBatch * 32) {
+      int pg[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) pg[k] = j0 + k * 32 < p.max_pages ? bt[j0 + k * 32] : -1;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (over && j0 + k * 32 < p.max_pages) p.row_keep[row * p.max_pages + j0 + k * 32] = pg[k];
+        if (pg[k] >= 0 && pg[k] < p.num_pages) atomicOr(bitmap + (pg[k] >> 5), 1u << (pg[k] & 31));
+        else if (pg[k] >= p.num_pages) raise_status(p.status, NBX_DEV_BAD_PAGE);
+      }
+    }
+  }
+  __syncthreads();   // the bitmap, and row_keep in global memory (same CTA)
+  fork_plan(q, bitmap);
+  __syncthreads();   // the outcomes
+  for (int i = warp; i < p.n_fork; i += kPlanThreads / 32) {
+    const int4 o = q.outcome[i];
+    if (o.x == kForkNone) continue;
+    const int32_t* const from = (info[src[i]].x < p.n_fork ? p.row_keep : p.block_table) + src[i] * p.max_pages;
+    int32_t* const to = p.block_table + dst[i] * p.max_pages;
+    const int len = o.x == kForkEmpty ? 0 : o.z;
+    const int pages = (len + p.page_tokens - 1) / p.page_tokens;   // len <= max_pages * page_tokens
+    for (int j0 = lane; j0 < p.max_pages; j0 += kBatch * 32) {
+      int pg[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int j = j0 + k * 32;
+        pg[k] = j >= pages ? -1 : (o.x == kForkCopy && j == pages - 1 ? o.w : from[j]);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (j0 + k * 32 < p.max_pages) to[j0 + k * 32] = pg[k];
+    }
+    if (lane == 0) p.seq_lens[dst[i]] = len;
+  }
+}
+
+// Raises a kernel's shared-memory limit, once per device.
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& configured) {
+  const uint64_t bit = 1ull << (device_info().device & 63);
+  if (configured.load() & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) configured.fetch_or(bit);
+  return e;
 }
 
 // ------------------------------------------------------------------------------------ compaction
@@ -564,16 +643,6 @@ CompactLayout compact_layout(int64_t num_pages) {
   w.total = off;
   return w;
 }
-// Raises compact_small_kernel's shared-memory limit, once per device.
-cudaError_t compact_small_smem() {
-  static std::atomic<uint64_t> configured{0};
-  const uint64_t bit = 1ull << (device_info().device & 63);
-  if (configured.load() & bit) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(compact_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCompactSmallPages * 6);
-  if (e == cudaSuccess) configured.fetch_or(bit);
-  return e;
-}
 bool table_ok(int batch, int max_pages) {
   return batch >= 0 && max_pages >= 1 && static_cast<int64_t>(batch) * max_pages <= 0x7fffffffll;
 }
@@ -642,9 +711,14 @@ NBX_API int nbx_paged_kv_fork(int32_t* block_table, int max_pages, int32_t* seq_
   p.page_tokens = page_tokens;
   p.copies = copies;
   cudaError_t e;
-  if (static_cast<int64_t>(batch) * max_pages <= kSmallTable && num_pages <= kForkSmallPages &&
-      static_cast<int64_t>(batch) * n_fork <= kForkSmallWork) {
-    e = launch_pdl(fork_small_kernel, 1u, kPlanThreads, 0, st, p);
+  if (static_cast<int64_t>(batch) * max_pages <= kSmallTable && batch <= kForkSmallRows && n_fork <= kForkSmallRows &&
+      num_pages <= kForkSmallPages) {
+    static std::atomic<uint64_t> configured{0};
+    e = allow_smem(reinterpret_cast<const void*>(fork_small_kernel),
+                   fork_small_bytes(kForkSmallRows, kForkSmallRows, kForkSmallPages), configured);
+    if (e == cudaSuccess)
+      e = launch_pdl(fork_small_kernel, 1u, kPlanThreads,
+                     static_cast<size_t>(fork_small_bytes(batch, n_fork, num_pages)), st, p);
     if (e == cudaSuccess && copies) e = launch_copy(copy_params(a, moves, n_moves, n_fork, status), st);
     return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
   }
@@ -700,7 +774,8 @@ NBX_API int nbx_paged_kv_compact(const int32_t* block_table, int32_t* new_block_
   const int64_t entries = static_cast<int64_t>(batch) * max_pages;
   cudaError_t e;
   if (entries <= kSmallTable && num_pages <= kCompactSmallPages) {
-    e = compact_small_smem();
+    static std::atomic<uint64_t> configured{0};
+    e = allow_smem(reinterpret_cast<const void*>(compact_small_kernel), kCompactSmallPages * 6, configured);
     if (e == cudaSuccess)
       e = launch_pdl(compact_small_kernel, 1u, kPlanThreads, (static_cast<size_t>(num_pages) + num_pages / 2) * 4, st, p);
     if (e == cudaSuccess && copies && max_moves > 0)

@@ -342,3 +342,29 @@ def test_calls_without_rows_or_forks_return_no_moves():
     assert c.tolist() == [0] and m.tolist() == [[-1, -1, -1]]
     new, m, c = nbx.nbx_paged_kv_compact(dev(np.zeros((0, 2))), none, *x)
     assert c.tolist() == [0, 0] and m.tolist() == [[-1, -1, -1]] * 4 and new.shape == (0, 2)
+
+
+def test_awkward_forks_in_a_table_of_many_rows():
+    # the cases above among 300 empty rows, more than one CTA's rows
+    rest = [0] * 300
+    check_fork([20, 33, 40, 50] + rest, [0, 1], [2, 3], 16, 4, spread=1.0, seed=5)
+    lens = [20, 33, 47, 50, 64, 5, 17] + rest
+    check_fork(lens, [1, 0, 2, 2, 2, 6, 6], [0, 1, 2, 3, 4, 5, 6], 16, 5, seed=6)
+    check_fork(lens, [3, 3, 3, 3, 3, 3, 3], [6, 5, 4, 3, 2, 1, 0], 16, 5, seed=7)
+    check_fork([20, 40, 0, 0] + rest, [0, 1], [2, 3], 16, 6, reserve=2, seed=8)
+    check_fork([20, 33, 0, 0, 0, 0] + rest, [0, 1, 0, 1], [2, 3, 4, 5], 16, 3, spread=1.0, seed=9, bits=nbx.DEV_NO_PAGE)
+    check_fork([20, 33, 7, 0] + rest, [0, 304, 1, -1], [3, 2, 999, 2], 16, 3, seed=10, bits=nbx.DEV_BAD_ROW)
+    check_fork([20, 33, 0, 0] + rest, [0, 1, 1], [2, 2, 3], 16, 3, seed=11, bits=nbx.DEV_BAD_ROW)
+
+
+@pytest.mark.parametrize("rows,width", [(256, 256), (257, 256), (256, 257), (200, 5), (1, 4000)])
+def test_fork_around_one_ctas_table(rows, width):
+    g = np.random.default_rng(rows + width)
+    lens = list(g.integers(0, min(width, 40) * 16 + 1, rows))
+    dst = g.permutation(rows)[: max(1, rows // 2)]
+    check_fork(lens, list(g.integers(0, rows, len(dst))), list(dst), 16, width, h=1, d=16, seed=rows)
+
+
+@pytest.mark.parametrize("num_pages", [12287, 12288, 12289])
+def test_compact_around_one_ctas_pages(num_pages):
+    test_compact_over_the_scan_chunks(num_pages)
