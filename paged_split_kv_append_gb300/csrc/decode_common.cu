@@ -1,5 +1,6 @@
 // The split plan kernel, the standalone merge kernel, the workspace layout and the
 // decode launch sequence (plan, then the persistent partial kernel).
+#include <atomic>
 #include <climits>
 #include <cuda_fp16.h>
 
@@ -17,6 +18,15 @@ constexpr int kSortMax = 2048;   // batches up to this size are planned in share
 inline size_t plan_smem_bytes(int batch) {
   return batch <= kSortMax ? static_cast<size_t>(5 * batch + 1) * sizeof(int) : 0;
 }
+// With key ranges two arrays more, and the entries and keys of what the plan puts in order.
+constexpr bool plan_orders(int batch, bool tc) { return tc && batch <= kOrderMax; }
+inline size_t plan_ranges_smem_bytes(int batch, bool tc) {
+  if (batch > kSortMax) return 0;
+  return static_cast<size_t>((7 * batch + 4) & ~3) * sizeof(int) + (plan_orders(batch, tc) ? kOrderMax * 20 : 0);
+}
+constexpr int kPlanMaxSmem = 64 << 10;
+static_assert((7 * kSortMax + 4) * 4 <= kPlanMaxSmem && (7 * kOrderMax + 4) * 4 + kOrderMax * 20 <= kPlanMaxSmem,
+              "the plan's shared memory");
 
 // Positions per split of the SIMT partial kernel: two of the pages' splits (NBX_SPLIT_POSITIONS).
 // Each work unit of the persistent kernel pays about 2.4 us at its boundaries (the cross-warp merge
@@ -108,10 +118,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   const int align = p.page_tokens <= NBX_SPLIT_POSITIONS ? p.page_tokens : NBX_SPLIT_POSITIONS;
   __shared__ long long s_total;
   __shared__ int s_multi;
-  // X: the ranges of a small call, and its entries' {b, start, end}, where the steps below read them again
-  __shared__ int2 s_range[X && TC ? kOrderMax : 1];
-  __shared__ int4 s_entry[X && TC ? kOrderMax : 1];
-  const bool kept = X && TC && static_cast<int64_t>(B) * p.range_tiles <= kOrderMax;
+  // with key ranges: the first and one past the last key that a sequence's rows see; then, where the work is put in
+  // order, its entries' {b, start, end} and the pairs' keys
+  int* const s_lo = s_base + B + 1;
+  int* const s_hi = s_lo + B;
+  int4* const s_entry = reinterpret_cast<int4*>(plan_sm + ((7 * B + 4) & ~3));
   if (tid == 0) {
     s_empty = 0;
     s_nb = 0;
@@ -124,46 +135,68 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   }
   __syncthreads();
   if constexpr (X) {
-    if (ranges) {   // a warp per (sequence, M tile), or per sequence: the keys its rows see between them
-      for (int64_t it = warp; it < static_cast<int64_t>(B) * p.range_tiles; it += kPlanThreads / 32) {
-        const int b = static_cast<int>(it / p.range_tiles);
+    if (ranges) {
+      // the keys that the rows of a (sequence, M tile), or of a sequence, see between them: `width` lanes to each (a
+      // whole warp for a single row made 1024 rows 115 us)
+      if (small) {
+        for (int b = tid; b < B; b += kPlanThreads) {
+          s_lo[b] = INT_MAX;
+          s_hi[b] = 0;
+        }
+        __syncthreads();
+      }
+      const int most = p.range_tiles == 1 ? p.rows : kMmaRowsPerTile / p.group + 2;   // rows of a tile
+      int width = 1;
+      while (width < most && width < 32) width <<= 1;
+      const int per_warp = 32 / width;
+      const int64_t items = static_cast<int64_t>(B) * p.range_tiles;
+      for (int64_t i0 = warp * per_warp; i0 < items; i0 += kPlanThreads / 32 * per_warp) {
+        const int64_t it = i0 + lane / width;
+        const int b = it < items ? static_cast<int>(it / p.range_tiles) : 0;
         const int mt = static_cast<int>(it - static_cast<int64_t>(b) * p.range_tiles);
         const int L = p.seq_lens[b];
-        const bool fit = L >= 0 && L <= p.max_seq_len && static_cast<int64_t>(L) <= cap;
+        const bool fit = it < items && L >= 0 && L <= p.max_seq_len && static_cast<int64_t>(L) <= cap;
         const int r0 = mt * kMmaRowsPerTile / p.group;
         const int r1 = p.range_tiles == 1 ? p.rows : min(p.rows, ((mt + 1) * kMmaRowsPerTile + p.group - 1) / p.group);
         int lo = INT_MAX, hi = 0;
-        for (int r = r0 + lane; r < r1; r += 32) {
-          const KeyRange kr = key_range(p, b, r, fit ? L : 0);
-          if (kr.hi > kr.lo) {
-            lo = min(lo, kr.lo);
-            hi = max(hi, kr.hi);
+        if (fit) {
+          for (int r = r0 + (lane & (width - 1)); r < r1; r += width) {
+            const KeyRange kr = key_range(p, b, r, L);
+            if (kr.hi > kr.lo) {
+              lo = min(lo, kr.lo);
+              hi = max(hi, kr.hi);
+            }
           }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
+        for (int o = width >> 1; o > 0; o >>= 1) {
           lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
           hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
-        const int2 r = hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
-        if (lane == 0) {
-          p.ranges[it] = r;
-          if (kept) s_range[it] = r;
+        if (it < items && (lane & (width - 1)) == 0) {
+          p.ranges[it] = hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
+          if (small && hi > lo) {
+            atomicMin(&s_lo[b], lo);
+            atomicMax(&s_hi[b], hi);
+          }
         }
       }
-      __syncthreads();   // orders the ranges' global writes before this CTA's reads
+      __syncthreads();   // orders the ranges' writes before this CTA's reads
     }
   }
   // the positions of sequence b that are read: its length, or its rows' range from an aligned start
   auto reach = [&](int b, int L) -> int2 {
     if (!ranges) return make_int2(0, L);
     int lo = INT_MAX, hi = 0;
-    for (int mt = 0; mt < p.range_tiles; ++mt) {
-      const int64_t i = static_cast<int64_t>(b) * p.range_tiles + mt;
-      const int2 r = kept ? s_range[i] : p.ranges[i];
-      if (r.y > r.x) {
-        lo = min(lo, r.x);
-        hi = max(hi, r.y);
+    if (small) {
+      lo = s_lo[b];
+      hi = s_hi[b];
+    } else {
+      for (int mt = 0; mt < p.range_tiles; ++mt) {
+        const int2 r = p.ranges[static_cast<int64_t>(b) * p.range_tiles + mt];
+        if (r.y > r.x) {
+          lo = min(lo, r.x);
+          hi = max(hi, r.y);
+        }
       }
     }
     return hi > 0 ? make_int2(lo / align * align, min(hi, L)) : make_int2(0, 0);
@@ -350,7 +383,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     en.pad0 = en.pad1 = 0;
     p.entries[e] = en;
     if constexpr (X && TC) {
-      if (e < kOrderMax) s_entry[e] = make_int4(en.b, en.start, en.end, 0);
+      if (ranges && e < kOrderMax && plan_orders(B, TC)) s_entry[e] = make_int4(en.b, en.start, en.end, 0);
     }
   }
   if (tid == 0) p.header[0] = total;
@@ -358,31 +391,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   // them. Most keys first, dealt to the CTAs there and back, the longest CTA of 512 rows of documents of up to
   // 1500 positions (256 units) reads 31 tiles where it read 39.
   if constexpr (TC && X) {
-    __shared__ int4 s_cost[kOrderMax / 4];
+    int4* const s_cost = s_entry + kOrderMax;
     int* const cost = reinterpret_cast<int*>(s_cost);
     const int64_t all = static_cast<int64_t>(total) * p.range_tiles;
-    if (ranges && kept && !p.tc_round_up && all <= kOrderMax && all * p.h_kv > p.tc_units) {
+    if (ranges && plan_orders(B, TC) && !p.tc_round_up && all <= kOrderMax && all * p.h_kv > p.tc_units) {
       const int items = static_cast<int>(all);
       __syncthreads();
       for (int i = tid; i < (items + 3) / 4 * 4; i += kPlanThreads) {
         int c = -1;
         if (i < items) {
           const int4 en = s_entry[i / p.range_tiles];
-          const int2 r = s_range[en.x * p.range_tiles + i % p.range_tiles];
+          const int2 r = p.ranges[en.x * p.range_tiles + i % p.range_tiles];
           c = max(0, min(en.z, r.y) - max(en.y, r.x));
         }
         cost[i] = c;
       }
       __syncthreads();
-      if (tid < items) {
-        const int c = cost[tid];
+      for (int x = tid; x < items; x += kPlanThreads) {
+        const int c = cost[x];
         int rank = 0;
         for (int i = 0; i < items; i += 4) {   // stable: ties keep their order
           const int4 o = s_cost[i / 4];
-          rank += (o.x > c || (o.x == c && i < tid)) + (o.y > c || (o.y == c && i + 1 < tid)) +
-                  (o.z > c || (o.z == c && i + 2 < tid)) + (o.w > c || (o.w == c && i + 3 < tid));
+          rank += (o.x > c || (o.x == c && i < x)) + (o.y > c || (o.y == c && i + 1 < x)) +
+                  (o.z > c || (o.z == c && i + 2 < x)) + (o.w > c || (o.w == c && i + 3 < x));
         }
-        p.order[rank] = tid;
+        p.order[rank] = x;
       }
       if (tid == 0) p.header[3] = items;
     }
@@ -776,9 +809,23 @@ cudaError_t bounds_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
 
 template <bool X>
 cudaError_t launch_plan(const DecodeParams& p, cudaStream_t stream) {
-  const size_t smem = plan_smem_bytes(p.batch);
-  return p.tc_units > 0 ? launch_pdl(plan_kernel<true, X>, 1u, kPlanThreads, smem, stream, p)
-                        : launch_pdl(plan_kernel<false, X>, 1u, kPlanThreads, smem, stream, p);
+  const bool tc = p.tc_units > 0;
+  size_t smem = plan_smem_bytes(p.batch);
+  if (X && (p.key_begin != nullptr || p.key_end != nullptr)) {
+    static std::atomic<uint64_t> configured{0};   // devices whose shared-memory limit is raised
+    const uint64_t bit = 1ull << (device_info().device & 63);
+    if ((configured.load() & bit) == 0) {
+      cudaError_t e =
+          cudaFuncSetAttribute(plan_kernel<true, X>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanMaxSmem);
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(plan_kernel<false, X>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanMaxSmem);
+      if (e != cudaSuccess) return e;
+      configured.fetch_or(bit);
+    }
+    smem = plan_ranges_smem_bytes(p.batch, tc);
+  }
+  return tc ? launch_pdl(plan_kernel<true, X>, 1u, kPlanThreads, smem, stream, p)
+            : launch_pdl(plan_kernel<false, X>, 1u, kPlanThreads, smem, stream, p);
 }
 
 template <bool X, int N>

@@ -564,6 +564,7 @@ def test_large_bf16_values_stay_finite():
 @pytest.mark.parametrize("pool,rows,h_q,h_kv,batch,longest", [
     ("bf16", 128, 16, 4, 10, 700),       # 160 units, dealt out by their keys
     ("block", 128, 16, 4, 10, 700),
+    ("bf16", 32, 16, 1, 100, 150),       # 400 M tiles: more than the plan's threads, fewer than it sorts
     ("bf16", 32, 16, 1, 131, 150),       # more M tiles than the plan sorts
 ])
 def test_windows_of_many_units_over_key_ranges(pool, rows, h_q, h_kv, batch, longest):
@@ -579,3 +580,12 @@ def test_windows_of_many_units_over_key_ranges(pool, rows, h_q, h_kv, batch, lon
             assert torch.equal(c.call("bf16", **mod), out)
         finally:
             nbx.nbx_set_decode_grid_limit(0)
+
+
+@pytest.mark.parametrize("batch,rows", [(700, 1), (2048, 1), (2049, 1), (300, 3), (70, 40)])
+@pytest.mark.parametrize("pool", ["f32", "bf16"])
+def test_key_ranges_of_large_batches(pool, batch, rows):
+    lens = np.random.default_rng(batch).integers(0, 60, batch)
+    c = Case(pool, "f32" if pool == "f32" else "bf16", rows, 2, 1, 64, 16, lens, seed=89)
+    c.check(**made(dict(mask="random"), c.lens, rows, 2))
+    c.check(**made(dict(mask="window", softcap=4.0), c.lens, rows, 2))
