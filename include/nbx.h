@@ -440,6 +440,21 @@ NBX_API int nbx_paged_kv_compact(const int32_t* block_table, int32_t* new_block_
                                  int scale_tokens, int32_t* moves, int max_moves, int32_t* counts, void* workspace,
                                  size_t workspace_bytes, int32_t* status, void* stream);
 
+/*
+ * nbx_call -- one of the calls above from an array of its arguments, for bindings to which every argument of a
+ * call costs (from Python it saves a call of twenty arguments 1 us of 10). args[i] is argument i: a pointer or an
+ * integer as it is, a float as the bits of a double. An unknown call returns NBX_ERR_VALUE.
+ */
+enum nbx_callable {
+  NBX_CALL_APPEND_BLOCK_SCALED = 0,
+  NBX_CALL_DECODE_BLOCK_SCALED = 1,
+  NBX_CALL_DECODE_MODIFIED = 2,
+  NBX_CALL_COPY_PAGES = 3,
+  NBX_CALL_FORK = 4,
+  NBX_CALL_COMPACT = 5
+};
+NBX_API int nbx_call(int call, const int64_t* args);
+
 /* Bytes of device scratch that libnbx keeps for nbx_paged_decode_attn_noalloc (32 MiB). */
 #define NBX_NOALLOC_SCRATCH_BYTES (32u * 1024u * 1024u)
 

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -119,6 +120,8 @@ def _declare(l):
     l.nbx_paged_kv_compact.argtypes = [vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp,
                                        vp, sz, vp, vp]
     l.nbx_paged_kv_compact.restype = i32
+    l.nbx_call.argtypes = [i32, ctypes.c_char_p]
+    l.nbx_call.restype = i32
     l.nbx_status_string.argtypes = [i32]
     l.nbx_status_string.restype = ctypes.c_char_p
     l.nbx_abi_version.argtypes = []
@@ -459,7 +462,7 @@ def _misfit(names: str, *tensors):
 
 
 def _p(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
 
 
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -473,15 +476,28 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     return t
 
 
+_calls = {}   # entry point -> its number in nbx_call, and what packs its arguments
+_CALLS = ("nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
+          "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork", "nbx_paged_kv_compact")
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _callable(func: str):
+    types = getattr(lib(), func).argtypes
+    form = struct.Struct("=" + "".join("d" if t is ctypes.c_float else "q" for t in types))
+    _calls[func] = _CALLS.index(func), form.pack
+    return _calls[func]
+
+
 def _run(func: str, dev: int, stream, *args):
     """Calls the entry point on device `dev` and the given (or its current) stream, the last argument."""
     st = _raw_stream(dev) if stream is None else getattr(stream, "cuda_stream", stream)
-    f = getattr(_lib or lib(), func)
-    if torch.cuda.current_device() == dev:
-        code = f(*args, st)
+    call, pack = _calls.get(func) or _callable(func)
+    if _current_device() == dev:
+        code = _lib.nbx_call(call, pack(*args, st))
     else:
         with torch.cuda.device(dev):
-            code = f(*args, st)
+            code = _lib.nbx_call(call, pack(*args, st))
     if code:
         raise NbxError(func, code)
 

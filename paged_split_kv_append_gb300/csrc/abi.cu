@@ -7,7 +7,10 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <mutex>
+#include <type_traits>
+#include <utility>
 
 #include "nbx_internal.h"
 
@@ -439,6 +442,44 @@ NBX_API int nbx_paged_decode_step(const void* q, int q_dtype, int batch, int row
   return decode_call(q, q_dtype, batch, rows, h_q, d, k_pool, v_pool, pool_dtype, num_pages, h_kv, page_tokens,
                      block_table, max_pages, lens, max_seq_len, scale, k_scale, v_scale, out, workspace,
                      workspace_bytes, status, st, false, lens, rows);
+}
+
+}  // extern "C"
+
+template <class T>
+static T argument(int64_t a) {
+  if constexpr (std::is_pointer_v<T>) {
+    return reinterpret_cast<T>(static_cast<uintptr_t>(a));
+  } else if constexpr (std::is_same_v<T, float>) {
+    double d;
+    std::memcpy(&d, &a, sizeof(d));
+    return static_cast<float>(d);
+  } else {
+    return static_cast<T>(a);
+  }
+}
+template <class... A, size_t... I>
+static int call_with(int (*f)(A...), const int64_t* a, std::index_sequence<I...>) {
+  return f(argument<A>(a[I])...);
+}
+template <class... A>
+static int call_with(int (*f)(A...), const int64_t* a) {
+  return call_with(f, a, std::index_sequence_for<A...>{});
+}
+
+extern "C" {
+
+NBX_API int nbx_call(int call, const int64_t* args) {
+  if (args == nullptr) return NBX_ERR_NULL;
+  switch (call) {
+    case NBX_CALL_APPEND_BLOCK_SCALED: return call_with(nbx_paged_kv_append_block_scaled, args);
+    case NBX_CALL_DECODE_BLOCK_SCALED: return call_with(nbx_paged_decode_attn_block_scaled, args);
+    case NBX_CALL_DECODE_MODIFIED: return call_with(nbx_paged_decode_attn_modified, args);
+    case NBX_CALL_COPY_PAGES: return call_with(nbx_paged_kv_copy_pages, args);
+    case NBX_CALL_FORK: return call_with(nbx_paged_kv_fork, args);
+    case NBX_CALL_COMPACT: return call_with(nbx_paged_kv_compact, args);
+    default: return NBX_ERR_VALUE;
+  }
 }
 
 NBX_API int nbx_paged_decode_merge(const float* acc_part, const float* m_part, const float* l_part, int n_rows,

@@ -217,6 +217,27 @@ def test_a_cap_past_the_range_is_refused(lib):
         assert call(f, args, softcap=3e38) == -8
 
 
+def test_calls_from_an_array_of_arguments(lib):
+    import struct
+    assert lib.nbx_call(99, b"") == -8 and lib.nbx_call(0, None) == -1
+
+    def packed(number, name, args, **kw):
+        a = {**args, **kw}
+        types = getattr(lib, name).argtypes
+        raw = [getattr(v, "value", v) or 0 for v in a.values()]
+        form = "=" + "".join("d" if t is ctypes.c_float else "q" for t in types)
+        return lib.nbx_call(number, struct.pack(form, *raw))
+
+    for number, (name, args) in enumerate([
+            ("nbx_paged_kv_append_block_scaled", APPEND), ("nbx_paged_decode_attn_block_scaled", BLOCK),
+            ("nbx_paged_decode_attn_modified", MODIFIED), ("nbx_paged_kv_copy_pages", COPY),
+            ("nbx_paged_kv_fork", FORK), ("nbx_paged_kv_compact", COMPACT)]):
+        for kw in (dict(num_pages=0), dict(k_pool=FAKE_ODD), dict(k_pool=NULL), dict(d=7), dict(page_tokens=0)):
+            assert packed(number, name, args, **kw) == call(getattr(lib, name), args, **kw) < 0
+    for kw in (dict(softcap=-1.0), dict(scale=float("nan")), dict(softcap=1e-40)):   # floats
+        assert packed(2, "nbx_paged_decode_attn_modified", MODIFIED, **kw) == -8
+
+
 # ------------------------------------------------------------------------- the session
 def test_session_refusals():
     from paged_split_kv_append_gb300.session import PagedDecodeSession
