@@ -1,5 +1,6 @@
 // The split plan kernel, the standalone merge kernel, the workspace layout and the
 // decode launch sequence (plan, then the persistent partial kernel).
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cuda_fp16.h>
@@ -872,8 +873,11 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
   else if (pool_dtype == NBX_BF16) e = decode_dispatch_BF16(q, q_dtype, grid_limit, stream);
   else e = decode_dispatch_E4M3(q, q_dtype, grid_limit, stream);
   if (e != cudaSuccess) return e;
-  // every sequence has one split: the partials are the output (but for rows a modified window marked)
-  if (q.max_splits <= 1 && !(x && mma)) return cudaSuccess;
+  // every sequence has one split: the partials are the output (but for rows a modified window marked). A modified
+  // decode's workspace has room for splits of 64 positions; the plan's own rules say how many there can be.
+  int most = q.max_splits;
+  if (x && !mma) most = std::min(most, warps ? q.max_seq_len / 64 : (q.max_seq_len - 1) / kSimtSplitPositions + 1);
+  if (most <= 1 && !(x && mma)) return cudaSuccess;
   const int64_t items = static_cast<int64_t>(q.batch) * q.h_kv * q.row_blocks * kQB * ((q.d / 4 + 31) / 32);
   int64_t grid = static_cast<int64_t>(device_info().sm_count) * 24;
   if (grid > items) grid = items;
