@@ -432,28 +432,27 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 
 
 def _one_device(names: str, *tensors) -> int:
-    """The index of the CUDA device that all the given tensors (None skipped) sit on; contiguous all."""
-    dev = -2
-    for i, t in enumerate(tensors):
-        if t is None:
-            continue
-        d = t.get_device()
-        if d != dev or not t.is_contiguous():
-            name = names.split()[i]
-            if d < 0:
+    """The index of the CUDA device that all the given tensors (None skipped, the first is one) sit on; contiguous
+    all."""
+    dev = tensors[0].get_device()
+    if dev < 0 or [1 for t in tensors if t is not None and (t.get_device() != dev or not t.is_contiguous())]:
+        for name, t in zip(names.split(), tensors):
+            if t is None:
+                continue
+            if t.get_device() < 0:
                 raise ValueError(f"{name} must be a CUDA tensor")
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
-            if dev >= 0:
-                raise ValueError(f"{name} is on cuda:{d}, not on cuda:{dev}")
-            dev = d
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on cuda:{t.get_device()}, not on cuda:{dev}")
     return dev
 
 
-def _int32(names: str, *tensors):
-    for i, t in enumerate(tensors):
-        if t is not None and t.dtype is not torch.int32:
-            raise ValueError(f"{names.split()[i]} must be int32")
+def _int32(names: str, *tensors, int32=torch.int32):
+    if [1 for t in tensors if t is not None and t.dtype is not int32]:
+        for name, t in zip(names.split(), tensors):
+            if t is not None and t.dtype is not int32:
+                raise ValueError(f"{name} must be int32")
 
 
 def _misfit(names: str, *tensors):
