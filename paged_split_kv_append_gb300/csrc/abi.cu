@@ -116,12 +116,7 @@ static bool decode_shape_ok(int batch, int rows, int h_q, int h_kv, int d, int m
   return true;
 }
 
-NBX_API int nbx_paged_decode_partial_kernel(int q_dtype, int pool_dtype, int rows, int h_q, int h_kv, int d,
-                                            int num_pages, int page_tokens) {
-  if (!decode_shape_ok(1, rows, h_q, h_kv, d, 0) || num_pages < 1 || page_tokens < 1) return NBX_ERR_SHAPE;
-  if ((page_tokens % NBX_TILE_POSITIONS) != 0) return NBX_ERR_PAGE_ALIGN;
-  if (q_dtype != NBX_F32 && q_dtype != NBX_BF16) return NBX_ERR_DTYPE;
-  if (pool_dtype != NBX_F32 && pool_dtype != NBX_BF16 && pool_dtype != NBX_E4M3) return NBX_ERR_DTYPE;
+static DecodeParams kernel_choice(int rows, int h_q, int h_kv, int d, int num_pages, int page_tokens) {
   DecodeParams p = {};
   p.rows = rows;
   p.h_q = h_q;
@@ -131,6 +126,16 @@ NBX_API int nbx_paged_decode_partial_kernel(int q_dtype, int pool_dtype, int row
   p.num_pages = num_pages;
   p.page_tokens = page_tokens;
   p.qk_scale_log2 = 1.f;   // a positive softmax scale
+  return p;
+}
+
+NBX_API int nbx_paged_decode_partial_kernel(int q_dtype, int pool_dtype, int rows, int h_q, int h_kv, int d,
+                                            int num_pages, int page_tokens) {
+  if (!decode_shape_ok(1, rows, h_q, h_kv, d, 0) || num_pages < 1 || page_tokens < 1) return NBX_ERR_SHAPE;
+  if ((page_tokens % NBX_TILE_POSITIONS) != 0) return NBX_ERR_PAGE_ALIGN;
+  if (q_dtype != NBX_F32 && q_dtype != NBX_BF16) return NBX_ERR_DTYPE;
+  if (pool_dtype != NBX_F32 && pool_dtype != NBX_BF16 && pool_dtype != NBX_E4M3) return NBX_ERR_DTYPE;
+  const DecodeParams p = kernel_choice(rows, h_q, h_kv, d, num_pages, page_tokens);
   if (!mma_path_applies(p, q_dtype, pool_dtype)) return NBX_PARTIAL_SIMT;
   return pool_dtype == NBX_E4M3 ? NBX_PARTIAL_TCGEN05_FP8 : NBX_PARTIAL_TCGEN05;
 }
@@ -140,7 +145,10 @@ NBX_API int nbx_paged_decode_modified_partial_kernel(int q_dtype, int pool_dtype
   const int k = nbx_paged_decode_partial_kernel(q_dtype, pool_dtype, rows, h_q, h_kv, d, num_pages, page_tokens);
   if (k < 0) return k;
   if (out_dtype != NBX_F32 && out_dtype != NBX_BF16) return NBX_ERR_DTYPE;
-  if (k == NBX_PARTIAL_TCGEN05 || (k == NBX_PARTIAL_TCGEN05_FP8 && out_dtype == NBX_BF16)) return k;
+  DecodeParams p = kernel_choice(rows, h_q, h_kv, d, num_pages, page_tokens);
+  p.out_bf16 = out_dtype == NBX_BF16;
+  if (mma_path_applies_modified(p, q_dtype, pool_dtype))
+    return pool_dtype == NBX_E4M3 ? NBX_PARTIAL_TCGEN05_FP8 : NBX_PARTIAL_TCGEN05;
   return warp_path_applies(q_dtype, pool_dtype) ? NBX_PARTIAL_WARP : NBX_PARTIAL_SIMT;
 }
 

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
       // units taken from a counter may pass one wave by a few, but must not be long: their splits round up
       if (X && p.tc_round_up) num += den - 1;
       const long long want = num / den;
-      // (a window's splits also hold 256 positions, as the pages': 16 sequences of 200 positions under 64 rows took
+      // (a window has no more splits than the pages' rule gives: 16 sequences of 200 positions under 64 rows took
       // 23.4 us a call cut in two, 20.7 whole)
       int cap_s = min(p.max_splits, max(1, L / 64));
       if (X && !p.tc_round_up) cap_s = min(cap_s, (L - 1) / NBX_SPLIT_POSITIONS + 1);

@@ -589,3 +589,15 @@ def test_key_ranges_of_large_batches(pool, batch, rows):
     c = Case(pool, "f32" if pool == "f32" else "bf16", rows, 2, 1, 64, 16, lens, seed=89)
     c.check(**made(dict(mask="random"), c.lens, rows, 2))
     c.check(**made(dict(mask="window", softcap=4.0), c.lens, rows, 2))
+
+
+@pytest.mark.parametrize("pool,rows,h_q,h_kv,d,P,T", [
+    ("bf16", 12, 8, 2, 128, 64, 0), ("block", 15, 4, 1, 128, 64, 64), ("e4m3", 10, 8, 2, 128, 128, 0),
+    ("bf16", 6, 12, 2, 256, 64, 0), ("block", 8, 4, 1, 256, 64, 16), ("e4m3", 11, 6, 2, 256, 64, 0)])
+def test_small_windows_with_a_bf16_output(pool, rows, h_q, h_kv, d, P, T):
+    """Windows of 32 to 63 query vectors of a KV head: on the tensor cores for a bf16 output alone."""
+    c = Case(pool, "bf16", rows, h_q, h_kv, d, P, (0, 1, 63, 200, 1500), T, seed=90)
+    assert on_tensor_cores(c, "bf16") and not on_tensor_cores(c, "f32")
+    for mod in (MODS[0], MODS[1], MODS[5], MODS[6]):
+        c.check("bf16", P_WEIGHT[pool], **made(mod, c.lens, rows, h_q))
+        c.check("f32", **made(mod, c.lens, rows, h_q))
