@@ -241,7 +241,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
       // about tc_units units in all, shared in proportion to the lengths (the grid's one wave); a
       // split keeps at least 64 positions (the tensor-core tile), and a sequence has at most the
       // workspace's partial slots (max_splits, the pages' rule at the longest length)
-      long long num = static_cast<long long>(p.tc_units) * L;
+      long long aim = p.tc_units;
+      if constexpr (X) {
+        // A pair of a sequence has few units then, and one split more for each may be a second round for some warps:
+        // three rounds, if the units stay long enough (32 sequences of 2048 positions with 32 KV heads, 2 splits or 5:
+        // 204 and 159 us; 64 ragged ones of up to 2048 with 8, where they would not: 56 and 58).
+        if (p.tc_round_up && 5ll * p.tc_pairs * B >= p.tc_warps && len_sum * p.tc_pairs >= 448ll * p.tc_warps)
+          aim += 2ll * p.tc_warps;
+      }
+      long long num = aim * L;
       const long long den = static_cast<long long>(p.tc_pairs) * len_sum;
       // units taken from a counter may pass one wave by a few, but must not be long: their splits round up
       if (X && p.tc_round_up) num += den - 1;
@@ -860,6 +868,7 @@ cudaError_t decode_dispatch(const DecodeParams& p, int q_dtype, int pool_dtype, 
     q.tc_pairs = p.h_kv * ((p.rows * p.group + kWarpUnitVectors - 1) / kWarpUnitVectors);
     const int64_t extra = static_cast<int64_t>(q.tc_pairs) * p.batch / 2;
     q.tc_units = extra < units / 2 ? units - static_cast<int>(extra) : units / 2;
+    q.tc_warps = units;
     q.tc_round_up = 1;
   }
   cudaError_t e = x ? launch_plan<true>(q, stream) : launch_plan<false>(q, stream);

@@ -10,7 +10,8 @@
 //  * Work unit = (split entry, KV head, 8 query vectors), taken by one warp from the list's counter. Warps
 //    share nothing: no barriers, no waits but for their own copies. Splits are sized for one unit a resident
 //    warp over the GPU (at least 64 positions each, at most 64 a sequence), rounded up: rounded down, some
-//    sequences' units were twice the mean (ragged bf16: 246 against 220 us).
+//    sequences' units were twice the mean (ragged bf16: 246 against 220 us). Three units a warp where pairs of a
+//    sequence and KV head are about as many as warps (the plan kernel says when).
 //  * What bounds it: of the 62 us of that kernel the copies alone take 55 (5.4 TB/s, with the first tiles'
 //    chain of loads and the tail; 44 us at the copy rate), the arithmetic alone 47.
 //  * Each warp streams its unit's 16-position tiles into a ring of its own in shared memory with 16-byte

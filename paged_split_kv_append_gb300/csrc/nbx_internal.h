@@ -214,6 +214,7 @@ struct DecodeParams {
   // len / 64)]
   int tc_units;
   int tc_pairs;
+  int tc_warps;      // warps that take units, of the one-warp kernel
   int tc_round_up;   // splits rounded up instead of down (units taken from the counter by single warps)
   // ---- read only by the kernels of the modified and block-scaled decodes (kScoreMod, kBlockScaled)
   int out_bf16;            // the output is bf16, rounded once from the fp32 result
