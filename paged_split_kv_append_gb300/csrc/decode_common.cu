@@ -76,17 +76,19 @@ bool workspace_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq
 }
 
 // The plan kernel may run while the kernel before it (a decode step's append, which reads the
-// lengths) still runs: it waits for that grid before the step's length advance, and before it
-// completes, so the kernels after it see the append's positions.
+// lengths; another decode's partial, where no merge follows it) still runs. Until it has waited for that
+// grid it only reads the lengths and works in shared memory: the workspace, the output and the advanced
+// lengths may all be memory that the grid ahead still uses. It has waited before it completes, so the kernels
+// after it see the append's positions.
 __device__ __forceinline__ void plan_finish(const DecodeParams& p) {
   pdl_wait();
   if (p.lens_out)   // the step's length advance; nothing later reads seq_lens
     for (int b = threadIdx.x; b < p.batch; b += blockDim.x) p.lens_out[b] = p.seq_lens[b] + p.len_add;
 }
 
-// Reads the device lengths, writes every sequence's plan (len, positions per split, non-empty
-// splits), zeroes the work counter, writes 0 to the output rows of empty sequences, and writes
-// the work list of (sequence, split) entries: every sequence's last split first, then the other
+// Reads the device lengths, cuts every sequence into splits, then (past the wait) writes every
+// sequence's plan (len, positions per split, non-empty splits), zeroes the work counter, writes 0 to
+// the output rows of empty sequences, and writes the work list of (sequence, split) entries: every sequence's last split first, then the other
 // splits, sequences with the longest splits first (stable), splits ascending. Batches above kSortMax
 // keep their own order and take a slower serial path.
 // TC: a tensor-core window, whose splits are sized by the call's total work (DecodeParams::tc_units);
@@ -105,13 +107,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   int* const s_base = s_order + p.batch;   // [batch + 1]
   __shared__ int s_warp[kPlanThreads / 32];
   __shared__ int s_empty;
+  __shared__ int s_bad;   // a length out of bounds
   __shared__ int s_nb;
   const int tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
   const int B = p.batch;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_tokens;
   const bool small = B <= kSortMax;
-  if constexpr (X) pdl_wait();
+  const bool waited = X || !small;
+  if (waited) pdl_wait();
   pdl_launch_dependents();   // the partial kernel may start its prologue now; it waits for this grid
   const bool ranges = X && (p.key_begin != nullptr || p.key_end != nullptr);
   // splits start on whole pages, or on 256-position boundaries when a page is longer (a
@@ -126,9 +130,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   int4* const s_entry = reinterpret_cast<int4*>(plan_sm + ((7 * B + 4) & ~3));
   if (tid == 0) {
     s_empty = 0;
+    s_bad = 0;
     s_nb = 0;
     if constexpr (TC) s_total = 0;
-    p.header[1] = 0;
+    if (waited) p.header[1] = 0;
     if constexpr (X) {
       p.header[3] = 0;
       s_multi = B > kSortMax;
@@ -224,9 +229,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   }
   for (int b = tid; b < B; b += kPlanThreads) {
     int L = p.seq_lens[b] + p.len_add;   // a decode step attends to its own new positions
-    if (p.ident_bt) p.ident_bt[b] = b;
     if (L < 0 || L > p.max_seq_len || static_cast<int64_t>(L) > cap) {
-      raise_status(p.status, NBX_DEV_BAD_LEN);
+      s_bad = 1;
       L = 0;
     }
     const int len = L;
@@ -268,7 +272,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     seg = ((seg + align - 1) / align) * align;
     const int n = L > 0 ? (L + seg - 1) / seg : 0;
     // kept in L2 for the merge, which reads the split counts after the K/V stream
-    st_global_hint(reinterpret_cast<int4*>(p.plan + b), make_int4(X ? len : L, seg, n, first), l2_evict_last_policy());
+    if (waited) {
+      if (p.ident_bt) p.ident_bt[b] = b;
+      st_global_hint(reinterpret_cast<int4*>(p.plan + b), make_int4(X ? len : L, seg, n, first), l2_evict_last_policy());
+    }
     if constexpr (X) {
       if (n > 1) s_multi = 1;
     }
@@ -285,7 +292,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
     if (tid == 0) p.header[2] = s_multi ? kMergeSplits : 0;
   }
   // a sequence with no position to read gets no work unit: its rows are written here (0)
-  if (s_empty) {
+  auto zero_empty_rows = [&]() {
+    if (!s_empty) return;
     // 16-byte pieces of a sequence's output (d is a multiple of 64)
     const int64_t row_vec4 = static_cast<int64_t>(p.rows) * p.h_q * p.d / (X && p.out_bf16 ? 8 : 4);
     for (int b = 0; b < B; ++b) {
@@ -293,10 +301,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
       float4* o = reinterpret_cast<float4*>(p.out) + b * row_vec4;
       for (int64_t x = tid; x < row_vec4; x += kPlanThreads) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  }
+  };
   if (!small) {
     // large batch: batch order, one thread writes the whole list
+    zero_empty_rows();
     if (tid == 0) {
+      if (s_bad) raise_status(p.status, NBX_DEV_BAD_LEN);
       int base = 0;
       for (int b = 0; b < B; ++b) {
         const SeqPlan sp = p.plan[b];
@@ -360,6 +370,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(DecodeParams p) {
   }
   if (tid == kPlanThreads - 1) s_base[B] = x + (warp > 0 ? s_warp[warp - 1] : 0);
   __syncthreads();
+  // ---- the wait (a modified decode's plan has waited already), then the global writes
+  pdl_wait();
+  if (!waited) {
+    for (int b = tid; b < B; b += kPlanThreads) {
+      if (p.ident_bt) p.ident_bt[b] = b;
+      st_global_hint(reinterpret_cast<int4*>(p.plan + b), make_int4(s_len[b], s_seg[b], s_n[b], 0), l2_evict_last_policy());
+    }
+    if (tid == 0) p.header[1] = 0;
+  }
+  if (tid == 0 && s_bad) raise_status(p.status, NBX_DEV_BAD_LEN);
+  zero_empty_rows();
   // the entries, in parallel: entry e belongs to the list position i with s_base[i] <= e < s_base[i+1]
   const int nb = s_nb;
   const int total = s_base[B] + nb;
