@@ -265,6 +265,8 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
     p.out_bf16 = mod->out_dtype == NBX_BF16;
     p.cap_log2 = mod->softcap * kLog2eHost;
     p.cap_inv = mod->softcap > 0.f ? 1.f / p.cap_log2 : 0.f;
+    const float factor = p.qk_scale_log2 * p.cap_inv;   // its ninth power times the cap: within 2^+-124
+    p.cap_folds = factor > 0x1p-12f && factor < 0x1p12f && p.cap_log2 > 0x1p-16f && p.cap_log2 < 0x1p16f;
     p.slopes = mod->slopes;
     p.key_begin = mod->key_begin;
     p.key_end = mod->key_end;

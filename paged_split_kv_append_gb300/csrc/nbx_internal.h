@@ -220,6 +220,7 @@ struct DecodeParams {
   int out_bf16;            // the output is bf16, rounded once from the fp32 result
   float cap_log2;          // softcap * log2(e), and its reciprocal; 0: no cap
   float cap_inv;
+  int cap_folds;           // qk_scale_log2 * cap_inv and the cap are near enough to 1 for a product with the ninth power
   const float* slopes;     // [h_q] bias per position of distance, or null
   const int32_t* key_begin;   // [batch, rows] first visible key and one past the last, or null (0, p + 1)
   const int32_t* key_end;
