@@ -216,6 +216,15 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
   WorkspaceLayout w;
   if (!workspace_layout(batch, rows, h_q, h_kv, d, max_seq_len, &w, mod != nullptr)) return NBX_ERR_SHAPE;
   if (workspace_bytes < w.total) return NBX_ERR_WORKSPACE;
+  int x = 0;
+  if (mod) {
+    const bool scored = mod->softcap > 0.f || mod->slopes || mod->key_begin || mod->key_end;
+    if (mod->block_scaled) x = kBlockScaled | (scored ? kScoreMod : 0);
+    // An fp32 output without a modification is the plain decode's, its splits included. An E4M3 pool's is not: the plain
+    // window holds weights to 2^-8, which only a bf16 output takes here.
+    else if (scored || mod->out_dtype == NBX_BF16 || pool_dtype == NBX_E4M3) x = kScoreMod;
+    else workspace_layout(batch, rows, h_q, h_kv, d, max_seq_len, &w);   // (no larger than the one above)
+  }
 
   char* ws = static_cast<char*>(workspace);
   DecodeParams p = {};
@@ -259,9 +268,7 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
     const double part_bytes = static_cast<double>(batch) * rows * h_q * w.max_splits * d * 4.0;
     p.keep_frac = static_cast<float>(part_bytes <= 67108864.0 ? 1.0 : 67108864.0 / part_bytes);
   }
-  int x = 0;
-  if (mod) {
-    const bool scored = mod->softcap > 0.f || mod->slopes || mod->key_begin || mod->key_end;
+  if (x) {
     p.out_bf16 = mod->out_dtype == NBX_BF16;
     p.cap_log2 = mod->softcap * kLog2eHost;
     p.cap_inv = mod->softcap > 0.f ? 1.f / p.cap_log2 : 0.f;
@@ -275,8 +282,6 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
     while (mod->block_scaled && (1 << p.scale_shift) < mod->scale_tokens) ++p.scale_shift;
     p.ranges = reinterpret_cast<int2*>(ws + w.ranges);
     p.order = reinterpret_cast<int32_t*>(ws + w.order);
-    // an fp32 output without a modification is the plain decode's
-    x = mod->block_scaled ? kBlockScaled | (scored ? kScoreMod : 0) : (scored || p.out_bf16 ? kScoreMod : 0);
   }
   const cudaError_t e = decode_dispatch(p, q_dtype, pool_dtype, x, g_grid_limit.load(), stream);
   return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
