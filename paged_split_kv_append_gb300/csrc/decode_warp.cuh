@@ -30,7 +30,7 @@
 //    they are, P as three bf16 terms, 2^-24. Sums are fp32, and results as near to 64 bits as the fp32 path's.
 //  * Block scales, caps, distances and key ranges as in the other kernels (a V block's scale goes into the
 //    exponent, and back out of the softmax's sum). Values at positions that only some vectors see may be NaN
-//    or infinite: such a tile is added key by key.
+//    or infinite: such a tile is added key by key. Rows that no vector sees are zeroed.
 #pragma once
 
 #include <atomic>
@@ -486,7 +486,19 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
         constexpr int kWords = C::kChunks >= 8 ? 4 : 2;   // 32-bit words of a load (rows of 64 bytes: 8 bytes a lane)
         bool by_key = false;
         if (!full) {
-          // values that are not finite at a position that some vector does not see (or past the keys)
+          // Rows that no vector sees hold what a page happens to hold past its sequence: zeros, so that a NaN there
+          // does not choose how the others are added.
+          const int first = lo - n0, past = end - n0;
+          if (first > 0 || past < kTileN) {
+            char* const v = smem_raw + warp * (C::kDepth * C::kStage) + slot * C::kStage + C::kTile;
+#pragma unroll
+            for (int i = lane; i < kTileN * C::kChunks; i += 32) {
+              const int row = i / C::kChunks;
+              if (row < first || row >= past) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            __syncwarp();
+          }
+          // values that are not finite at a position that some vector does not see
           bool bad = false;
 #pragma unroll
           for (int c = 0; c < kVLoads; ++c)
