@@ -345,8 +345,9 @@ NBX_API size_t nbx_paged_decode_modified_workspace_bytes(int batch, int rows, in
  * nbx_paged_decode_modified_partial_kernel -- which split-partial kernel these two calls run (block-scaled
  * pools: pool_dtype NBX_E4M3). Host-only. A window that nbx_paged_decode_partial_kernel gives to the tensor
  * cores runs there, but an fp8 one only with a bf16 output (its weights are held to 2^-8, a bf16 window's to
- * 2^-17); with a bf16 output so do windows of 40 query vectors of a KV head, 32 at d = 256. Other E4M3 pools, and
- * bf16 pools under bf16 queries, run NBX_PARTIAL_WARP, the rest NBX_PARTIAL_SIMT; both are as exact as fp32 sums.
+ * 2^-17, a capped score to 2^-20 of itself); with a bf16 output so do windows of 40 query vectors of a KV head,
+ * 32 at d = 256. Other E4M3 pools, and bf16 pools under bf16 queries, run NBX_PARTIAL_WARP, the rest
+ * NBX_PARTIAL_SIMT; both are as exact as fp32 sums.
  * Over an fp32 or bf16 pool, nbx_paged_decode_attn_modified without a modification and with an fp32 output is
  * nbx_paged_decode_attn, bit for bit, and runs that call's kernel.
  */

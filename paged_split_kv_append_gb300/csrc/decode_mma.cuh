@@ -69,9 +69,9 @@
 //    does, and the row's sum takes each 16-column part of P' divided by its V scale. So P' keeps its terms'
 //    precision relative to what a position adds to the output, whatever the scales, for a few operations
 //    per 16 positions. The scales of a tile are loaded one tile ahead.
-//  * a cap: z = cap tanh(s / cap). A tile whose scores all lie within 0.6 cap takes an odd polynomial (degree
-//    9, minimax-fitted, relative error 8e-8; 6 operations, packed in pairs); others 1 - 2 / (1 + e^2x), whose
-//    two special-function results per score would make the cap, not the stream, the bound of every tile.
+//  * a cap: z = cap tanh(s / cap). A score within 0.6 cap takes an odd polynomial (degree 9, minimax-fitted, relative
+//    error 8e-8; 6 operations, packed in pairs), others 1 - 2 / (1 + e^2x), whose two special-function results per
+//    score would make the cap, not the stream, the bound of every tile: a tile without such a score skips them.
 //  * a bias by distance (one FMA) and key ranges: a unit reads only the 64-position tiles between the
 //    first and the last key that some row of its M tile sees; the plan kernel wrote these ranges, and the order
 //    in which units of uneven length are dealt to the CTAs.
@@ -453,9 +453,53 @@ __device__ __forceinline__ bool scale_fits(float s) {
   return __float_as_uint(s) - __float_as_uint(kMinScale) <= __float_as_uint(kMaxScale) - __float_as_uint(kMinScale);
 }
 
-// Capped scores in log2 units, cap * tanh(s * c / cap): sr[j] raw in, z out. c: each part's factor from a raw
-// score to s / cap.
-// kFold: the factor goes into the polynomial's coefficients, which saves a product of 32 (capped 16-row windows of bf16
+// Capped scores in log2 units, cap * tanh(s * c / cap).
+//
+// |x| <= 0.6, x = s c: cap x q(x^2), the polynomial of least maximum error for tanh(x) / x in x^2, fitted in 64 bits,
+// relative error 8e-8. Above, cap - 2 cap / (1 + e^2x), whose error of cap 2^-22 is 2^-21 of the result there (near 0 it
+// would be far more). Which of the two a score takes is its own matter: a tile whose scores all lie below skips the
+// second, with the same bits. (A NaN is passed over by fmaxf, and stays a NaN either way.)
+// fold: the factor c goes into the polynomial's coefficients, and x is s itself.
+struct CapPoly {
+  f32x2 q[5];
+  __device__ __forceinline__ CapPoly(float c, float cap, bool fold) {
+    const float a[5] = {0.9999999403953552f, -0.3333234488964081f, 0.13310648500919342f, -0.052122555673122406f,
+                        0.015504649840295315f};
+    const float u1 = fold ? c * c : 1.f;
+    float w = fold ? cap * c : cap;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      q[i] = pack2(a[i] * w, a[i] * w);
+      w *= u1;
+    }
+  }
+  __device__ __forceinline__ float2 operator()(f32x2 x) const {
+    const f32x2 u = mul2(x, x);
+    f32x2 t = fma2(u, q[4], q[3]);
+    t = fma2(u, t, q[2]);
+    t = fma2(u, t, q[1]);
+    t = fma2(u, t, q[0]);
+    return unpack2(mul2(x, t));
+  }
+};
+
+// Either form, by each score's size. Not inlined: a branch of this length beside the polynomial cost every tile (capped
+// bf16 windows 145 to 151 us).
+__device__ __noinline__ void cap_scores_of_any_size(float* s, float c0, float c1, float cap, bool fold) {
+  const CapPoly poly(c0, cap, fold);
+#pragma unroll 4
+  for (int j = 0; j < kHalf; j += 2) {
+    const float c = j < 16 ? c0 : c1;
+    const f32x2 raw = pack2(s[j], s[j + 1]), scaled = mul2(raw, pack2(c, c));
+    const float2 x = unpack2(scaled), z = poly(fold ? raw : scaled);
+    const float e0 = fast_exp2(x.x * (2.f * kLog2e)), e1 = fast_exp2(x.y * (2.f * kLog2e));   // e^2x
+    s[j] = fabsf(x.x) <= 0.6f ? z.x : fmaf(-2.f * cap, fast_rcp(1.f + e0), cap);
+    s[j + 1] = fabsf(x.y) <= 0.6f ? z.y : fmaf(-2.f * cap, fast_rcp(1.f + e1), cap);
+  }
+}
+
+// The scores of a thread: sr[j] raw in, z out. c: each part's factor from a raw score to s / cap.
+// kFold: the factor goes into the coefficients, which saves a product of 32 (capped 16-row windows of bf16
 // 126.8 against 129.2 us), where `fold` says that its ninth power stays in fp32's range. An E4M3 window's does not: its
 // queries are scaled up, and at a factor of 2^-22 scores would be off by 2e-3 of themselves.
 template <bool kFold>
@@ -470,41 +514,26 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[kHalf], const float (&
     for (int i = 4; i < 16; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(__uint_as_float(sr[16 * k + i])));
     ax = fmaxf(ax, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * c[k]);
   }
-  // (a NaN is passed over by fmaxf, and stays a NaN in either branch; an infinity takes the second)
   if (__all_sync(0xffffffffu, ax <= 0.6f && (!kFold || fold))) {
-    // cap tanh(x) = x q(x^2), |x| <= 0.6: the polynomial of least maximum error for tanh(x) / x in x^2, fitted in 64
-    // bits, relative error 8e-8
-    const float u1 = kFold ? c[0] * c[0] : 1.f;
-    float w = kFold ? cap * c[0] : cap;
-    const float a[5] = {0.9999999403953552f, -0.3333234488964081f, 0.13310648500919342f, -0.052122555673122406f,
-                        0.015504649840295315f};
-    f32x2 q[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      q[i] = pack2(a[i] * w, a[i] * w);
-      w *= u1;
-    }
+    const CapPoly poly(c[0], cap, kFold);
 #pragma unroll
     for (int j = 0; j < kHalf; j += 2) {
       f32x2 x = pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1]));
       if constexpr (!kFold) x = mul2(x, pack2(c[j >> 4], c[j >> 4]));
-      const f32x2 u = mul2(x, x);
-      f32x2 t = fma2(u, q[4], q[3]);
-      t = fma2(u, t, q[2]);
-      t = fma2(u, t, q[1]);
-      t = fma2(u, t, q[0]);
-      const float2 z = unpack2(mul2(x, t));
+      const float2 z = poly(x);
       sr[j] = __float_as_uint(z.x);
       sr[j + 1] = __float_as_uint(z.y);
     }
   } else {
+    float s[kHalf];
 #pragma unroll
-    for (int j = 0; j < kHalf; ++j) {
-      const float e = fast_exp2(__uint_as_float(sr[j]) * (c[j >> 4] * (2.f * kLog2e)));   // e^2x
-      sr[j] = __float_as_uint(fmaf(-2.f * cap, fast_rcp(1.f + e), cap));
-    }
+    for (int j = 0; j < kHalf; ++j) s[j] = __uint_as_float(sr[j]);
+    cap_scores_of_any_size(s, c[0], c[1], cap, kFold && fold);
+#pragma unroll
+    for (int j = 0; j < kHalf; ++j) sr[j] = __float_as_uint(s[j]);
   }
 }
+static_assert(kParts == 2, "cap_scores_of_any_size");
 
 // The same terms by two threads a row, each of half of the vector. (Held in registers between its two passes it
 // spilled: 187 against 181 us for the 128-row chunk.) `swap` gives the other half's largest element. Returns 2^-e, or a negative number if a
@@ -694,7 +723,17 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       tmem_wait_ld();
       // ---- the scores: raw, with factors ck, or, capped or biased, z in log2 units with factors 1
       if constexpr (kCap) {
-        if (p.cap_log2 > 0.f) {   // (true but in a test of the waits; as a branch it is scheduled better, 125 against 143 us)
+        if (p.cap_log2 > 0.f) {
+          if constexpr (!F8) {
+            // Keys that a row does not see are no reason for the longer form. (The bits are the same without; a capped
+            // 16-row window takes 125 us so, and 144 as the compiler then orders it. E4M3 windows are the faster
+            // without: 111 against 135, block-scaled 132 against 145.)
+            const int lim = tile_ok ? last_key - n0 : -1, low = kMod ? first_key - n0 : 0;
+            if (!__all_sync(0xffffffffu, lim >= kHalf - 1 && low <= 0)) {
+#pragma unroll
+              for (int j = 0; j < kHalf; ++j) sr[j] = j <= lim && j >= low ? sr[j] : 0u;
+            }
+          }   // (true but in a test of the waits; as a branch it is scheduled better, 125 against 143 us)
           float cx[kParts];
 #pragma unroll
           for (int k = 0; k < kParts; ++k) cx[k] = ck[k] * p.cap_inv;

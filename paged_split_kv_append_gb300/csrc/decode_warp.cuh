@@ -170,7 +170,7 @@ __device__ __forceinline__ bool not_finite(const uint4& v) {
   return bad != 0;
 }
 
-// tanh for the cap: a polynomial up to 0.75 (relative error 1.2e-8; the tensor-core kernel's), else CUDA's.
+// tanh for the cap: a polynomial up to 0.75 (relative error 1.2e-8); above, CUDA's.
 __device__ __forceinline__ float small_tanh(float x) {
   const float u = x * x;
   float t = fmaf(u, 0.0017277069855481386f, -0.0076394579373300076f);
@@ -414,12 +414,13 @@ __global__ void __launch_bounds__(WarpCfg<PT, QT, D, X>::kWarpsCta * 32, WarpCfg
           if (p.cap_log2 > 0.f) {
             const float x[4] = {z[0] * p.cap_inv, z[1] * p.cap_inv, z[2] * p.cap_inv, z[3] * p.cap_inv};
             const float far = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-            if (__all_sync(0xffffffffu, far <= 0.75f)) {   // (a NaN is passed over, and stays one either way)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) z[e] = p.cap_log2 * small_tanh(x[e]);
-            } else {
+            for (int e = 0; e < 4; ++e) z[e] = p.cap_log2 * small_tanh(x[e]);
+            // (each score by its own size, whatever the others are: a key that nobody sees changes no bit)
+            if (!__all_sync(0xffffffffu, far <= 0.75f)) {   // (a NaN is passed over, and stays one either way)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) z[e] = p.cap_log2 * tanhf(x[e]);
+              for (int e = 0; e < 4; ++e)
+                if (fabsf(x[e]) > 0.75f) z[e] = p.cap_log2 * tanhf(x[e]);
             }
           }
           if (p.slopes != nullptr) {

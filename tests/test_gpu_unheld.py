@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.cache as oc
 import paged_split_kv_append_gb300 as nbx
 from tests.test_gpu_modified import DEV, Case, made
 
@@ -46,3 +47,35 @@ def test_values_behind_a_sequence(pool, rows, h_q, h_kv, d, P, T, mod, out_type)
         out.append(c.call(out_type, **made(mod, LENS, rows, h_q)))
     assert bool(torch.isfinite(out[0]).all())
     assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+
+
+@pytest.mark.parametrize("out_type", ["f32", "bf16"])
+@pytest.mark.parametrize("pool,rows,h_q,h_kv,d,P,T", SHAPES)
+def test_keys_behind_a_sequence_under_a_cap(pool, rows, h_q, h_kv, d, P, T, out_type):
+    # scores within the cap's polynomial: a key that nobody sees may not choose the form that they take
+    c = Case(pool, "bf16", rows, h_q, h_kv, d, P, LENS, T, seed=41)
+    for cap in (12.0, 100.0):
+        out = []
+        for what in ("zero", "large", "nan"):
+            c.dev = filled(c, what)
+            out.append(c.call(out_type, softcap=cap))
+        assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+
+
+@pytest.mark.parametrize("pool,T", [("bf16", 0), ("e4m3", 0), ("block", 16)])
+def test_a_cap_does_not_see_the_other_rows(pool, T):
+    # rows of small scores beside one of large ones, a large cap: what it leaves of a small score is the score, to
+    # 2^-21 of the score itself and not of the cap. Tolerance as in test_gpu_unmodified (fp32 sums), weights 2^-17
+    rows, h_q, h_kv, d, P = 16, 16, 2, 128, 64
+    c = Case(pool, "bf16", rows, h_q, h_kv, d, P, (700,), T, seed=42)
+    q = c.q.float()
+    q[0, ::5] *= 3e6
+    c.q = q.to(torch.bfloat16)
+    cap = 1e5
+    ref = oc.attention(c.q.float().numpy(), *c.values, c.table, c.lens, c.scale, softcap=cap)
+    quiet = [r for r in range(rows) if r % 5]
+    z = c.scale * float(np.linalg.norm(c.q.float().numpy()[0, quiet], axis=-1).max()) * \
+        float(np.linalg.norm(c.values[0], axis=-1).max())
+    got = c.call("f32", softcap=cap).double().cpu().numpy()
+    off = np.linalg.norm(got[0, quiet] - ref[0, quiet]) / np.linalg.norm(ref[0, quiet])
+    assert off <= 2.0 ** -17 + 2.0 ** -19 * z + 2.0 ** -14, off
