@@ -173,6 +173,28 @@ def _check(func: str, status: int):
         raise NbxError(func, status)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _new(shape, dtype, like: torch.Tensor, stream, fill=None) -> torch.Tensor:
+    """A tensor on `like`'s device for a call on `stream`, uninitialised or filled. For a stream that is not the
+    current one the memory comes from that stream's own (the current one may have work to do on what it has freed),
+    the filling is that stream's work, and the allocator learns that the current one may use the tensor too."""
+    dev = like.get_device()
+    handle = None if stream is None else int(getattr(stream, "cuda_stream", stream))
+    if handle is None or handle == _raw_stream(dev):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        return t if fill is None else t.fill_(fill)
+    current = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=like.device)):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+        if fill is not None:
+            t.fill_(fill)
+    t.record_stream(current)
+    return t
+
+
 def _cuda_contig(name: str, t: torch.Tensor):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -233,12 +255,12 @@ def nbx_paged_decode_attn(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.T
                          f"seq_lens {list(seq_lens.shape)} do not fit")
     max_pages = block_table.shape[1]
     if out is None:
-        out = torch.empty((batch, rows, h_q, d), dtype=torch.float32, device=q.device)
+        out = _new((batch, rows, h_q, d), torch.float32, q, stream)
     _cuda_contig("out", out)
     need = nbx_paged_decode_workspace_bytes_for(dtype_code(q), dtype_code(k_pool), batch, rows, h_q, h_kv, d,
                                                 max_seq_len, page_tokens)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 256), torch.uint8, q, stream)
     st = lib().nbx_paged_decode_attn(_ptr(q), dtype_code(q), batch, rows, h_q, d, _ptr(k_pool), _ptr(v_pool),
                                      dtype_code(k_pool), num_pages, h_kv, page_tokens, _ptr(block_table), max_pages,
                                      _ptr(seq_lens), int(max_seq_len), float(scale), float(k_scale),
@@ -271,12 +293,12 @@ def nbx_paged_decode_step(q: torch.Tensor, new_k: torch.Tensor, new_v: torch.Ten
         raise ValueError(f"q {list(q.shape)}, new_k {list(new_k.shape)}, pool {list(k_pool.shape)}, "
                          f"block_table {list(block_table.shape)}, lens {list(lens.shape)} do not fit")
     if out is None:
-        out = torch.empty((batch, rows, h_q, d), dtype=torch.float32, device=q.device)
+        out = _new((batch, rows, h_q, d), torch.float32, q, stream)
     _cuda_contig("out", out)
     need = nbx_paged_decode_workspace_bytes_for(dtype_code(q), dtype_code(k_pool), batch, rows, h_q, h_kv, d,
                                                 max_seq_len, page_tokens)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 256), torch.uint8, q, stream)
     st = lib().nbx_paged_decode_step(_ptr(q), dtype_code(q), batch, rows, h_q, d, _ptr(new_k), _ptr(new_v),
                                      dtype_code(new_k), _ptr(k_pool), _ptr(v_pool), dtype_code(k_pool), num_pages,
                                      h_kv, page_tokens, _ptr(block_table), block_table.shape[1], _ptr(lens),
@@ -303,12 +325,12 @@ def nbx_decode_attn_contiguous(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     if b_c != batch or d_c != d or seq_lens.numel() != batch:
         raise ValueError(f"q {list(q.shape)}, cache {list(k_cache.shape)}, seq_lens {list(seq_lens.shape)} do not fit")
     if out is None:
-        out = torch.empty((batch, rows, h_q, d), dtype=torch.float32, device=q.device)
+        out = _new((batch, rows, h_q, d), torch.float32, q, stream)
     _cuda_contig("out", out)
     need = nbx_paged_decode_workspace_bytes_for(dtype_code(q), dtype_code(k_cache), batch, rows, h_q, h_kv, d,
                                                 max_seq_len, capacity)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 256), torch.uint8, q, stream)
     st = lib().nbx_decode_attn_contiguous(_ptr(q), dtype_code(q), batch, rows, h_q, d, _ptr(k_cache), _ptr(v_cache),
                                           dtype_code(k_cache), h_kv, capacity, _ptr(seq_lens), int(max_seq_len),
                                           float(scale), float(k_scale), float(v_scale), _ptr(out), _ptr(workspace),
@@ -327,7 +349,7 @@ def nbx_paged_decode_merge(acc_part: torch.Tensor, m_part: torch.Tensor, l_part:
             raise ValueError(f"{n} must be fp32")
     n_rows, splits, d = acc_part.shape
     if out is None:
-        out = torch.empty((n_rows, d), dtype=torch.float32, device=acc_part.device)
+        out = _new((n_rows, d), torch.float32, acc_part, stream)
     st = lib().nbx_paged_decode_merge(_ptr(acc_part), _ptr(m_part), _ptr(l_part), n_rows, splits, d, _ptr(out),
                                       _stream(stream))
     _check("nbx_paged_decode_merge", st)
@@ -374,8 +396,8 @@ def nbx_paged_decode_bounds(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch
     """The fixed-shift softmax's score bounds: (q_norm [batch, rows, h_q], kv_max [batch, h_kv, 2]) fp32."""
     batch, rows, h_q, d, num_pages, h_kv, page_tokens, max_pages = _decode_shapes(q, k_pool, v_pool, block_table,
                                                                                   seq_lens)
-    q_norm = torch.empty((batch, rows, h_q), dtype=torch.float32, device=q.device)
-    kv_max = torch.empty((batch, h_kv, 2), dtype=torch.float32, device=q.device)
+    q_norm = _new((batch, rows, h_q), torch.float32, q, stream)
+    kv_max = _new((batch, h_kv, 2), torch.float32, q, stream)
     st = lib().nbx_paged_decode_bounds(_ptr(q), dtype_code(q), batch, rows, h_q, d, _ptr(k_pool), _ptr(v_pool),
                                        dtype_code(k_pool), num_pages, h_kv, page_tokens, _ptr(block_table), max_pages,
                                        _ptr(seq_lens), int(max_seq_len), float(k_scale), float(v_scale), _ptr(q_norm),
@@ -399,12 +421,12 @@ def nbx_paged_decode_attn_fixed_shift(q: torch.Tensor, k_pool: torch.Tensor, v_p
             kv_max.numel() != batch * h_kv * 2:
         raise ValueError("q_norm [batch, rows, h_q] and kv_max [batch, h_kv, 2] must be fp32")
     if out is None:
-        out = torch.empty((batch, rows, h_q, d), dtype=torch.float32, device=q.device)
+        out = _new((batch, rows, h_q, d), torch.float32, q, stream)
     _cuda_contig("out", out)
     need = nbx_paged_decode_workspace_bytes_for(dtype_code(q), dtype_code(k_pool), batch, rows, h_q, h_kv, d,
                                                 max_seq_len, page_tokens)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(need, 256), torch.uint8, q, stream)
     st = lib().nbx_paged_decode_attn_fixed_shift(_ptr(q), dtype_code(q), batch, rows, h_q, d, _ptr(k_pool),
                                                  _ptr(v_pool), dtype_code(k_pool), num_pages, h_kv, page_tokens,
                                                  _ptr(block_table), max_pages, _ptr(seq_lens), int(max_seq_len),
@@ -427,10 +449,6 @@ def nbx_decode_fixed_shift_gate(n_keys: int, v_max_bound: float = 256.0):
 # These calls check that every tensor sits on one device, and run there whatever the current device is.
 # Their GPU work can be as short as a few microseconds, so the checks keep to a few cheap tensor methods,
 # pointers are passed as plain integers and the stream is looked up as a raw handle.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
 def _one_device(names: str, *tensors) -> int:
     """The index of the CUDA device that all the given tensors (None skipped, the first is one) sit on; contiguous
     all."""
@@ -464,15 +482,6 @@ def _p(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
-    """An uninitialised tensor on `like`'s device for a call on `stream`. The allocator learns of a stream that is
-    not the current one, so that the memory is not handed out again while the call still runs there."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        handle = int(getattr(stream, "cuda_stream", stream))
-        if handle != _raw_stream(t.get_device()):
-            t.record_stream(torch.cuda.ExternalStream(handle, device=t.device))
-    return t
 
 
 _calls = {}   # entry point -> its number in nbx_call, and what packs its arguments
@@ -669,14 +678,11 @@ def nbx_paged_kv_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, fork_sr
     num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
     n, table = fork_src.numel(), block_table.shape
     # (the call writes all of both; one without a fork or a row writes nothing)
+    no_rows = len(table) == 2 and table[0] == 0
     if moves is None:
-        moves = _new((n, 3), torch.int32, block_table, stream)
-        if len(table) == 2 and table[0] == 0:
-            moves.fill_(-1)
+        moves = _new((n, 3), torch.int32, block_table, stream, -1 if no_rows else None)
     if n_moves is None:
-        n_moves = _new(1, torch.int32, block_table, stream)
-        if n == 0 or (len(table) == 2 and table[0] == 0):
-            n_moves.zero_()
+        n_moves = _new(1, torch.int32, block_table, stream, 0 if n == 0 or no_rows else None)
     if len(table) != 2 or seq_lens.numel() != table[0] or fork_dst.numel() != n or moves.shape != (n, 3) or \
             n_moves.numel() < 1:
         _misfit("block_table seq_lens fork_src fork_dst moves n_moves", block_table, seq_lens, fork_src, fork_dst,
@@ -713,13 +719,9 @@ def nbx_paged_kv_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, k_po
         new_block_table = _new(table, torch.int32, block_table, stream)
     empty = len(table) == 2 and table[0] == 0   # (such a call writes nothing, any other all of moves and counts)
     if moves is None:
-        moves = _new((max(1, num_pages // 2), 3), torch.int32, block_table, stream)
-        if empty:
-            moves.fill_(-1)
+        moves = _new((max(1, num_pages // 2), 3), torch.int32, block_table, stream, -1 if empty else None)
     if counts is None:
-        counts = _new(2, torch.int32, block_table, stream)
-        if empty:
-            counts.zero_()
+        counts = _new(2, torch.int32, block_table, stream, 0 if empty else None)
     if len(table) != 2 or seq_lens.numel() != table[0] or new_block_table.shape != table or moves.dim() != 2 or \
             moves.shape[1] != 3 or counts.numel() < 2:
         _misfit("block_table seq_lens new_block_table moves counts", block_table, seq_lens, new_block_table, moves,
