@@ -19,7 +19,7 @@ from typing import Optional
 
 import torch
 
-from . import (NBX_BF16, NBX_E4M3, NBX_F32, nbx_paged_decode_attn, nbx_paged_decode_attn_block_scaled,
+from . import (NBX_BF16, NBX_E4M3, NBX_F32, _new, nbx_paged_decode_attn, nbx_paged_decode_attn_block_scaled,
                nbx_paged_decode_attn_modified, nbx_paged_decode_modified_workspace_bytes,
                nbx_paged_decode_workspace_bytes_for, nbx_paged_kv_append, nbx_paged_kv_append_block_scaled,
                nbx_paged_kv_compact, nbx_paged_kv_compact_workspace_bytes, nbx_paged_kv_fork,
@@ -76,7 +76,7 @@ class PagedDecodeSession:
         self.held = self.tok_start = None
         self.scale, self.k_scale, self.v_scale = 1.0, 1.0, 1.0
         self.modifications = {}
-        self._page_workspace = None
+        self._page_workspaces = []
 
     # ---------------------------------------------------------------- state
     def append(self, new_k: torch.Tensor, new_v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
@@ -135,24 +135,25 @@ class PagedDecodeSession:
         self.modifications = dict(softcap=softcap, slopes=slopes, key_begin=key_begin, key_end=key_end)
 
     # ---------------------------------------------------------------- rows and pages
-    def _page_scratch(self) -> torch.Tensor:
-        """The workspace of forks (of up to a row each) and compactions, kept."""
+    def _page_scratch(self, stream) -> torch.Tensor:
+        """The workspace of forks (of up to a row each) and compactions. One that a larger table outgrows is kept beside
+        its successor: captured graphs, and calls on other streams, may still use it."""
         need = max(nbx_paged_kv_fork_workspace_bytes(*self.block_table.shape, self.batch, self.num_pages),
                    nbx_paged_kv_compact_workspace_bytes(self.num_pages))
-        if self._page_workspace is None or self._page_workspace.numel() < need:
-            self._page_workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        return self._page_workspace
+        if not self._page_workspaces or self._page_workspaces[-1].numel() < need:
+            self._page_workspaces.append(_new(need, torch.uint8, self.block_table, stream))
+        return self._page_workspaces[-1]
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
         """Rows dst of the block table and the lengths become rows src as they were (int32 device tensors). Returns
         (moves, n_moves)."""
         return nbx_paged_kv_fork(self.block_table, self.seq_lens, src, dst, self.k_pool, self.v_pool, self.k_scales,
-                                 self.v_scales, workspace=self._page_scratch(), status=self.status, stream=stream)
+                                 self.v_scales, workspace=self._page_scratch(stream), status=self.status, stream=stream)
 
     def compact(self, stream=None):
         """The pages in use move to the lowest ids, in the block table too. Returns (moves, {moves, pages in use})."""
         return nbx_paged_kv_compact(self.block_table, self.seq_lens, self.k_pool, self.v_pool, self.k_scales,
-                                    self.v_scales, new_block_table=self.block_table, workspace=self._page_scratch(),
+                                    self.v_scales, new_block_table=self.block_table, workspace=self._page_scratch(stream),
                                     status=self.status, stream=stream)[1:]
 
     # ---------------------------------------------------------------- the step

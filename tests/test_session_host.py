@@ -1,0 +1,34 @@
+"""The session without a GPU: the scratch of its page calls, and the calls that do not fit a block-scaled cache."""
+
+import weakref
+
+import pytest
+import torch
+
+import paged_split_kv_append_gb300 as nbx
+from paged_split_kv_append_gb300.session import PagedDecodeSession
+
+SIZES = dict(num_pages=8, h_kv=1, page_tokens=32, d=64, batch=4, rows=1, h_q=1, max_seq_len=32, device="cpu")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    nbx.build()
+
+
+def inputs(s, width, **kw):
+    s.set_inputs(torch.zeros((4, 1, 1, 64)), torch.full((4, width), -1), torch.zeros(4), None, None, None, 1.0, **kw)
+
+
+def test_a_page_scratch_that_grows_keeps_the_one_before():
+    # a captured graph, or a call on another stream, may still use it
+    s = PagedDecodeSession(**SIZES, pool_dtype="bf16")
+    inputs(s, 4)
+    first = s._page_scratch(None)
+    assert s._page_scratch(None).data_ptr() == first.data_ptr()
+    kept = weakref.ref(first)
+    at, size = first.data_ptr(), first.numel()
+    del first
+    inputs(s, 4096)
+    assert s._page_scratch(None).numel() > size and s._page_scratch(None).data_ptr() != at
+    assert kept() is not None
