@@ -79,12 +79,19 @@ class PagedDecodeSession:
         self._page_workspaces = []
 
     # ---------------------------------------------------------------- state
+    def _fits(self, call: str, block_scaled: bool) -> None:
+        """Refuses a call that does not know of the pools' block scales, or one that needs them."""
+        if (self.k_scales is not None) != block_scaled:
+            raise ValueError(f"{call} is for a session " + ("with" if block_scaled else "without") + " block scales")
+
     def append(self, new_k: torch.Tensor, new_v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+        self._fits("append", False)
         nbx_paged_kv_append(new_k, new_v, self.k_pool, self.v_pool, slots, self.k_scale, self.v_scale,
                             status=self.status, stream=stream)
 
     def prefill(self, k_raw: torch.Tensor, v_raw: torch.Tensor, index, slots, chunk_tokens: int = 1 << 18) -> None:
         """Append the tokens k_raw[index] at the given slots, in chunks (index/slots on the host)."""
+        self._fits("prefill", False)
         import numpy as np
         index = np.asarray(index)
         slots = np.asarray(slots, dtype=np.int32)
@@ -99,7 +106,10 @@ class PagedDecodeSession:
     def set_inputs(self, q: torch.Tensor, block_table, seq_lens, new_k: Optional[torch.Tensor],
                    new_v: Optional[torch.Tensor], new_slots, scale: float, k_scale: float = 1.0,
                    v_scale: float = 1.0) -> None:
-        """The step's inputs; host arrays are copied to the device once."""
+        """The step's inputs; host arrays are copied to the device once. (A block-scaled session's scales are its
+        blocks', and what its steps append is said by set_new_tokens.)"""
+        if self.k_scales is not None and (k_scale != 1.0 or v_scale != 1.0):
+            raise ValueError("a session with block scales takes no scale of the pool")
         def dev(x, dtype=None):
             t = x if isinstance(x, torch.Tensor) else torch.as_tensor(x)
             if dtype is not None:
@@ -117,11 +127,13 @@ class PagedDecodeSession:
                             tok_start: torch.Tensor, stream=None) -> None:
         """Rows tok_start[b] .. tok_start[b + 1] - 1 to positions held[b] and up of sequence b (a block-scaled
         cache)."""
+        self._fits("append_block_scaled", True)
         nbx_paged_kv_append_block_scaled(new_k, new_v, self.k_pool, self.v_pool, self.k_scales, self.v_scales,
                                          self.block_table, held, tok_start, status=self.status, stream=stream)
 
     def set_new_tokens(self, new_k: torch.Tensor, new_v: torch.Tensor, held, tok_start) -> None:
         """The tokens a step of a block-scaled session appends; host arrays are copied to the device once."""
+        self._fits("set_new_tokens", True)
         def dev(x):
             return torch.as_tensor(x).to(torch.int32).to(self.device).contiguous()
         self.new_k, self.new_v = new_k.to(self.device).contiguous(), new_v.to(self.device).contiguous()
@@ -176,6 +188,8 @@ class PagedDecodeSession:
         """Append the step's new positions, then decode: one pass of the hot path."""
         if self.k_scales is not None:
             if self.new_k is not None:
+                if self.held is None:
+                    raise ValueError("a step of a session with block scales appends what set_new_tokens gives it")
                 self.append_block_scaled(self.new_k, self.new_v, self.held, self.tok_start, stream=stream)
         elif self.new_k is not None and self.new_k.shape[0] > 0:
             self.append(self.new_k, self.new_v, self.new_slots, stream=stream)
