@@ -467,6 +467,9 @@ def _one_device(names: str, *tensors) -> int:
 
 
 def _int32(names: str, *tensors, int32=torch.int32):
+    """All int32; the last is the status word, with room for it."""
+    if tensors[-1] is not None and not tensors[-1].numel():
+        raise ValueError("status has no element")
     if [1 for t in tensors if t is not None and t.dtype is not int32]:
         for name, t in zip(names.split(), tensors):
             if t is not None and t.dtype is not int32:
@@ -510,16 +513,17 @@ def _run(func: str, dev: int, stream, *args):
         raise NbxError(func, code)
 
 
-def _pools(k_pool, v_pool, k_scales, v_scales):
-    """(num_pages, h_kv, page_tokens, d, positions per scale or 0) of a layer's pools."""
+def _pools(k_pool, v_pool, k_scales, v_scales, scaled=False):
+    """(num_pages, h_kv, page_tokens, d, positions per scale or 0) of a layer's pools. scaled: the call needs scales."""
     shape = k_pool.shape
     if len(shape) != 4 or shape != v_pool.shape or k_pool.dtype != v_pool.dtype:
         raise ValueError("k_pool and v_pool [num_pages, h_kv, page_tokens, d] must match")
     num_pages, h_kv, page_tokens, d = shape
-    if k_scales is None and v_scales is None:
+    if k_scales is None and v_scales is None and not scaled:
         return num_pages, h_kv, page_tokens, d, 0
     if k_scales is None or v_scales is None:
-        raise ValueError("k_scales and v_scales come together")
+        raise ValueError("a block-scaled call takes k_scales and v_scales" if scaled else
+                         "k_scales and v_scales come together")
     blocks = k_scales.shape
     if k_scales.dtype is not torch.float32 or v_scales.dtype is not torch.float32 or blocks != v_scales.shape or \
             len(blocks) != 3 or blocks[0] != num_pages or blocks[1] != h_kv or blocks[2] < 1 or \
@@ -541,7 +545,7 @@ def nbx_paged_kv_append_block_scaled(new_k: torch.Tensor, new_v: torch.Tensor, k
     dev = _one_device("new_k new_v k_pool v_pool k_scales v_scales block_table lens tok_start status", new_k, new_v,
                       k_pool, v_pool, k_scales, v_scales, block_table, lens, tok_start, status)
     _int32("block_table lens tok_start status", block_table, lens, tok_start, status)
-    num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
+    num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales, True)
     new, table, batch = new_k.shape, block_table.shape, lens.numel()
     if new != new_v.shape or new_k.dtype != new_v.dtype or len(new) != 3 or new[1] != h_kv or new[2] != d or \
             len(table) != 2 or table[0] != batch or tok_start.numel() != batch + 1:
@@ -601,7 +605,7 @@ def nbx_paged_decode_attn_block_scaled(q: torch.Tensor, k_pool: torch.Tensor, v_
     dev = _one_device("q k_pool v_pool k_scales v_scales block_table seq_lens slopes key_begin key_end out workspace "
                       "status", q, k_pool, v_pool, k_scales, v_scales, block_table, seq_lens, slopes, key_begin,
                       key_end, out, workspace, status)
-    num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales)
+    num_pages, h_kv, page_tokens, d, block = _pools(k_pool, v_pool, k_scales, v_scales, True)
     batch, rows, h_q, max_pages, out = _modified_shapes(q, d, block_table, seq_lens, slopes, key_begin, key_end, out,
                                                         out_dtype, status, stream)
     if workspace is None:
