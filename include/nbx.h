@@ -292,7 +292,8 @@ NBX_API int nbx_decode_fixed_shift_gate(int n_keys, double v_max_bound, int* c_o
  *          of the block's new tokens;
  *   S    = need when the block's first position is new, else max(the block's scale, need);
  *   new codes are e4m3(x / S) (nearest even, saturating at +-448; NaN stays NaN); if S grew, the codes
- *   of the positions held before become e4m3(code * old S / S), which is exact but for results under 2^-6.
+ *   of the positions held before become e4m3(code * old S / S), which is exact but for results under 2^-6
+ *   where the old S was written here too. Quotient and product are fp32 (exact with powers of two).
  * Positions past the new ones are left as they are. lens is not advanced. Appending the same tokens
  * again at the same lens gives the same cache.
  *

@@ -102,6 +102,17 @@ __device__ __forceinline__ uint2 to_codes(const float* x, float mul) {
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
+// The same of x / s. With a power of two the quotient is a product, exactly; a held scale that another program wrote
+// may be anything, and x * (1 / s) would round twice (codes beside a tie between two of them came out the other way).
+__device__ __forceinline__ uint2 divided_codes(float* x, float s, float inv, bool power) {
+  if (!power) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(x[i], s);
+    inv = 1.f;
+  }
+  return to_codes(x, inv);
+}
+
 // The smallest power of two S in [2^-48, 2^48] with amax <= 448 S, from amax's bits (finite, >= 0):
 // 448 = 1.75 * 2^8, so S = 2^(e - 8) for a significand up to 1.75, else 2^(e - 7).
 __device__ __forceinline__ float need_scale(uint32_t amax_bits) {
@@ -247,7 +258,8 @@ __global__ void __launch_bounds__(D <= 128 ? 256 : 512) __maxnreg__(In::kBytes =
     const bool was_ok = was >= kMinScale && was <= kMaxScale;   // false for NaN
     if (!was_ok && lane == 0 && wg == 0) raise_status(p.status, NBX_DEV_BAD_SCALE);
     const float s = begins || !was_ok ? need : fmaxf(was, need);
-    const float inv = 1.f / s;                      // exact for the powers of two written here
+    const float inv = 1.f / s;
+    const bool power = (__float_as_uint(s) & 0x7fffffu) == 0;   // as every scale written here
     const bool again = !begins && was_ok && s > was;
     const float ratio = was / s;
     uint8_t* const to = pool + (static_cast<int64_t>(it.head) * p.page_tokens + it.in_page + wg * kWarpRows + sub) * D + col;
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(D <= 128 ? 256 : 512) __maxnreg__(In::kBytes =
       for (int i = 0; i < kPasses; ++i) {
         float f[8];
         x[i].get(f);
-        *reinterpret_cast<uint2*>(to + i * (kRpp * D)) = to_codes(f, inv);
+        *reinterpret_cast<uint2*>(to + i * (kRpp * D)) = divided_codes(f, s, inv, power);
       }
       continue;
     }
@@ -268,7 +280,7 @@ __global__ void __launch_bounds__(D <= 128 ? 256 : 512) __maxnreg__(In::kBytes =
       if (pos >= it.held && pos < it.end) {
         float f[8];
         x[i].get(f);
-        *dst = to_codes(f, inv);
+        *dst = divided_codes(f, s, inv, power);
       } else if (again && pos < it.held) {
         const uint2 c = *dst;
         float f[8];
