@@ -301,7 +301,7 @@ NBX_API int nbx_decode_fixed_shift_gate(int n_keys, double v_max_bound, int* c_o
  *   block_table  [device] int32 [batch, max_pages];  lens [device] int32 [batch]
  *   tok_start    [device] int32 [batch + 1], ascending, tok_start[batch] <= n_tok
  * A sequence whose tok_start or lens make no sense, or a block past max_pages, is skipped with
- * NBX_DEV_BAD_LEN, a page outside the pool with NBX_DEV_BAD_PAGE; a held block whose scale is not in
+ * NBX_DEV_BAD_LEN (where tok_start does not ascend, parts of others may be skipped too), a page outside the pool with NBX_DEV_BAD_PAGE; a held block whose scale is not in
  * [2^-48, 2^48] gets need and NBX_DEV_BAD_SCALE. No two sequences may append to one page.
  * Requirements: d in {64, 128, 256}; buffers 16-byte aligned. n_tok == 0 or batch == 0 returns NBX_OK
  * without a launch.

@@ -33,3 +33,18 @@ def test_held_scales_that_are_no_powers_of_two(dtype):
         x.append(torch.from_numpy((tie * s * g.choice([-1.0, 1.0], tie.shape)).astype(np.float32)).to(dtype).to(DEV))
     c.append(x, table, [5] * B, list(range(0, 6 * B + 1, 6)))
     c.check()
+
+
+@pytest.mark.parametrize("start,bits", [([0, 1000, 0, 10], nbx.DEV_BAD_LEN), ([1000, 5, 6, 7], nbx.DEV_BAD_LEN),
+                                        ([0, 1000, 1005, 1010], 0), ([0, 1000, 1000, 1000], 0), ([3, 3, 4, 4], 0)])
+def test_ranges_that_do_not_ascend_are_reported(start, bits):
+    # [0, 1000, 0, 10]: the blocks of the first sequence from the fifth on belong to nobody
+    P, T, h, d = 16, 16, 1, 64
+    table, pages = table_for([1100, 20, 20], P, 63)
+    c = Cache(pages, h, P, d, T, 64)
+    x = [torch.randn((1010, h, d), device=DEV) for _ in range(2)]
+    dt = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(DEV)   # noqa: E731
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    nbx.nbx_paged_kv_append_block_scaled(*x, *c.dev, *c.dev_scales, dt(table), dt([0, 0, 0]), dt(start), status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == bits
