@@ -325,8 +325,9 @@ NBX_API int nbx_paged_kv_append_block_scaled(const void* new_k, const void* new_
  *     with slopes: z_j -= slopes[h] * |p - j|;
  *   out = sum_j e^(z_j - max z) v_j / sum_j e^(z_j - max z), 0 for a row that sees no key.
  * A document mask is key_begin = the start of the row's document, a prefix mask key_end =
- * max(p + 1, prefix length), a window key_begin = p + 1 - window. Keys that no row of a work unit sees are
- * not read: their pages may be gone from the table (-1).
+ * max(p + 1, prefix length), a window key_begin = p + 1 - window. Keys before the first and behind the last that
+ * some row of a sequence sees are not read: their pages may be gone from the table (-1). One between them may be
+ * read without being seen, where ranges leave a gap: its page and scale count as read for the status word.
  *
  *   softcap      0 (none), or such that softcap * log2 e and its reciprocal are finite floats
  *   slopes       [device] fp32 [h_q] or NULL
@@ -350,7 +351,8 @@ NBX_API size_t nbx_paged_decode_modified_workspace_bytes(int batch, int rows, in
  * 32 at d = 256. Other E4M3 pools, and bf16 pools under bf16 queries, run NBX_PARTIAL_WARP, the rest
  * NBX_PARTIAL_SIMT; both are as exact as fp32 sums.
  * Over an fp32 or bf16 pool, nbx_paged_decode_attn_modified without a modification and with an fp32 output is
- * nbx_paged_decode_attn, bit for bit, and runs that call's kernel.
+ * nbx_paged_decode_attn, bit for bit, and runs that call's kernel. (Over an E4M3 pool it is not: that call's windows
+ * hold weights to 2^-8 whatever the output, and are four to six times as fast as this one's fp32.)
  */
 NBX_API int nbx_paged_decode_modified_partial_kernel(int q_dtype, int pool_dtype, int out_dtype, int rows, int h_q,
                                                      int h_kv, int d, int num_pages, int page_tokens);
@@ -434,7 +436,8 @@ NBX_API int nbx_paged_kv_fork(int32_t* block_table, int max_pages, int32_t* seq_
  *   counts       [device] int32 [2], written: {moves, pages in use}
  *   workspace    [device] nbx_paged_kv_compact_workspace_bytes(num_pages) bytes, 256-byte aligned
  *   pools        as for nbx_paged_kv_fork (both NULL: nothing is copied)
- * Entries that name no page of the pool are kept (NBX_DEV_BAD_PAGE if >= num_pages). num_pages <= 2^30.
+ * Entries that name no page of the pool are kept (NBX_DEV_BAD_PAGE if >= num_pages); a length outside its bounds
+ * sets NBX_DEV_BAD_LEN and is cut to them. num_pages <= 2^30.
  * batch == 0 returns NBX_OK without a launch.
  */
 NBX_API size_t nbx_paged_kv_compact_workspace_bytes(int num_pages);
