@@ -352,7 +352,7 @@ NBX_API size_t nbx_paged_decode_modified_workspace_bytes(int batch, int rows, in
  * NBX_PARTIAL_SIMT; both are as exact as fp32 sums.
  * Over an fp32 or bf16 pool, nbx_paged_decode_attn_modified without a modification and with an fp32 output is
  * nbx_paged_decode_attn, bit for bit, and runs that call's kernel. (Over an E4M3 pool it is not: that call's windows
- * hold weights to 2^-8 whatever the output, and are four to six times as fast as this one's fp32.)
+ * hold weights to 2^-8 whatever the output, and are three to four times as fast as this one's fp32.)
  */
 NBX_API int nbx_paged_decode_modified_partial_kernel(int q_dtype, int pool_dtype, int out_dtype, int rows, int h_q,
                                                      int h_kv, int d, int num_pages, int page_tokens);
