@@ -13,9 +13,9 @@
 // (block, KV head, K or V): D / 8 lanes to a position, 8 elements a lane (one 16-byte load of bf16, two of
 // fp32; one 8-byte store of codes). Items are ordered KV head fastest, as
 // the new tokens lie in memory, so the groups running side by side read whole lines. The grid is what the
-// GPU holds at once, one CTA of it without items; a group looks its next item up while the values of the current one are on their way (one
-// item a group and as many CTAs as items took 51 us for 30 thousand bf16 tokens of 4 heads of 256, two thirds
-// of it the chain of lookups before the first value).
+// GPU holds at once, one CTA of it without items; a group looks its next item up while the values of the
+// current one are on their way (one item a group and as many CTAs as items took 51 us for 30 thousand bf16
+// tokens of 4 heads of 256, two thirds of it the chain of lookups before the first value).
 //
 // Which block an item is: sequence b owns the flat indices from tok_start[b] / T + 2 b on. Its n new
 // tokens touch at most n / T + 2 blocks, so the ranges do not meet, the grid needs no device-side

@@ -723,7 +723,7 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
       tmem_wait_ld();
       // ---- the scores: raw, with factors ck, or, capped or biased, z in log2 units with factors 1
       if constexpr (kCap) {
-        if (p.cap_log2 > 0.f) {
+        if (p.cap_log2 > 0.f) {   // (true but in a test of the waits; as a branch it is scheduled better, 125 against 143 us)
           if constexpr (!F8) {
             // Keys that a row does not see are no reason for the longer form. (The bits are the same without; a capped
             // 16-row window takes 125 us so, and 144 as the compiler then orders it. E4M3 windows are the faster
@@ -733,7 +733,7 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
 #pragma unroll
               for (int j = 0; j < kHalf; ++j) sr[j] = j <= lim && j >= low ? sr[j] : 0u;
             }
-          }   // (true but in a test of the waits; as a branch it is scheduled better, 125 against 143 us)
+          }
           float cx[kParts];
 #pragma unroll
           for (int k = 0; k < kParts; ++k) cx[k] = ck[k] * p.cap_inv;
