@@ -105,6 +105,37 @@ NBX_API int nbx_paged_kv_append(const void* new_k, const void* new_v, int new_dt
                                 void* stream);
 
 /*
+ * nbx_paged_kv_append_rotated -- the append with the position rotation applied on the way.
+ *
+ * Token t's query and key heads are turned by its position, x' of x with the pair (a, b) at i < turned / 2:
+ *   a' = a * cos[positions[t], i] - b * sin[positions[t], i],  b' = b * cos[...] + a * sin[...],
+ * a and b being elements i and turned / 2 + i of the head, or with `interleaved` 2i and 2i + 1; elements from `turned`
+ * on stay as they are. The turned queries go to q_out in their own type; the turned keys and the values go to the
+ * pools as nbx_paged_kv_append writes them (cast(x * (1 / scale))). Arithmetic is fp32, rounded once. This call is an
+ * addition of this library; the pages it was written from have no counterpart.
+ *
+ *   q, new_k, new_v [device] token t at element t * stride, heads [h, d] contiguous there, all in new_dtype
+ *                (NBX_F32 or NBX_BF16): strides allow for the pieces of one projection
+ *   h_q          query heads; 0: keys and values only (q and q_out are not read then)
+ *   cos_table, sin_table [device] fp32 [n_pos, turned / 2]
+ *   positions    [device] int32 [n_tok]; a position outside [0, n_pos) sets NBX_DEV_BAD_LEN and the token is
+ *                skipped (its q_out too)
+ *   q_out        [device] as q with q_out_stride; may be q itself (with q's stride)
+ *   slot_mapping [device] int32 [n_tok]; a slot outside the pool sets NBX_DEV_BAD_SLOT, the token's keys and values
+ *                are skipped and its queries turned all the same
+ *   the other arguments as for nbx_paged_kv_append
+ * Requirements: d and turned multiples of 16, turned <= d <= 1024; buffers and rows 16-byte aligned (strides of whole
+ * 16 bytes). n_tok == 0 returns NBX_OK without a launch.
+ */
+NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q, const void* new_k, int64_t k_stride,
+                                        const void* new_v, int64_t v_stride, int new_dtype, int n_tok, int h_kv, int d,
+                                        const float* cos_table, const float* sin_table, int n_pos, int turned,
+                                        int interleaved, const int32_t* positions, void* q_out, int64_t q_out_stride,
+                                        void* k_pool, void* v_pool, int pool_dtype, int num_pages, int page_tokens,
+                                        const int32_t* slot_mapping, float k_scale, float v_scale, int32_t* status,
+                                        void* stream);
+
+/*
  * nbx_paged_decode_workspace_bytes -- bytes of workspace nbx_paged_decode_attn needs for
  * these sizes (the split plan, the work list and the fp32 split partials).
  * Returns 0 if the sizes are invalid. max_seq_len is the host-known bound on seq_lens.
@@ -458,7 +489,8 @@ enum nbx_callable {
   NBX_CALL_DECODE_MODIFIED = 2,
   NBX_CALL_COPY_PAGES = 3,
   NBX_CALL_FORK = 4,
-  NBX_CALL_COMPACT = 5
+  NBX_CALL_COMPACT = 5,
+  NBX_CALL_APPEND_ROTATED = 6
 };
 NBX_API int nbx_call(int call, const int64_t* args);
 

@@ -23,7 +23,7 @@ from . import _build
 
 __all__ = [
     "NBX_F32", "NBX_BF16", "NBX_E4M3", "NbxError", "NbxLibraryMissing", "build", "lib", "library_path",
-    "nbx_paged_kv_append", "nbx_paged_decode_workspace_bytes", "nbx_paged_decode_attn",
+    "nbx_paged_kv_append", "nbx_paged_kv_append_rotated", "nbx_paged_decode_workspace_bytes", "nbx_paged_decode_attn",
     "nbx_paged_decode_merge", "nbx_set_decode_grid_limit", "nbx_set_decode_wait_test", "nbx_status_string",
     "nbx_paged_decode_bounds", "nbx_paged_decode_attn_fixed_shift", "nbx_decode_fixed_shift_gate",
     "nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
@@ -120,6 +120,10 @@ def _declare(l):
     l.nbx_paged_kv_compact.argtypes = [vp, vp, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, i32, vp,
                                        vp, sz, vp, vp]
     l.nbx_paged_kv_compact.restype = i32
+    i64 = ctypes.c_int64
+    l.nbx_paged_kv_append_rotated.argtypes = [vp, i64, i32, vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, i32, i32, i32,
+                                              vp, vp, i64, vp, vp, i32, i32, i32, vp, f32, f32, vp, vp]
+    l.nbx_paged_kv_append_rotated.restype = i32
     l.nbx_call.argtypes = [i32, ctypes.c_char_p]
     l.nbx_call.restype = i32
     l.nbx_status_string.argtypes = [i32]
@@ -489,7 +493,7 @@ def _p(t):
 
 _calls = {}   # entry point -> its number in nbx_call, and what packs its arguments
 _CALLS = ("nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
-          "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork", "nbx_paged_kv_compact")
+          "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork", "nbx_paged_kv_compact", "nbx_paged_kv_append_rotated")
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -737,3 +741,64 @@ def nbx_paged_kv_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, k_po
          page_tokens, d, _p(k_scales), _p(v_scales), block, moves.data_ptr(), moves.shape[0], counts.data_ptr(),
          workspace.data_ptr(), workspace.nbytes, _p(status))
     return new_block_table, moves, counts
+
+
+# ---------------------------------------------------------------- prompts and shared prefixes
+def _tokens(dev, names: str, *tensors):
+    """Token tensors [n_tok, heads, d] on device `dev` whose rows are contiguous; their strides between tokens, in
+    elements."""
+    strides = []
+    for name, t in zip(names.split(), tensors):
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on cuda:{dev}" if dev >= 0 else f"{name} must be a CUDA tensor")
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 3:
+            raise ValueError(f"{name} must be [tokens, heads, d]")
+        if (stride[2] != 1 and shape[2] > 1) or (stride[1] != shape[2] and shape[1] > 1):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        strides.append(stride[0])
+    return strides
+
+
+def nbx_paged_kv_append_rotated(q: Optional[torch.Tensor], new_k: torch.Tensor, new_v: torch.Tensor, cos: torch.Tensor,
+                                sin: torch.Tensor, positions: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                                slot_mapping: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
+                                interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                                status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """q [n_tok, h_q, d] (or None) and new_k [n_tok, h_kv, d] turned by their positions [n_tok] int32, whose angles'
+    cosines and sines are rows of cos / sin [n_pos, turned / 2] fp32 (halves of the first `turned` elements against each
+    other, or neighbours with `interleaved`); keys and values [n_tok, h_kv, d] into the pools [num_pages, h_kv,
+    page_tokens, d] at slot_mapping [n_tok] int32, cast on store. q, new_k and new_v may be strided between tokens.
+    Returns the turned queries (q_out, which may be q), or None without q."""
+    dev = _one_device("k_pool v_pool cos sin positions slot_mapping status", k_pool, v_pool, cos, sin, positions,
+                      slot_mapping, status)
+    _int32("positions slot_mapping status", positions, slot_mapping, status)
+    num_pages, h_kv, page_tokens, d, _ = _pools(k_pool, v_pool, None, None)
+    k_stride, v_stride = _tokens(dev, "new_k new_v", new_k, new_v)
+    n_tok, table, dtype = new_k.shape[0], cos.shape, new_k.dtype
+    if new_k.shape != (n_tok, h_kv, d) or new_v.shape != new_k.shape or new_v.dtype != dtype or len(table) != 2 or \
+            sin.shape != table or positions.numel() != n_tok or slot_mapping.numel() != n_tok:
+        _misfit("new_k new_v k_pool cos sin positions slot_mapping", new_k, new_v, k_pool, cos, sin, positions,
+                slot_mapping)
+    if cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
+        raise ValueError("cos and sin must be fp32")
+    h_q = q_stride = out_stride = 0
+    if q is not None:
+        (q_stride,) = _tokens(dev, "q", q)
+        h_q = q.shape[1]
+        if q.shape != (n_tok, h_q, d) or q.dtype != dtype:
+            raise ValueError(f"q {list(q.shape)} {q.dtype} does not fit new_k {list(new_k.shape)} {dtype}")
+        if q_out is None:
+            q_out = _new(q.shape, dtype, q, stream)
+        (out_stride,) = _tokens(dev, "q_out", q_out)
+        if q_out.shape != q.shape or q_out.dtype != dtype:
+            raise ValueError(f"q_out must be {list(q.shape)} {dtype}")
+        if q_out.data_ptr() == q.data_ptr() and out_stride != q_stride and n_tok > 1:
+            raise ValueError("q_out in q's place must have q's stride")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _run("nbx_paged_kv_append_rotated", dev, stream, _p(q), q_stride, h_q, new_k.data_ptr(), k_stride, new_v.data_ptr(),
+         v_stride, dtype_code(new_k), n_tok, h_kv, d, cos.data_ptr(), sin.data_ptr(), table[0], 2 * table[1],
+         int(interleaved), positions.data_ptr(), _p(q_out), out_stride, k_pool.data_ptr(), v_pool.data_ptr(),
+         dtype_code(k_pool), num_pages, page_tokens, slot_mapping.data_ptr(), float(k_scale), float(v_scale), _p(status))
+    return q_out

@@ -109,6 +109,69 @@ NBX_API int nbx_paged_kv_append(const void* new_k, const void* new_v, int new_dt
   return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
 }
 
+// Rows of `heads` heads a token, `stride` elements apart: whole 16-byte pieces, no token over another.
+static bool rows_ok(int64_t stride, int n_tok, int heads, int d, int elt) {
+  return (n_tok <= 1 || stride >= static_cast<int64_t>(heads) * d) && (n_tok <= 1 || (stride * elt) % 16 == 0);
+}
+
+NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q, const void* new_k, int64_t k_stride,
+                                        const void* new_v, int64_t v_stride, int new_dtype, int n_tok, int h_kv, int d,
+                                        const float* cos_table, const float* sin_table, int n_pos, int turned,
+                                        int interleaved, const int32_t* positions, void* q_out, int64_t q_out_stride,
+                                        void* k_pool, void* v_pool, int pool_dtype, int num_pages, int page_tokens,
+                                        const int32_t* slot_mapping, float k_scale, float v_scale, int32_t* status,
+                                        void* stream) {
+  if (n_tok < 0 || h_q < 0 || h_kv < 1 || h_kv > (1 << 20) || h_q > (1 << 20) || d < 16 || d > 1024 || (d % 16) != 0 ||
+      num_pages < 1 || page_tokens < 1)
+    return NBX_ERR_SHAPE;
+  if (n_pos < 1 || turned < 16 || turned > d || (turned % 16) != 0) return NBX_ERR_SHAPE;
+  if (new_dtype != NBX_F32 && new_dtype != NBX_BF16) return NBX_ERR_DTYPE;
+  if (pool_dtype != NBX_F32 && pool_dtype != NBX_BF16 && pool_dtype != NBX_E4M3) return NBX_ERR_DTYPE;
+  if (!finite(k_scale) || !finite(v_scale) || !(k_scale > 0.f) || !(v_scale > 0.f)) return NBX_ERR_VALUE;
+  if (interleaved != 0 && interleaved != 1) return NBX_ERR_VALUE;
+  const int elt = new_dtype == NBX_F32 ? 4 : 2;
+  if (!rows_ok(k_stride, n_tok, h_kv, d, elt) || !rows_ok(v_stride, n_tok, h_kv, d, elt) ||
+      (h_q > 0 && (!rows_ok(q_stride, n_tok, h_q, d, elt) || !rows_ok(q_out_stride, n_tok, h_q, d, elt))))
+    return NBX_ERR_SHAPE;
+  if (n_tok == 0) return NBX_OK;
+  if (!new_k || !new_v || !cos_table || !sin_table || !positions || !k_pool || !v_pool || !slot_mapping ||
+      (h_q > 0 && (!q || !q_out)))
+    return NBX_ERR_NULL;
+  if (!aligned16(q) || !aligned16(new_k) || !aligned16(new_v) || !aligned16(cos_table) || !aligned16(sin_table) ||
+      !aligned16(q_out) || !aligned16(k_pool) || !aligned16(v_pool))
+    return NBX_ERR_ALIGN;
+  RotateParams p = {};
+  p.q = q;
+  p.new_k = new_k;
+  p.new_v = new_v;
+  p.cos_table = cos_table;
+  p.sin_table = sin_table;
+  p.positions = positions;
+  p.slot_mapping = slot_mapping;
+  p.q_out = q_out;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.status = status;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out_stride = q_out_stride;
+  p.n_tok = n_tok;
+  p.h_q = h_q;
+  p.h_kv = h_kv;
+  p.d = d;
+  p.n_pos = n_pos;
+  p.turned = turned;
+  p.interleaved = interleaved;
+  p.num_pages = num_pages;
+  p.page_tokens = page_tokens;
+  p.slots = h_q + 2 * h_kv;
+  p.k_inv = 1.0f / k_scale;
+  p.v_inv = 1.0f / v_scale;
+  const cudaError_t e = append_rotated_dispatch(p, new_dtype, pool_dtype, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
+}
+
 static bool decode_shape_ok(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len) {
   if (batch < 0 || rows < 1 || h_q < 1 || h_kv < 1 || (h_q % h_kv) != 0) return false;
   if (d != 64 && d != 128 && d != 256) return false;
@@ -493,6 +556,7 @@ NBX_API int nbx_call(int call, const int64_t* args) {
     case NBX_CALL_COPY_PAGES: return call_with(nbx_paged_kv_copy_pages, args);
     case NBX_CALL_FORK: return call_with(nbx_paged_kv_fork, args);
     case NBX_CALL_COMPACT: return call_with(nbx_paged_kv_compact, args);
+    case NBX_CALL_APPEND_ROTATED: return call_with(nbx_paged_kv_append_rotated, args);
     default: return NBX_ERR_VALUE;
   }
 }

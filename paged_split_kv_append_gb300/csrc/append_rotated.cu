@@ -1,0 +1,204 @@
+// The append with the position rotation on the way: queries and keys are turned by their positions, keys and
+// values go to the paged cache.
+//
+// With the pair (a, b) of a head's vector (elements i and turned / 2 + i, or neighbours 2i and 2i + 1) and the angle
+// whose cosine c and sine s row `position` of the tables holds at i:
+//   a' = a c - b s,   b' = b c + a s          (fp32: a product and an FMA each, then one rounding on the store)
+// Elements from `turned` on, and values, are only cast.
+//
+//  * What bounds it: bytes. A token's row of the tables serves all its heads, everything else is touched once.
+//  * A work item is 16 elements of a row, two vectors of 8 that hold whole pairs: for halves the vectors lie
+//    turned / 2 apart, for neighbours side by side. So every access is 16 bytes or more and no lane exchanges anything.
+//  * A thread keeps its 8 cosines and sines in registers for kHeads heads, and has the loads of all of them in
+//    flight before it turns the first.
+#include "nbx_device.cuh"
+#include "nbx_internal.h"
+
+namespace nbx {
+namespace {
+
+constexpr int kRotThreads = 256;
+
+// Eight consecutive elements as floats (address aligned to 16 bytes).
+struct F8 {
+  float x[8];
+};
+template <class T>
+struct Raw8 {   // as they are in memory
+  uint4 w[T::kBytes / 2];
+};
+template <class T>
+__device__ __forceinline__ Raw8<T> load8(const char* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < T::kBytes / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+template <class T>
+__device__ __forceinline__ F8 floats8(const Raw8<T>& r) {
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < T::kBytes / 2; ++i) {
+    float2 o[T::kEPV / 2];
+    unpack16<T>(r.w[i], o);
+#pragma unroll
+    for (int j = 0; j < T::kEPV / 2; ++j) {
+      f.x[i * T::kEPV + 2 * j] = o[j].x;
+      f.x[i * T::kEPV + 2 * j + 1] = o[j].y;
+    }
+  }
+  return f;
+}
+template <class T>
+__device__ __forceinline__ void store8(char* p, const F8& f);
+template <>
+__device__ __forceinline__ void store8<F32>(char* p, const F8& f) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f.x[0], f.x[1], f.x[2], f.x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f.x[4], f.x[5], f.x[6], f.x[7]);
+}
+template <>
+__device__ __forceinline__ void store8<BF16>(char* p, const F8& f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x[2 * i], f.x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <>
+__device__ __forceinline__ void store8<E4M3>(char* p, const F8& f) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f.x[2 * i], f.x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+  *reinterpret_cast<uint2*>(p) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// In: the new tokens' type (and the queries'); Out: the pools'. kHeads: heads a thread takes.
+// Slots are a token's rows: its query heads, then its key heads, then its value heads; a thread takes slots
+// g, g + groups, ... of its token, at one place of 16 elements.
+template <class In, class Out, int kHeads>
+__global__ void __launch_bounds__(kRotThreads) append_rotated_kernel(RotateParams p) {
+  pdl_launch_dependents();   // as the plain append: what follows waits before it reads the pools or the queries
+  const int places = p.d / 16;
+  const int per_tok = p.groups * places;
+  for (int item = threadIdx.x; item < p.toks * per_tok; item += kRotThreads) {
+    const int tl = item / per_tok, rest = item - tl * per_tok;
+    const int group = rest / places, place = rest - group * places;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * p.toks + tl;
+    if (t >= p.n_tok) break;
+    const int pos = p.positions[t];
+    const int64_t slot = p.slot_mapping[t];
+    const bool reports = group == 0 && place == 0;
+    if (pos < 0 || pos >= p.n_pos) {
+      if (reports) raise_status(p.status, NBX_DEV_BAD_LEN);
+      continue;
+    }
+    const bool held = slot >= 0 && slot < static_cast<int64_t>(p.num_pages) * p.page_tokens;
+    if (reports && !held) raise_status(p.status, NBX_DEV_BAD_SLOT);
+    const int64_t page = held ? slot / p.page_tokens : 0;
+    const int64_t in_page = slot - page * p.page_tokens;
+    // the two vectors of the place
+    const bool turns = place < p.turned / 16;
+    const int a = turns && !p.interleaved ? 8 * place : 16 * place;
+    const int b = turns && !p.interleaved ? a + p.turned / 2 : a + 8;
+    Raw8<In> va[kHeads], vb[kHeads];
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const int s = group + k * p.groups;
+      if (s >= p.slots) break;
+      if (s >= p.h_q && !held) continue;
+      const int hk = s - p.h_q, hv = hk - p.h_kv;
+      const char* src = hk < 0   ? static_cast<const char*>(p.q) + (t * p.q_stride + s * p.d) * In::kBytes
+                        : hv < 0 ? static_cast<const char*>(p.new_k) + (t * p.k_stride + hk * p.d) * In::kBytes
+                                 : static_cast<const char*>(p.new_v) + (t * p.v_stride + hv * p.d) * In::kBytes;
+      va[k] = load8<In>(src + a * In::kBytes);
+      vb[k] = load8<In>(src + b * In::kBytes);
+    }
+    F8 c, n;
+    if (turns) {
+      const char* row_c = reinterpret_cast<const char*>(p.cos_table + static_cast<int64_t>(pos) * (p.turned / 2) + 8 * place);
+      const char* row_n = reinterpret_cast<const char*>(p.sin_table + static_cast<int64_t>(pos) * (p.turned / 2) + 8 * place);
+      c = floats8<F32>(load8<F32>(row_c));
+      n = floats8<F32>(load8<F32>(row_n));
+    }
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const int s = group + k * p.groups;
+      if (s >= p.slots) break;
+      if (s >= p.h_q && !held) continue;
+      const int hk = s - p.h_q, hv = hk - p.h_kv;
+      F8 x = floats8<In>(va[k]), y = floats8<In>(vb[k]);
+      if (turns && hv < 0) {
+        if (p.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x0 = x.x[2 * i], y0 = y.x[2 * i];
+            x.x[2 * i] = fmaf(-x.x[2 * i + 1], n.x[i], x0 * c.x[i]);
+            x.x[2 * i + 1] = fmaf(x0, n.x[i], x.x[2 * i + 1] * c.x[i]);
+            y.x[2 * i] = fmaf(-y.x[2 * i + 1], n.x[4 + i], y0 * c.x[4 + i]);
+            y.x[2 * i + 1] = fmaf(y0, n.x[4 + i], y.x[2 * i + 1] * c.x[4 + i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x0 = x.x[i];
+            x.x[i] = fmaf(-y.x[i], n.x[i], x0 * c.x[i]);
+            y.x[i] = fmaf(x0, n.x[i], y.x[i] * c.x[i]);
+          }
+        }
+      }
+      if (hk < 0) {
+        char* dst = static_cast<char*>(p.q_out) + (t * p.q_out_stride + s * p.d) * In::kBytes;
+        store8<In>(dst + a * In::kBytes, x);
+        store8<In>(dst + b * In::kBytes, y);
+      } else {
+        const float inv = hv < 0 ? p.k_inv : p.v_inv;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x.x[i] *= inv;
+          y.x[i] *= inv;
+        }
+        const int h = hv < 0 ? hk : hv;
+        char* dst = static_cast<char*>(hv < 0 ? p.k_pool : p.v_pool) +
+                    (((page * p.h_kv + h) * p.page_tokens + in_page) * p.d) * Out::kBytes;
+        store8<Out>(dst + a * Out::kBytes, x);
+        store8<Out>(dst + b * Out::kBytes, y);
+      }
+    }
+  }
+}
+
+template <class In, class Out, int kHeads>
+cudaError_t launch_rotated(RotateParams p, cudaStream_t stream) {
+  p.groups = (p.slots + kHeads - 1) / kHeads;
+  const int per_tok = p.groups * (p.d / 16);
+  p.toks = kRotThreads / per_tok > 0 ? kRotThreads / per_tok : 1;
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(p.n_tok) + p.toks - 1) / p.toks);
+  append_rotated_kernel<In, Out, kHeads><<<blocks, kRotThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <class In, class Out>
+cudaError_t launch_rotated(const RotateParams& p, cudaStream_t stream) {
+  // few tokens: fewer heads a thread, so that their loads are on more SMs
+  return static_cast<int64_t>(p.n_tok) * p.slots * (p.d / 16) < static_cast<int64_t>(device_info().sm_count) * 2048
+             ? launch_rotated<In, Out, 1>(p, stream)
+             : launch_rotated<In, Out, 4>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t append_rotated_dispatch(const RotateParams& p, int new_dtype, int pool_dtype, cudaStream_t stream) {
+  if (new_dtype == NBX_F32) {
+    if (pool_dtype == NBX_F32) return launch_rotated<F32, F32>(p, stream);
+    if (pool_dtype == NBX_BF16) return launch_rotated<F32, BF16>(p, stream);
+    return launch_rotated<F32, E4M3>(p, stream);
+  }
+  if (pool_dtype == NBX_F32) return launch_rotated<BF16, F32>(p, stream);
+  if (pool_dtype == NBX_BF16) return launch_rotated<BF16, BF16>(p, stream);
+  return launch_rotated<BF16, E4M3>(p, stream);
+}
+
+}  // namespace nbx

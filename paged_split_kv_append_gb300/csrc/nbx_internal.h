@@ -116,6 +116,28 @@ struct AppendParams {
 
 cudaError_t append_dispatch(const AppendParams& p, int new_dtype, int pool_dtype, cudaStream_t stream);
 
+// The append with the position rotation; strides in elements between tokens.
+struct RotateParams {
+  const void* q;
+  const void* new_k;
+  const void* new_v;
+  const float* cos_table;   // [n_pos, turned / 2]
+  const float* sin_table;
+  const int32_t* positions;
+  const int32_t* slot_mapping;
+  void* q_out;
+  void* k_pool;
+  void* v_pool;
+  int32_t* status;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int n_tok, h_q, h_kv, d, n_pos, turned, interleaved, num_pages, page_tokens;
+  int slots;          // rows of a token: h_q + 2 h_kv
+  int groups, toks;   // set by the launch: groups of slots, tokens of a CTA
+  float k_inv, v_inv;
+};
+
+cudaError_t append_rotated_dispatch(const RotateParams& p, int new_dtype, int pool_dtype, cudaStream_t stream);
+
 // ---------------------------------------------------------------- decode
 constexpr int kTileN = NBX_TILE_POSITIONS;  // positions per staged tile
 constexpr int kQB = 4;                      // query vectors (rows x heads of one KV head) per work unit
