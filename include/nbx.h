@@ -136,6 +136,31 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
                                         void* stream);
 
 /*
+ * nbx_prompt_attn -- causal attention over whole prompts, packed one behind the other.
+ *
+ * Sequence b's tokens are rows seq_start[b] .. seq_start[b + 1] - 1 of q, k and v. Token i of a sequence (from 0) and
+ * query head h attend keys 0 .. i of the sequence and KV head h / (h_q / h_kv):
+ *   z_j = scale * (q . k_j),  out = sum_j e^(z_j - max z) v_j / sum_j e^(z_j - max z),
+ * 0 where every z_j is -infinity. Scores, sums and statistics are fp32; weights enter the product with the values
+ * rounded to bf16 (2^-8), the output is rounded once. Values at keys that a row does not see never reach it, not even a
+ * NaN. Results do not depend on what else is packed into the call. This call is an addition of this library; the
+ * pages it was written from have no counterpart.
+ *
+ *   q [n_tok, h_q, d], k, v [n_tok, h_kv, d] [device] NBX_BF16 (dtype), token t at element t * stride, its heads
+ *                contiguous there: strides allow for the pieces of one projection
+ *   seq_start    [device] int32 [batch + 1], ascending, seq_start[0] >= 0, seq_start[batch] <= n_tok. A sequence whose
+ *                bounds make no sense sets NBX_DEV_BAD_LEN and is skipped.
+ *   scale        softmax scale (finite)
+ *   out          [device] bf16 [n_tok, h_q, d], contiguous; rows of no sequence are left as they were
+ *   status       [device] int32 or NULL;  stream  cudaStream_t
+ * Requirements: h_q % h_kv == 0; d in {64, 128, 256}; buffers and rows 16-byte aligned (strides of whole 16 bytes).
+ * n_tok == 0 or batch == 0 returns NBX_OK without a launch.
+ */
+NBX_API int nbx_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, int dtype, int n_tok, int h_q, int h_kv, int d, const int32_t* seq_start,
+                            int batch, float scale, void* out, int32_t* status, void* stream);
+
+/*
  * nbx_paged_decode_workspace_bytes -- bytes of workspace nbx_paged_decode_attn needs for
  * these sizes (the split plan, the work list and the fp32 split partials).
  * Returns 0 if the sizes are invalid. max_seq_len is the host-known bound on seq_lens.
@@ -490,7 +515,8 @@ enum nbx_callable {
   NBX_CALL_COPY_PAGES = 3,
   NBX_CALL_FORK = 4,
   NBX_CALL_COMPACT = 5,
-  NBX_CALL_APPEND_ROTATED = 6
+  NBX_CALL_APPEND_ROTATED = 6,
+  NBX_CALL_PROMPT = 7
 };
 NBX_API int nbx_call(int call, const int64_t* args);
 

@@ -23,7 +23,7 @@ from . import _build
 
 __all__ = [
     "NBX_F32", "NBX_BF16", "NBX_E4M3", "NbxError", "NbxLibraryMissing", "build", "lib", "library_path",
-    "nbx_paged_kv_append", "nbx_paged_kv_append_rotated", "nbx_paged_decode_workspace_bytes", "nbx_paged_decode_attn",
+    "nbx_paged_kv_append", "nbx_paged_kv_append_rotated", "nbx_prompt_attn", "nbx_paged_decode_workspace_bytes", "nbx_paged_decode_attn",
     "nbx_paged_decode_merge", "nbx_set_decode_grid_limit", "nbx_set_decode_wait_test", "nbx_status_string",
     "nbx_paged_decode_bounds", "nbx_paged_decode_attn_fixed_shift", "nbx_decode_fixed_shift_gate",
     "nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
@@ -124,6 +124,8 @@ def _declare(l):
     l.nbx_paged_kv_append_rotated.argtypes = [vp, i64, i32, vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, i32, i32, i32,
                                               vp, vp, i64, vp, vp, i32, i32, i32, vp, f32, f32, vp, vp]
     l.nbx_paged_kv_append_rotated.restype = i32
+    l.nbx_prompt_attn.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, i32, vp, i32, f32, vp, vp, vp]
+    l.nbx_prompt_attn.restype = i32
     l.nbx_call.argtypes = [i32, ctypes.c_char_p]
     l.nbx_call.restype = i32
     l.nbx_status_string.argtypes = [i32]
@@ -493,7 +495,8 @@ def _p(t):
 
 _calls = {}   # entry point -> its number in nbx_call, and what packs its arguments
 _CALLS = ("nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
-          "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork", "nbx_paged_kv_compact", "nbx_paged_kv_append_rotated")
+          "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork", "nbx_paged_kv_compact", "nbx_paged_kv_append_rotated",
+          "nbx_prompt_attn")
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -802,3 +805,26 @@ def nbx_paged_kv_append_rotated(q: Optional[torch.Tensor], new_k: torch.Tensor, 
          int(interleaved), positions.data_ptr(), _p(q_out), out_stride, k_pool.data_ptr(), v_pool.data_ptr(),
          dtype_code(k_pool), num_pages, page_tokens, slot_mapping.data_ptr(), float(k_scale), float(v_scale), _p(status))
     return q_out
+
+
+def nbx_prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start: torch.Tensor, scale: float,
+                    out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Causal attention over packed prompts: q [n_tok, h_q, d], k and v [n_tok, h_kv, d] bf16 (they may be strided
+    between tokens), sequence b being rows seq_start[b] .. seq_start[b + 1] - 1 (seq_start [batch + 1] int32)
+    -> out [n_tok, h_q, d] bf16; rows of no sequence are left as they were (unwritten in a new tensor)."""
+    dev = _one_device("seq_start out status", seq_start, out, status)
+    _int32("seq_start status", seq_start, status)
+    q_stride, k_stride, v_stride = _tokens(dev, "q k v", q, k, v)
+    (n_tok, h_q, d), kv, batch = q.shape, k.shape, seq_start.numel() - 1
+    if kv != v.shape or kv[0] != n_tok or kv[2] != d or batch < 0:
+        _misfit("q k v seq_start", q, k, v, seq_start)
+    if q.dtype is not torch.bfloat16 or k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
+        raise TypeError("q, k and v must be bf16")
+    if out is None:
+        out = _new(q.shape, torch.bfloat16, q, stream)
+    elif out.shape != q.shape or out.dtype is not torch.bfloat16:
+        raise ValueError(f"out must be {list(q.shape)} bf16")
+    _run("nbx_prompt_attn", dev, stream, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+         NBX_BF16, n_tok, h_q, kv[1], d, seq_start.data_ptr(), batch, float(scale), out.data_ptr(), _p(status))
+    return out

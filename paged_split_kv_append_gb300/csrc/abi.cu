@@ -172,6 +172,39 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
   return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
 }
 
+NBX_API int nbx_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, int dtype, int n_tok, int h_q, int h_kv, int d, const int32_t* seq_start,
+                            int batch, float scale, void* out, int32_t* status, void* stream) {
+  if (n_tok < 0 || batch < 0 || h_q < 1 || h_kv < 1 || (h_q % h_kv) != 0 || h_q > (1 << 20)) return NBX_ERR_SHAPE;
+  if (d != 64 && d != 128 && d != 256) return NBX_ERR_SHAPE;
+  if (dtype != NBX_BF16) return NBX_ERR_DTYPE;
+  if (!finite(scale) || !finite(scale * kLog2eHost)) return NBX_ERR_VALUE;
+  if (!rows_ok(q_stride, n_tok, h_q, d, 2) || !rows_ok(k_stride, n_tok, h_kv, d, 2) || !rows_ok(v_stride, n_tok, h_kv, d, 2))
+    return NBX_ERR_SHAPE;
+  if (n_tok == 0 || batch == 0) return NBX_OK;
+  if (!q || !k || !v || !seq_start || !out) return NBX_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return NBX_ERR_ALIGN;
+  PromptParams p = {};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.seq_start = seq_start;
+  p.out = out;
+  p.status = status;
+  // (a single token's stride is never used; the tensor maps want one that fits)
+  p.q_stride = n_tok > 1 ? q_stride : static_cast<int64_t>(h_q) * d;
+  p.k_stride = n_tok > 1 ? k_stride : static_cast<int64_t>(h_kv) * d;
+  p.v_stride = n_tok > 1 ? v_stride : static_cast<int64_t>(h_kv) * d;
+  p.n_tok = n_tok;
+  p.h_q = h_q;
+  p.h_kv = h_kv;
+  p.d = d;
+  p.batch = batch;
+  p.scale_log2 = scale * kLog2eHost;
+  const cudaError_t e = prompt_dispatch(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
+}
+
 static bool decode_shape_ok(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len) {
   if (batch < 0 || rows < 1 || h_q < 1 || h_kv < 1 || (h_q % h_kv) != 0) return false;
   if (d != 64 && d != 128 && d != 256) return false;
@@ -557,6 +590,7 @@ NBX_API int nbx_call(int call, const int64_t* args) {
     case NBX_CALL_FORK: return call_with(nbx_paged_kv_fork, args);
     case NBX_CALL_COMPACT: return call_with(nbx_paged_kv_compact, args);
     case NBX_CALL_APPEND_ROTATED: return call_with(nbx_paged_kv_append_rotated, args);
+    case NBX_CALL_PROMPT: return call_with(nbx_prompt_attn, args);
     default: return NBX_ERR_VALUE;
   }
 }

@@ -138,6 +138,21 @@ struct RotateParams {
 
 cudaError_t append_rotated_dispatch(const RotateParams& p, int new_dtype, int pool_dtype, cudaStream_t stream);
 
+// Attention over packed prompts; strides in elements between tokens.
+struct PromptParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* seq_start;   // [batch + 1]
+  void* out;
+  int32_t* status;
+  int64_t q_stride, k_stride, v_stride;
+  int n_tok, h_q, h_kv, d, batch;
+  float scale_log2;           // scale * log2(e)
+};
+
+cudaError_t prompt_dispatch(const PromptParams& p, cudaStream_t stream);
+
 // ---------------------------------------------------------------- decode
 constexpr int kTileN = NBX_TILE_POSITIONS;  // positions per staged tile
 constexpr int kQB = 4;                      // query vectors (rows x heads of one KV head) per work unit

@@ -1,0 +1,71 @@
+// Causal attention of one query vector, key by key in fp32, by one warp.
+#pragma once
+
+#include "nbx_device.cuh"
+
+namespace nbx {
+
+// out = sum_j e^(z_j - max z) v_j / sum_j e^(z_j - max z), z_j = scale (q . k_j), over keys 0 .. n - 1 (0 where no z_j
+// is above -inf), rounded once to bf16. Keys 32 at a time: lane l scores key l of the block, then every lane gathers its
+// D / 32 columns. k, v: key 0 of the head, rows `k_stride` and `v_stride` elements apart. c = scale * log2(e).
+template <int D>
+__device__ __noinline__ void prompt_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                        int64_t k_stride, int64_t v_stride, int n, float c, __nv_bfloat16* out) {
+  constexpr int kCols = D / 32;
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f, acc[kCols];
+#pragma unroll
+  for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+  for (int n0 = 0; n0 < n; n0 += 32) {
+    float z = -INFINITY;
+    if (n0 + lane < n) {
+      const uint4* kr = reinterpret_cast<const uint4*>(k + (n0 + lane) * k_stride);
+      const uint4* qr = reinterpret_cast<const uint4*>(q);
+      f32x2 s = pack2(0.f, 0.f);
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        f32x2 a[4], b[4];
+        unpack16x2<BF16>(__ldg(kr + i), a);
+        unpack16x2<BF16>(__ldg(qr + i), b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fma2(a[j], b[j], s);
+      }
+      const float2 t = unpack2(s);
+      z = (t.x + t.y) * c;
+    }
+    float top = z;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float m2 = max_nan(m, top);
+    if (m2 == -INFINITY) continue;
+    const float f = fast_exp2(m - m2);
+    const float w = n0 + lane < n ? fast_exp2(z - m2) : 0.f;
+    float sum = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = fmaf(l, f, sum);
+    m = m2;
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) acc[e] *= f;
+    const int keys = min(32, n - n0);
+    for (int j = 0; j < keys; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const __nv_bfloat16* vr = v + (n0 + j) * v_stride + lane * kCols;
+#pragma unroll
+      for (int e = 0; e < kCols; e += 2) {
+        const float2 x = bf16x2_to_float2(__ldg(reinterpret_cast<const uint32_t*>(vr + e)));
+        acc[e] = fmaf(wj, x.x, acc[e]);
+        acc[e + 1] = fmaf(wj, x.y, acc[e + 1]);
+      }
+    }
+  }
+  const float inv = m == -INFINITY ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < kCols; e += 2) {
+    const __nv_bfloat162 h = m == -INFINITY ? __floats2bfloat162_rn(0.f, 0.f)
+                                            : __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+    *reinterpret_cast<__nv_bfloat162*>(out + lane * kCols + e) = h;
+  }
+}
+
+}  // namespace nbx
