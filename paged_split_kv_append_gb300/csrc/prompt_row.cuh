@@ -7,10 +7,12 @@ namespace nbx {
 
 // out = sum_j e^(z_j - max z) v_j / sum_j e^(z_j - max z), z_j = scale (q . k_j), over keys 0 .. n - 1 (0 where no z_j
 // is above -inf), rounded once to bf16. Keys 32 at a time: lane l scores key l of the block, then every lane gathers its
-// D / 32 columns. k, v: key 0 of the head, rows `k_stride` and `v_stride` elements apart. c = scale * log2(e).
+// D / 32 columns. k, v: key 0 of the head, rows `k_stride` and `v_stride` elements apart. c = scale * log2(e). Columns
+// [col0, col1) are written.
 template <int D>
 __device__ __noinline__ void prompt_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                                        int64_t k_stride, int64_t v_stride, int n, float c, __nv_bfloat16* out) {
+                                        int64_t k_stride, int64_t v_stride, int n, float c, __nv_bfloat16* out, int col0,
+                                        int col1) {
   constexpr int kCols = D / 32;
   const int lane = threadIdx.x & 31;
   float m = -INFINITY, l = 0.f, acc[kCols];
@@ -62,6 +64,7 @@ __device__ __noinline__ void prompt_row(const __nv_bfloat16* q, const __nv_bfloa
   const float inv = m == -INFINITY ? 0.f : 1.f / l;
 #pragma unroll
   for (int e = 0; e < kCols; e += 2) {
+    if (lane * kCols < col0 || lane * kCols >= col1) break;
     const __nv_bfloat162 h = m == -INFINITY ? __floats2bfloat162_rn(0.f, 0.f)
                                             : __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
     *reinterpret_cast<__nv_bfloat162*>(out + lane * kCols + e) = h;
