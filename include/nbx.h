@@ -428,6 +428,34 @@ NBX_API int nbx_paged_decode_attn_modified(const void* q, int q_dtype, int batch
                                            const int32_t* key_begin, const int32_t* key_end, void* out, int out_dtype,
                                            void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
 
+/*
+ * nbx_paged_decode_attn_shared -- decode attention for sequences that share a prefix of the cache, read once a group.
+ *
+ * The results are nbx_paged_decode_attn's (out in out_dtype, fp32 or bf16, rounded once), to fp32 rounding. Group g is the
+ * sequences group_start[g] .. group_start[g + 1] - 1, and says that the rows of the block table that belong to them name
+ * the same pages for positions 0 .. shared_lens[g] - 1, as nbx_paged_kv_fork leaves them. That many positions, cut to
+ * whole pages and to what every query row of the group sees, are read through the group's first row that is not empty,
+ * for all of its query vectors at once; each sequence's other positions are its own. What shared_lens may say: anything up to the
+ * common prefix (a row that holds other pages there is read as if it held the first row's). Sequences of no group, groups
+ * of one and short prefixes are read sequence by sequence; empty sequences may lie in a group.
+ * Prefixes are read apart for bf16 and E4M3 pools under bf16 queries, on the tensor cores: a bf16 output takes the
+ * prefix's weights rounded to 2^-8, an fp32 one to 2^-17 or better. Elsewhere the groups are ignored.
+ *
+ *   group_start  [device] int32 [n_groups + 1], ascending, within [0, batch]
+ *   shared_lens  [device] int32 [n_groups], >= 0. Groups that make no sense set NBX_DEV_BAD_ROW and none counts.
+ *   workspace    [device] nbx_paged_decode_shared_workspace_bytes(...) bytes, 256-byte aligned
+ *   every other argument, rule and status bit as for nbx_paged_decode_attn_modified without a modification
+ */
+NBX_API size_t nbx_paged_decode_shared_workspace_bytes(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len,
+                                                       int n_groups);
+NBX_API int nbx_paged_decode_attn_shared(const void* q, int q_dtype, int batch, int rows, int h_q, int d,
+                                         const void* k_pool, const void* v_pool, int pool_dtype, int num_pages, int h_kv,
+                                         int page_tokens, const int32_t* block_table, int max_pages,
+                                         const int32_t* seq_lens, int max_seq_len, const int32_t* group_start,
+                                         const int32_t* shared_lens, int n_groups, float scale, float k_scale,
+                                         float v_scale, void* out, int out_dtype, void* workspace,
+                                         size_t workspace_bytes, int32_t* status, void* stream);
+
 /* ------------------------------------------------------------------------------------------------
  * Pages. A page is in use while an entry of the block table names it, within its row's length or past
  * it (a page reserved for growth). There are no reference counts: filling a row with -1 frees the pages
@@ -516,7 +544,8 @@ enum nbx_callable {
   NBX_CALL_FORK = 4,
   NBX_CALL_COMPACT = 5,
   NBX_CALL_APPEND_ROTATED = 6,
-  NBX_CALL_PROMPT = 7
+  NBX_CALL_PROMPT = 7,
+  NBX_CALL_DECODE_SHARED = 8
 };
 NBX_API int nbx_call(int call, const int64_t* args);
 

@@ -28,6 +28,7 @@ __all__ = [
     "nbx_paged_decode_bounds", "nbx_paged_decode_attn_fixed_shift", "nbx_decode_fixed_shift_gate",
     "nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
     "nbx_paged_decode_modified_workspace_bytes", "nbx_paged_decode_modified_partial_kernel",
+    "nbx_paged_decode_attn_shared", "nbx_paged_decode_shared_workspace_bytes",
     "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork",
     "nbx_paged_kv_fork_workspace_bytes", "nbx_paged_kv_compact", "nbx_paged_kv_compact_workspace_bytes",
     "dtype_code",
@@ -126,6 +127,11 @@ def _declare(l):
     l.nbx_paged_kv_append_rotated.restype = i32
     l.nbx_prompt_attn.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, i32, vp, i32, f32, vp, vp, vp]
     l.nbx_prompt_attn.restype = i32
+    l.nbx_paged_decode_shared_workspace_bytes.argtypes = [i32] * 7
+    l.nbx_paged_decode_shared_workspace_bytes.restype = sz
+    l.nbx_paged_decode_attn_shared.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp, i32,
+                                               vp, vp, i32, f32, f32, f32, vp, i32, vp, sz, vp, vp]
+    l.nbx_paged_decode_attn_shared.restype = i32
     l.nbx_call.argtypes = [i32, ctypes.c_char_p]
     l.nbx_call.restype = i32
     l.nbx_status_string.argtypes = [i32]
@@ -496,7 +502,7 @@ def _p(t):
 _calls = {}   # entry point -> its number in nbx_call, and what packs its arguments
 _CALLS = ("nbx_paged_kv_append_block_scaled", "nbx_paged_decode_attn_block_scaled", "nbx_paged_decode_attn_modified",
           "nbx_paged_kv_copy_pages", "nbx_paged_kv_fork", "nbx_paged_kv_compact", "nbx_paged_kv_append_rotated",
-          "nbx_prompt_attn")
+          "nbx_prompt_attn", "nbx_paged_decode_attn_shared")
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -827,4 +833,39 @@ def nbx_prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start
         raise ValueError(f"out must be {list(q.shape)} bf16")
     _run("nbx_prompt_attn", dev, stream, q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
          NBX_BF16, n_tok, h_q, kv[1], d, seq_start.data_ptr(), batch, float(scale), out.data_ptr(), _p(status))
+    return out
+
+
+def nbx_paged_decode_shared_workspace_bytes(batch: int, rows: int, h_q: int, h_kv: int, d: int, max_seq_len: int,
+                                            n_groups: int) -> int:
+    return int(lib().nbx_paged_decode_shared_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len, n_groups))
+
+
+def nbx_paged_decode_attn_shared(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor,
+                                 seq_lens: torch.Tensor, max_seq_len: int, group_start: torch.Tensor,
+                                 shared_lens: torch.Tensor, scale: float, k_scale: float = 1.0, v_scale: float = 1.0,
+                                 out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                                 workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                                 stream=None) -> torch.Tensor:
+    """nbx_paged_decode_attn for groups of sequences whose first positions lie in the same pages: sequences
+    group_start[g] .. group_start[g + 1] - 1 (int32 [n_groups + 1]) share their first shared_lens[g] positions (int32
+    [n_groups]), which are read once for all of them. out [batch, rows, h_q, d] is fp32 or bf16 (out's dtype, or
+    out_dtype)."""
+    dev = _one_device("q k_pool v_pool block_table seq_lens group_start shared_lens out workspace status", q, k_pool,
+                      v_pool, block_table, seq_lens, group_start, shared_lens, out, workspace, status)
+    num_pages, h_kv, page_tokens, d, _ = _pools(k_pool, v_pool, None, None)
+    _int32("group_start shared_lens status", group_start, shared_lens, status)
+    n_groups = shared_lens.numel()
+    if group_start.numel() != n_groups + 1:
+        _misfit("group_start shared_lens", group_start, shared_lens)
+    batch, rows, h_q, max_pages, out = _modified_shapes(q, d, block_table, seq_lens, None, None, None, out, out_dtype,
+                                                        status, stream)
+    if workspace is None:
+        workspace = _workspace(nbx_paged_decode_shared_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len, n_groups),
+                               q, stream)
+    _run("nbx_paged_decode_attn_shared", dev, stream, q.data_ptr(), dtype_code(q), batch, rows, h_q, d,
+         k_pool.data_ptr(), v_pool.data_ptr(), dtype_code(k_pool), num_pages, h_kv, page_tokens, block_table.data_ptr(),
+         max_pages, seq_lens.data_ptr(), int(max_seq_len), group_start.data_ptr(), shared_lens.data_ptr(), n_groups,
+         float(scale), float(k_scale), float(v_scale), out.data_ptr(), dtype_code(out), workspace.data_ptr(),
+         workspace.nbytes, _p(status))
     return out

@@ -22,7 +22,7 @@ LIB = os.path.join(LIB_DIR, "libnbx.so")
 SOURCES = ["abi.cu", "append.cu", "decode_common.cu", "decode_f32.cu", "decode_bf16.cu", "decode_e4m3.cu",
            "decode_simt_mod.cu", "decode_warp_bf16.cu", "decode_warp_e4m3.cu", "decode_warp_block.cu",
            "decode_mma.cu", "decode_mma_mod.cu", "decode_mma_block.cu", "noalloc.cu", "append_block.cu",
-           "append_rotated.cu", "prompt.cu", "pages.cu"]
+           "append_rotated.cu", "prompt.cu", "shared.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "-I", INCLUDE]

@@ -281,14 +281,16 @@ struct ModArgs {
 
 // The decode call behind every decode entry point. `identity` reads the pools as one page per
 // sequence through an identity block table the plan kernel writes into the workspace; `lens_out`
-// and `len_add` make it a decode step's (attend with seq_lens + len_add, write that length back).
+// and `len_add` make it a decode step's (attend with seq_lens + len_add, write that length back). `groups`: a decode of
+// sequences that share prefixes.
 static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q, int d, const void* k_pool,
                        const void* v_pool, int pool_dtype, int num_pages, int h_kv, int page_tokens,
                        const int32_t* block_table, int max_pages, const int32_t* seq_lens, int max_seq_len,
                        float scale, float k_scale, float v_scale, float* out, void* workspace,
                        size_t workspace_bytes, int32_t* status, cudaStream_t stream, bool identity,
                        int32_t* lens_out, int len_add, const float* fs_q_norm = nullptr,
-                       const float* fs_kv_max = nullptr, const ModArgs* mod = nullptr) {
+                       const float* fs_kv_max = nullptr, const ModArgs* mod = nullptr,
+                       const SharedParams* groups = nullptr) {
   if (!decode_shape_ok(batch, rows, h_q, h_kv, d, max_seq_len)) return NBX_ERR_SHAPE;
   if (num_pages < 1 || page_tokens < 1 || max_pages < 1) return NBX_ERR_SHAPE;
   if (static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_pages) * page_tokens) return NBX_ERR_SHAPE;
@@ -312,6 +314,13 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
   WorkspaceLayout w;
   if (!workspace_layout(batch, rows, h_q, h_kv, d, max_seq_len, &w, mod != nullptr)) return NBX_ERR_SHAPE;
   if (workspace_bytes < w.total) return NBX_ERR_WORKSPACE;
+  SharedLayout sw = {};
+  if (groups) {
+    if (groups->n_groups > 0 && (!groups->group_start || !groups->shared_lens)) return NBX_ERR_NULL;
+    if (!finite(scale * k_scale * kLog2eHost)) return NBX_ERR_VALUE;
+    if (!shared_layout(batch, rows, h_q, h_kv, d, max_seq_len, groups->n_groups, &sw)) return NBX_ERR_SHAPE;
+    if (workspace_bytes < sw.total) return NBX_ERR_WORKSPACE;
+  }
   int x = 0;
   if (mod) {
     const bool scored = mod->softcap > 0.f || mod->slopes || mod->key_begin || mod->key_end;
@@ -379,6 +388,21 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
     p.ranges = reinterpret_cast<int2*>(ws + w.ranges);
     p.order = reinterpret_cast<int32_t*>(ws + w.order);
   }
+  if (groups && groups->n_groups > 0 && prefix_path_applies(p, q_dtype, pool_dtype)) {
+    SharedParams g = *groups;
+    g.seqs = reinterpret_cast<int2*>(ws + sw.seqs);
+    g.groups = reinterpret_cast<PrefixGroup*>(ws + sw.groups);
+    p.header = reinterpret_cast<int32_t*>(ws + sw.header);
+    p.plan = reinterpret_cast<SeqPlan*>(ws + sw.plan);
+    p.entries = reinterpret_cast<Entry*>(ws + sw.entries);
+    p.m_part = reinterpret_cast<float*>(ws + sw.m_part);
+    p.l_part = reinterpret_cast<float*>(ws + sw.l_part);
+    p.acc_part = reinterpret_cast<float*>(ws + sw.acc_part);
+    p.max_splits = sw.max_splits;
+    p.out_bf16 = mod->out_dtype == NBX_BF16;
+    const cudaError_t e = shared_dispatch(g, p, q_dtype, pool_dtype, g_grid_limit.load(), stream);
+    return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
+  }
   const cudaError_t e = decode_dispatch(p, q_dtype, pool_dtype, x, g_grid_limit.load(), stream);
   return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
 }
@@ -429,6 +453,29 @@ NBX_API int nbx_paged_decode_attn_block_scaled(const void* q, int q_dtype, int b
                      block_table, max_pages, seq_lens, max_seq_len, scale, 1.f, 1.f, static_cast<float*>(out), workspace,
                      workspace_bytes, status, static_cast<cudaStream_t>(stream), false, nullptr, 0, nullptr, nullptr,
                      &mod);
+}
+
+NBX_API size_t nbx_paged_decode_shared_workspace_bytes(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len,
+                                                       int n_groups) {
+  if (!decode_shape_ok(batch, rows, h_q, h_kv, d, max_seq_len) || n_groups < 0) return 0;
+  SharedLayout w;
+  return shared_layout(batch, rows, h_q, h_kv, d, max_seq_len, n_groups, &w) ? w.total : 0;
+}
+
+NBX_API int nbx_paged_decode_attn_shared(const void* q, int q_dtype, int batch, int rows, int h_q, int d,
+                                         const void* k_pool, const void* v_pool, int pool_dtype, int num_pages, int h_kv,
+                                         int page_tokens, const int32_t* block_table, int max_pages,
+                                         const int32_t* seq_lens, int max_seq_len, const int32_t* group_start,
+                                         const int32_t* shared_lens, int n_groups, float scale, float k_scale,
+                                         float v_scale, void* out, int out_dtype, void* workspace,
+                                         size_t workspace_bytes, int32_t* status, void* stream) {
+  if (n_groups < 0) return NBX_ERR_SHAPE;
+  const ModArgs mod = {false, nullptr, nullptr, 0, 0.f, nullptr, nullptr, nullptr, out_dtype};
+  const SharedParams groups = {group_start, shared_lens, n_groups, nullptr, nullptr};
+  return decode_call(q, q_dtype, batch, rows, h_q, d, k_pool, v_pool, pool_dtype, num_pages, h_kv, page_tokens,
+                     block_table, max_pages, seq_lens, max_seq_len, scale, k_scale, v_scale, static_cast<float*>(out),
+                     workspace, workspace_bytes, status, static_cast<cudaStream_t>(stream), false, nullptr, 0, nullptr,
+                     nullptr, &mod, &groups);
 }
 
 NBX_API int nbx_paged_decode_attn_fixed_shift(const void* q, int q_dtype, int batch, int rows, int h_q, int d,
@@ -591,6 +638,7 @@ NBX_API int nbx_call(int call, const int64_t* args) {
     case NBX_CALL_COMPACT: return call_with(nbx_paged_kv_compact, args);
     case NBX_CALL_APPEND_ROTATED: return call_with(nbx_paged_kv_append_rotated, args);
     case NBX_CALL_PROMPT: return call_with(nbx_prompt_attn, args);
+    case NBX_CALL_DECODE_SHARED: return call_with(nbx_paged_decode_attn_shared, args);
     default: return NBX_ERR_VALUE;
   }
 }

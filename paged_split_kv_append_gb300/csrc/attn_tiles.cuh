@@ -496,7 +496,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *sh.tmem_slot;
-  pdl_wait();                // the inputs are written and visible from here on
+  // the inputs are written and visible from here on. (kWaitLate: they were before the grid ahead began, which this one
+  // may run beside; the grid behind waits for both through this one)
+  if constexpr (!W::kWaitLate) pdl_wait();
   pdl_launch_dependents();
   bool ok = true;
   if (warp < 8) {
@@ -555,6 +557,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_dealloc(tmem, 512);
+  if constexpr (W::kWaitLate) pdl_wait();
 }
 
 // ---- host side

@@ -345,6 +345,33 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned block, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// ---------------------------------------------------------------- shared prefixes
+// What the plan says of a group: its first sequence, their number, positions shared (whole pages), positions of a split
+// of them and their number, M tile pairs of its query vectors, its first work unit, the row of the block table that
+// names the pages.
+struct PrefixGroup {
+  int32_t b0, n, eff, seg, splits, pairs, unit, row;
+};
+
+struct SharedParams {
+  const int32_t* group_start;   // [n_groups + 1]
+  const int32_t* shared_lens;   // [n_groups]
+  int n_groups;
+  // workspace
+  int2* seqs;                   // [batch] positions read with the group, splits of them
+  PrefixGroup* groups;          // [n_groups]
+};
+
+struct SharedLayout {
+  size_t header, plan, entries, m_part, l_part, acc_part, seqs, groups, total;
+  int max_splits;
+};
+bool shared_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len, int n_groups, SharedLayout* out);
+// Whether prefixes are read apart for these formats; elsewhere a call is a decode that ignores its groups.
+bool prefix_path_applies(const DecodeParams& p, int q_dtype, int pool_dtype);
+cudaError_t shared_dispatch(const SharedParams& s, const DecodeParams& p, int q_dtype, int pool_dtype, int grid_limit,
+                            cudaStream_t stream);
+
 struct MergeParams {
   const float* acc_part;
   const float* m_part;

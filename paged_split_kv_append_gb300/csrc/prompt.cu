@@ -35,6 +35,7 @@ struct PromptWork {
   using Params = PromptTilesParams;
   using C = AttnCfg<D>;
   static constexpr bool kPaged = false;
+  static constexpr bool kWaitLate = false;
   static constexpr int kTerms = 1;
   const Params& p;
   int tpt, tpb;        // tokens of a tile, of a block
