@@ -1,24 +1,31 @@
 // Attention of 128-row tiles of query vectors on tcgen05: what prompt attention and the shared-prefix decode run.
 //
-// A work unit is one or two M tiles of 128 query vectors of one KV head (a tile holds `toks` tokens with `heads` query
-// heads each) and the keys they attend, in tiles of 128. Per key tile, with scores in log2 units:
+// A work unit is one or two M tiles of 128 query vectors of one KV head (a tile holds some tokens with `heads` query heads
+// each) and the keys they attend, in tiles of kN. Per key tile, with scores in log2 units:
 //   S = Q K^T;  m' = max(m, rowmax S) (moved only when it grows by more than 2^8);  P = 2^(c S - m');
 //   l = l 2^(m - m') + rowsum P;  O = O 2^(m - m') + P V.
-// S and O are fp32 accumulators in TMEM; P is written over S, in bf16 (kTerms = 1: each weight is off by up to 2^-8 of
-// itself, as much as the bf16 output's own rounding) or as two bf16 terms (kTerms = 2: 2^-17, for fp32 outputs).
+// S and O are fp32 accumulators in TMEM; P is written over S in kTerms terms of the values' 16-bit type: one for bf16
+// outputs (each weight off by up to 2^-8 of itself in bf16, as much as the output's own rounding; 2^-11 in f16), for fp32
+// outputs as many as leave 2^-22 or less (three in bf16, two in f16), on key tiles of 64, whose S leaves them room.
 //
-// One persistent CTA per SM, ten warps, every wait bounded:
+// One persistent CTA per SM, twelve warps, every wait bounded:
 //  * warps 0-3 and 4-7: two softmax groups. Up to d = 128 each has an M tile of its own, one row a thread, and the two
-//    take turns with the tensor pipe: while one group works on its S, the MMAs of the other's tile run. At d = 256 O
-//    fills half of the TMEM, so there is one M tile, S is double-buffered, and the groups share each row, 64 columns
-//    each; the two threads of a row swap their maxima through shared memory.
-//  * warp 8 fills the ring of K and V with TMA: slots of 32 KB (16 KB at d = 64), a whole tile, or at d = 256 half of one
-//    (128 columns of K, 64 keys of V); and the unit's Q tiles.
-//  * warp 9 issues the MMAs: QK^T (both operands from shared memory, M = N = 128) and PV (P from TMEM, N = d), in an
-//    order in which the group whose P is awaited is never the one whose S was asked for last. Waiting for P(j) of a
-//    tile is all that orders PV(j), QK(j + 1) of the same tile follows it in the pipe and may overwrite P(j).
+//    take turns with the tensor pipe: while one group works on its S, the MMAs of the other's tile run. Both tiles attend
+//    the same keys, or (dual units, whose query vectors fill one tile) the same vectors attend two ranges of keys. At
+//    d = 256 O fills half of the TMEM, so there is one M tile, S is double-buffered, and the groups share each row, half
+//    of the columns each; the two threads of a row swap their maxima through shared memory.
+//  * warp 8 fills the ring of K and V with TMA: slots of a whole tile, or at d = 256 half of one (128 columns of K, half
+//    of V's keys); and the unit's Q tiles.
+//  * warp 9 issues the MMAs: QK^T (both operands from shared memory) and PV (P from TMEM, N = d), in an order in which the
+//    group whose P is awaited is never the one whose S was asked for last. Waiting for P(j) of a tile is all that orders
+//    PV(j), QK(j + 1) of the same tile follows it in the pipe and may overwrite P(j).
+//  * E4M3 pools: warp 8 copies the codes of a tile as they are stored, and warps 10 and 11 convert them to f16 (exactly)
+//    into the ring. Queries enter as f16 too, times a power of two that brings the largest element of each vector into
+//    [2^14, 2^15): exact but for elements under 2^-29 of it. The softmax threads write them, each its own row, and take
+//    the factor back in their row's c. The running maximum sits 2^7 above P's largest weight then, so that small weights
+//    keep their bits in f16's range.
 // What bounds it: the tensor pipe. Per 128 keys and two tiles of d = 128 it is busy 2048 cycles; the softmax issues
-// about 900 instructions on each scheduler and takes 1024 or 2048 cycles of the special-function units.
+// about 900 instructions on each scheduler and takes 1024 cycles of the special-function units (4 a warp measured).
 #pragma once
 
 #include <atomic>
@@ -33,30 +40,37 @@ namespace nbx {
 namespace {
 
 constexpr int kAtM = 128;         // query vectors of an M tile = TMEM lanes
-constexpr int kAtN = 128;         // keys of a tile
+constexpr int kAtBuf = 128;       // TMEM columns of an S/P buffer
 constexpr int kAtThreads = 384;
-// Registers a thread: of the 168 each is launched with (65536 over three warps a scheduler), the loader's and the MMA
-// warp's group gives what a softmax thread needs to hold its 128 scores: 2 * 208 + 88 = 3 * 168.
+// Registers a thread: of the 168 each is launched with (65536 over three warps a scheduler), the group of the loader and
+// the MMA warp gives what a softmax thread needs to hold its 128 scores: 2 * 208 + 88 = 3 * 168.
 constexpr int kAtSoftmaxRegs = 208, kAtOtherRegs = 88;
 constexpr float kAtTau = 8.f;     // the running maximum moves when it would grow by more, log2 units
 
-template <int D>
+template <int D, int N, bool F8>
 struct AttnCfg {
   static constexpr int kTiles = D <= 128 ? 2 : 1;                // M tiles of a unit
   static constexpr int kParts = D <= 128 ? 1 : 2;                // ring slots of a K or V tile
   static constexpr int kAhead = D <= 128 ? 1 : 2;                // QK^T of tile j + kAhead follows PV of tile j
-  static constexpr int kCols = D <= 128 ? kAtN : kAtN / 2;       // columns of S a softmax thread takes
-  static constexpr int kSlotBytes = D == 64 ? 16384 : 32768;
-  static constexpr int kSlots = D == 64 ? 8 : 5;
-  static constexpr int kAtom = kAtM * 128;                       // 128 rows of 128 bytes
-  static constexpr int kQTile = D / 64 * kAtom;
+  static constexpr int kCols = D <= 128 ? N : N / 2;             // columns of S a softmax thread takes
+  static constexpr int kAtoms = D / 64;                          // 64-column atoms of a row
+  static constexpr int kSlotBytes = N * D * 2 / kParts;
+  static constexpr int kQAtom = kAtM * 128;                      // 128 rows of 128 bytes
+  static constexpr int kQTile = kAtoms * kQAtom;
+  static constexpr int kRawBytes = F8 ? N * D : 0;               // a tile of codes
+  static constexpr int kRaws = F8 ? 2 : 0;
+  static constexpr int kRoom = 224 * 1024 - kTiles * kQTile - kRaws * kRawBytes;
+  static constexpr int kMost = kTiles == 1 || F8 ? 6 : 8;        // (what the barrier area holds)
+  static constexpr int kSlots = kRoom / kSlotBytes < kMost ? kRoom / kSlotBytes : kMost;
   static constexpr int kRingOff = kTiles * kQTile;
-  static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kRawOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
   static constexpr int kXOff = kBarOff + 256;
-  static constexpr int kSmem = kXOff + (D == 256 ? 2 * 256 * 4 : 0) + 768;   // slack: 256-byte alignment to 1024
-  static constexpr uint32_t kOCol = 256;                         // S (and P) in columns [0, 256), O from there
+  static constexpr int kSmem = kXOff + (kTiles == 1 ? 2 * 256 * 4 : 0) + 768;   // slack: 256-byte alignment to 1024
+  static constexpr uint32_t kOCol = 2 * kAtBuf;                  // S (and P) in columns [0, 256), O from there
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert((2 * kSlots + 14) * 8 <= 256, "barrier area");
+  static_assert(kSlots >= 3, "ring");
+  static_assert((2 * kSlots + 2 * kRaws + 12) * 8 <= 256, "barrier area");
 };
 
 // One work unit.
@@ -65,9 +79,11 @@ struct AttnUnit {
   int toks;       // tokens of the unit, of both tiles
   int head, kvh;  // first query head, KV head
   int pos;        // causal: position of the first token in its sequence
-  int kv;         // causal: first key's row; paged: first position
-  int end;        // paged: one past the last position
-  int b, slot;    // paged: row of the block table, slot of the partials
+  int b;          // paged: row of the block table
+  bool dual;      // the two tiles are the same query vectors, over keys of their own
+  int kv[2];      // causal: first key's row; paged: first position
+  int end[2];     // paged: one past the last position
+  int slot[2];    // paged: slot of the partials
   int n[2];       // key tiles of each M tile
 };
 
@@ -123,17 +139,54 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 f16x2_floats(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+// Four E4M3 codes to two f16 pairs, exactly (the low two codes in lo).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// Calls f(is_v, t, j) for the K and V tiles of a unit in the order in which the MMA warp consumes them (t: the M tile that
+// they are for, 0 where both read them). f returns false to give up.
+template <class C, class F>
+__device__ __forceinline__ bool at_each_tile(const AttnUnit& u, F f) {
+  if (C::kTiles == 2 && u.dual) {
+    for (int t = 0; t < 2; ++t)
+      if (u.n[t] > 0 && !f(false, t, 0)) return false;
+    const int n = max(u.n[0], u.n[1]);
+    for (int j = 0; j < n; ++j)
+      for (int t = 0; t < 2; ++t) {
+        if (j < u.n[t] && !f(true, t, j)) return false;
+        if (j + 1 < u.n[t] && !f(false, t, j + 1)) return false;
+      }
+    return true;
+  }
+  const int n = C::kTiles == 2 ? max(u.n[0], u.n[1]) : u.n[0];
+  for (int j = 0; j < C::kAhead && j < n; ++j)
+    if (!f(false, 0, j)) return false;
+  for (int j = 0; j < n; ++j) {
+    if (!f(true, 0, j)) return false;
+    if (j + C::kAhead < n && !f(false, 0, j + C::kAhead)) return false;
+  }
+  return true;
+}
 
 // What a work policy W provides (prompt.cu, shared.cu):
 //   typename W::Params with c (|scale| log2 e, or the least positive number for a scale of 0), negative and status;
-//   W::kPaged, W::kTerms; W(params, lane) (after the grid ahead is waited for), bool unit(round, AttnUnit&): warp-wide;
-//   toks_per_tile(), heads(); load_q / load_kv by the loader warp; store(...) by a softmax thread.
-template <class W, int D>
+//   W::kN, kTerms, kF8, kPaged, kWaitLate; W(params, lane), bool unit(round, AttnUnit&): warp-wide; toks_per_tile(),
+//   heads(); last_keys, last_key, bad_keys; load_q / load_kv by the loader warp (or q_row for the softmax threads);
+//   store(...) by a softmax thread.
+template <class C>
 struct AttnShared {
-  using C = AttnCfg<D>;
   char* q_s;
   char* ring;
-  uint64_t* full;      // [kSlots] a ring slot's copies have landed
+  char* raw;
+  uint64_t* full;      // [kSlots] a ring slot holds its part of a tile
   uint64_t* empty;     // [kSlots] its MMAs are done
   uint64_t* q_full;
   uint64_t* q_empty;   // every QK^T of the unit is done
@@ -141,21 +194,23 @@ struct AttnShared {
   uint64_t* p_full;    // [2] P over it
   uint64_t* pv_done;   // [2] the PV from that buffer is done: O holds it
   uint64_t* o_free;    // [2] the epilogue has read O of M tile t
-  uint64_t* x_bar;     // [4] d = 256: the two warps of 32 rows have left their numbers
   uint64_t* done;
+  uint64_t* raw_full;  // [kRaws] a tile's codes have landed
+  uint64_t* raw_empty; // [kRaws] and are converted
+  uint64_t* x_bar;     // [4] d = 256: the two warps of 32 rows have left their numbers
   volatile int* abort_flag;
   uint32_t* tmem_slot;
   float* xbuf;         // [2][256]
 };
 
 // ---------------------------------------------------------------- the MMA warp
-template <class W, int D>
-__device__ __forceinline__ bool attn_mma(W& w, const AttnShared<W, D>& sh, uint32_t tmem) {
-  using C = AttnCfg<D>;
-  constexpr int T = C::kTiles, NS = C::kSlots;
-  constexpr uint32_t kIdescO = mma_idesc(kAtM, D, true);
+template <class W, class C, int D>
+__device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t tmem) {
+  constexpr int T = C::kTiles, NS = C::kSlots, N = W::kN;
+  constexpr int kAtomBytes = N * 128 / (C::kParts);   // of V: N (or N / 2) rows of 128 bytes
+  constexpr uint32_t kIdescO = mma_idesc(kAtM, D, true, W::kF8);
   // a negative scale: S of -Q (the descriptor's bit 13 negates A), and its magnitude
-  const uint32_t idesc_s = mma_idesc(kAtM, kAtN, false) | (w.p.negative ? 1u << 13 : 0u);
+  const uint32_t idesc_s = mma_idesc(kAtM, N, false, W::kF8) | (w.p.negative ? 1u << 13 : 0u);
   const int lane = threadIdx.x & 31;
   volatile int* ab = sh.abort_flag;
   const uint32_t q_addr = smem_u32(sh.q_s), ring = smem_u32(sh.ring);
@@ -172,9 +227,9 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<W, D>& sh, uint3
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const int a = kk >> 2, sub = kk & 3;   // 64-column atom, 16-column step in it
-        const uint64_t ad = smem_desc(q_addr + t * C::kQTile + a * C::kAtom + sub * 32, 16, 1024);
-        const uint32_t kb = C::kParts == 1 ? slot_addr(at) + a * C::kAtom : slot_addr(at + (a >> 1)) + (a & 1) * C::kAtom;
-        tc_mma_ss(tmem + buf * kAtN, ad, smem_desc(kb + sub * 32, 16, 1024), idesc_s, kk > 0);
+        const uint64_t ad = smem_desc(q_addr + t * C::kQTile + a * C::kQAtom + sub * 32, 16, 1024);
+        const uint32_t kb = C::kParts == 1 ? slot_addr(at) + a * (N * 128) : slot_addr(at + (a >> 1)) + (a & 1) * (N * 128);
+        tc_mma_ss(tmem + buf * kAtBuf, ad, smem_desc(kb + sub * 32, 16, 1024), idesc_s, kk > 0);
       }
       tc_commit(&sh.s_full[buf]);
     }
@@ -186,15 +241,16 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<W, D>& sh, uint3
   // O(tile t) += P(buffer) V, `keys` of the tile's keys, V in ring slots at, ...
   auto pv = [&](int t, uint32_t buf, uint32_t at, int keys, bool first) {
     if (lane == 0) {
+      constexpr int kSteps = N / 16, kPartSteps = kSteps / C::kParts;
       const int steps = (keys + 15) >> 4;
 #pragma unroll
       for (int term = 0; term < W::kTerms; ++term)
 #pragma unroll
-        for (int kk = 0; kk < kAtN / 16; ++kk)
+        for (int kk = 0; kk < kSteps; ++kk)
           if (kk < steps) {
-            const uint32_t vb = C::kParts == 1 ? slot_addr(at) + kk * 2048 : slot_addr(at + (kk >> 2)) + (kk & 3) * 2048;
-            const uint64_t bd = smem_desc(vb, C::kParts == 1 ? C::kAtom : C::kAtom / 2, 1024);
-            tc_mma_ts(tmem + C::kOCol + t * D, tmem + buf * kAtN + term * (kAtN / 2) + kk * 8, bd, kIdescO,
+            const uint32_t vb = slot_addr(at + kk / kPartSteps) + (kk % kPartSteps) * 2048;
+            const uint64_t bd = smem_desc(vb, kAtomBytes, 1024);
+            tc_mma_ts(tmem + C::kOCol + t * D, tmem + buf * kAtBuf + term * (N / 2) + kk * 8, bd, kIdescO,
                       !(first && term == 0 && kk == 0));
           }
       tc_commit(&sh.pv_done[buf]);
@@ -204,94 +260,125 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<W, D>& sh, uint3
   auto clear_tail = [&](uint32_t at, int keys) {
     if ((keys & 15) == 0) return;
     const int to = (keys + 15) & ~15;
-    for (int row = keys; row < to; ++row) {
-      // 16-byte pieces of the row: D / 64 atoms of 8
-      for (int i = lane; i < D / 8; i += 32) {
-        const uint32_t off = C::kParts == 1 ? slot_addr(at) + (i >> 3) * C::kAtom + row * 128
-                                            : slot_addr(at + (row >> 6)) + (i >> 3) * (C::kAtom / 2) + (row & 63) * 128;
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(off + (i & 7) * 16), "r"(0) : "memory");
+    constexpr int kRows = N / C::kParts;
+    for (int row = keys; row < to; ++row)
+      for (int i = lane; i < D / 8; i += 32) {   // 16-byte pieces of the row: D / 64 atoms of 8
+        const uint32_t off = slot_addr(at + row / kRows) + (i >> 3) * kAtomBytes + (row % kRows) * 128 + (i & 7) * 16;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(off), "r"(0) : "memory");
       }
-    }
     fence_proxy_async();
     __syncwarp();
+  };
+  // P of tile t (buffer buf) has been written, and O is free: PV may be issued
+  auto ready = [&](int t, uint32_t buf, uint32_t parity, bool first) -> bool {
+    if (first && units[t] > 0 && !at_warp_wait(&sh.o_free[t], (units[t] - 1) & 1u, ab)) return false;
+    if (!at_warp_wait(&sh.p_full[buf], parity, ab)) return false;
+    tc_fence_after();
+    return true;
   };
   for (uint32_t k = 0; w.unit(k, u); ++k) {
     if (!at_warp_wait(sh.q_full, k & 1u, ab)) return false;
     const int n = T == 2 ? max(u.n[0], u.n[1]) : u.n[0];
-    // the keys that the last tile holds (V rows behind them are not the sequence's)
-    const int last_keys = w.last_keys(u, n);
-    auto issue_qk = [&](int j) -> bool {   // of key tile j, T == 1
-      const uint32_t at = r;
-      for (int i = 0; i < C::kParts; ++i)
-        if (!slot_wait(at + i)) return false;
-      r += C::kParts;
-      tc_fence_after();
-      qk(0, xs & 1u, at);
-      ++xs;
-      release(at);
-      if (j == n - 1 && lane == 0) tc_commit(sh.q_empty);
-      return true;
-    };
     if constexpr (T == 2) {
-      if (!slot_wait(r)) return false;
-      tc_fence_after();
+      if (u.dual) {
+        auto next_k = [&](int t) -> bool {
+          if (!slot_wait(r)) return false;
+          tc_fence_after();
+          qk(t, t, r);
+          release(r);
+          ++r;
+          return true;
+        };
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (u.n[t] > 0) qk(t, t, r);
-      release(r);
-      ++r;
-      if (n == 1 && lane == 0) tc_commit(sh.q_empty);
-      for (int j = 0; j < n; ++j) {
-        const uint32_t rv = r++;
-        const bool more = j + 1 < n;
-        const uint32_t rk = r;
-        if (more) ++r;
-        const int keys = more ? kAtN : last_keys;
-        bool have_v = false, have_k = false;
+        for (int t = 0; t < 2; ++t)
+          if (u.n[t] > 0 && !next_k(t)) return false;
+        if (n == 1 && lane == 0) tc_commit(sh.q_empty);
+        for (int j = 0; j < n; ++j) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (j < u.n[t]) {
-            if (!have_v) {
-              if (!slot_wait(rv)) return false;
-              clear_tail(rv, keys);
-              have_v = true;
+          for (int t = 0; t < 2; ++t) {
+            if (j < u.n[t]) {
+              if (!slot_wait(r)) return false;
+              const int keys = j + 1 < u.n[t] ? N : w.last_keys(u, t);
+              clear_tail(r, keys);
+              if (!ready(t, t, np[t] & 1u, j == 0)) return false;
+              ++np[t];
+              pv(t, t, r, keys, j == 0);
+              release(r);
+              ++r;
             }
-            if (j == 0 && units[t] > 0 && !at_warp_wait(&sh.o_free[t], (units[t] - 1) & 1u, ab)) return false;
-            if (!at_warp_wait(&sh.p_full[t], np[t] & 1u, ab)) return false;
-            ++np[t];
-            tc_fence_after();
-            pv(t, t, rv, keys, j == 0);
+            if (j + 1 < u.n[t] && !next_k(t)) return false;
           }
-          if (j + 1 < u.n[t]) {
-            if (!have_k) {
-              if (!slot_wait(rk)) return false;
-              tc_fence_after();
-              have_k = true;
-            }
-            qk(t, t, rk);
-          }
-        }
-        release(rv);
-        if (more) {
-          release(rk);
           if (j + 2 == n && lane == 0) tc_commit(sh.q_empty);
+        }
+      } else {
+        if (!slot_wait(r)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (u.n[t] > 0) qk(t, t, r);
+        release(r);
+        ++r;
+        if (n == 1 && lane == 0) tc_commit(sh.q_empty);
+        for (int j = 0; j < n; ++j) {
+          const uint32_t rv = r++;
+          const bool more = j + 1 < n;
+          const uint32_t rk = r;
+          if (more) ++r;
+          const int keys = more ? N : w.last_keys(u, 0);
+          bool have_v = false, have_k = false;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j < u.n[t]) {
+              if (!have_v) {
+                if (!slot_wait(rv)) return false;
+                clear_tail(rv, keys);
+                have_v = true;
+              }
+              if (!ready(t, t, np[t] & 1u, j == 0)) return false;
+              ++np[t];
+              pv(t, t, rv, keys, j == 0);
+            }
+            if (j + 1 < u.n[t]) {
+              if (!have_k) {
+                if (!slot_wait(rk)) return false;
+                tc_fence_after();
+                have_k = true;
+              }
+              qk(t, t, rk);
+            }
+          }
+          release(rv);
+          if (more) {
+            release(rk);
+            if (j + 2 == n && lane == 0) tc_commit(sh.q_empty);
+          }
         }
       }
     } else {
+      auto issue_qk = [&](int j) -> bool {
+        const uint32_t at = r;
+        for (int i = 0; i < C::kParts; ++i)
+          if (!slot_wait(at + i)) return false;
+        r += C::kParts;
+        tc_fence_after();
+        qk(0, xs & 1u, at);
+        ++xs;
+        release(at);
+        if (j == n - 1 && lane == 0) tc_commit(sh.q_empty);
+        return true;
+      };
       for (int j = 0; j < C::kAhead && j < n; ++j)
         if (!issue_qk(j)) return false;
       for (int j = 0; j < n; ++j) {
         const uint32_t rv = r;
-        const int keys = j + 1 < n ? kAtN : last_keys;
+        const int keys = j + 1 < n ? N : w.last_keys(u, 0);
         for (int i = 0; i < C::kParts; ++i)
           if (!slot_wait(rv + i)) return false;
         r += C::kParts;
         clear_tail(rv, keys);
-        if (j == 0 && units[0] > 0 && !at_warp_wait(&sh.o_free[0], (units[0] - 1) & 1u, ab)) return false;
         const uint32_t buf = np[0] & 1u;
-        if (!at_warp_wait(&sh.p_full[buf], (np[0] >> 1) & 1u, ab)) return false;
+        if (!ready(0, buf, (np[0] >> 1) & 1u, j == 0)) return false;
         ++np[0];
-        tc_fence_after();
         pv(0, buf, rv, keys, j == 0);
         release(rv);
         if (j + C::kAhead < n && !issue_qk(j + C::kAhead)) return false;
@@ -303,12 +390,47 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<W, D>& sh, uint3
   return true;
 }
 
+// ---------------------------------------------------------------- queries of E4M3 pools
+// This thread's query vector (null: zeros) times 2^e as f16 into row `row` of a Q tile's swizzled atoms, elements
+// [d0, d0 + kCount) of it. Returns 2^-e.
+template <int D, int kCount>
+__device__ __forceinline__ float q_to_f16(const __nv_bfloat16* q, char* tile, int row, int d0) {
+  const uint4* src = reinterpret_cast<const uint4*>(q);
+  float amax = 0.f;
+  if (q != nullptr) {
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+      float2 x[4];
+      unpack16<BF16>(__ldg(src + i), x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) amax = max_nan(amax, max_nan(fabsf(x[e].x), fabsf(x[e].y)));
+    }
+  }
+  int e2 = 0;   // a NaN or an infinity in the vector: as it is
+  if (amax > 0.f && amax <= 3.402823466e38f)
+    e2 = min(120, max(-120, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)));
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
+#pragma unroll 4
+  for (int i = d0 / 8; i < (d0 + kCount) / 8; ++i) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (q != nullptr) {
+      float2 x[4];
+      unpack16<BF16>(__ldg(src + i), x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = f16x2_bits(x[e].x * up, x[e].y * up);
+    }
+    *reinterpret_cast<uint4*>(tile + (i >> 3) * (kAtM * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
+}
+
 // ---------------------------------------------------------------- a softmax warp
-template <class W, int D>
-__device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<W, D>& sh, uint32_t tmem) {
-  using C = AttnCfg<D>;
-  constexpr int T = C::kTiles, NC = C::kCols;
+template <class W, class C, int D>
+__device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint32_t tmem) {
+  constexpr int T = C::kTiles, NC = C::kCols, N = W::kN;
   constexpr int kOCols = T == 2 ? D : D / 2;   // columns of O that this thread rescales and stores
+  constexpr float kMid = W::kF8 ? 7.f : 0.f;   // log2 of the largest weight when m has moved
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp >> 2, quarter = warp & 3;
   const int row = quarter * 32 + lane;
@@ -318,7 +440,7 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<W, D>& sh, u
   const int c0 = T == 2 ? 0 : group * NC;      // first column of S
   const int tpt = w.toks_per_tile();
   const int tok = row / w.heads(), head = row - tok * w.heads();
-  const float c = w.p.c;
+  float c = w.p.c;
   volatile int* ab = sh.abort_flag;
   uint32_t x = 0;         // key tiles of this M tile so far
   uint32_t xphase = 0;
@@ -348,22 +470,34 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<W, D>& sh, u
   AttnUnit u;
   for (uint32_t k = 0; w.unit(k, u); ++k) {
     const int n = u.n[t];
-    if (n == 0) continue;
-    const int my_tok = t * tpt + tok;                       // of the unit
+    const int my_tok = (u.dual ? 0 : t * tpt) + tok;        // of the unit
     const bool row_ok = tok < tpt && my_tok < u.toks;
-    const int last_key = w.last_key(u, my_tok, row_ok);     // of the unit's keys, from 0
-    float m = -INFINITY, l = 0.f;
+    if constexpr (W::kF8) {
+      if (k > 0 && !at_warp_wait(sh.q_empty, (k - 1) & 1u, ab)) return false;
+      if (n > 0) {
+        const float down = q_to_f16<D, kOCols>(row_ok ? w.q_row(u, my_tok, head) : nullptr, sh.q_s + t * C::kQTile, row,
+                                               T == 2 ? 0 : group * kOCols);
+        c = fmaxf(w.p.c * down, 1.4012985e-45f);   // (0 x a masked score would be a NaN)
+        fence_proxy_async();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sh.q_full);
+    }
+    if (n == 0) continue;
+    const int last_key = w.last_key(u, t, my_tok, row_ok);  // of the unit's keys, from 0
+    float m = -INFINITY, l = 0.f;                           // weights are 2^(c s - m)
     for (int j = 0; j < n; ++j, ++x) {
       const uint32_t buf = T == 2 ? t : (x & 1u);
-      const uint32_t s_col = lane_base + buf * kAtN;
-      const uint32_t bad = w.bad_keys(u, j, c0);            // paged: 16-key pieces of this thread's columns without a page
+      const uint32_t s_col = lane_base + buf * kAtBuf;
+      uint32_t bad = 0;                                     // paged: 16-key pieces of this thread's columns without a page
+      if constexpr (W::kPaged) bad = w.bad_keys(u, t, j, c0);
       if (!at_warp_wait(&sh.s_full[buf], (T == 2 ? x : x >> 1) & 1u, ab)) return false;
       tc_fence_after();
       uint32_t s[NC];
 #pragma unroll
       for (int i = 0; i < NC; i += 32) tmem_ld32(s_col + c0 + i, s + i);
       tmem_wait_ld();
-      const int limit = last_key - (j * kAtN + c0);          // this thread's columns up to here are seen
+      const int limit = last_key - (j * N + c0);             // this thread's columns up to here are seen
       if (!__all_sync(0xffffffffu, limit >= NC - 1)) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) s[i] = i <= limit ? s[i] : 0xff800000u;
@@ -384,29 +518,38 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<W, D>& sh, u
         z = fmaxf(z, other);
       }
       // (a NaN score leaves m alone: its own weight is a NaN, and the row's sum)
-      const bool up = z > m + kAtTau;
-      const float f = up ? fast_exp2(m - z) : 1.f;
-      if (up) m = z;
+      const bool up = z > m + (kMid + kAtTau);
+      const float f = up ? fast_exp2(m - (z - kMid)) : 1.f;
+      if (up) m = z - kMid;
       const float neg = m == -INFINITY ? 0.f : -m;
       const f32x2 c2 = pack2(c, c), neg2 = pack2(neg, neg);
       f32x2 sum[2] = {pack2(l * f, 0.f), pack2(0.f, 0.f)};
+      constexpr int kChunk = NC < 64 ? NC : 64;   // columns of S whose terms are stored at once
 #pragma unroll
-      for (int h = 0; h < NC; h += 64) {
-        uint32_t hi[32];
-        uint32_t lo[W::kTerms == 2 ? 32 : 1];
+      for (int h = 0; h < NC; h += kChunk) {
+        uint32_t term[W::kTerms][kChunk / 2];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < kChunk / 2; ++i) {
           const float2 e = unpack2(fma2(pack2(__uint_as_float(s[h + 2 * i]), __uint_as_float(s[h + 2 * i + 1])), c2, neg2));
-          const float a = fast_exp2(e.x), b = fast_exp2(e.y);
+          float a = fast_exp2(e.x), b = fast_exp2(e.y);
           sum[i & 1] = add2(sum[i & 1], pack2(a, b));
-          hi[i] = bf16x2_bits(a, b);
-          if constexpr (W::kTerms == 2) {
-            const float2 g = bf16x2_to_float2(hi[i]);
-            lo[i] = bf16x2_bits(a - g.x, b - g.y);
+#pragma unroll
+          for (int y = 0; y < W::kTerms; ++y) {
+            const uint32_t bits = W::kF8 ? f16x2_bits(a, b) : bf16x2_bits(a, b);
+            term[y][i] = bits;
+            if (y + 1 < W::kTerms) {
+              const float2 g = W::kF8 ? f16x2_floats(bits) : bf16x2_to_float2(bits);
+              a -= g.x;
+              b -= g.y;
+            }
           }
         }
-        tmem_st32(s_col + (c0 + h) / 2, hi);
-        if constexpr (W::kTerms == 2) tmem_st32(s_col + kAtN / 2 + (c0 + h) / 2, lo);
+#pragma unroll
+        for (int y = 0; y < W::kTerms; ++y) {
+          const uint32_t at = s_col + y * (N / 2) + (c0 + h) / 2;
+          if constexpr (kChunk == 64) tmem_st32(at, term[y]);
+          else tmem_st16(at, term[y]);
+        }
       }
       const float2 s0 = unpack2(sum[0]), s1 = unpack2(sum[1]);
       l = (s0.x + s0.y) + (s1.x + s1.y);
@@ -439,41 +582,105 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<W, D>& sh, u
       l = group == 0 ? l + other : other + l;
     }
     if (!pv_wait()) return false;
-    w.template store<kOCols>(u, o_base, T == 2 ? 0 : group * kOCols, my_tok, head, row_ok, m, l, &sh.o_free[t]);
+    w.template store<kOCols>(u, t, o_base, T == 2 ? 0 : group * kOCols, my_tok, head, row_ok, m, l, &sh.o_free[t]);
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------- a converting warp (E4M3 pools)
+// Codes of K and V tiles, [keys][D] as they are stored, to f16 in the ring's swizzled atoms. Warp `half` takes every other
+// group of 8 rows of a slot. Lane (rr, i) takes 16 codes of row rr, of atom (rr & 1) ^ s in turn s: the eight lanes that
+// access shared memory at a time then read 128 bytes of distinct banks, and write 16-byte chunks of distinct ones.
+template <class W, class C, int D>
+__device__ __forceinline__ bool attn_convert(W& w, const AttnShared<C>& sh, int half) {
+  constexpr int NS = C::kSlots, N = W::kN;
+  const int lane = threadIdx.x & 31;
+  const int rr = lane >> 2, i = lane & 3;
+  uint32_t r = 0, x = 0;   // ring slots, tiles
+  AttnUnit u;
+  for (uint32_t k = 0; w.unit(k, u); ++k) {
+    const bool ok = at_each_tile<C>(u, [&](bool is_v, int, int) -> bool {
+      if (!at_warp_wait(&sh.raw_full[x % C::kRaws], (x / C::kRaws) & 1u, sh.abort_flag)) return false;
+      const char* raw = sh.raw + (x % C::kRaws) * C::kRawBytes;
+      for (int part = 0; part < C::kParts; ++part, ++r) {
+        if (r >= NS && !at_warp_wait(&sh.empty[r % NS], (r / NS - 1) & 1u, sh.abort_flag)) return false;
+        char* dst = sh.ring + (r % NS) * C::kSlotBytes;
+        // the part's rows and atoms: at d = 256 two atoms of every row of K, half of V's rows
+        const int rows = C::kParts == 2 && is_v ? N / 2 : N;
+        constexpr int kAtomsK = C::kParts == 2 ? 2 : C::kAtoms;
+        const int atoms = C::kParts == 2 && is_v ? C::kAtoms : kAtomsK;
+        const char* src = raw + (C::kParts == 2 && part ? (is_v ? N / 2 * D : 128) : 0);
+#pragma unroll 2
+        for (int r0 = half * 8; r0 < rows; r0 += 16) {
+          const int row = r0 + rr;
+#pragma unroll
+          for (int a0 = 0; a0 < C::kAtoms; a0 += 2) {
+            if (a0 >= atoms) break;
+#pragma unroll
+            for (int s = 0; s < (C::kAtoms > 1 ? 2 : 1); ++s) {
+              const int atom = C::kAtoms > 1 ? a0 + ((rr & 1) ^ s) : 0;
+              const uint4 v = *reinterpret_cast<const uint4*>(src + row * D + atom * 64 + i * 16);
+              uint4 lo, hi;
+              e4m3x4_to_f16x4(v.x, lo.x, lo.y);
+              e4m3x4_to_f16x4(v.y, lo.z, lo.w);
+              e4m3x4_to_f16x4(v.z, hi.x, hi.y);
+              e4m3x4_to_f16x4(v.w, hi.z, hi.w);
+              char* to = dst + atom * (rows * 128) + row * 128;
+              *reinterpret_cast<uint4*>(to + (((2 * i) ^ (row & 7)) << 4)) = lo;
+              *reinterpret_cast<uint4*>(to + (((2 * i + 1) ^ (row & 7)) << 4)) = hi;
+            }
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[r % NS]);
+      }
+      if (lane == 0) mbar_arrive(&sh.raw_empty[x % C::kRaws]);
+      ++x;
+      return true;
+    });
+    if (!ok) return false;
   }
   return true;
 }
 
 template <class W, int D>
 __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_constant__ typename W::Params params) {
-  using C = AttnCfg<D>;
+  using C = AttnCfg<D, W::kN, W::kF8>;
   constexpr int NS = C::kSlots;
   extern __shared__ __align__(256) char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  AttnShared<W, D> sh;
+  AttnShared<C> sh;
   sh.q_s = smem;
   sh.ring = smem + C::kRingOff;
+  sh.raw = smem + C::kRawOff;
   sh.full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
   sh.empty = sh.full + NS;
-  sh.q_full = sh.empty + NS;
+  sh.raw_full = sh.empty + NS;
+  sh.raw_empty = sh.raw_full + C::kRaws;
+  sh.q_full = sh.raw_empty + C::kRaws;
   sh.q_empty = sh.q_full + 1;
   sh.s_full = sh.q_full + 2;
   sh.p_full = sh.q_full + 4;
   sh.pv_done = sh.q_full + 6;
   sh.o_free = sh.q_full + 8;
   sh.done = sh.q_full + 10;
-  sh.x_bar = nullptr;
   sh.abort_flag = reinterpret_cast<int*>(sh.q_full + 11);
   sh.tmem_slot = reinterpret_cast<uint32_t*>(sh.q_full + 11) + 1;
+  sh.x_bar = reinterpret_cast<uint64_t*>(smem + C::kXOff) - 4;   // d = 256 (whose ring is short): behind them
   sh.xbuf = reinterpret_cast<float*>(smem + C::kXOff);
-  if constexpr (C::kTiles == 1) sh.x_bar = sh.q_full + 12;
+  static_assert(C::kTiles == 2 || (2 * NS + 2 * C::kRaws + 16) * 8 <= 256, "barrier area");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], W::kF8 ? 2 : 1);
       mbar_init(&sh.empty[i], 1);
     }
-    mbar_init(sh.q_full, 1);
+    for (int i = 0; i < C::kRaws; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], 2);
+    }
+    mbar_init(sh.q_full, W::kF8 ? 8 : 1);
     mbar_init(sh.q_empty, 1);
     constexpr int kRowWarps = C::kTiles == 2 ? 4 : 8;
     for (int i = 0; i < 2; ++i) {
@@ -502,52 +709,56 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   pdl_launch_dependents();
   bool ok = true;
   if (warp < 8) {
-    W w(params, lane);
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtSoftmaxRegs));
-    ok = attn_softmax<W, D>(w, sh, tmem);
+    W w(params, lane);
+    ok = attn_softmax<W, C, D>(w, sh, tmem);
   } else {
-   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
-   if (warp == 8) {
-    // ---- the loader: Q of each unit, then K and V in the order in which the MMA warp consumes them
-    W w(params, lane);
-    uint32_t r = 0, q_units = 0;
-    AttnUnit u;
-    auto load = [&](bool is_v, int j) -> bool {
-      for (int part = 0; part < C::kParts; ++part, ++r) {
-        if (r >= NS && !at_warp_wait(&sh.empty[r % NS], (r / NS - 1) & 1u, sh.abort_flag)) return false;
-        w.template load_kv<D>(u, is_v, j, part, sh.ring + (r % NS) * C::kSlotBytes, &sh.full[r % NS]);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
+    if (warp == 8) {
+      // ---- the loader: Q of each unit, then K and V in the order in which the MMA warp consumes them
+      W w(params, lane);
+      constexpr int kDepth = W::kF8 ? C::kRaws : NS, kPieces = W::kF8 ? 1 : C::kParts;
+      constexpr int kBytes = W::kF8 ? C::kRawBytes : C::kSlotBytes;
+      uint64_t* const full = W::kF8 ? sh.raw_full : sh.full;
+      uint64_t* const empty = W::kF8 ? sh.raw_empty : sh.empty;
+      char* const ring = W::kF8 ? sh.raw : sh.ring;
+      uint32_t r = 0, q_units = 0;
+      AttnUnit u;
+      for (uint32_t k = 0; ok && w.unit(k, u); ++k) {
+        if constexpr (!W::kF8) {   // (the softmax threads write an E4M3 pool's Q)
+          if (k > 0) ok = at_warp_wait(sh.q_empty, (k - 1) & 1u, sh.abort_flag);
+          if (!ok) break;
+          w.template load_q<C>(u, sh.q_s, sh.q_full);
+          ++q_units;
+        }
+        ok = at_each_tile<C>(u, [&](bool is_v, int t, int j) -> bool {
+          for (int part = 0; part < kPieces; ++part, ++r) {
+            if (r >= kDepth && !at_warp_wait(&empty[r % kDepth], (r / kDepth - 1) & 1u, sh.abort_flag)) return false;
+            w.template load_kv<C>(u, is_v, t, j, part, ring + (r % kDepth) * kBytes, &full[r % kDepth]);
+          }
+          return true;
+        });
       }
-      return true;
-    };
-    for (uint32_t k = 0; ok && w.unit(k, u); ++k) {
-      if (k > 0) ok = at_warp_wait(sh.q_empty, (k - 1) & 1u, sh.abort_flag);
-      if (!ok) break;
-      w.template load_q<D>(u, sh.q_s, sh.q_full);
-      ++q_units;
-      const int n = C::kTiles == 2 ? max(u.n[0], u.n[1]) : u.n[0];
-      for (int j = 0; j < C::kAhead && j < n && ok; ++j) ok = load(false, j);
-      for (int j = 0; j < n && ok; ++j) {
-        ok = load(true, j);
-        if (ok && j + C::kAhead < n) ok = load(false, j + C::kAhead);
+      if (!ok) *sh.abort_flag = 1;
+      // the copies issued last have landed before the CTA can exit
+      if (lane == 0) {
+        for (uint32_t i = r > kDepth ? r - kDepth : 0; i < r; ++i) mbar_wait(&full[i % kDepth], (i / kDepth) & 1u, 100000000ull);
+        if (q_units > 0) mbar_wait(sh.q_full, (q_units - 1) & 1u, 100000000ull);
       }
+      __syncwarp();
+    } else if (warp == 9) {
+      W w(params, lane);
+      ok = attn_mma<W, C, D>(w, sh, tmem);
+      if (!ok) *sh.abort_flag = 1;
+      if (lane == 0) {   // every MMA of this CTA has completed before the TMEM is released
+        tc_commit(sh.done);
+        mbar_wait(sh.done, 0, 100000000ull);
+      }
+      __syncwarp();
+    } else if constexpr (W::kF8) {
+      W w(params, lane);
+      ok = attn_convert<W, C, D>(w, sh, warp - 10);
     }
-    if (!ok) *sh.abort_flag = 1;
-    // the copies issued last have landed before the CTA can exit
-    if (lane == 0) {
-      for (uint32_t i = r > NS ? r - NS : 0; i < r; ++i) mbar_wait(&sh.full[i % NS], (i / NS) & 1u, 100000000ull);
-      if (q_units > 0) mbar_wait(sh.q_full, (q_units - 1) & 1u, 100000000ull);
-    }
-    __syncwarp();
-   } else if (warp == 9) {
-    W w(params, lane);
-    ok = attn_mma<W, D>(w, sh, tmem);
-    if (!ok) *sh.abort_flag = 1;
-    if (lane == 0) {   // every MMA of this CTA has completed before the TMEM is released
-      tc_commit(sh.done);
-      mbar_wait(sh.done, 0, 100000000ull);
-    }
-    __syncwarp();
-   }
   }
   if (!ok) {
     *sh.abort_flag = 1;
@@ -590,11 +801,11 @@ cudaError_t launch_attn_tiles(const typename W::Params& p, unsigned grid, cudaSt
   const uint64_t bit = 1ull << (device_info().device & 63);
   if ((configured.load() & bit) == 0) {
     const cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<W, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               AttnCfg<D>::kSmem);
+                                               (AttnCfg<D, W::kN, W::kF8>::kSmem));
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  return launch_pdl(attn_tiles_kernel<W, D>, grid, kAtThreads, AttnCfg<D>::kSmem, stream, p);
+  return launch_pdl(attn_tiles_kernel<W, D>, grid, kAtThreads, (AttnCfg<D, W::kN, W::kF8>::kSmem), stream, p);
 }
 
 }  // namespace

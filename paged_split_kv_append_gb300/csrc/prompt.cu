@@ -33,7 +33,9 @@ struct PromptTilesParams {
 template <int D>
 struct PromptWork {
   using Params = PromptTilesParams;
-  using C = AttnCfg<D>;
+  using C = AttnCfg<D, 128, false>;
+  static constexpr int kN = 128;   // keys of a tile
+  static constexpr bool kF8 = false;
   static constexpr bool kPaged = false;
   static constexpr bool kWaitLate = false;
   static constexpr int kTerms = 1;
@@ -104,7 +106,8 @@ struct PromptWork {
     }
     const int s = __ldg(p.a.seq_start + b), len = __ldg(p.a.seq_start + b + 1) - s;
     u.pos = lo * tpb;
-    u.kv = s;
+    u.kv[0] = u.kv[1] = s;
+    u.dual = false;
     u.tok = s + u.pos;
     u.toks = min(tpb, len - u.pos);
     u.head = set * p.heads;
@@ -113,15 +116,16 @@ struct PromptWork {
 #pragma unroll
     for (int t = 0; t < C::kTiles; ++t) {
       const int last = min(u.toks, (t + 1) * tpt) - 1;   // last token of the tile, within the unit
-      u.n[t] = last >= t * tpt ? (u.pos + last) / kAtN + 1 : 0;
+      u.n[t] = last >= t * tpt ? (u.pos + last) / kN + 1 : 0;
     }
     return true;
   }
-  __device__ __forceinline__ int last_keys(const AttnUnit& u, int n) const { return u.pos + u.toks - (n - 1) * kAtN; }
-  __device__ __forceinline__ int last_key(const AttnUnit& u, int tok, bool ok) const { return ok ? u.pos + tok : 1 << 30; }
-  __device__ __forceinline__ uint32_t bad_keys(const AttnUnit&, int, int) const { return 0; }
+  __device__ __forceinline__ int last_keys(const AttnUnit& u, int) const {
+    return u.pos + u.toks - (max(u.n[0], u.n[1]) - 1) * kN;
+  }
+  __device__ __forceinline__ int last_key(const AttnUnit& u, int, int tok, bool ok) const { return ok ? u.pos + tok : 1 << 30; }
 
-  template <int>
+  template <class>
   __device__ __forceinline__ void load_q(const AttnUnit& u, char* q_s, uint64_t* bar) const {
     if ((threadIdx.x & 31) != 0) return;
     mbar_arrive_expect_tx(bar, C::kQTile * (C::kTiles == 2 && u.n[1] > 0 ? 2 : 1));
@@ -130,18 +134,18 @@ struct PromptWork {
       if (u.n[t] > 0)
 #pragma unroll
         for (int a = 0; a < D / 64; ++a)
-          tma_load_3d(q_s + t * C::kQTile + a * C::kAtom, &p.q, a * 64, u.head, u.tok + t * tpt, bar);
+          tma_load_3d(q_s + t * C::kQTile + a * C::kQAtom, &p.q, a * 64, u.head, u.tok + t * tpt, bar);
   }
-  template <int>
-  __device__ __forceinline__ void load_kv(const AttnUnit& u, bool is_v, int j, int part, char* dst, uint64_t* bar) const {
+  template <class>
+  __device__ __forceinline__ void load_kv(const AttnUnit& u, bool is_v, int, int j, int part, char* dst, uint64_t* bar) const {
     if ((threadIdx.x & 31) != 0) return;
     mbar_arrive_expect_tx(bar, C::kSlotBytes);
-    const int row = u.kv + j * kAtN;
-    if (is_v) tma_load_4d(dst, &p.v, 0, row + part * (kAtN / 2), 0, u.kvh, bar);
+    const int row = u.kv[0] + j * kN;
+    if (is_v) tma_load_4d(dst, &p.v, 0, row + part * (kN / 2), 0, u.kvh, bar);
     else tma_load_4d(dst, &p.k, 0, row, part * 2, u.kvh, bar);
   }
   template <int kCols>
-  __device__ __forceinline__ void store(const AttnUnit& u, uint32_t o_base, int col0, int tok, int head, bool ok, float m,
+  __device__ __forceinline__ void store(const AttnUnit& u, int, uint32_t o_base, int col0, int tok, int head, bool ok, float m,
                                         float l, uint64_t* o_free) const {
     const int lane = threadIdx.x & 31;
     const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -182,8 +186,8 @@ struct PromptWork {
       const int64_t rr = __shfl_sync(0xffffffffu, row, src);
       prompt_row<D>(static_cast<const __nv_bfloat16*>(p.a.q) + (static_cast<int64_t>(u.tok) + rt) * p.a.q_stride +
                         (rr % p.a.h_q) * D,
-                    static_cast<const __nv_bfloat16*>(p.a.k) + u.kv * p.a.k_stride + static_cast<int64_t>(u.kvh) * D,
-                    static_cast<const __nv_bfloat16*>(p.a.v) + u.kv * p.a.v_stride + static_cast<int64_t>(u.kvh) * D,
+                    static_cast<const __nv_bfloat16*>(p.a.k) + u.kv[0] * p.a.k_stride + static_cast<int64_t>(u.kvh) * D,
+                    static_cast<const __nv_bfloat16*>(p.a.v) + u.kv[0] * p.a.v_stride + static_cast<int64_t>(u.kvh) * D,
                     p.a.k_stride, p.a.v_stride, u.pos + rt + 1, p.a.scale_log2, out + rr * D, col0, col0 + kCols);
     }
   }
@@ -199,8 +203,9 @@ bool encode_maps(PromptTilesParams* m) {
   const cuuint64_t dims[4] = {64, n, d / 64, static_cast<cuuint64_t>(a.h_kv)};
   const cuuint64_t k_str[3] = {static_cast<cuuint64_t>(a.k_stride) * 2, 128, d * 2};
   const cuuint64_t v_str[3] = {static_cast<cuuint64_t>(a.v_stride) * 2, 128, d * 2};
-  const cuuint32_t k_box[4] = {64, kAtN, static_cast<cuuint32_t>(a.d == 64 ? 1 : 2), 1};
-  const cuuint32_t v_box[4] = {64, static_cast<cuuint32_t>(a.d == 256 ? kAtN / 2 : kAtN),
+  constexpr cuuint32_t kN = 128;   // PromptWork's
+  const cuuint32_t k_box[4] = {64, kN, static_cast<cuuint32_t>(a.d == 64 ? 1 : 2), 1};
+  const cuuint32_t v_box[4] = {64, static_cast<cuuint32_t>(a.d == 256 ? kN / 2 : kN),
                                static_cast<cuuint32_t>(a.d == 256 ? 4 : a.d / 64), 1};
   return at_encode(&m->k, 4, a.k, dims, k_str, k_box) && at_encode(&m->v, 4, a.v, dims, v_str, v_box);
 }
@@ -250,7 +255,7 @@ cudaError_t launch_prompt(const PromptParams& a, cudaStream_t stream) {
   p.c = std::max(std::fabs(a.scale_log2), std::numeric_limits<float>::denorm_min());
   p.heads = heads;
   p.sets = a.h_q / heads;
-  const int tpb = AttnCfg<D>::kTiles * kAtM / heads;
+  const int tpb = AttnCfg<D, 128, false>::kTiles * kAtM / heads;
   // a sequence has its blocks and at most one that is not full
   const int64_t most = (static_cast<int64_t>(a.n_tok) / tpb + std::min(a.batch, a.n_tok)) * p.sets;
   const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(di.sm_count, most)));

@@ -29,7 +29,7 @@ struct PrefixParams {
   int negative;
   int32_t* status;
   int heads, sets;    // query heads of a tile; h_q / heads
-  int box;            // positions of a copy: gcd(page_tokens, 128)
+  int box;            // positions of a copy: gcd(page_tokens, keys of a tile)
 };
 
 // Query heads of one tile: the whole group, if it fits, so that few sequences fill few tiles.
@@ -43,9 +43,11 @@ int prefix_heads(int group) {
 struct PlanArgs {
   SharedParams s;
   DecodeParams a;
-  int tpu;        // tokens of a prefix unit
+  int tpt, tiles; // tokens of a tile; tiles of a prefix unit
   int sets;       // head sets
   int sms;
+  // its query vectors fill one M tile of the two, which then take splits of their own
+  __device__ __forceinline__ bool dual(const PrefixGroup& g) const { return tiles == 2 && g.n * a.rows <= tpt; }
 };
 
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
@@ -95,11 +97,13 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
     least = __reduce_min_sync(0xffffffffu, least);
     const int eff = live >= 2 && least >= kLeastPrefix ? least / p.page_tokens * p.page_tokens : 0;
     if (lane == 0) {
-      const int pairs = (n * p.rows + x.tpu - 1) / x.tpu;
+      const int tpu = x.tpt * x.tiles, pairs = (n * p.rows + tpu - 1) / tpu;
       PrefixGroup pg = {b0, n, eff, 0, 0, pairs, 0, row};
       s.groups[g] = pg;
+      // (a dual unit works through two splits in the time of one)
       if (eff > 0)
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s_prefix), static_cast<unsigned long long>(eff) * pairs * x.sets);
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s_prefix),
+                  static_cast<unsigned long long>(eff) * pairs * x.sets * (x.dual(pg) ? 1 : 2));
     }
   }
   __syncthreads();
@@ -107,10 +111,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
   for (int g = warp; g < s.n_groups; g += kWarps) {
     const PrefixGroup pg = s.groups[g];
     if (pg.eff == 0) continue;
-    long long want = (static_cast<long long>(x.sms) * pg.eff + s_prefix / 2) / s_prefix;
-    const int most = min(min(kPrefixSplits, p.max_splits / 2), (pg.eff + 255) / 256);
+    const long long want = (2ll * x.sms * pg.eff + s_prefix / 2) / s_prefix;
+    const int least = x.dual(pg) ? 128 : 256;
+    const int most = min(min(kPrefixSplits, p.max_splits / 2), (pg.eff + least - 1) / least);
     const int n = static_cast<int>(want < 1 ? 1 : (want > most ? most : want));
-    const int seg = ((pg.eff + n - 1) / n + kAtN - 1) / kAtN * kAtN;
+    const int seg = ((pg.eff + n - 1) / n + 127) / 128 * 128;
     const int splits = (pg.eff + seg - 1) / seg;
     for (int i = lane; i < pg.n; i += 32)
       if (len_of(pg.b0 + i, false) > 0) s.seqs[pg.b0 + i] = make_int2(pg.eff, splits);
@@ -126,7 +131,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
     for (int g0 = 0; g0 < s.n_groups; g0 += 32) {
       const int g = g0 + lane;
       int units = 0;
-      if (g < s.n_groups) units = s.groups[g].splits * s.groups[g].pairs * x.sets;
+      if (g < s.n_groups) {
+        const PrefixGroup pg = s.groups[g];
+        units = (x.dual(pg) ? (pg.splits + 1) / 2 : pg.splits) * pg.pairs * x.sets;
+      }
       int sum = units;
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, sum, o);
@@ -209,31 +217,33 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
 }
 
 // ---------------------------------------------------------------- prefixes
-template <int D, int kTermsOfP>
+template <int D, bool kE4, int kTermsOfP>
 struct PrefixWork {
   using Params = PrefixParams;
-  using C = AttnCfg<D>;
+  static constexpr int kN = kTermsOfP == 3 ? 64 : 128;   // keys of a tile
+  static constexpr bool kF8 = kE4;
   static constexpr bool kPaged = true;
   static constexpr bool kWaitLate = true;
   static constexpr int kTerms = kTermsOfP;
+  static constexpr bool kPairs = D <= 128;               // two M tiles a unit, or one over two ranges of keys
   // What is read before the grid ahead is waited for comes past L1 (__ldcg): the plan is complete, but an older line may
   // still lie there.
   const Params& p;
   int tpt, n_units;
-  int ids_next, ids[2];   // loader: page of lane's box of the next K tile, of the last two
-  int id_next;            // softmax: page of lane's 16-key piece of the next tile
+  int ids_next[2], ids[2];   // loader: pages of lane's box, of the next K tile and the last (of M tile t, or the last two)
+  int id_next;               // softmax: page of lane's 16-key piece of the next tile
 
   __device__ __forceinline__ int toks_per_tile() const { return tpt; }
   __device__ __forceinline__ int heads() const { return p.heads; }
   __device__ __forceinline__ PrefixWork(const Params& params, int) : p(params) {
     tpt = kAtM / p.heads;
     n_units = __ldcg(p.a.header + 4);
-    ids_next = ids[0] = ids[1] = id_next = 0;
+    ids_next[0] = ids_next[1] = ids[0] = ids[1] = id_next = 0;
   }
   __device__ __forceinline__ bool unit(uint32_t round, AttnUnit& u) const {
-    const int64_t at = static_cast<int64_t>(round) * gridDim.x + blockIdx.x;
-    if (at >= n_units) return false;
-    const int un = static_cast<int>(at), lane = threadIdx.x & 31;
+    const int64_t place = static_cast<int64_t>(round) * gridDim.x + blockIdx.x;
+    if (place >= n_units) return false;
+    const int un = static_cast<int>(place), lane = threadIdx.x & 31;
     // the last group whose first unit is not behind this one (groups without units share theirs with the next)
     int g = 0;
     for (int g0 = 0; g0 < p.s.n_groups; g0 += 32) {
@@ -243,43 +253,52 @@ struct PrefixWork {
       g = g0 + 31 - __clz(has);
     }
     const int4* const at_g = reinterpret_cast<const int4*>(p.s.groups + g);
-    const int4 g0 = __ldcg(at_g), g1 = __ldcg(at_g + 1);
-    const PrefixGroup pg = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+    const int4 w0 = __ldcg(at_g), w1 = __ldcg(at_g + 1);
+    const PrefixGroup pg = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
     const int rest = un - pg.unit;
     const int pair = rest % pg.pairs, which = rest / pg.pairs;
     const int set = which % p.sets, split = which / p.sets;
-    u.toks = min(C::kTiles * tpt, pg.n * p.a.rows - pair * C::kTiles * tpt);
-    u.tok = pg.b0 * p.a.rows + pair * C::kTiles * tpt;
+    u.dual = kPairs && pg.n * p.a.rows <= tpt;
+    const int tpu = (kPairs ? 2 : 1) * tpt;
+    u.toks = min(tpu, pg.n * p.a.rows - pair * tpu);
+    u.tok = pg.b0 * p.a.rows + pair * tpu;
     u.head = set * p.heads;
     u.kvh = u.head / p.a.group;
     u.pos = 0;
-    u.kv = split * pg.seg;
-    u.end = min(pg.eff, u.kv + pg.seg);
     u.b = pg.row;
-    u.slot = split;
-    const int n = (u.end - u.kv + kAtN - 1) / kAtN;
-    u.n[0] = n;
-    u.n[1] = C::kTiles == 2 && u.toks > tpt ? n : 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      u.slot[t] = u.dual ? 2 * split + t : split;
+      u.kv[t] = u.slot[t] * pg.seg;
+      u.end[t] = min(pg.eff, u.kv[t] + pg.seg);
+      u.n[t] = max(0, u.end[t] - u.kv[t] + kN - 1) / kN;
+    }
+    if (!u.dual && !(kPairs && u.toks > tpt)) u.n[1] = 0;
     return true;
   }
-  __device__ __forceinline__ int last_keys(const AttnUnit& u, int n) const { return u.end - u.kv - (n - 1) * kAtN; }
-  __device__ __forceinline__ int last_key(const AttnUnit& u, int, bool) const { return u.end - u.kv - 1; }
+  __device__ __forceinline__ int last_keys(const AttnUnit& u, int t) const {
+    return u.end[t] - u.kv[t] - (u.n[t] - 1) * kN;
+  }
+  __device__ __forceinline__ int last_key(const AttnUnit& u, int t, int, bool) const { return u.end[t] - u.kv[t] - 1; }
   __device__ __forceinline__ bool in_pool(int page) const { return page >= 0 && page < p.a.num_pages; }
   // the page of the 16 (or box) positions from `at` on; 0 past the end
-  __device__ __forceinline__ int page_at(const AttnUnit& u, int at) const {
-    return at < u.end ? __ldcg(p.a.block_table + static_cast<int64_t>(u.b) * p.a.max_pages + at / p.a.page_tokens) : 0;
+  __device__ __forceinline__ int page_at(const AttnUnit& u, int t, int at) const {
+    return at < u.end[t] ? __ldcg(p.a.block_table + static_cast<int64_t>(u.b) * p.a.max_pages + at / p.a.page_tokens) : 0;
   }
-  __device__ __forceinline__ uint32_t bad_keys(const AttnUnit& u, int j, int c0) {
+  __device__ __forceinline__ uint32_t bad_keys(const AttnUnit& u, int t, int j, int c0) {
+    constexpr int kPieces = (kPairs ? kN : kN / 2) / 16;
     const int lane = threadIdx.x & 31;
-    const int at = u.kv + j * kAtN + c0 + lane * 16;
-    if (j == 0) id_next = lane < C::kCols / 16 ? page_at(u, at) : 0;
+    const int at = u.kv[t] + j * kN + c0 + lane * 16;
+    if (j == 0) id_next = lane < kPieces ? page_at(u, t, at) : 0;
     const int id = id_next;
-    if (lane < C::kCols / 16 && at + kAtN < u.end) id_next = page_at(u, at + kAtN);
-    else id_next = 0;
+    id_next = lane < kPieces ? page_at(u, t, at + kN) : 0;
     return __ballot_sync(0xffffffffu, !in_pool(id));
   }
+  __device__ __forceinline__ const __nv_bfloat16* q_row(const AttnUnit& u, int tok, int head) const {
+    return static_cast<const __nv_bfloat16*>(p.a.q) + ((static_cast<int64_t>(u.tok) + tok) * p.a.h_q + u.head + head) * D;
+  }
 
-  template <int>
+  template <class C>
   __device__ __forceinline__ void load_q(const AttnUnit& u, char* q_s, uint64_t* bar) const {
     if ((threadIdx.x & 31) != 0) return;
     const uint32_t bytes = tpt * p.heads * 128;   // of an atom; the lanes behind them hold what was there
@@ -289,51 +308,77 @@ struct PrefixWork {
       if (u.n[t] > 0)
 #pragma unroll
         for (int a = 0; a < D / 64; ++a)
-          tma_load_3d(q_s + t * C::kQTile + a * C::kAtom, &p.q, a * 64, u.head, u.tok + t * tpt, bar);
+          tma_load_3d(q_s + t * C::kQTile + a * C::kQAtom, &p.q, a * 64, u.head, u.tok + (u.dual ? 0 : t * tpt), bar);
   }
-  // Lane l copies a box of positions by 64 columns; page ids are fetched a tile ahead.
-  template <int>
-  __device__ __forceinline__ void load_kv(const AttnUnit& u, bool is_v, int j, int part, char* dst, uint64_t* bar) {
+  // Lane l copies a box of positions (bf16: by 64 columns); page ids are fetched a tile ahead.
+  template <class C>
+  __device__ __forceinline__ void load_kv(const AttnUnit& u, bool is_v, int t, int j, int part, char* dst, uint64_t* bar) {
     const int lane = threadIdx.x & 31, box = p.box;
-    const int boxes = kAtN / box;
-    if (!is_v && part == 0) {
-      const int at = u.kv + j * kAtN + lane * box;
-      ids[1] = ids[0];
-      ids[0] = j == 0 ? (lane < boxes ? page_at(u, at) : 0) : ids_next;
-      ids_next = lane < boxes ? page_at(u, at + kAtN) : 0;
-      if (lane < boxes && at < u.end && !in_pool(ids[0])) raise_status(p.status, NBX_DEV_BAD_PAGE);
+    const int boxes = kN / box;
+    const int tile = u.kv[t] + j * kN;
+    int id;
+    if constexpr (kPairs) {   // V of a tile follows its K before the next K of the same M tile
+      if (!is_v) {
+        const int at = tile + lane * box;
+        const int now = j == 0 ? (lane < boxes ? page_at(u, t, at) : 0) : ids_next[t];
+        const int next = lane < boxes ? page_at(u, t, at + kN) : 0;
+        if (t == 0) ids[0] = now, ids_next[0] = next;
+        else ids[1] = now, ids_next[1] = next;
+        if (lane < boxes && at < u.end[t] && !in_pool(now)) raise_status(p.status, NBX_DEV_BAD_PAGE);
+      }
+      id = t == 0 ? ids[0] : ids[1];
+    } else {                  // K runs two tiles ahead of V, but for a unit's last
+      if (!is_v && part == 0) {
+        const int at = tile + lane * box;
+        ids[1] = ids[0];
+        ids[0] = j == 0 ? (lane < boxes ? page_at(u, t, at) : 0) : ids_next[0];
+        ids_next[0] = lane < boxes ? page_at(u, t, at + kN) : 0;
+        if (lane < boxes && at < u.end[t] && !in_pool(ids[0])) raise_status(p.status, NBX_DEV_BAD_PAGE);
+      }
+      id = is_v && j + 1 < u.n[0] ? ids[1] : ids[0];
     }
-    // (K runs kAhead tiles ahead of V, but for a unit's last tiles)
-    const int id = is_v && C::kAhead == 2 && j + 1 < u.n[0] ? ids[1] : ids[0];
-    constexpr int kAtoms = C::kParts == 1 ? D / 64 : 0;
-    const int atoms = C::kParts == 1 ? kAtoms : (is_v ? 4 : 2);
-    const int here = C::kParts == 2 && is_v ? boxes / 2 : boxes;             // boxes of this slot
-    const int first = C::kParts == 2 && is_v && part ? kAtN / 2 : 0;         // its first position in the tile
-    // d = 256 with boxes of 128 positions: V's halves are boxes of 64 of their own map
-    const int vbox = C::kParts == 2 && is_v && box == kAtN ? kAtN / 2 : box;
-    const int n_here = C::kParts == 2 && is_v && box == kAtN ? 1 : here;
-    const int atom = lane / n_here, b = lane - atom * n_here;
-    const int off = first + b * vbox;                                         // in the tile
-    const int at = u.kv + j * kAtN + off;
-    const int page = __shfl_sync(0xffffffffu, id, (off / box) & 31);
-    const bool mine = atom < atoms && at < u.end;
-    const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine));
-    if (lane == 0) mbar_arrive_expect_tx(bar, copies * vbox * 128);
-    __syncwarp();
-    if (mine) {
-      const int row = in_pool(page) ? (page * p.a.h_kv + u.kvh) * p.a.page_tokens + at % p.a.page_tokens : -kAtN;
-      const int atom_bytes = C::kParts == 2 && is_v ? C::kAtom / 2 : C::kAtom;
-      const int col = (C::kParts == 2 && !is_v ? part * 2 + atom : atom) * 64;
-      tma_load_2d(dst + atom * atom_bytes + b * vbox * 128, is_v ? &p.v : &p.k, col, row, bar);
+    if constexpr (kF8) {      // the codes as they are stored: a box of a head is one run of bytes
+      const int at = tile + lane * box;
+      const bool mine = lane < boxes && at < u.end[t], held = mine && in_pool(id);
+      if (mine && !held) {    // 0 x whatever lay here must not be a NaN
+        for (int i = 0; i < box * D; i += 16) *reinterpret_cast<uint4*>(dst + lane * box * D + i) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();  // a copy may fill the place next time
+      }
+      const uint32_t copies = __popc(__ballot_sync(0xffffffffu, held));
+      if (lane == 0) mbar_arrive_expect_tx(bar, copies * box * D);
+      __syncwarp();
+      if (held) {
+        const char* pool = static_cast<const char*>(is_v ? p.a.v_pool : p.a.k_pool);
+        const int64_t row = (static_cast<int64_t>(id) * p.a.h_kv + u.kvh) * p.a.page_tokens + at % p.a.page_tokens;
+        bulk_g2s(dst + lane * box * D, pool + row * D, box * D, bar);
+      }
+    } else {
+      const bool half_v = C::kParts == 2 && is_v;                        // half of V's keys
+      const int vbox = half_v && box > kN / 2 ? kN / 2 : box;            // (V has a map of its own for such boxes)
+      const int atoms = C::kParts == 1 || is_v ? C::kAtoms : 2;          // columns of this slot
+      const int here = (half_v ? kN / 2 : kN) / vbox;                    // boxes of this slot
+      const int atom = lane / here, b = lane - atom * here;
+      const int off = (half_v && part ? kN / 2 : 0) + b * vbox;          // in the tile
+      const int at = tile + off;
+      const int page = __shfl_sync(0xffffffffu, id, (off / box) & 31);
+      const bool mine = atom < atoms && at < u.end[t];
+      const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine));
+      if (lane == 0) mbar_arrive_expect_tx(bar, copies * vbox * 128);
+      __syncwarp();
+      if (mine) {   // a page outside the pool: rows before the tensor, which read as zeros
+        const int row = in_pool(page) ? (page * p.a.h_kv + u.kvh) * p.a.page_tokens + at % p.a.page_tokens : -kN;
+        const int col = (C::kParts == 2 && !is_v ? part * 2 + atom : atom) * 64;
+        tma_load_2d(dst + atom * (half_v ? kN * 64 : kN * 128) + b * vbox * 128, is_v ? &p.v : &p.k, col, row, bar);
+      }
     }
   }
   template <int kCols>
-  __device__ __forceinline__ void store(const AttnUnit& u, uint32_t o_base, int col0, int tok, int head, bool ok, float m,
-                                        float l, uint64_t* o_free) const {
+  __device__ __forceinline__ void store(const AttnUnit& u, int t, uint32_t o_base, int col0, int tok, int head, bool ok,
+                                        float m, float l, uint64_t* o_free) const {
     const int lane = threadIdx.x & 31;
     const uint64_t keep = l2_keep_policy(p.a.keep_frac);
     const int64_t row = (static_cast<int64_t>(u.tok) + tok) * p.a.h_q + u.head + head;
-    const int64_t at = row * p.a.max_splits + u.slot;
+    const int64_t at = row * p.a.max_splits + u.slot[t];
     if (ok && col0 == 0) {
       st_global_hint(p.a.m_part + at, m, keep);
       st_global_hint(p.a.l_part + at, l, keep);
@@ -433,8 +478,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(SharedPa
   }
 }
 
-bool encode_maps(PrefixParams* m) {
+bool encode_maps(PrefixParams* m, int pool_dtype, int tile_keys) {
   const DecodeParams& a = m->a;
+  if (pool_dtype == NBX_E4M3) return true;   // queries by threads, codes by plain copies
   const cuuint64_t d = static_cast<cuuint64_t>(a.d);
   const cuuint64_t q_dims[3] = {d, static_cast<cuuint64_t>(a.h_q), static_cast<cuuint64_t>(a.batch) * a.rows};
   const cuuint64_t q_str[2] = {d * 2, static_cast<cuuint64_t>(a.h_q) * d * 2};
@@ -443,26 +489,28 @@ bool encode_maps(PrefixParams* m) {
   const cuuint64_t dims[2] = {d, static_cast<cuuint64_t>(a.num_pages) * a.h_kv * a.page_tokens};
   const cuuint64_t str[1] = {d * 2};
   const cuuint32_t k_box[2] = {64, static_cast<cuuint32_t>(m->box)};
-  const cuuint32_t v_box[2] = {64, static_cast<cuuint32_t>(a.d == 256 ? std::min(m->box, kAtN / 2) : m->box)};
+  const cuuint32_t v_box[2] = {64, static_cast<cuuint32_t>(a.d == 256 ? std::min(m->box, tile_keys / 2) : m->box)};
   return at_encode(&m->k, 2, a.k_pool, dims, str, k_box) && at_encode(&m->v, 2, a.v_pool, dims, str, v_box);
 }
 
 // The maps of the last few calls from this host thread, keyed by everything they encode.
 struct PrefixKey {
   const void *q, *k, *v;
-  int rows, h_q, h_kv, d, num_pages, page_tokens, device;
+  int rows, h_q, h_kv, d, num_pages, page_tokens, pool_dtype, tile_keys, device;
   bool operator==(const PrefixKey& o) const {
     return q == o.q && k == o.k && v == o.v && rows == o.rows && h_q == o.h_q && h_kv == o.h_kv && d == o.d &&
-           num_pages == o.num_pages && page_tokens == o.page_tokens && device == o.device;
+           num_pages == o.num_pages && page_tokens == o.page_tokens && pool_dtype == o.pool_dtype && tile_keys == o.tile_keys &&
+           device == o.device;
   }
 };
 
-const PrefixParams* prefix_maps(const DecodeParams& a, int heads, int box, int device) {
+const PrefixParams* prefix_maps(const DecodeParams& a, int heads, int box, int pool_dtype, int tile_keys, int device) {
   constexpr int kEntries = 8;
   thread_local PrefixKey keys[kEntries];
   thread_local PrefixParams maps[kEntries];
   thread_local int used = 0, next = 0;
-  const PrefixKey key{a.q, a.k_pool, a.v_pool, a.batch * a.rows, a.h_q, a.h_kv, a.d, a.num_pages, a.page_tokens, device};
+  const PrefixKey key{a.q, a.k_pool, a.v_pool, a.batch * a.rows, a.h_q, a.h_kv, a.d, a.num_pages, a.page_tokens,
+                      pool_dtype, tile_keys, device};
   for (int i = 0; i < used; ++i)
     if (keys[i] == key) return &maps[i];
   const int at = next;
@@ -472,18 +520,19 @@ const PrefixParams* prefix_maps(const DecodeParams& a, int heads, int box, int d
   maps[at].a = a;
   maps[at].heads = heads;
   maps[at].box = box;
-  if (!encode_maps(&maps[at])) return nullptr;
+  if (!encode_maps(&maps[at], pool_dtype, tile_keys)) return nullptr;
   keys[at] = key;
   return &maps[at];
 }
 
-template <int D>
+template <int D, bool kE4, int kTerms>
 cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, cudaStream_t stream) {
+  using W = PrefixWork<D, kE4, kTerms>;
   const DeviceInfo& di = device_info();
   const int heads = prefix_heads(a.group);
-  int box = kAtN;
+  int box = W::kN;
   while (a.page_tokens % box) box >>= 1;
-  const PrefixParams* maps = prefix_maps(a, heads, box, di.device);
+  const PrefixParams* maps = prefix_maps(a, heads, box, kE4 ? NBX_E4M3 : NBX_BF16, W::kN, di.device);
   if (maps == nullptr) return cudaErrorInvalidValue;
   PrefixParams p = *maps;
   p.s = s;
@@ -494,9 +543,13 @@ cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, cudaStre
   p.heads = heads;
   p.sets = a.h_q / heads;
   p.box = box;
-  const unsigned grid = static_cast<unsigned>(di.sm_count);
-  return a.out_bf16 ? launch_attn_tiles<PrefixWork<D, 1>, D>(p, grid, stream)
-                    : launch_attn_tiles<PrefixWork<D, 2>, D>(p, grid, stream);
+  return launch_attn_tiles<W, D>(p, static_cast<unsigned>(di.sm_count), stream);
+}
+template <int D>
+cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, int pool_dtype, cudaStream_t stream) {
+  if (pool_dtype == NBX_E4M3)
+    return a.out_bf16 ? launch_prefix<D, true, 1>(s, a, stream) : launch_prefix<D, true, 2>(s, a, stream);
+  return a.out_bf16 ? launch_prefix<D, false, 1>(s, a, stream) : launch_prefix<D, false, 3>(s, a, stream);
 }
 
 }  // namespace
@@ -534,7 +587,7 @@ bool shared_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq_le
 
 bool prefix_path_applies(const DecodeParams& p, int q_dtype, int pool_dtype) {
   const int64_t pool_rows = static_cast<int64_t>(p.num_pages) * p.h_kv * p.page_tokens;
-  return q_dtype == NBX_BF16 && pool_dtype == NBX_BF16 && pool_rows < (int64_t{1} << 31) - kAtN;
+  return q_dtype == NBX_BF16 && (pool_dtype == NBX_E4M3 || (pool_dtype == NBX_BF16 && pool_rows < (int64_t{1} << 31) - 128));
 }
 
 cudaError_t shared_dispatch(const SharedParams& s, const DecodeParams& p, int q_dtype, int pool_dtype, int grid_limit,
@@ -552,14 +605,18 @@ cudaError_t shared_dispatch(const SharedParams& s, const DecodeParams& p, int q_
   x.s = s;
   x.a = q;
   const int heads = prefix_heads(p.group);
-  x.tpu = (p.d <= 128 ? 2 : 1) * (kAtM / heads);
+  x.tpt = kAtM / heads;
+  x.tiles = p.d <= 128 ? 2 : 1;
   x.sets = p.h_q / heads;
   x.sms = di.sm_count;
   cudaError_t e = launch_pdl(shared_plan_kernel, 1u, kPlanThreads, 0, stream, x);
   if (e != cudaSuccess) return e;
-  e = decode_dispatch_warp_bf16(q, grid_limit, stream);
+  e = pool_dtype == NBX_E4M3 ? decode_dispatch_warp_e4m3(q, q_dtype, grid_limit, stream)
+                             : decode_dispatch_warp_bf16(q, grid_limit, stream);
   if (e != cudaSuccess) return e;
-  e = p.d == 64 ? launch_prefix<64>(s, q, stream) : p.d == 128 ? launch_prefix<128>(s, q, stream) : launch_prefix<256>(s, q, stream);
+  e = p.d == 64    ? launch_prefix<64>(s, q, pool_dtype, stream)
+      : p.d == 128 ? launch_prefix<128>(s, q, pool_dtype, stream)
+                   : launch_prefix<256>(s, q, pool_dtype, stream);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(p.batch) * p.rows * p.h_q * ((p.d / 4 + 31) / 32);
   const int64_t grid = std::min<int64_t>((items + kMergeWarps - 1) / kMergeWarps, static_cast<int64_t>(di.sm_count) * 8);
