@@ -388,7 +388,7 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
     p.ranges = reinterpret_cast<int2*>(ws + w.ranges);
     p.order = reinterpret_cast<int32_t*>(ws + w.order);
   }
-  if (groups && groups->n_groups > 0 && prefix_path_applies(p, q_dtype, pool_dtype)) {
+  if (groups && groups->n_groups > 0 && prefix_path_applies(q_dtype, pool_dtype)) {
     SharedParams g = *groups;
     g.seqs = reinterpret_cast<int2*>(ws + sw.seqs);
     g.groups = reinterpret_cast<PrefixGroup*>(ws + sw.groups);

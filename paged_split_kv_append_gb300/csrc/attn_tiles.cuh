@@ -8,22 +8,25 @@
 // outputs (each weight off by up to 2^-8 of itself in bf16, as much as the output's own rounding; 2^-11 in f16), for fp32
 // outputs as many as leave 2^-22 or less (three in bf16, two in f16), on key tiles of 64, whose S leaves them room.
 //
-// One persistent CTA per SM, twelve warps, every wait bounded:
+// One persistent CTA per SM, sixteen warps, every wait bounded:
 //  * warps 0-3 and 4-7: two softmax groups. Up to d = 128 each has an M tile of its own, one row a thread, and the two
 //    take turns with the tensor pipe: while one group works on its S, the MMAs of the other's tile run. Both tiles attend
 //    the same keys, or (dual units, whose query vectors fill one tile) the same vectors attend two ranges of keys. At
 //    d = 256 O fills half of the TMEM, so there is one M tile, S is double-buffered, and the groups share each row, half
 //    of the columns each; the two threads of a row swap their maxima through shared memory.
-//  * warp 8 fills the ring of K and V with TMA: slots of a whole tile, or at d = 256 half of one (128 columns of K, half
-//    of V's keys); and the unit's Q tiles.
-//  * warp 9 issues the MMAs: QK^T (both operands from shared memory) and PV (P from TMEM, N = d), in an order in which the
-//    group whose P is awaited is never the one whose S was asked for last. Waiting for P(j) of a tile is all that orders
-//    PV(j), QK(j + 1) of the same tile follows it in the pipe and may overwrite P(j).
-//  * E4M3 pools: warp 8 copies the codes of a tile as they are stored, and warps 10 and 11 convert them to f16 (exactly)
-//    into the ring. Queries enter as f16 too, times a power of two that brings the largest element of each vector into
-//    [2^14, 2^15): exact but for elements under 2^-29 of it. The softmax threads write them, each its own row, and take
-//    the factor back in their row's c. The running maximum sits 2^7 above P's largest weight then, so that small weights
-//    keep their bits in f16's range.
+//  * warps 9 and 10 issue the MMAs: QK^T (both operands from shared memory) and PV (P from TMEM, N = d). Up to d = 128 each
+//    has an M tile: waiting for P(j) is all that orders PV(j), and QK(j + 1) of the same tile follows it in the pipe and
+//    may overwrite P(j). At d = 256 warp 9 has the PVs and warp 10 the QK^Ts. A single warp's chain of waits and issues
+//    took 2.4 us for 128 keys and two tiles of d = 128, whose MMAs take 1.1.
+//  * warp 8 fills the ring of K and V with TMA: slots of a whole tile, or at d = 256 half of one (128 columns of K, half of
+//    V's keys); and the unit's Q tiles.
+//  * Paged K and V come by 16-byte cp.async of warps 12-15. (A tensor copy costs the copy engine some 135 ns whatever its
+//    size, and pages of 16 positions take 16 of 2 KB for 32 KB.)
+//  * E4M3 pools: warp 8 copies the codes of a tile as they are stored (cp.async), and warps 12-15 convert them to f16
+//    (exactly) into the ring. Queries enter as f16 too, times a power of two that brings the largest element of each
+//    vector into [2^14, 2^15): exact but for elements under 2^-29 of it. The softmax threads write them, each its own row,
+//    and take the factor back in their row's c. The running maximum sits 2^7 above P's largest weight then, so that small
+//    weights keep their bits in f16's range.
 // What bounds it: the tensor pipe. Per 128 keys and two tiles of d = 128 it is busy 2048 cycles; the softmax issues
 // about 900 instructions on each scheduler and takes 1024 cycles of the special-function units (4 a warp measured).
 #pragma once
@@ -41,10 +44,11 @@ namespace {
 
 constexpr int kAtM = 128;         // query vectors of an M tile = TMEM lanes
 constexpr int kAtBuf = 128;       // TMEM columns of an S/P buffer
-constexpr int kAtThreads = 384;
-// Registers a thread: of the 168 each is launched with (65536 over three warps a scheduler), the group of the loader and
-// the MMA warp gives what a softmax thread needs to hold its 128 scores: 2 * 208 + 88 = 3 * 168.
-constexpr int kAtSoftmaxRegs = 208, kAtOtherRegs = 88;
+constexpr int kAtThreads = 512;
+// Registers a thread: of the 128 each is launched with, the eight warps of copies and MMAs give what a softmax thread
+// needs to hold its 128 scores: 200 + 56 = 2 * 128.
+constexpr int kAtSoftmaxRegs = 200, kAtOtherRegs = 56;
+constexpr int kAtCopyWarps = 4;   // warps 12-15
 constexpr float kAtTau = 8.f;     // the running maximum moves when it would grow by more, log2 units
 
 template <int D, int N, bool F8>
@@ -58,19 +62,20 @@ struct AttnCfg {
   static constexpr int kQAtom = kAtM * 128;                      // 128 rows of 128 bytes
   static constexpr int kQTile = kAtoms * kQAtom;
   static constexpr int kRawBytes = F8 ? N * D : 0;               // a tile of codes
-  static constexpr int kRaws = F8 ? 2 : 0;
+  static constexpr int kRaws = F8 ? 4 : 0;
   static constexpr int kRoom = 224 * 1024 - kTiles * kQTile - kRaws * kRawBytes;
-  static constexpr int kMost = kTiles == 1 || F8 ? 6 : 8;        // (what the barrier area holds)
+  static constexpr int kMost = kTiles == 2 ? 8 : (F8 ? 5 : 6);   // (d = 256: what the barriers and xbuf leave)
   static constexpr int kSlots = kRoom / kSlotBytes < kMost ? kRoom / kSlotBytes : kMost;
   static constexpr int kRingOff = kTiles * kQTile;
   static constexpr int kRawOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
-  static constexpr int kXOff = kBarOff + 256;
+  static constexpr int kBarBytes = F8 ? 384 : 256;
+  static constexpr int kXOff = kBarOff + kBarBytes;
   static constexpr int kSmem = kXOff + (kTiles == 1 ? 2 * 256 * 4 : 0) + 768;   // slack: 256-byte alignment to 1024
   static constexpr uint32_t kOCol = 2 * kAtBuf;                  // S (and P) in columns [0, 256), O from there
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kSlots >= 3, "ring");
-  static_assert((2 * kSlots + 2 * kRaws + 12) * 8 <= 256, "barrier area");
+  static_assert((2 * kSlots + 2 * kRaws + 12) * 8 <= kBarBytes, "barrier area");
 };
 
 // One work unit.
@@ -87,18 +92,18 @@ struct AttnUnit {
   int n[2];       // key tiles of each M tile
 };
 
-__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait(bar, parity)) return true;
+// Bounded wait of a whole warp, with one answer: gives up when another role of the CTA has, or after kWaitLimitNs. Every
+// branch is on a vote, so the compiler knows the warp to be together behind it (and may use uniform registers there).
+__device__ __forceinline__ bool at_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if ((i & 3u) == 0u && global_timer_ns() - t0 > kWaitLimitNs) return false;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || ((i & 3u) == 0u && global_timer_ns() - t0 > kWaitLimitNs))) return false;
   }
 }
-__device__ __forceinline__ bool at_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-  return __all_sync(0xffffffffu, at_wait(bar, parity, abort_flag));
-}
+// x, the same in every lane of the warp, as a value that the compiler knows to be
+__device__ __forceinline__ int at_uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
   asm volatile(
@@ -144,6 +149,9 @@ __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float2 f16x2_floats(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+__device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 // Four E4M3 codes to two f16 pairs, exactly (the low two codes in lo).
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
@@ -203,189 +211,207 @@ struct AttnShared {
   float* xbuf;         // [2][256]
 };
 
-// ---------------------------------------------------------------- the MMA warp
+// ---------------------------------------------------------------- the MMA warps
+// MMAs and commits of one lane, as predicated instructions: the warp stays together, so that descriptors are computed once
+// a warp, in uniform registers. (In a branch of one lane every operand went there by itself, and issuing 8 MMAs took 420 ns,
+// twice their time in the tensor pipe.)
+// Four K steps of 16: A advances by 32 bytes of its swizzled rows, B too (K-major) or by 16 rows (MN-major), or A by 8
+// TMEM columns. `left`: steps that there are.
+__device__ __forceinline__ void at_mma_ss4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "add.s64 a1, %1, 2;\n\tadd.s64 b1, %2, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 b2, %2, 4;\n\t"
+      "add.s64 a3, %1, 6;\n\tadd.s64 b3, %2, 6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, 1;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, 1;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(issue)
+      : "memory");
+}
+__device__ __forceinline__ void at_mma_ts4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, int left) {
+  asm volatile(
+      "{\n\t.reg .pred p, q0, q1, q2, q3;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "setp.gt.s32 q0, %5, 0;\n\tsetp.gt.s32 q1, %5, 1;\n\tsetp.gt.s32 q2, %5, 2;\n\tsetp.gt.s32 q3, %5, 3;\n\t"
+      "add.s32 a1, %1, 8;\n\tadd.s64 b1, %2, 128;\n\tadd.s32 a2, %1, 16;\n\tadd.s64 b2, %2, 256;\n\t"
+      "add.s32 a3, %1, 24;\n\tadd.s64 b3, %2, 384;\n\t"
+      "@q0 tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@q1 tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n\t"
+      "@q2 tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n\t"
+      "@q3 tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(left)
+      : "memory");
+}
+__device__ __forceinline__ void at_commit(uint64_t* bar, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(issue)
+      : "memory");
+}
+
+// which: the M tile of this warp, or at d = 256 what it issues (0: PV, 1: QK^T).
 template <class W, class C, int D>
-__device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t tmem) {
+__device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t tmem, int which) {
   constexpr int T = C::kTiles, NS = C::kSlots, N = W::kN;
-  constexpr int kAtomBytes = N * 128 / (C::kParts);   // of V: N (or N / 2) rows of 128 bytes
+  constexpr int kAtomBytes = N * 128 / C::kParts;   // of V: N (or N / 2) rows of 128 bytes
   constexpr uint32_t kIdescO = mma_idesc(kAtM, D, true, W::kF8);
   // a negative scale: S of -Q (the descriptor's bit 13 negates A), and its magnitude
   const uint32_t idesc_s = mma_idesc(kAtM, N, false, W::kF8) | (w.p.negative ? 1u << 13 : 0u);
   const int lane = threadIdx.x & 31;
+  const uint32_t one = lane == 0;    // the lane that issues
+  const int t = T == 2 ? which : 0;
+  const bool does_pv = T == 2 || which == 0, does_qk = T == 2 || which == 1;
   volatile int* ab = sh.abort_flag;
-  const uint32_t q_addr = smem_u32(sh.q_s), ring = smem_u32(sh.ring);
-  uint32_t r = 0;                    // ring slots consumed so far, in the loader's order
-  uint32_t np[2] = {0, 0};           // P buffers consumed
-  uint32_t units[2] = {0, 0};        // units with this M tile
-  uint32_t xs = 0;                   // d = 256: key tiles whose QK^T was issued (buffer xs & 1)
+  const uint32_t ring = smem_u32(sh.ring);
+  const uint64_t q_desc = smem_desc(smem_u32(sh.q_s) + t * C::kQTile, 16, 1024);
+  const uint64_t k_desc = smem_desc(ring, 16, 1024), v_desc = smem_desc(ring, kAtomBytes, 1024);
+  const uint32_t o_addr = tmem + C::kOCol + t * D;
+  int slot = 0;                      // the ring slot next consumed, in the loader's order, and its phase
+  uint32_t phase = 0;
+  uint32_t p_phase = 0, s_phase = 0; // bit: phase of a P buffer; d = 256: of the PV that frees an S buffer
+  uint32_t o_phase = 0;
+  bool o_used = false;               // O has been used
+  uint32_t x = 0;                    // key tiles of this M tile so far (d = 256: its buffer is bit 0)
   AttnUnit u;
-  auto slot_wait = [&](uint32_t at) { return at_warp_wait(&sh.full[at % NS], (at / NS) & 1u, ab); };
-  auto slot_addr = [&](uint32_t at) { return ring + (at % NS) * C::kSlotBytes; };
-  // S(buffer) = Q(tile t) K^T, K in ring slots at, ...
-  auto qk = [&](int t, uint32_t buf, uint32_t at) {
-    if (lane == 0) {
+  // The slots of the next tile (C::kParts of them, in a row but for the ring's end): the first, or -1. Both warps wait for
+  // every slot, their own or not, and both give it back: a parity wait must know the phase before to be over, and the one
+  // after not to be.
+  int second = 0;
+  auto acquire = [&]() -> int {
+    const int first = slot;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const int a = kk >> 2, sub = kk & 3;   // 64-column atom, 16-column step in it
-        const uint64_t ad = smem_desc(q_addr + t * C::kQTile + a * C::kQAtom + sub * 32, 16, 1024);
-        const uint32_t kb = C::kParts == 1 ? slot_addr(at) + a * (N * 128) : slot_addr(at + (a >> 1)) + (a & 1) * (N * 128);
-        tc_mma_ss(tmem + buf * kAtBuf, ad, smem_desc(kb + sub * 32, 16, 1024), idesc_s, kk > 0);
+    for (int i = 0; i < C::kParts; ++i) {
+      if (!at_warp_wait(&sh.full[slot], phase, ab)) return -1;
+      if (i == 1) second = slot;
+      if (++slot == NS) {
+        slot = 0;
+        phase ^= 1u;
       }
-      tc_commit(&sh.s_full[buf]);
+    }
+    return first;
+  };
+  auto release = [&](int first, bool own) {
+    if (own) {   // once its MMAs are done
+      at_commit(&sh.empty[first], one);
+      if constexpr (C::kParts == 2) at_commit(&sh.empty[second], one);
+    } else if (one) {
+      mbar_arrive(&sh.empty[first]);
+      if constexpr (C::kParts == 2) mbar_arrive(&sh.empty[second]);
     }
   };
-  auto release = [&](uint32_t at) {
-    if (lane == 0)
-      for (int i = 0; i < C::kParts; ++i) tc_commit(&sh.empty[(at + i) % NS]);
+  auto fences = [&]() {
+    if constexpr (W::kPaged && !W::kF8) fence_proxy_async();   // written by cp.async
+    tc_fence_after();
   };
-  // O(tile t) += P(buffer) V, `keys` of the tile's keys, V in ring slots at, ...
-  auto pv = [&](int t, uint32_t buf, uint32_t at, int keys, bool first) {
-    if (lane == 0) {
-      constexpr int kSteps = N / 16, kPartSteps = kSteps / C::kParts;
-      const int steps = (keys + 15) >> 4;
+  // S(buffer) = Q K^T
+  auto qk = [&](uint32_t buf, int first) {
+    const uint64_t k0 = k_desc + first * (C::kSlotBytes >> 4), k1 = C::kParts == 2 ? k_desc + second * (C::kSlotBytes >> 4) : 0;
+#pragma unroll
+    for (int a = 0; a < C::kAtoms; ++a) {
+      const uint64_t kd = C::kParts == 1 ? k0 + (a * (N * 128) >> 4) : (a < 2 ? k0 : k1) + ((a & 1) * (N * 128) >> 4);
+      at_mma_ss4(tmem + buf * kAtBuf, q_desc + (a * C::kQAtom >> 4), kd, idesc_s, a > 0, one);
+    }
+    at_commit(&sh.s_full[buf], one);
+  };
+  // O += P(buffer) V, `keys` of the tile's keys
+  auto pv = [&](uint32_t buf, int first, int keys, bool fresh) {
+    constexpr int kSteps = N / 16, kPartSteps = kSteps / C::kParts;
+    const int steps = one ? (keys + 15) >> 4 : 0;
+    const uint64_t v0 = v_desc + first * (C::kSlotBytes >> 4), v1 = C::kParts == 2 ? v_desc + second * (C::kSlotBytes >> 4) : 0;
+    const uint32_t p = tmem + buf * kAtBuf;
+    if constexpr (kPartSteps % 4 == 0) {
 #pragma unroll
       for (int term = 0; term < W::kTerms; ++term)
 #pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk)
-          if (kk < steps) {
-            const uint32_t vb = slot_addr(at + kk / kPartSteps) + (kk % kPartSteps) * 2048;
-            const uint64_t bd = smem_desc(vb, kAtomBytes, 1024);
-            tc_mma_ts(tmem + C::kOCol + t * D, tmem + buf * kAtBuf + term * (N / 2) + kk * 8, bd, kIdescO,
-                      !(first && term == 0 && kk == 0));
-          }
-      tc_commit(&sh.pv_done[buf]);
+        for (int kk = 0; kk < kSteps; kk += 4)
+          at_mma_ts4(o_addr, p + term * (N / 2) + kk * 8, (kk < kPartSteps ? v0 : v1) + ((kk % kPartSteps) * 2048 >> 4),
+                     kIdescO, !(term == 0 && kk == 0 && fresh), steps - kk);
+    } else {   // two steps a slot (d = 256, 64 keys)
+#pragma unroll
+      for (int term = 0; term < W::kTerms; ++term)
+#pragma unroll
+        for (int kk = 0; kk < kSteps; kk += 2)
+          at_mma_ts4(o_addr, p + term * (N / 2) + kk * 8, kk < kPartSteps ? v0 : v1, kIdescO,
+                     !(term == 0 && kk == 0 && fresh), min(2, steps - kk));
     }
+    at_commit(&sh.pv_done[buf], one);
   };
-  // rows of V past the last key inside its 16-key step are zeroed: 0 x NaN would reach every row
-  auto clear_tail = [&](uint32_t at, int keys) {
+  // rows of V past the last key inside its 16-key step are zeroed: 0 x NaN would reach every row. (Both warps of a slot do,
+  // to the same effect.)
+  auto clear_tail = [&](int first, int keys) {
     if ((keys & 15) == 0) return;
     const int to = (keys + 15) & ~15;
     constexpr int kRows = N / C::kParts;
     for (int row = keys; row < to; ++row)
       for (int i = lane; i < D / 8; i += 32) {   // 16-byte pieces of the row: D / 64 atoms of 8
-        const uint32_t off = slot_addr(at + row / kRows) + (i >> 3) * kAtomBytes + (row % kRows) * 128 + (i & 7) * 16;
+        const uint32_t off = ring + (row < kRows ? first : second) * C::kSlotBytes + (i >> 3) * kAtomBytes +
+                             (row % kRows) * 128 + (i & 7) * 16;
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(off), "r"(0) : "memory");
       }
     fence_proxy_async();
     __syncwarp();
   };
-  // P of tile t (buffer buf) has been written, and O is free: PV may be issued
-  auto ready = [&](int t, uint32_t buf, uint32_t parity, bool first) -> bool {
-    if (first && units[t] > 0 && !at_warp_wait(&sh.o_free[t], (units[t] - 1) & 1u, ab)) return false;
-    if (!at_warp_wait(&sh.p_full[buf], parity, ab)) return false;
+  auto q_ready = [&](uint32_t k) -> bool {
+    if (!at_warp_wait(sh.q_full, k & 1u, ab)) return false;
     tc_fence_after();
     return true;
   };
   for (uint32_t k = 0; w.unit(k, u); ++k) {
-    if (!at_warp_wait(sh.q_full, k & 1u, ab)) return false;
-    const int n = T == 2 ? max(u.n[0], u.n[1]) : u.n[0];
-    if constexpr (T == 2) {
-      if (u.dual) {
-        auto next_k = [&](int t) -> bool {
-          if (!slot_wait(r)) return false;
-          tc_fence_after();
-          qk(t, t, r);
-          release(r);
-          ++r;
-          return true;
-        };
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (u.n[t] > 0 && !next_k(t)) return false;
-        if (n == 1 && lane == 0) tc_commit(sh.q_empty);
-        for (int j = 0; j < n; ++j) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (j < u.n[t]) {
-              if (!slot_wait(r)) return false;
-              const int keys = j + 1 < u.n[t] ? N : w.last_keys(u, t);
-              clear_tail(r, keys);
-              if (!ready(t, t, np[t] & 1u, j == 0)) return false;
-              ++np[t];
-              pv(t, t, r, keys, j == 0);
-              release(r);
-              ++r;
+    if (does_qk && !q_ready(k)) return false;
+    const int n0 = at_uniform(u.n[0]), n1 = T == 2 ? at_uniform(u.n[1]) : 0;
+    const int n = max(n0, n1), nt = t == 0 ? n0 : n1;
+    const bool dual = T == 2 && at_uniform(u.dual);
+    const int last = at_uniform(w.last_keys(u, t));
+    for (int j = -C::kAhead; j < n; ++j) {
+#pragma unroll 1
+      for (int o = 0; o < (dual ? 2 : 1); ++o) {   // dual: the other tile's slots too, in their order
+        const bool own = !dual || o == t;
+        const int no = dual ? (o == 0 ? n0 : n1) : n;
+        // PV of key tile j
+        if (j >= 0 && j < no) {
+          const int vs = acquire();
+          if (vs < 0) return false;
+          if (own && j < nt && does_pv) {
+            const uint32_t buf = T == 2 ? t : x & 1u;
+            const int keys = j + 1 < (dual ? nt : n) ? N : last;
+            clear_tail(vs, keys);
+            if (j == 0) {
+              if (o_used) {
+                if (!at_warp_wait(&sh.o_free[t], o_phase, ab)) return false;
+                o_phase ^= 1u;
+              }
+              o_used = true;
             }
-            if (j + 1 < u.n[t] && !next_k(t)) return false;
+            if (!at_warp_wait(&sh.p_full[buf], (p_phase >> buf) & 1u, ab)) return false;
+            p_phase ^= 1u << buf;
+            fences();
+            pv(buf, vs, keys, j == 0);
+            if (T == 1) ++x;
           }
-          if (j + 2 == n && lane == 0) tc_commit(sh.q_empty);
+          release(vs, own && does_pv);
         }
-      } else {
-        if (!slot_wait(r)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (u.n[t] > 0) qk(t, t, r);
-        release(r);
-        ++r;
-        if (n == 1 && lane == 0) tc_commit(sh.q_empty);
-        for (int j = 0; j < n; ++j) {
-          const uint32_t rv = r++;
-          const bool more = j + 1 < n;
-          const uint32_t rk = r;
-          if (more) ++r;
-          const int keys = more ? N : w.last_keys(u, 0);
-          bool have_v = false, have_k = false;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (j < u.n[t]) {
-              if (!have_v) {
-                if (!slot_wait(rv)) return false;
-                clear_tail(rv, keys);
-                have_v = true;
+        // QK^T of key tile j + kAhead
+        if (j + C::kAhead < no) {
+          const int ks = acquire();
+          if (ks < 0) return false;
+          if (own && j + C::kAhead < nt && does_qk) {
+            const uint32_t buf = T == 2 ? t : x & 1u;
+            if constexpr (T == 1) {   // the buffer's last PV is done (in the pipe of another warp)
+              if (x >= 2) {
+                if (!at_warp_wait(&sh.pv_done[buf], (s_phase >> buf) & 1u, ab)) return false;
+                s_phase ^= 1u << buf;
               }
-              if (!ready(t, t, np[t] & 1u, j == 0)) return false;
-              ++np[t];
-              pv(t, t, rv, keys, j == 0);
+              ++x;
             }
-            if (j + 1 < u.n[t]) {
-              if (!have_k) {
-                if (!slot_wait(rk)) return false;
-                tc_fence_after();
-                have_k = true;
-              }
-              qk(t, t, rk);
-            }
+            fences();
+            qk(buf, ks);
           }
-          release(rv);
-          if (more) {
-            release(rk);
-            if (j + 2 == n && lane == 0) tc_commit(sh.q_empty);
-          }
+          release(ks, own && does_qk);
         }
       }
-    } else {
-      auto issue_qk = [&](int j) -> bool {
-        const uint32_t at = r;
-        for (int i = 0; i < C::kParts; ++i)
-          if (!slot_wait(at + i)) return false;
-        r += C::kParts;
-        tc_fence_after();
-        qk(0, xs & 1u, at);
-        ++xs;
-        release(at);
-        if (j == n - 1 && lane == 0) tc_commit(sh.q_empty);
-        return true;
-      };
-      for (int j = 0; j < C::kAhead && j < n; ++j)
-        if (!issue_qk(j)) return false;
-      for (int j = 0; j < n; ++j) {
-        const uint32_t rv = r;
-        const int keys = j + 1 < n ? N : w.last_keys(u, 0);
-        for (int i = 0; i < C::kParts; ++i)
-          if (!slot_wait(rv + i)) return false;
-        r += C::kParts;
-        clear_tail(rv, keys);
-        const uint32_t buf = np[0] & 1u;
-        if (!ready(0, buf, (np[0] >> 1) & 1u, j == 0)) return false;
-        ++np[0];
-        pv(0, buf, rv, keys, j == 0);
-        release(rv);
-        if (j + C::kAhead < n && !issue_qk(j + C::kAhead)) return false;
-      }
+      if (j + C::kAhead == n - 1 && does_qk) at_commit(sh.q_empty, one);
     }
-    for (int t = 0; t < T; ++t)
-      if (u.n[t] > 0) ++units[t];
   }
   return true;
 }
@@ -588,11 +614,46 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
 }
 
 // ---------------------------------------------------------------- a converting warp (E4M3 pools)
-// Codes of K and V tiles, [keys][D] as they are stored, to f16 in the ring's swizzled atoms. Warp `half` takes every other
+// Codes of K and V tiles, [keys][D] as they are stored, to f16 in the ring's swizzled atoms. Warp `which` takes every fourth
 // group of 8 rows of a slot. Lane (rr, i) takes 16 codes of row rr, of atom (rr & 1) ^ s in turn s: the eight lanes that
 // access shared memory at a time then read 128 bytes of distinct banks, and write 16-byte chunks of distinct ones.
+// kRows rows and kAtoms atoms of a slot, this warp's quarter; 4 pieces of 16 codes are loaded before the first is converted
+// (one at a time, by two warps, a slot of 128 rows took 1.3 us).
+template <int D, int kRows, int kAtoms>
+__device__ __forceinline__ void convert_slot(const char* src, char* dst, int which, int rr, int i) {
+  constexpr int kSides = kAtoms > 1 ? 2 : 1;
+  constexpr int kItems = kRows / 32 * kAtoms;   // a warp's pieces of a lane: (group of 8 rows, pair of atoms, side)
+  constexpr int kBatch = kItems < 4 ? kItems : 4;
+  const uint32_t from = smem_u32(src) + (which * 8 + rr) * D + i * 16;
+  const uint32_t to = smem_u32(dst) + (which * 8 + rr) * 128;
+  const uint32_t c0 = ((2 * i) ^ rr) << 4, c1 = ((2 * i + 1) ^ rr) << 4;
+#pragma unroll 1
+  for (int b = 0; b < kItems; b += kBatch) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int item = b + e, g = item / kAtoms, y = item % kAtoms;
+      const int atom = kSides == 2 ? (y & ~1) + ((rr & 1) ^ (y & 1)) : 0;
+      v[e] = lds128(from + g * (32 * D) + atom * 64);
+    }
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int item = b + e, g = item / kAtoms, y = item % kAtoms;
+      const int atom = kSides == 2 ? (y & ~1) + ((rr & 1) ^ (y & 1)) : 0;
+      uint4 lo, hi;
+      e4m3x4_to_f16x4(v[e].x, lo.x, lo.y);
+      e4m3x4_to_f16x4(v[e].y, lo.z, lo.w);
+      e4m3x4_to_f16x4(v[e].z, hi.x, hi.y);
+      e4m3x4_to_f16x4(v[e].w, hi.z, hi.w);
+      const uint32_t at = to + atom * (kRows * 128) + g * 4096;
+      sts128(at + c0, lo);
+      sts128(at + c1, hi);
+    }
+  }
+}
+
 template <class W, class C, int D>
-__device__ __forceinline__ bool attn_convert(W& w, const AttnShared<C>& sh, int half) {
+__device__ __forceinline__ bool attn_convert(W& w, const AttnShared<C>& sh, int which) {
   constexpr int NS = C::kSlots, N = W::kN;
   const int lane = threadIdx.x & 31;
   const int rr = lane >> 2, i = lane & 3;
@@ -606,31 +667,10 @@ __device__ __forceinline__ bool attn_convert(W& w, const AttnShared<C>& sh, int 
         if (r >= NS && !at_warp_wait(&sh.empty[r % NS], (r / NS - 1) & 1u, sh.abort_flag)) return false;
         char* dst = sh.ring + (r % NS) * C::kSlotBytes;
         // the part's rows and atoms: at d = 256 two atoms of every row of K, half of V's rows
-        const int rows = C::kParts == 2 && is_v ? N / 2 : N;
-        constexpr int kAtomsK = C::kParts == 2 ? 2 : C::kAtoms;
-        const int atoms = C::kParts == 2 && is_v ? C::kAtoms : kAtomsK;
+        const bool half_v = C::kParts == 2 && is_v;
         const char* src = raw + (C::kParts == 2 && part ? (is_v ? N / 2 * D : 128) : 0);
-#pragma unroll 2
-        for (int r0 = half * 8; r0 < rows; r0 += 16) {
-          const int row = r0 + rr;
-#pragma unroll
-          for (int a0 = 0; a0 < C::kAtoms; a0 += 2) {
-            if (a0 >= atoms) break;
-#pragma unroll
-            for (int s = 0; s < (C::kAtoms > 1 ? 2 : 1); ++s) {
-              const int atom = C::kAtoms > 1 ? a0 + ((rr & 1) ^ s) : 0;
-              const uint4 v = *reinterpret_cast<const uint4*>(src + row * D + atom * 64 + i * 16);
-              uint4 lo, hi;
-              e4m3x4_to_f16x4(v.x, lo.x, lo.y);
-              e4m3x4_to_f16x4(v.y, lo.z, lo.w);
-              e4m3x4_to_f16x4(v.z, hi.x, hi.y);
-              e4m3x4_to_f16x4(v.w, hi.z, hi.w);
-              char* to = dst + atom * (rows * 128) + row * 128;
-              *reinterpret_cast<uint4*>(to + (((2 * i) ^ (row & 7)) << 4)) = lo;
-              *reinterpret_cast<uint4*>(to + (((2 * i + 1) ^ (row & 7)) << 4)) = hi;
-            }
-          }
-        }
+        if (half_v) convert_slot<D, N / 2, C::kAtoms>(src, dst, which, rr, i);
+        else convert_slot<D, N, (C::kParts == 2 ? 2 : C::kAtoms)>(src, dst, which, rr, i);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.full[r % NS]);
@@ -648,6 +688,7 @@ template <class W, int D>
 __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_constant__ typename W::Params params) {
   using C = AttnCfg<D, W::kN, W::kF8>;
   constexpr int NS = C::kSlots;
+  constexpr bool kCopies = W::kPaged && !W::kF8;   // warps 12-15 load K and V (else warp 8)
   extern __shared__ __align__(256) char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   AttnShared<C> sh;
@@ -669,19 +710,19 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   sh.tmem_slot = reinterpret_cast<uint32_t*>(sh.q_full + 11) + 1;
   sh.x_bar = reinterpret_cast<uint64_t*>(smem + C::kXOff) - 4;   // d = 256 (whose ring is short): behind them
   sh.xbuf = reinterpret_cast<float*>(smem + C::kXOff);
-  static_assert(C::kTiles == 2 || (2 * NS + 2 * C::kRaws + 16) * 8 <= 256, "barrier area");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  static_assert(C::kTiles == 2 || (2 * NS + 2 * C::kRaws + 16) * 8 <= C::kBarBytes, "barrier area");
+  const int warp = at_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.full[i], W::kF8 ? 2 : 1);
-      mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.full[i], W::kF8 ? kAtCopyWarps : (W::kPaged ? 32 * kAtCopyWarps : 1));
+      mbar_init(&sh.empty[i], 2);
     }
     for (int i = 0; i < C::kRaws; ++i) {
-      mbar_init(&sh.raw_full[i], 1);
-      mbar_init(&sh.raw_empty[i], 2);
+      mbar_init(&sh.raw_full[i], 32);
+      mbar_init(&sh.raw_empty[i], kAtCopyWarps);
     }
     mbar_init(sh.q_full, W::kF8 ? 8 : 1);
-    mbar_init(sh.q_empty, 1);
+    mbar_init(sh.q_empty, C::kTiles);
     constexpr int kRowWarps = C::kTiles == 2 ? 4 : 8;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -689,7 +730,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.o_free[i], kRowWarps);
     }
-    mbar_init(sh.done, 1);
+    mbar_init(sh.done, 2);
     if constexpr (C::kTiles == 1)
       for (int i = 0; i < 4; ++i) mbar_init(&sh.x_bar[i], 2);
     *sh.abort_flag = 0;
@@ -702,7 +743,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sh.tmem_slot;
+  const uint32_t tmem = at_uniform(*sh.tmem_slot);
   // the inputs are written and visible from here on. (kWaitLate: they were before the grid ahead began, which this one
   // may run beside; the grid behind waits for both through this one)
   if constexpr (!W::kWaitLate) pdl_wait();
@@ -714,50 +755,59 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
     ok = attn_softmax<W, C, D>(w, sh, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
-    if (warp == 8) {
-      // ---- the loader: Q of each unit, then K and V in the order in which the MMA warp consumes them
+    if (warp == 8 || (kCopies && warp >= 12)) {
+      // ---- the loaders: Q of each unit, and K and V in the order in which the MMA warps consume them
       W w(params, lane);
       constexpr int kDepth = W::kF8 ? C::kRaws : NS, kPieces = W::kF8 ? 1 : C::kParts;
       constexpr int kBytes = W::kF8 ? C::kRawBytes : C::kSlotBytes;
       uint64_t* const full = W::kF8 ? sh.raw_full : sh.full;
       uint64_t* const empty = W::kF8 ? sh.raw_empty : sh.empty;
       char* const ring = W::kF8 ? sh.raw : sh.ring;
-      uint32_t r = 0, q_units = 0;
+      uint32_t r = 0, q_units = 0, phase = 1;   // (the first round finds every slot empty)
+      int slot = 0;
       AttnUnit u;
       for (uint32_t k = 0; ok && w.unit(k, u); ++k) {
-        if constexpr (!W::kF8) {   // (the softmax threads write an E4M3 pool's Q)
+        if (!W::kF8 && warp == 8) {   // (the softmax threads write an E4M3 pool's Q)
           if (k > 0) ok = at_warp_wait(sh.q_empty, (k - 1) & 1u, sh.abort_flag);
           if (!ok) break;
           w.template load_q<C>(u, sh.q_s, sh.q_full);
           ++q_units;
         }
+        if (kCopies && warp == 8) continue;
         ok = at_each_tile<C>(u, [&](bool is_v, int t, int j) -> bool {
+#pragma unroll 1
           for (int part = 0; part < kPieces; ++part, ++r) {
-            if (r >= kDepth && !at_warp_wait(&empty[r % kDepth], (r / kDepth - 1) & 1u, sh.abort_flag)) return false;
-            w.template load_kv<C>(u, is_v, t, j, part, ring + (r % kDepth) * kBytes, &full[r % kDepth]);
+            if (r >= kDepth && !at_warp_wait(&empty[slot], phase, sh.abort_flag)) return false;
+            w.template load_kv<C>(u, is_v, t, j, part, ring + slot * kBytes, &full[slot], warp - 12);
+            if (++slot == kDepth) {
+              slot = 0;
+              phase ^= 1u;
+            }
           }
           return true;
         });
       }
       if (!ok) *sh.abort_flag = 1;
       // the copies issued last have landed before the CTA can exit
+      if constexpr (W::kPaged) cp_async_wait_all();
       if (lane == 0) {
         for (uint32_t i = r > kDepth ? r - kDepth : 0; i < r; ++i) mbar_wait(&full[i % kDepth], (i / kDepth) & 1u, 100000000ull);
         if (q_units > 0) mbar_wait(sh.q_full, (q_units - 1) & 1u, 100000000ull);
       }
       __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 9 || warp == 10) {
       W w(params, lane);
-      ok = attn_mma<W, C, D>(w, sh, tmem);
+      ok = attn_mma<W, C, D>(w, sh, tmem, warp - 9);
       if (!ok) *sh.abort_flag = 1;
-      if (lane == 0) {   // every MMA of this CTA has completed before the TMEM is released
-        tc_commit(sh.done);
-        mbar_wait(sh.done, 0, 100000000ull);
-      }
+      // every MMA of this CTA has completed before the TMEM is released
+      at_commit(sh.done, lane == 0);
+      mbar_wait(sh.done, 0, 100000000ull);
       __syncwarp();
-    } else if constexpr (W::kF8) {
-      W w(params, lane);
-      ok = attn_convert<W, C, D>(w, sh, warp - 10);
+    } else if (W::kF8 && warp >= 12) {
+      if constexpr (W::kF8) {
+        W w(params, lane);
+        ok = attn_convert<W, C, D>(w, sh, warp - 12);
+      }
     }
   }
   if (!ok) {

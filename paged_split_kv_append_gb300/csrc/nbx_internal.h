@@ -368,7 +368,7 @@ struct SharedLayout {
 };
 bool shared_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len, int n_groups, SharedLayout* out);
 // Whether prefixes are read apart for these formats; elsewhere a call is a decode that ignores its groups.
-bool prefix_path_applies(const DecodeParams& p, int q_dtype, int pool_dtype);
+bool prefix_path_applies(int q_dtype, int pool_dtype);
 cudaError_t shared_dispatch(const SharedParams& s, const DecodeParams& p, int q_dtype, int pool_dtype, int grid_limit,
                             cudaStream_t stream);
 

@@ -137,7 +137,8 @@ struct PromptWork {
           tma_load_3d(q_s + t * C::kQTile + a * C::kQAtom, &p.q, a * 64, u.head, u.tok + t * tpt, bar);
   }
   template <class>
-  __device__ __forceinline__ void load_kv(const AttnUnit& u, bool is_v, int, int j, int part, char* dst, uint64_t* bar) const {
+  __device__ __forceinline__ void load_kv(const AttnUnit& u, bool is_v, int, int j, int part, char* dst, uint64_t* bar,
+                                          int) const {
     if ((threadIdx.x & 31) != 0) return;
     mbar_arrive_expect_tx(bar, C::kSlotBytes);
     const int row = u.kv[0] + j * kN;

@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cmath>
 #include <limits>
+#include <type_traits>
 
 #include "attn_tiles.cuh"
 
@@ -22,14 +23,12 @@ constexpr int kPrefixSplits = 32;      // most splits of a prefix
 
 struct PrefixParams {
   CUtensorMap q;      // [batch * rows][h_q][d], box {64, heads, tokens of a tile}
-  CUtensorMap k, v;   // pools as rows of d, box {64, positions}
   SharedParams s;
   DecodeParams a;
   float c;            // |scale * k_scale| log2 e
   int negative;
   int32_t* status;
   int heads, sets;    // query heads of a tile; h_q / heads
-  int box;            // positions of a copy: gcd(page_tokens, keys of a tile)
 };
 
 // Query heads of one tile: the whole group, if it fits, so that few sequences fill few tiles.
@@ -46,93 +45,111 @@ struct PlanArgs {
   int tpt, tiles; // tokens of a tile; tiles of a prefix unit
   int sets;       // head sets
   int sms;
+  bool small;     // its arrays lie in shared memory
   // its query vectors fill one M tile of the two, which then take splits of their own
   __device__ __forceinline__ bool dual(const PrefixGroup& g) const { return tiles == 2 && g.n * a.rows <= tpt; }
 };
 
-__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
+constexpr int kPlanBatch = 2048, kPlanGroups = 512;   // up to these the plan works in shared memory
+inline bool plan_small(int batch, int n_groups) { return batch <= kPlanBatch && n_groups <= kPlanGroups; }
+inline size_t plan_smem(int batch, int n_groups) {
+  return plan_small(batch, n_groups) ? static_cast<size_t>(n_groups) * sizeof(PrefixGroup) + static_cast<size_t>(batch) * 12 : 0;
+}
+
+// One CTA. What it reads (lengths, groups) it reads once, all at a time: a chain of dependent reads from global memory took
+// 7.5 us of a call. (Larger batches keep their arrays in the workspace, and read lengths again.)
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_constant__ PlanArgs x) {
+  extern __shared__ __align__(16) char plan_sm[];
   const SharedParams& s = x.s;
   const DecodeParams& p = x.a;
-  __shared__ long long s_prefix, s_own;
-  __shared__ int s_ok, s_empty, s_base, s_warp[kPlanThreads / 32];
+  __shared__ unsigned long long s_prefix, s_own;
+  __shared__ int s_ok, s_empty, s_warp[kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kPlanThreads / 32;
-  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_tokens;
+  PrefixGroup* const groups = x.small ? reinterpret_cast<PrefixGroup*>(plan_sm) : s.groups;
+  int2* const seqs = x.small ? reinterpret_cast<int2*>(plan_sm + s.n_groups * sizeof(PrefixGroup)) : s.seqs;
+  int* const lens = reinterpret_cast<int*>(seqs + p.batch);   // small only
+  const int64_t cap = min(static_cast<int64_t>(p.max_pages) * p.page_tokens, static_cast<int64_t>(p.max_seq_len));
   if (tid == 0) {
     s_prefix = s_own = 0;
     s_ok = 1;
-    s_empty = s_base = 0;
+    s_empty = 0;
   }
   pdl_wait();
   pdl_launch_dependents();
   __syncthreads();
-  auto len_of = [&](int b, bool report) -> int {
+  // ---- the lengths and the groups as they are given
+  bool bad_len = false;
+  for (int b = tid; b < p.batch; b += kPlanThreads) {
     const int L = p.seq_lens[b];
-    if (L >= 0 && L <= p.max_seq_len && L <= cap) return L;
-    if (report) raise_status(p.status, NBX_DEV_BAD_LEN);
-    return 0;
-  };
-  // ---- what each group shares
-  for (int g = tid; g < s.n_groups; g += kPlanThreads) {
-    const int b0 = s.group_start[g], b1 = s.group_start[g + 1];
-    if (b0 < 0 || b1 < b0 || b1 > p.batch || s.shared_lens[g] < 0) s_ok = 0;   // no group counts then
+    bad_len |= L < 0 || L > cap;
+    seqs[b] = make_int2(0, 0);
+    if (x.small) lens[b] = L < 0 || L > cap ? 0 : L;
   }
-  for (int b = tid; b < p.batch; b += kPlanThreads) s.seqs[b] = make_int2(0, 0);
+  for (int g = tid; g < s.n_groups; g += kPlanThreads) {
+    const int b0 = s.group_start[g], b1 = s.group_start[g + 1], n = s.shared_lens[g];
+    if (b0 < 0 || b1 < b0 || b1 > p.batch || n < 0) s_ok = 0;   // no group counts then
+    groups[g] = PrefixGroup{b0, b1 - b0, n, 0, 0, 0, 0, 0};
+  }
+  if (bad_len) raise_status(p.status, NBX_DEV_BAD_LEN);
   __syncthreads();
+  auto len_of = [&](int b) -> int {
+    if (x.small) return lens[b];
+    const int L = p.seq_lens[b];
+    return L < 0 || L > cap ? 0 : L;
+  };
   if (tid == 0 && !s_ok) raise_status(p.status, NBX_DEV_BAD_ROW);
+  // ---- what each group shares: what every row of every member that holds something sees
   for (int g = warp; g < s.n_groups; g += kWarps) {
-    const int b0 = s.group_start[g], n = s_ok ? s.group_start[g + 1] - b0 : 0;
-    // every row of every member that holds something sees the prefix whole
-    int least = s.shared_lens[g], live = 0, row = p.batch;
-    for (int i = lane; i < n; i += 32) {
-      const int L = len_of(b0 + i, false);
+    PrefixGroup pg = groups[g];
+    if (!s_ok) pg.n = 0;
+    int least = pg.eff, live = 0, row = p.batch;
+    for (int i = lane; i < pg.n; i += 32) {
+      const int L = len_of(pg.b0 + i);
       if (L > 0) {
         ++live;
-        row = min(row, b0 + i);
+        row = min(row, pg.b0 + i);
         least = min(least, L - p.rows + 1);
       }
     }
     live = __reduce_add_sync(0xffffffffu, live);
     row = __reduce_min_sync(0xffffffffu, row);
     least = __reduce_min_sync(0xffffffffu, least);
-    const int eff = live >= 2 && least >= kLeastPrefix ? least / p.page_tokens * p.page_tokens : 0;
+    pg.eff = live >= 2 && least >= kLeastPrefix ? least / p.page_tokens * p.page_tokens : 0;
+    pg.row = row;
+    const int tpu = x.tpt * x.tiles;
+    pg.pairs = (pg.n * p.rows + tpu - 1) / tpu;
     if (lane == 0) {
-      const int tpu = x.tpt * x.tiles, pairs = (n * p.rows + tpu - 1) / tpu;
-      PrefixGroup pg = {b0, n, eff, 0, 0, pairs, 0, row};
-      s.groups[g] = pg;
+      groups[g] = pg;
       // (a dual unit works through two splits in the time of one)
-      if (eff > 0)
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s_prefix),
-                  static_cast<unsigned long long>(eff) * pairs * x.sets * (x.dual(pg) ? 1 : 2));
+      if (pg.eff > 0) atomicAdd(&s_prefix, static_cast<unsigned long long>(pg.eff) * pg.pairs * x.sets * (x.dual(pg) ? 1 : 2));
     }
   }
   __syncthreads();
-  // ---- its splits: about one unit an SM in all, and not below 256 positions
+  // ---- its splits: about one unit an SM in all, and not below 256 positions (a dual unit's: 128)
   for (int g = warp; g < s.n_groups; g += kWarps) {
-    const PrefixGroup pg = s.groups[g];
+    PrefixGroup pg = groups[g];
     if (pg.eff == 0) continue;
-    const long long want = (2ll * x.sms * pg.eff + s_prefix / 2) / s_prefix;
+    const unsigned long long want = (2ull * x.sms * pg.eff + s_prefix / 2) / s_prefix;
     const int least = x.dual(pg) ? 128 : 256;
     const int most = min(min(kPrefixSplits, p.max_splits / 2), (pg.eff + least - 1) / least);
-    const int n = static_cast<int>(want < 1 ? 1 : (want > most ? most : want));
-    const int seg = ((pg.eff + n - 1) / n + 127) / 128 * 128;
-    const int splits = (pg.eff + seg - 1) / seg;
+    const int n = want < 1 ? 1 : (want > most ? most : static_cast<int>(want));
+    pg.seg = ((pg.eff + n - 1) / n + 127) / 128 * 128;
+    pg.splits = (pg.eff + pg.seg - 1) / pg.seg;
     for (int i = lane; i < pg.n; i += 32)
-      if (len_of(pg.b0 + i, false) > 0) s.seqs[pg.b0 + i] = make_int2(pg.eff, splits);
-    if (lane == 0) {
-      s.groups[g].seg = seg;
-      s.groups[g].splits = splits;
-    }
+      if (len_of(pg.b0 + i) > 0) seqs[pg.b0 + i] = make_int2(pg.eff, pg.splits);
+    if (lane == 0) groups[g] = pg;
   }
   __syncthreads();
-  // ---- the prefixes' work list: each group's first unit
+  // ---- each group's first work unit
   if (warp == 0) {
     int base = 0;
     for (int g0 = 0; g0 < s.n_groups; g0 += 32) {
       const int g = g0 + lane;
+      PrefixGroup pg = {};
       int units = 0;
       if (g < s.n_groups) {
-        const PrefixGroup pg = s.groups[g];
+        pg = groups[g];
         units = (x.dual(pg) ? (pg.splits + 1) / 2 : pg.splits) * pg.pairs * x.sets;
       }
       int sum = units;
@@ -140,39 +157,41 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
         const int y = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += y;
       }
-      if (g < s.n_groups) s.groups[g].unit = base + sum - units;
+      if (g < s.n_groups) {
+        pg.unit = base + sum - units;
+        s.groups[g] = pg;
+      }
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
     if (lane == 0) p.header[4] = base;
   }
-  // ---- the positions of each one's own
-  long long part = 0;
-  for (int b = tid; b < p.batch; b += kPlanThreads) {
-    const int L = len_of(b, true);
-    part += L - min(L, s.seqs[b].x);
-  }
+  // ---- the positions of each one's own, and their splits
+  unsigned long long part = 0;
+  for (int b = tid; b < p.batch; b += kPlanThreads) part += len_of(b) - seqs[b].x;
   for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-  if (lane == 0 && part) atomicAdd(reinterpret_cast<unsigned long long*>(&s_own), static_cast<unsigned long long>(part));
+  if (lane == 0 && part) atomicAdd(&s_own, part);
   __syncthreads();
   const int align = p.page_tokens <= NBX_SPLIT_POSITIONS ? p.page_tokens : NBX_SPLIT_POSITIONS;
-  for (int b00 = 0; b00 < p.batch; b00 += kPlanThreads) {
-    const int b = b00 + tid;
+  int total = 0;   // entries so far
+  for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
     int n = 0, seg = 1, L = 0;
     int2 sh = make_int2(0, 0);
     if (b < p.batch) {
-      L = len_of(b, false);
-      sh = s.seqs[b];
+      L = len_of(b);
+      sh = seqs[b];
       const int own = L - sh.x;
       if (own > 0) {
-        const long long num = static_cast<long long>(p.tc_units) * own, den = static_cast<long long>(p.tc_pairs) * s_own;
-        const long long want = (num + den - 1) / den;
+        const unsigned long long num = static_cast<unsigned long long>(p.tc_units) * own, den = p.tc_pairs * s_own;
+        const unsigned long long want = (num + den - 1) / den;
         const int most = min(p.max_splits - sh.y, max(1, own / 64));
-        const int S = static_cast<int>(want < 1 ? 1 : (want > most ? most : want));
+        const int S = want < 1 ? 1 : (want > most ? most : static_cast<int>(want));
         seg = (own + S - 1) / S;
         seg = (seg + align - 1) / align * align;
         n = (own + seg - 1) / seg;
       }
       p.plan[b] = SeqPlan{L, seg, sh.y + n, sh.x};
+      if (x.small) s.seqs[b] = sh;
       if (sh.y + n == 0) s_empty = 1;
     }
     int sum = n;
@@ -182,26 +201,20 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
     }
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
-    int base = s_base;
-    for (int w = 0; w < warp; ++w) base += s_warp[w];
-    base += sum - n;
-    for (int i = 0; i < n; ++i) {
-      Entry e;
-      e.b = b;
-      e.s = sh.y + i;
-      e.start = sh.x + i * seg;
-      e.end = min(L, sh.x + (i + 1) * seg);
-      e.len = L;
-      e.n_splits = sh.y + n;
-      e.pad0 = e.pad1 = 0;
-      p.entries[base + i] = e;
+    int base = total + sum - n;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) base += s_warp[w];
+      total += s_warp[w];
     }
-    __syncthreads();
-    if (tid == kPlanThreads - 1) s_base = base + n;
+    for (int i = 0; i < n; ++i) {
+      int4* const e = reinterpret_cast<int4*>(p.entries + base + i);
+      e[0] = make_int4(b, sh.y + i, sh.x + i * seg, min(L, sh.x + (i + 1) * seg));
+      e[1] = make_int4(L, sh.y + n, 0, 0);
+    }
     __syncthreads();
   }
   if (tid == 0) {
-    p.header[0] = s_base;
+    p.header[0] = total;
     p.header[1] = 0;
     p.header[2] = kMergeSplits;
     p.header[3] = 0;
@@ -209,7 +222,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
   if (s_empty) {   // a sequence with no position to read: its rows are 0
     const int64_t vec4 = static_cast<int64_t>(p.rows) * p.h_q * p.d / (p.out_bf16 ? 8 : 4);
     for (int b = 0; b < p.batch; ++b) {
-      if (p.plan[b].n_splits != 0) continue;
+      if (len_of(b) != 0) continue;
       float4* o = reinterpret_cast<float4*>(p.out) + b * vec4;
       for (int64_t i = tid; i < vec4; i += kPlanThreads) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -220,7 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(PlanArgs x) {
 template <int D, bool kE4, int kTermsOfP>
 struct PrefixWork {
   using Params = PrefixParams;
-  static constexpr int kN = kTermsOfP == 3 ? 64 : 128;   // keys of a tile
+  static constexpr int kN = kTermsOfP == 3 || (kE4 && D == 256) ? 64 : 128;   // keys of a tile
   static constexpr bool kF8 = kE4;
   static constexpr bool kPaged = true;
   static constexpr bool kWaitLate = true;
@@ -230,31 +243,51 @@ struct PrefixWork {
   // still lie there.
   const Params& p;
   int tpt, n_units;
-  int ids_next[2], ids[2];   // loader: pages of lane's box, of the next K tile and the last (of M tile t, or the last two)
-  int id_next;               // softmax: page of lane's 16-key piece of the next tile
+  int step_idx, step_off;    // a key tile further on: pages and positions
+  // Pieces of 16 positions, which no page splits: lane l < kN / 16 keeps track of piece l of a tile. The cursor is a tile
+  // ahead, its page id on the way; loaders keep the places of the last K tile (of M tile t; at d = 256 of the last two).
+  struct Cursor {
+    int idx, off, id;        // page of the row, position in it, page id
+  };
+  Cursor cur[2];
+  int64_t place[2];          // byte offset of the piece in a pool, or -1
 
   __device__ __forceinline__ int toks_per_tile() const { return tpt; }
   __device__ __forceinline__ int heads() const { return p.heads; }
   __device__ __forceinline__ PrefixWork(const Params& params, int) : p(params) {
     tpt = kAtM / p.heads;
     n_units = __ldcg(p.a.header + 4);
-    ids_next[0] = ids_next[1] = ids[0] = ids[1] = id_next = 0;
+    step_idx = kN / p.a.page_tokens;
+    step_off = kN - step_idx * p.a.page_tokens;
+    cur[0] = cur[1] = Cursor{0, 0, 0};
+    place[0] = place[1] = -1;
   }
   __device__ __forceinline__ bool unit(uint32_t round, AttnUnit& u) const {
     const int64_t place = static_cast<int64_t>(round) * gridDim.x + blockIdx.x;
     if (place >= n_units) return false;
     const int un = static_cast<int>(place), lane = threadIdx.x & 31;
     // the last group whose first unit is not behind this one (groups without units share theirs with the next)
-    int g = 0;
+    PrefixGroup pg = {};
     for (int g0 = 0; g0 < p.s.n_groups; g0 += 32) {
-      const bool at_or_before = g0 + lane < p.s.n_groups && __ldcg(&p.s.groups[g0 + lane].unit) <= un;
-      const uint32_t has = __ballot_sync(0xffffffffu, at_or_before);
+      int4 w0 = make_int4(0, 0, 0, 0), w1 = w0;
+      const bool there = g0 + lane < p.s.n_groups;
+      if (there) {
+        const int4* const g = reinterpret_cast<const int4*>(p.s.groups + g0 + lane);
+        w0 = __ldcg(g);
+        w1 = __ldcg(g + 1);
+      }
+      const uint32_t has = __ballot_sync(0xffffffffu, there && w1.z <= un);
       if (has == 0) break;
-      g = g0 + 31 - __clz(has);
+      const int src = 31 - __clz(has);
+      pg.b0 = __shfl_sync(0xffffffffu, w0.x, src);
+      pg.n = __shfl_sync(0xffffffffu, w0.y, src);
+      pg.eff = __shfl_sync(0xffffffffu, w0.z, src);
+      pg.seg = __shfl_sync(0xffffffffu, w0.w, src);
+      pg.splits = __shfl_sync(0xffffffffu, w1.x, src);
+      pg.pairs = __shfl_sync(0xffffffffu, w1.y, src);
+      pg.unit = __shfl_sync(0xffffffffu, w1.z, src);
+      pg.row = __shfl_sync(0xffffffffu, w1.w, src);
     }
-    const int4* const at_g = reinterpret_cast<const int4*>(p.s.groups + g);
-    const int4 w0 = __ldcg(at_g), w1 = __ldcg(at_g + 1);
-    const PrefixGroup pg = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
     const int rest = un - pg.unit;
     const int pair = rest % pg.pairs, which = rest / pg.pairs;
     const int set = which % p.sets, split = which / p.sets;
@@ -281,17 +314,31 @@ struct PrefixWork {
   }
   __device__ __forceinline__ int last_key(const AttnUnit& u, int t, int, bool) const { return u.end[t] - u.kv[t] - 1; }
   __device__ __forceinline__ bool in_pool(int page) const { return page >= 0 && page < p.a.num_pages; }
-  // the page of the 16 (or box) positions from `at` on; 0 past the end
-  __device__ __forceinline__ int page_at(const AttnUnit& u, int t, int at) const {
-    return at < u.end[t] ? __ldcg(p.a.block_table + static_cast<int64_t>(u.b) * p.a.max_pages + at / p.a.page_tokens) : 0;
+  __device__ __forceinline__ int page_id(const AttnUnit& u, int idx, bool there) const {
+    return there ? __ldcg(p.a.block_table + static_cast<int64_t>(u.b) * p.a.max_pages + idx) : 0;
+  }
+  // The cursor on the piece at position `at` (there: it is one of this lane's, before the end)
+  __device__ __forceinline__ void begin(Cursor& c, const AttnUnit& u, int at, bool there) const {
+    c.idx = at / p.a.page_tokens;
+    c.off = at - c.idx * p.a.page_tokens;
+    c.id = page_id(u, c.idx, there);
+  }
+  __device__ __forceinline__ void advance(Cursor& c, const AttnUnit& u, bool there) const {
+    c.idx += step_idx;
+    c.off += step_off;
+    if (c.off >= p.a.page_tokens) {
+      c.off -= p.a.page_tokens;
+      ++c.idx;
+    }
+    c.id = page_id(u, c.idx, there);
   }
   __device__ __forceinline__ uint32_t bad_keys(const AttnUnit& u, int t, int j, int c0) {
     constexpr int kPieces = (kPairs ? kN : kN / 2) / 16;
     const int lane = threadIdx.x & 31;
     const int at = u.kv[t] + j * kN + c0 + lane * 16;
-    if (j == 0) id_next = lane < kPieces ? page_at(u, t, at) : 0;
-    const int id = id_next;
-    id_next = lane < kPieces ? page_at(u, t, at + kN) : 0;
+    if (j == 0) begin(cur[0], u, at, lane < kPieces && at < u.end[t]);
+    const int id = cur[0].id;
+    advance(cur[0], u, lane < kPieces && at + kN < u.end[t]);
     return __ballot_sync(0xffffffffu, !in_pool(id));
   }
   __device__ __forceinline__ const __nv_bfloat16* q_row(const AttnUnit& u, int tok, int head) const {
@@ -310,66 +357,77 @@ struct PrefixWork {
         for (int a = 0; a < D / 64; ++a)
           tma_load_3d(q_s + t * C::kQTile + a * C::kQAtom, &p.q, a * 64, u.head, u.tok + (u.dual ? 0 : t * tpt), bar);
   }
-  // Lane l copies a box of positions (bf16: by 64 columns); page ids are fetched a tile ahead.
+  // K tile j of M tile t is next: where its pieces lie, and the cursor a tile further on. Returns the places.
+  __device__ __forceinline__ int64_t next_places(Cursor& c, const AttnUnit& u, int t, int j, bool reports) const {
+    constexpr int kElt = kF8 ? 1 : 2;
+    const int lane = threadIdx.x & 31;
+    const int at = u.kv[t] + j * kN + lane * 16;
+    const bool mine = lane < kN / 16 && at < u.end[t];
+    if (j == 0) begin(c, u, at, mine);
+    const bool held = in_pool(c.id);
+    if (reports && mine && !held) raise_status(p.status, NBX_DEV_BAD_PAGE);
+    const int64_t row = (static_cast<int64_t>(c.id) * p.a.h_kv + u.kvh) * p.a.page_tokens + c.off;
+    advance(c, u, lane < kN / 16 && at + kN < u.end[t]);
+    return held ? row * (D * kElt) : -1;
+  }
+  // This warp's part of a slot, or of a tile of codes, 16 bytes a lane: every piece is one run of bytes.
   template <class C>
-  __device__ __forceinline__ void load_kv(const AttnUnit& u, bool is_v, int t, int j, int part, char* dst, uint64_t* bar) {
-    const int lane = threadIdx.x & 31, box = p.box;
-    const int boxes = kN / box;
-    const int tile = u.kv[t] + j * kN;
-    int id;
+  __device__ __forceinline__ void load_kv(const AttnUnit& u, bool is_v, int t, int j, int part, char* dst, uint64_t* bar,
+                                          int loader) {
+    constexpr int kPieces = kN / 16;
+    const int lane = threadIdx.x & 31;
+    int64_t at;
     if constexpr (kPairs) {   // V of a tile follows its K before the next K of the same M tile
       if (!is_v) {
-        const int at = tile + lane * box;
-        const int now = j == 0 ? (lane < boxes ? page_at(u, t, at) : 0) : ids_next[t];
-        const int next = lane < boxes ? page_at(u, t, at + kN) : 0;
-        if (t == 0) ids[0] = now, ids_next[0] = next;
-        else ids[1] = now, ids_next[1] = next;
-        if (lane < boxes && at < u.end[t] && !in_pool(now)) raise_status(p.status, NBX_DEV_BAD_PAGE);
+        if (t == 0) place[0] = next_places(cur[0], u, t, j, loader <= 0);
+        else place[1] = next_places(cur[1], u, t, j, loader <= 0);
       }
-      id = t == 0 ? ids[0] : ids[1];
+      at = t == 0 ? place[0] : place[1];
     } else {                  // K runs two tiles ahead of V, but for a unit's last
       if (!is_v && part == 0) {
-        const int at = tile + lane * box;
-        ids[1] = ids[0];
-        ids[0] = j == 0 ? (lane < boxes ? page_at(u, t, at) : 0) : ids_next[0];
-        ids_next[0] = lane < boxes ? page_at(u, t, at + kN) : 0;
-        if (lane < boxes && at < u.end[t] && !in_pool(ids[0])) raise_status(p.status, NBX_DEV_BAD_PAGE);
+        place[1] = place[0];
+        place[0] = next_places(cur[0], u, t, j, loader <= 0);
       }
-      id = is_v && j + 1 < u.n[0] ? ids[1] : ids[0];
+      at = is_v && j + 1 < u.n[0] ? place[1] : place[0];
     }
-    if constexpr (kF8) {      // the codes as they are stored: a box of a head is one run of bytes
-      const int at = tile + lane * box;
-      const bool mine = lane < boxes && at < u.end[t], held = mine && in_pool(id);
-      if (mine && !held) {    // 0 x whatever lay here must not be a NaN
-        for (int i = 0; i < box * D; i += 16) *reinterpret_cast<uint4*>(dst + lane * box * D + i) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async();  // a copy may fill the place next time
+    const char* const pool = static_cast<const char*>(is_v ? p.a.v_pool : p.a.k_pool);
+    const int held = min(kPieces, (u.end[t] - u.kv[t] - j * kN + 15) >> 4);   // pieces of the tile before the end
+    if constexpr (kF8) {      // the codes as they are stored
+      const uint32_t to = smem_u32(dst) + lane * 16;
+      const char* const from = pool + lane * 16;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int64_t o = __shfl_sync(0xffffffffu, at, i);
+        if (i >= held) break;
+#pragma unroll
+        for (int x = 0; x < 16 * D; x += 512) cp_async16_zfill(to + i * 16 * D + x, from + (o < 0 ? 0 : o) + x, o >= 0);
       }
-      const uint32_t copies = __popc(__ballot_sync(0xffffffffu, held));
-      if (lane == 0) mbar_arrive_expect_tx(bar, copies * box * D);
-      __syncwarp();
-      if (held) {
-        const char* pool = static_cast<const char*>(is_v ? p.a.v_pool : p.a.k_pool);
-        const int64_t row = (static_cast<int64_t>(id) * p.a.h_kv + u.kvh) * p.a.page_tokens + at % p.a.page_tokens;
-        bulk_g2s(dst + lane * box * D, pool + row * D, box * D, bar);
-      }
+    } else if constexpr (C::kParts == 2) {
+      if (is_v) copy_pieces<32, kPieces / 2, kN * 64>(at, part * (kPieces / 2), held, dst, pool, loader);
+      else copy_pieces<16, kPieces, kN * 128>(at, 0, held, dst, pool + part * 256, loader);
     } else {
-      const bool half_v = C::kParts == 2 && is_v;                        // half of V's keys
-      const int vbox = half_v && box > kN / 2 ? kN / 2 : box;            // (V has a map of its own for such boxes)
-      const int atoms = C::kParts == 1 || is_v ? C::kAtoms : 2;          // columns of this slot
-      const int here = (half_v ? kN / 2 : kN) / vbox;                    // boxes of this slot
-      const int atom = lane / here, b = lane - atom * here;
-      const int off = (half_v && part ? kN / 2 : 0) + b * vbox;          // in the tile
-      const int at = tile + off;
-      const int page = __shfl_sync(0xffffffffu, id, (off / box) & 31);
-      const bool mine = atom < atoms && at < u.end[t];
-      const uint32_t copies = __popc(__ballot_sync(0xffffffffu, mine));
-      if (lane == 0) mbar_arrive_expect_tx(bar, copies * vbox * 128);
-      __syncwarp();
-      if (mine) {   // a page outside the pool: rows before the tensor, which read as zeros
-        const int row = in_pool(page) ? (page * p.a.h_kv + u.kvh) * p.a.page_tokens + at % p.a.page_tokens : -kN;
-        const int col = (C::kParts == 2 && !is_v ? part * 2 + atom : atom) * 64;
-        tma_load_2d(dst + atom * (half_v ? kN * 64 : kN * 128) + b * vbox * 128, is_v ? &p.v : &p.k, col, row, bar);
-      }
+      copy_pieces<D / 8, kPieces, kN * 128>(at, 0, held, dst, pool, loader);
+    }
+    cp_async_arrive_noinc(bar);
+  }
+  // Every fourth of kCount pieces from `first` on into a slot's swizzled atoms; kChunks 16-byte chunks of a row.
+  template <int kChunks, int kCount, int kAtomBytes>
+  __device__ __forceinline__ void copy_pieces(int64_t at, int first, int held, char* dst, const char* pool, int loader) const {
+    constexpr int kRows = 32 / kChunks;   // rows a warp copies at a time
+    const int lane = threadIdx.x & 31;
+    const int lr = lane / kChunks, lc = lane % kChunks;
+    const uint32_t to = smem_u32(dst) + (lc >> 3) * kAtomBytes + lr * 128 + (((lc & 7) ^ lr) << 4);
+    const char* const from = pool + lr * (D * 2) + lc * 16;
+#pragma unroll
+    for (int i0 = 0; i0 < kCount; i0 += kAtCopyWarps) {
+      const int i = i0 + loader;
+      const int64_t o = __shfl_sync(0xffffffffu, at, (first + i) & 31);
+      if (i >= kCount || first + i >= held) break;
+      const char* const src = from + (o < 0 ? 0 : o);
+      const uint32_t to_i = to + i * 2048;
+      // (rows x + lr of the piece: x and lr share no bit, so the swizzle of row x + lr is that of lr, times x)
+#pragma unroll
+      for (int x = 0; x < 16; x += kRows) cp_async16_zfill((to_i ^ ((x & 7) << 4)) + x * 128, src + x * (D * 2), o >= 0);
     }
   }
   template <int kCols>
@@ -478,49 +536,32 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(SharedPa
   }
 }
 
-bool encode_maps(PrefixParams* m, int pool_dtype, int tile_keys) {
-  const DecodeParams& a = m->a;
-  if (pool_dtype == NBX_E4M3) return true;   // queries by threads, codes by plain copies
-  const cuuint64_t d = static_cast<cuuint64_t>(a.d);
-  const cuuint64_t q_dims[3] = {d, static_cast<cuuint64_t>(a.h_q), static_cast<cuuint64_t>(a.batch) * a.rows};
-  const cuuint64_t q_str[2] = {d * 2, static_cast<cuuint64_t>(a.h_q) * d * 2};
-  const cuuint32_t q_box[3] = {64, static_cast<cuuint32_t>(m->heads), static_cast<cuuint32_t>(kAtM / m->heads)};
-  if (!at_encode(&m->q, 3, a.q, q_dims, q_str, q_box)) return false;
-  const cuuint64_t dims[2] = {d, static_cast<cuuint64_t>(a.num_pages) * a.h_kv * a.page_tokens};
-  const cuuint64_t str[1] = {d * 2};
-  const cuuint32_t k_box[2] = {64, static_cast<cuuint32_t>(m->box)};
-  const cuuint32_t v_box[2] = {64, static_cast<cuuint32_t>(a.d == 256 ? std::min(m->box, tile_keys / 2) : m->box)};
-  return at_encode(&m->k, 2, a.k_pool, dims, str, k_box) && at_encode(&m->v, 2, a.v_pool, dims, str, v_box);
-}
-
-// The maps of the last few calls from this host thread, keyed by everything they encode.
+// The query map of the last few calls from this host thread, keyed by everything it encodes.
 struct PrefixKey {
-  const void *q, *k, *v;
-  int rows, h_q, h_kv, d, num_pages, page_tokens, pool_dtype, tile_keys, device;
+  const void* q;
+  int tokens, h_q, d, heads, device;
   bool operator==(const PrefixKey& o) const {
-    return q == o.q && k == o.k && v == o.v && rows == o.rows && h_q == o.h_q && h_kv == o.h_kv && d == o.d &&
-           num_pages == o.num_pages && page_tokens == o.page_tokens && pool_dtype == o.pool_dtype && tile_keys == o.tile_keys &&
-           device == o.device;
+    return q == o.q && tokens == o.tokens && h_q == o.h_q && d == o.d && heads == o.heads && device == o.device;
   }
 };
 
-const PrefixParams* prefix_maps(const DecodeParams& a, int heads, int box, int pool_dtype, int tile_keys, int device) {
+const CUtensorMap* query_map(const DecodeParams& a, int heads, int device) {
   constexpr int kEntries = 8;
   thread_local PrefixKey keys[kEntries];
-  thread_local PrefixParams maps[kEntries];
+  thread_local CUtensorMap maps[kEntries];
   thread_local int used = 0, next = 0;
-  const PrefixKey key{a.q, a.k_pool, a.v_pool, a.batch * a.rows, a.h_q, a.h_kv, a.d, a.num_pages, a.page_tokens,
-                      pool_dtype, tile_keys, device};
+  const PrefixKey key{a.q, a.batch * a.rows, a.h_q, a.d, heads, device};
   for (int i = 0; i < used; ++i)
     if (keys[i] == key) return &maps[i];
   const int at = next;
   next = (next + 1) % kEntries;
   if (used < kEntries) ++used;
   keys[at] = PrefixKey{};   // not valid until encoded
-  maps[at].a = a;
-  maps[at].heads = heads;
-  maps[at].box = box;
-  if (!encode_maps(&maps[at], pool_dtype, tile_keys)) return nullptr;
+  const cuuint64_t d = static_cast<cuuint64_t>(a.d);
+  const cuuint64_t dims[3] = {d, static_cast<cuuint64_t>(a.h_q), static_cast<cuuint64_t>(a.batch) * a.rows};
+  const cuuint64_t strides[2] = {d * 2, static_cast<cuuint64_t>(a.h_q) * d * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(kAtM / heads)};
+  if (!at_encode(&maps[at], 3, a.q, dims, strides, box)) return nullptr;
   keys[at] = key;
   return &maps[at];
 }
@@ -530,11 +571,12 @@ cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, cudaStre
   using W = PrefixWork<D, kE4, kTerms>;
   const DeviceInfo& di = device_info();
   const int heads = prefix_heads(a.group);
-  int box = W::kN;
-  while (a.page_tokens % box) box >>= 1;
-  const PrefixParams* maps = prefix_maps(a, heads, box, kE4 ? NBX_E4M3 : NBX_BF16, W::kN, di.device);
-  if (maps == nullptr) return cudaErrorInvalidValue;
-  PrefixParams p = *maps;
+  PrefixParams p;
+  if (!kE4) {   // (the softmax threads write an E4M3 pool's Q)
+    const CUtensorMap* map = query_map(a, heads, di.device);
+    if (map == nullptr) return cudaErrorInvalidValue;
+    p.q = *map;
+  }
   p.s = s;
   p.a = a;
   p.status = a.status;
@@ -542,7 +584,6 @@ cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, cudaStre
   p.c = std::max(std::fabs(a.qk_scale_log2), std::numeric_limits<float>::denorm_min());
   p.heads = heads;
   p.sets = a.h_q / heads;
-  p.box = box;
   return launch_attn_tiles<W, D>(p, static_cast<unsigned>(di.sm_count), stream);
 }
 template <int D>
@@ -585,9 +626,8 @@ bool shared_layout(int batch, int rows, int h_q, int h_kv, int d, int max_seq_le
   return true;
 }
 
-bool prefix_path_applies(const DecodeParams& p, int q_dtype, int pool_dtype) {
-  const int64_t pool_rows = static_cast<int64_t>(p.num_pages) * p.h_kv * p.page_tokens;
-  return q_dtype == NBX_BF16 && (pool_dtype == NBX_E4M3 || (pool_dtype == NBX_BF16 && pool_rows < (int64_t{1} << 31) - 128));
+bool prefix_path_applies(int q_dtype, int pool_dtype) {
+  return q_dtype == NBX_BF16 && (pool_dtype == NBX_E4M3 || pool_dtype == NBX_BF16);
 }
 
 cudaError_t shared_dispatch(const SharedParams& s, const DecodeParams& p, int q_dtype, int pool_dtype, int grid_limit,
@@ -609,7 +649,8 @@ cudaError_t shared_dispatch(const SharedParams& s, const DecodeParams& p, int q_
   x.tiles = p.d <= 128 ? 2 : 1;
   x.sets = p.h_q / heads;
   x.sms = di.sm_count;
-  cudaError_t e = launch_pdl(shared_plan_kernel, 1u, kPlanThreads, 0, stream, x);
+  x.small = plan_small(p.batch, s.n_groups);
+  cudaError_t e = launch_pdl(shared_plan_kernel, 1u, kPlanThreads, plan_smem(p.batch, s.n_groups), stream, x);
   if (e != cudaSuccess) return e;
   e = pool_dtype == NBX_E4M3 ? decode_dispatch_warp_e4m3(q, q_dtype, grid_limit, stream)
                              : decode_dispatch_warp_bf16(q, grid_limit, stream);
