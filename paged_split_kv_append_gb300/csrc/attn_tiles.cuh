@@ -22,7 +22,7 @@
 //    V's keys); and the unit's Q tiles.
 //  * Paged K and V come by 16-byte cp.async of warps 12-15. (A tensor copy costs the copy engine some 135 ns whatever its
 //    size, and pages of 16 positions take 16 of 2 KB for 32 KB.)
-//  * E4M3 pools: warp 8 copies the codes of a tile as they are stored (cp.async), and warps 12-15 convert them to f16
+//  * E4M3 pools: warps 8 and 11 copy the codes of a tile as they are stored (cp.async), and warps 12-15 convert them to f16
 //    (exactly) into the ring. Queries enter as f16 too, times a power of two that brings the largest element of each
 //    vector into [2^14, 2^15): exact but for elements under 2^-29 of it. The softmax threads write them, each its own row,
 //    and take the factor back in their row's c. The running maximum sits 2^7 above P's largest weight then, so that small
@@ -75,7 +75,7 @@ struct AttnCfg {
   static constexpr uint32_t kOCol = 2 * kAtBuf;                  // S (and P) in columns [0, 256), O from there
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kSlots >= 3, "ring");
-  static_assert((2 * kSlots + 2 * kRaws + 12) * 8 <= kBarBytes, "barrier area");
+  static_assert((2 * kSlots + 2 * kRaws + 14) * 8 <= kBarBytes, "barrier area");
 };
 
 // One work unit.
@@ -202,6 +202,7 @@ struct AttnShared {
   uint64_t* p_full;    // [2] P over it
   uint64_t* pv_done;   // [2] the PV from that buffer is done: O holds it
   uint64_t* o_free;    // [2] the epilogue has read O of M tile t
+  uint64_t* turn;      // [2] d <= 128: it is the turn of M tile t's warp to issue
   uint64_t* done;
   uint64_t* raw_full;  // [kRaws] a tile's codes have landed
   uint64_t* raw_empty; // [kRaws] and are converted
@@ -272,7 +273,8 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
   uint32_t p_phase = 0, s_phase = 0; // bit: phase of a P buffer; d = 256: of the PV that frees an S buffer
   uint32_t o_phase = 0;
   bool o_used = false;               // O has been used
-  uint32_t x = 0;                    // key tiles of this M tile so far (d = 256: its buffer is bit 0)
+  uint32_t x = 0;                    // d = 256: key tiles so far (the buffer is bit 0)
+  uint32_t steps = 0;                // turns so far
   AttnUnit u;
   // The slots of the next tile (C::kParts of them, in a row but for the ring's end): the first, or -1. Both warps wait for
   // every slot, their own or not, and both give it back: a parity wait must know the phase before to be over, and the one
@@ -291,13 +293,13 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
     }
     return first;
   };
-  auto release = [&](int first, bool own) {
+  auto release = [&](int first, int next, bool own) {
     if (own) {   // once its MMAs are done
       at_commit(&sh.empty[first], one);
-      if constexpr (C::kParts == 2) at_commit(&sh.empty[second], one);
+      if constexpr (C::kParts == 2) at_commit(&sh.empty[next], one);
     } else if (one) {
       mbar_arrive(&sh.empty[first]);
-      if constexpr (C::kParts == 2) mbar_arrive(&sh.empty[second]);
+      if constexpr (C::kParts == 2) mbar_arrive(&sh.empty[next]);
     }
   };
   auto fences = [&]() {
@@ -305,20 +307,19 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
     tc_fence_after();
   };
   // S(buffer) = Q K^T
-  auto qk = [&](uint32_t buf, int first) {
-    const uint64_t k0 = k_desc + first * (C::kSlotBytes >> 4), k1 = C::kParts == 2 ? k_desc + second * (C::kSlotBytes >> 4) : 0;
+  auto qk = [&](uint32_t buf, int first, int next) {
+    const uint64_t k0 = k_desc + first * (C::kSlotBytes >> 4), k1 = C::kParts == 2 ? k_desc + next * (C::kSlotBytes >> 4) : 0;
 #pragma unroll
     for (int a = 0; a < C::kAtoms; ++a) {
       const uint64_t kd = C::kParts == 1 ? k0 + (a * (N * 128) >> 4) : (a < 2 ? k0 : k1) + ((a & 1) * (N * 128) >> 4);
       at_mma_ss4(tmem + buf * kAtBuf, q_desc + (a * C::kQAtom >> 4), kd, idesc_s, a > 0, one);
     }
-    at_commit(&sh.s_full[buf], one);
   };
   // O += P(buffer) V, `keys` of the tile's keys
-  auto pv = [&](uint32_t buf, int first, int keys, bool fresh) {
+  auto pv = [&](uint32_t buf, int first, int next, int keys, bool fresh) {
     constexpr int kSteps = N / 16, kPartSteps = kSteps / C::kParts;
     const int steps = one ? (keys + 15) >> 4 : 0;
-    const uint64_t v0 = v_desc + first * (C::kSlotBytes >> 4), v1 = C::kParts == 2 ? v_desc + second * (C::kSlotBytes >> 4) : 0;
+    const uint64_t v0 = v_desc + first * (C::kSlotBytes >> 4), v1 = C::kParts == 2 ? v_desc + next * (C::kSlotBytes >> 4) : 0;
     const uint32_t p = tmem + buf * kAtBuf;
     if constexpr (kPartSteps % 4 == 0) {
 #pragma unroll
@@ -335,17 +336,16 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
           at_mma_ts4(o_addr, p + term * (N / 2) + kk * 8, kk < kPartSteps ? v0 : v1, kIdescO,
                      !(term == 0 && kk == 0 && fresh), min(2, steps - kk));
     }
-    at_commit(&sh.pv_done[buf], one);
   };
   // rows of V past the last key inside its 16-key step are zeroed: 0 x NaN would reach every row. (Both warps of a slot do,
   // to the same effect.)
-  auto clear_tail = [&](int first, int keys) {
+  auto clear_tail = [&](int first, int next, int keys) {
     if ((keys & 15) == 0) return;
     const int to = (keys + 15) & ~15;
     constexpr int kRows = N / C::kParts;
     for (int row = keys; row < to; ++row)
       for (int i = lane; i < D / 8; i += 32) {   // 16-byte pieces of the row: D / 64 atoms of 8
-        const uint32_t off = ring + (row < kRows ? first : second) * C::kSlotBytes + (i >> 3) * kAtomBytes +
+        const uint32_t off = ring + (row < kRows ? first : next) * C::kSlotBytes + (i >> 3) * kAtomBytes +
                              (row % kRows) * 128 + (i & 7) * 16;
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(off), "r"(0) : "memory");
       }
@@ -364,52 +364,77 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
     const bool dual = T == 2 && at_uniform(u.dual);
     const int last = at_uniform(w.last_keys(u, t));
     for (int j = -C::kAhead; j < n; ++j) {
-#pragma unroll 1
-      for (int o = 0; o < (dual ? 2 : 1); ++o) {   // dual: the other tile's slots too, in their order
-        const bool own = !dual || o == t;
-        const int no = dual ? (o == 0 ? n0 : n1) : n;
-        // PV of key tile j
-        if (j >= 0 && j < no) {
-          const int vs = acquire();
-          if (vs < 0) return false;
-          if (own && j < nt && does_pv) {
-            const uint32_t buf = T == 2 ? t : x & 1u;
-            const int keys = j + 1 < (dual ? nt : n) ? N : last;
-            clear_tail(vs, keys);
-            if (j == 0) {
-              if (o_used) {
-                if (!at_warp_wait(&sh.o_free[t], o_phase, ab)) return false;
-                o_phase ^= 1u;
-              }
-              o_used = true;
-            }
-            if (!at_warp_wait(&sh.p_full[buf], (p_phase >> buf) & 1u, ab)) return false;
-            p_phase ^= 1u << buf;
-            fences();
-            pv(buf, vs, keys, j == 0);
-            if (T == 1) ++x;
+      // the slots of the other tile of a dual unit, V of key tile j and K of tile j + kAhead
+      auto pass = [&](int no) -> bool {
+        for (int is_k = 0; is_k < 2; ++is_k)
+          if (is_k ? j + C::kAhead < no : j >= 0 && j < no) {
+            const int at = acquire();
+            if (at < 0) return false;
+            release(at, second, false);
           }
-          release(vs, own && does_pv);
-        }
-        // QK^T of key tile j + kAhead
-        if (j + C::kAhead < no) {
-          const int ks = acquire();
-          if (ks < 0) return false;
-          if (own && j + C::kAhead < nt && does_qk) {
-            const uint32_t buf = T == 2 ? t : x & 1u;
-            if constexpr (T == 1) {   // the buffer's last PV is done (in the pipe of another warp)
-              if (x >= 2) {
-                if (!at_warp_wait(&sh.pv_done[buf], (s_phase >> buf) & 1u, ab)) return false;
-                s_phase ^= 1u << buf;
-              }
-              ++x;
-            }
-            fences();
-            qk(buf, ks);
-          }
-          release(ks, own && does_qk);
-        }
+        return true;
+      };
+      if (dual && t == 1 && !pass(n0)) return false;
+      const int no = dual ? nt : n;   // key tiles with slots that this warp has a part in
+      const bool pvs = does_pv && j >= 0 && j < nt, qks = does_qk && j + C::kAhead < nt;
+      const uint32_t buf = T == 2 ? t : x & 1u;
+      // ---- V, P and O of key tile j
+      int vs = -1, vs2 = 0;
+      if (j >= 0 && j < no) {
+        if ((vs = acquire()) < 0) return false;
+        vs2 = second;
+        if (!does_pv) release(vs, vs2, false);
       }
+      if (pvs) {
+        const int keys = j + 1 < no ? N : last;
+        clear_tail(vs, vs2, keys);
+        if (j == 0) {
+          if (o_used) {
+            if (!at_warp_wait(&sh.o_free[t], o_phase, ab)) return false;
+            o_phase ^= 1u;
+          }
+          o_used = true;
+        }
+        if (!at_warp_wait(&sh.p_full[buf], (p_phase >> buf) & 1u, ab)) return false;
+        p_phase ^= 1u << buf;
+      }
+      // ---- the two M tiles' warps issue in turns, PV and QK^T together: side by side their MMAs mix in the pipe, both S are
+      // done at the same time, and then the pipe waits for two softmaxes at once (16384 tokens of 32 heads: 1872 us, 1588
+      // in turns)
+      if constexpr (T == 2) {
+        if ((t == 1 || steps > 0) && !at_warp_wait(&sh.turn[t], (steps - (t == 0)) & 1u, ab)) return false;
+        ++steps;
+      }
+      if (pvs) {
+        fences();
+        pv(buf, vs, vs2, j + 1 < no ? N : last, j == 0);
+      }
+      // ---- K of tile j + kAhead
+      int ks = -1, ks2 = 0;
+      if (j + C::kAhead < no) {
+        if ((ks = acquire()) < 0) return false;
+        ks2 = second;
+        if (!does_qk) release(ks, ks2, false);
+      }
+      if (qks) {
+        if constexpr (T == 1) {   // the buffer's last PV is done (in the pipe of another warp)
+          if (x >= 2) {
+            if (!at_warp_wait(&sh.pv_done[buf], (s_phase >> buf) & 1u, ab)) return false;
+            s_phase ^= 1u << buf;
+          }
+        }
+        fences();
+        qk(buf, ks, ks2);
+      }
+      if constexpr (T == 2) {
+        if (one) mbar_arrive(&sh.turn[t ^ 1]);
+      }
+      if (pvs) at_commit(&sh.pv_done[buf], one);
+      if (qks) at_commit(&sh.s_full[buf], one);
+      if (T == 1 && (pvs || qks)) ++x;
+      if (does_pv && vs >= 0) release(vs, vs2, true);
+      if (does_qk && ks >= 0) release(ks, ks2, true);
+      if (dual && t == 0 && !pass(n1)) return false;
       if (j + C::kAhead == n - 1 && does_qk) at_commit(sh.q_empty, one);
     }
   }
@@ -706,6 +731,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   sh.pv_done = sh.q_full + 6;
   sh.o_free = sh.q_full + 8;
   sh.done = sh.q_full + 10;
+  sh.turn = sh.q_full + 12;
   sh.abort_flag = reinterpret_cast<int*>(sh.q_full + 11);
   sh.tmem_slot = reinterpret_cast<uint32_t*>(sh.q_full + 11) + 1;
   sh.x_bar = reinterpret_cast<uint64_t*>(smem + C::kXOff) - 4;   // d = 256 (whose ring is short): behind them
@@ -718,7 +744,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       mbar_init(&sh.empty[i], 2);
     }
     for (int i = 0; i < C::kRaws; ++i) {
-      mbar_init(&sh.raw_full[i], 32);
+      mbar_init(&sh.raw_full[i], 64);
       mbar_init(&sh.raw_empty[i], kAtCopyWarps);
     }
     mbar_init(sh.q_full, W::kF8 ? 8 : 1);
@@ -731,6 +757,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       mbar_init(&sh.o_free[i], kRowWarps);
     }
     mbar_init(sh.done, 2);
+    if constexpr (C::kTiles == 2)
+      for (int i = 0; i < 2; ++i) mbar_init(&sh.turn[i], 1);
     if constexpr (C::kTiles == 1)
       for (int i = 0; i < 4; ++i) mbar_init(&sh.x_bar[i], 2);
     *sh.abort_flag = 0;
@@ -755,7 +783,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
     ok = attn_softmax<W, C, D>(w, sh, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
-    if (warp == 8 || (kCopies && warp >= 12)) {
+    if (warp == 8 || (W::kF8 && warp == 11) || (kCopies && warp >= 12)) {
       // ---- the loaders: Q of each unit, and K and V in the order in which the MMA warps consume them
       W w(params, lane);
       constexpr int kDepth = W::kF8 ? C::kRaws : NS, kPieces = W::kF8 ? 1 : C::kParts;
@@ -778,7 +806,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
 #pragma unroll 1
           for (int part = 0; part < kPieces; ++part, ++r) {
             if (r >= kDepth && !at_warp_wait(&empty[slot], phase, sh.abort_flag)) return false;
-            w.template load_kv<C>(u, is_v, t, j, part, ring + slot * kBytes, &full[slot], warp - 12);
+            w.template load_kv<C>(u, is_v, t, j, part, ring + slot * kBytes, &full[slot], kCopies ? warp - 12 : warp == 11);
             if (++slot == kDepth) {
               slot = 0;
               phase ^= 1u;

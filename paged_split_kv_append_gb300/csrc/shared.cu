@@ -238,6 +238,9 @@ struct PrefixWork {
   static constexpr bool kPaged = true;
   static constexpr bool kWaitLate = true;
   static constexpr int kTerms = kTermsOfP;
+  // A bf16 output takes a prefix's partials as bf16(acc / l), in the first half of their slots: half the bytes both ways,
+  // for up to 2^-8 of a split's share, less than the weights' own rounding leaves.
+  static constexpr bool kHalfParts = kTermsOfP == 1;
   static constexpr bool kPairs = D <= 128;               // two M tiles a unit, or one over two ranges of keys
   // What is read before the grid ahead is waited for comes past L1 (__ldcg): the plan is complete, but an older line may
   // still lie there.
@@ -379,14 +382,14 @@ struct PrefixWork {
     int64_t at;
     if constexpr (kPairs) {   // V of a tile follows its K before the next K of the same M tile
       if (!is_v) {
-        if (t == 0) place[0] = next_places(cur[0], u, t, j, loader <= 0);
-        else place[1] = next_places(cur[1], u, t, j, loader <= 0);
+        if (t == 0) place[0] = next_places(cur[0], u, t, j, loader == 0);
+        else place[1] = next_places(cur[1], u, t, j, loader == 0);
       }
       at = t == 0 ? place[0] : place[1];
     } else {                  // K runs two tiles ahead of V, but for a unit's last
       if (!is_v && part == 0) {
         place[1] = place[0];
-        place[0] = next_places(cur[0], u, t, j, loader <= 0);
+        place[0] = next_places(cur[0], u, t, j, loader == 0);
       }
       at = is_v && j + 1 < u.n[0] ? place[1] : place[0];
     }
@@ -396,7 +399,8 @@ struct PrefixWork {
       const uint32_t to = smem_u32(dst) + lane * 16;
       const char* const from = pool + lane * 16;
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
+      for (int i0 = 0; i0 < kPieces; i0 += 2) {   // two warps copy
+        const int i = i0 + loader;
         const int64_t o = __shfl_sync(0xffffffffu, at, i);
         if (i >= held) break;
 #pragma unroll
@@ -441,6 +445,7 @@ struct PrefixWork {
       st_global_hint(p.a.m_part + at, m, keep);
       st_global_hint(p.a.l_part + at, l, keep);
     }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (a NaN stays one)
 #pragma unroll
     for (int i = 0; i < kCols; i += 32) {
       uint32_t o[32];
@@ -451,7 +456,15 @@ struct PrefixWork {
         __syncwarp();
         if (lane == 0) mbar_arrive(o_free);
       }
-      if (ok) {
+      if (ok && kHalfParts) {
+        float w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          w[e] = __uint_as_float(bf16x2_bits(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv));
+        float* dst = reinterpret_cast<float*>(reinterpret_cast<__nv_bfloat16*>(p.a.acc_part + at * D) + col0 + i);
+        st_global_v8_hint(dst, *reinterpret_cast<const float(*)[8]>(w), keep);
+        st_global_v8_hint(dst + 8, *reinterpret_cast<const float(*)[8]>(w + 8), keep);
+      } else if (ok) {
         float* dst = p.a.acc_part + at * D + col0 + i;
 #pragma unroll
         for (int e = 0; e < 32; e += 8) {
@@ -486,11 +499,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(SharedPa
     const float* l = p.l_part + row * p.max_splits;
     const float4* acc = reinterpret_cast<const float4*>(p.acc_part + row * p.max_splits * p.d);
     constexpr int N = 16;   // splits whose accumulators are loaded at once
+    const int halves = p.out_bf16 ? s.seqs[b].y : 0;   // the first partials are bf16 acc / l
     float4 a[N];
     auto load = [&](int s0) {
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        a[k] = j < d4 && s0 + k < S ? acc[static_cast<int64_t>(s0 + k) * d4 + j] : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < N; ++k) {
+        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < d4 && s0 + k < S) {
+          const float4* at = acc + static_cast<int64_t>(s0 + k) * d4;
+          if (s0 + k < halves) {
+            const uint2 h = reinterpret_cast<const uint2*>(at)[j];
+            a[k] = make_float4(__uint_as_float(h.x), __uint_as_float(h.y), 0.f, 0.f);
+          } else {
+            a[k] = at[j];
+          }
+        }
+      }
     };
     load(0);
     float mv[2], w[2], M = -INFINITY, L = 0.f;
@@ -506,7 +530,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(SharedPa
     for (int k = 0; k < 2; ++k) {
       const float e = mv[k] != -INFINITY ? fast_exp2(mv[k] - M) : -1.f;   // -1: skipped
       if (e != -1.f) L += e * w[k];
-      w[k] = e;
+      w[k] = e != -1.f && lane + 32 * k < halves ? e * w[k] : e;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -519,10 +543,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(SharedPa
         if (s0 + k >= S) break;
         const float e = __shfl_sync(0xffffffffu, s0 + k < 32 ? w[0] : w[1], (s0 + k) & 31);
         if (e != -1.f) {
-          A.x += e * a[k].x;
-          A.y += e * a[k].y;
-          A.z += e * a[k].z;
-          A.w += e * a[k].w;
+          float4 v = a[k];
+          if (s0 + k < halves) {
+            const float2 lo = bf16x2_to_float2(__float_as_uint(v.x)), hi = bf16x2_to_float2(__float_as_uint(v.y));
+            v = make_float4(lo.x, lo.y, hi.x, hi.y);
+          }
+          A.x += e * v.x;
+          A.y += e * v.y;
+          A.z += e * v.z;
+          A.w += e * v.w;
         }
       }
     }

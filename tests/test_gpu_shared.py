@@ -7,7 +7,7 @@ Tolerance of an output o = sum a_j v_j, with M = sum a_j |v_j| (a: the exact wei
 - fp32 output: prefix weights are three bf16 terms, each rounding what the one before left by half a step, 2^-24 M, or two
   f16 ones, 2^-22 M and 2^-25 of a weight of 2^7 or more in the sum for each of n keys: 2^-32 n max |v|. The own positions'
   weights are as exact as fp32.
-- bf16 output: prefix weights rounded to bf16, 2^-8 M; the output's own rounding 2^-8 |o|.
+- bf16 output: prefix weights rounded to bf16, 2^-8 M, their splits' results too, 2^-8 M; the output's own rounding 2^-8 |o|.
 E4M3 pools: their values are what the codes stand for, exactly; queries as f16 after a power of two are exact but for
 elements under 2^-24 of the vector's largest (2^-25 of it each: d 2^-25 max|q| max|k| scale more in E); weights as f16 terms
 are better than bf16 ones.
@@ -114,7 +114,7 @@ class Case:
         E = self.d * 2.0 ** -23 * S.amax(-1, keepdim=True) + 2.0 ** -22 * big + 2.0 ** -21
         if self.pools[0].dtype is torch.float8_e4m3fn:
             E = E + self.d * 2.0 ** -25 * float(q.abs().max()) * float(kv[0].abs().max()) * abs(self.scale)
-        tol = (2 * E + (n + 64) * 2.0 ** -23 + (2.0 ** -8 if self.out is torch.bfloat16 else 2.0 ** -22)) * M + \
+        tol = (2 * E + (n + 64) * 2.0 ** -23 + (2.0 ** -7 if self.out is torch.bfloat16 else 2.0 ** -22)) * M + \
             n * 2.0 ** -32 * float(kv[1].abs().max())
         if self.out is torch.bfloat16:
             tol = (tol + 2.0 ** -8 * o.abs()) * (1 + 2.0 ** -7)
