@@ -306,6 +306,12 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
     if constexpr (W::kPaged && !W::kF8) fence_proxy_async();   // written by cp.async
     tc_fence_after();
   };
+  // The other M tile's warp may issue
+  auto pass_turn = [&]() {
+    if constexpr (T == 2) {
+      if (one) mbar_arrive(&sh.turn[t ^ 1]);
+    }
+  };
   // S(buffer) = Q K^T
   auto qk = [&](uint32_t buf, int first, int next) {
     const uint64_t k0 = k_desc + first * (C::kSlotBytes >> 4), k1 = C::kParts == 2 ? k_desc + next * (C::kSlotBytes >> 4) : 0;
@@ -385,6 +391,18 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
         vs2 = second;
         if (!does_pv) release(vs, vs2, false);
       }
+      // ---- K of tile j + kAhead: asked for early where it has been there for long
+      int ks = -1, ks2 = 0;
+      auto take_k = [&]() -> bool {
+        if (j + C::kAhead >= no) return true;
+        if ((ks = acquire()) < 0) return false;
+        ks2 = second;
+        if (!does_qk) release(ks, ks2, false);
+        return true;
+      };
+      constexpr bool kEarlyK = T == 2 && !W::kPaged;
+      if constexpr (kEarlyK)
+        if (!take_k()) return false;
       if (pvs) {
         const int keys = j + 1 < no ? N : last;
         clear_tail(vs, vs2, keys);
@@ -409,13 +427,8 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
         fences();
         pv(buf, vs, vs2, j + 1 < no ? N : last, j == 0);
       }
-      // ---- K of tile j + kAhead
-      int ks = -1, ks2 = 0;
-      if (j + C::kAhead < no) {
-        if ((ks = acquire()) < 0) return false;
-        ks2 = second;
-        if (!does_qk) release(ks, ks2, false);
-      }
+      if constexpr (!kEarlyK)
+        if (!take_k()) return false;
       if (qks) {
         if constexpr (T == 1) {   // the buffer's last PV is done (in the pipe of another warp)
           if (x >= 2) {
@@ -426,9 +439,7 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
         fences();
         qk(buf, ks, ks2);
       }
-      if constexpr (T == 2) {
-        if (one) mbar_arrive(&sh.turn[t ^ 1]);
-      }
+      pass_turn();
       if (pvs) at_commit(&sh.pv_done[buf], one);
       if (qks) at_commit(&sh.s_full[buf], one);
       if (T == 1 && (pvs || qks)) ++x;
