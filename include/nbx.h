@@ -153,8 +153,8 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
  *   scale        softmax scale (finite)
  *   out          [device] bf16 [n_tok, h_q, d], contiguous; rows of no sequence are left as they were
  *   status       [device] int32 or NULL;  stream  cudaStream_t
- * Requirements: h_q % h_kv == 0; d in {64, 128, 256}; buffers and rows 16-byte aligned (strides of whole 16 bytes).
- * n_tok == 0 or batch == 0 returns NBX_OK without a launch.
+ * Requirements: h_q % h_kv == 0; d in {64, 128, 256}; buffers and rows 16-byte aligned (strides of whole 16 bytes), out
+ * 32-byte aligned. n_tok == 0 or batch == 0 returns NBX_OK without a launch.
  */
 NBX_API int nbx_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                             int64_t v_stride, int dtype, int n_tok, int h_q, int h_kv, int d, const int32_t* seq_start,

@@ -22,6 +22,7 @@
 //    V's keys); and the unit's Q tiles.
 //  * Paged K and V come by 16-byte cp.async of warps 12-15. (A tensor copy costs the copy engine some 135 ns whatever its
 //    size, and pages of 16 positions take 16 of 2 KB for 32 KB.)
+//  * warp 11 finds the units and hands them to the others through shared memory, one ahead.
 //  * E4M3 pools: warps 8 and 11 copy the codes of a tile as they are stored (cp.async), and warps 12-15 convert them to f16
 //    (exactly) into the ring. Queries enter as f16 too, times a power of two that brings the largest element of each
 //    vector into [2^14, 2^15): exact but for elements under 2^-29 of it. The softmax threads write them, each its own row,
@@ -69,28 +70,31 @@ struct AttnCfg {
   static constexpr int kRingOff = kTiles * kQTile;
   static constexpr int kRawOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kBarOff = kRawOff + kRaws * kRawBytes;
-  static constexpr int kBarBytes = F8 ? 384 : 256;
-  static constexpr int kXOff = kBarOff + kBarBytes;
-  static constexpr int kSmem = kXOff + (kTiles == 1 ? 2 * 256 * 4 : 0) + 768;   // slack: 256-byte alignment to 1024
+  static constexpr int kBarBytes = 384;
+  static constexpr int kUnitOff = kBarOff + kBarBytes;
+  static constexpr int kXOff = kUnitOff + 128;                   // two units
+  static constexpr int kSmem = kXOff + (kTiles == 1 ? 2 * 256 * 4 : 0);
   static constexpr uint32_t kOCol = 2 * kAtBuf;                  // S (and P) in columns [0, 256), O from there
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kSlots >= 3, "ring");
-  static_assert((2 * kSlots + 2 * kRaws + 14) * 8 <= kBarBytes, "barrier area");
+  static_assert((2 * kSlots + 2 * kRaws + 18) * 8 <= kBarBytes, "barrier area");
 };
 
-// One work unit.
-struct AttnUnit {
+// One work unit. (It is moved as 16-byte words: where it lies in local memory, too, it is aligned to them.)
+struct alignas(16) AttnUnit {
   int tok;        // first token of the first tile (rows of the query tensor)
   int toks;       // tokens of the unit, of both tiles
   int head, kvh;  // first query head, KV head
   int pos;        // causal: position of the first token in its sequence
   int b;          // paged: row of the block table
-  bool dual;      // the two tiles are the same query vectors, over keys of their own
+  int dual;       // the two tiles are the same query vectors, over keys of their own
   int kv[2];      // causal: first key's row; paged: first position
   int end[2];     // paged: one past the last position
   int slot[2];    // paged: slot of the partials
   int n[2];       // key tiles of each M tile
+  int pad;
 };
+static_assert(sizeof(AttnUnit) == 64, "a unit is four 16-byte words");
 
 // Bounded wait of a whole warp, with one answer: gives up when another role of the CTA has, or after kWaitLimitNs. Every
 // branch is on a vote, so the compiler knows the warp to be together behind it (and may use uniform registers there).
@@ -186,8 +190,8 @@ __device__ __forceinline__ bool at_each_tile(const AttnUnit& u, F f) {
 
 // What a work policy W provides (prompt.cu, shared.cu):
 //   typename W::Params with c (|scale| log2 e, or the least positive number for a scale of 0), negative and status;
-//   W::kN, kTerms, kF8, kPaged, kWaitLate; W(params, lane), bool unit(round, AttnUnit&): warp-wide; toks_per_tile(),
-//   heads(); last_keys, last_key, bad_keys; load_q / load_kv by the loader warp (or q_row for the softmax threads);
+//   W::kN, kTerms, kF8, kPaged, kWaitLate; begin() and bool unit(round, AttnUnit&) of the warp that finds the units (toks > 0
+//   in each); toks_per_tile(), heads(); last_keys, last_key, bad_keys; load_q / load_kv by the loader warp (or q_row for the softmax threads);
 //   store(...) by a softmax thread.
 template <class C>
 struct AttnShared {
@@ -202,6 +206,9 @@ struct AttnShared {
   uint64_t* p_full;    // [2] P over it
   uint64_t* pv_done;   // [2] the PV from that buffer is done: O holds it
   uint64_t* o_free;    // [2] the epilogue has read O of M tile t
+  uint64_t* unit_full; // [2] a unit is written, every reader has read it
+  uint64_t* unit_empty;
+  AttnUnit* units;     // [2]
   uint64_t* turn;      // [2] d <= 128: it is the turn of M tile t's warp to issue
   uint64_t* done;
   uint64_t* raw_full;  // [kRaws] a tile's codes have landed
@@ -211,6 +218,45 @@ struct AttnShared {
   uint32_t* tmem_slot;
   float* xbuf;         // [2][256]
 };
+
+// ---------------------------------------------------------------- units
+// The k-th unit of this CTA, to every warp that asks (W::kReaders of them): false behind the last.
+template <class C>
+__device__ __forceinline__ bool at_unit(const AttnShared<C>& sh, uint32_t k, AttnUnit& u) {
+  if (!at_warp_wait(&sh.unit_full[k & 1u], (k >> 1) & 1u, sh.abort_flag)) {
+    *sh.abort_flag = 1;
+    return false;
+  }
+  uint4* const to = reinterpret_cast<uint4*>(&u);
+  const uint32_t from = smem_u32(sh.units + (k & 1u));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) to[i] = lds128(from + 16 * i);
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.unit_empty[k & 1u]);
+  return u.toks > 0;
+}
+// Finds the units; `each` is called with every one of them.
+template <class W, class C, class F>
+__device__ __forceinline__ bool attn_units(W& w, const AttnShared<C>& sh, F each) {
+  w.begin();
+  bool more = true;
+  for (uint32_t k = 0; more; ++k) {
+    AttnUnit u = {};
+    more = w.unit(k, u);
+    if (!more) u.toks = 0;
+    if (k >= 2 && !at_warp_wait(&sh.unit_empty[k & 1u], ((k >> 1) - 1) & 1u, sh.abort_flag)) return false;
+    if ((threadIdx.x & 31) == 0) {
+      const uint4* const from = reinterpret_cast<const uint4*>(&u);
+      const uint32_t to = smem_u32(sh.units + (k & 1u));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sts128(to + 16 * i, from[i]);
+      mbar_arrive(&sh.unit_full[k & 1u]);
+    }
+    __syncwarp();
+    if (more && !each(u)) return false;
+  }
+  return true;
+}
 
 // ---------------------------------------------------------------- the MMA warps
 // MMAs and commits of one lane, as predicated instructions: the warp stays together, so that descriptors are computed once
@@ -363,7 +409,7 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
     tc_fence_after();
     return true;
   };
-  for (uint32_t k = 0; w.unit(k, u); ++k) {
+  for (uint32_t k = 0; at_unit(sh, k, u); ++k) {
     if (does_qk && !q_ready(k)) return false;
     const int n0 = at_uniform(u.n[0]), n1 = T == 2 ? at_uniform(u.n[1]) : 0;
     const int n = max(n0, n1), nt = t == 0 ? n0 : n1;
@@ -530,7 +576,7 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
     return ok;
   };
   AttnUnit u;
-  for (uint32_t k = 0; w.unit(k, u); ++k) {
+  for (uint32_t k = 0; at_unit(sh, k, u); ++k) {
     const int n = u.n[t];
     const int my_tok = (u.dual ? 0 : t * tpt) + tok;        // of the unit
     const bool row_ok = tok < tpt && my_tok < u.toks;
@@ -695,7 +741,7 @@ __device__ __forceinline__ bool attn_convert(W& w, const AttnShared<C>& sh, int 
   const int rr = lane >> 2, i = lane & 3;
   uint32_t r = 0, x = 0;   // ring slots, tiles
   AttnUnit u;
-  for (uint32_t k = 0; w.unit(k, u); ++k) {
+  for (uint32_t k = 0; at_unit(sh, k, u); ++k) {
     const bool ok = at_each_tile<C>(u, [&](bool is_v, int, int) -> bool {
       if (!at_warp_wait(&sh.raw_full[x % C::kRaws], (x / C::kRaws) & 1u, sh.abort_flag)) return false;
       const char* raw = sh.raw + (x % C::kRaws) * C::kRawBytes;
@@ -725,8 +771,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   using C = AttnCfg<D, W::kN, W::kF8>;
   constexpr int NS = C::kSlots;
   constexpr bool kCopies = W::kPaged && !W::kF8;   // warps 12-15 load K and V (else warp 8)
-  extern __shared__ __align__(256) char smem_raw[];
-  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) char smem[];
   AttnShared<C> sh;
   sh.q_s = smem;
   sh.ring = smem + C::kRingOff;
@@ -743,11 +788,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   sh.o_free = sh.q_full + 8;
   sh.done = sh.q_full + 10;
   sh.turn = sh.q_full + 12;
+  sh.unit_full = sh.q_full + 14;
+  sh.unit_empty = sh.q_full + 16;
+  sh.units = reinterpret_cast<AttnUnit*>(smem + C::kUnitOff);
   sh.abort_flag = reinterpret_cast<int*>(sh.q_full + 11);
   sh.tmem_slot = reinterpret_cast<uint32_t*>(sh.q_full + 11) + 1;
-  sh.x_bar = reinterpret_cast<uint64_t*>(smem + C::kXOff) - 4;   // d = 256 (whose ring is short): behind them
+  sh.x_bar = reinterpret_cast<uint64_t*>(smem + C::kUnitOff) - 4;   // d = 256 (whose ring is short): behind them
   sh.xbuf = reinterpret_cast<float*>(smem + C::kXOff);
-  static_assert(C::kTiles == 2 || (2 * NS + 2 * C::kRaws + 16) * 8 <= C::kBarBytes, "barrier area");
+  static_assert(C::kTiles == 2 || (2 * NS + 2 * C::kRaws + 20) * 8 <= C::kBarBytes, "barrier area");
   const int warp = at_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -768,6 +816,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       mbar_init(&sh.o_free[i], kRowWarps);
     }
     mbar_init(sh.done, 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.unit_full[i], 1);
+      // the softmax and MMA warps, the loader, and the warps that copy or convert
+      mbar_init(&sh.unit_empty[i], 11 + (W::kPaged ? kAtCopyWarps : 0));
+    }
     if constexpr (C::kTiles == 2)
       for (int i = 0; i < 2; ++i) mbar_init(&sh.turn[i], 1);
     if constexpr (C::kTiles == 1)
@@ -790,41 +843,55 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   bool ok = true;
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtSoftmaxRegs));
-    W w(params, lane);
+    W w(params);
     ok = attn_softmax<W, C, D>(w, sh, tmem);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtOtherRegs));
-    if (warp == 8 || (W::kF8 && warp == 11) || (kCopies && warp >= 12)) {
-      // ---- the loaders: Q of each unit, and K and V in the order in which the MMA warps consume them
-      W w(params, lane);
+    if (warp == 8 || warp == 11 || (kCopies && warp >= 12)) {
+      // ---- Q of each unit (warp 8), and K and V in the order in which the MMA warps consume them: warp 8, or for paged
+      // pools warps 12-15, or for E4M3 pools, whose Q the softmax threads write, warps 8 and 11, which finds the units too
+      W w(params);
       constexpr int kDepth = W::kF8 ? C::kRaws : NS, kPieces = W::kF8 ? 1 : C::kParts;
       constexpr int kBytes = W::kF8 ? C::kRawBytes : C::kSlotBytes;
       uint64_t* const full = W::kF8 ? sh.raw_full : sh.full;
       uint64_t* const empty = W::kF8 ? sh.raw_empty : sh.empty;
       char* const ring = W::kF8 ? sh.raw : sh.ring;
+      const int loader = kCopies ? warp - 12 : (warp == 11);
       uint32_t r = 0, q_units = 0, phase = 1;   // (the first round finds every slot empty)
       int slot = 0;
-      AttnUnit u;
-      for (uint32_t k = 0; ok && w.unit(k, u); ++k) {
-        if (!W::kF8 && warp == 8) {   // (the softmax threads write an E4M3 pool's Q)
-          if (k > 0) ok = at_warp_wait(sh.q_empty, (k - 1) & 1u, sh.abort_flag);
-          if (!ok) break;
-          w.template load_q<C>(u, sh.q_s, sh.q_full);
-          ++q_units;
-        }
-        if (kCopies && warp == 8) continue;
-        ok = at_each_tile<C>(u, [&](bool is_v, int t, int j) -> bool {
+      auto next_q = [&](const AttnUnit& u) -> bool {
+        if (q_units > 0 && !at_warp_wait(sh.q_empty, (q_units - 1) & 1u, sh.abort_flag)) return false;
+        w.template load_q<C>(u, sh.q_s, sh.q_full);
+        ++q_units;
+        return true;
+      };
+      auto tiles = [&](const AttnUnit& u) -> bool {
+        bool first = !W::kF8 && !kCopies;   // Q comes behind the first key tile, which need not wait for the last unit's Q
+        return at_each_tile<C>(u, [&](bool is_v, int t, int j) -> bool {
 #pragma unroll 1
           for (int part = 0; part < kPieces; ++part, ++r) {
             if (r >= kDepth && !at_warp_wait(&empty[slot], phase, sh.abort_flag)) return false;
-            w.template load_kv<C>(u, is_v, t, j, part, ring + slot * kBytes, &full[slot], kCopies ? warp - 12 : warp == 11);
+            w.template load_kv<C>(u, is_v, t, j, part, ring + slot * kBytes, &full[slot], loader);
             if (++slot == kDepth) {
               slot = 0;
               phase ^= 1u;
             }
           }
+          if (first) {
+            first = false;
+            return next_q(u);
+          }
           return true;
         });
+      };
+      if (warp == 11) {
+        ok = attn_units<W, C>(w, sh, [&](const AttnUnit& u) -> bool {
+          if constexpr (W::kF8) return tiles(u);
+          return true;
+        });
+      } else {
+        AttnUnit u;
+        for (uint32_t k = 0; ok && at_unit(sh, k, u); ++k) ok = kCopies && warp == 8 ? next_q(u) : tiles(u);
       }
       if (!ok) *sh.abort_flag = 1;
       // the copies issued last have landed before the CTA can exit
@@ -835,7 +902,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       }
       __syncwarp();
     } else if (warp == 9 || warp == 10) {
-      W w(params, lane);
+      W w(params);
       ok = attn_mma<W, C, D>(w, sh, tmem, warp - 9);
       if (!ok) *sh.abort_flag = 1;
       // every MMA of this CTA has completed before the TMEM is released
@@ -844,7 +911,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       __syncwarp();
     } else if (W::kF8 && warp >= 12) {
       if constexpr (W::kF8) {
-        W w(params, lane);
+        W w(params);
         ok = attn_convert<W, C, D>(w, sh, warp - 12);
       }
     }

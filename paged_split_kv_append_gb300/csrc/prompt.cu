@@ -4,7 +4,7 @@
 //    fill its M tiles, heads being the largest power of two that divides the group, so every tile but a sequence's last
 //    is full whatever the group. K and V tiles start at the sequence's first token; key tiles past a tile's last
 //    position are not read, and the scores of those on the diagonal are masked by selects.
-//  * The number of tokens of each sequence is known on the device only. Every warp finds its unit by itself from
+//  * The number of tokens of each sequence is known on the device only. One warp of each CTA finds its units from
 //    seq_start: units are ordered by their block's place in its sequence, the last (those with most keys) first, and
 //    dealt to the CTAs there and back. With S(i) = the number of blocks at place i or later, unit u lies at the place i
 //    with S(i + 1) <= u < S(i). No plan kernel, no workspace.
@@ -50,8 +50,9 @@ struct PromptWork {
     const int s = __ldg(p.a.seq_start + b), e = __ldg(p.a.seq_start + b + 1);
     return s >= 0 && e > s && e <= p.a.n_tok ? (e - s + tpb - 1) / tpb : 0;
   }
-  __device__ __forceinline__ PromptWork(const Params& params, int lane) : p(params) {
-    tpt = kAtM / p.heads;
+  __device__ __forceinline__ PromptWork(const Params& params) : p(params) { tpt = kAtM / p.heads; }
+  __device__ __forceinline__ void begin() {
+    const int lane = threadIdx.x & 31;
     tpb = C::kTiles * tpt;
     int sum = 0;
     most = 0;
@@ -64,7 +65,7 @@ struct PromptWork {
     }
     n_units = __reduce_add_sync(0xffffffffu, sum) * p.sets;
     most = __reduce_max_sync(0xffffffffu, most);
-    if (blockIdx.x == 0 && threadIdx.x < 32) {
+    if (blockIdx.x == 0) {
       for (int b = lane; b < p.a.batch; b += 32) {
         const int s = p.a.seq_start[b], e = p.a.seq_start[b + 1];
         if (s < 0 || e < s || e > p.a.n_tok) raise_status(p.status, NBX_DEV_BAD_LEN);
@@ -99,7 +100,9 @@ struct PromptWork {
       const uint32_t has = __ballot_sync(0xffffffffu, n > lo);
       const int count = __popc(has);
       if (left < count) {
-        b = b0 + __fns(has, 0, left + 1);
+        const uint32_t below = has & ((1u << (threadIdx.x & 31)) - 1u);
+        const bool here = ((has >> (threadIdx.x & 31)) & 1u) && __popc(below) == left;
+        b = b0 + __ffs(__ballot_sync(0xffffffffu, here)) - 1;
         break;
       }
       left -= count;
@@ -107,7 +110,9 @@ struct PromptWork {
     const int s = __ldg(p.a.seq_start + b), len = __ldg(p.a.seq_start + b + 1) - s;
     u.pos = lo * tpb;
     u.kv[0] = u.kv[1] = s;
-    u.dual = false;
+    u.dual = 0;
+    u.b = u.pad = 0;
+    u.end[0] = u.end[1] = u.slot[0] = u.slot[1] = 0;
     u.tok = s + u.pos;
     u.toks = min(tpb, len - u.pos);
     u.head = set * p.heads;

@@ -257,14 +257,14 @@ struct PrefixWork {
 
   __device__ __forceinline__ int toks_per_tile() const { return tpt; }
   __device__ __forceinline__ int heads() const { return p.heads; }
-  __device__ __forceinline__ PrefixWork(const Params& params, int) : p(params) {
+  __device__ __forceinline__ PrefixWork(const Params& params) : p(params) {
     tpt = kAtM / p.heads;
-    n_units = __ldcg(p.a.header + 4);
     step_idx = kN / p.a.page_tokens;
     step_off = kN - step_idx * p.a.page_tokens;
     cur[0] = cur[1] = Cursor{0, 0, 0};
     place[0] = place[1] = -1;
   }
+  __device__ __forceinline__ void begin() { n_units = __ldcg(p.a.header + 4); }
   __device__ __forceinline__ bool unit(uint32_t round, AttnUnit& u) const {
     const int64_t place = static_cast<int64_t>(round) * gridDim.x + blockIdx.x;
     if (place >= n_units) return false;

@@ -27,7 +27,7 @@ CALL = dict(q=FAKE, q_stride=1024, k=FAKE, k_stride=256, v=FAKE, v_stride=256, d
     (-1, dict(start=NULL)), (-1, dict(out=NULL)), (-2, dict(n_tok=-1)), (-2, dict(batch=-1)), (-2, dict(h_q=0)),
     (-2, dict(h_kv=0)), (-2, dict(h_kv=3)), (-2, dict(d=96)), (-2, dict(d=32)), (-2, dict(q_stride=1000)),
     (-2, dict(k_stride=252)), (-2, dict(v_stride=260)), (-3, dict(dtype=0)), (-3, dict(dtype=2)), (-7, dict(q=FAKE_ODD)),
-    (-7, dict(v=FAKE_ODD)), (-7, dict(out=FAKE_ODD)), (-8, dict(scale=float("nan"))), (-8, dict(scale=float("inf"))),
+    (-7, dict(v=FAKE_ODD)), (-7, dict(out=FAKE_ODD)), (-7, dict(out=ctypes.c_void_p(0x10010))), (-8, dict(scale=float("nan"))), (-8, dict(scale=float("inf"))),
     (-8, dict(scale=3e38))])
 def test_refusals(lib, want, kw):
     a = dict(CALL)
