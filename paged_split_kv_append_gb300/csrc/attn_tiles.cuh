@@ -98,13 +98,36 @@ static_assert(sizeof(AttnUnit) == 64, "a unit is four 16-byte words");
 
 // Bounded wait of a whole warp, with one answer: gives up when another role of the CTA has, or after kWaitLimitNs. Every
 // branch is on a vote, so the compiler knows the warp to be together behind it (and may use uniform registers there).
+// The loop is a function, one for all sites of the warps beside the softmax (whose registers leave no room for a call): up to
+// fourteen warps wait at a time, and loops of their own pushed the others' code out of the instruction caches (stalls for
+// want of an instruction were a third of a shared E4M3 prefix's cycles).
+__device__ __forceinline__ bool at_wait_loop(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    uint32_t ok = 0;
+#pragma unroll 1
+    for (int i = 0; i < 4 && !ok; ++i) {
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(bar), "r"(parity)
+          : "memory");
+      ok = __all_sync(0xffffffffu, ok != 0);
+    }
+    if (ok) return true;
+    if (__any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+  }
+}
+__device__ __noinline__ bool at_wait_call(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return at_wait_loop(bar, parity, abort_flag);
+}
+template <bool kCall = true>
 __device__ __forceinline__ bool at_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if (__any_sync(0xffffffffu, *abort_flag != 0 || ((i & 3u) == 0u && global_timer_ns() - t0 > kWaitLimitNs))) return false;
-  }
+  if constexpr (kCall) return __all_sync(0xffffffffu, at_wait_call(smem_u32(bar), parity, abort_flag));
+  return at_wait_loop(smem_u32(bar), parity, abort_flag);
 }
 // x, the same in every lane of the warp, as a value that the compiler knows to be
 __device__ __forceinline__ int at_uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -165,25 +188,19 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
 
 // Calls f(is_v, t, j) for the K and V tiles of a unit in the order in which the MMA warp consumes them (t: the M tile that
 // they are for, 0 where both read them). f returns false to give up.
+// (One place to call it from: f is long, and inlined.)
 template <class C, class F>
 __device__ __forceinline__ bool at_each_tile(const AttnUnit& u, F f) {
-  if (C::kTiles == 2 && u.dual) {
-    for (int t = 0; t < 2; ++t)
-      if (u.n[t] > 0 && !f(false, t, 0)) return false;
-    const int n = max(u.n[0], u.n[1]);
-    for (int j = 0; j < n; ++j)
-      for (int t = 0; t < 2; ++t) {
-        if (j < u.n[t] && !f(true, t, j)) return false;
-        if (j + 1 < u.n[t] && !f(false, t, j + 1)) return false;
-      }
-    return true;
-  }
-  const int n = C::kTiles == 2 ? max(u.n[0], u.n[1]) : u.n[0];
-  for (int j = 0; j < C::kAhead && j < n; ++j)
-    if (!f(false, 0, j)) return false;
-  for (int j = 0; j < n; ++j) {
-    if (!f(true, 0, j)) return false;
-    if (j + C::kAhead < n && !f(false, 0, j + C::kAhead)) return false;
+  const bool dual = C::kTiles == 2 && u.dual;
+  const int n0 = u.n[0], n1 = u.n[1], n = C::kTiles == 2 ? max(n0, n1) : n0;
+#pragma unroll 1
+  for (int j = -C::kAhead; j < n; ++j) {
+#pragma unroll 1
+    for (int i = 0; i < (dual ? 4 : 2); ++i) {   // V of tile j, K of tile j + kAhead, for each tile of a dual unit
+      const int t = i >> 1, at = (i & 1) ? j + C::kAhead : j;
+      if (at < 0 || at >= (dual ? (t ? n1 : n0) : n)) continue;
+      if (!f((i & 1) == 0, t, at)) return false;
+    }
   }
   return true;
 }
@@ -221,9 +238,9 @@ struct AttnShared {
 
 // ---------------------------------------------------------------- units
 // The k-th unit of this CTA, to every warp that asks (W::kReaders of them): false behind the last.
-template <class C>
+template <bool kCall = true, class C>
 __device__ __forceinline__ bool at_unit(const AttnShared<C>& sh, uint32_t k, AttnUnit& u) {
-  if (!at_warp_wait(&sh.unit_full[k & 1u], (k >> 1) & 1u, sh.abort_flag)) {
+  if (!at_warp_wait<kCall>(&sh.unit_full[k & 1u], (k >> 1) & 1u, sh.abort_flag)) {
     *sh.abort_flag = 1;
     return false;
   }
@@ -560,7 +577,7 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.x_bar[quarter]);
-    const bool ok = at_warp_wait(&sh.x_bar[quarter], xphase & 1u, ab);
+    const bool ok = at_warp_wait<false>(&sh.x_bar[quarter], xphase & 1u, ab);
     ++xphase;
     if (!ok) return false;
     tc_fence_after();
@@ -571,17 +588,17 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
   // each group, S(x - 1) follows PV(x - 2) in the pipe, and at d = 256, with two buffers, PV(x - 3).
   auto pv_wait = [&]() -> bool {
     const uint32_t y = x - 1;
-    const bool ok = T == 2 ? at_warp_wait(&sh.pv_done[t], y & 1u, ab) : at_warp_wait(&sh.pv_done[y & 1u], (y >> 1) & 1u, ab);
+    const bool ok = T == 2 ? at_warp_wait<false>(&sh.pv_done[t], y & 1u, ab) : at_warp_wait<false>(&sh.pv_done[y & 1u], (y >> 1) & 1u, ab);
     tc_fence_after();
     return ok;
   };
   AttnUnit u;
-  for (uint32_t k = 0; at_unit(sh, k, u); ++k) {
+  for (uint32_t k = 0; at_unit<false>(sh, k, u); ++k) {
     const int n = u.n[t];
     const int my_tok = (u.dual ? 0 : t * tpt) + tok;        // of the unit
     const bool row_ok = tok < tpt && my_tok < u.toks;
     if constexpr (W::kF8) {
-      if (k > 0 && !at_warp_wait(sh.q_empty, (k - 1) & 1u, ab)) return false;
+      if (k > 0 && !at_warp_wait<false>(sh.q_empty, (k - 1) & 1u, ab)) return false;
       if (n > 0) {
         const float down = q_to_f16<D, kOCols>(row_ok ? w.q_row(u, my_tok, head) : nullptr, sh.q_s + t * C::kQTile, row,
                                                T == 2 ? 0 : group * kOCols);
@@ -599,7 +616,7 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
       const uint32_t s_col = lane_base + buf * kAtBuf;
       uint32_t bad = 0;                                     // paged: 16-key pieces of this thread's columns without a page
       if constexpr (W::kPaged) bad = w.bad_keys(u, t, j, c0);
-      if (!at_warp_wait(&sh.s_full[buf], (T == 2 ? x : x >> 1) & 1u, ab)) return false;
+      if (!at_warp_wait<false>(&sh.s_full[buf], (T == 2 ? x : x >> 1) & 1u, ab)) return false;
       tc_fence_after();
       uint32_t s[NC];
 #pragma unroll
