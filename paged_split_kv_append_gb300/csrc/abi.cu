@@ -121,7 +121,7 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
                                         void* k_pool, void* v_pool, int pool_dtype, int num_pages, int page_tokens,
                                         const int32_t* slot_mapping, float k_scale, float v_scale, int32_t* status,
                                         void* stream) {
-  if (n_tok < 0 || h_q < 0 || h_kv < 1 || h_kv > (1 << 20) || h_q > (1 << 20) || d < 16 || d > 1024 || (d % 16) != 0 ||
+  if (n_tok < 0 || h_q < 0 || h_kv < 1 || h_kv > (1 << 16) || h_q > (1 << 16) || d < 16 || d > 1024 || (d % 16) != 0 ||
       num_pages < 1 || page_tokens < 1)
     return NBX_ERR_SHAPE;
   if (n_pos < 1 || turned < 16 || turned > d || (turned % 16) != 0) return NBX_ERR_SHAPE;

@@ -132,7 +132,7 @@ struct RotateParams {
   int64_t q_stride, k_stride, v_stride, q_out_stride;
   int n_tok, h_q, h_kv, d, n_pos, turned, interleaved, num_pages, page_tokens;
   int slots;          // rows of a token: h_q + 2 h_kv
-  int groups, toks;   // set by the launch: groups of slots, tokens of a CTA
+  int groups, block_groups, toks;   // set by the launch: groups of slots, of a CTA, tokens of a CTA at a time
   float k_inv, v_inv;
 };
 

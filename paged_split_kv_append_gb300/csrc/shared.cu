@@ -446,7 +446,7 @@ struct PrefixWork {
       st_global_hint(p.a.l_part + at, l, keep);
     }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (a NaN stays one)
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kCols; i += 32) {
       uint32_t o[32];
       tmem_ld32(o_base + i, o);
