@@ -20,7 +20,7 @@ namespace nbx {
 namespace {
 
 constexpr int kRotThreads = 512;   // at most
-constexpr int kRotBlocks = 4;      // an SM, of a call with many tokens
+constexpr int kRotBlocks = 1;      // an SM, of a call with many tokens: more tokens a thread (4: 70 us, 2: 67.6, 1: 66.9)
 
 // Eight consecutive elements as floats (address aligned to 16 bytes).
 struct F8 {
@@ -82,7 +82,7 @@ __device__ __forceinline__ void store8<E4M3>(char* p, const F8& f) {
 // Slots are a token's rows: its query heads, then its key heads, then its value heads. A thread keeps one place of 16
 // elements and the slots g, g + groups, ... for all of its tokens (blockIdx.x * toks + its own, then gridDim.x * toks
 // further on), so that a token costs it no division but its page's. Found anew for every token, the places took 16384 tokens
-// of 48 heads 76 to 97 us where this takes 70.
+// of 48 heads 76 to 97 us where this takes 67.
 template <class In, class Out, int kHeads>
 __global__ void __launch_bounds__(kRotThreads) append_rotated_kernel(RotateParams p) {
   pdl_launch_dependents();   // as the plain append: what follows waits before it reads the pools or the queries

@@ -48,6 +48,15 @@ struct PlanArgs {
   bool small;     // its arrays lie in shared memory
   // its query vectors fill one M tile of the two, which then take splits of their own
   __device__ __forceinline__ bool dual(const PrefixGroup& g) const { return tiles == 2 && g.n * a.rows <= tpt; }
+  __device__ __forceinline__ int units_of(const PrefixGroup& g, int splits) const { return dual(g) ? (splits + 1) / 2 : splits; }
+  // A group's splits of about `want` positions: their number, even if a unit takes two, and positions (of whole key tiles)
+  __device__ __forceinline__ void cut(const PrefixGroup& g, int want, int& n, int& seg) const {
+    const int most = min(kPrefixSplits, a.max_splits / 2);
+    n = min(most, static_cast<int>((static_cast<uint32_t>(g.eff) + want - 1) / static_cast<uint32_t>(want)));
+    if (dual(g)) n = min(most, (n + 1) / 2 * 2);
+    seg = ((g.eff - 1) / n + 128) & ~127;
+    n = (g.eff - 1) / seg + 1;
+  }
 };
 
 constexpr int kPlanBatch = 2048, kPlanGroups = 512;   // up to these the plan works in shared memory
@@ -63,7 +72,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   const SharedParams& s = x.s;
   const DecodeParams& p = x.a;
   __shared__ unsigned long long s_prefix, s_own;
-  __shared__ int s_ok, s_empty, s_warp[kPlanThreads / 32];
+  __shared__ int s_ok, s_empty, s_seg, s_warp[kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kPlanThreads / 32;
   PrefixGroup* const groups = x.small ? reinterpret_cast<PrefixGroup*>(plan_sm) : s.groups;
@@ -121,23 +130,44 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     pg.pairs = (pg.n * p.rows + tpu - 1) / tpu;
     if (lane == 0) {
       groups[g] = pg;
-      // (a dual unit works through two splits in the time of one)
-      if (pg.eff > 0) atomicAdd(&s_prefix, static_cast<unsigned long long>(pg.eff) * pg.pairs * x.sets * (x.dual(pg) ? 1 : 2));
+      // (a dual unit works through two splits at a time)
+      if (pg.eff > 0)
+        atomicAdd(&s_prefix, static_cast<unsigned long long>(x.dual(pg) ? (pg.eff + 1) / 2 : pg.eff) * pg.pairs * x.sets);
     }
   }
   __syncthreads();
-  // ---- its splits: about one unit an SM in all, and not below 256 positions (a dual unit's: 128)
+  // ---- the splits: one length for all groups, of 32 candidates the one whose rounds of units over the SMs are done first.
+  // (A number of splits for each group, rounded to one round of units, left the longest at twice the mean: samples of five
+  // documents of 6000 to 20000 positions 150 us, XX so.)
+  if (warp == 0 && s_prefix > 0) {
+    // s_prefix: positions that all units work through one at a time. Lane i: a round would take 1 / (1 + i / 6) of them.
+    // (fp32: 64-bit divisions cost a call 4 us here)
+    const float round = __fdividef(static_cast<float>(s_prefix) * 6.f, static_cast<float>(x.sms * (6 + lane)));
+    const int seg = max((static_cast<int>(fminf(round, 1e9f)) + 127) & ~127, 128);
+    float units = 0.f;
+    int longest = 0;
+    for (int g = 0; g < s.n_groups; ++g) {
+      const PrefixGroup pg = groups[g];
+      if (pg.eff == 0) continue;
+      int n, len;
+      x.cut(pg, seg, n, len);
+      units += static_cast<float>(x.units_of(pg, n) * pg.pairs) * x.sets;
+      longest = max(longest, len);
+    }
+    // a unit's own costs: about as long as 256 positions
+    const float cost = ceilf(units / x.sms) * (static_cast<float>(longest) + 256.f);
+    float best = cost;
+    for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane == __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1) s_seg = seg;
+  }
+  __syncthreads();
   for (int g = warp; g < s.n_groups; g += kWarps) {
     PrefixGroup pg = groups[g];
     if (pg.eff == 0) continue;
-    const unsigned long long want = (2ull * x.sms * pg.eff + s_prefix / 2) / s_prefix;
-    const int least = x.dual(pg) ? 128 : 256;
-    const int most = min(min(kPrefixSplits, p.max_splits / 2), (pg.eff + least - 1) / least);
-    const int n = want < 1 ? 1 : (want > most ? most : static_cast<int>(want));
-    pg.seg = ((pg.eff + n - 1) / n + 127) / 128 * 128;
-    pg.splits = (pg.eff + pg.seg - 1) / pg.seg;
+    x.cut(pg, s_seg, pg.splits, pg.seg);
     for (int i = lane; i < pg.n; i += 32)
       if (len_of(pg.b0 + i) > 0) seqs[pg.b0 + i] = make_int2(pg.eff, pg.splits);
+    __syncwarp();
     if (lane == 0) groups[g] = pg;
   }
   __syncthreads();
@@ -150,7 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
       int units = 0;
       if (g < s.n_groups) {
         pg = groups[g];
-        units = (x.dual(pg) ? (pg.splits + 1) / 2 : pg.splits) * pg.pairs * x.sets;
+        units = x.units_of(pg, pg.splits) * pg.pairs * x.sets;
       }
       int sum = units;
       for (int o = 1; o < 32; o <<= 1) {
@@ -182,11 +212,11 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
       sh = seqs[b];
       const int own = L - sh.x;
       if (own > 0) {
-        const unsigned long long num = static_cast<unsigned long long>(p.tc_units) * own, den = p.tc_pairs * s_own;
-        const unsigned long long want = (num + den - 1) / den;
+        // (the share of the units, rounded up)
+        const float want = ceilf(static_cast<float>(p.tc_units) * own / (static_cast<float>(p.tc_pairs) * s_own));
         const int most = min(p.max_splits - sh.y, max(1, own / 64));
-        const int S = want < 1 ? 1 : (want > most ? most : static_cast<int>(want));
-        seg = (own + S - 1) / S;
+        const int S = want < 1.f ? 1 : (want > most ? most : static_cast<int>(want));
+        seg = (own - 1) / S + 1;
         seg = (seg + align - 1) / align * align;
         n = (own + seg - 1) / seg;
       }
