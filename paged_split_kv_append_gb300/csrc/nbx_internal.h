@@ -358,7 +358,7 @@ struct SharedParams {
   const int32_t* shared_lens;   // [n_groups]
   int n_groups;
   // workspace
-  int2* seqs;                   // [batch] positions read with the group, splits of them
+  int2* seqs;                   // [batch] positions read with the group, splits of them (the plan's scratch)
   PrefixGroup* groups;          // [n_groups]
 };
 

@@ -220,8 +220,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         seg = (seg + align - 1) / align * align;
         n = (own + seg - 1) / seg;
       }
-      p.plan[b] = SeqPlan{L, seg, sh.y + n, sh.x};
-      if (x.small) s.seqs[b] = sh;
+      // (what the merge needs, in one read: the prefix's splits stand where other plans have the split's length)
+      reinterpret_cast<int4*>(p.plan)[b] = make_int4(L, sh.y, sh.y + n, sh.x);
       if (sh.y + n == 0) s_empty = 1;
     }
     int sum = n;
@@ -512,8 +512,12 @@ struct PrefixWork {
 constexpr int kMergeWarps = 4;
 
 // One warp per (query vector, 128 columns): M = max m_s, w_s = 2^(m_s - M) (a split with m = -inf is skipped),
-// out = v_scale sum w_s acc_s / sum w_s l_s, s ascending. Sequences with one split and no prefix are written already.
-__global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(SharedParams s, DecodeParams p) {
+// out = v_scale sum w_s acc_s / sum w_s l_s, s ascending: the prefix's splits, then the sequence's own. Sequences with one
+// split and no prefix are written already. kHalves: the output is bf16, and the prefix's partials are bf16 acc / l.
+// What bounds it: a chain of three reads (plan, first accumulators and statistics, the rest).
+template <bool kHalves>
+__global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(DecodeParams p) {
+  constexpr int N = 8;   // splits whose accumulators are loaded at once, of either kind
   const int lane = threadIdx.x & 31;
   const int d4 = p.d / 4, pieces = (d4 + 31) / 32;
   const int64_t rows = static_cast<int64_t>(p.batch) * p.rows * p.h_q;
@@ -523,30 +527,25 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(SharedPa
     const int64_t row = it / pieces;
     const int j = static_cast<int>(it - row * pieces) * 32 + lane;
     const int b = static_cast<int>(row / (static_cast<int64_t>(p.rows) * p.h_q));
-    const int S = p.plan[b].n_splits;
-    if (S == 0 || (S == 1 && s.seqs[b].y == 0)) continue;
+    const int4 plan = reinterpret_cast<const int4*>(p.plan)[b];
+    const int S = plan.z, pre = plan.y;
+    if (S == 0 || (S == 1 && pre == 0)) continue;
     const float* m = p.m_part + row * p.max_splits;
     const float* l = p.l_part + row * p.max_splits;
-    const float4* acc = reinterpret_cast<const float4*>(p.acc_part + row * p.max_splits * p.d);
-    constexpr int N = 16;   // splits whose accumulators are loaded at once
-    const int halves = p.out_bf16 ? s.seqs[b].y : 0;   // the first partials are bf16 acc / l
+    const float4* acc = reinterpret_cast<const float4*>(p.acc_part + row * p.max_splits * p.d) + (j < d4 ? j : 0);
+    const uint2* half = reinterpret_cast<const uint2*>(p.acc_part + row * p.max_splits * p.d) + (j < d4 ? j : 0);
     float4 a[N];
-    auto load = [&](int s0) {
+    uint2 h[N];
+    auto load_own = [&](int s0) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < d4 && s0 + k < S) {
-          const float4* at = acc + static_cast<int64_t>(s0 + k) * d4;
-          if (s0 + k < halves) {
-            const uint2 h = reinterpret_cast<const uint2*>(at)[j];
-            a[k] = make_float4(__uint_as_float(h.x), __uint_as_float(h.y), 0.f, 0.f);
-          } else {
-            a[k] = at[j];
-          }
-        }
-      }
+      for (int k = 0; k < N; ++k) a[k] = acc[static_cast<int64_t>(min(s0 + k, S - 1)) * d4];
     };
-    load(0);
+    auto load_half = [&](int s0) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) h[k] = half[static_cast<int64_t>(min(s0 + k, S - 1)) * (2 * d4)];
+    };
+    if (kHalves && pre > 0) load_half(0);
+    load_own(kHalves ? pre : 0);
     float mv[2], w[2], M = -INFINITY, L = 0.f;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -560,34 +559,40 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(SharedPa
     for (int k = 0; k < 2; ++k) {
       const float e = mv[k] != -INFINITY ? fast_exp2(mv[k] - M) : -1.f;   // -1: skipped
       if (e != -1.f) L += e * w[k];
-      w[k] = e != -1.f && lane + 32 * k < halves ? e * w[k] : e;
+      w[k] = kHalves && e != -1.f && lane + 32 * k < pre ? e * w[k] : e;  // (bf16 partials carry no l)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     const float sc = p.v_scale / L;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < S; s0 += N) {
-      if (s0 > 0) load(s0);
+    auto add = [&](int sp, const float4& v) {
+      const float e = __shfl_sync(0xffffffffu, sp < 32 ? w[0] : w[1], sp & 31);
+      if (e != -1.f) A = make_float4(fmaf(e, v.x, A.x), fmaf(e, v.y, A.y), fmaf(e, v.z, A.z), fmaf(e, v.w, A.w));
+    };
+    if constexpr (kHalves) {
+#pragma unroll 1
+      for (int s0 = 0; s0 < pre; s0 += N) {
+        if (s0 > 0) load_half(s0);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          if (s0 + k >= pre) break;
+          const float2 lo = bf16x2_to_float2(h[k].x), hi = bf16x2_to_float2(h[k].y);
+          add(s0 + k, make_float4(lo.x, lo.y, hi.x, hi.y));
+        }
+      }
+    }
+#pragma unroll 1
+    for (int s0 = kHalves ? pre : 0; s0 < S; s0 += N) {
+      if (s0 > (kHalves ? pre : 0)) load_own(s0);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         if (s0 + k >= S) break;
-        const float e = __shfl_sync(0xffffffffu, s0 + k < 32 ? w[0] : w[1], (s0 + k) & 31);
-        if (e != -1.f) {
-          float4 v = a[k];
-          if (s0 + k < halves) {
-            const float2 lo = bf16x2_to_float2(__float_as_uint(v.x)), hi = bf16x2_to_float2(__float_as_uint(v.y));
-            v = make_float4(lo.x, lo.y, hi.x, hi.y);
-          }
-          A.x += e * v.x;
-          A.y += e * v.y;
-          A.z += e * v.z;
-          A.w += e * v.w;
-        }
+        add(s0 + k, a[k]);
       }
     }
     if (j >= d4) continue;
     const float4 o = M == -INFINITY ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(A.x * sc, A.y * sc, A.z * sc, A.w * sc);
-    if (p.out_bf16)
+    if (kHalves)
       reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * p.d)[j] =
           make_uint2(bf16x2_bits(o.x, o.y), bf16x2_bits(o.z, o.w));
     else
@@ -720,7 +725,8 @@ cudaError_t shared_dispatch(const SharedParams& s, const DecodeParams& p, int q_
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(p.batch) * p.rows * p.h_q * ((p.d / 4 + 31) / 32);
   const int64_t grid = std::min<int64_t>((items + kMergeWarps - 1) / kMergeWarps, static_cast<int64_t>(di.sm_count) * 8);
-  return launch_pdl(shared_merge_kernel, static_cast<unsigned>(grid), kMergeWarps * 32, 0, stream, s, q);
+  return p.out_bf16 ? launch_pdl(shared_merge_kernel<true>, static_cast<unsigned>(grid), kMergeWarps * 32, 0, stream, q)
+                    : launch_pdl(shared_merge_kernel<false>, static_cast<unsigned>(grid), kMergeWarps * 32, 0, stream, q);
 }
 
 }  // namespace nbx
