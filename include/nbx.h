@@ -119,10 +119,12 @@ NBX_API int nbx_paged_kv_append(const void* new_k, const void* new_v, int new_dt
  *   h_q          query heads; 0: keys and values only (q and q_out are not read then)
  *   cos_table, sin_table [device] fp32 [n_pos, turned / 2]
  *   positions    [device] int32 [n_tok]; a position outside [0, n_pos) sets NBX_DEV_BAD_LEN and the token is
- *                skipped (its q_out too)
+ *                skipped (in q_out and k_out too)
  *   q_out        [device] as q with q_out_stride; may be q itself (with q's stride)
- *   slot_mapping [device] int32 [n_tok]; a slot outside the pool sets NBX_DEV_BAD_SLOT, the token's keys and values
- *                are skipped and its queries turned all the same
+ *   k_out        [device] the turned keys once more, in new_dtype and unscaled, as new_k with k_out_stride (for the
+ *                attention of the prompt that they belong to); may be new_k itself (with its stride), or NULL
+ *   slot_mapping [device] int32 [n_tok]; a slot outside the pool sets NBX_DEV_BAD_SLOT, the pools are left alone and
+ *                q_out and k_out written all the same
  *   the other arguments as for nbx_paged_kv_append
  * Requirements: d and turned multiples of 16, turned <= d <= 1024; buffers and rows 16-byte aligned (strides of whole
  * 16 bytes). n_tok == 0 returns NBX_OK without a launch.
@@ -131,9 +133,9 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
                                         const void* new_v, int64_t v_stride, int new_dtype, int n_tok, int h_kv, int d,
                                         const float* cos_table, const float* sin_table, int n_pos, int turned,
                                         int interleaved, const int32_t* positions, void* q_out, int64_t q_out_stride,
-                                        void* k_pool, void* v_pool, int pool_dtype, int num_pages, int page_tokens,
-                                        const int32_t* slot_mapping, float k_scale, float v_scale, int32_t* status,
-                                        void* stream);
+                                        void* k_out, int64_t k_out_stride, void* k_pool, void* v_pool, int pool_dtype,
+                                        int num_pages, int page_tokens, const int32_t* slot_mapping, float k_scale,
+                                        float v_scale, int32_t* status, void* stream);
 
 /*
  * nbx_prompt_attn -- causal attention over whole prompts, packed one behind the other.

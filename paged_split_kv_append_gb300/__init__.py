@@ -123,7 +123,7 @@ def _declare(l):
     l.nbx_paged_kv_compact.restype = i32
     i64 = ctypes.c_int64
     l.nbx_paged_kv_append_rotated.argtypes = [vp, i64, i32, vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, i32, i32, i32,
-                                              vp, vp, i64, vp, vp, i32, i32, i32, vp, f32, f32, vp, vp]
+                                              vp, vp, i64, vp, i64, vp, vp, i32, i32, i32, vp, f32, f32, vp, vp]
     l.nbx_paged_kv_append_rotated.restype = i32
     l.nbx_prompt_attn.argtypes = [vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, i32, vp, i32, f32, vp, vp, vp]
     l.nbx_prompt_attn.restype = i32
@@ -773,16 +773,66 @@ def nbx_paged_kv_append_rotated(q: Optional[torch.Tensor], new_k: torch.Tensor, 
                                 sin: torch.Tensor, positions: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
                                 slot_mapping: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0,
                                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
-                                status: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+                                status: Optional[torch.Tensor] = None, stream=None,
+                                k_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """q [n_tok, h_q, d] (or None) and new_k [n_tok, h_kv, d] turned by their positions [n_tok] int32, whose angles'
     cosines and sines are rows of cos / sin [n_pos, turned / 2] fp32 (halves of the first `turned` elements against each
     other, or neighbours with `interleaved`); keys and values [n_tok, h_kv, d] into the pools [num_pages, h_kv,
-    page_tokens, d] at slot_mapping [n_tok] int32, cast on store. q, new_k and new_v may be strided between tokens.
-    Returns the turned queries (q_out, which may be q), or None without q."""
+    page_tokens, d] at slot_mapping [n_tok] int32, cast on store; the turned keys to k_out too, where it is given (it may be
+    new_k). All but the pools may be strided between tokens. Returns the turned queries (q_out, which may be q), or None
+    without q."""
+    dtype, dev = new_k.dtype, k_pool.get_device()
+    num_pages, h_kv, page_tokens, d = pool = k_pool.shape if k_pool.dim() == 4 else (0, 0, 0, 0)
+    shape, table, h_q, q_stride, out_stride = new_k.shape, cos.shape, 0, 0, 0
+    if q is not None and q_out is None:
+        q_out = _new(q.shape, dtype, q, stream)
+    # (a call of one token each for 32 sequences takes the GPU 2.4 us, and checks one by one 7: what is right passes here)
+    k_strides, v_strides, one = new_k.stride(), new_v.stride(), (d, 1)
+    fits = len(shape) == 3 and shape[1] == h_kv and shape[2] == d and new_v.shape == shape and v_pool.shape == pool and \
+        k_strides[1:] == one and v_strides[1:] == one and len(table) == 2 and sin.shape == table and \
+        new_v.dtype is dtype and v_pool.dtype is k_pool.dtype and cos.dtype is sin.dtype is torch.float32 and \
+        positions.dtype is slot_mapping.dtype is torch.int32 and positions.numel() == slot_mapping.numel() == shape[0] and \
+        dev >= 0 and dev == v_pool.get_device() == new_k.get_device() == new_v.get_device() == cos.get_device() == \
+        sin.get_device() == positions.get_device() == slot_mapping.get_device() and k_pool.is_contiguous() and \
+        v_pool.is_contiguous() and cos.is_contiguous() and sin.is_contiguous() and positions.is_contiguous() and \
+        slot_mapping.is_contiguous()
+    if fits and q is not None:
+        q_shape, q_strides, out_strides = q.shape, q.stride(), q_out.stride()
+        fits = len(q_shape) == 3 and q_shape[0] == shape[0] and q_shape[2] == d and q_out.shape == q_shape and \
+            q_strides[1:] == one and out_strides[1:] == one and q.dtype is q_out.dtype is dtype and \
+            dev == q.get_device() == q_out.get_device() and \
+            (q_out.data_ptr() != q.data_ptr() or out_strides == q_strides)
+        if fits:
+            h_q, q_stride, out_stride = q_shape[1], q_strides[0], out_strides[0]
+    elif q_out is not None and q is None:
+        raise ValueError("q_out without q")
+    k_out_stride = 0
+    if k_out is not None:
+        (k_out_stride,) = _tokens(dev, "k_out", k_out)
+        if k_out.shape != shape or k_out.dtype != dtype:
+            raise ValueError(f"k_out must be {list(shape)} {dtype}")
+        if k_out.data_ptr() == new_k.data_ptr() and k_out_stride != k_strides[0] and shape[0] > 1:
+            raise ValueError("k_out in new_k's place must have its stride")
+    if status is not None and (status.get_device() != dev or status.dtype is not torch.int32 or not status.numel()):
+        fits = False
+    if not fits:
+        h_q, q_stride, k_strides, v_strides, out_stride = _rotated_checks(q, new_k, new_v, cos, sin, positions, k_pool, v_pool,
+                                                                          slot_mapping, q_out, status)
+    _run("nbx_paged_kv_append_rotated", dev, stream, _p(q), q_stride, h_q, new_k.data_ptr(), k_strides[0],
+         new_v.data_ptr(), v_strides[0], dtype_code(new_k), shape[0], h_kv, d, cos.data_ptr(), sin.data_ptr(), table[0],
+         2 * table[1], int(interleaved), positions.data_ptr(), _p(q_out), out_stride, _p(k_out), k_out_stride, k_pool.data_ptr(),
+         v_pool.data_ptr(), dtype_code(k_pool), num_pages, page_tokens, slot_mapping.data_ptr(), float(k_scale),
+         float(v_scale), _p(status))
+    return q_out
+
+
+def _rotated_checks(q, new_k, new_v, cos, sin, positions, k_pool, v_pool, slot_mapping, q_out, status):
+    """Every check of nbx_paged_kv_append_rotated by itself: (h_q, stride of q, strides of new_k and new_v, stride of q_out)
+    of a call that fits after all (a single head's stride says nothing), an error that says what does not."""
     dev = _one_device("k_pool v_pool cos sin positions slot_mapping status", k_pool, v_pool, cos, sin, positions,
                       slot_mapping, status)
     _int32("positions slot_mapping status", positions, slot_mapping, status)
-    num_pages, h_kv, page_tokens, d, _ = _pools(k_pool, v_pool, None, None)
+    _, h_kv, _, d, _ = _pools(k_pool, v_pool, None, None)
     k_stride, v_stride = _tokens(dev, "new_k new_v", new_k, new_v)
     n_tok, table, dtype = new_k.shape[0], cos.shape, new_k.dtype
     if new_k.shape != (n_tok, h_kv, d) or new_v.shape != new_k.shape or new_v.dtype != dtype or len(table) != 2 or \
@@ -791,26 +841,17 @@ def nbx_paged_kv_append_rotated(q: Optional[torch.Tensor], new_k: torch.Tensor, 
                 slot_mapping)
     if cos.dtype is not torch.float32 or sin.dtype is not torch.float32:
         raise ValueError("cos and sin must be fp32")
-    h_q = q_stride = out_stride = 0
-    if q is not None:
-        (q_stride,) = _tokens(dev, "q", q)
-        h_q = q.shape[1]
-        if q.shape != (n_tok, h_q, d) or q.dtype != dtype:
-            raise ValueError(f"q {list(q.shape)} {q.dtype} does not fit new_k {list(new_k.shape)} {dtype}")
-        if q_out is None:
-            q_out = _new(q.shape, dtype, q, stream)
-        (out_stride,) = _tokens(dev, "q_out", q_out)
-        if q_out.shape != q.shape or q_out.dtype != dtype:
-            raise ValueError(f"q_out must be {list(q.shape)} {dtype}")
-        if q_out.data_ptr() == q.data_ptr() and out_stride != q_stride and n_tok > 1:
-            raise ValueError("q_out in q's place must have q's stride")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    _run("nbx_paged_kv_append_rotated", dev, stream, _p(q), q_stride, h_q, new_k.data_ptr(), k_stride, new_v.data_ptr(),
-         v_stride, dtype_code(new_k), n_tok, h_kv, d, cos.data_ptr(), sin.data_ptr(), table[0], 2 * table[1],
-         int(interleaved), positions.data_ptr(), _p(q_out), out_stride, k_pool.data_ptr(), v_pool.data_ptr(),
-         dtype_code(k_pool), num_pages, page_tokens, slot_mapping.data_ptr(), float(k_scale), float(v_scale), _p(status))
-    return q_out
+    if q is None:
+        return 0, 0, (k_stride,), (v_stride,), 0
+    q_stride, out_stride = _tokens(dev, "q q_out", q, q_out)
+    h_q = q.shape[1]
+    if q.shape != (n_tok, h_q, d) or q.dtype != dtype:
+        raise ValueError(f"q {list(q.shape)} {q.dtype} does not fit new_k {list(new_k.shape)} {dtype}")
+    if q_out.shape != q.shape or q_out.dtype != dtype:
+        raise ValueError(f"q_out must be {list(q.shape)} {dtype}")
+    if q_out.data_ptr() == q.data_ptr() and out_stride != q_stride and n_tok > 1:
+        raise ValueError("q_out in q's place must have q's stride")
+    return h_q, q_stride, (k_stride,), (v_stride,), out_stride
 
 
 def nbx_prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start: torch.Tensor, scale: float,

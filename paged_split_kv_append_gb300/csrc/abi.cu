@@ -118,9 +118,9 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
                                         const void* new_v, int64_t v_stride, int new_dtype, int n_tok, int h_kv, int d,
                                         const float* cos_table, const float* sin_table, int n_pos, int turned,
                                         int interleaved, const int32_t* positions, void* q_out, int64_t q_out_stride,
-                                        void* k_pool, void* v_pool, int pool_dtype, int num_pages, int page_tokens,
-                                        const int32_t* slot_mapping, float k_scale, float v_scale, int32_t* status,
-                                        void* stream) {
+                                        void* k_out, int64_t k_out_stride, void* k_pool, void* v_pool, int pool_dtype,
+                                        int num_pages, int page_tokens, const int32_t* slot_mapping, float k_scale,
+                                        float v_scale, int32_t* status, void* stream) {
   if (n_tok < 0 || h_q < 0 || h_kv < 1 || h_kv > (1 << 16) || h_q > (1 << 16) || d < 16 || d > 1024 || (d % 16) != 0 ||
       num_pages < 1 || page_tokens < 1)
     return NBX_ERR_SHAPE;
@@ -131,6 +131,7 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
   if (interleaved != 0 && interleaved != 1) return NBX_ERR_VALUE;
   const int elt = new_dtype == NBX_F32 ? 4 : 2;
   if (!rows_ok(k_stride, n_tok, h_kv, d, elt) || !rows_ok(v_stride, n_tok, h_kv, d, elt) ||
+      (k_out && !rows_ok(k_out_stride, n_tok, h_kv, d, elt)) ||
       (h_q > 0 && (!rows_ok(q_stride, n_tok, h_q, d, elt) || !rows_ok(q_out_stride, n_tok, h_q, d, elt))))
     return NBX_ERR_SHAPE;
   if (n_tok == 0) return NBX_OK;
@@ -138,7 +139,7 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
       (h_q > 0 && (!q || !q_out)))
     return NBX_ERR_NULL;
   if (!aligned16(q) || !aligned16(new_k) || !aligned16(new_v) || !aligned16(cos_table) || !aligned16(sin_table) ||
-      !aligned16(q_out) || !aligned16(k_pool) || !aligned16(v_pool))
+      !aligned16(q_out) || !aligned16(k_out) || !aligned16(k_pool) || !aligned16(v_pool))
     return NBX_ERR_ALIGN;
   RotateParams p = {};
   p.q = q;
@@ -149,6 +150,8 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
   p.positions = positions;
   p.slot_mapping = slot_mapping;
   p.q_out = q_out;
+  p.k_out = k_out;
+  p.k_out_stride = k_out_stride;
   p.k_pool = k_pool;
   p.v_pool = v_pool;
   p.status = status;

@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kRotThreads) append_rotated_kernel(RotateParam
     }
     const bool held = slot >= 0 && slot < static_cast<int64_t>(p.num_pages) * p.page_tokens;
     if (reports && !held) raise_status(p.status, NBX_DEV_BAD_SLOT);
+    const int wanted = held ? p.slots : (p.k_out ? p.h_q + p.h_kv : p.h_q);   // a token without a slot still turns
     const int page = held ? slot / p.page_tokens : 0;
     const int64_t in_pool = (static_cast<int64_t>(page) * p.h_kv * p.page_tokens + (slot - page * p.page_tokens)) *
                             (p.d * Out::kBytes);
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kRotThreads) append_rotated_kernel(RotateParam
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
       const int s = group + k * p.groups;
-      if (s >= p.slots || (s >= p.h_q && !held)) continue;
+      if (s >= wanted) continue;
       const char* src = from[k] + (s < p.h_q ? at_q : (s < p.h_q + p.h_kv ? at_k : at_v));
       va[k] = load8<In>(src);
       vb[k] = load8<In>(src + ab * In::kBytes);
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kRotThreads) append_rotated_kernel(RotateParam
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
       const int s = group + k * p.groups;
-      if (s >= p.slots || (s >= p.h_q && !held)) continue;
+      if (s >= wanted) continue;
       F8 x = floats8<In>(va[k]), y = floats8<In>(vb[k]);
       if (turns && s < p.h_q + p.h_kv) {
         if (p.interleaved) {
@@ -173,6 +174,12 @@ __global__ void __launch_bounds__(kRotThreads) append_rotated_kernel(RotateParam
         store8<In>(to[k] + at_out, x);
         store8<In>(to[k] + at_out + ab * In::kBytes, y);
       } else {
+        if (p.k_out && s < p.h_q + p.h_kv) {
+          char* const out = static_cast<char*>(p.k_out) + (t * p.k_out_stride + (s - p.h_q) * p.d + a) * In::kBytes;
+          store8<In>(out, x);
+          store8<In>(out + ab * In::kBytes, y);
+        }
+        if (!held) continue;
         const float inv = s < p.h_q + p.h_kv ? p.k_inv : p.v_inv;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {

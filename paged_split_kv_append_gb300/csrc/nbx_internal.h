@@ -126,10 +126,11 @@ struct RotateParams {
   const int32_t* positions;
   const int32_t* slot_mapping;
   void* q_out;
+  void* k_out;              // or null
   void* k_pool;
   void* v_pool;
   int32_t* status;
-  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
   int n_tok, h_q, h_kv, d, n_pos, turned, interleaved, num_pages, page_tokens;
   int slots;          // rows of a token: h_q + 2 h_kv
   int groups, block_groups, toks;   // set by the launch: groups of slots, of a CTA, tokens of a CTA at a time

@@ -10,7 +10,9 @@ With ``scale_tokens`` the pools are a block-scaled cache (E4M3 codes, a scale pe
 head), appended to by ``nbx_paged_kv_append_block_scaled`` and read by
 ``nbx_paged_decode_attn_block_scaled``; with score modifications (``set_modifications``) a decode is
 ``nbx_paged_decode_attn_modified``. ``fork`` and ``compact`` manage the rows and pages of the block table
-in place. Nothing here computes: torch provides memory and streams only.
+in place. ``append_rotated`` turns a prompt's (or a step's) queries and keys by their positions on the way into the pools,
+``prompt`` attends over packed prompts, and with ``set_groups`` decodes read what forked rows share once
+(``nbx_paged_decode_attn_shared``). Nothing here computes: torch provides memory and streams only.
 """
 
 from __future__ import annotations
@@ -20,10 +22,12 @@ from typing import Optional
 import torch
 
 from . import (NBX_BF16, NBX_E4M3, NBX_F32, _new, nbx_paged_decode_attn, nbx_paged_decode_attn_block_scaled,
-               nbx_paged_decode_attn_modified, nbx_paged_decode_modified_workspace_bytes,
+               nbx_paged_decode_attn_modified, nbx_paged_decode_attn_shared, nbx_paged_decode_modified_workspace_bytes,
+               nbx_paged_decode_shared_workspace_bytes,
                nbx_paged_decode_workspace_bytes_for, nbx_paged_kv_append, nbx_paged_kv_append_block_scaled,
+               nbx_paged_kv_append_rotated,
                nbx_paged_kv_compact, nbx_paged_kv_compact_workspace_bytes, nbx_paged_kv_fork,
-               nbx_paged_kv_fork_workspace_bytes)
+               nbx_paged_kv_fork_workspace_bytes, nbx_prompt_attn)
 
 POOL_TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.uint8}
 
@@ -41,10 +45,11 @@ def new_pool(num_pages: int, h_kv: int, page_tokens: int, d: int, dtype: str, de
 class PagedDecodeSession:
     def __init__(self, *, num_pages: int, h_kv: int, page_tokens: int, d: int, pool_dtype: str, batch: int,
                  rows: int, h_q: int, max_seq_len: int, device, fill_nan: bool = True, q_dtype: str = "bf16",
-                 scale_tokens: int = 0, modified: bool = False, out_dtype: torch.dtype = torch.float32):
+                 scale_tokens: int = 0, modified: bool = False, out_dtype: torch.dtype = torch.float32,
+                 shared_groups: int = 0):
         """scale_tokens: positions per scale of a block-scaled cache (pool_dtype "e4m3"), 0 for one scale per
-        pool. modified: size the workspace for score modifications. out_dtype: fp32, or bf16 for a session that is
-        block-scaled or modified."""
+        pool. modified: size the workspace for score modifications. shared_groups: most groups of sequences that share
+        prefixes (set_groups). out_dtype: fp32, or bf16 for a session that is block-scaled, modified or has groups."""
         self.device = torch.device(device)
         self.num_pages, self.h_kv, self.page_tokens, self.d = num_pages, h_kv, page_tokens, d
         self.pool_dtype = pool_dtype
@@ -60,12 +65,17 @@ class PagedDecodeSession:
             self.k_scales = torch.ones(shape, dtype=torch.float32, device=self.device)
             self.v_scales = torch.ones_like(self.k_scales)
         self.modified = modified or scale_tokens > 0
-        if out_dtype != torch.float32 and not self.modified:
+        self.shared_groups = shared_groups
+        if shared_groups and self.modified:
+            raise ValueError("groups that share prefixes go with plain decodes")
+        if out_dtype != torch.float32 and not self.modified and not shared_groups:
             raise ValueError("a plain decode's output is fp32")
         ws = nbx_paged_decode_workspace_bytes_for(codes[q_dtype], codes[pool_dtype], batch, rows, h_q, h_kv, d,
                                                   max_seq_len, page_tokens)
         if self.modified:
             ws = nbx_paged_decode_modified_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len)
+        if shared_groups:
+            ws = nbx_paged_decode_shared_workspace_bytes(batch, rows, h_q, h_kv, d, max_seq_len, shared_groups)
         if ws == 0 and batch > 0:
             raise ValueError("invalid decode sizes")
         self.workspace = torch.empty(max(ws, 256), dtype=torch.uint8, device=self.device)
@@ -76,6 +86,7 @@ class PagedDecodeSession:
         self.held = self.tok_start = None
         self.scale, self.k_scale, self.v_scale = 1.0, 1.0, 1.0
         self.modifications = {}
+        self.groups = None
         self._page_workspaces = []
 
     # ---------------------------------------------------------------- state
@@ -88,6 +99,20 @@ class PagedDecodeSession:
         self._fits("append", False)
         nbx_paged_kv_append(new_k, new_v, self.k_pool, self.v_pool, slots, self.k_scale, self.v_scale,
                             status=self.status, stream=stream)
+
+    def append_rotated(self, q: Optional[torch.Tensor], new_k: torch.Tensor, new_v: torch.Tensor, cos: torch.Tensor,
+                       sin: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor, interleaved: bool = False,
+                       q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+        """append with queries and keys turned by their positions on the way; returns the turned queries."""
+        self._fits("append_rotated", False)
+        return nbx_paged_kv_append_rotated(q, new_k, new_v, cos, sin, positions, self.k_pool, self.v_pool, slots,
+                                           self.k_scale, self.v_scale, interleaved, q_out=q_out, k_out=k_out,
+                                           status=self.status, stream=stream)
+
+    def prompt(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start: torch.Tensor,
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Causal attention over packed prompts (their own keys and values, not the pools')."""
+        return nbx_prompt_attn(q, k, v, seq_start, self.scale, out=out, status=self.status, stream=stream)
 
     def prefill(self, k_raw: torch.Tensor, v_raw: torch.Tensor, index, slots, chunk_tokens: int = 1 << 18) -> None:
         """Append the tokens k_raw[index] at the given slots, in chunks (index/slots on the host)."""
@@ -146,6 +171,16 @@ class PagedDecodeSession:
             raise ValueError("the session was not made for score modifications")
         self.modifications = dict(softcap=softcap, slopes=slopes, key_begin=key_begin, key_end=key_end)
 
+    def set_groups(self, group_start: Optional[torch.Tensor], shared_lens: Optional[torch.Tensor]) -> None:
+        """Decodes from here on read the first shared_lens[g] positions of sequences group_start[g] .. group_start[g + 1] - 1
+        once (int32 device tensors), or, with None, each sequence's by themselves."""
+        if group_start is None and shared_lens is None:
+            self.groups = None
+            return
+        if not self.shared_groups or shared_lens.numel() > self.shared_groups:
+            raise ValueError("the session was not made for so many groups")
+        self.groups = group_start, shared_lens
+
     # ---------------------------------------------------------------- rows and pages
     def _page_scratch(self, stream) -> torch.Tensor:
         """The workspace of forks (of up to a row each) and compactions. One that a larger table outgrows is kept beside
@@ -169,12 +204,20 @@ class PagedDecodeSession:
                                     status=self.status, stream=stream)[1:]
 
     # ---------------------------------------------------------------- the step
+    def _no_groups(self, n: int) -> torch.Tensor:
+        return torch.zeros(n, dtype=torch.int32, device=self.device)
+
     def decode(self, stream=None) -> torch.Tensor:
         if self.k_scales is not None:
             return nbx_paged_decode_attn_block_scaled(self.q, self.k_pool, self.v_pool, self.k_scales, self.v_scales,
                                                       self.block_table, self.seq_lens, self.max_seq_len, self.scale,
                                                       out=self.out, workspace=self.workspace, status=self.status,
                                                       stream=stream, **self.modifications)
+        if self.shared_groups:
+            start, shared = self.groups or (self._no_groups(1), self._no_groups(0))
+            return nbx_paged_decode_attn_shared(self.q, self.k_pool, self.v_pool, self.block_table, self.seq_lens,
+                                                self.max_seq_len, start, shared, self.scale, self.k_scale, self.v_scale,
+                                                out=self.out, workspace=self.workspace, status=self.status, stream=stream)
         if self.modified:
             return nbx_paged_decode_attn_modified(self.q, self.k_pool, self.v_pool, self.block_table, self.seq_lens,
                                                   self.max_seq_len, self.scale, self.k_scale, self.v_scale,

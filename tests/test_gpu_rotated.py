@@ -126,6 +126,23 @@ def test_queries_in_place_and_keys_alone(interleaved):
     assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(pools, pools2))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("with_q", [False, True])
+def test_turned_keys_beside_the_pool(interleaved, in_place, with_q):
+    q, k, v, cos, sin, at, pools, slots = case(70, 4, 2, 64, 32, 16, "bf16", "e4m3", 15)
+    slots[3] = -1                            # no place in the pool: its keys and queries are turned all the same
+    was, before = k.clone(), [p.clone() for p in pools]
+    k_out = k if in_place else torch.full_like(was, 9.0)
+    out = nbx.nbx_paged_kv_append_rotated(q if with_q else None, k, v, cos, sin, at, *pools, slots, 0.02, 0.02, interleaved,
+                                          k_out=k_out)
+    near(k_out, *turn(was, cos, sin, at, interleaved), 1)
+    if with_q:
+        near(out, *turn(q, cos, sin, at, interleaved), 1)
+    keep = torch.arange(70, device=DEV) != 3
+    check(None, was[keep], v[keep], cos, sin, at[keep], pools, before, slots[keep], None, 0.02, 0.02, interleaved)
+
+
 def test_an_angle_of_zero_is_the_plain_append():
     q, k, v, cos, sin, at, pools, slots = case(50, 4, 2, 128, 128, 16, "f32", "e4m3", 6, fused=False)
     plain = [p.clone() for p in pools]
@@ -217,6 +234,8 @@ def test_refusals_of_the_binding():
                 lambda: call(q, k, v, cos, sin, at.long(), *pools, slots), lambda: call(q[:3], k, v, cos, sin, at, *pools, slots),
                 lambda: call(q.transpose(0, 1), k, v, cos, sin, at, *pools, slots), lambda: call(q, k[..., :32], v[..., :32], cos, sin, at, *pools, slots),
                 lambda: call(None, k, v, cos, sin, at, *pools, slots, q_out=q),
+                lambda: call(q, k, v, cos, sin, at, *pools, slots, k_out=q),
+                lambda: call(q, k, v, cos, sin, at, *pools, slots, k_out=k.float()),
                 lambda: call(q, k, v, cos, sin, at, *pools, slots, status=at[4:]),
                 lambda: call(q, k, v, cos, sin, at, pools[0], pools[1][:1], slots),
                 lambda: call(q, k, v, cos.cpu(), sin, at, *pools, slots)):

@@ -20,7 +20,7 @@ def lib():
 
 CALL = dict(q=FAKE, q_stride=1024, h_q=8, new_k=FAKE, k_stride=256, new_v=FAKE, v_stride=256, new_dtype=1, n_tok=4, h_kv=2,
             d=128, cos=FAKE, sin=FAKE, n_pos=100, turned=128, interleaved=0, positions=FAKE, q_out=FAKE, q_out_stride=1024,
-            k_pool=FAKE, v_pool=FAKE, pool_dtype=1, num_pages=8, page_tokens=16, slots=FAKE, k_scale=1.0, v_scale=1.0,
+            k_out=FAKE, k_out_stride=256, k_pool=FAKE, v_pool=FAKE, pool_dtype=1, num_pages=8, page_tokens=16, slots=FAKE, k_scale=1.0, v_scale=1.0,
             status=NULL, stream=NULL)
 
 
@@ -31,7 +31,7 @@ CALL = dict(q=FAKE, q_stride=1024, h_q=8, new_k=FAKE, k_stride=256, new_v=FAKE, 
     (-2, dict(d=8)), (-2, dict(d=72)), (-2, dict(d=2048)), (-2, dict(num_pages=0)), (-2, dict(page_tokens=0)),
     (-2, dict(n_pos=0)), (-2, dict(turned=0)), (-2, dict(turned=24)), (-2, dict(turned=144)), (-2, dict(q_stride=1016)),
     (-2, dict(k_stride=255)), (-2, dict(v_stride=260)), (-2, dict(q_out_stride=1028)), (-3, dict(new_dtype=2)),
-    (-3, dict(pool_dtype=5)), (-7, dict(q=FAKE_ODD)), (-7, dict(sin=FAKE_ODD)), (-7, dict(k_pool=FAKE_ODD)),
+    (-3, dict(pool_dtype=5)), (-2, dict(k_out_stride=252)), (0, dict(k_out_stride=252, n_tok=0, k_out=NULL)), (-7, dict(q=FAKE_ODD)), (-7, dict(k_out=FAKE_ODD)), (-7, dict(sin=FAKE_ODD)), (-7, dict(k_pool=FAKE_ODD)),
     (-8, dict(k_scale=0.0)), (-8, dict(v_scale=float("inf"))), (-8, dict(interleaved=2))])
 def test_refusals(lib, want, kw):
     a = dict(CALL)
