@@ -611,7 +611,8 @@ NBX_API void nbx_set_decode_grid_limit(int max_ctas);
 
 /*
  * nbx_set_decode_wait_test -- for tests of the timeout path only; the pages have no counterpart.
- * Every wait inside the split-partial kernels is bounded (2 s by default): a wait that runs out
+ * Every wait inside the split-partial kernels, and inside those of prompts and of shared prefixes, is
+ * bounded (2 s by default): a wait that runs out
  * sets NBX_DEV_TIMEOUT, the kernel lets its copies in flight land (and, on tensor cores, its MMAs
  * complete and its TMEM go back) and returns, and the output of the call is incomplete. This sets
  * that bound (wait_limit_ns; 0 restores 2 s) and holds each CTA's producer warps back for

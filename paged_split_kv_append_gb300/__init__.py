@@ -381,8 +381,8 @@ def nbx_set_decode_grid_limit(max_ctas: int) -> None:
 
 
 def nbx_set_decode_wait_test(wait_limit_ns: int = 0, producer_delay_ns: int = 0) -> None:
-    """Tests of the timeout path only: the SIMT partial kernel's wait bound (0 = the default 2 s) and
-    a delay before its producer warps start (0 = none)."""
+    """Tests of the timeout path only: the wait bound of the partial, prompt and prefix kernels (0 = the
+    default 2 s) and a delay before their producer warps start (0 = none)."""
     lib().nbx_set_decode_wait_test(int(wait_limit_ns), int(producer_delay_ns))
 
 

@@ -205,6 +205,8 @@ NBX_API int nbx_prompt_attn(const void* q, int64_t q_stride, const void* k, int6
   p.d = d;
   p.batch = batch;
   p.scale_log2 = scale * kLog2eHost;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  p.producer_delay_ns = g_producer_delay_ns.load();
   const cudaError_t e = prompt_dispatch(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? NBX_OK : NBX_ERR_CUDA;
 }

@@ -65,7 +65,7 @@ struct AttnCfg {
   static constexpr int kRawBytes = F8 ? N * D : 0;               // a tile of codes
   static constexpr int kRaws = F8 ? 4 : 0;
   static constexpr int kRoom = 224 * 1024 - kTiles * kQTile - kRaws * kRawBytes;
-  static constexpr int kMost = kTiles == 2 ? 8 : (F8 ? 5 : 6);   // (d = 256: what the barriers and xbuf leave)
+  static constexpr int kMost = F8 ? (kTiles == 2 ? 6 : 5) : (kTiles == 2 ? 8 : 6);   // (what the barriers and xbuf leave)
   static constexpr int kSlots = kRoom / kSlotBytes < kMost ? kRoom / kSlotBytes : kMost;
   static constexpr int kRingOff = kTiles * kQTile;
   static constexpr int kRawOff = kRingOff + kSlots * kSlotBytes;
@@ -77,7 +77,7 @@ struct AttnCfg {
   static constexpr uint32_t kOCol = 2 * kAtBuf;                  // S (and P) in columns [0, 256), O from there
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kSlots >= 3, "ring");
-  static_assert((2 * kSlots + 2 * kRaws + 18) * 8 <= kBarBytes, "barrier area");
+  static_assert((2 * kSlots + 2 * kRaws + 18) * 8 <= kBarBytes - 64, "barrier area");
 };
 
 // One work unit. (It is moved as 16-byte words: where it lies in local memory, too, it is aligned to them.)
@@ -96,12 +96,22 @@ struct alignas(16) AttnUnit {
 };
 static_assert(sizeof(AttnUnit) == 64, "a unit is four 16-byte words");
 
-// Bounded wait of a whole warp, with one answer: gives up when another role of the CTA has, or after kWaitLimitNs. Every
-// branch is on a vote, so the compiler knows the warp to be together behind it (and may use uniform registers there).
+// What the roles of a CTA share beside barriers, in shared memory.
+struct AttnControl {
+  int abort;          // some role has given up
+  uint32_t tmem;      // TMEM's first column
+  uint64_t wait_ns;   // how long a wait may take
+};
+__device__ __forceinline__ const volatile AttnControl* volatile_of(const AttnControl* c) { return c; }
+__device__ __forceinline__ void volatile_set(AttnControl* c) { static_cast<volatile AttnControl*>(c)->abort = 1; }
+
+// Bounded wait of a whole warp, with one answer: gives up when another role of the CTA has, or after the limit (2 s, but in
+// a test of this path). Every branch is on a vote, so the compiler knows the warp to be together behind it (and may use
+// uniform registers there).
 // The loop is a function, one for all sites of the warps beside the softmax (whose registers leave no room for a call): up to
 // fourteen warps wait at a time, and loops of their own pushed the others' code out of the instruction caches (stalls for
 // want of an instruction were a third of a shared E4M3 prefix's cycles).
-__device__ __forceinline__ bool at_wait_loop(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool at_wait_loop(uint32_t bar, uint32_t parity, const AttnControl* ctl) {
   const uint64_t t0 = global_timer_ns();
   for (;;) {
     uint32_t ok = 0;
@@ -117,17 +127,17 @@ __device__ __forceinline__ bool at_wait_loop(uint32_t bar, uint32_t parity, vola
       ok = __all_sync(0xffffffffu, ok != 0);
     }
     if (ok) return true;
-    if (__any_sync(0xffffffffu, *abort_flag != 0 || global_timer_ns() - t0 > kWaitLimitNs)) return false;
+    if (__any_sync(0xffffffffu, volatile_of(ctl)->abort != 0 || global_timer_ns() - t0 > ctl->wait_ns)) return false;
   }
 }
-__device__ __noinline__ bool at_wait_call(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  return at_wait_loop(bar, parity, abort_flag);
+__device__ __noinline__ bool at_wait_call(uint32_t bar, uint32_t parity, const AttnControl* ctl) {
+  return at_wait_loop(bar, parity, ctl);
 }
 template <bool kCall = true>
-__device__ __forceinline__ bool at_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool at_warp_wait(uint64_t* bar, uint32_t parity, const AttnControl* ctl) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  if constexpr (kCall) return __all_sync(0xffffffffu, at_wait_call(smem_u32(bar), parity, abort_flag));
-  return at_wait_loop(smem_u32(bar), parity, abort_flag);
+  if constexpr (kCall) return __all_sync(0xffffffffu, at_wait_call(smem_u32(bar), parity, ctl));
+  return at_wait_loop(smem_u32(bar), parity, ctl);
 }
 // x, the same in every lane of the warp, as a value that the compiler knows to be
 __device__ __forceinline__ int at_uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
@@ -231,17 +241,17 @@ struct AttnShared {
   uint64_t* raw_full;  // [kRaws] a tile's codes have landed
   uint64_t* raw_empty; // [kRaws] and are converted
   uint64_t* x_bar;     // [4] d = 256: the two warps of 32 rows have left their numbers
-  volatile int* abort_flag;
-  uint32_t* tmem_slot;
+  AttnControl* ctl;
   float* xbuf;         // [2][256]
 };
 
 // ---------------------------------------------------------------- units
-// The k-th unit of this CTA, to every warp that asks (W::kReaders of them): false behind the last.
+// The k-th unit of this CTA, to every warp that asks: false behind the last, and when the wait for it ran out (which the
+// abort flag says).
 template <bool kCall = true, class C>
 __device__ __forceinline__ bool at_unit(const AttnShared<C>& sh, uint32_t k, AttnUnit& u) {
-  if (!at_warp_wait<kCall>(&sh.unit_full[k & 1u], (k >> 1) & 1u, sh.abort_flag)) {
-    *sh.abort_flag = 1;
+  if (!at_warp_wait<kCall>(&sh.unit_full[k & 1u], (k >> 1) & 1u, sh.ctl)) {
+    volatile_set(sh.ctl);
     return false;
   }
   uint4* const to = reinterpret_cast<uint4*>(&u);
@@ -261,7 +271,7 @@ __device__ __forceinline__ bool attn_units(W& w, const AttnShared<C>& sh, F each
     AttnUnit u = {};
     more = w.unit(k, u);
     if (!more) u.toks = 0;
-    if (k >= 2 && !at_warp_wait(&sh.unit_empty[k & 1u], ((k >> 1) - 1) & 1u, sh.abort_flag)) return false;
+    if (k >= 2 && !at_warp_wait(&sh.unit_empty[k & 1u], ((k >> 1) - 1) & 1u, sh.ctl)) return false;
     if ((threadIdx.x & 31) == 0) {
       const uint4* const from = reinterpret_cast<const uint4*>(&u);
       const uint32_t to = smem_u32(sh.units + (k & 1u));
@@ -326,7 +336,7 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
   const uint32_t one = lane == 0;    // the lane that issues
   const int t = T == 2 ? which : 0;
   const bool does_pv = T == 2 || which == 0, does_qk = T == 2 || which == 1;
-  volatile int* ab = sh.abort_flag;
+  const AttnControl* ab = sh.ctl;
   const uint32_t ring = smem_u32(sh.ring);
   const uint64_t q_desc = smem_desc(smem_u32(sh.q_s) + t * C::kQTile, 16, 1024);
   const uint64_t k_desc = smem_desc(ring, 16, 1024), v_desc = smem_desc(ring, kAtomBytes, 1024);
@@ -566,7 +576,7 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
   const int tpt = w.toks_per_tile();
   const int tok = row / w.heads(), head = row - tok * w.heads();
   float c = w.p.c;
-  volatile int* ab = sh.abort_flag;
+  const AttnControl* ab = sh.ctl;
   uint32_t x = 0;         // key tiles of this M tile so far
   uint32_t xphase = 0;
   // d = 256: swaps a number with the other thread of the row. What each did before is visible to the other then, its
@@ -760,10 +770,10 @@ __device__ __forceinline__ bool attn_convert(W& w, const AttnShared<C>& sh, int 
   AttnUnit u;
   for (uint32_t k = 0; at_unit(sh, k, u); ++k) {
     const bool ok = at_each_tile<C>(u, [&](bool is_v, int, int) -> bool {
-      if (!at_warp_wait(&sh.raw_full[x % C::kRaws], (x / C::kRaws) & 1u, sh.abort_flag)) return false;
+      if (!at_warp_wait(&sh.raw_full[x % C::kRaws], (x / C::kRaws) & 1u, sh.ctl)) return false;
       const char* raw = sh.raw + (x % C::kRaws) * C::kRawBytes;
       for (int part = 0; part < C::kParts; ++part, ++r) {
-        if (r >= NS && !at_warp_wait(&sh.empty[r % NS], (r / NS - 1) & 1u, sh.abort_flag)) return false;
+        if (r >= NS && !at_warp_wait(&sh.empty[r % NS], (r / NS - 1) & 1u, sh.ctl)) return false;
         char* dst = sh.ring + (r % NS) * C::kSlotBytes;
         // the part's rows and atoms: at d = 256 two atoms of every row of K, half of V's rows
         const bool half_v = C::kParts == 2 && is_v;
@@ -808,11 +818,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   sh.unit_full = sh.q_full + 14;
   sh.unit_empty = sh.q_full + 16;
   sh.units = reinterpret_cast<AttnUnit*>(smem + C::kUnitOff);
-  sh.abort_flag = reinterpret_cast<int*>(sh.q_full + 11);
-  sh.tmem_slot = reinterpret_cast<uint32_t*>(sh.q_full + 11) + 1;
+  sh.ctl = reinterpret_cast<AttnControl*>(sh.full + (C::kBarBytes - 64) / 8);   // (before x_bar)
   sh.x_bar = reinterpret_cast<uint64_t*>(smem + C::kUnitOff) - 4;   // d = 256 (whose ring is short): behind them
   sh.xbuf = reinterpret_cast<float*>(smem + C::kXOff);
-  static_assert(C::kTiles == 2 || (2 * NS + 2 * C::kRaws + 20) * 8 <= C::kBarBytes, "barrier area");
   const int warp = at_uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -842,17 +850,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       for (int i = 0; i < 2; ++i) mbar_init(&sh.turn[i], 1);
     if constexpr (C::kTiles == 1)
       for (int i = 0; i < 4; ++i) mbar_init(&sh.x_bar[i], 2);
-    *sh.abort_flag = 0;
+    sh.ctl->abort = 0;
+    sh.ctl->wait_ns = params.wait_ns();
     fence_mbar_init();
   }
   if (warp == 9) {
-    tmem_alloc(smem_u32(sh.tmem_slot), 512);
+    tmem_alloc(smem_u32(&sh.ctl->tmem), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = at_uniform(*sh.tmem_slot);
+  const uint32_t tmem = at_uniform(volatile_of(sh.ctl)->tmem);
   // the inputs are written and visible from here on. (kWaitLate: they were before the grid ahead began, which this one
   // may run beside; the grid behind waits for both through this one)
   if constexpr (!W::kWaitLate) pdl_wait();
@@ -874,10 +883,14 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       uint64_t* const empty = W::kF8 ? sh.raw_empty : sh.empty;
       char* const ring = W::kF8 ? sh.raw : sh.ring;
       const int loader = kCopies ? warp - 12 : (warp == 11);
+      if (params.delay_ns() != 0) {   // a test holds the loaders back so that the other roles' waits run out
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < params.delay_ns()) __nanosleep(10000);
+      }
       uint32_t r = 0, q_units = 0, phase = 1;   // (the first round finds every slot empty)
       int slot = 0;
       auto next_q = [&](const AttnUnit& u) -> bool {
-        if (q_units > 0 && !at_warp_wait(sh.q_empty, (q_units - 1) & 1u, sh.abort_flag)) return false;
+        if (q_units > 0 && !at_warp_wait(sh.q_empty, (q_units - 1) & 1u, sh.ctl)) return false;
         w.template load_q<C>(u, sh.q_s, sh.q_full);
         ++q_units;
         return true;
@@ -887,7 +900,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
         return at_each_tile<C>(u, [&](bool is_v, int t, int j) -> bool {
 #pragma unroll 1
           for (int part = 0; part < kPieces; ++part, ++r) {
-            if (r >= kDepth && !at_warp_wait(&empty[slot], phase, sh.abort_flag)) return false;
+            if (r >= kDepth && !at_warp_wait(&empty[slot], phase, sh.ctl)) return false;
             w.template load_kv<C>(u, is_v, t, j, part, ring + slot * kBytes, &full[slot], loader);
             if (++slot == kDepth) {
               slot = 0;
@@ -910,7 +923,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
         AttnUnit u;
         for (uint32_t k = 0; ok && at_unit(sh, k, u); ++k) ok = kCopies && warp == 8 ? next_q(u) : tiles(u);
       }
-      if (!ok) *sh.abort_flag = 1;
+      if (!ok) volatile_set(sh.ctl);
       // the copies issued last have landed before the CTA can exit
       if constexpr (W::kPaged) cp_async_wait_all();
       if (lane == 0) {
@@ -921,7 +934,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
     } else if (warp == 9 || warp == 10) {
       W w(params);
       ok = attn_mma<W, C, D>(w, sh, tmem, warp - 9);
-      if (!ok) *sh.abort_flag = 1;
+      if (!ok) volatile_set(sh.ctl);
       // every MMA of this CTA has completed before the TMEM is released
       at_commit(sh.done, lane == 0);
       mbar_wait(sh.done, 0, 100000000ull);
@@ -933,13 +946,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       }
     }
   }
-  if (!ok) {
-    *sh.abort_flag = 1;
-    if (lane == 0) raise_status(params.status, NBX_DEV_TIMEOUT);
-  }
+  if (!ok) volatile_set(sh.ctl);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (threadIdx.x == 0 && volatile_of(sh.ctl)->abort != 0) raise_status(params.status, NBX_DEV_TIMEOUT);
   if (warp == 9) tmem_dealloc(tmem, 512);
   if constexpr (W::kWaitLate) pdl_wait();
 }

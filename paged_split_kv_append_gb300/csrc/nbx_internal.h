@@ -150,6 +150,8 @@ struct PromptParams {
   int64_t q_stride, k_stride, v_stride;
   int n_tok, h_q, h_kv, d, batch;
   float scale_log2;           // scale * log2(e)
+  uint64_t wait_limit_ns;     // as DecodeParams'
+  uint64_t producer_delay_ns;
 };
 
 cudaError_t prompt_dispatch(const PromptParams& p, cudaStream_t stream);

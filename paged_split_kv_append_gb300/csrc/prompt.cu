@@ -28,6 +28,8 @@ struct PromptTilesParams {
   int negative;       // the scale is
   int32_t* status;
   int heads, sets;    // query heads of a tile; h_q / heads
+  __device__ __forceinline__ uint64_t wait_ns() const { return a.wait_limit_ns; }
+  __device__ __forceinline__ uint64_t delay_ns() const { return a.producer_delay_ns; }
 };
 
 template <int D>

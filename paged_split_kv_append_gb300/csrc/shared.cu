@@ -29,6 +29,8 @@ struct PrefixParams {
   int negative;
   int32_t* status;
   int heads, sets;    // query heads of a tile; h_q / heads
+  __device__ __forceinline__ uint64_t wait_ns() const { return a.wait_limit_ns; }
+  __device__ __forceinline__ uint64_t delay_ns() const { return a.producer_delay_ns; }
 };
 
 // Query heads of one tile: the whole group, if it fits, so that few sequences fill few tiles.
