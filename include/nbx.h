@@ -120,9 +120,10 @@ NBX_API int nbx_paged_kv_append(const void* new_k, const void* new_v, int new_dt
  *   cos_table, sin_table [device] fp32 [n_pos, turned / 2]
  *   positions    [device] int32 [n_tok]; a position outside [0, n_pos) sets NBX_DEV_BAD_LEN and the token is
  *                skipped (in q_out and k_out too)
- *   q_out        [device] as q with q_out_stride; may be q itself (with q's stride)
+ *   q_out        [device] as q with q_out_stride; may be q itself (with q's stride), but not overlap an input otherwise
  *   k_out        [device] the turned keys once more, in new_dtype and unscaled, as new_k with k_out_stride (for the
- *                attention of the prompt that they belong to); may be new_k itself (with its stride), or NULL
+ *                attention of the prompt that they belong to); may be new_k itself (with its stride), but not overlap
+ *                an input otherwise; or NULL
  *   slot_mapping [device] int32 [n_tok]; a slot outside the pool sets NBX_DEV_BAD_SLOT, the pools are left alone and
  *                q_out and k_out written all the same
  *   the other arguments as for nbx_paged_kv_append
@@ -153,7 +154,8 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
  *   seq_start    [device] int32 [batch + 1], ascending, seq_start[0] >= 0, seq_start[batch] <= n_tok. A sequence whose
  *                bounds make no sense sets NBX_DEV_BAD_LEN and is skipped.
  *   scale        softmax scale (finite)
- *   out          [device] bf16 [n_tok, h_q, d], contiguous; rows of no sequence are left as they were
+ *   out          [device] bf16 [n_tok, h_q, d], contiguous; rows of no sequence are left as they were. May not overlap q, k
+ *                or v (NBX_ERR_VALUE).
  *   status       [device] int32 or NULL;  stream  cudaStream_t
  * Requirements: h_q % h_kv == 0; d in {64, 128, 256}; buffers and rows 16-byte aligned (strides of whole 16 bytes), out
  * 32-byte aligned. n_tok == 0 or batch == 0 returns NBX_OK without a launch.
@@ -441,12 +443,14 @@ NBX_API int nbx_paged_decode_attn_modified(const void* q, int q_dtype, int batch
  * common prefix (a row that holds other pages there is read as if it held the first row's). Sequences of no group, groups
  * of one and short prefixes are read sequence by sequence; empty sequences may lie in a group.
  * Prefixes are read apart for bf16 and E4M3 pools under bf16 queries, on the tensor cores: a bf16 output takes the
- * prefix's weights rounded to 2^-8, an fp32 one to 2^-17 or better. Elsewhere the groups are ignored.
+ * prefix's weights rounded to 2^-8 and each split's share of it to 2^-8, an fp32 one the weights to 2^-22 of the
+ * largest. Elsewhere the groups are ignored.
  *
  *   group_start  [device] int32 [n_groups + 1], ascending, within [0, batch]
  *   shared_lens  [device] int32 [n_groups], >= 0. Groups that make no sense set NBX_DEV_BAD_ROW and none counts.
  *   workspace    [device] nbx_paged_decode_shared_workspace_bytes(...) bytes, 256-byte aligned
- *   every other argument, rule and status bit as for nbx_paged_decode_attn_modified without a modification
+ *   every other argument, rule and status bit as for nbx_paged_decode_attn_modified without a modification, but that out
+ *                is 32-byte aligned
  */
 NBX_API size_t nbx_paged_decode_shared_workspace_bytes(int batch, int rows, int h_q, int h_kv, int d, int max_seq_len,
                                                        int n_groups);

@@ -141,6 +141,9 @@ NBX_API int nbx_paged_kv_append_rotated(const void* q, int64_t q_stride, int h_q
   if (!aligned16(q) || !aligned16(new_k) || !aligned16(new_v) || !aligned16(cos_table) || !aligned16(sin_table) ||
       !aligned16(q_out) || !aligned16(k_out) || !aligned16(k_pool) || !aligned16(v_pool))
     return NBX_ERR_ALIGN;
+  // in place: each token over itself
+  if (n_tok > 1 && ((h_q > 0 && q_out == q && q_out_stride != q_stride) || (k_out == new_k && k_out_stride != k_stride)))
+    return NBX_ERR_VALUE;
   RotateParams p = {};
   p.q = q;
   p.new_k = new_k;
@@ -188,6 +191,12 @@ NBX_API int nbx_prompt_attn(const void* q, int64_t q_stride, const void* k, int6
   if (!q || !k || !v || !seq_start || !out) return NBX_ERR_NULL;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return NBX_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(out) & 31u) != 0) return NBX_ERR_ALIGN;   // written 32 bytes at a time
+  auto over_out = [&](const void* p, int64_t stride, int heads) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), o = reinterpret_cast<uintptr_t>(out);
+    const uintptr_t last = n_tok > 1 ? static_cast<uintptr_t>(stride) * (n_tok - 1) : 0;
+    return a < o + static_cast<uintptr_t>(n_tok) * h_q * d * 2 && o < a + (last + static_cast<uintptr_t>(heads) * d) * 2;
+  };
+  if (over_out(q, q_stride, h_q) || over_out(k, k_stride, h_kv) || over_out(v, v_stride, h_kv)) return NBX_ERR_VALUE;
   PromptParams p = {};
   p.q = q;
   p.k = k;
@@ -323,6 +332,7 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
   SharedLayout sw = {};
   if (groups) {
     if (groups->n_groups > 0 && (!groups->group_start || !groups->shared_lens)) return NBX_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(out) & 31u) != 0) return NBX_ERR_ALIGN;   // without groups written 32 bytes at a time
     if (!finite(scale * k_scale * kLog2eHost)) return NBX_ERR_VALUE;
     if (!shared_layout(batch, rows, h_q, h_kv, d, max_seq_len, groups->n_groups, &sw)) return NBX_ERR_SHAPE;
     if (workspace_bytes < sw.total) return NBX_ERR_WORKSPACE;

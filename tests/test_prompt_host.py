@@ -40,3 +40,17 @@ def test_the_binding_refuses_host_tensors():
     x = torch.zeros((4, 1, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
         nbx.nbx_prompt_attn(x, x, x, torch.zeros(2, dtype=torch.int32), 1.0)
+
+
+def far(n):
+    return ctypes.c_void_p(0x10000 + n)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=FAKE), dict(out=far(40 * 2048 - 32)), dict(q=far(1 << 20), out=far(39 * 512 + 480)),
+    dict(q=far(1 << 20), k=far(1 << 21), out=far(32)), dict(q=far(40 * 2048 - 16), k=far(1 << 21), v=far(1 << 22)),
+    dict(n_tok=1, q_stride=0, k_stride=0, v_stride=0, out=far(2016))], ids=str)
+def test_an_output_over_an_input_is_refused(lib, kw):
+    a = dict(CALL)
+    a.update(kw)
+    assert lib.nbx_prompt_attn(*a.values()) == -8

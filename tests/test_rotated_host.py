@@ -46,3 +46,11 @@ def test_the_binding_refuses_host_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         nbx.nbx_paged_kv_append_rotated(None, x, x, torch.zeros(4, 32), torch.zeros(4, 32), i, torch.zeros(1, 1, 16, 64),
                                         torch.zeros(1, 1, 16, 64), i)
+
+
+@pytest.mark.parametrize("kw", [dict(q_out_stride=2048), dict(q_stride=2048), dict(k_out_stride=512),
+                                dict(k_stride=512, k_out_stride=256)], ids=str)
+def test_in_place_with_another_stride_is_refused(lib, kw):
+    a = dict(CALL)
+    a.update(kw)
+    assert lib.nbx_paged_kv_append_rotated(*a.values()) == -8

@@ -46,3 +46,8 @@ def test_workspace(lib):
     n = f(4, 1, 8, 2, 128, 160, 2)
     assert n >= lib.nbx_paged_decode_modified_workspace_bytes(4, 1, 8, 2, 128, 160)
     assert call(lib, ws_bytes=n - 1) == -5
+
+
+def test_an_output_of_16_byte_alignment_is_refused(lib):
+    assert call(lib, out=ctypes.c_void_p(0x10010)) == -7
+    assert call(lib, out=ctypes.c_void_p(0x10010), n_groups=0) == -7
