@@ -956,27 +956,31 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
 }
 
 // ---- host side
-PFN_cuTensorMapEncodeTiled_v12000 at_encode_fn() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  }();
-  return fn;
+template <class Fn>
+Fn at_driver_fn(const char* name) {
+  void* f = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion(name, &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<Fn>(f);
 }
 
 // A tiled bf16 map with 128-byte swizzle; dims and box innermost first, strides in bytes for dims 1...
 bool at_encode(CUtensorMap* map, int rank, const void* base, const cuuint64_t* dims, const cuuint64_t* strides,
                const cuuint32_t* box) {
-  const PFN_cuTensorMapEncodeTiled_v12000 fn = at_encode_fn();
+  static const auto fn = at_driver_fn<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled");
   if (fn == nullptr) return false;
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same map over another address.
+bool at_rebase(CUtensorMap* map, const void* base) {
+  static const auto fn = at_driver_fn<PFN_cuTensorMapReplaceAddress_v12000>("cuTensorMapReplaceAddress");
+  return fn != nullptr && fn(map, const_cast<void*>(base)) == CUDA_SUCCESS;
 }
 
 template <class W, int D>

@@ -218,35 +218,38 @@ bool encode_maps(PromptTilesParams* m) {
   return at_encode(&m->k, 4, a.k, dims, k_str, k_box) && at_encode(&m->v, 4, a.v, dims, v_str, v_box);
 }
 
-// The maps of the last few calls from this host thread, keyed by everything they encode: three encodings cost a call a
-// few microseconds.
+// The maps of the last few shapes from this host thread, put over a call's addresses: three encodings cost a call a few
+// microseconds.
 struct PromptKey {
-  const void *q, *k, *v;
   int64_t qs, ks, vs;
-  int n_tok, h_q, h_kv, d, device;
+  int n_tok, h_q, h_kv, d;
   bool operator==(const PromptKey& o) const {
-    return q == o.q && k == o.k && v == o.v && qs == o.qs && ks == o.ks && vs == o.vs && n_tok == o.n_tok && h_q == o.h_q &&
-           h_kv == o.h_kv && d == o.d && device == o.device;
+    return qs == o.qs && ks == o.ks && vs == o.vs && n_tok == o.n_tok && h_q == o.h_q && h_kv == o.h_kv && d == o.d;
   }
 };
 
-const PromptTilesParams* prompt_maps(const PromptParams& a, int heads, int device) {
+bool prompt_maps(PromptTilesParams* p) {
   constexpr int kEntries = 8;
   thread_local PromptKey keys[kEntries];
-  thread_local PromptTilesParams maps[kEntries];
+  thread_local CUtensorMap maps[kEntries][3];
   thread_local int used = 0, next = 0;
-  const PromptKey key{a.q, a.k, a.v, a.q_stride, a.k_stride, a.v_stride, a.n_tok, a.h_q, a.h_kv, a.d, device};
-  for (int i = 0; i < used; ++i)
-    if (keys[i] == key) return &maps[i];
-  const int at = next;
+  const PromptParams& a = p->a;
+  const PromptKey key{a.q_stride, a.k_stride, a.v_stride, a.n_tok, a.h_q, a.h_kv, a.d};
+  for (int i = 0; i < used; ++i) {
+    if (!(keys[i] == key)) continue;
+    p->q = maps[i][0];
+    p->k = maps[i][1];
+    p->v = maps[i][2];
+    return at_rebase(&p->q, a.q) && at_rebase(&p->k, a.k) && at_rebase(&p->v, a.v);
+  }
+  if (!encode_maps(p)) return false;
+  keys[next] = key;
+  maps[next][0] = p->q;
+  maps[next][1] = p->k;
+  maps[next][2] = p->v;
   next = (next + 1) % kEntries;
   if (used < kEntries) ++used;
-  keys[at] = PromptKey{};   // not valid until encoded
-  maps[at].a = a;
-  maps[at].heads = heads;
-  if (!encode_maps(&maps[at])) return nullptr;
-  keys[at] = key;
-  return &maps[at];
+  return true;
 }
 
 template <int D>
@@ -254,15 +257,14 @@ cudaError_t launch_prompt(const PromptParams& a, cudaStream_t stream) {
   const DeviceInfo& di = device_info();
   int heads = a.h_q / a.h_kv;
   heads = std::min(heads & -heads, kAtM);   // the largest power of two in the group
-  const PromptTilesParams* maps = prompt_maps(a, heads, di.device);
-  if (maps == nullptr) return cudaErrorInvalidValue;
-  PromptTilesParams p = *maps;
+  PromptTilesParams p;
   p.a = a;
   p.status = a.status;
   p.negative = a.scale_log2 < 0.f;
   p.c = std::max(std::fabs(a.scale_log2), std::numeric_limits<float>::denorm_min());
   p.heads = heads;
   p.sets = a.h_q / heads;
+  if (!prompt_maps(&p)) return cudaErrorInvalidValue;
   const int tpb = AttnCfg<D, 128, false>::kTiles * kAtM / heads;
   // a sequence has its blocks and at most one that is not full
   const int64_t most = (static_cast<int64_t>(a.n_tok) / tpb + std::min(a.batch, a.n_tok)) * p.sets;

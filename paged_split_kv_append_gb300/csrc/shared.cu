@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   __syncthreads();
   // ---- the splits: one length for all groups, of 32 candidates the one whose rounds of units over the SMs are done first.
   // (A number of splits for each group, rounded to one round of units, left the longest at twice the mean: samples of five
-  // documents of 6000 to 20000 positions 150 us, XX so.)
+  // documents of 6000 to 20000 positions 150 us where this took 126.)
   if (warp == 0 && s_prefix > 0) {
     // s_prefix: positions that all units work through one at a time. Lane i: a round would take 1 / (1 + i / 6) of them.
     // (fp32: 64-bit divisions cost a call 4 us here)
@@ -602,34 +602,36 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(DecodePa
   }
 }
 
-// The query map of the last few calls from this host thread, keyed by everything it encodes.
+// The query map of the last few shapes from this host thread, put over a call's address.
 struct PrefixKey {
-  const void* q;
-  int tokens, h_q, d, heads, device;
+  int64_t tokens;
+  int h_q, d, heads;
   bool operator==(const PrefixKey& o) const {
-    return q == o.q && tokens == o.tokens && h_q == o.h_q && d == o.d && heads == o.heads && device == o.device;
+    return tokens == o.tokens && h_q == o.h_q && d == o.d && heads == o.heads;
   }
 };
 
-const CUtensorMap* query_map(const DecodeParams& a, int heads, int device) {
+bool query_map(const DecodeParams& a, int heads, CUtensorMap* map) {
   constexpr int kEntries = 8;
   thread_local PrefixKey keys[kEntries];
   thread_local CUtensorMap maps[kEntries];
   thread_local int used = 0, next = 0;
-  const PrefixKey key{a.q, a.batch * a.rows, a.h_q, a.d, heads, device};
-  for (int i = 0; i < used; ++i)
-    if (keys[i] == key) return &maps[i];
-  const int at = next;
-  next = (next + 1) % kEntries;
-  if (used < kEntries) ++used;
-  keys[at] = PrefixKey{};   // not valid until encoded
+  const PrefixKey key{static_cast<int64_t>(a.batch) * a.rows, a.h_q, a.d, heads};
+  for (int i = 0; i < used; ++i) {
+    if (!(keys[i] == key)) continue;
+    *map = maps[i];
+    return at_rebase(map, a.q);
+  }
   const cuuint64_t d = static_cast<cuuint64_t>(a.d);
-  const cuuint64_t dims[3] = {d, static_cast<cuuint64_t>(a.h_q), static_cast<cuuint64_t>(a.batch) * a.rows};
+  const cuuint64_t dims[3] = {d, static_cast<cuuint64_t>(a.h_q), static_cast<cuuint64_t>(key.tokens)};
   const cuuint64_t strides[2] = {d * 2, static_cast<cuuint64_t>(a.h_q) * d * 2};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(kAtM / heads)};
-  if (!at_encode(&maps[at], 3, a.q, dims, strides, box)) return nullptr;
-  keys[at] = key;
-  return &maps[at];
+  if (!at_encode(map, 3, a.q, dims, strides, box)) return false;
+  keys[next] = key;
+  maps[next] = *map;
+  next = (next + 1) % kEntries;
+  if (used < kEntries) ++used;
+  return true;
 }
 
 template <int D, bool kE4, int kTerms>
@@ -638,11 +640,7 @@ cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, cudaStre
   const DeviceInfo& di = device_info();
   const int heads = prefix_heads(a.group);
   PrefixParams p;
-  if (!kE4) {   // (the softmax threads write an E4M3 pool's Q)
-    const CUtensorMap* map = query_map(a, heads, di.device);
-    if (map == nullptr) return cudaErrorInvalidValue;
-    p.q = *map;
-  }
+  if (!kE4 && !query_map(a, heads, &p.q)) return cudaErrorInvalidValue;   // (the softmax threads write an E4M3 pool's Q)
   p.s = s;
   p.a = a;
   p.status = a.status;

@@ -142,6 +142,28 @@ def test_rising_and_falling_scores(d, step):
     check(q, k, v, [n], 1.0, out)
 
 
+def test_far_offsets():
+    """Token strides, and rows of q and out, whose offsets pass 2^31 elements."""
+    n, stride = 3, (1 << 30) + 64
+    base = torch.empty(2 * stride + 64, dtype=torch.bfloat16, device=DEV)
+    x = torch.as_strided(base, (n, 1, 64), (stride, 64, 1))
+    x.copy_(torch.randn((n, 1, 64), device=DEV))
+    check(x, x, x, [n], 0.125, nbx.nbx_prompt_attn(x, x, x, starts([n]), 0.125))
+    del base, x
+    n, h = 70_000, 256
+    q = torch.empty((n, h, 128), dtype=torch.bfloat16, device=DEV)
+    _, k, v = inputs(n, 1, 1, 128, 21)
+    lens = [700] * 100
+    for lo in (0, 69_300):
+        q[lo:lo + 700] = inputs(700, h, 1, 128, lo)[0]
+    q[700:69_300] = 1.0
+    out = nbx.nbx_prompt_attn(q, k, v, starts(lens), 0.1)
+    for lo in (0, 69_300):
+        rows = [0, 1, 500, 699]
+        want, tol = expect(q, k, v, lo, lo + 700, 0.1, rows)
+        near(out[lo:lo + 700][rows], want, tol)
+
+
 def test_many_short_sequences():
     g = torch.Generator().manual_seed(5)
     lens = torch.randint(0, 6, (3000,), generator=g).tolist()

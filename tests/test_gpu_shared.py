@@ -169,6 +169,27 @@ def test_groups(pool, d, groups):
     Case(groups, 1, 8, 2, d, 16, pool, "f32", 3).check_run()
 
 
+def test_many_sequences_and_groups():
+    """More of both than the plan holds in shared memory, among them empty sequences and groups of one."""
+    g = torch.Generator().manual_seed(11)
+    groups = []
+    for i in range(700):
+        n = (128, 256, 0, 160)[i % 4]
+        members = torch.randint(n, n + 90, (1 + i % 6,), generator=g).tolist()
+        groups.append((n, [0 if i % 9 == 0 and j == 1 else max(1, m) for j, m in enumerate(members)]))
+    c = Case(groups, 1, 2, 1, 64, 16, "bf16", "f32", 12)
+    assert len(c.lens_list) > 2048
+    c.check_run()
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+def test_pages_whose_offsets_pass_32_bits(pool):
+    c = Case([(1024, [1100, 1500, 1030]), (512, [600, 513])], 1, 8, 8, 128, 256, pool, "f32", 13,
+             spare=(1 << 32) // (8 * 256 * 128 * (2 if pool == "bf16" else 1)) + 3000)
+    assert int(c.table.max()) * 8 * 256 * 128 * c.pools[0].element_size() > 1 << 32
+    c.check_run()
+
+
 def test_what_is_said_to_be_shared_is_cut_to_what_every_row_sees():
     """A prefix that runs into a member's own new rows, one that is no whole number of pages, one past a length."""
     c = Case([(1024, [1024, 1030, 1100]), (700, [760, 800])], 4, 8, 2, 128, 64, "bf16", "f32", 4)
