@@ -442,9 +442,10 @@ NBX_API int nbx_paged_decode_attn_modified(const void* q, int q_dtype, int batch
  * for all of its query vectors at once; each sequence's other positions are its own. What shared_lens may say: anything up to the
  * common prefix (a row that holds other pages there is read as if it held the first row's). Sequences of no group, groups
  * of one and short prefixes are read sequence by sequence; empty sequences may lie in a group.
- * Prefixes are read apart for bf16 and E4M3 pools under bf16 queries, on the tensor cores: a bf16 output takes the
- * prefix's weights rounded to 2^-8 and each split's share of it to 2^-8, an fp32 one the weights to 2^-22 of the
- * largest. Elsewhere the groups are ignored.
+ * Prefixes are read apart for bf16 and E4M3 pools under bf16 queries, on the tensor cores, and so are the sequences' own
+ * positions in a bf16 pool from 8 query vectors to a KV head on (rows * h_q / h_kv). There a bf16 output takes the weights
+ * rounded to 2^-8 and each split's share to 2^-8, an fp32 one the weights to 2^-22 of the largest. Elsewhere the groups
+ * are ignored.
  *
  *   group_start  [device] int32 [n_groups + 1], ascending, within [0, batch]
  *   shared_lens  [device] int32 [n_groups], >= 0. Groups that make no sense set NBX_DEV_BAD_ROW and none counts.

@@ -217,7 +217,7 @@ __device__ __forceinline__ bool at_each_tile(const AttnUnit& u, F f) {
 
 // What a work policy W provides (prompt.cu, shared.cu):
 //   typename W::Params with c (|scale| log2 e, or the least positive number for a scale of 0), negative and status;
-//   W::kN, kTerms, kF8, kPaged, kWaitLate; begin() and bool unit(round, AttnUnit&) of the warp that finds the units (toks > 0
+//   W::kN, kTerms, kF8, kPaged, kMayWaitLate and wait_late(params); begin() and bool unit(round, AttnUnit&) of the warp that finds the units (toks > 0
 //   in each); toks_per_tile(), heads(); last_keys, last_key, bad_keys; load_q / load_kv by the loader warp (or q_row for the softmax threads);
 //   store(...) by a softmax thread.
 template <class C>
@@ -862,9 +862,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = at_uniform(volatile_of(sh.ctl)->tmem);
-  // the inputs are written and visible from here on. (kWaitLate: they were before the grid ahead began, which this one
+  // the inputs are written and visible from here on. (wait_late: they were before the grid ahead began, which this one
   // may run beside; the grid behind waits for both through this one)
-  if constexpr (!W::kWaitLate) pdl_wait();
+  if (!W::wait_late(params)) pdl_wait();
   pdl_launch_dependents();
   bool ok = true;
   if (warp < 8) {
@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
   tc_fence_after();
   if (threadIdx.x == 0 && volatile_of(sh.ctl)->abort != 0) raise_status(params.status, NBX_DEV_TIMEOUT);
   if (warp == 9) tmem_dealloc(tmem, 512);
-  if constexpr (W::kWaitLate) pdl_wait();
+  if constexpr (W::kMayWaitLate) pdl_wait();
 }
 
 // ---- host side

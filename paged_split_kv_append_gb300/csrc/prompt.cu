@@ -39,13 +39,14 @@ struct PromptWork {
   static constexpr int kN = 128;   // keys of a tile
   static constexpr bool kF8 = false;
   static constexpr bool kPaged = false;
-  static constexpr bool kWaitLate = false;
+  static constexpr bool kMayWaitLate = false;
   static constexpr int kTerms = 1;
   const Params& p;
   int tpt, tpb;        // tokens of a tile, of a block
   int n_units, most;   // most blocks of a sequence
   int own_blocks;      // of sequence `lane`
 
+  __device__ __forceinline__ static bool wait_late(const Params&) { return false; }
   __device__ __forceinline__ int toks_per_tile() const { return tpt; }
   __device__ __forceinline__ int heads() const { return p.heads; }
   __device__ __forceinline__ int blocks(int b) const {

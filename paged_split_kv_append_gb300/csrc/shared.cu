@@ -1,11 +1,13 @@
 // Decode attention for sequences that share a prefix of the cache: the prefix is read once for a whole group.
 //
 // The query vectors of all sequences of a group that belong to one KV head attend the group's prefix together, as the rows
-// of the matrix products of attn_tiles.cuh; each sequence's own positions are read by the one-warp kernel of the modified
-// decodes (decode_warp.cuh). Both leave partials (m, l, acc), and one merge joins them. Launches:
+// of the matrix products of attn_tiles.cuh. Each sequence's own positions are work units of the same kernel where the
+// sequence has many query vectors to a KV head (kOwnTileVectors), and read by the one-warp kernel of the modified decodes
+// (decode_warp.cuh) where it has few. All leave partials (m, l, acc), and one merge joins them. Launches:
 //   shared_plan_kernel     what each group shares, the splits of prefixes and own positions, the work lists
-//   decode_partial_warp_kernel   the own positions
-//   attn_tiles_kernel      the prefixes; it starts as the CTAs of the one before retire, and waits for it at its end
+//   decode_partial_warp_kernel   own positions of few vectors
+//   attn_tiles_kernel      the prefixes (behind the one-warp kernel it starts as that one's CTAs retire, and waits for it at
+//                          its end), and own positions of many vectors
 //   shared_merge_kernel
 #include <algorithm>
 #include <cmath>
@@ -20,6 +22,13 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kLeastPrefix = 128;      // positions: a shorter prefix is read with each sequence's own
 constexpr int kPrefixSplits = 32;      // most splits of a prefix
+// From so many query vectors to a KV head of a sequence on, the tiles read a bf16 pool's own positions too. The one-warp
+// kernel reads keys once for 8 vectors and multiplies in fp32: behind a prefix of 4096, 32 sequences' 10 to 1000 own
+// positions of one KV head of 128 take a call of 32 vectors to 39.9 us, 29.7 in the tiles; 128 vectors to four KV heads
+// 127.0 and 85.0; 8 to two 35.8 and 31.7. But 64 sequences with 4 vectors to eight KV heads 47.3 and 59.0: a unit of few
+// keys costs the tiles as much for 4 rows as for 128. (An E4M3 pool's codes the tiles have to convert.)
+// Five documents of 6000 to 20000, four rows of 24 heads of 256: 119.9 us, 108.9 so.
+constexpr int kOwnTileVectors = 8;
 
 struct PrefixParams {
   CUtensorMap q;      // [batch * rows][h_q][d], box {64, heads, tokens of a tile}
@@ -29,6 +38,7 @@ struct PrefixParams {
   int negative;
   int32_t* status;
   int heads, sets;    // query heads of a tile; h_q / heads
+  bool own_tiles;     // as PlanArgs'
   __device__ __forceinline__ uint64_t wait_ns() const { return a.wait_limit_ns; }
   __device__ __forceinline__ uint64_t delay_ns() const { return a.producer_delay_ns; }
 };
@@ -48,17 +58,27 @@ struct PlanArgs {
   int sets;       // head sets
   int sms;
   bool small;     // its arrays lie in shared memory
+  int own_pairs;  // units that a range of a sequence's own positions takes for one head set
+  bool own_dual;  // such a unit takes two ranges
   // its query vectors fill one M tile of the two, which then take splits of their own
   __device__ __forceinline__ bool dual(const PrefixGroup& g) const { return tiles == 2 && g.n * a.rows <= tpt; }
   __device__ __forceinline__ int units_of(const PrefixGroup& g, int splits) const { return dual(g) ? (splits + 1) / 2 : splits; }
-  // A group's splits of about `want` positions: their number, even if a unit takes two, and positions (of whole key tiles)
-  __device__ __forceinline__ void cut(const PrefixGroup& g, int want, int& n, int& seg) const {
-    const int most = min(kPrefixSplits, a.max_splits / 2);
-    n = min(most, static_cast<int>((static_cast<uint32_t>(g.eff) + want - 1) / static_cast<uint32_t>(want)));
-    if (dual(g)) n = min(most, (n + 1) / 2 * 2);
-    seg = ((g.eff - 1) / n + 128) & ~127;
-    n = (g.eff - 1) / seg + 1;
+  // `len` positions in at most `most` splits of about `want`: their number, even if a unit takes two, and positions (of
+  // whole key tiles)
+  __device__ __forceinline__ static void cut(int len, bool two, int most, int want, int& n, int& seg) {
+    n = min(most, static_cast<int>((static_cast<uint32_t>(len) + want - 1) / static_cast<uint32_t>(want)));
+    if (two) n = min(most, (n + 1) / 2 * 2);
+    seg = ((len - 1) / n + 128) & ~127;
+    n = (len - 1) / seg + 1;
   }
+  __device__ __forceinline__ void cut(const PrefixGroup& g, int want, int& n, int& seg) const {
+    cut(g.eff, dual(g), min(kPrefixSplits, a.max_splits / 2), want, n, seg);
+  }
+  // (there is room for a split of every 64 of a sequence's positions beside the prefix's)
+  __device__ __forceinline__ void cut_own(int own, int pre, int want, int& n, int& seg) const {
+    cut(own, own_dual, a.max_splits - pre, want, n, seg);
+  }
+  __device__ __forceinline__ int own_entries(int n) const { return own_dual ? (n + 1) / 2 : n; }
 };
 
 constexpr int kPlanBatch = 2048, kPlanGroups = 512;   // up to these the plan works in shared memory
@@ -69,12 +89,15 @@ inline size_t plan_smem(int batch, int n_groups) {
 
 // One CTA. What it reads (lengths, groups) it reads once, all at a time: a chain of dependent reads from global memory took
 // 7.5 us of a call. (Larger batches keep their arrays in the workspace, and read lengths again.)
+// kOwnTiles: own positions are units of the tiles, too. (Asked at run time, that cost the other calls 3 us of 46.)
+template <bool kOwnTiles>
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_constant__ PlanArgs x) {
   extern __shared__ __align__(16) char plan_sm[];
   const SharedParams& s = x.s;
   const DecodeParams& p = x.a;
   __shared__ unsigned long long s_prefix, s_own;
-  __shared__ int s_ok, s_empty, s_seg, s_warp[kPlanThreads / 32];
+  __shared__ int s_ok, s_empty, s_seg, s_base, s_warp[kPlanThreads / 32], s_longest[32];
+  __shared__ float s_units[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kPlanThreads / 32;
   PrefixGroup* const groups = x.small ? reinterpret_cast<PrefixGroup*>(plan_sm) : s.groups;
@@ -85,6 +108,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     s_prefix = s_own = 0;
     s_ok = 1;
     s_empty = 0;
+  }
+  if (kOwnTiles && tid < 32) {
+    s_units[tid] = 0.f;
+    s_longest[tid] = 0;
   }
   pdl_wait();
   pdl_launch_dependents();
@@ -130,6 +157,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     pg.row = row;
     const int tpu = x.tpt * x.tiles;
     pg.pairs = (pg.n * p.rows + tpu - 1) / tpu;
+    if (pg.eff > 0)
+      for (int i = lane; i < pg.n; i += 32)
+        if (len_of(pg.b0 + i) > 0) seqs[pg.b0 + i].x = pg.eff;
     if (lane == 0) {
       groups[g] = pg;
       // (a dual unit works through two splits at a time)
@@ -138,17 +168,30 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     }
   }
   __syncthreads();
-  // ---- the splits: one length for all groups, of 32 candidates the one whose rounds of units over the SMs are done first.
-  // (A number of splits for each group, rounded to one round of units, left the longest at twice the mean: samples of five
-  // documents of 6000 to 20000 positions 150 us where this took 126.)
-  if (warp == 0 && s_prefix > 0) {
+  auto sum_own = [&]() {
+    unsigned long long part = 0;
+    for (int b = tid; b < p.batch; b += kPlanThreads) {
+      const int own = len_of(b) - seqs[b].x;
+      part += kOwnTiles && x.own_dual ? (own + 1) / 2 : own;
+    }
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == 0 && part) atomicAdd(kOwnTiles ? &s_prefix : &s_own, kOwnTiles ? part * x.own_pairs * x.sets : part);
+  };
+  if constexpr (kOwnTiles) {
+    sum_own();
+    __syncthreads();
+  }
+  // ---- the splits: one length for all that the tiles read, of 32 candidates the one whose rounds of units over the SMs
+  // are done first. (A number of splits for each group, rounded to one round of units, left the longest at twice the mean:
+  // samples of five documents of 6000 to 20000 positions 150 us where this took 126.)
+  if ((kOwnTiles || warp == 0) && s_prefix > 0) {   // (few groups: one warp is done with them before several have met)
     // s_prefix: positions that all units work through one at a time. Lane i: a round would take 1 / (1 + i / 6) of them.
     // (fp32: 64-bit divisions cost a call 4 us here)
     const float round = __fdividef(static_cast<float>(s_prefix) * 6.f, static_cast<float>(x.sms * (6 + lane)));
     const int seg = max((static_cast<int>(fminf(round, 1e9f)) + 127) & ~127, 128);
     float units = 0.f;
     int longest = 0;
-    for (int g = 0; g < s.n_groups; ++g) {
+    for (int g = warp; g < s.n_groups; g += kOwnTiles ? kWarps : 1) {
       const PrefixGroup pg = groups[g];
       if (pg.eff == 0) continue;
       int n, len;
@@ -156,11 +199,28 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
       units += static_cast<float>(x.units_of(pg, n) * pg.pairs) * x.sets;
       longest = max(longest, len);
     }
-    // a unit's own costs: about as long as 256 positions
-    const float cost = ceilf(units / x.sms) * (static_cast<float>(longest) + 256.f);
-    float best = cost;
-    for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
-    if (lane == __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1) s_seg = seg;
+    if constexpr (kOwnTiles) {
+      for (int b = warp; b < p.batch; b += kWarps) {
+        const int own = len_of(b) - seqs[b].x;
+        if (own == 0) continue;
+        int n, len;
+        x.cut_own(own, 0, seg, n, len);
+        units += static_cast<float>(x.own_entries(n) * x.own_pairs) * x.sets;
+        longest = max(longest, n == 1 ? own : len);
+      }
+      atomicAdd(&s_units[lane], units);   // (whole numbers: in any order the same, but above 2^24, where it is an estimate)
+      atomicMax(&s_longest[lane], longest);
+      __syncthreads();
+      units = s_units[lane];
+      longest = s_longest[lane];
+    }
+    if (warp == 0) {
+      // a unit's own costs: about as long as 256 positions
+      const float cost = ceilf(units / x.sms) * (static_cast<float>(longest) + 256.f);
+      float best = cost;
+      for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
+      if (lane == __ffs(__ballot_sync(0xffffffffu, cost == best)) - 1) s_seg = seg;
+    }
   }
   __syncthreads();
   for (int g = warp; g < s.n_groups; g += kWarps) {
@@ -168,7 +228,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     if (pg.eff == 0) continue;
     x.cut(pg, s_seg, pg.splits, pg.seg);
     for (int i = lane; i < pg.n; i += 32)
-      if (len_of(pg.b0 + i) > 0) seqs[pg.b0 + i] = make_int2(pg.eff, pg.splits);
+      if (seqs[pg.b0 + i].x > 0) seqs[pg.b0 + i].y = pg.splits;
     __syncwarp();
     if (lane == 0) groups[g] = pg;
   }
@@ -195,52 +255,55 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
       }
       base += __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (lane == 0) p.header[4] = base;
+    if (lane == 0) s_base = base;
   }
-  // ---- the positions of each one's own, and their splits
-  unsigned long long part = 0;
-  for (int b = tid; b < p.batch; b += kPlanThreads) part += len_of(b) - seqs[b].x;
-  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-  if (lane == 0 && part) atomicAdd(&s_own, part);
-  __syncthreads();
+  // ---- the splits of the positions of each one's own
+  if constexpr (!kOwnTiles) {
+    sum_own();
+    __syncthreads();
+  }
   const int align = p.page_tokens <= NBX_SPLIT_POSITIONS ? p.page_tokens : NBX_SPLIT_POSITIONS;
   int total = 0;   // entries so far
   for (int b0 = 0; b0 < p.batch; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    int n = 0, seg = 1, L = 0;
+    int n = 0, items = 0, seg = 1, L = 0;   // splits, entries
     int2 sh = make_int2(0, 0);
     if (b < p.batch) {
       L = len_of(b);
       sh = seqs[b];
       const int own = L - sh.x;
-      if (own > 0) {
+      if (own > 0 && kOwnTiles) {
+        x.cut_own(own, sh.y, s_seg, n, seg);
+        items = x.own_entries(n);
+      } else if (own > 0) {
         // (the share of the units, rounded up)
         const float want = ceilf(static_cast<float>(p.tc_units) * own / (static_cast<float>(p.tc_pairs) * s_own));
         const int most = min(p.max_splits - sh.y, max(1, own / 64));
         const int S = want < 1.f ? 1 : (want > most ? most : static_cast<int>(want));
         seg = (own - 1) / S + 1;
         seg = (seg + align - 1) / align * align;
-        n = (own + seg - 1) / seg;
+        items = n = (own + seg - 1) / seg;
       }
-      // (what the merge needs, in one read: the prefix's splits stand where other plans have the split's length)
-      reinterpret_cast<int4*>(p.plan)[b] = make_int4(L, sh.y, sh.y + n, sh.x);
+      // (what the merge needs, in one read: the splits that the tiles leave stand where other plans have the split's length)
+      reinterpret_cast<int4*>(p.plan)[b] = make_int4(L, kOwnTiles ? sh.y + n : sh.y, sh.y + n, sh.x);
       if (sh.y + n == 0) s_empty = 1;
     }
-    int sum = n;
+    int sum = items;
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += y;
     }
     if (lane == 31) s_warp[warp] = sum;
     __syncthreads();
-    int base = total + sum - n;
+    int base = total + sum - items;
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) base += s_warp[w];
       total += s_warp[w];
     }
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < items; ++i) {
       int4* const e = reinterpret_cast<int4*>(p.entries + base + i);
-      e[0] = make_int4(b, sh.y + i, sh.x + i * seg, min(L, sh.x + (i + 1) * seg));
+      const int k = kOwnTiles && x.own_dual ? 2 * i : i, lo = sh.x + k * seg;
+      e[0] = make_int4(b, sh.y + k, lo, kOwnTiles ? seg : min(L, lo + seg));
       e[1] = make_int4(L, sh.y + n, 0, 0);
     }
     __syncthreads();
@@ -250,6 +313,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     p.header[1] = 0;
     p.header[2] = kMergeSplits;
     p.header[3] = 0;
+    p.header[4] = s_base;
+    p.header[5] = s_base + (kOwnTiles ? total * x.own_pairs * x.sets : 0);
   }
   if (s_empty) {   // a sequence with no position to read: its rows are 0
     const int64_t vec4 = static_cast<int64_t>(p.rows) * p.h_q * p.d / (p.out_bf16 ? 8 : 4);
@@ -261,6 +326,82 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   }
 }
 
+// ---------------------------------------------------------------- one row
+// The partial (m, l, acc) of one query vector over positions [lo, hi) of sequence b, key by key in fp32, by one warp:
+// columns [col0, col1) of acc, or (kHalf) of bf16(acc / l), and with the first of them m and l.
+template <int D, bool kHalf>
+__device__ __noinline__ void own_row(const DecodeParams& p, const __nv_bfloat16* q, int b, int kvh, int lo, int hi, int64_t at,
+                                     int col0, int col1) {
+  constexpr int kCols = D / 32;
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f, acc[kCols];
+#pragma unroll
+  for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
+  // element offset of position x of the head, or -1
+  auto place = [&](int x) -> int64_t {
+    const int idx = x / p.page_tokens, id = __ldcg(p.block_table + static_cast<int64_t>(b) * p.max_pages + idx);
+    return id < 0 || id >= p.num_pages
+               ? -1 : ((static_cast<int64_t>(id) * p.h_kv + kvh) * p.page_tokens + (x - idx * p.page_tokens)) * D;
+  };
+  for (int n0 = lo; n0 < hi; n0 += 32) {
+    float z = -INFINITY;
+    const int64_t mine = n0 + lane < hi ? place(n0 + lane) : -1;
+    if (mine >= 0) {
+      const uint4* const kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_pool) + mine);
+      f32x2 s = pack2(0.f, 0.f);
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        f32x2 x[4], y[4];
+        unpack16x2<BF16>(__ldg(kr + i), x);
+        unpack16x2<BF16>(__ldg(reinterpret_cast<const uint4*>(q) + i), y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fma2(x[j], y[j], s);
+      }
+      const float2 t = unpack2(s);
+      z = (t.x + t.y) * p.qk_scale_log2;
+    }
+    float top = z;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float m2 = max_nan(m, top);
+    if (m2 == -INFINITY) continue;
+    const float f = fast_exp2(m - m2);
+    const float w = mine >= 0 ? fast_exp2(z - m2) : 0.f;
+    float sum = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = fmaf(l, f, sum);
+    m = m2;
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) acc[e] *= f;
+    for (int j = 0; j < min(32, hi - n0); ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const int64_t from = __shfl_sync(0xffffffffu, mine, j);
+      if (from < 0) continue;
+      const __nv_bfloat16* const vr = static_cast<const __nv_bfloat16*>(p.v_pool) + from + lane * kCols;
+#pragma unroll
+      for (int e = 0; e < kCols; e += 2) {
+        const float2 x = bf16x2_to_float2(__ldg(reinterpret_cast<const uint32_t*>(vr + e)));
+        acc[e] = fmaf(wj, x.x, acc[e]);
+        acc[e + 1] = fmaf(wj, x.y, acc[e + 1]);
+      }
+    }
+  }
+  if (col0 == 0 && lane == 0) {
+    p.m_part[at] = m;
+    p.l_part[at] = l;
+  }
+  if (lane * kCols < col0 || lane * kCols >= col1) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < kCols; e += 2) {
+    if constexpr (kHalf)
+      reinterpret_cast<uint32_t*>(p.acc_part + at * D)[(lane * kCols + e) / 2] = bf16x2_bits(acc[e] * inv, acc[e + 1] * inv);
+    else
+      *reinterpret_cast<float2*>(p.acc_part + at * D + lane * kCols + e) = make_float2(acc[e], acc[e + 1]);
+  }
+}
+
 // ---------------------------------------------------------------- prefixes
 template <int D, bool kE4, int kTermsOfP>
 struct PrefixWork {
@@ -268,16 +409,16 @@ struct PrefixWork {
   static constexpr int kN = kTermsOfP == 3 || (kE4 && D == 256) ? 64 : 128;   // keys of a tile
   static constexpr bool kF8 = kE4;
   static constexpr bool kPaged = true;
-  static constexpr bool kWaitLate = true;
+  static constexpr bool kMayWaitLate = true;
   static constexpr int kTerms = kTermsOfP;
-  // A bf16 output takes a prefix's partials as bf16(acc / l), in the first half of their slots: half the bytes both ways,
+  // A bf16 output takes the partials as bf16(acc / l), in the first half of their slots: half the bytes both ways,
   // for up to 2^-8 of a split's share, less than the weights' own rounding leaves.
   static constexpr bool kHalfParts = kTermsOfP == 1;
   static constexpr bool kPairs = D <= 128;               // two M tiles a unit, or one over two ranges of keys
   // What is read before the grid ahead is waited for comes past L1 (__ldcg): the plan is complete, but an older line may
   // still lie there.
   const Params& p;
-  int tpt, n_units;
+  int tpt, n_prefix, n_units;
   int step_idx, step_off;    // a key tile further on: pages and positions
   // Pieces of 16 positions, which no page splits: lane l < kN / 16 keeps track of piece l of a tile. The cursor is a tile
   // ahead, its page id on the way; loaders keep the places of the last K tile (of M tile t; at d = 256 of the last two).
@@ -287,6 +428,7 @@ struct PrefixWork {
   Cursor cur[2];
   int64_t place[2];          // byte offset of the piece in a pool, or -1
 
+  __device__ __forceinline__ static bool wait_late(const Params& p) { return kE4 || !p.own_tiles; }   // beside the one-warp kernel
   __device__ __forceinline__ int toks_per_tile() const { return tpt; }
   __device__ __forceinline__ int heads() const { return p.heads; }
   __device__ __forceinline__ PrefixWork(const Params& params) : p(params) {
@@ -296,11 +438,45 @@ struct PrefixWork {
     cur[0] = cur[1] = Cursor{0, 0, 0};
     place[0] = place[1] = -1;
   }
-  __device__ __forceinline__ void begin() { n_units = __ldcg(p.a.header + 4); }
+  __device__ __forceinline__ void begin() {
+    n_prefix = __ldcg(p.a.header + 4);
+    n_units = __ldcg(p.a.header + 5);
+  }
+  // A unit of a sequence's own positions
+  __device__ __forceinline__ void own_unit(int place, AttnUnit& u) const {
+    const int rows = p.a.rows, tpu = (kPairs ? 2 : 1) * tpt;
+    const int pairs = (rows + tpu - 1) / tpu, per = pairs * p.sets;
+    const int entry = place / per, rest = place - entry * per;
+    const int set = rest / pairs, pair = rest - set * pairs;
+    const int4 e = __ldcg(reinterpret_cast<const int4*>(p.a.entries + entry));   // sequence, split, begin, its positions
+    const int len = __ldcg(reinterpret_cast<const int4*>(p.a.entries + entry) + 1).x;
+    u.dual = kPairs && rows <= tpt;
+    u.toks = min(tpu, rows - pair * tpu);
+    u.tok = e.x * rows + pair * tpu;
+    u.head = set * p.heads;
+    u.kvh = u.head / p.a.group;
+    u.pos = len - rows + pair * tpu + 1;
+    u.pad = 1;
+    u.b = e.x;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      u.slot[t] = e.y + (u.dual ? t : 0);
+      u.kv[t] = e.z + (u.dual ? t * e.w : 0);
+      u.end[t] = min(len, u.kv[t] + e.w);
+      u.n[t] = max(0, u.end[t] - u.kv[t] + kN - 1) / kN;
+    }
+    if (!u.dual && !(kPairs && u.toks > tpt)) u.n[1] = 0;
+  }
   __device__ __forceinline__ bool unit(uint32_t round, AttnUnit& u) const {
     const int64_t place = static_cast<int64_t>(round) * gridDim.x + blockIdx.x;
     if (place >= n_units) return false;
     const int un = static_cast<int>(place), lane = threadIdx.x & 31;
+    if constexpr (!kF8) {   // (E4M3 pools: without the code, a shared prefix of 65536 positions takes 3 us less)
+      if (un >= n_prefix) {
+        own_unit(un - n_prefix, u);
+        return true;
+      }
+    }
     // the last group whose first unit is not behind this one (groups without units share theirs with the next)
     PrefixGroup pg = {};
     for (int g0 = 0; g0 < p.s.n_groups; g0 += 32) {
@@ -332,7 +508,7 @@ struct PrefixWork {
     u.tok = pg.b0 * p.a.rows + pair * tpu;
     u.head = set * p.heads;
     u.kvh = u.head / p.a.group;
-    u.pos = 0;
+    u.pos = 1 << 30;
     u.b = pg.row;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -347,7 +523,10 @@ struct PrefixWork {
   __device__ __forceinline__ int last_keys(const AttnUnit& u, int t) const {
     return u.end[t] - u.kv[t] - (u.n[t] - 1) * kN;
   }
-  __device__ __forceinline__ int last_key(const AttnUnit& u, int t, int, bool) const { return u.end[t] - u.kv[t] - 1; }
+  // (u.pos: how many positions the unit's first token sees)
+  __device__ __forceinline__ int last_key(const AttnUnit& u, int t, int tok, bool) const {
+    return min(u.end[t], u.pos + tok) - u.kv[t] - 1;
+  }
   __device__ __forceinline__ bool in_pool(int page) const { return page >= 0 && page < p.a.num_pages; }
   __device__ __forceinline__ int page_id(const AttnUnit& u, int idx, bool there) const {
     return there ? __ldcg(p.a.block_table + static_cast<int64_t>(u.b) * p.a.max_pages + idx) : 0;
@@ -478,6 +657,18 @@ struct PrefixWork {
       st_global_hint(p.a.l_part + at, l, keep);
     }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (a NaN stays one)
+    float sick = l * 0.f;   // a NaN, if some value is not finite
+    const bool parted = !kF8 && u.pad && p.a.rows > 1;   // own positions of several rows
+    if (parted) {
+#pragma unroll 1
+      for (int i = 0; i < kCols; i += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_base + i, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) sick = fmaf(__uint_as_float(o[e]), 0.f, sick);
+      }
+    }
 #pragma unroll 1
     for (int i = 0; i < kCols; i += 32) {
       uint32_t o[32];
@@ -507,6 +698,19 @@ struct PrefixWork {
         }
       }
     }
+    if constexpr (!kF8) {
+      // Among the own positions, some of the keys of the later rows are not the earlier ones', but a NaN or an infinity
+      // among their values reaches all rows of the product (0 x NaN): rows that are not finite are computed again
+      if (!parted) return;
+      uint32_t again = __ballot_sync(0xffffffffu, ok && sick != 0.f);
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        const int rt = __shfl_sync(0xffffffffu, tok, src), rh = __shfl_sync(0xffffffffu, head, src);
+        const int64_t ra = __shfl_sync(0xffffffffu, at, src);
+        own_row<D, kHalfParts>(p.a, q_row(u, rt, rh), u.b, u.kvh, u.kv[t], min(u.end[t], u.pos + rt), ra, col0, col0 + kCols);
+      }
+    }
   }
 };
 
@@ -515,7 +719,7 @@ constexpr int kMergeWarps = 4;
 
 // One warp per (query vector, 128 columns): M = max m_s, w_s = 2^(m_s - M) (a split with m = -inf is skipped),
 // out = v_scale sum w_s acc_s / sum w_s l_s, s ascending: the prefix's splits, then the sequence's own. Sequences with one
-// split and no prefix are written already. kHalves: the output is bf16, and the prefix's partials are bf16 acc / l.
+// split from the one-warp kernel are written already. kHalves: the output is bf16, and the tiles' partials are bf16 acc / l.
 // What bounds it: a chain of three reads (plan, first accumulators and statistics, the rest).
 template <bool kHalves>
 __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(DecodeParams p) {
@@ -635,7 +839,7 @@ bool query_map(const DecodeParams& a, int heads, CUtensorMap* map) {
 }
 
 template <int D, bool kE4, int kTerms>
-cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, cudaStream_t stream) {
+cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, bool own_tiles, cudaStream_t stream) {
   using W = PrefixWork<D, kE4, kTerms>;
   const DeviceInfo& di = device_info();
   const int heads = prefix_heads(a.group);
@@ -648,13 +852,14 @@ cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, cudaStre
   p.c = std::max(std::fabs(a.qk_scale_log2), std::numeric_limits<float>::denorm_min());
   p.heads = heads;
   p.sets = a.h_q / heads;
+  p.own_tiles = own_tiles;
   return launch_attn_tiles<W, D>(p, static_cast<unsigned>(di.sm_count), stream);
 }
 template <int D>
-cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, int pool_dtype, cudaStream_t stream) {
+cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, int pool_dtype, bool own_tiles, cudaStream_t stream) {
   if (pool_dtype == NBX_E4M3)
-    return a.out_bf16 ? launch_prefix<D, true, 1>(s, a, stream) : launch_prefix<D, true, 2>(s, a, stream);
-  return a.out_bf16 ? launch_prefix<D, false, 1>(s, a, stream) : launch_prefix<D, false, 3>(s, a, stream);
+    return a.out_bf16 ? launch_prefix<D, true, 1>(s, a, own_tiles, stream) : launch_prefix<D, true, 2>(s, a, own_tiles, stream);
+  return a.out_bf16 ? launch_prefix<D, false, 1>(s, a, own_tiles, stream) : launch_prefix<D, false, 3>(s, a, own_tiles, stream);
 }
 
 }  // namespace
@@ -714,14 +919,20 @@ cudaError_t shared_dispatch(const SharedParams& s, const DecodeParams& p, int q_
   x.sets = p.h_q / heads;
   x.sms = di.sm_count;
   x.small = plan_small(p.batch, s.n_groups);
-  cudaError_t e = launch_pdl(shared_plan_kernel, 1u, kPlanThreads, plan_smem(p.batch, s.n_groups), stream, x);
+  const bool own_tiles = pool_dtype == NBX_BF16 && p.rows * p.group >= kOwnTileVectors;
+  x.own_pairs = (p.rows + x.tpt * x.tiles - 1) / (x.tpt * x.tiles);
+  x.own_dual = x.tiles == 2 && p.rows <= x.tpt;
+  cudaError_t e = launch_pdl(own_tiles ? shared_plan_kernel<true> : shared_plan_kernel<false>, 1u, kPlanThreads,
+                             plan_smem(p.batch, s.n_groups), stream, x);
   if (e != cudaSuccess) return e;
-  e = pool_dtype == NBX_E4M3 ? decode_dispatch_warp_e4m3(q, q_dtype, grid_limit, stream)
-                             : decode_dispatch_warp_bf16(q, grid_limit, stream);
-  if (e != cudaSuccess) return e;
-  e = p.d == 64    ? launch_prefix<64>(s, q, pool_dtype, stream)
-      : p.d == 128 ? launch_prefix<128>(s, q, pool_dtype, stream)
-                   : launch_prefix<256>(s, q, pool_dtype, stream);
+  if (!own_tiles) {
+    e = pool_dtype == NBX_E4M3 ? decode_dispatch_warp_e4m3(q, q_dtype, grid_limit, stream)
+                               : decode_dispatch_warp_bf16(q, grid_limit, stream);
+    if (e != cudaSuccess) return e;
+  }
+  e = p.d == 64    ? launch_prefix<64>(s, q, pool_dtype, own_tiles, stream)
+      : p.d == 128 ? launch_prefix<128>(s, q, pool_dtype, own_tiles, stream)
+                   : launch_prefix<256>(s, q, pool_dtype, own_tiles, stream);
   if (e != cudaSuccess) return e;
   const int64_t items = static_cast<int64_t>(p.batch) * p.rows * p.h_q * ((p.d / 4 + 31) / 32);
   const int64_t grid = std::min<int64_t>((items + kMergeWarps - 1) / kMergeWarps, static_cast<int64_t>(di.sm_count) * 8);

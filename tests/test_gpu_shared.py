@@ -269,6 +269,34 @@ def test_a_nan_in_the_prefix_reaches_all_of_its_head(pool, where):
     assert bool(nan[:2, :, 4:].all()) == (where == "k")
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("d,h_q,rows", [(64, 8, 4), (128, 8, 4), (256, 8, 4), (128, 4, 4), (128, 24, 40), (256, 6, 70)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_of_later_rows_do_not_reach_earlier_ones(d, h_q, rows, out, bad):
+    """In a sequence's last positions, which its last rows alone see: at the last and at row r's own."""
+    c = Case([(512, [700, 620]), (0, [rows, 300])], rows, h_q, 2, d, 32, "bf16", out, 21)
+    hit = {0: rows - 1, 3: rows // 2}   # sequence -> the first row that sees the value
+    at = {b: c.lens_list[b] - rows + r for b, r in hit.items()}
+    for b, x in at.items():
+        c.pools[1][c.table[b, x // 32].long(), 1, x % 32, 5] = bad
+        c.pools[0][c.table[b, x // 32].long(), 0, x % 32, 7] = bad
+    out = c.run()
+    torch.cuda.synchronize()
+    for b, x in at.items():
+        r, h = hit[b], h_q // 2
+        assert bool(torch.isfinite(out[b, :r]).all())
+        assert not bool(torch.isfinite(out[b, r:, h:, 5]).any())
+        # (an infinite key may leave a row its other weights; a NaN does not)
+        assert not bool(torch.isfinite(out[b, r:, :h]).all())
+        c.pools[1][c.table[b, x // 32].long(), 1, x % 32, 5] = 0
+        c.pools[0][c.table[b, x // 32].long(), 0, x % 32, 7] = 0
+        want, tol = c.expect(b)
+        assert bool(((out[b].double() - want).abs() <= tol)[:r].all())
+    for b in (1, 2):
+        want, tol = c.expect(b)
+        assert bool(((out[b].double() - want).abs() <= tol).all())
+
+
 def test_page_ids_do_not_matter_and_the_same_again():
     c = Case([(2048, [2100, 2060, 3000]), (512, [530, 700])], 2, 8, 2, 128, 16, "bf16", "f32", 10)
     one = c.run()
