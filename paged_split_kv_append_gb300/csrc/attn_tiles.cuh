@@ -1,4 +1,5 @@
-// Attention of 128-row tiles of query vectors on tcgen05: what prompt attention and the shared-prefix decode run.
+// Attention of 128-row tiles of query vectors on tcgen05: what prompt attention and the shared-prefix decode run. (A
+// prompt of 16384 tokens, 32 / 8 heads of 128, takes 1454 us, at 79 % of the measured matrix rate and the power limit.)
 //
 // A work unit is one or two M tiles of 128 query vectors of one KV head (a tile holds some tokens with `heads` query heads
 // each) and the keys they attend, in tiles of kN. Per key tile, with scores in log2 units:
@@ -85,14 +86,14 @@ struct alignas(16) AttnUnit {
   int tok;        // first token of the first tile (rows of the query tensor)
   int toks;       // tokens of the unit, of both tiles
   int head, kvh;  // first query head, KV head
-  int pos;        // causal: position of the first token in its sequence
+  int pos;        // causal: position of the first token in its sequence; paged: how many positions that token sees
   int b;          // paged: row of the block table
   int dual;       // the two tiles are the same query vectors, over keys of their own
   int kv[2];      // causal: first key's row; paged: first position
   int end[2];     // paged: one past the last position
   int slot[2];    // paged: slot of the partials
   int n[2];       // key tiles of each M tile
-  int pad;
+  int own;        // paged: the positions are a sequence's own
 };
 static_assert(sizeof(AttnUnit) == 64, "a unit is four 16-byte words");
 
@@ -217,9 +218,9 @@ __device__ __forceinline__ bool at_each_tile(const AttnUnit& u, F f) {
 
 // What a work policy W provides (prompt.cu, shared.cu):
 //   typename W::Params with c (|scale| log2 e, or the least positive number for a scale of 0), negative and status;
-//   W::kN, kTerms, kF8, kPaged, kMayWaitLate and wait_late(params); begin() and bool unit(round, AttnUnit&) of the warp that finds the units (toks > 0
-//   in each); toks_per_tile(), heads(); last_keys, last_key, bad_keys; load_q / load_kv by the loader warp (or q_row for the softmax threads);
-//   store(...) by a softmax thread.
+//   W::kN, kTerms, kF8, kPaged, kMayWaitLate and wait_late(params); begin() and bool unit(round, AttnUnit&) of the warp that
+//   finds the units (toks > 0 in each); toks_per_tile(), heads(); last_keys, last_key, bad_keys; load_q / load_kv by the
+//   loader warps (or q_row for the softmax threads); store(...) by a softmax warp.
 template <class C>
 struct AttnShared {
   char* q_s;

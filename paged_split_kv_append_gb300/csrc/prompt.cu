@@ -114,7 +114,7 @@ struct PromptWork {
     u.pos = lo * tpb;
     u.kv[0] = u.kv[1] = s;
     u.dual = 0;
-    u.b = u.pad = 0;
+    u.b = u.own = 0;
     u.end[0] = u.end[1] = u.slot[0] = u.slot[1] = 0;
     u.tok = s + u.pos;
     u.toks = min(tpb, len - u.pos);

@@ -456,7 +456,7 @@ struct PrefixWork {
     u.head = set * p.heads;
     u.kvh = u.head / p.a.group;
     u.pos = len - rows + pair * tpu + 1;
-    u.pad = 1;
+    u.own = 1;
     u.b = e.x;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -658,7 +658,7 @@ struct PrefixWork {
     }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (a NaN stays one)
     float sick = l * 0.f;   // a NaN, if some value is not finite
-    const bool parted = !kF8 && u.pad && p.a.rows > 1;   // own positions of several rows
+    const bool parted = !kF8 && u.own && p.a.rows > 1;   // own positions of several rows
     if (parted) {
 #pragma unroll 1
       for (int i = 0; i < kCols; i += 32) {
