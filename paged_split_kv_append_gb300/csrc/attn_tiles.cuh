@@ -221,6 +221,12 @@ __device__ __forceinline__ bool at_each_tile(const AttnUnit& u, F f) {
 //   W::kN, kTerms, kF8, kPaged, kMayWaitLate and wait_late(params); begin() and bool unit(round, AttnUnit&) of the warp that
 //   finds the units (toks > 0 in each); toks_per_tile(), heads(); last_keys, last_key, bad_keys; load_q / load_kv by the
 //   loader warps (or q_row for the softmax threads); store(...) by a softmax warp.
+// d = 64 leaves TMEM for a P of its own beside S: the next S is computed as soon as this one is in registers, during its
+// exponentials, and the two tiles need no turns.
+template <class W, int D>
+constexpr bool kAtOwnP = D == 64 && W::kN == 128 && W::kTerms == 1;
+constexpr int kAtPCol = 384;      // [2][64] columns
+
 template <class C>
 struct AttnShared {
   char* q_s;
@@ -237,7 +243,7 @@ struct AttnShared {
   uint64_t* unit_full; // [2] a unit is written, every reader has read it
   uint64_t* unit_empty;
   AttnUnit* units;     // [2]
-  uint64_t* turn;      // [2] d <= 128: it is the turn of M tile t's warp to issue
+  uint64_t* turn;      // [2] d <= 128: it is the turn of M tile t's warp to issue; own P: S of tile t is in registers
   uint64_t* done;
   uint64_t* raw_full;  // [kRaws] a tile's codes have landed
   uint64_t* raw_empty; // [kRaws] and are converted
@@ -342,6 +348,7 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
   const uint64_t q_desc = smem_desc(smem_u32(sh.q_s) + t * C::kQTile, 16, 1024);
   const uint64_t k_desc = smem_desc(ring, 16, 1024), v_desc = smem_desc(ring, kAtomBytes, 1024);
   const uint32_t o_addr = tmem + C::kOCol + t * D;
+  constexpr bool kOwnP = kAtOwnP<W, D>;
   int slot = 0;                      // the ring slot next consumed, in the loader's order, and its phase
   uint32_t phase = 0;
   uint32_t p_phase = 0, s_phase = 0; // bit: phase of a P buffer; d = 256: of the PV that frees an S buffer
@@ -400,7 +407,7 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
     constexpr int kSteps = N / 16, kPartSteps = kSteps / C::kParts;
     const int steps = one ? (keys + 15) >> 4 : 0;
     const uint64_t v0 = v_desc + first * (C::kSlotBytes >> 4), v1 = C::kParts == 2 ? v_desc + next * (C::kSlotBytes >> 4) : 0;
-    const uint32_t p = tmem + buf * kAtBuf;
+    const uint32_t p = kOwnP ? tmem + kAtPCol + t * 64 : tmem + buf * kAtBuf;
     if constexpr (kPartSteps % 4 == 0) {
 #pragma unroll
       for (int term = 0; term < W::kTerms; ++term)
@@ -474,9 +481,20 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
         if (!does_qk) release(ks, ks2, false);
         return true;
       };
-      constexpr bool kEarlyK = T == 2 && !W::kPaged;
+      constexpr bool kEarlyK = T == 2 && (kOwnP || !W::kPaged);
       if constexpr (kEarlyK)
         if (!take_k()) return false;
+      if constexpr (kOwnP) {
+        if (qks) {
+          if (steps > 0 && !at_warp_wait(&sh.turn[t], (steps - 1) & 1u, ab)) return false;
+          ++steps;
+          fences();
+          qk(buf, ks, ks2);
+          at_commit(&sh.s_full[buf], one);
+        }
+        if (ks >= 0) release(ks, ks2, true);
+        if (j + C::kAhead == n - 1) at_commit(sh.q_empty, one);
+      }
       if (pvs) {
         const int keys = j + 1 < no ? N : last;
         clear_tail(vs, vs2, keys);
@@ -493,7 +511,7 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
       // ---- the two M tiles' warps issue in turns, PV and QK^T together: side by side their MMAs mix in the pipe, both S are
       // done at the same time, and then the pipe waits for two softmaxes at once (16384 tokens of 32 heads: 1872 us, 1588
       // in turns)
-      if constexpr (T == 2) {
+      if constexpr (T == 2 && !kOwnP) {
         if ((t == 1 || steps > 0) && !at_warp_wait(&sh.turn[t], (steps - (t == 0)) & 1u, ab)) return false;
         ++steps;
       }
@@ -503,7 +521,7 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
       }
       if constexpr (!kEarlyK)
         if (!take_k()) return false;
-      if (qks) {
+      if (qks && !kOwnP) {
         if constexpr (T == 1) {   // the buffer's last PV is done (in the pipe of another warp)
           if (x >= 2) {
             if (!at_warp_wait(&sh.pv_done[buf], (s_phase >> buf) & 1u, ab)) return false;
@@ -513,14 +531,14 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
         fences();
         qk(buf, ks, ks2);
       }
-      pass_turn();
+      if constexpr (!kOwnP) pass_turn();
       if (pvs) at_commit(&sh.pv_done[buf], one);
-      if (qks) at_commit(&sh.s_full[buf], one);
+      if (qks && !kOwnP) at_commit(&sh.s_full[buf], one);
       if (T == 1 && (pvs || qks)) ++x;
       if (does_pv && vs >= 0) release(vs, vs2, true);
-      if (does_qk && ks >= 0) release(ks, ks2, true);
+      if (does_qk && ks >= 0 && !kOwnP) release(ks, ks2, true);
       if (dual && t == 0 && !pass(n1)) return false;
-      if (j + C::kAhead == n - 1 && does_qk) at_commit(sh.q_empty, one);
+      if (j + C::kAhead == n - 1 && does_qk && !kOwnP) at_commit(sh.q_empty, one);
     }
   }
   return true;
@@ -577,6 +595,7 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
   const int tpt = w.toks_per_tile();
   const int tok = row / w.heads(), head = row - tok * w.heads();
   float c = w.p.c;
+  constexpr bool kOwnP = kAtOwnP<W, D>;
   const AttnControl* ab = sh.ctl;
   uint32_t x = 0;         // key tiles of this M tile so far
   uint32_t xphase = 0;
@@ -633,6 +652,11 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
 #pragma unroll
       for (int i = 0; i < NC; i += 32) tmem_ld32(s_col + c0 + i, s + i);
       tmem_wait_ld();
+      if constexpr (kOwnP) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.turn[t]);
+      }
       const int limit = last_key - (j * N + c0);             // this thread's columns up to here are seen
       if (!__all_sync(0xffffffffu, limit >= NC - 1)) {
 #pragma unroll
@@ -680,9 +704,10 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
             }
           }
         }
+        if (kOwnP && h == 0 && j > 0 && !pv_wait()) return false;   // (the last P has been read)
 #pragma unroll
         for (int y = 0; y < W::kTerms; ++y) {
-          const uint32_t at = s_col + y * (N / 2) + (c0 + h) / 2;
+          const uint32_t at = kOwnP ? lane_base + kAtPCol + t * 64 + h / 2 : s_col + y * (N / 2) + (c0 + h) / 2;
           if constexpr (kChunk == 64) tmem_st32(at, term[y]);
           else tmem_st16(at, term[y]);
         }
@@ -848,7 +873,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       mbar_init(&sh.unit_empty[i], 11 + (W::kPaged ? kAtCopyWarps : 0));
     }
     if constexpr (C::kTiles == 2)
-      for (int i = 0; i < 2; ++i) mbar_init(&sh.turn[i], 1);
+      for (int i = 0; i < 2; ++i) mbar_init(&sh.turn[i], kAtOwnP<W, D> ? kRowWarps : 1);
     if constexpr (C::kTiles == 1)
       for (int i = 0; i < 4; ++i) mbar_init(&sh.x_bar[i], 2);
     sh.ctl->abort = 0;
