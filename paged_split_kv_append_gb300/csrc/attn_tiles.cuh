@@ -13,6 +13,9 @@
 //  * warps 0-3 and 4-7: two softmax groups. Up to d = 128 each has an M tile of its own, one row a thread, and the two
 //    take turns with the tensor pipe: while one group works on its S, the MMAs of the other's tile run. Both tiles attend
 //    the same keys, or (dual units, whose query vectors fill one tile) the same vectors attend two ranges of keys. At
+//    d = 64 a P of 16-bit terms has columns of its own, the next S is computed while this one's exponentials run, and the
+//    turns fall away (8 prompts of 700 to 1700 tokens, 16 heads of 64: 52.4 us in turns, 46.7 so: 1.2 us for 128 keys, of
+//    which S is waited for in 0.06, where the two softmaxes share a scheduler's pipes in the same phases). At
 //    d = 256 O fills half of the TMEM, so there is one M tile, S is double-buffered, and the groups share each row, half
 //    of the columns each; the two threads of a row swap their maxima through shared memory.
 //  * warps 9 and 10 issue the MMAs: QK^T (both operands from shared memory) and PV (P from TMEM, N = d). Up to d = 128 each
@@ -29,7 +32,7 @@
 //    vector into [2^14, 2^15): exact but for elements under 2^-29 of it. The softmax threads write them, each its own row,
 //    and take the factor back in their row's c. The running maximum sits 2^7 above P's largest weight then, so that small
 //    weights keep their bits in f16's range.
-// What bounds it: the tensor pipe. Per 128 keys and two tiles of d = 128 it is busy 2048 cycles; the softmax issues
+// What bounds it: the tensor pipe (d = 64: the softmax). Per 128 keys and two tiles of d = 128 it is busy 2048 cycles; the softmax issues
 // about 900 instructions on each scheduler and takes 1024 cycles of the special-function units (4 a warp measured).
 #pragma once
 
@@ -216,17 +219,16 @@ __device__ __forceinline__ bool at_each_tile(const AttnUnit& u, F f) {
   return true;
 }
 
+// d = 64 leaves TMEM for a P of its own beside S (three terms would not fit)
+template <class W, int D>
+constexpr bool kAtOwnP = D == 64 && W::kN == 128 && W::kTerms == 1;
+constexpr int kAtPCol = 384;      // [2][64] columns
+
 // What a work policy W provides (prompt.cu, shared.cu):
 //   typename W::Params with c (|scale| log2 e, or the least positive number for a scale of 0), negative and status;
 //   W::kN, kTerms, kF8, kPaged, kMayWaitLate and wait_late(params); begin() and bool unit(round, AttnUnit&) of the warp that
 //   finds the units (toks > 0 in each); toks_per_tile(), heads(); last_keys, last_key, bad_keys; load_q / load_kv by the
 //   loader warps (or q_row for the softmax threads); store(...) by a softmax warp.
-// d = 64 leaves TMEM for a P of its own beside S: the next S is computed as soon as this one is in registers, during its
-// exponentials, and the two tiles need no turns.
-template <class W, int D>
-constexpr bool kAtOwnP = D == 64 && W::kN == 128 && W::kTerms == 1;
-constexpr int kAtPCol = 384;      // [2][64] columns
-
 template <class C>
 struct AttnShared {
   char* q_s;
