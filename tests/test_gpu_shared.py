@@ -242,6 +242,87 @@ def test_a_bad_page_in_the_prefix_and_a_bad_length(pool, d):
     assert float(((out[0].double() - want).abs() - tol).max()) <= 0
 
 
+# ---- sequences of 8 query vectors to a KV head and more, whose own positions the tiles read too
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 48, 256])
+@pytest.mark.parametrize("rows,h_q", [(4, 8), (1, 16), (20, 4)])
+def test_own_positions_of_many_vectors(page, d, out, rows, h_q):
+    """Own positions of no, one and many tiles, sequences shorter than their rows, of no group, and empty."""
+    groups = [(768, [769, 768 + 255, 768 + 256, 768 + 257, 1900]), (0, [1, 5, 0, 2000]), (0, [130]), (300, [300, 0, 431])]
+    Case(groups, rows, h_q, 2, d, page, "bf16", out, page + d).check_run()
+
+
+@pytest.mark.parametrize("n", [0, 3])
+def test_many_sequences_of_many_vectors(n):
+    g = torch.Generator().manual_seed(11 + n)
+    groups = []
+    for i in range(500):
+        shared = (128, 0, 160)[i % 3]
+        members = torch.randint(shared, shared + 90, (2 + i % 5 + n,), generator=g).tolist()
+        groups.append((shared, [0 if i % 7 == 0 and j == 1 else max(1, m) for j, m in enumerate(members)]))
+    c = Case(groups, 2, 4, 1, 64, 16, "bf16", "bf16", 12)
+    assert (len(c.lens_list) > 2048) == (n == 3)
+    c.check_run()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scales_of_many_vectors(d, scale):
+    c = Case([(1024, [1100, 1030]), (0, [333])], 3, 8, 2, d, 16, "bf16", "f32", 8)
+    c.scale = scale
+    c.check_run()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_a_bad_page_among_own_positions_of_many_vectors(d, out):
+    for page in (-1, 1 << 30):
+        c = Case([(1024, [1100, 1500])], 1, 16, 2, d, 16, "bf16", out, 14)
+        c.table[1, 70] = page
+        status = ints([0])
+        out_t = c.run(status=status)
+        torch.cuda.synchronize()
+        assert int(status) == nbx.DEV_BAD_PAGE
+        want, tol = c.expect(0)
+        assert bool(((out_t[0].double() - want).abs() <= tol).all())
+        c.table = c.table[:, [i for i in range(c.table.shape[1]) if i != 70]].contiguous()
+        c.lens_list = [1100, 1500 - 16]
+        want, tol = c.expect(1)
+        assert bool(((out_t[1].double() - want).abs() <= tol).all())
+
+
+def test_streams_and_graphs_of_many_vectors():
+    a = Case([(512, [700, 620]), (0, [90])], 4, 8, 2, 128, 32, "bf16", "bf16", 15)
+    b = Case([(640, [700, 900])], 4, 8, 2, 128, 32, "bf16", "bf16", 16)
+    want = [a.run().clone(), b.run().clone()]
+    outs = [torch.empty_like(w) for w in want]
+    ws = nbx.nbx_paged_decode_shared_workspace_bytes(3, 4, 8, 2, 128, 900, 2)
+    ws = torch.empty(ws, dtype=torch.uint8, device=DEV)
+    graphs = []
+    for c, o in zip((a, b), outs):   # two graphs over one workspace, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.run(out=o, workspace=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for st, c, o in zip(streams, (a, b), outs):
+            o.zero_()
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                c.run(out=o)
+            torch.cuda.current_stream().wait_stream(st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
 @pytest.mark.parametrize("q_type,pool", [("f32", "f32"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "e4m3")])
 def test_formats_whose_groups_are_ignored(q_type, pool):
     c = Case([(512, [600, 700, 513])], 2, 4, 2, 64, 16, pool, "f32", 7, q_type=q_type)
