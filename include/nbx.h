@@ -443,7 +443,7 @@ NBX_API int nbx_paged_decode_attn_modified(const void* q, int q_dtype, int batch
  * common prefix (a row that holds other pages there is read as if it held the first row's). Sequences of no group, groups
  * of one and short prefixes are read sequence by sequence; empty sequences may lie in a group.
  * Prefixes are read apart for bf16 and E4M3 pools under bf16 queries, on the tensor cores, and so are the sequences' own
- * positions in a bf16 pool from 8 query vectors to a KV head on (rows * h_q / h_kv). There a bf16 output takes the weights
+ * positions from 8 query vectors to a KV head on (rows * h_q / h_kv). There a bf16 output takes the weights
  * rounded to 2^-8 and each split's share to 2^-8, an fp32 one the weights to 2^-22 of the largest. Elsewhere the groups
  * are ignored.
  *

@@ -22,12 +22,12 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kLeastPrefix = 128;      // positions: a shorter prefix is read with each sequence's own
 constexpr int kPrefixSplits = 32;      // most splits of a prefix
-// From so many query vectors to a KV head of a sequence on, the tiles read a bf16 pool's own positions too. The one-warp
-// kernel reads keys once for 8 vectors and multiplies in fp32: behind a prefix of 4096, 32 sequences' 10 to 1000 own
-// positions of one KV head of 128 take a call of 32 vectors to 39.9 us, 29.7 in the tiles; 128 vectors to four KV heads
-// 127.0 and 85.0; 8 to two 35.8 and 31.7. But 64 sequences with 4 vectors to eight KV heads 47.3 and 59.0: a unit of few
-// keys costs the tiles as much for 4 rows as for 128. (An E4M3 pool's codes the tiles have to convert.)
-// Five documents of 6000 to 20000, four rows of 24 heads of 256: 119.9 us, 108.9 so.
+// From so many query vectors to a KV head of a sequence on, the tiles read its own positions too. The one-warp kernel reads
+// keys once for every 8 vectors, on a tensor path that makes little of them: behind a prefix of 4096, 32 sequences' 10 to
+// 1000 own positions of one KV head of 128 take a call of 32 vectors to 39.9 us, 29.7 in the tiles (E4M3 46.1 and 35.8); 128
+// vectors to four KV heads 127.0 and 85.0 (140.3 and 103.4); 8 to two 35.8 and 31.7 (37.9 and 35.8); 24 to four 48.1 and
+// 44.0 (but 56.3 and 58.4). Five documents of 6000 to 20000, four rows of 24 heads of 256: 119.9 and 108.9. But 64 sequences
+// with 4 vectors to eight KV heads 47.3 and 59.0: a unit of few keys costs the tiles as much for 4 rows as for 128.
 constexpr int kOwnTileVectors = 8;
 
 struct PrefixParams {
@@ -327,14 +327,15 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
 }
 
 // ---------------------------------------------------------------- one row
-// The partial (m, l, acc) of one query vector over positions [lo, hi) of sequence b, key by key in fp32, by one warp:
-// columns [col0, col1) of acc, or (kHalf) of bf16(acc / l), and with the first of them m and l.
-template <int D, bool kHalf>
+// acc = sum_j 2^(z_j - m) v_j of one query vector over positions [lo, hi) of sequence b, key by key in fp32, by one warp;
+// columns [col0, col1) of it, or (kHalf) of bf16(acc inv), go to the partial `at`. m is the partial's own: at d = 256 the
+// other columns, and l, belong to it.
+template <int D, bool kE4, bool kHalf>
 __device__ __noinline__ void own_row(const DecodeParams& p, const __nv_bfloat16* q, int b, int kvh, int lo, int hi, int64_t at,
-                                     int col0, int col1) {
+                                     float m, float inv, int col0, int col1) {
   constexpr int kCols = D / 32;
   const int lane = threadIdx.x & 31;
-  float m = -INFINITY, l = 0.f, acc[kCols];
+  float acc[kCols];
 #pragma unroll
   for (int e = 0; e < kCols; ++e) acc[e] = 0.f;
   // element offset of position x of the head, or -1
@@ -344,55 +345,49 @@ __device__ __noinline__ void own_row(const DecodeParams& p, const __nv_bfloat16*
                ? -1 : ((static_cast<int64_t>(id) * p.h_kv + kvh) * p.page_tokens + (x - idx * p.page_tokens)) * D;
   };
   for (int n0 = lo; n0 < hi; n0 += 32) {
-    float z = -INFINITY;
+    float w = 0.f;
     const int64_t mine = n0 + lane < hi ? place(n0 + lane) : -1;
     if (mine >= 0) {
-      const uint4* const kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k_pool) + mine);
+      const uint4* const kr = reinterpret_cast<const uint4*>(static_cast<const char*>(p.k_pool) + mine * (kE4 ? 1 : 2));
       f32x2 s = pack2(0.f, 0.f);
-#pragma unroll 4
-      for (int i = 0; i < D / 8; ++i) {
-        f32x2 x[4], y[4];
-        unpack16x2<BF16>(__ldg(kr + i), x);
-        unpack16x2<BF16>(__ldg(reinterpret_cast<const uint4*>(q) + i), y);
+      constexpr int kPer = kE4 ? 2 : 1;   // queries' 16-byte pieces to one of the keys
+#pragma unroll 2
+      for (int i = 0; i < D / 8 / kPer; ++i) {
+        f32x2 x[4 * kPer], y[4];
+        unpack16x2<std::conditional_t<kE4, E4M3, BF16>>(__ldg(kr + i), x);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s = fma2(x[j], y[j], s);
+        for (int e = 0; e < kPer; ++e) {
+          unpack16x2<BF16>(__ldg(reinterpret_cast<const uint4*>(q) + i * kPer + e), y);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s = fma2(x[4 * e + j], y[j], s);
+        }
       }
       const float2 t = unpack2(s);
-      z = (t.x + t.y) * p.qk_scale_log2;
+      const float z = (t.x + t.y) * p.qk_scale_log2;
+      w = m == -INFINITY ? 0.f : fast_exp2(z - m);   // (then every z is -inf)
     }
-    float top = z;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float m2 = max_nan(m, top);
-    if (m2 == -INFINITY) continue;
-    const float f = fast_exp2(m - m2);
-    const float w = mine >= 0 ? fast_exp2(z - m2) : 0.f;
-    float sum = w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = fmaf(l, f, sum);
-    m = m2;
-#pragma unroll
-    for (int e = 0; e < kCols; ++e) acc[e] *= f;
     for (int j = 0; j < min(32, hi - n0); ++j) {
       const float wj = __shfl_sync(0xffffffffu, w, j);
       const int64_t from = __shfl_sync(0xffffffffu, mine, j);
       if (from < 0) continue;
-      const __nv_bfloat16* const vr = static_cast<const __nv_bfloat16*>(p.v_pool) + from + lane * kCols;
+      const char* const vr = static_cast<const char*>(p.v_pool) + (from + lane * kCols) * (kE4 ? 1 : 2);
 #pragma unroll
       for (int e = 0; e < kCols; e += 2) {
-        const float2 x = bf16x2_to_float2(__ldg(reinterpret_cast<const uint32_t*>(vr + e)));
+        float2 x;
+        if constexpr (kE4) {
+          const uint32_t codes = __ldg(reinterpret_cast<const uint16_t*>(vr + e));
+          uint32_t lo, hi;
+          e4m3x4_to_f16x4(codes, lo, hi);
+          x = f16x2_floats(lo);
+        } else {
+          x = bf16x2_to_float2(__ldg(reinterpret_cast<const uint32_t*>(vr + 2 * e)));
+        }
         acc[e] = fmaf(wj, x.x, acc[e]);
         acc[e + 1] = fmaf(wj, x.y, acc[e + 1]);
       }
     }
   }
-  if (col0 == 0 && lane == 0) {
-    p.m_part[at] = m;
-    p.l_part[at] = l;
-  }
   if (lane * kCols < col0 || lane * kCols >= col1) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
   for (int e = 0; e < kCols; e += 2) {
     if constexpr (kHalf)
@@ -403,7 +398,9 @@ __device__ __noinline__ void own_row(const DecodeParams& p, const __nv_bfloat16*
 }
 
 // ---------------------------------------------------------------- prefixes
-template <int D, bool kE4, int kTermsOfP>
+// kOwn: it may have units of sequences' own positions. (E4M3 pools: without their code, a shared prefix of 65536 positions
+// takes 3 us less.)
+template <int D, bool kE4, int kTermsOfP, bool kOwn>
 struct PrefixWork {
   using Params = PrefixParams;
   static constexpr int kN = kTermsOfP == 3 || (kE4 && D == 256) ? 64 : 128;   // keys of a tile
@@ -428,7 +425,7 @@ struct PrefixWork {
   Cursor cur[2];
   int64_t place[2];          // byte offset of the piece in a pool, or -1
 
-  __device__ __forceinline__ static bool wait_late(const Params& p) { return kE4 || !p.own_tiles; }   // beside the one-warp kernel
+  __device__ __forceinline__ static bool wait_late(const Params& p) { return !kOwn || !p.own_tiles; }   // beside the one-warp kernel
   __device__ __forceinline__ int toks_per_tile() const { return tpt; }
   __device__ __forceinline__ int heads() const { return p.heads; }
   __device__ __forceinline__ PrefixWork(const Params& params) : p(params) {
@@ -471,7 +468,7 @@ struct PrefixWork {
     const int64_t place = static_cast<int64_t>(round) * gridDim.x + blockIdx.x;
     if (place >= n_units) return false;
     const int un = static_cast<int>(place), lane = threadIdx.x & 31;
-    if constexpr (!kF8) {   // (E4M3 pools: without the code, a shared prefix of 65536 positions takes 3 us less)
+    if constexpr (kOwn) {
       if (un >= n_prefix) {
         own_unit(un - n_prefix, u);
         return true;
@@ -657,8 +654,8 @@ struct PrefixWork {
       st_global_hint(p.a.l_part + at, l, keep);
     }
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // (a NaN stays one)
-    float sick = l * 0.f;   // a NaN, if some value is not finite
-    const bool parted = !kF8 && u.own && p.a.rows > 1;   // own positions of several rows
+    float sick = 0.f;   // or a NaN, if some value is not finite
+    const bool parted = kOwn && u.own && p.a.rows > 1;   // own positions of several rows
     if (parted) {
 #pragma unroll 1
       for (int i = 0; i < kCols; i += 32) {
@@ -698,7 +695,7 @@ struct PrefixWork {
         }
       }
     }
-    if constexpr (!kF8) {
+    if constexpr (kOwn) {
       // Among the own positions, some of the keys of the later rows are not the earlier ones', but a NaN or an infinity
       // among their values reaches all rows of the product (0 x NaN): rows that are not finite are computed again
       if (!parted) return;
@@ -708,7 +705,8 @@ struct PrefixWork {
         again &= again - 1;
         const int rt = __shfl_sync(0xffffffffu, tok, src), rh = __shfl_sync(0xffffffffu, head, src);
         const int64_t ra = __shfl_sync(0xffffffffu, at, src);
-        own_row<D, kHalfParts>(p.a, q_row(u, rt, rh), u.b, u.kvh, u.kv[t], min(u.end[t], u.pos + rt), ra, col0, col0 + kCols);
+        own_row<D, kE4, kHalfParts>(p.a, q_row(u, rt, rh), u.b, u.kvh, u.kv[t], min(u.end[t], u.pos + rt), ra,
+                                    __shfl_sync(0xffffffffu, m, src), __shfl_sync(0xffffffffu, inv, src), col0, col0 + kCols);
       }
     }
   }
@@ -838,9 +836,9 @@ bool query_map(const DecodeParams& a, int heads, CUtensorMap* map) {
   return true;
 }
 
-template <int D, bool kE4, int kTerms>
+template <int D, bool kE4, int kTerms, bool kOwn>
 cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, bool own_tiles, cudaStream_t stream) {
-  using W = PrefixWork<D, kE4, kTerms>;
+  using W = PrefixWork<D, kE4, kTerms, kOwn>;
   const DeviceInfo& di = device_info();
   const int heads = prefix_heads(a.group);
   PrefixParams p;
@@ -857,9 +855,15 @@ cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, bool own
 }
 template <int D>
 cudaError_t launch_prefix(const SharedParams& s, const DecodeParams& a, int pool_dtype, bool own_tiles, cudaStream_t stream) {
-  if (pool_dtype == NBX_E4M3)
-    return a.out_bf16 ? launch_prefix<D, true, 1>(s, a, own_tiles, stream) : launch_prefix<D, true, 2>(s, a, own_tiles, stream);
-  return a.out_bf16 ? launch_prefix<D, false, 1>(s, a, own_tiles, stream) : launch_prefix<D, false, 3>(s, a, own_tiles, stream);
+  if (pool_dtype == NBX_E4M3) {
+    if (own_tiles)
+      return a.out_bf16 ? launch_prefix<D, true, 1, true>(s, a, true, stream)
+                        : launch_prefix<D, true, 2, true>(s, a, true, stream);
+    return a.out_bf16 ? launch_prefix<D, true, 1, false>(s, a, false, stream)
+                      : launch_prefix<D, true, 2, false>(s, a, false, stream);
+  }
+  return a.out_bf16 ? launch_prefix<D, false, 1, true>(s, a, own_tiles, stream)
+                    : launch_prefix<D, false, 3, true>(s, a, own_tiles, stream);
 }
 
 }  // namespace
@@ -919,7 +923,7 @@ cudaError_t shared_dispatch(const SharedParams& s, const DecodeParams& p, int q_
   x.sets = p.h_q / heads;
   x.sms = di.sm_count;
   x.small = plan_small(p.batch, s.n_groups);
-  const bool own_tiles = pool_dtype == NBX_BF16 && p.rows * p.group >= kOwnTileVectors;
+  const bool own_tiles = p.rows * p.group >= kOwnTileVectors;
   x.own_pairs = (p.rows + x.tpt * x.tiles - 1) / (x.tpt * x.tiles);
   x.own_dual = x.tiles == 2 && p.rows <= x.tpt;
   cudaError_t e = launch_pdl(own_tiles ? shared_plan_kernel<true> : shared_plan_kernel<false>, 1u, kPlanThreads,

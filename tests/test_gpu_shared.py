@@ -247,10 +247,11 @@ def test_a_bad_page_in_the_prefix_and_a_bad_length(pool, d):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("page", [16, 48, 256])
 @pytest.mark.parametrize("rows,h_q", [(4, 8), (1, 16), (20, 4)])
-def test_own_positions_of_many_vectors(page, d, out, rows, h_q):
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+def test_own_positions_of_many_vectors(page, d, out, rows, h_q, pool):
     """Own positions of no, one and many tiles, sequences shorter than their rows, of no group, and empty."""
     groups = [(768, [769, 768 + 255, 768 + 256, 768 + 257, 1900]), (0, [1, 5, 0, 2000]), (0, [130]), (300, [300, 0, 431])]
-    Case(groups, rows, h_q, 2, d, page, "bf16", out, page + d).check_run()
+    Case(groups, rows, h_q, 2, d, page, pool, out, page + d).check_run()
 
 
 @pytest.mark.parametrize("n", [0, 3])
@@ -268,17 +269,19 @@ def test_many_sequences_of_many_vectors(n):
 
 @pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_scales_of_many_vectors(d, scale):
-    c = Case([(1024, [1100, 1030]), (0, [333])], 3, 8, 2, d, 16, "bf16", "f32", 8)
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+def test_scales_of_many_vectors(d, scale, pool):
+    c = Case([(1024, [1100, 1030]), (0, [333])], 3, 8, 2, d, 16, pool, "f32", 8)
     c.scale = scale
     c.check_run()
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-def test_a_bad_page_among_own_positions_of_many_vectors(d, out):
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+def test_a_bad_page_among_own_positions_of_many_vectors(d, out, pool):
     for page in (-1, 1 << 30):
-        c = Case([(1024, [1100, 1500])], 1, 16, 2, d, 16, "bf16", out, 14)
+        c = Case([(1024, [1100, 1500])], 1, 16, 2, d, 16, pool, out, 14)
         c.table[1, 70] = page
         status = ints([0])
         out_t = c.run(status=status)
@@ -352,25 +355,35 @@ def test_a_nan_in_the_prefix_reaches_all_of_its_head(pool, where):
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("d,h_q,rows", [(64, 8, 4), (128, 8, 4), (256, 8, 4), (128, 4, 4), (128, 24, 40), (256, 6, 70)])
-@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_values_of_later_rows_do_not_reach_earlier_ones(d, h_q, rows, out, bad):
-    """In a sequence's last positions, which its last rows alone see: at the last and at row r's own."""
-    c = Case([(512, [700, 620]), (0, [rows, 300])], rows, h_q, 2, d, 32, "bf16", out, 21)
-    hit = {0: rows - 1, 3: rows // 2}   # sequence -> the first row that sees the value
+@pytest.mark.parametrize("pool,bad", [("bf16", float("nan")), ("bf16", float("inf")), ("e4m3", float("nan"))])
+def test_values_of_later_rows_do_not_reach_earlier_ones(d, h_q, rows, out, pool, bad):
+    """In a sequence's last positions, which its last rows alone see: at the last and at row r's own; in a split's first key
+    tile, and in one whose maximum is an earlier tile's."""
+    c = Case([(512, [700, 620]), (0, [rows, 300, 120])], rows, h_q, 2, d, 32, pool, out, 21)
+
+    def put(kv, b, x, head, column, value):
+        y = c.pools[kv]
+        if pool == "e4m3":
+            y, value = y.view(torch.uint8), 0x7F if value != 0 else 0
+        y[c.table[b, x // 32].long(), head, x % 32, column] = value
+
+    hit = {0: rows - 1, 3: rows // 2, 4: rows - 1}   # sequence -> the first row that sees the value
     at = {b: c.lens_list[b] - rows + r for b, r in hit.items()}
     for b, x in at.items():
-        c.pools[1][c.table[b, x // 32].long(), 1, x % 32, 5] = bad
-        c.pools[0][c.table[b, x // 32].long(), 0, x % 32, 7] = bad
+        put(1, b, x, 1, 5, bad)
+        put(0, b, x, 0, 7, bad)
     out = c.run()
     torch.cuda.synchronize()
     for b, x in at.items():
         r, h = hit[b], h_q // 2
         assert bool(torch.isfinite(out[b, :r]).all())
         assert not bool(torch.isfinite(out[b, r:, h:, 5]).any())
-        # (an infinite key may leave a row its other weights; a NaN does not)
-        assert not bool(torch.isfinite(out[b, r:, :h]).all())
-        c.pools[1][c.table[b, x // 32].long(), 1, x % 32, 5] = 0
-        c.pools[0][c.table[b, x // 32].long(), 0, x % 32, 7] = 0
+        # a NaN among the key's elements leaves no score; +inf a score of -inf to a vector that is negative there (the
+        # scale is positive), which takes the key's weight away and leaves the others
+        spared = (c.q[b, r:, :h, 7] < 0) & (bad == float("inf"))
+        assert torch.equal(torch.isfinite(out[b, r:, :h]).all(-1), spared)
+        put(1, b, x, 1, 5, 0)
+        put(0, b, x, 0, 7, 0)
         want, tol = c.expect(b)
         assert bool(((out[b].double() - want).abs() <= tol)[:r].all())
     for b in (1, 2):
