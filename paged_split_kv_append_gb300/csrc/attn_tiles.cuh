@@ -15,7 +15,7 @@
 //    the same keys, or (dual units, whose query vectors fill one tile) the same vectors attend two ranges of keys. At
 //    d = 64 a P of 16-bit terms has columns of its own, the next S is computed while this one's exponentials run, and the
 //    turns fall away (8 prompts of 700 to 1700 tokens, 16 heads of 64: 52.4 us in turns, 46.7 so: 1.2 us for 128 keys, of
-//    which S is waited for in 0.06, where the two softmaxes share a scheduler's pipes in the same phases). At
+//    which S is waited for in 0.06; one softmax warp of a scheduler alone takes 0.5 us, two 1.0, in step or out of it). At
 //    d = 256 O fills half of the TMEM, so there is one M tile, S is double-buffered, and the groups share each row, half
 //    of the columns each; the two threads of a row swap their maxima through shared memory.
 //  * warps 9 and 10 issue the MMAs: QK^T (both operands from shared memory) and PV (P from TMEM, N = d). Up to d = 128 each
@@ -32,8 +32,9 @@
 //    vector into [2^14, 2^15): exact but for elements under 2^-29 of it. The softmax threads write them, each its own row,
 //    and take the factor back in their row's c. The running maximum sits 2^7 above P's largest weight then, so that small
 //    weights keep their bits in f16's range.
-// What bounds it: the tensor pipe (d = 64: the softmax). Per 128 keys and two tiles of d = 128 it is busy 2048 cycles; the softmax issues
-// about 900 instructions on each scheduler and takes 1024 cycles of the special-function units (4 a warp measured).
+// What bounds it: the tensor pipe (d = 64: the softmax). Per 128 keys and two tiles of d = 128 it is busy 2048 cycles; the
+// softmax issues about 900 instructions on each scheduler and takes 1024 cycles of the special-function units (4 a warp
+// measured).
 #pragma once
 
 #include <atomic>

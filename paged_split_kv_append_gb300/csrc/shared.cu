@@ -425,7 +425,8 @@ struct PrefixWork {
   Cursor cur[2];
   int64_t place[2];          // byte offset of the piece in a pool, or -1
 
-  __device__ __forceinline__ static bool wait_late(const Params& p) { return !kOwn || !p.own_tiles; }   // beside the one-warp kernel
+  // (beside the one-warp kernel)
+  __device__ __forceinline__ static bool wait_late(const Params& p) { return !kOwn || !p.own_tiles; }
   __device__ __forceinline__ int toks_per_tile() const { return tpt; }
   __device__ __forceinline__ int heads() const { return p.heads; }
   __device__ __forceinline__ PrefixWork(const Params& params) : p(params) {
