@@ -27,7 +27,7 @@
 //  * Paged K and V come by 16-byte cp.async of warps 12-15. (A tensor copy costs the copy engine some 135 ns whatever its
 //    size, and pages of 16 positions take 16 of 2 KB for 32 KB.)
 //  * warp 11 finds the units and hands them to the others through shared memory, one ahead.
-//  * E4M3 pools: warps 8 and 11 copy the codes of a tile as they are stored (cp.async), and warps 12-15 convert them to f16
+//  * E4M3 pools: warps 8 and 11 copy the codes of a tile as they are stored (bulk copies or cp.async), and warps 12-15 convert them to f16
 //    (exactly) into the ring. Queries enter as f16 too, times a power of two that brings the largest element of each
 //    vector into [2^14, 2^15): exact but for elements under 2^-29 of it. The softmax threads write them, each its own row,
 //    and take the factor back in their row's c. The running maximum sits 2^7 above P's largest weight then, so that small
@@ -227,7 +227,7 @@ constexpr int kAtPCol = 384;      // [2][64] columns
 
 // What a work policy W provides (prompt.cu, shared.cu):
 //   typename W::Params with c (|scale| log2 e, or the least positive number for a scale of 0), negative and status;
-//   W::kN, kTerms, kF8, kPaged, kMayWaitLate and wait_late(params); begin() and bool unit(round, AttnUnit&) of the warp that
+//   W::kN, kTerms, kF8, kBulk, kPaged, kMayWaitLate and wait_late(params); begin() and bool unit(round, AttnUnit&) of the warp that
 //   finds the units (toks > 0 in each); toks_per_tile(), heads(); last_keys, last_key, bad_keys; load_q / load_kv by the
 //   loader warps (or q_row for the softmax threads); store(...) by a softmax warp.
 template <class C>
@@ -857,7 +857,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
       mbar_init(&sh.empty[i], 2);
     }
     for (int i = 0; i < C::kRaws; ++i) {
-      mbar_init(&sh.raw_full[i], 64);
+      mbar_init(&sh.raw_full[i], W::kBulk ? 2 : 64);
       mbar_init(&sh.raw_empty[i], kAtCopyWarps);
     }
     mbar_init(sh.q_full, W::kF8 ? 8 : 1);

@@ -39,6 +39,7 @@ struct PromptWork {
   static constexpr int kN = 128;   // keys of a tile
   static constexpr bool kF8 = false;
   static constexpr bool kPaged = false;
+  static constexpr bool kBulk = false;
   static constexpr bool kMayWaitLate = false;
   static constexpr int kTerms = 1;
   const Params& p;

@@ -406,6 +406,9 @@ struct PrefixWork {
   static constexpr int kN = kTermsOfP == 3 || (kE4 && D == 256) ? 64 : 128;   // keys of a tile
   static constexpr bool kF8 = kE4;
   static constexpr bool kPaged = true;
+  // E4M3 codes come by bulk copies up to d = 128 (32 sequences behind 65536, pages of 64: 95.3 us by cp.async, 91.0 so; behind
+  // 32768, pages of 16: 70.7 and 66.6), by cp.async at d = 256 (85.0, by bulk copies 91.1).
+  static constexpr bool kBulk = kE4 && D <= 128;
   static constexpr bool kMayWaitLate = true;
   static constexpr int kTerms = kTermsOfP;
   // A bf16 output takes the partials as bf16(acc / l), in the first half of their slots: half the bytes both ways,
@@ -604,7 +607,32 @@ struct PrefixWork {
     }
     const char* const pool = static_cast<const char*>(is_v ? p.a.v_pool : p.a.k_pool);
     const int held = min(kPieces, (u.end[t] - u.kv[t] - j * kN + 15) >> 4);   // pieces of the tile before the end
-    if constexpr (kF8) {      // the codes as they are stored
+    if constexpr (kBulk) {
+      // The codes as they are stored, half a tile a warp: each run of pieces that lie together (a page, or what is left of the
+      // half) is one bulk copy. What a missing page would hold is zeroed.
+      constexpr int kBytes = 16 * D;
+      const int first = loader * (kPieces / 2);
+      const bool mine = lane >= first && lane < min(first + kPieces / 2, held);
+      const bool have = mine && at >= 0;
+      const int64_t before = __shfl_up_sync(0xffffffffu, at, 1);
+      const bool leads = have && !(lane > first && before >= 0 && before + kBytes == at);
+      const uint32_t got = __ballot_sync(0xffffffffu, have), heads = __ballot_sync(0xffffffffu, leads);
+      uint32_t missing = __ballot_sync(0xffffffffu, mine && !have);
+      if (missing) {
+        for (; missing; missing &= missing - 1)
+          for (int i = lane; i < kBytes / 16; i += 32)
+            sts128(smem_u32(dst) + (__ffs(missing) - 1) * kBytes + i * 16, make_uint4(0, 0, 0, 0));
+        fence_proxy_async();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive_expect_tx(bar, __popc(got) * kBytes);
+      __syncwarp();
+      if (leads) {
+        const uint32_t ends = ~(got & ~heads) >> lane >> 1;   // bit 0: piece lane + 1 is not of the run
+        bulk_g2s(dst + lane * kBytes, pool + at, (ends ? __ffs(ends) : 32) * kBytes, bar);
+      }
+      return;
+    } else if constexpr (kF8) {
       const uint32_t to = smem_u32(dst) + lane * 16;
       const char* const from = pool + lane * 16;
 #pragma unroll
