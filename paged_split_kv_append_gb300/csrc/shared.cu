@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
 // ---------------------------------------------------------------- one row
 // acc = sum_j 2^(z_j - m) v_j of one query vector over positions [lo, hi) of sequence b, key by key in fp32, by one warp;
 // columns [col0, col1) of it, or (kHalf) of bf16(acc inv), go to the partial `at`. m is the partial's own: at d = 256 the
-// other columns, and l, belong to it.
+// other columns, and l, belong to it; -inf where every z is, a NaN where one is.
 template <int D, bool kE4, bool kHalf>
 __device__ __noinline__ void own_row(const DecodeParams& p, const __nv_bfloat16* q, int b, int kvh, int lo, int hi, int64_t at,
                                      float m, float inv, int col0, int col1) {
@@ -364,7 +364,7 @@ __device__ __noinline__ void own_row(const DecodeParams& p, const __nv_bfloat16*
       }
       const float2 t = unpack2(s);
       const float z = (t.x + t.y) * p.qk_scale_log2;
-      w = m == -INFINITY ? 0.f : fast_exp2(z - m);   // (then every z is -inf)
+      w = m == -INFINITY ? 0.f : fast_exp2(z - m);
     }
     for (int j = 0; j < min(32, hi - n0); ++j) {
       const float wj = __shfl_sync(0xffffffffu, w, j);
@@ -678,6 +678,9 @@ struct PrefixWork {
     const uint64_t keep = l2_keep_policy(p.a.keep_frac);
     const int64_t row = (static_cast<int64_t>(u.tok) + tok) * p.a.h_q + u.head + head;
     const int64_t at = row * p.a.max_splits + u.slot[t];
+    // A NaN score leaves the running maximum alone, -inf where the row's every score here is a NaN: the merge, which skips
+    // such a split, learns of it from m
+    if (l != l) m = l;
     if (ok && col0 == 0) {
       st_global_hint(p.a.m_part + at, m, keep);
       st_global_hint(p.a.l_part + at, l, keep);
