@@ -3,7 +3,7 @@
 //
 // A work unit is one or two M tiles of 128 query vectors of one KV head (a tile holds some tokens with `heads` query heads
 // each) and the keys they attend, in tiles of kN. Per key tile, with scores in log2 units:
-//   S = Q K^T;  m' = max(m, rowmax S) (moved only when it grows by more than 2^8);  P = 2^(c S - m');
+//   S = Q K^T;  m' = max(m, rowmax S) (moved only when it grows by more than 2^8);  P = 2^(c S - m'), 2^-8 to 1 at most;
 //   l = l 2^(m - m') + rowsum P;  O = O 2^(m - m') + P V.
 // S and O are fp32 accumulators in TMEM; P is written over S in kTerms terms of the values' 16-bit type: one for bf16
 // outputs (each weight off by up to 2^-8 of itself in bf16, as much as the output's own rounding; 2^-11 in f16), for fp32
@@ -587,7 +587,10 @@ template <class W, class C, int D>
 __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint32_t tmem) {
   constexpr int T = C::kTiles, NC = C::kCols, N = W::kN;
   constexpr int kOCols = T == 2 ? D : D / 2;   // columns of O that this thread rescales and stores
-  constexpr float kMid = W::kF8 ? 7.f : 0.f;   // log2 of the largest weight when m has moved
+  // log2 of the largest weight when m has moved. In bf16 and fp32 as low as keeps weights at 1 or less until it moves again:
+  // O then passes fp32's range no sooner than in sums of weights under a maximum that always moves (values of 2^118 and
+  // weights of 2^7.5 did). In f16's range as high as it goes: E4M3's values are 448 at most.
+  constexpr float kMid = W::kF8 ? 7.f : -kAtTau;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = warp >> 2, quarter = warp & 3;
   const int row = quarter * 32 + lane;
