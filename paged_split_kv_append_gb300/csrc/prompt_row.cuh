@@ -39,9 +39,9 @@ __device__ __noinline__ void prompt_row(const __nv_bfloat16* q, const __nv_bfloa
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float m2 = max_nan(m, top);
-    if (m2 == -INFINITY) continue;
-    const float f = fast_exp2(m - m2);
-    const float w = n0 + lane < n ? fast_exp2(z - m2) : 0.f;
+    const float ref = m2 == -INFINITY ? 0.f : m2;   // (no score yet: weights of 0, under which a NaN value still is one)
+    const float f = fast_exp2(m - ref);
+    const float w = n0 + lane < n ? fast_exp2(z - ref) : 0.f;
     float sum = w;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
