@@ -157,19 +157,6 @@ __device__ __forceinline__ void add_tile(float (&acc)[4], uint32_t a0, uint32_t 
   for (int i = 0; i < 4; ++i) acc[i] += o[i];
 }
 
-// A 16-byte chunk of V that holds a NaN (E4M3) or a value that is not finite (bf16).
-template <bool kE4>
-__device__ __forceinline__ bool not_finite(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t bad = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (kE4) bad |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    else bad |= ((w[i] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
-  }
-  return bad != 0;
-}
-
 // tanh for the cap: a polynomial up to 0.75 (relative error 1.2e-8); above, CUDA's.
 __device__ __forceinline__ float small_tanh(float x) {
   const float u = x * x;

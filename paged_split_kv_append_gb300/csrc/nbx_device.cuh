@@ -174,8 +174,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // 2^x with the hardware approximation (relative error ~2^-22; ex2(-inf) = +0), results below
-// 2^-126 flushed to +0. Every caller weights terms against a largest weight of at least 1 in the
-// same sum (a softmax weight against the row maximum, a split against the largest split maximum),
+// 2^-126 flushed to +0. Every caller weights terms against a largest weight of at least 2^-8 in
+// the same sum (a softmax weight against the row maximum, a split against the largest split maximum),
 // so a flushed weight is far below the sum's fp32 resolution; without the flush each call carries
 // extra instructions for subnormal results.
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -189,6 +189,19 @@ __device__ __forceinline__ float fast_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// A 16-byte chunk of V that holds a NaN (E4M3) or a value that is not finite (bf16).
+template <bool kE4>
+__device__ __forceinline__ bool not_finite(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kE4) bad |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    else bad |= ((w[i] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
+  }
+  return bad != 0;
 }
 
 // ---------------------------------------------------------------- status word

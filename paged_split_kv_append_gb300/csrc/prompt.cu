@@ -8,8 +8,8 @@
 //    seq_start: units are ordered by their block's place in its sequence, the last (those with most keys) first, and
 //    dealt to the CTAs there and back. With S(i) = the number of blocks at place i or later, unit u lies at the place i
 //    with S(i + 1) <= u < S(i). No plan kernel, no workspace.
-//  * A row whose output is not finite is computed again key by key (prompt_row): a NaN or an infinity among the values
-//    that a tile holds but the row does not see (0 x NaN) stays out of it.
+//  * A NaN or an infinity among the values that a tile holds but the row does not see (0 x NaN) stays out of it: a row whose
+//    output is not finite, with such a value behind it in its last tile, is computed again key by key (prompt_row).
 #include <algorithm>
 #include <cmath>
 #include <limits>
@@ -155,7 +155,7 @@ struct PromptWork {
     else tma_load_4d(dst, &p.k, 0, row, part * 2, u.kvh, bar);
   }
   template <int kCols>
-  __device__ __forceinline__ void store(const AttnUnit& u, int, uint32_t o_base, int col0, int tok, int head, bool ok, float m,
+  __device__ __forceinline__ void store(const AttnUnit& u, int t, uint32_t o_base, int col0, int tok, int head, bool ok, float m,
                                         float l, uint64_t* o_free) const {
     const int lane = threadIdx.x & 31;
     const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -188,7 +188,21 @@ struct PromptWork {
       }
     }
     const float2 s = unpack2(sick);
-    uint32_t again = __ballot_sync(0xffffffffu, ok && !(s.x + s.y == 0.f));
+    const bool odd = ok && !(s.x + s.y == 0.f);
+    if (!__any_sync(0xffffffffu, odd)) return;
+    if (odd && l == 0.f) {   // every score is -inf: 0
+      const float none[8] = {};
+#pragma unroll 1
+      for (int i = 0; i < kCols; i += 16) st_global_v8(reinterpret_cast<float*>(out + row * D + col0 + i), none);
+    }
+    // A score that is a NaN leaves l one, and the row its NaN. For the others: is there a value that is not finite behind the
+    // row, among those that its tile's last products took?
+    const __nv_bfloat16* const v = static_cast<const __nv_bfloat16*>(p.a.v) + u.kv[0] * p.a.v_stride + static_cast<int64_t>(u.kvh) * D;
+    const bool may = odd && l > 0.f;
+    if (!__any_sync(0xffffffffu, may)) return;
+    const int pos = u.pos + tok, first = __reduce_min_sync(0xffffffffu, may ? pos + 1 : 0x7fffffff);
+    const int last = last_not_finite(v, p.a.v_stride, first, min(u.n[t] * kN, u.pos + u.toks), col0, col0 + kCols);
+    uint32_t again = __ballot_sync(0xffffffffu, may && pos < last);
     while (again) {
       const int src = __ffs(again) - 1;
       again &= again - 1;
@@ -197,8 +211,7 @@ struct PromptWork {
       prompt_row<D>(static_cast<const __nv_bfloat16*>(p.a.q) + (static_cast<int64_t>(u.tok) + rt) * p.a.q_stride +
                         (rr % p.a.h_q) * D,
                     static_cast<const __nv_bfloat16*>(p.a.k) + u.kv[0] * p.a.k_stride + static_cast<int64_t>(u.kvh) * D,
-                    static_cast<const __nv_bfloat16*>(p.a.v) + u.kv[0] * p.a.v_stride + static_cast<int64_t>(u.kvh) * D,
-                    p.a.k_stride, p.a.v_stride, u.pos + rt + 1, p.a.scale_log2, out + rr * D, col0, col0 + kCols);
+                    v, p.a.k_stride, p.a.v_stride, u.pos + rt + 1, p.a.scale_log2, out + rr * D, col0, col0 + kCols);
     }
   }
 };

@@ -1,4 +1,4 @@
-// Causal attention of one query vector, key by key in fp32, by one warp.
+// Causal attention of one query vector, key by key in fp32, by one warp; and which rows need it.
 #pragma once
 
 #include "nbx_device.cuh"
@@ -69,6 +69,17 @@ __device__ __noinline__ void prompt_row(const __nv_bfloat16* q, const __nv_bfloa
                                             : __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
     *reinterpret_cast<__nv_bfloat162*>(out + lane * kCols + e) = h;
   }
+}
+
+// The last of keys [lo, hi) whose value has an element among columns [col0, col1) that is not finite, or -1. A warp's work.
+__device__ __noinline__ int last_not_finite(const __nv_bfloat16* v, int64_t v_stride, int lo, int hi, int col0, int col1) {
+  const int chunks = (col1 - col0) / 8;
+  int last = -1;
+  for (int i = threadIdx.x & 31; i < (hi - lo) * chunks; i += 32) {
+    const int key = lo + i / chunks, chunk = i % chunks;
+    if (not_finite<false>(__ldg(reinterpret_cast<const uint4*>(v + key * v_stride + col0) + chunk))) last = key;
+  }
+  return __reduce_max_sync(0xffffffffu, last);
 }
 
 }  // namespace nbx

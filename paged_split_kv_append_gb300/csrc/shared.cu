@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
 // ---------------------------------------------------------------- one row
 // acc = sum_j 2^(z_j - m) v_j of one query vector over positions [lo, hi) of sequence b, key by key in fp32, by one warp;
 // columns [col0, col1) of it, or (kHalf) of bf16(acc inv), go to the partial `at`. m is the partial's own: at d = 256 the
-// other columns, and l, belong to it; -inf where every z is, a NaN where one is.
+// other columns, and l, belong to it. (It is finite: a row with a NaN among its scores, or with none above -inf, is not
+// computed again.)
 template <int D, bool kE4, bool kHalf>
 __device__ __noinline__ void own_row(const DecodeParams& p, const __nv_bfloat16* q, int b, int kvh, int lo, int hi, int64_t at,
                                      float m, float inv, int col0, int col1) {
@@ -364,7 +365,7 @@ __device__ __noinline__ void own_row(const DecodeParams& p, const __nv_bfloat16*
       }
       const float2 t = unpack2(s);
       const float z = (t.x + t.y) * p.qk_scale_log2;
-      w = m == -INFINITY ? 0.f : fast_exp2(z - m);
+      w = fast_exp2(z - m);
     }
     for (int j = 0; j < min(32, hi - n0); ++j) {
       const float wj = __shfl_sync(0xffffffffu, w, j);
@@ -395,6 +396,23 @@ __device__ __noinline__ void own_row(const DecodeParams& p, const __nv_bfloat16*
     else
       *reinterpret_cast<float2*>(p.acc_part + at * D + lane * kCols + e) = make_float2(acc[e], acc[e + 1]);
   }
+}
+
+// The last of positions [lo, hi) of sequence b whose value has an element among columns [col0, col1) that is not finite, or
+// -1. A warp's work.
+template <int D, bool kE4>
+__device__ __noinline__ int own_not_finite(const DecodeParams& p, int b, int kvh, int lo, int hi, int col0, int col1) {
+  constexpr int kElt = kE4 ? 1 : 2;
+  const int chunks = (col1 - col0) * kElt / 16;
+  int last = -1;
+  for (int i = threadIdx.x & 31; i < (hi - lo) * chunks; i += 32) {
+    const int x = lo + i / chunks, idx = x / p.page_tokens;
+    const int id = __ldcg(p.block_table + static_cast<int64_t>(b) * p.max_pages + idx);
+    if (id < 0 || id >= p.num_pages) continue;
+    const int64_t at = ((static_cast<int64_t>(id) * p.h_kv + kvh) * p.page_tokens + (x - idx * p.page_tokens)) * D + col0;
+    if (not_finite<kE4>(__ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.v_pool) + at * kElt) + i % chunks))) last = x;
+  }
+  return __reduce_max_sync(0xffffffffu, last);
 }
 
 // ---------------------------------------------------------------- prefixes
@@ -729,9 +747,15 @@ struct PrefixWork {
     }
     if constexpr (kOwn) {
       // Among the own positions, some of the keys of the later rows are not the earlier ones', but a NaN or an infinity
-      // among their values reaches all rows of the product (0 x NaN): rows that are not finite are computed again
+      // among their values reaches all rows of the product (0 x NaN): rows that are not finite, with such a value behind
+      // them, are computed again. (Not those with l = 0, which the merge skips, or a NaN, which is every column's.)
       if (!parted) return;
-      uint32_t again = __ballot_sync(0xffffffffu, ok && sick != 0.f);
+      const bool may = ok && sick != 0.f && l > 0.f;
+      if (!__any_sync(0xffffffffu, may)) return;
+      const int past = max(u.kv[t], u.pos + tok);   // the first position that the row does not see
+      const int first = __reduce_min_sync(0xffffffffu, may ? past : 0x7fffffff);
+      const int last = own_not_finite<D, kE4>(p.a, u.b, u.kvh, first, u.end[t], col0, col0 + kCols);
+      uint32_t again = __ballot_sync(0xffffffffu, may && past <= last);
       while (again) {
         const int src = __ffs(again) - 1;
         again &= again - 1;

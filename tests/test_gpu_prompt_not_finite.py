@@ -1,19 +1,49 @@
-"""Prompts with values that are not finite."""
+"""Values that are not finite, in prompts and among own positions. Rows that see them are done as quickly as any other."""
+
+import math
 
 import pytest
 import torch
 
 import paged_split_kv_append_gb300 as nbx
-from test_gpu_prompt import check, expect, inputs, near, starts
+from test_gpu_prompt import check, expect, inputs, ints, near, starts
+from test_gpu_shared import Case
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 INF, NAN = float("inf"), float("nan")
+LIMIT_NS = 20_000_000   # the calls below take about 1 ms
 
 
 @pytest.fixture(scope="module", autouse=True)
 def built():
     nbx.build()
+    yield
+    nbx.nbx_set_decode_wait_test(0, 0)
+
+
+def call_with_limit(q, k, v, n, scale):
+    """A call whose waits may take 20 ms. (Every wait is bounded: one that ran out would set a bit, and the call return.)"""
+    status = ints([0])
+    nbx.nbx_set_decode_wait_test(LIMIT_NS, 0)
+    out = nbx.nbx_prompt_attn(q, k, v, starts([n]), scale, status=status)
+    torch.cuda.synchronize()
+    nbx.nbx_set_decode_wait_test(0, 0)
+    assert int(status) == 0
+    return out
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bad", [INF, -INF, NAN])
+def test_a_value_that_every_row_sees(d, bad):
+    """16384 rows that all see the value of the first key: not one is computed again."""
+    n, scale = 16384, 1 / math.sqrt(d)
+    q, k, v = inputs(n, 8, 1, d, d, fused=False)
+    v[0, 0, 7] = bad
+    out = call_with_limit(q, k, v, n, scale)
+    assert bool((torch.isnan(out[:, :, 7]) if bad != bad else out[:, :, 7] == bad).all())
+    rows = [0, 1, 127, 128, 5000, n - 1]
+    near(out[rows], *expect(q, k, v, 0, n, scale, rows))
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
@@ -42,3 +72,31 @@ def test_rows_without_a_score_beside_such_values(d):
     assert bool((out[:150] == 0).all())
     want, tol = expect(q, k, v, 0, 200, 0.1, list(range(150, 200)))
     near(out[150:], want, tol)
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_own_positions_that_every_row_sees(pool, d):
+    """Windows of 64 rows behind 3000 positions, two units an SM and more: the fourth position holds such a value, and none of
+    the rows, of which the earlier ones do not see the last positions, is computed again."""
+    c = Case([(0, [3000])] * 160, 64, 8, 2, d, 64, pool, "f32", d)
+    v = c.pools[1].view(torch.uint8) if pool == "e4m3" else c.pools[1]
+    first = c.table[:, 0].long()
+    v[first, 0, 3, 7] = 0x7F if pool == "e4m3" else INF
+    v[first[::2], 1, 3, 9] = 0x7F if pool == "e4m3" else -INF
+    out, status = torch.empty_like(c.q, dtype=torch.float32), ints([0])
+    ws = torch.empty(nbx.nbx_paged_decode_shared_workspace_bytes(160, 64, 8, 2, d, c.max_len, 160), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    nbx.nbx_set_decode_wait_test(2_000_000, 0)   # (the call takes less)
+    c.run(out=out, workspace=ws, status=status)
+    torch.cuda.synchronize()
+    nbx.nbx_set_decode_wait_test(0, 0)
+    assert int(status) == 0
+    odd = torch.zeros(out.shape, dtype=torch.bool, device=DEV)
+    odd[:, :, :4, 7] = True
+    odd[::2, :, 4:, 9] = True
+    assert torch.equal(torch.isfinite(out), ~odd)
+    v[first, 0, 3, 7] = v[first[::2], 1, 3, 9] = 0
+    for b in (0, 1, 158, 159):
+        want, tol = c.expect(b)
+        assert bool((((out[b].double() - want).abs() <= tol) | odd[b]).all())
