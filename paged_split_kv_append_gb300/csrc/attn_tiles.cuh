@@ -104,20 +104,27 @@ static_assert(sizeof(AttnUnit) == 64, "a unit is four 16-byte words");
 // What the roles of a CTA share beside barriers, in shared memory.
 struct AttnControl {
   int abort;          // some role has given up
-  uint32_t tmem;      // TMEM's first column
+  int busy;           // warps that compute rows again: as long as there are some, no wait runs out
   uint64_t wait_ns;   // how long a wait may take
+  uint32_t tmem;      // TMEM's first column
 };
+static_assert(sizeof(AttnControl) <= 32, "x_bar lies behind it");
 __device__ __forceinline__ const volatile AttnControl* volatile_of(const AttnControl* c) { return c; }
 __device__ __forceinline__ void volatile_set(AttnControl* c) { static_cast<volatile AttnControl*>(c)->abort = 1; }
+// This warp begins (1) or ends (-1) to compute rows again, which takes as long as their keys are many, and ends by itself.
+__device__ __forceinline__ void at_busy(AttnControl* c, int more) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) atomicAdd(&c->busy, more);
+}
 
 // Bounded wait of a whole warp, with one answer: gives up when another role of the CTA has, or after the limit (2 s, but in
-// a test of this path). Every branch is on a vote, so the compiler knows the warp to be together behind it (and may use
+// a test of this path), which begins anew while some warp computes rows again. Every branch is on a vote, so the compiler knows the warp to be together behind it (and may use
 // uniform registers there).
 // The loop is a function, one for all sites of the warps beside the softmax (whose registers leave no room for a call): up to
 // fourteen warps wait at a time, and loops of their own pushed the others' code out of the instruction caches (stalls for
 // want of an instruction were a third of a shared E4M3 prefix's cycles).
 __device__ __forceinline__ bool at_wait_loop(uint32_t bar, uint32_t parity, const AttnControl* ctl) {
-  const uint64_t t0 = global_timer_ns();
+  uint64_t t0 = global_timer_ns();
   for (;;) {
     uint32_t ok = 0;
 #pragma unroll 1
@@ -132,7 +139,10 @@ __device__ __forceinline__ bool at_wait_loop(uint32_t bar, uint32_t parity, cons
       ok = __all_sync(0xffffffffu, ok != 0);
     }
     if (ok) return true;
-    if (__any_sync(0xffffffffu, volatile_of(ctl)->abort != 0 || global_timer_ns() - t0 > ctl->wait_ns)) return false;
+    const bool busy = volatile_of(ctl)->busy != 0;
+    const uint64_t now = global_timer_ns();
+    if (__any_sync(0xffffffffu, volatile_of(ctl)->abort != 0 || (!busy && now - t0 > ctl->wait_ns))) return false;
+    if (busy) t0 = now;
   }
 }
 __device__ __noinline__ bool at_wait_call(uint32_t bar, uint32_t parity, const AttnControl* ctl) {
@@ -749,7 +759,7 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
       l = group == 0 ? l + other : other + l;
     }
     if (!pv_wait()) return false;
-    w.template store<kOCols>(u, t, o_base, T == 2 ? 0 : group * kOCols, my_tok, head, row_ok, m, l, &sh.o_free[t]);
+    w.template store<kOCols>(u, t, o_base, T == 2 ? 0 : group * kOCols, my_tok, head, row_ok, m, l, &sh.o_free[t], sh.ctl);
   }
   return true;
 }
@@ -883,6 +893,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_tiles_kernel(const __grid_
     if constexpr (C::kTiles == 1)
       for (int i = 0; i < 4; ++i) mbar_init(&sh.x_bar[i], 2);
     sh.ctl->abort = 0;
+    sh.ctl->busy = 0;
     sh.ctl->wait_ns = params.wait_ns();
     fence_mbar_init();
   }

@@ -156,7 +156,7 @@ struct PromptWork {
   }
   template <int kCols>
   __device__ __forceinline__ void store(const AttnUnit& u, int t, uint32_t o_base, int col0, int tok, int head, bool ok, float m,
-                                        float l, uint64_t* o_free) const {
+                                        float l, uint64_t* o_free, AttnControl* ctl) const {
     const int lane = threadIdx.x & 31;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.a.out);
@@ -203,6 +203,8 @@ struct PromptWork {
     const int pos = u.pos + tok, first = __reduce_min_sync(0xffffffffu, may ? pos + 1 : 0x7fffffff);
     const int last = last_not_finite(v, p.a.v_stride, first, min(u.n[t] * kN, u.pos + u.toks), col0, col0 + kCols);
     uint32_t again = __ballot_sync(0xffffffffu, may && pos < last);
+    if (!again) return;
+    at_busy(ctl, 1);
     while (again) {
       const int src = __ffs(again) - 1;
       again &= again - 1;
@@ -213,6 +215,7 @@ struct PromptWork {
                     static_cast<const __nv_bfloat16*>(p.a.k) + u.kv[0] * p.a.k_stride + static_cast<int64_t>(u.kvh) * D,
                     v, p.a.k_stride, p.a.v_stride, u.pos + rt + 1, p.a.scale_log2, out + rr * D, col0, col0 + kCols);
     }
+    at_busy(ctl, -1);
   }
 };
 

@@ -691,7 +691,7 @@ struct PrefixWork {
   }
   template <int kCols>
   __device__ __forceinline__ void store(const AttnUnit& u, int t, uint32_t o_base, int col0, int tok, int head, bool ok,
-                                        float m, float l, uint64_t* o_free) const {
+                                        float m, float l, uint64_t* o_free, AttnControl* ctl) const {
     const int lane = threadIdx.x & 31;
     const uint64_t keep = l2_keep_policy(p.a.keep_frac);
     const int64_t row = (static_cast<int64_t>(u.tok) + tok) * p.a.h_q + u.head + head;
@@ -756,6 +756,8 @@ struct PrefixWork {
       const int first = __reduce_min_sync(0xffffffffu, may ? past : 0x7fffffff);
       const int last = own_not_finite<D, kE4>(p.a, u.b, u.kvh, first, u.end[t], col0, col0 + kCols);
       uint32_t again = __ballot_sync(0xffffffffu, may && past <= last);
+      if (!again) return;
+      at_busy(ctl, 1);
       while (again) {
         const int src = __ffs(again) - 1;
         again &= again - 1;
@@ -764,6 +766,7 @@ struct PrefixWork {
         own_row<D, kE4, kHalfParts>(p.a, q_row(u, rt, rh), u.b, u.kvh, u.kv[t], min(u.end[t], u.pos + rt), ra,
                                     __shfl_sync(0xffffffffu, m, src), __shfl_sync(0xffffffffu, inv, src), col0, col0 + kCols);
       }
+      at_busy(ctl, -1);
     }
   }
 };

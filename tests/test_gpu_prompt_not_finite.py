@@ -1,4 +1,5 @@
-"""Values that are not finite, in prompts and among own positions. Rows that see them are done as quickly as any other."""
+"""Values that are not finite, in prompts and among own positions. Rows that see them are done as quickly as any other; rows
+that merely share a key tile with them are computed again, however long that takes."""
 
 import math
 
@@ -43,6 +44,19 @@ def test_a_value_that_every_row_sees(d, bad):
     out = call_with_limit(q, k, v, n, scale)
     assert bool((torch.isnan(out[:, :, 7]) if bad != bad else out[:, :, 7] == bad).all())
     rows = [0, 1, 127, 128, 5000, n - 1]
+    near(out[rows], *expect(q, k, v, 0, n, scale, rows))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_value_behind_the_rows_of_its_tile(d):
+    """The last key's value: the rows before it in the last tile of keys, which do not see it, are computed again over all
+    their 16384 keys, while the units behind them wait."""
+    n, scale = 16384, 1 / math.sqrt(d)
+    q, k, v = inputs(n, 8, 1, d, d, fused=False)
+    v[n - 1, 0, 7] = NAN
+    out = call_with_limit(q, k, v, n, scale)
+    assert bool(torch.isnan(out[n - 1, :, 7]).all())
+    rows = [0, 5000, n - 129, n - 128, n - 100, n - 2, n - 1]
     near(out[rows], *expect(q, k, v, 0, n, scale, rows))
 
 
@@ -97,6 +111,31 @@ def test_own_positions_that_every_row_sees(pool, d):
     odd[::2, :, 4:, 9] = True
     assert torch.equal(torch.isfinite(out), ~odd)
     v[first, 0, 3, 7] = v[first[::2], 1, 3, 9] = 0
+    for b in (0, 1, 158, 159):
+        want, tol = c.expect(b)
+        assert bool((((out[b].double() - want).abs() <= tol) | odd[b]).all())
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_own_positions_behind_earlier_rows(pool, d):
+    """Such a value at the last of 3000 positions: 63 of the 64 rows are computed again, while the units behind them wait."""
+    c = Case([(0, [3000])] * 160, 64, 8, 2, d, 64, pool, "f32", d)
+    v = c.pools[1].view(torch.uint8) if pool == "e4m3" else c.pools[1]
+    at, off = c.table[:, 2999 // 64].long(), 2999 % 64
+    v[at, :, off, 7] = 0x7F if pool == "e4m3" else NAN
+    out, status = torch.empty_like(c.q, dtype=torch.float32), ints([0])
+    ws = torch.empty(nbx.nbx_paged_decode_shared_workspace_bytes(160, 64, 8, 2, d, c.max_len, 160), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    nbx.nbx_set_decode_wait_test(2_000_000, 0)
+    c.run(out=out, workspace=ws, status=status)
+    torch.cuda.synchronize()
+    nbx.nbx_set_decode_wait_test(0, 0)
+    assert int(status) == 0
+    odd = torch.zeros(out.shape, dtype=torch.bool, device=DEV)
+    odd[:, 63, :, 7] = True
+    assert torch.equal(torch.isfinite(out), ~odd)
+    v[at, :, off, 7] = 0
     for b in (0, 1, 158, 159):
         want, tol = c.expect(b)
         assert bool((((out[b].double() - want).abs() <= tol) | odd[b]).all())
