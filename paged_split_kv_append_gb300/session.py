@@ -111,7 +111,10 @@ class PagedDecodeSession:
 
     def prompt(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start: torch.Tensor,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """Causal attention over packed prompts (their own keys and values, not the pools')."""
+        """Causal attention over packed prompts (their own keys and values, not the pools'). It knows of no score
+        modification: while one is set, whose decodes would attend otherwise, it is refused."""
+        if self.modifications.get("softcap") or any(isinstance(x, torch.Tensor) for x in self.modifications.values()):
+            raise ValueError("prompts take no score modification, and the session has one set")
         return nbx_prompt_attn(q, k, v, seq_start, self.scale, out=out, status=self.status, stream=stream)
 
     def prefill(self, k_raw: torch.Tensor, v_raw: torch.Tensor, index, slots, chunk_tokens: int = 1 << 18) -> None:
