@@ -87,6 +87,8 @@ class PagedDecodeSession:
         self.scale, self.k_scale, self.v_scale = 1.0, 1.0, 1.0
         self.modifications = {}
         self.groups = None
+        if shared_groups:   # what a decode without groups is given
+            self._no_groups = tuple(torch.zeros(n, dtype=torch.int32, device=self.device) for n in (1, 0))
         self._page_workspaces = []
 
     # ---------------------------------------------------------------- state
@@ -207,9 +209,6 @@ class PagedDecodeSession:
                                     status=self.status, stream=stream)[1:]
 
     # ---------------------------------------------------------------- the step
-    def _no_groups(self, n: int) -> torch.Tensor:
-        return torch.zeros(n, dtype=torch.int32, device=self.device)
-
     def decode(self, stream=None) -> torch.Tensor:
         if self.k_scales is not None:
             return nbx_paged_decode_attn_block_scaled(self.q, self.k_pool, self.v_pool, self.k_scales, self.v_scales,
@@ -217,7 +216,7 @@ class PagedDecodeSession:
                                                       out=self.out, workspace=self.workspace, status=self.status,
                                                       stream=stream, **self.modifications)
         if self.shared_groups:
-            start, shared = self.groups or (self._no_groups(1), self._no_groups(0))
+            start, shared = self.groups or self._no_groups
             return nbx_paged_decode_attn_shared(self.q, self.k_pool, self.v_pool, self.block_table, self.seq_lens,
                                                 self.max_seq_len, start, shared, self.scale, self.k_scale, self.v_scale,
                                                 out=self.out, workspace=self.workspace, status=self.status, stream=stream)
