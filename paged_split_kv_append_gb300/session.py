@@ -182,6 +182,8 @@ class PagedDecodeSession:
         if group_start is None and shared_lens is None:
             self.groups = None
             return
+        if group_start is None or shared_lens is None:
+            raise ValueError("groups are given by their starts and their shared lengths, both or neither")
         if not self.shared_groups or shared_lens.numel() > self.shared_groups:
             raise ValueError("the session was not made for so many groups")
         self.groups = group_start, shared_lens

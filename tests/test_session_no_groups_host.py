@@ -43,3 +43,12 @@ def test_a_decode_without_groups_makes_no_tensor(monkeypatch):
     s.set_groups(None, None)
     s.decode()
     assert given[3][0] is start and given[3][1] is shared
+
+
+def test_half_of_the_groups_is_refused():
+    s = PagedDecodeSession(**SIZES, pool_dtype="bf16", shared_groups=2)
+    x = torch.tensor([0, 4], dtype=torch.int32)
+    for half in ((x, None), (None, x[:1])):
+        with pytest.raises(ValueError, match="both or neither"):
+            s.set_groups(*half)
+        assert s.groups is None
