@@ -386,6 +386,8 @@ static int decode_call(const void* q, int q_dtype, int batch, int rows, int h_q,
   p.k_scale_host = k_scale;
   p.producer_delay_ns = g_producer_delay_ns.load();
   {
+    // (Behind shared prefixes there is room for more splits than this counts, but few calls use it: with that room counted,
+    // 64 rows of 8 behind 1500 positions took 131 us, 129.5 so, 256 sequences of 16 groups 324 and 322.)
     const double part_bytes = static_cast<double>(batch) * rows * h_q * w.max_splits * d * 4.0;
     p.keep_frac = static_cast<float>(part_bytes <= 67108864.0 ? 1.0 : 67108864.0 / part_bytes);
   }
