@@ -527,7 +527,7 @@ struct PrefixWork {
     u.tok = pg.b0 * p.a.rows + pair * tpu;
     u.head = set * p.heads;
     u.kvh = u.head / p.a.group;
-    u.pos = 1 << 30;
+    u.pos = 0x7fffffff - (kPairs ? 2 : 1) * kAtM;   // (its tokens' are added to it)
     u.b = pg.row;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
