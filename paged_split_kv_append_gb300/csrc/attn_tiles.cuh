@@ -704,7 +704,7 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
       if (up) m = z - kMid;
       const float neg = m == -INFINITY ? 0.f : -m;
       const f32x2 c2 = pack2(c, c), neg2 = pack2(neg, neg);
-      f32x2 sum[2] = {pack2(l * f, 0.f), pack2(0.f, 0.f)};
+      f32x2 sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};   // a tile's weights by themselves: beside l's 2^24 a 1 is lost
       constexpr int kChunk = NC < 64 ? NC : 64;   // columns of S whose terms are stored at once
 #pragma unroll
       for (int h = 0; h < NC; h += kChunk) {
@@ -734,7 +734,7 @@ __device__ __forceinline__ bool attn_softmax(W& w, const AttnShared<C>& sh, uint
         }
       }
       const float2 s0 = unpack2(sum[0]), s1 = unpack2(sum[1]);
-      l = (s0.x + s0.y) + (s1.x + s1.y);
+      l = fmaf(l, f, (s0.x + s0.y) + (s1.x + s1.y));
       // O follows a maximum that moved, once the last PV into it is done
       if (j > 0 && __any_sync(0xffffffffu, up)) {
         if (!pv_wait()) return false;

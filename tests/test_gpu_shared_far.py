@@ -38,3 +38,19 @@ def test_positions_past_2_to_the_30(h_q):
     assert int(status) == 0
     # the sum of 2^30 and more weights, each term within 2^-24 of its place: far within this
     assert float((out - 1.0).abs().max()) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+def test_as_many_equal_weights(pool):
+    """2^30 weights of 1 and values of -1. Of a split, 2^25 and more positions, sums of whole tiles are exact in fp32 up to
+    2^31; joined and divided, they are off by a few 2^-24."""
+    page = 1 << 16
+    n = 1 << 30
+    pools = [torch.zeros((3, 1, page, 64), device=DEV) for _ in range(2)]
+    pools[1].fill_(-1.0)
+    pools = [x.to(torch.float8_e4m3fn if pool == "e4m3" else torch.bfloat16) for x in pools]
+    table = torch.zeros((2, n // page + 1), dtype=torch.int32, device=DEV)
+    table[:, -1] = ints([1, 2])
+    q = torch.zeros((2, 1, 1, 64), dtype=torch.bfloat16, device=DEV)
+    out = nbx.nbx_paged_decode_attn_shared(q, *pools, table, ints([n + 17, n + 30]), n + 30, ints([0, 2]), ints([n]), 1.0)
+    assert float((out + 1.0).abs().max()) < 2.0 ** -20
