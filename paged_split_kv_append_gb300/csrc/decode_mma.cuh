@@ -1595,6 +1595,7 @@ __global__ void __launch_bounds__(X ? kMmaThreadsMod : kMmaThreads, 1)
         // f16 partials (fp8 pools): acc / l, which stays within the E4M3 codes' range
         const bool half_part = F8 && p.part_f16 && !single;
         const float il = (m_run == -INFINITY) ? 0.f : 1.f / l_run;
+        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;   // (rows are whole 32 bytes)
         float* dst = nullptr;
         if (row_ok) {
           const int64_t orow = (static_cast<int64_t>(mu.b) * p.rows + r) * p.h_q + static_cast<int64_t>(mu.h) * G + gq;
@@ -1633,8 +1634,15 @@ __global__ void __launch_bounds__(X ? kMmaThreadsMod : kMmaThreads, 1)
               float v[8];
   #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[8 * c8 + e]) * sc;
-              if (single) st_global_v8(dst + ch * kChunk + c8 * 8, v);
-              else st_global_v8_hint(dst + ch * kChunk + c8 * 8, v, keep);   // kept in L2 for the merge
+              float* const to = dst + ch * kChunk + c8 * 8;
+              if (!single) {
+                st_global_v8_hint(to, v, keep);   // kept in L2 for the merge
+              } else if (out32) {
+                st_global_v8(to, v);
+              } else {   // an output is aligned to 16 bytes
+                reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+              }
             }
           }
         }
