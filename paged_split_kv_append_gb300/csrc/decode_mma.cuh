@@ -1038,7 +1038,8 @@ __device__ __forceinline__ bool softmax_modified(const DecodeParams& p, char* q_
 // F8: the pools hold E4M3 codes, read as they are by kind::f8f6f4 MMAs (Q and P as two E4M3 terms
 // each); otherwise bf16 pools and kind::f16 MMAs (P as two bf16 terms). TW: a test of the timeout
 // path (nbx_set_decode_wait_test): the waits take DecodeParams::wait_limit_ns and the producers
-// start after DecodeParams::producer_delay_ns.
+// start after DecodeParams::producer_delay_ns; or an output that is aligned to 16 bytes only, where
+// its rows are stored so (asked in the epilogue of all, an fp8 chunk of 128 rows took 142.9 us for 133.5).
 // X: a modified decode (see above).
 template <int D, bool F8, bool TW, int X = 0>
 __global__ void __launch_bounds__(X ? kMmaThreadsMod : kMmaThreads, 1)
@@ -1595,7 +1596,6 @@ __global__ void __launch_bounds__(X ? kMmaThreadsMod : kMmaThreads, 1)
         // f16 partials (fp8 pools): acc / l, which stays within the E4M3 codes' range
         const bool half_part = F8 && p.part_f16 && !single;
         const float il = (m_run == -INFINITY) ? 0.f : 1.f / l_run;
-        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;   // (rows are whole 32 bytes)
         float* dst = nullptr;
         if (row_ok) {
           const int64_t orow = (static_cast<int64_t>(mu.b) * p.rows + r) * p.h_q + static_cast<int64_t>(mu.h) * G + gq;
@@ -1634,15 +1634,12 @@ __global__ void __launch_bounds__(X ? kMmaThreadsMod : kMmaThreads, 1)
               float v[8];
   #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[8 * c8 + e]) * sc;
-              float* const to = dst + ch * kChunk + c8 * 8;
-              if (!single) {
-                st_global_v8_hint(to, v, keep);   // kept in L2 for the merge
-              } else if (out32) {
-                st_global_v8(to, v);
-              } else {   // an output is aligned to 16 bytes
-                reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
-              }
+              if (TW && single && (reinterpret_cast<uintptr_t>(p.out) & 31u) != 0) {
+                float4* const to = reinterpret_cast<float4*>(dst + ch * kChunk + c8 * 8);
+                to[0] = make_float4(v[0], v[1], v[2], v[3]);
+                to[1] = make_float4(v[4], v[5], v[6], v[7]);
+              } else if (single) st_global_v8(dst + ch * kChunk + c8 * 8, v);
+              else st_global_v8_hint(dst + ch * kChunk + c8 * 8, v, keep);   // kept in L2 for the merge
             }
           }
         }
@@ -1777,7 +1774,7 @@ cudaError_t launch_mma(const DecodeParams& p, int grid_limit, cudaStream_t strea
   if (grid < 1) grid = 1;
   constexpr unsigned threads = X ? kMmaThreadsMod : kMmaThreads;
   if constexpr (mma_tests_waits(X))
-    if (waits_tested(p))
+    if (waits_tested(p) || (X == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31u) != 0))
       return launch_pdl(decode_partial_mma_kernel<D, F8, true, X>, static_cast<unsigned>(grid), threads, C::kSmem, stream, p,
                         *maps);
   return launch_pdl(decode_partial_mma_kernel<D, F8, false, X>, static_cast<unsigned>(grid), threads, C::kSmem, stream, p,
