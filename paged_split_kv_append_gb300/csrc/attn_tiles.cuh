@@ -563,36 +563,30 @@ __device__ __forceinline__ bool attn_mma(W& w, const AttnShared<C>& sh, uint32_t
 template <int D, int kCount>
 __device__ __forceinline__ float q_to_f16(const __nv_bfloat16* q, char* tile, int row, int d0) {
   const uint4* src = reinterpret_cast<const uint4*>(q);
-  uint4 raw[kCount / 8];
-#pragma unroll
-  for (int i = 0; i < kCount / 8; ++i) raw[i] = q != nullptr ? __ldcg(src + d0 / 8 + i) : make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t to = smem_u32(tile) + row * 128;
+  auto place = [&](int i) { return to + (i >> 3) * (kAtM * 128) + (((i & 7) ^ (row & 7)) << 4); };
   float amax = 0.f;
-  auto larger = [&](const uint4& v) {
+#pragma unroll 4
+  for (int i = 0; i < D / 8; ++i) {
+    const uint4 v = q != nullptr ? __ldcg(src + i) : make_uint4(0u, 0u, 0u, 0u);
     float2 x[4];
     unpack16<BF16>(v, x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) amax = max_nan(amax, max_nan(fabsf(x[e].x), fabsf(x[e].y)));
-  };
-  if (kCount < D && q != nullptr) {   // the other thread's half
-#pragma unroll 4
-    for (int i = 0; i < kCount / 8; ++i) larger(__ldcg(src + (d0 == 0 ? kCount / 8 : 0) + i));
+    if (kCount == D || (i >= d0 / 8 && i < (d0 + kCount) / 8)) sts128(place(i), v);   // as it is, for the second pass
   }
-#pragma unroll
-  for (int i = 0; i < kCount / 8; ++i) larger(raw[i]);
   int e2 = 0;   // a NaN or an infinity in the vector: as it is
   if (amax > 0.f && amax <= 3.402823466e38f)
     e2 = min(120, max(-120, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127)));
   const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23);
-#pragma unroll
-  for (int k = 0; k < kCount / 8; ++k) {
-    const int i = d0 / 8 + k;
+#pragma unroll 4
+  for (int i = d0 / 8; i < (d0 + kCount) / 8; ++i) {
     uint32_t w[4];
     float2 x[4];
-    unpack16<BF16>(raw[k], x);
+    unpack16<BF16>(lds128(place(i)), x);
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = f16x2_bits(x[e].x * up, x[e].y * up);
-    *reinterpret_cast<uint4*>(tile + (i >> 3) * (kAtM * 128) + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
-        make_uint4(w[0], w[1], w[2], w[3]);
+    sts128(place(i), make_uint4(w[0], w[1], w[2], w[3]));
   }
   return __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
 }
