@@ -1,5 +1,5 @@
 // Attention of 128-row tiles of query vectors on tcgen05: what prompt attention and the shared-prefix decode run. (A
-// prompt of 16384 tokens, 32 / 8 heads of 128, takes 1454 us, at 79 % of the measured matrix rate and the power limit.)
+// prompt of 16384 tokens, 32 / 8 heads of 128, takes 1442 us, at 80 % of the measured matrix rate and the power limit.)
 //
 // A work unit is one or two M tiles of 128 query vectors of one KV head (a tile holds some tokens with `heads` query heads
 // each) and the keys they attend, in tiles of kN. Per key tile, with scores in log2 units:
